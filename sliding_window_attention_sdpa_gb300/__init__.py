@@ -6,7 +6,8 @@ functions ``sdpa_bwd_workspace_bytes``, ``sdpa_bwd_preprocess``, ``sdpa_bwd``,
 ``sdpa_bwd_dq_convert``, ``sdpa_bwd_gqa_reduce`` and ``sdpa_bwd_check_status``
 mirror the C entry points one to one; ``backward()`` is the convenience call a
 PyTorch user makes (it allocates outputs and the workspace with torch and runs
-the four kernels on the current stream).
+the four kernels on the current stream). The key/value cache's calls
+(``include/sdpa_cache.h``) are in ``cache.py`` and offered here by name.
 
 If the compiled library is missing this module raises: there is no fallback.
 """
@@ -18,6 +19,12 @@ import threading
 from typing import Optional
 
 from . import _build
+from . import cache as _cache
+from .cache import (KVCache, SdpaCache, SdpaCacheAppendParams, SdpaCacheEvictParams, SdpaCacheFwdParams,
+                    SdpaCacheWeighParams, cache_append, cache_evict, cache_forward, cache_weigh,
+                    sdpa_cache_append, sdpa_cache_check_status, sdpa_cache_evict,
+                    sdpa_cache_evict_workspace_bytes, sdpa_cache_fwd, sdpa_cache_fwd_workspace_bytes,
+                    sdpa_cache_weigh)
 
 SDPA_OK, SDPA_ERR_INVALID_ARG, SDPA_ERR_UNSUPPORTED, SDPA_ERR_CUDA = 0, 1, 2, 3
 SDPA_ERR_TIMEOUT, SDPA_ERR_BAD_LENGTHS, SDPA_ERR_WORKSPACE, SDPA_ERR_BOUNDS = 4, 5, 6, 7
@@ -30,7 +37,7 @@ ENTRY_POINTS = ("sdpa_bwd_workspace_bytes", "sdpa_bwd_preprocess", "sdpa_bwd",
                 "sdpa_bwd_last_error", "sdpa_bwd_params_bytes", "sdpa_bwd_tile_kv",
                 "sdpa_bwd_tile_q", "sdpa_bwd_no_alloc", "sdpa_bwd_kernel_launches",
                 "sdpa_fwd", "sdpa_fwd_check_status", "sdpa_fwd_params_bytes",
-                "sdpa_bwd_test_hook", "sdpa_bwd_no_alloc_check_status")
+                "sdpa_bwd_test_hook", "sdpa_bwd_no_alloc_check_status", *_cache.ENTRY_POINTS)
 
 _i64x3 = ctypes.c_int64 * 3
 
@@ -130,6 +137,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.sdpa_fwd_check_status.argtypes = [vp]
         lib.sdpa_fwd_check_status.restype = st
         lib.sdpa_fwd_params_bytes.restype = sz
+        _cache.bind(lib)
         _lib = lib
         return lib
 

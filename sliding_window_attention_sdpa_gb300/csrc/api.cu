@@ -6,39 +6,79 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
-#include <string>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/sdpa_bwd.h"
 #include "../../include/sdpa_fwd.h"
+#include "api_util.h"
 #include "sdpa_internal.h"
 #include "seq.cuh"
 
+namespace swa {
+namespace api {
+
+// A fixed buffer: recording an error allocates nothing and cannot throw.
+static thread_local char g_last_error[512];
+
+sdpa_status_t fail(sdpa_status_t code, const char* fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
+    va_end(ap);
+    return code;
+}
+
+void clear_error() { g_last_error[0] = 0; }
+
+sdpa_status_t check_device_ptr(const char* name, const void* ptr, bool required, int device, unsigned align)
+{
+    if (ptr == nullptr) {
+        if (required) return fail(SDPA_ERR_INVALID_ARG, "%s is NULL", name);
+        return SDPA_OK;
+    }
+    if ((reinterpret_cast<uintptr_t>(ptr) & (align - 1)) != 0)
+        return fail(SDPA_ERR_INVALID_ARG, "%s=%p is not %u-byte aligned", name, ptr, align);
+    cudaPointerAttributes attr;
+    cudaError_t e = cudaPointerGetAttributes(&attr, ptr);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(SDPA_ERR_INVALID_ARG, "%s=%p: not a CUDA pointer (%s)", name, ptr,
+                    cudaGetErrorString(e));
+    }
+    if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged)
+        return fail(SDPA_ERR_INVALID_ARG, "%s=%p is not device memory (memory type %d)", name, ptr,
+                    (int)attr.type);
+    if (attr.device != device)
+        return fail(SDPA_ERR_INVALID_ARG, "%s=%p lives on device %d, current device is %d", name, ptr,
+                    attr.device, device);
+    return SDPA_OK;
+}
+
+sdpa_status_t cuda_status(cudaError_t e, const char* what)
+{
+    if (e == cudaSuccess) return SDPA_OK;
+    return fail(SDPA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+}  // namespace api
+}  // namespace swa
+
 namespace {
 
-thread_local std::string g_last_error;
+using swa::api::check_device_ptr;
+using swa::api::clear_error;
+using swa::api::cuda_status;
+using swa::api::fail;
 
 // sdpa_bwd_test_hook's settings for this thread's next sdpa_bwd calls.
 constexpr int64_t kWaitLimitNs = 2000000000LL;
 thread_local int64_t g_test_wait_ns = 0;
 thread_local int32_t g_test_flags = 0;
 
-sdpa_status_t fail(sdpa_status_t code, const char* fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return code;
-}
-
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Host-side validation that needs no device access.
 sdpa_status_t check_shape(const sdpa_bwd_params* p)
@@ -91,30 +131,6 @@ sdpa_status_t check_strides(const char* name, const int64_t* st, bool thd)
             return fail(SDPA_ERR_INVALID_ARG,
                         "%s_stride[%d]=%lld: strides must be non-negative multiples of 8 elements",
                         name, i, (long long)st[i]);
-    return SDPA_OK;
-}
-
-sdpa_status_t check_device_ptr(const char* name, const void* ptr, bool required, int device)
-{
-    if (ptr == nullptr) {
-        if (required) return fail(SDPA_ERR_INVALID_ARG, "%s is NULL", name);
-        return SDPA_OK;
-    }
-    if (!aligned16(ptr))
-        return fail(SDPA_ERR_INVALID_ARG, "%s=%p is not 16-byte aligned", name, ptr);
-    cudaPointerAttributes attr;
-    cudaError_t e = cudaPointerGetAttributes(&attr, ptr);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return fail(SDPA_ERR_INVALID_ARG, "%s=%p: not a CUDA pointer (%s)", name, ptr,
-                    cudaGetErrorString(e));
-    }
-    if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged)
-        return fail(SDPA_ERR_INVALID_ARG, "%s=%p is not device memory (memory type %d)", name, ptr,
-                    (int)attr.type);
-    if (attr.device != device)
-        return fail(SDPA_ERR_INVALID_ARG, "%s=%p lives on device %d, current device is %d", name, ptr,
-                    attr.device, device);
     return SDPA_OK;
 }
 
@@ -283,12 +299,6 @@ sdpa_status_t check_all(const sdpa_bwd_params* p, const void* ws, size_t ws_byte
     return SDPA_OK;
 }
 
-sdpa_status_t cuda_status(cudaError_t e, const char* what)
-{
-    if (e == cudaSuccess) return SDPA_OK;
-    return fail(SDPA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -413,7 +423,7 @@ extern "C" {
 size_t sdpa_bwd_workspace_bytes(const sdpa_bwd_params* p)
 {
     if (check_shape(p) != SDPA_OK) return 0;
-    g_last_error.clear();
+    clear_error();
     return layout_of(p).total;
 }
 
@@ -601,14 +611,14 @@ sdpa_status_t sdpa_bwd_check_status(const void* ws, void* stream)
     return SDPA_OK;
 }
 
-const char* sdpa_bwd_last_error(void) { return g_last_error.c_str(); }
+const char* sdpa_bwd_last_error(void) { return swa::api::g_last_error; }
 
 sdpa_status_t sdpa_bwd_test_hook(int64_t wait_limit_ns, int32_t flags)
 {
     if (flags & ~3) return fail(SDPA_ERR_INVALID_ARG, "test hook flags=%d: only bits 0 and 1 are defined", flags);
     g_test_wait_ns = wait_limit_ns > 0 ? wait_limit_ns : 0;
     g_test_flags = flags;
-    g_last_error.clear();
+    clear_error();
     return SDPA_OK;
 }
 
@@ -685,7 +695,7 @@ int32_t sdpa_bwd_tile_q(void) { return swa::kTileQ; }
 int32_t sdpa_bwd_kernel_launches(const sdpa_bwd_params* p)
 {
     if (check_shape(p) != SDPA_OK) return -1;
-    g_last_error.clear();
+    clear_error();
     const swa::WsLayout w = layout_of(p);
     const int64_t n_kv_tiles = (p->s_kv + swa::kTileKV - 1) / swa::kTileKV;
     const int64_t stats_row = ((p->s_q + swa::kTileQ - 1) / swa::kTileQ) * swa::kTileQ;

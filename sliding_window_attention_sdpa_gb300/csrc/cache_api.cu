@@ -1,0 +1,389 @@
+// cache_api.cu -- the C ABI declared in include/sdpa_cache.h: host-side
+// argument checks and the launches on the caller's stream. Nothing here
+// allocates or synchronises (except sdpa_cache_check_status).
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "../../include/sdpa_cache.h"
+#include "api_util.h"
+#include "cache_internal.h"
+
+namespace {
+
+using swa::api::check_device_ptr;
+using swa::api::clear_error;
+using swa::api::cuda_status;
+using swa::api::fail;
+
+constexpr int64_t kMax31 = int64_t(1) << 31;
+
+void copy3(int64_t* dst, const int64_t* src) { memcpy(dst, src, 3 * sizeof(int64_t)); }
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+sdpa_status_t check_strides(const char* name, const int64_t* st, int first = 0)
+{
+    for (int i = first; i < 3; ++i)
+        if (st[i] < 0 || st[i] % 8 != 0)
+            return fail(SDPA_ERR_INVALID_ARG,
+                        "%s_stride[%d]=%lld: strides must be non-negative multiples of 8 elements", name, i,
+                        (long long)st[i]);
+    return SDPA_OK;
+}
+
+// Whether any sequence has room for a key; without, the arrays may be empty (NULL).
+bool holds_keys(const sdpa_cache* c) { return c->b > 0 && c->max_pages > 0; }
+
+// The cache's fields, without device access.
+sdpa_status_t check_cache(const sdpa_cache* c)
+{
+    if (c == nullptr) return fail(SDPA_ERR_INVALID_ARG, "cache is NULL");
+    if (c->dtype != SDPA_BF16 && c->dtype != SDPA_F16)
+        return fail(SDPA_ERR_INVALID_ARG, "cache dtype: expected SDPA_BF16 or SDPA_F16, got %d", c->dtype);
+    if (c->b < 0 || c->h_kv <= 0 || c->n_pages < 0 || c->page_size <= 0 || c->max_pages < 0)
+        return fail(SDPA_ERR_INVALID_ARG,
+                    "cache: b=%lld h_kv=%lld n_pages=%lld page_size=%lld max_pages=%lld (need h_kv, page_size > 0, "
+                    "others >= 0)",
+                    (long long)c->b, (long long)c->h_kv, (long long)c->n_pages, (long long)c->page_size,
+                    (long long)c->max_pages);
+    if (c->d != 64 && c->d != 128)
+        return fail(SDPA_ERR_UNSUPPORTED, "cache d=%lld: only head dimensions 64 and 128 are implemented",
+                    (long long)c->d);
+    if (c->page_size >= kMax31 || c->max_pages >= kMax31 || c->page_size * c->max_pages >= kMax31)
+        return fail(SDPA_ERR_UNSUPPORTED, "cache capacity max_pages * page_size = %lld * %lld: at most 2^31 - 1 keys",
+                    (long long)c->max_pages, (long long)c->page_size);
+    if (c->b >= kMax31 || c->h_kv >= kMax31 || c->b * c->h_kv >= kMax31)
+        return fail(SDPA_ERR_UNSUPPORTED, "cache b * h_kv = %lld * %lld: at most 2^31 - 1", (long long)c->b,
+                    (long long)c->h_kv);
+    if (holds_keys(c) && c->page_table == nullptr && (c->max_pages != 1 || c->n_pages < c->b))
+        return fail(SDPA_ERR_INVALID_ARG,
+                    "cache without a page_table: max_pages=%lld n_pages=%lld (need one page per sequence)",
+                    (long long)c->max_pages, (long long)c->n_pages);
+    if (holds_keys(c) && (c->positions == nullptr) != (c->next_pos == nullptr))
+        return fail(SDPA_ERR_INVALID_ARG, "cache positions and next_pos must both be set or both be NULL");
+    sdpa_status_t st;
+    if ((st = check_strides("cache k", c->k_stride)) != SDPA_OK) return st;
+    return check_strides("cache v", c->v_stride);
+}
+
+struct Ptr {
+    const char* name;
+    const void* p;
+    bool required;
+    unsigned align;
+};
+
+template <size_t N>
+sdpa_status_t check_ptrs(const Ptr (&ptrs)[N], int dev)
+{
+    for (const Ptr& p : ptrs) {
+        const sdpa_status_t st = check_device_ptr(p.name, p.p, p.required, dev, p.align);
+        if (st != SDPA_OK) return st;
+    }
+    return SDPA_OK;
+}
+
+sdpa_status_t current_device(int* dev)
+{
+    if (cudaGetDevice(dev) == cudaSuccess) return SDPA_OK;
+    cudaGetLastError();
+    return fail(SDPA_ERR_CUDA, "no CUDA device available");
+}
+
+sdpa_status_t check_cache_ptrs(const sdpa_cache* c, int dev)
+{
+    const bool held = holds_keys(c) && c->n_pages > 0;
+    const Ptr ptrs[] = {{"cache k", c->k, held, 16},
+                        {"cache v", c->v, held, 16},
+                        {"cache page_table", c->page_table, false, 4},
+                        {"cache lengths", c->lengths, c->b > 0, 4},
+                        {"cache next_pos", c->next_pos, false, 4},
+                        {"cache positions", c->positions, false, 4},
+                        {"cache weights", c->weights, false, 4},
+                        {"cache status", c->status, true, 4}};
+    return check_ptrs(ptrs, dev);
+}
+
+swa::CacheView view_of(const sdpa_cache* c)
+{
+    swa::CacheView v{};
+    v.b = c->b;
+    v.h_kv = c->h_kv;
+    v.d = c->d;
+    v.n_pages = c->n_pages;
+    v.page_size = static_cast<uint32_t>(c->page_size);
+    v.max_pages = static_cast<uint32_t>(c->max_pages);
+    v.cap = c->page_size * c->max_pages;
+    v.k = static_cast<uint16_t*>(c->k);
+    v.v = static_cast<uint16_t*>(c->v);
+    copy3(v.k_stride, c->k_stride);
+    copy3(v.v_stride, c->v_stride);
+    v.page_table = c->page_table;
+    v.lengths = c->lengths;
+    v.next_pos = c->next_pos;
+    v.positions = c->positions;
+    v.weights = c->weights;
+    v.status = c->status;
+    return v;
+}
+
+sdpa_status_t check_rows(const sdpa_cache* c, int64_t s_q, int64_t h_q, int64_t window_left, float scale)
+{
+    if (h_q <= 0 || h_q % c->h_kv != 0)
+        return fail(SDPA_ERR_INVALID_ARG, "h_q=%lld is not a positive multiple of h_kv=%lld", (long long)h_q,
+                    (long long)c->h_kv);
+    if (h_q >= kMax31 || s_q >= kMax31 || c->b * s_q >= kMax31 || c->b * s_q * h_q >= kMax31)
+        return fail(SDPA_ERR_UNSUPPORTED, "b * s_q * h_q = %lld * %lld * %lld rows: at most 2^31 - 1", (long long)c->b,
+                    (long long)s_q, (long long)h_q);
+    if (window_left < -1)
+        return fail(SDPA_ERR_INVALID_ARG, "window_left=%lld: must be >= -1", (long long)window_left);
+    if (!(scale > 0.f) || scale - scale != 0.f)
+        return fail(SDPA_ERR_INVALID_ARG, "scale must be a positive finite number");
+    return SDPA_OK;
+}
+
+sdpa_status_t check_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p)
+{
+    sdpa_status_t st = check_cache(c);
+    if (st != SDPA_OK) return st;
+    if (p == nullptr) return fail(SDPA_ERR_INVALID_ARG, "params is NULL");
+    if (p->s_q < 1 || p->s_q > 64)
+        return fail(SDPA_ERR_UNSUPPORTED, "s_q=%lld: 1 to 64 new tokens per sequence (longer ones: sdpa_fwd)",
+                    (long long)p->s_q);
+    if ((st = check_rows(c, p->s_q, p->h_q, p->window_left, p->scale)) != SDPA_OK) return st;
+    const struct { const char* n; const int64_t* s; } strides[] = {
+        {"q", p->q_stride}, {"k", p->k_stride}, {"v", p->v_stride}, {"o", p->o_stride}};
+    for (const auto& x : strides)
+        if ((st = check_strides(x.n, x.s)) != SDPA_OK) return st;
+    return SDPA_OK;
+}
+
+sdpa_status_t check_append(const sdpa_cache* c, const sdpa_cache_append_params* p)
+{
+    sdpa_status_t st = check_cache(c);
+    if (st != SDPA_OK) return st;
+    if (p == nullptr) return fail(SDPA_ERR_INVALID_ARG, "params is NULL");
+    if (p->layout != SDPA_BSHD && p->layout != SDPA_THD)
+        return fail(SDPA_ERR_INVALID_ARG, "layout: expected SDPA_BSHD or SDPA_THD, got %d", p->layout);
+    const bool thd = p->layout == SDPA_THD;
+    if (p->s < 0 || p->s >= kMax31) return fail(SDPA_ERR_INVALID_ARG, "s=%lld: must be 0 to 2^31 - 1", (long long)p->s);
+    if (p->index != nullptr && (p->n < 0 || p->n >= kMax31))
+        return fail(SDPA_ERR_INVALID_ARG, "n=%lld: must be 0 to 2^31 - 1", (long long)p->n);
+    if (thd && p->index != nullptr) return fail(SDPA_ERR_INVALID_ARG, "index: only with SDPA_BSHD");
+    if (thd && p->offsets == nullptr) return fail(SDPA_ERR_INVALID_ARG, "THD layout needs offsets");
+    if (thd && p->total < 0) return fail(SDPA_ERR_INVALID_ARG, "total=%lld: must be >= 0", (long long)p->total);
+    if ((st = check_strides("k", p->k_stride, thd ? 1 : 0)) != SDPA_OK) return st;
+    return check_strides("v", p->v_stride, thd ? 1 : 0);
+}
+
+sdpa_status_t check_evict(const sdpa_cache* c, const sdpa_cache_evict_params* p)
+{
+    sdpa_status_t st = check_cache(c);
+    if (st != SDPA_OK) return st;
+    if (p == nullptr) return fail(SDPA_ERR_INVALID_ARG, "params is NULL");
+    if (holds_keys(c) && (c->positions == nullptr || c->weights == nullptr))
+        return fail(SDPA_ERR_INVALID_ARG, "evict needs a cache with positions and weights");
+    if (p->keep < 0 || p->first < 0 || p->recent < 0 || p->keep >= kMax31 || p->first > p->keep ||
+        p->recent > p->keep - p->first)
+        return fail(SDPA_ERR_INVALID_ARG,
+                    "keep=%lld first=%lld recent=%lld: need keep >= first + recent, all >= 0, keep < 2^31",
+                    (long long)p->keep, (long long)p->first, (long long)p->recent);
+    return SDPA_OK;
+}
+
+sdpa_status_t check_ws(const void* ws, size_t have, size_t need)
+{
+    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+        return fail(SDPA_ERR_WORKSPACE, "workspace=%p must be non-NULL and 256-byte aligned", ws);
+    if (have < need) return fail(SDPA_ERR_WORKSPACE, "workspace_bytes=%zu, need %zu", have, need);
+    return SDPA_OK;
+}
+
+struct EvictLayout {
+    int64_t m;
+    size_t holes, tails, counts, total;
+};
+
+EvictLayout evict_layout(const sdpa_cache* c, const sdpa_cache_evict_params* p)
+{
+    EvictLayout l{};
+    const int64_t cap = c->page_size * c->max_pages;
+    const int64_t over = cap > p->keep ? cap - p->keep : 0;
+    l.m = p->keep < over ? p->keep : over;
+    const size_t units = static_cast<size_t>(c->b) * c->h_kv;
+    l.holes = 0;
+    l.tails = align256(units * l.m * 4);
+    l.counts = align256(l.tails + units * l.m * 4);
+    l.total = align256(l.counts + units * 4 + 4);
+    return l;
+}
+
+template <typename T>
+T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
+
+}  // namespace
+
+extern "C" {
+
+size_t sdpa_cache_bytes(void) { return sizeof(sdpa_cache); }
+size_t sdpa_cache_fwd_params_bytes(void) { return sizeof(sdpa_cache_fwd_params); }
+size_t sdpa_cache_append_params_bytes(void) { return sizeof(sdpa_cache_append_params); }
+size_t sdpa_cache_weigh_params_bytes(void) { return sizeof(sdpa_cache_weigh_params); }
+size_t sdpa_cache_evict_params_bytes(void) { return sizeof(sdpa_cache_evict_params); }
+
+size_t sdpa_cache_fwd_workspace_bytes(const sdpa_cache* c, const sdpa_cache_fwd_params* p)
+{
+    if (check_fwd(c, p) != SDPA_OK) return 0;
+    clear_error();
+    return 256;
+}
+
+sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p, void* ws, size_t ws_bytes,
+                             void* stream)
+{
+    sdpa_status_t st = check_fwd(c, p);
+    if (st != SDPA_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, 256)) != SDPA_OK) return st;
+    int dev = 0;
+    if ((st = current_device(&dev)) != SDPA_OK) return st;
+    const bool rows = c->b > 0;
+    const Ptr ptrs[] = {{"q", p->q, rows, 16},     {"k", p->k, rows, 16},           {"v", p->v, rows, 16},
+                        {"o", p->o, rows, 16},     {"lse", p->lse, rows, 4},        {"tree", p->tree, false, 8},
+                        {"sink", p->sink, false, 4}, {"seq_q_lens", p->seq_q_lens, false, 4}, {"workspace", ws, true, 256}};
+    if ((st = check_cache_ptrs(c, dev)) != SDPA_OK || (st = check_ptrs(ptrs, dev)) != SDPA_OK) return st;
+    if (!rows) return SDPA_OK;
+    swa::CacheFwdArgs a{};
+    a.c = view_of(c);
+    a.s_q = static_cast<int32_t>(p->s_q);
+    a.h_q = static_cast<int32_t>(p->h_q);
+    a.group = static_cast<int32_t>(p->h_q / c->h_kv);
+    a.window_left = p->window_left;
+    a.scale = p->scale;
+    a.scale_log2 = p->scale * 1.4426950408889634f;
+    a.q = static_cast<const uint16_t*>(p->q);
+    a.k = static_cast<const uint16_t*>(p->k);
+    a.v = static_cast<const uint16_t*>(p->v);
+    copy3(a.q_stride, p->q_stride);
+    copy3(a.k_stride, p->k_stride);
+    copy3(a.v_stride, p->v_stride);
+    copy3(a.o_stride, p->o_stride);
+    a.tree = p->tree;
+    a.seq_q_lens = p->seq_q_lens;
+    a.sink = p->sink;
+    a.o = static_cast<uint16_t*>(p->o);
+    a.lse = p->lse;
+    return cuda_status(swa::launch_cache_fwd(a, c->dtype, static_cast<cudaStream_t>(stream)), "cache forward launch");
+}
+
+sdpa_status_t sdpa_cache_append(const sdpa_cache* c, const sdpa_cache_append_params* p, void* stream)
+{
+    sdpa_status_t st = check_append(c, p);
+    if (st != SDPA_OK) return st;
+    int dev = 0;
+    if ((st = current_device(&dev)) != SDPA_OK) return st;
+    const bool thd = p->layout == SDPA_THD;
+    const bool rows = c->b > 0 && p->s > 0 && (thd ? p->total > 0 : true) && (p->index == nullptr || p->n > 0);
+    const Ptr ptrs[] = {{"k", p->k, rows, 16},
+                        {"v", p->v, rows, 16},
+                        {"index", p->index, false, 4},
+                        {"counts", p->counts, false, 4},
+                        {"offsets", p->offsets, thd, 4}};
+    if ((st = check_cache_ptrs(c, dev)) != SDPA_OK || (st = check_ptrs(ptrs, dev)) != SDPA_OK) return st;
+    if (!rows) return SDPA_OK;
+    swa::CacheAppendArgs a{};
+    a.c = view_of(c);
+    a.thd = thd ? 1 : 0;
+    a.s = p->s;
+    a.n = p->n;
+    a.total = p->total;
+    a.k = static_cast<const uint16_t*>(p->k);
+    a.v = static_cast<const uint16_t*>(p->v);
+    copy3(a.k_stride, p->k_stride);
+    copy3(a.v_stride, p->v_stride);
+    a.index = p->index;
+    a.counts = p->counts;
+    a.offsets = thd ? p->offsets : nullptr;
+    return cuda_status(swa::launch_cache_append(a, static_cast<cudaStream_t>(stream)), "cache append launch");
+}
+
+sdpa_status_t sdpa_cache_weigh(const sdpa_cache* c, const sdpa_cache_weigh_params* p, void* stream)
+{
+    sdpa_status_t st = check_cache(c);
+    if (st != SDPA_OK) return st;
+    if (p == nullptr) return fail(SDPA_ERR_INVALID_ARG, "params is NULL");
+    if (holds_keys(c) && c->weights == nullptr) return fail(SDPA_ERR_INVALID_ARG, "weigh needs a cache with weights");
+    if (p->s_q < 1) return fail(SDPA_ERR_INVALID_ARG, "s_q=%lld: must be >= 1", (long long)p->s_q);
+    if ((st = check_rows(c, p->s_q, p->h_q, p->window_left, p->scale)) != SDPA_OK) return st;
+    if ((st = check_strides("q", p->q_stride)) != SDPA_OK) return st;
+    int dev = 0;
+    if ((st = current_device(&dev)) != SDPA_OK) return st;
+    const bool rows = c->b > 0;
+    const Ptr ptrs[] = {{"q", p->q, rows, 16}, {"lse", p->lse, rows, 4}, {"q_pos", p->q_pos, false, 4}};
+    if ((st = check_cache_ptrs(c, dev)) != SDPA_OK || (st = check_ptrs(ptrs, dev)) != SDPA_OK) return st;
+    if (!rows) return SDPA_OK;
+    swa::CacheWeighArgs a{};
+    a.c = view_of(c);
+    a.s_q = static_cast<int32_t>(p->s_q);
+    a.h_q = static_cast<int32_t>(p->h_q);
+    a.group = static_cast<int32_t>(p->h_q / c->h_kv);
+    a.window_left = p->window_left;
+    a.scale_log2 = p->scale * 1.4426950408889634f;
+    a.q = static_cast<const uint16_t*>(p->q);
+    copy3(a.q_stride, p->q_stride);
+    a.lse = p->lse;
+    a.q_pos = p->q_pos;
+    return cuda_status(swa::launch_cache_weigh(a, c->dtype, static_cast<cudaStream_t>(stream)), "cache weigh launch");
+}
+
+size_t sdpa_cache_evict_workspace_bytes(const sdpa_cache* c, const sdpa_cache_evict_params* p)
+{
+    if (check_evict(c, p) != SDPA_OK) return 0;
+    clear_error();
+    return evict_layout(c, p).total;
+}
+
+sdpa_status_t sdpa_cache_evict(const sdpa_cache* c, const sdpa_cache_evict_params* p, void* ws, size_t ws_bytes,
+                               void* stream)
+{
+    sdpa_status_t st = check_evict(c, p);
+    if (st != SDPA_OK) return st;
+    const EvictLayout l = evict_layout(c, p);
+    if ((st = check_ws(ws, ws_bytes, l.total)) != SDPA_OK) return st;
+    int dev = 0;
+    if ((st = current_device(&dev)) != SDPA_OK) return st;
+    const Ptr ptrs[] = {{"workspace", ws, true, 256}};
+    if ((st = check_cache_ptrs(c, dev)) != SDPA_OK || (st = check_ptrs(ptrs, dev)) != SDPA_OK) return st;
+    swa::CacheEvictArgs a{};
+    a.c = view_of(c);
+    a.keep = p->keep;
+    a.first = p->first;
+    a.recent = p->recent;
+    a.m = l.m;
+    a.holes = at<int32_t>(ws, l.holes);
+    a.tails = at<int32_t>(ws, l.tails);
+    a.counts = at<int32_t>(ws, l.counts);
+    return cuda_status(swa::launch_cache_evict(a, static_cast<cudaStream_t>(stream)), "cache evict launch");
+}
+
+sdpa_status_t sdpa_cache_check_status(const sdpa_cache* c, void* stream)
+{
+    if (c == nullptr) return fail(SDPA_ERR_INVALID_ARG, "cache is NULL");
+    if (c->status == nullptr) return fail(SDPA_ERR_INVALID_ARG, "cache status is NULL");
+    sdpa_status_t st = cuda_status(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)), "stream synchronize");
+    if (st != SDPA_OK) return st;
+    int32_t host = 0;
+    if ((st = cuda_status(cudaMemcpy(&host, c->status, sizeof(host), cudaMemcpyDeviceToHost), "status read")) != SDPA_OK)
+        return st;
+    if (host == 0) return SDPA_OK;
+    if ((st = cuda_status(cudaMemset(c->status, 0, sizeof(int32_t)), "status reset")) != SDPA_OK) return st;
+    if (host == SDPA_ERR_BAD_LENGTHS)
+        return fail(SDPA_ERR_BAD_LENGTHS, "a length, count or row index of the cache is out of its range");
+    if (host == SDPA_ERR_BOUNDS) return fail(SDPA_ERR_BOUNDS, "a page-table entry is outside [0, n_pages)");
+    if (host == SDPA_ERR_TIMEOUT) return fail(SDPA_ERR_TIMEOUT, "a wait of the cache forward ran out on the device");
+    if (host == SDPA_ERR_UNSUPPORTED)
+        return fail(SDPA_ERR_UNSUPPORTED, "the device gave the cache forward shared memory not 1024-byte aligned");
+    return fail(SDPA_ERR_CUDA, "unknown cache status %d", host);
+}
+
+}  // extern "C"

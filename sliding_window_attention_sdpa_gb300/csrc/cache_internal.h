@@ -1,0 +1,73 @@
+// cache_internal.h -- argument blocks shared by the cache's host launcher
+// (cache_api.cu) and its kernels. Plain structs passed by value.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace swa {
+
+// The cache as the kernels see it (fields as in sdpa_cache).
+struct CacheView {
+    int64_t b, h_kv, d;
+    int64_t n_pages;
+    uint32_t page_size, max_pages;
+    int64_t cap;                    // max_pages * page_size, < 2^31
+    uint16_t *k, *v;
+    int64_t k_stride[3], v_stride[3];   // page, row, head
+    const int32_t* page_table;
+    int32_t *lengths, *next_pos, *positions;
+    float* weights;
+    int32_t* status;
+};
+
+struct CacheFwdArgs {
+    CacheView c;
+    int32_t s_q, h_q, group;
+    int64_t window_left;
+    float scale, scale_log2;
+    const uint16_t *q, *k, *v;
+    int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+    const int64_t* tree;
+    const int32_t* seq_q_lens;
+    const float* sink;
+    uint16_t* o;
+    float* lse;
+};
+
+struct CacheAppendArgs {
+    CacheView c;
+    int32_t thd;
+    int64_t s, n, total;
+    const uint16_t *k, *v;
+    int64_t k_stride[3], v_stride[3];
+    const int32_t *index, *counts, *offsets;
+    int32_t rows_per_cta;
+};
+
+struct CacheWeighArgs {
+    CacheView c;
+    int32_t s_q, h_q, group;
+    int64_t window_left;
+    float scale_log2;
+    const uint16_t* q;
+    int64_t q_stride[3];
+    const float* lse;
+    const int32_t* q_pos;
+};
+
+struct CacheEvictArgs {
+    CacheView c;
+    int64_t keep, first, recent;
+    int64_t m;             // most rows that a (sequence, kv-head) moves: min(keep, cap - keep)
+    int32_t *holes, *tails;  // [b * h_kv][m] free slots below keep, kept slots from keep on
+    int32_t* counts;       // [b * h_kv] rows to move; -1: the sequence is not touched
+};
+
+cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_cache_append(const CacheAppendArgs& a, cudaStream_t s);
+cudaError_t launch_cache_weigh(const CacheWeighArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_cache_evict(const CacheEvictArgs& a, cudaStream_t s);
+
+}  // namespace swa
