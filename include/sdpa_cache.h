@@ -46,7 +46,8 @@ typedef struct sdpa_cache {
     int64_t b, h_kv, d;         /* sequences, kv-heads, head dimension (64 or 128) */
     int64_t n_pages, page_size; /* pages in k and v, rows of a page (any number >= 1) */
     int64_t max_pages;          /* entries of a page-table row; a sequence has room for
-                                   max_pages * page_size keys (its capacity, < 2^31) */
+                                   max_pages * page_size keys (its capacity, at most
+                                   2^31 - 2^16) */
     void *k, *v;                /* device [n_pages][page_size][h_kv][d] */
     int64_t k_stride[3], v_stride[3]; /* page, row, head */
     const int32_t *page_table;  /* device [b][max_pages]; NULL: page i is sequence i's only one

@@ -18,7 +18,7 @@ __device__ __forceinline__ int64_t cache_page(const CacheView& c, int64_t bi, ui
         row = slot;
         return bi;
     }
-    const uint32_t p = slot / c.page_size;
+    const uint32_t p = c.page_shift >= 0 ? slot >> c.page_shift : slot / c.page_size;
     row = slot - p * c.page_size;
     const int64_t page = c.page_table[bi * c.max_pages + p];
     if (page < 0 || page >= c.n_pages) {

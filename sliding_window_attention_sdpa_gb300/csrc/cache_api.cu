@@ -17,8 +17,13 @@ using swa::api::cuda_status;
 using swa::api::fail;
 
 constexpr int64_t kMax31 = int64_t(1) << 31;
+// a sequence's keys, rounded up to tiles, are numbered in 32 bits
+constexpr int64_t kMaxCap = kMax31 - (int64_t(1) << 16);
 
 void copy3(int64_t* dst, const int64_t* src) { memcpy(dst, src, 3 * sizeof(int64_t)); }
+
+template <typename T>
+T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -50,8 +55,8 @@ sdpa_status_t check_cache(const sdpa_cache* c)
     if (c->d != 64 && c->d != 128)
         return fail(SDPA_ERR_UNSUPPORTED, "cache d=%lld: only head dimensions 64 and 128 are implemented",
                     (long long)c->d);
-    if (c->page_size >= kMax31 || c->max_pages >= kMax31 || c->page_size * c->max_pages >= kMax31)
-        return fail(SDPA_ERR_UNSUPPORTED, "cache capacity max_pages * page_size = %lld * %lld: at most 2^31 - 1 keys",
+    if (c->page_size >= kMax31 || c->max_pages >= kMax31 || c->page_size * c->max_pages > kMaxCap)
+        return fail(SDPA_ERR_UNSUPPORTED, "cache capacity max_pages * page_size = %lld * %lld: at most 2^31 - 2^16 keys",
                     (long long)c->max_pages, (long long)c->page_size);
     if (c->b >= kMax31 || c->h_kv >= kMax31 || c->b * c->h_kv >= kMax31)
         return fail(SDPA_ERR_UNSUPPORTED, "cache b * h_kv = %lld * %lld: at most 2^31 - 1", (long long)c->b,
@@ -114,6 +119,9 @@ swa::CacheView view_of(const sdpa_cache* c)
     v.n_pages = c->n_pages;
     v.page_size = static_cast<uint32_t>(c->page_size);
     v.max_pages = static_cast<uint32_t>(c->max_pages);
+    v.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (c->page_size == int64_t(1) << i) v.page_shift = i;
     v.cap = c->page_size * c->max_pages;
     v.k = static_cast<uint16_t*>(c->k);
     v.v = static_cast<uint16_t*>(c->v);
@@ -143,6 +151,40 @@ sdpa_status_t check_rows(const sdpa_cache* c, int64_t s_q, int64_t h_q, int64_t 
     return SDPA_OK;
 }
 
+// Most key tiles of a forward: over all units, as many as the room and the
+// window allow, and the new tokens' (in floating point: it cannot overflow).
+double fwd_tiles(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa::CacheFwdPlan& plan)
+{
+    int64_t keys = c->page_size * c->max_pages;
+    if (p->window_left >= 0 && c->positions == nullptr && p->window_left < keys) keys = p->window_left;
+    const int64_t rows = p->s_q * (p->h_q / c->h_kv);
+    const int64_t blocks = (rows + plan.rows - 1) / plan.rows;
+    // the reach begins and the new tokens end up to 15 keys off a group of 16
+    const int64_t tiles = (keys + 30 + ((p->s_q + 15) & ~int64_t(15)) + plan.tile - 1) / plan.tile;
+    return double(c->b) * double(c->h_kv) * double(blocks) * double(tiles);
+}
+
+struct FwdLayout {
+    int32_t parts;
+    size_t part_o, part_ml, cuts, total;
+};
+
+// As many parts as CTAs are resident on a GB300 (152 SMs), fewer if there are
+// fewer tiles; each has two partials.
+FwdLayout fwd_layout(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa::CacheFwdPlan& plan)
+{
+    FwdLayout l{};
+    const double tiles = fwd_tiles(c, p, plan);
+    l.parts = 152 * plan.occ;
+    if (tiles < l.parts) l.parts = tiles < 1 ? 1 : static_cast<int32_t>(tiles);
+    const size_t rows = static_cast<size_t>(l.parts) * 2 * plan.rows;
+    l.part_o = 0;
+    l.part_ml = align256(rows * c->d * 4);
+    l.cuts = align256(l.part_ml + rows * 8);
+    l.total = align256(l.cuts + l.parts * sizeof(swa::CacheFwdCut));
+    return l;
+}
+
 sdpa_status_t check_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p)
 {
     sdpa_status_t st = check_cache(c);
@@ -156,6 +198,9 @@ sdpa_status_t check_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p)
         {"q", p->q_stride}, {"k", p->k_stride}, {"v", p->v_stride}, {"o", p->o_stride}};
     for (const auto& x : strides)
         if ((st = check_strides(x.n, x.s)) != SDPA_OK) return st;
+    const swa::CacheFwdPlan plan = swa::cache_fwd_plan(c->d, p->s_q * (p->h_q / c->h_kv));
+    if (fwd_tiles(c, p, plan) >= double(int64_t(1) << 50))
+        return fail(SDPA_ERR_UNSUPPORTED, "the forward's tiles (b * h_kv * row blocks * keys) pass 2^50");
     return SDPA_OK;
 }
 
@@ -219,9 +264,6 @@ EvictLayout evict_layout(const sdpa_cache* c, const sdpa_cache_evict_params* p)
     return l;
 }
 
-template <typename T>
-T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
-
 }  // namespace
 
 extern "C" {
@@ -236,7 +278,7 @@ size_t sdpa_cache_fwd_workspace_bytes(const sdpa_cache* c, const sdpa_cache_fwd_
 {
     if (check_fwd(c, p) != SDPA_OK) return 0;
     clear_error();
-    return 256;
+    return fwd_layout(c, p, swa::cache_fwd_plan(c->d, p->s_q * (p->h_q / c->h_kv))).total;
 }
 
 sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p, void* ws, size_t ws_bytes,
@@ -244,7 +286,8 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
 {
     sdpa_status_t st = check_fwd(c, p);
     if (st != SDPA_OK) return st;
-    if ((st = check_ws(ws, ws_bytes, 256)) != SDPA_OK) return st;
+    const FwdLayout l = fwd_layout(c, p, swa::cache_fwd_plan(c->d, p->s_q * (p->h_q / c->h_kv)));
+    if ((st = check_ws(ws, ws_bytes, l.total)) != SDPA_OK) return st;
     int dev = 0;
     if ((st = current_device(&dev)) != SDPA_OK) return st;
     const bool rows = c->b > 0;
@@ -258,8 +301,8 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.s_q = static_cast<int32_t>(p->s_q);
     a.h_q = static_cast<int32_t>(p->h_q);
     a.group = static_cast<int32_t>(p->h_q / c->h_kv);
-    a.window_left = p->window_left;
-    a.scale = p->scale;
+    // positions stay below 2^31 and rows within 64 of it: a wider window is none
+    a.window_left = p->window_left < (int64_t(1) << 32) ? p->window_left : -1;
     a.scale_log2 = p->scale * 1.4426950408889634f;
     a.q = static_cast<const uint16_t*>(p->q);
     a.k = static_cast<const uint16_t*>(p->k);
@@ -273,6 +316,10 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.sink = p->sink;
     a.o = static_cast<uint16_t*>(p->o);
     a.lse = p->lse;
+    a.parts = l.parts;
+    a.part_o = at<float>(ws, l.part_o);
+    a.part_ml = at<float>(ws, l.part_ml);
+    a.cuts = at<swa::CacheFwdCut>(ws, l.cuts);
     return cuda_status(swa::launch_cache_fwd(a, c->dtype, static_cast<cudaStream_t>(stream)), "cache forward launch");
 }
 

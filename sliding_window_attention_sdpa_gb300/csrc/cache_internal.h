@@ -13,6 +13,7 @@ struct CacheView {
     int64_t b, h_kv, d;
     int64_t n_pages;
     uint32_t page_size, max_pages;
+    int32_t page_shift;             // log2 of page_size if it is a power of two, else -1
     int64_t cap;                    // max_pages * page_size, < 2^31
     uint16_t *k, *v;
     int64_t k_stride[3], v_stride[3];   // page, row, head
@@ -22,11 +23,27 @@ struct CacheView {
     int32_t* status;
 };
 
+// A unit of the forward's work that is cut between parts: its sequence (-1:
+// none), its number in the sequence, the last part that has some of it, and
+// which of the first part's two partials is the unit's.
+struct CacheFwdCut {
+    int64_t bi, un;
+    int32_t last, slot0;
+};
+
+// Kernel for a head dimension and a kv-head's number of rows: rows of a unit,
+// keys of a tile, CTAs per SM.
+enum CacheFwdVariant { kRows128x8, kRows128x16, kRows64x8, kRows64x16, kRows64x32 };
+struct CacheFwdPlan {
+    int variant, rows, tile, occ;
+};
+CacheFwdPlan cache_fwd_plan(int64_t d, int64_t rows);
+
 struct CacheFwdArgs {
     CacheView c;
     int32_t s_q, h_q, group;
     int64_t window_left;
-    float scale, scale_log2;
+    float scale_log2;
     const uint16_t *q, *k, *v;
     int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
     const int64_t* tree;
@@ -34,6 +51,11 @@ struct CacheFwdArgs {
     const float* sink;
     uint16_t* o;
     float* lse;
+    // workspace: per part two partials [rows][d] with their (reference, sum),
+    // and the cut that the part names
+    int32_t parts;
+    float *part_o, *part_ml;
+    CacheFwdCut* cuts;
 };
 
 struct CacheAppendArgs {

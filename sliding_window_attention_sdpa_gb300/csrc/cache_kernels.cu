@@ -1,5 +1,4 @@
-// cache_kernels.cu -- the cache's plain kernels: append, evict, and the
-// simplest forms of forward and weigh (one warp per row, one warp per key).
+// cache_kernels.cu -- append, evict and weigh on the paged cache.
 #include "cache.cuh"
 #include "ptx.cuh"
 
@@ -8,7 +7,6 @@ namespace swa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float warp_sum(float x)
 {
@@ -18,98 +16,6 @@ __device__ __forceinline__ float warp_sum(float x)
 }
 
 }  // namespace
-
-// ---------------------------------------------------------------- forward
-
-template <int HD, bool BF16>
-__global__ void __launch_bounds__(128) cache_fwd_kernel(const CacheFwdArgs a)
-{
-    constexpr int E = HD / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    if (row >= a.c.b * a.s_q * a.h_q) return;
-    const int64_t h = row % a.h_q, bt = row / a.h_q, t = bt % a.s_q, bi = bt / a.s_q;
-    const int64_t g = h / a.group;
-    bool bad;
-    const int32_t len = cache_length(a.c, bi, bad);
-    int32_t nq = a.seq_q_lens ? a.seq_q_lens[bi] : a.s_q;
-    if (nq < 0 || nq > a.s_q) {
-        set_status(a.c.status, SDPA_ERR_BAD_LENGTHS);
-        nq = nq < 0 ? 0 : a.s_q;
-    }
-    const uint64_t in = nq == 64 ? ~0ull : (1ull << nq) - 1;
-    auto mask_of = [&](int64_t u) -> uint64_t {
-        return in & (a.tree ? static_cast<uint64_t>(a.tree[bi * a.s_q + u]) : (2ull << u) - 1);
-    };
-    const uint64_t mask = t < nq ? mask_of(t) : 0;
-    const bool live = (mask >> t) & 1;
-    const int64_t depth = __popcll(mask) - 1;
-    const int64_t pos = (a.c.next_pos ? a.c.next_pos[bi] : len) + depth;
-    float q[E], o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = to_float<BF16>(a.q[bi * a.q_stride[0] + t * a.q_stride[1] + h * a.q_stride[2] + lane * E + e]);
-        o[e] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    auto key = [&](const uint16_t* kp, const uint16_t* vp) {
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s += q[e] * to_float<BF16>(kp[lane * E + e]);
-        s = warp_sum(s) * a.scale_log2;
-        const float mn = fmaxf(m, s), al = m == -INFINITY ? 0.f : exp2f(m - mn), p = exp2f(s - mn);
-        l = l * al + p;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * al + p * to_float<BF16>(vp[lane * E + e]);
-        m = mn;
-    };
-    if (live) {
-        for (int32_t j = 0; j < len; ++j) {
-            const int64_t kpos = a.c.positions ? a.c.positions[(bi * a.c.h_kv + g) * a.c.cap + j] : j;
-            if (a.window_left >= 0 && pos - kpos > a.window_left) continue;
-            uint32_t r;
-            const int64_t page = cache_page(a.c, bi, j, r);
-            if (page < 0) continue;
-            key(a.c.k + page * a.c.k_stride[0] + r * a.c.k_stride[1] + g * a.c.k_stride[2],
-                a.c.v + page * a.c.v_stride[0] + r * a.c.v_stride[1] + g * a.c.v_stride[2]);
-        }
-        for (int64_t u = 0; u < nq; ++u) {
-            if (!((mask >> u) & 1)) continue;
-            if (a.window_left >= 0 && depth - (__popcll(mask_of(u)) - 1) > a.window_left) continue;
-            key(a.k + bi * a.k_stride[0] + u * a.k_stride[1] + g * a.k_stride[2],
-                a.v + bi * a.v_stride[0] + u * a.v_stride[1] + g * a.v_stride[2]);
-        }
-    }
-    float mf = m, lt = l;
-    if (a.sink != nullptr && t < nq) {
-        const float sk = a.sink[h] * kLog2e;
-        mf = fmaxf(m, sk);
-        lt = (m == -INFINITY ? 0.f : l * exp2f(m - mf)) + exp2f(sk - mf);
-    }
-    const float mul = l > 0.f ? exp2f(m - mf) / lt : 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        a.o[bi * a.o_stride[0] + t * a.o_stride[1] + h * a.o_stride[2] + lane * E + e] = from_float<BF16>(o[e] * mul);
-    if (lane == 0) {
-        float lse = lt > 0.f ? (mf + log2f(lt)) * kLn2 : -INFINITY;
-        if (m == -INFINITY && a.sink != nullptr && t < nq) lse = a.sink[h];   // no key: the sink itself
-        a.lse[(bi * a.h_q + h) * a.s_q + t] = lse;
-    }
-}
-
-cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int dtype, cudaStream_t s)
-{
-    const unsigned grid = static_cast<unsigned>((a.c.b * a.s_q * a.h_q + 3) / 4);
-    if (grid == 0) return cudaSuccess;
-    if (a.c.d == 64) {
-        if (dtype == SDPA_BF16) cache_fwd_kernel<64, true><<<grid, 128, 0, s>>>(a);
-        else cache_fwd_kernel<64, false><<<grid, 128, 0, s>>>(a);
-    } else {
-        if (dtype == SDPA_BF16) cache_fwd_kernel<128, true><<<grid, 128, 0, s>>>(a);
-        else cache_fwd_kernel<128, false><<<grid, 128, 0, s>>>(a);
-    }
-    return cudaGetLastError();
-}
 
 // ---------------------------------------------------------------- weigh
 
