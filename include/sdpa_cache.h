@@ -105,9 +105,11 @@ typedef struct sdpa_cache_fwd_params {
     float *lse;                          /* device fp32 [b][h_q][s_q], contiguous */
 } sdpa_cache_fwd_params;
 
-/* Workspace of sdpa_cache_fwd in bytes on the current device (0 on invalid
- * arguments); needs no initialisation, 256-byte aligned. Calls that may overlap
- * on the GPU (other streams, two graphs) need a workspace each. */
+/* Workspace of sdpa_cache_fwd in bytes: 0 on invalid arguments (then
+ * sdpa_bwd_last_error() names one) and where none is needed (it is empty, and
+ * the workspace may be NULL). It needs no initialisation and is 256-byte
+ * aligned. Calls that may overlap on the GPU (other streams, two graphs) need a
+ * workspace each. */
 size_t sdpa_cache_fwd_workspace_bytes(const sdpa_cache *cache, const sdpa_cache_fwd_params *params);
 sdpa_status_t sdpa_cache_fwd(const sdpa_cache *cache, const sdpa_cache_fwd_params *params, void *workspace,
                              size_t workspace_bytes, void *stream);

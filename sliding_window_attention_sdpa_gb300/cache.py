@@ -17,6 +17,7 @@ A decoding step of a model that drafts tokens:
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 _i64x3 = ctypes.c_int64 * 3
@@ -100,6 +101,41 @@ def _check(code: int, where: str) -> None:
         raise SdpaError(code, where, last_error())
 
 
+class _Calls:
+    """The entry points with their parameter blocks as packed bytes (the layout
+    of the structs above), and torch's current stream: filling a ctypes
+    structure field by field costs more than the smallest call's kernel."""
+
+    def __init__(self):
+        import torch
+        lib = _lib()
+        for name in ("fwd", "evict"):
+            f = lib[f"sdpa_cache_{name}"]
+            f.argtypes, f.restype = [_vp, ctypes.c_char_p, _vp, ctypes.c_size_t, _vp], ctypes.c_int
+            setattr(self, name, f)
+        for name in ("append", "weigh"):
+            f = lib[f"sdpa_cache_{name}"]
+            f.argtypes, f.restype = [_vp, ctypes.c_char_p, _vp], ctypes.c_int
+            setattr(self, name, f)
+        self.empty, self.float32, self.int32, self.int64, self.uint8 = (
+            torch.empty, torch.float32, torch.int32, torch.int64, torch.uint8)
+        self.stream = torch._C._cuda_getCurrentRawStream
+
+
+_FWD = struct.Struct("3qfi3Q12q5Q")
+_APPEND = struct.Struct("2i3q2Q6q3Q")
+_WEIGH = struct.Struct("3qfiQ3q2Q")
+_EVICT = struct.Struct("3q")
+_calls = None
+
+
+def _c() -> _Calls:
+    global _calls
+    if _calls is None:
+        _calls = _Calls()
+    return _calls
+
+
 # ----------------------------------------------------- one-to-one C entry points
 
 def sdpa_cache_fwd_workspace_bytes(cache: SdpaCache, params: SdpaCacheFwdParams) -> int:
@@ -132,31 +168,33 @@ def sdpa_cache_check_status(cache, stream: int) -> int:
 
 # ------------------------------------------------------------- torch helpers
 
+def _wrong(name, t, shape, device, dtype):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    raise ValueError(f"{name}: expected device {device}, got {t.device}")
+
+
 def _strides(name, t, shape, device, dtype):
     """Element strides of all but the feature dimension of a tensor of this
     shape; 0 where the dimension has no second entry to address."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        _wrong(name, t, shape, device, dtype)
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}: the feature dimension must be contiguous (stride 1)")
-    return [s if n > 1 else 0 for s, n in zip(st[:-1], shape)]
+    if 1 in shape:
+        return [s if n > 1 else 0 for s, n in zip(st[:-1], shape)]
+    return st[:-1]
 
 
 def _flat(name, t, shape, device, dtype):
-    """Address of a contiguous array of this shape and type; None for None."""
+    """Address of a contiguous array of this shape and type; 0 for None."""
     if t is None:
-        return None
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+        return 0
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        _wrong(name, t, shape, device, dtype)
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
@@ -219,6 +257,8 @@ class KVCache:
         self.next_pos, self.positions, self.weights = next_pos, positions, weights
         self.b, self.h_kv, self.d, self.dtype, self.device = b, h_kv, d, k.dtype, dev
         self.params = c
+        self._ref, self._key, self._index = ctypes.addressof(c), (b, h_kv, d, dev, k.dtype), dev.index or 0
+        self._ws_bytes = {}     # workspace bytes of the calls made so far, by their sizes
 
     @classmethod
     def empty(cls, b: int, h_kv: int, d: int, max_len: int, *, dtype, device, page_size: int = 64,
@@ -244,16 +284,22 @@ class KVCache:
                "sdpa_cache_check_status")
 
 
-def _workspace(n, cache, workspace, where):
-    import torch
+def _workspace(cache, key, size, workspace, c):
+    """Address and bytes of the workspace: the caller's, or a new tensor of the
+    bytes that `size()` says (kept by `key`, the arguments it depends on)."""
     if workspace is not None:
-        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        if workspace.dtype is not c.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace: expected a contiguous uint8 tensor")
         return workspace
-    if n == 0:
-        from . import SDPA_ERR_INVALID_ARG, SdpaError, last_error
-        raise SdpaError(SDPA_ERR_INVALID_ARG, where, last_error())
-    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    n = cache._ws_bytes.get(key)
+    if n is None:
+        n = size()
+        if n == 0:
+            from . import SDPA_ERR_INVALID_ARG, SdpaError, last_error
+            if last_error():
+                raise SdpaError(SDPA_ERR_INVALID_ARG, f"sdpa_cache_{key[0]}_workspace_bytes", last_error())
+        cache._ws_bytes[key] = n
+    return c.empty(n, dtype=c.uint8, device=cache.device) if n else None
 
 
 def cache_forward(cache: KVCache, q, k, v, *, scale: float, window_left: int = -1, tree=None, seq_q_lens=None,
@@ -267,32 +313,32 @@ def cache_forward(cache: KVCache, q, k, v, *, scale: float, window_left: int = -
     seq_q_lens: int32 [b] real rows of each sequence; sink: fp32 [h_q].
     Returns (o, lse) with o like q and lse fp32 [b, h_q, s_q].
     """
-    import torch
+    c = _calls or _c()
     if q.dim() != 4:
         raise ValueError(f"q: expected [b, s_q, h_q, d], got {tuple(q.shape)}")
-    b, s_q, h_q, d = q.shape
-    dev, dt = cache.device, cache.dtype
-    kv = (cache.b, s_q, cache.h_kv, cache.d)
-    p = SdpaCacheFwdParams(
-        s_q, h_q, window_left, scale, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-        _i64x3(*_strides("q", q, (cache.b, s_q, h_q, cache.d), dev, dt)), _i64x3(*_strides("k", k, kv, dev, dt)),
-        _i64x3(*_strides("v", v, kv, dev, dt)))
+    _, s_q, h_q, _ = q.shape
+    b, h_kv, d, dev, dt = cache._key
+    rows, kv = (b, s_q, h_q, d), (b, s_q, h_kv, d)
+    sq = _strides("q", q, rows, dev, dt)
+    sk = _strides("k", k, kv, dev, dt)
+    sv = _strides("v", v, kv, dev, dt)
     if out is None:
-        out = torch.empty((b, s_q, h_q, d), dtype=dt, device=dev)
+        out = c.empty(rows, dtype=dt, device=dev)
+        so = (s_q * h_q * d, h_q * d, d)
     else:
         _apart("out", out)
+        so = _strides("out", out, rows, dev, dt)
     if lse is None:
-        lse = torch.empty((b, h_q, s_q), dtype=torch.float32, device=dev)
-    p.o_stride = _i64x3(*_strides("out", out, (b, s_q, h_q, d), dev, dt))
-    p.tree = _flat("tree", tree, (b, s_q), dev, torch.int64)
-    p.seq_q_lens = _flat("seq_q_lens", seq_q_lens, (b,), dev, torch.int32)
-    p.sink = _flat("sink", sink, (h_q,), dev, torch.float32)
-    p.o, p.lse = out.data_ptr(), _flat("lse", lse, (b, h_q, s_q), dev, torch.float32)
-    c = cache.params
-    workspace = _workspace(0 if workspace is not None else sdpa_cache_fwd_workspace_bytes(c, p), cache, workspace,
-                           "sdpa_cache_fwd_workspace_bytes")
-    _check(sdpa_cache_fwd(c, p, workspace.data_ptr(), workspace.numel(),
-                          torch.cuda.current_stream(dev).cuda_stream), "sdpa_cache_fwd")
+        lse = c.empty((b, h_q, s_q), dtype=c.float32, device=dev)
+    p = _FWD.pack(s_q, h_q, window_left, scale, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), *sq, *sk, *sv, *so,
+                  _flat("tree", tree, (b, s_q), dev, c.int64), _flat("seq_q_lens", seq_q_lens, (b,), dev, c.int32),
+                  _flat("sink", sink, (h_q,), dev, c.float32), out.data_ptr(),
+                  _flat("lse", lse, (b, h_q, s_q), dev, c.float32))
+    ws = _workspace(cache, ("fwd", s_q, h_q, window_left),
+                    lambda: sdpa_cache_fwd_workspace_bytes(cache.params, SdpaCacheFwdParams.from_buffer_copy(p)),
+                    workspace, c)
+    _check(c.fwd(cache._ref, p, ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0,
+                 c.stream(cache._index)), "sdpa_cache_fwd")
     if check_status:
         cache.check_status()
     return out, lse
@@ -308,38 +354,33 @@ def cache_append(cache: KVCache, k, v, *, index=None, counts=None, offsets=None,
     [total, h_kv, d] with offsets (int32 [b + 1]) and max_seqlen, the most rows
     of a sequence.
     """
-    import torch
-    from . import SDPA_BSHD, SDPA_THD
-    dev, dt, b = cache.device, cache.dtype, cache.b
-    i32 = torch.int32
-    p = SdpaCacheAppendParams()
+    c = _calls or _c()
+    b, h_kv, d, dev, dt = cache._key
+    n = total = 0
     if k.dim() == 3:
         if offsets is None or max_seqlen is None:
             raise ValueError("packed k, v need offsets and max_seqlen")
-        shape = (k.shape[0], cache.h_kv, cache.d)
-        p.layout, p.s, p.total = SDPA_THD, max_seqlen, k.shape[0]
-        p.k_stride = _i64x3(0, *_strides("k", k, shape, dev, dt))
-        p.v_stride = _i64x3(0, *_strides("v", v, shape, dev, dt))
-        p.offsets = _flat("offsets", offsets, (b + 1,), dev, i32)
+        layout, s, total = 1, max_seqlen, k.shape[0]
+        shape = (total, h_kv, d)
+        sk, sv = (0, *_strides("k", k, shape, dev, dt)), (0, *_strides("v", v, shape, dev, dt))
     else:
         if offsets is not None:
             raise ValueError("offsets: only with packed k, v ([total, h_kv, d])")
         if k.dim() != 4:
             raise ValueError(f"k: expected [b, s, h_kv, d] or [total, h_kv, d], got {tuple(k.shape)}")
-        shape = (b, k.shape[1], cache.h_kv, cache.d)
-        p.layout, p.s = SDPA_BSHD, k.shape[1]
-        p.k_stride = _i64x3(*_strides("k", k, shape, dev, dt))
-        p.v_stride = _i64x3(*_strides("v", v, shape, dev, dt))
+        layout, s = 0, k.shape[1]
+        shape = (b, s, h_kv, d)
+        sk, sv = _strides("k", k, shape, dev, dt), _strides("v", v, shape, dev, dt)
     if index is not None:
         if index.dim() != 2:
             raise ValueError("index: expected [b, n]")
-        p.n = index.shape[1]
-        p.index = _flat("index", index, (b, index.shape[1]), dev, i32)
-        if index.numel() == 0:
-            return      # no row of any sequence
-    p.counts = _flat("counts", counts, (b,), dev, i32)
-    p.k, p.v = k.data_ptr(), v.data_ptr()
-    _check(sdpa_cache_append(cache.params, p, torch.cuda.current_stream(dev).cuda_stream), "sdpa_cache_append")
+        n = index.shape[1]
+    p = _APPEND.pack(layout, 0, s, n, total, k.data_ptr(), v.data_ptr(), *sk, *sv,
+                     _flat("index", index, (b, n), dev, c.int32), _flat("counts", counts, (b,), dev, c.int32),
+                     _flat("offsets", offsets, (b + 1,), dev, c.int32))
+    if index is not None and n == 0:
+        return      # no row of any sequence
+    _check(c.append(cache._ref, p, c.stream(cache._index)), "sdpa_cache_append")
     if check_status:
         cache.check_status()
 
@@ -352,16 +393,14 @@ def cache_weigh(cache: KVCache, q, lse, *, scale: float, window_left: int = -1, 
     forward took and gave them; q_pos: int32 [b, s_q] positions of the rows
     (negative: the row does not count), or None for the last s_q tokens.
     """
-    import torch
+    c = _calls or _c()
     if q.dim() != 4:
         raise ValueError(f"q: expected [b, s_q, h_q, d], got {tuple(q.shape)}")
     _, s_q, h_q, _ = q.shape
-    dev, b = cache.device, cache.b
-    p = SdpaCacheWeighParams(
-        s_q, h_q, window_left, scale, 0, q.data_ptr(),
-        _i64x3(*_strides("q", q, (b, s_q, h_q, cache.d), dev, cache.dtype)),
-        _flat("lse", lse, (b, h_q, s_q), dev, torch.float32), _flat("q_pos", q_pos, (b, s_q), dev, torch.int32))
-    _check(sdpa_cache_weigh(cache.params, p, torch.cuda.current_stream(dev).cuda_stream), "sdpa_cache_weigh")
+    b, _, d, dev, dt = cache._key
+    p = _WEIGH.pack(s_q, h_q, window_left, scale, 0, q.data_ptr(), *_strides("q", q, (b, s_q, h_q, d), dev, dt),
+                    _flat("lse", lse, (b, h_q, s_q), dev, c.float32), _flat("q_pos", q_pos, (b, s_q), dev, c.int32))
+    _check(c.weigh(cache._ref, p, c.stream(cache._index)), "sdpa_cache_weigh")
     if check_status:
         cache.check_status()
 
@@ -371,12 +410,12 @@ def cache_evict(cache: KVCache, keep: int, *, first: int = 0, recent: int = 0, w
     """Brings each sequence that holds more than `keep` keys back to `keep`:
     the keys at positions below `first`, the `recent` last positions and the
     heaviest of the others stay, for each kv-head on its own."""
-    import torch
-    p = SdpaCacheEvictParams(keep, first, recent)
-    c = cache.params
-    workspace = _workspace(0 if workspace is not None else sdpa_cache_evict_workspace_bytes(c, p), cache, workspace,
-                           "sdpa_cache_evict_workspace_bytes")
-    _check(sdpa_cache_evict(c, p, workspace.data_ptr(), workspace.numel(),
-                            torch.cuda.current_stream(cache.device).cuda_stream), "sdpa_cache_evict")
+    c = _calls or _c()
+    p = _EVICT.pack(keep, first, recent)
+    ws = _workspace(cache, ("evict", keep, first, recent),
+                    lambda: sdpa_cache_evict_workspace_bytes(cache.params, SdpaCacheEvictParams.from_buffer_copy(p)),
+                    workspace, c)
+    _check(c.evict(cache._ref, p, ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0,
+                   c.stream(cache._index)), "sdpa_cache_evict")
     if check_status:
         cache.check_status()

@@ -151,32 +151,49 @@ sdpa_status_t check_rows(const sdpa_cache* c, int64_t s_q, int64_t h_q, int64_t 
     return SDPA_OK;
 }
 
-// Most key tiles of a forward: over all units, as many as the room and the
-// window allow, and the new tokens' (in floating point: it cannot overflow).
-double fwd_tiles(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa::CacheFwdPlan& plan)
+// Sizes of a forward's work: its units (a kv-head's block of rows), the most
+// key tiles that one has (as many as the room and the window allow, and the new
+// tokens'), their product in floating point (it cannot overflow).
+struct FwdSize {
+    int64_t blocks, tiles;
+    double units, total;
+};
+
+FwdSize fwd_size(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa::CacheFwdPlan& plan)
 {
+    FwdSize z{};
     int64_t keys = c->page_size * c->max_pages;
     if (p->window_left >= 0 && c->positions == nullptr && p->window_left < keys) keys = p->window_left;
     const int64_t rows = p->s_q * (p->h_q / c->h_kv);
-    const int64_t blocks = (rows + plan.rows - 1) / plan.rows;
+    z.blocks = (rows + plan.rows - 1) / plan.rows;
     // the reach begins and the new tokens end up to 15 keys off a group of 16
-    const int64_t tiles = (keys + 30 + ((p->s_q + 15) & ~int64_t(15)) + plan.tile - 1) / plan.tile;
-    return double(c->b) * double(c->h_kv) * double(blocks) * double(tiles);
+    z.tiles = (keys + 30 + ((p->s_q + 15) & ~int64_t(15)) + plan.tile - 1) / plan.tile;
+    z.units = double(c->b) * double(c->h_kv) * double(z.blocks);
+    z.total = z.units * double(z.tiles);
+    return z;
 }
 
 struct FwdLayout {
-    int32_t parts;
+    int32_t parts, whole;
     size_t part_o, part_ml, cuts, total;
 };
 
-// As many parts as CTAs are resident on a GB300 (152 SMs), fewer if there are
+// Units of up to kWholeTiles tiles go to one CTA each. Else the work is cut into
+// as many parts as CTAs are resident on a GB300 (152 SMs), fewer if there are
 // fewer tiles; each has two partials.
+constexpr int64_t kWholeTiles = 4;
+
 FwdLayout fwd_layout(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa::CacheFwdPlan& plan)
 {
     FwdLayout l{};
-    const double tiles = fwd_tiles(c, p, plan);
+    const FwdSize z = fwd_size(c, p, plan);
+    if (z.tiles <= kWholeTiles && z.units < double(kMax31)) {
+        l.parts = static_cast<int32_t>(z.units);
+        l.whole = 1;
+        return l;
+    }
     l.parts = 152 * plan.occ;
-    if (tiles < l.parts) l.parts = tiles < 1 ? 1 : static_cast<int32_t>(tiles);
+    if (z.total < l.parts) l.parts = z.total < 1 ? 1 : static_cast<int32_t>(z.total);
     const size_t rows = static_cast<size_t>(l.parts) * 2 * plan.rows;
     l.part_o = 0;
     l.part_ml = align256(rows * c->d * 4);
@@ -199,7 +216,7 @@ sdpa_status_t check_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p)
     for (const auto& x : strides)
         if ((st = check_strides(x.n, x.s)) != SDPA_OK) return st;
     const swa::CacheFwdPlan plan = swa::cache_fwd_plan(c->d, p->s_q * (p->h_q / c->h_kv));
-    if (fwd_tiles(c, p, plan) >= double(int64_t(1) << 50))
+    if (fwd_size(c, p, plan).total >= double(int64_t(1) << 50))
         return fail(SDPA_ERR_UNSUPPORTED, "the forward's tiles (b * h_kv * row blocks * keys) pass 2^50");
     return SDPA_OK;
 }
@@ -239,6 +256,7 @@ sdpa_status_t check_evict(const sdpa_cache* c, const sdpa_cache_evict_params* p)
 
 sdpa_status_t check_ws(const void* ws, size_t have, size_t need)
 {
+    if (need == 0) return SDPA_OK;
     if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
         return fail(SDPA_ERR_WORKSPACE, "workspace=%p must be non-NULL and 256-byte aligned", ws);
     if (have < need) return fail(SDPA_ERR_WORKSPACE, "workspace_bytes=%zu, need %zu", have, need);
@@ -293,7 +311,7 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     const bool rows = c->b > 0;
     const Ptr ptrs[] = {{"q", p->q, rows, 16},     {"k", p->k, rows, 16},           {"v", p->v, rows, 16},
                         {"o", p->o, rows, 16},     {"lse", p->lse, rows, 4},        {"tree", p->tree, false, 8},
-                        {"sink", p->sink, false, 4}, {"seq_q_lens", p->seq_q_lens, false, 4}, {"workspace", ws, true, 256}};
+                        {"sink", p->sink, false, 4}, {"seq_q_lens", p->seq_q_lens, false, 4}, {"workspace", ws, l.total > 0, 256}};
     if ((st = check_cache_ptrs(c, dev)) != SDPA_OK || (st = check_ptrs(ptrs, dev)) != SDPA_OK) return st;
     if (!rows) return SDPA_OK;
     swa::CacheFwdArgs a{};
@@ -317,6 +335,7 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.o = static_cast<uint16_t*>(p->o);
     a.lse = p->lse;
     a.parts = l.parts;
+    a.whole = l.whole;
     a.part_o = at<float>(ws, l.part_o);
     a.part_ml = at<float>(ws, l.part_ml);
     a.cuts = at<swa::CacheFwdCut>(ws, l.cuts);

@@ -213,24 +213,28 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
     const int64_t units = a.c.h_kv * blocks;      // per sequence
 
     // ---- this CTA's part of the line
-    Line line;
-    {
+    Line line{0};
+    int64_t parts = 1, at = 0, end = 0, bi = 0, rem = 0;
+    CacheFwdCut cut{-1, 0, 0, 0};
+    if (a.whole) {
+        // short units: a CTA takes one from end to end, nothing is cut
+        bi = blockIdx.x / units;
+        const int64_t n = seq_view(a, bi, TK).tiles;
+        rem = (blockIdx.x - bi * units) * n;
+        end = n;
+    } else {
         int64_t s = 0;
         for (int64_t i = tid; i < a.c.b; i += kThreads) s += seq_view(a, i, TK).tiles;
         line.total = block_sum64<kThreads>(s, sh_sum) * units;
-    }
-    const int64_t parts = imin64(gridDim.x, line.total);   // every part has a tile
-    int64_t at = line.start(blockIdx.x, parts);
-    const int64_t end = line.start(blockIdx.x + 1, parts);
-    const int64_t part0 = at;
-    CacheFwdCut cut{-1, 0, 0, 0};
-    if (blockIdx.x >= parts) {
-        if (tid == 0) a.cuts[blockIdx.x] = cut;
-        grid_dep_launch();
-        return;
-    }
-    int64_t bi, rem;
-    {
+        parts = imin64(gridDim.x, line.total);   // every part has a tile
+        if (blockIdx.x >= parts) {
+            if (tid == 0) a.cuts[blockIdx.x] = cut;
+            grid_dep_launch();
+            return;
+        }
+        at = line.start(blockIdx.x, parts);
+        end = line.start(blockIdx.x + 1, parts);
+        // the sequence that holds the part's first tile
         int64_t before = 0;
         for (int64_t base = 0; base < a.c.b; base += kThreads) {
             const int64_t i = base + tid;
@@ -257,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
         bi = sh_at[0];
         rem = sh_at[1];
     }
+    const int64_t part0 = at;
 
     SeqView sv{};
     int64_t cur = -1;
@@ -625,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
             rem = 0;
         }
     }
+    if (a.whole) return;
     if (tid == 0) a.cuts[blockIdx.x] = cut;
     grid_dep_launch();
 }
@@ -705,7 +711,7 @@ cudaError_t launch_rows(const CacheFwdArgs& a, cudaStream_t s)
     const int64_t units = a.c.b * a.c.h_kv * blocks;
     cache_fwd_rows_kernel<HD, BF16, NT, OCC><<<a.parts, kThreads, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || a.parts == 1) return e;
+    if (e != cudaSuccess || a.whole || a.parts == 1) return e;
     // with an eighth as many units as parts a unit has few cuts
     const bool spread = units * 8 < a.parts;
     cudaLaunchConfig_t cfg{};

@@ -53,7 +53,7 @@ struct CacheFwdArgs {
     float* lse;
     // workspace: per part two partials [rows][d] with their (reference, sum),
     // and the cut that the part names
-    int32_t parts;
+    int32_t parts, whole;   // whole: one unit per CTA, no workspace
     float *part_o, *part_ml;
     CacheFwdCut* cuts;
 };

@@ -153,11 +153,16 @@ def test_evict_refusals(keep, first, recent):
 
 
 def test_workspace_refusals():
-    n = swa.sdpa_cache_fwd_workspace_bytes(cache(), fwd())
+    big = cache(max_pages=1000)
+    n = swa.sdpa_cache_fwd_workspace_bytes(big, fwd())
     assert n > 0 and n % 256 == 0
-    refused(WS, swa.sdpa_cache_fwd(cache(), fwd(), 0, n, 0), "workspace")
-    refused(WS, swa.sdpa_cache_fwd(cache(), fwd(), 4096 + 16, n, 0), "aligned")
-    refused(WS, swa.sdpa_cache_fwd(cache(), fwd(), 4096, n - 1, 0), "need")
+    refused(WS, swa.sdpa_cache_fwd(big, fwd(), 0, n, 0), "workspace")
+    refused(WS, swa.sdpa_cache_fwd(big, fwd(), 4096 + 16, n, 0), "aligned")
+    refused(WS, swa.sdpa_cache_fwd(big, fwd(), 4096, n - 1, 0), "need")
+    # short ranges need none: 0 bytes and no message
+    for c, p in ((cache(), fwd()), (cache(max_pages=1000), fwd(window_left=64)), (cache(b=0), fwd())):
+        c.positions = c.next_pos = 0
+        assert swa.sdpa_cache_fwd_workspace_bytes(c, p) == 0 and swa.last_error() == ""
     e = swa.SdpaCacheEvictParams(4, 0, 0)
     n = swa.sdpa_cache_evict_workspace_bytes(cache(), e)
     assert n > 0
