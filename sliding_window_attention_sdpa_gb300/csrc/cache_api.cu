@@ -16,6 +16,7 @@ using swa::api::clear_error;
 using swa::api::cuda_status;
 using swa::api::fail;
 
+constexpr int64_t kWaitLimitNs = 2000000000LL;
 constexpr int64_t kMax31 = int64_t(1) << 31;
 // a sequence's keys, rounded up to tiles, are numbered in 32 bits
 constexpr int64_t kMaxCap = kMax31 - (int64_t(1) << 16);
@@ -336,6 +337,7 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.lse = p->lse;
     a.parts = l.parts;
     a.whole = l.whole;
+    a.timeout_ns = kWaitLimitNs;
     a.part_o = at<float>(ws, l.part_o);
     a.part_ml = at<float>(ws, l.part_ml);
     a.cuts = at<swa::CacheFwdCut>(ws, l.cuts);

@@ -30,18 +30,12 @@
 // sequences' lengths. A unit inside one part is finished there; a unit cut
 // between parts leaves fp32 partials (row reference, sum, O) that
 // cache_fwd_join_kernel adds in the order of the parts.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "cache.cuh"
-#include "ptx.cuh"
+#include "cache_fwd.cuh"
 
 namespace swa {
 
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 128;
 
 __device__ __forceinline__ uint32_t movm_trans(uint32_t x)
@@ -69,25 +63,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
-{
-    uint32_t r;
-    if constexpr (BF16)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-template <bool BF16>
-__device__ __forceinline__ float2 unpack2(uint32_t x)
-{
-    if constexpr (BF16) return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-    const __half2 h = *reinterpret_cast<const __half2*>(&x);
-    return __half22float2(h);
-}
-
 // 16 bytes that this kernel reads once.
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p)
 {
@@ -96,94 +71,6 @@ __device__ __forceinline__ uint4 ld_stream(const uint16_t* p)
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
-}
-
-// One sequence as the rows and keys of this call see it.
-struct SeqView {
-    int32_t len, nq;    // cached keys, new tokens
-    int32_t lo;         // first cached key in reach of any row, a multiple of 16
-    int32_t new0;       // place of new token 0 in the line of keys (lo ... ), a multiple of 16 from lo
-    int32_t tiles;
-};
-
-__device__ __forceinline__ SeqView seq_view(const CacheFwdArgs& a, int64_t bi, int tk)
-{
-    SeqView v;
-    bool bad;
-    v.len = cache_length(a.c, bi, bad);
-    v.nq = a.s_q;
-    if (a.seq_q_lens) {
-        v.nq = a.seq_q_lens[bi];
-        if (v.nq < 0 || v.nq > a.s_q) {
-            set_status(a.c.status, SDPA_ERR_BAD_LENGTHS);
-            v.nq = v.nq < 0 ? 0 : a.s_q;
-        }
-    }
-    // without positions the lowest row's window starts at len - W
-    v.lo = 0;
-    if (a.window_left >= 0 && a.c.positions == nullptr)
-        v.lo = static_cast<int32_t>(imax64(0, v.len - a.window_left)) & ~15;
-    const int64_t cached = ((static_cast<int64_t>(v.len) + 15) & ~int64_t(15)) - v.lo;
-    v.new0 = static_cast<int32_t>(cached);
-    v.tiles = static_cast<int32_t>((cached + ((max(v.nq, 1) + 15) & ~15) + tk - 1) / tk);
-    return v;
-}
-
-// The line of tiles: all sequences' units, cut evenly between the parts.
-struct Line {
-    int64_t total;
-    __device__ __forceinline__ int64_t start(int64_t c, int64_t parts) const { return c * total / parts; }
-    // the part that holds tile t
-    __device__ __forceinline__ int64_t part_of(int64_t t, int64_t parts) const { return ((t + 1) * parts - 1) / total; }
-};
-
-__device__ __forceinline__ int64_t warp_sum64(int64_t x)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
-// Sum of per-thread values over the CTA (every thread calls it).
-template <int THREADS>
-__device__ __forceinline__ int64_t block_sum64(int64_t x, int64_t* sh)
-{
-    x = warp_sum64(x);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
-    __syncthreads();
-    int64_t s = 0;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) s += sh[i];
-    return s;
-}
-
-// Finishes E features (from c) of a row: O and, with its first feature, LSE.
-// `top` is the reference of the row's exponentials (log2), -inf for no key.
-template <bool BF16, int E>
-__device__ __forceinline__ void store_row(const CacheFwdArgs& a, int64_t bi, int tok, int64_t h, int c, bool in_rows,
-                                          float top, float sum, const float (&x)[E])
-{
-    const bool sunk = a.sink != nullptr && in_rows;
-    float mf = top, lt = sum;
-    if (sunk) {
-        const float sk = a.sink[h] * kLog2e;
-        mf = fmaxf(top, sk);
-        lt = (top == -INFINITY ? 0.f : sum * ex2_approx(top - mf)) + ex2_approx(sk - mf);
-    }
-    const float mul = top == -INFINITY ? 0.f : ex2_approx(top - mf) / lt;
-    uint16_t* o = a.o + bi * a.o_stride[0] + tok * a.o_stride[1] + h * a.o_stride[2] + c;
-    uint32_t w[E / 2];
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) w[e] = pack2<BF16>(x[2 * e] * mul, x[2 * e + 1] * mul);
-    if constexpr (E == 8) *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-    else if constexpr (E == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(o) = w[0];
-    if (c == 0) {
-        // a row without a key: the sink itself, or -inf
-        const float lse = top == -INFINITY ? (sunk ? a.sink[h] : -INFINITY) : (mf + log2f(lt)) * kLn2;
-        a.lse[(bi * a.h_q + h) * a.s_q + tok] = lse;
-    }
 }
 
 }  // namespace
@@ -213,55 +100,24 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
     const int64_t units = a.c.h_kv * blocks;      // per sequence
 
     // ---- this CTA's part of the line
-    Line line{0};
-    int64_t parts = 1, at = 0, end = 0, bi = 0, rem = 0;
+    Part part{1, 0, 0, 0, 0, Line{0}};
     CacheFwdCut cut{-1, 0, 0, 0};
     if (a.whole) {
         // short units: a CTA takes one from end to end, nothing is cut
-        bi = blockIdx.x / units;
-        const int64_t n = seq_view(a, bi, TK).tiles;
-        rem = (blockIdx.x - bi * units) * n;
-        end = n;
+        part.bi = blockIdx.x / units;
+        part.end = seq_view(a, part.bi, TK).tiles;
+        part.rem = (blockIdx.x - part.bi * units) * part.end;
     } else {
-        int64_t s = 0;
-        for (int64_t i = tid; i < a.c.b; i += kThreads) s += seq_view(a, i, TK).tiles;
-        line.total = block_sum64<kThreads>(s, sh_sum) * units;
-        parts = imin64(gridDim.x, line.total);   // every part has a tile
-        if (blockIdx.x >= parts) {
+        part = find_part<kThreads>(a.c.b, [&](int64_t i) { return seq_view(a, i, TK).tiles * units; }, sh_sum, sh_at);
+        if (part.end == 0) {
             if (tid == 0) a.cuts[blockIdx.x] = cut;
             grid_dep_launch();
             return;
         }
-        at = line.start(blockIdx.x, parts);
-        end = line.start(blockIdx.x + 1, parts);
-        // the sequence that holds the part's first tile
-        int64_t before = 0;
-        for (int64_t base = 0; base < a.c.b; base += kThreads) {
-            const int64_t i = base + tid;
-            const int64_t n = i < a.c.b ? seq_view(a, i, TK).tiles * units : 0;
-            int64_t incl = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += x;
-            }
-            __syncthreads();
-            if (lane == 31) sh_sum[warp] = incl;
-            __syncthreads();
-            int64_t off = before;
-            for (int w = 0; w < warp; ++w) off += sh_sum[w];
-            if (off + incl - n <= at && at < off + incl) {
-                sh_at[0] = i;
-                sh_at[1] = at - (off + incl - n);
-            }
-            before += sh_sum[0] + sh_sum[1] + sh_sum[2] + sh_sum[3];
-            if (before > at) break;
-        }
-        __syncthreads();
-        bi = sh_at[0];
-        rem = sh_at[1];
     }
-    const int64_t part0 = at;
+    const Line& line = part.line;
+    const int64_t parts = part.parts, end = part.end, part0 = part.at;
+    int64_t at = part.at, bi = part.bi, rem = part.rem;
 
     SeqView sv{};
     int64_t cur = -1;
@@ -638,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
 // Adds the partials of a unit that was cut between parts, in the order of the
 // parts. CTA x looks after the unit whose first cut is at part x's start.
 // SPREAD: CTA y takes row y, its warps every eighth part (few units, many
-// parts each); else a warp takes a row with all its parts.
+// parts each); else CTA y takes 8 rows, a warp each with all its parts.
 template <int HD, bool BF16, int ROWS, bool SPREAD>
 __global__ void __launch_bounds__(256) cache_fwd_join_kernel(const __grid_constant__ CacheFwdArgs a)
 {
@@ -656,7 +512,8 @@ __global__ void __launch_bounds__(256) cache_fwd_join_kernel(const __grid_consta
     auto slot = [&](int i) -> int64_t { return i == 0 ? c0 * int64_t(2) + cut.slot0 : (c0 + i) * int64_t(2); };
     int nq = a.s_q;
     if (a.seq_q_lens) nq = max(0, min(a.seq_q_lens[cut.bi], a.s_q));
-    for (int r = SPREAD ? blockIdx.y : warp; r < ROWS; r += SPREAD ? ROWS : 8) {
+    {
+        const int r = SPREAD ? blockIdx.y : blockIdx.y * 8 + warp;
         const int rr = r0 + r;
         if (rr >= R) return;
         float top = -INFINITY;
@@ -703,19 +560,15 @@ __global__ void __launch_bounds__(256) cache_fwd_join_kernel(const __grid_consta
 
 namespace {
 
-template <int HD, bool BF16, int NT, int OCC>
-cudaError_t launch_rows(const CacheFwdArgs& a, cudaStream_t s)
+template <int HD, bool BF16, int ROWS>
+cudaError_t launch_join(const CacheFwdArgs& a, cudaStream_t s)
 {
-    constexpr int ROWS = 8 * NT;
+    if (a.whole || a.parts == 1) return cudaSuccess;
     const int blocks = (a.s_q * a.group + ROWS - 1) / ROWS;
-    const int64_t units = a.c.b * a.c.h_kv * blocks;
-    cache_fwd_rows_kernel<HD, BF16, NT, OCC><<<a.parts, kThreads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || a.whole || a.parts == 1) return e;
     // with an eighth as many units as parts a unit has few cuts
-    const bool spread = units * 8 < a.parts;
+    const bool spread = a.c.b * a.c.h_kv * blocks * 8 < a.parts;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.parts), spread ? ROWS : 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.parts), spread ? ROWS : ROWS / 8);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -727,6 +580,21 @@ cudaError_t launch_rows(const CacheFwdArgs& a, cudaStream_t s)
                   : cudaLaunchKernelEx(&cfg, cache_fwd_join_kernel<HD, BF16, ROWS, false>, a);
 }
 
+template <int HD, bool BF16, int NT, int OCC>
+cudaError_t launch_rows(const CacheFwdArgs& a, cudaStream_t s)
+{
+    cache_fwd_rows_kernel<HD, BF16, NT, OCC><<<a.parts, kThreads, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join<HD, BF16, 8 * NT>(a, s);
+}
+
+template <int HD, bool BF16>
+cudaError_t launch_tiles(const CacheFwdArgs& a, cudaStream_t s)
+{
+    const cudaError_t e = launch_cache_fwd_tiles(a, BF16 ? SDPA_BF16 : SDPA_F16, s);
+    return e != cudaSuccess ? e : launch_join<HD, BF16, 256>(a, s);
+}
+
 template <bool BF16>
 cudaError_t launch_fwd_typed(const CacheFwdArgs& a, cudaStream_t s)
 {
@@ -735,7 +603,9 @@ cudaError_t launch_fwd_typed(const CacheFwdArgs& a, cudaStream_t s)
         case kRows128x16: return launch_rows<128, BF16, 2, 2>(a, s);
         case kRows64x8: return launch_rows<64, BF16, 1, 4>(a, s);
         case kRows64x16: return launch_rows<64, BF16, 2, 3>(a, s);
-        default: return launch_rows<64, BF16, 4, 2>(a, s);
+        case kRows64x32: return launch_rows<64, BF16, 4, 2>(a, s);
+        case kTiles128: return launch_tiles<128, BF16>(a, s);
+        default: return launch_tiles<64, BF16>(a, s);
     }
 }
 
@@ -743,10 +613,15 @@ cudaError_t launch_fwd_typed(const CacheFwdArgs& a, cudaStream_t s)
 
 CacheFwdPlan cache_fwd_plan(int64_t d, int64_t rows)
 {
-    if (d == 128) return rows <= 8 ? CacheFwdPlan{kRows128x8, 8, 64, 3} : CacheFwdPlan{kRows128x16, 16, 64, 2};
+    if (d == 128) {
+        if (rows <= 8) return CacheFwdPlan{kRows128x8, 8, 64, 3};
+        if (rows <= 16) return CacheFwdPlan{kRows128x16, 16, 64, 2};
+        return CacheFwdPlan{kTiles128, 256, 128, 1};
+    }
     if (rows <= 8) return CacheFwdPlan{kRows64x8, 8, 128, 4};
     if (rows <= 16) return CacheFwdPlan{kRows64x16, 16, 128, 3};
-    return CacheFwdPlan{kRows64x32, 32, 128, 2};
+    if (rows <= 32) return CacheFwdPlan{kRows64x32, 32, 128, 2};
+    return CacheFwdPlan{kTiles64, 256, 128, 1};
 }
 
 cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int dtype, cudaStream_t s)

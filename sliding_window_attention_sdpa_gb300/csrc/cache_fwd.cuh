@@ -1,0 +1,173 @@
+// cache_fwd.cuh -- what the cache forward's kernels share: the sequence as its
+// rows and keys, the line of tiles that is cut between CTAs, and the last step
+// of a row.
+#pragma once
+
+#include "cache.cuh"
+#include "ptx.cuh"
+
+namespace swa {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t x)
+{
+    if constexpr (BF16) return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+    const __half2 h = *reinterpret_cast<const __half2*>(&x);
+    return __half22float2(h);
+}
+
+// One sequence as the rows and keys of this call see it.
+struct SeqView {
+    int32_t len, nq;    // cached keys, new tokens
+    int32_t lo;         // first cached key in reach of any row, a multiple of 16
+    int32_t new0;       // place of new token 0 in the line of keys (lo ... ), a multiple of 16 from lo
+    int32_t tiles;
+};
+
+__device__ __forceinline__ SeqView seq_view(const CacheFwdArgs& a, int64_t bi, int tk)
+{
+    SeqView v;
+    bool bad;
+    v.len = cache_length(a.c, bi, bad);
+    v.nq = a.s_q;
+    if (a.seq_q_lens) {
+        v.nq = a.seq_q_lens[bi];
+        if (v.nq < 0 || v.nq > a.s_q) {
+            set_status(a.c.status, SDPA_ERR_BAD_LENGTHS);
+            v.nq = v.nq < 0 ? 0 : a.s_q;
+        }
+    }
+    // without positions the lowest row's window starts at len - W
+    v.lo = 0;
+    if (a.window_left >= 0 && a.c.positions == nullptr)
+        v.lo = static_cast<int32_t>(imax64(0, v.len - a.window_left)) & ~15;
+    const int64_t cached = ((static_cast<int64_t>(v.len) + 15) & ~int64_t(15)) - v.lo;
+    v.new0 = static_cast<int32_t>(cached);
+    v.tiles = static_cast<int32_t>((cached + ((max(v.nq, 1) + 15) & ~15) + tk - 1) / tk);
+    return v;
+}
+
+// The line of tiles: all sequences' units, cut evenly between the parts.
+struct Line {
+    int64_t total;
+    __device__ __forceinline__ int64_t start(int64_t c, int64_t parts) const { return c * total / parts; }
+    // the part that holds tile t
+    __device__ __forceinline__ int64_t part_of(int64_t t, int64_t parts) const { return ((t + 1) * parts - 1) / total; }
+};
+
+__device__ __forceinline__ int64_t warp_sum64(int64_t x)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// Sum of per-thread values over the CTA (every thread calls it).
+template <int THREADS>
+__device__ __forceinline__ int64_t block_sum64(int64_t x, int64_t* sh)
+{
+    x = warp_sum64(x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+    __syncthreads();
+    int64_t s = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) s += sh[i];
+    return s;
+}
+
+// A CTA's part of the line: its tiles [at, end) (end 0: none), the sequence bi
+// that holds the first one, and that tile's place among the sequence's.
+struct Part {
+    int64_t parts, at, end, bi, rem;
+    Line line;
+};
+
+// Cuts the line of all sequences' tiles (tiles_of(i), each more than 0) into
+// one part per CTA, fewer if there are fewer tiles. Every thread calls it; sh
+// has a place per warp, sh_at two.
+template <int THREADS, class F>
+__device__ __forceinline__ Part find_part(int64_t b, F tiles_of, int64_t* sh, int64_t* sh_at)
+{
+    constexpr int W = THREADS / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    Part p{};
+    int64_t s = 0;
+    for (int64_t i = tid; i < b; i += THREADS) s += tiles_of(i);
+    p.line.total = block_sum64<THREADS>(s, sh);
+    p.parts = imin64(gridDim.x, p.line.total);
+    if (blockIdx.x >= p.parts) return p;
+    p.at = p.line.start(blockIdx.x, p.parts);
+    p.end = p.line.start(blockIdx.x + 1, p.parts);
+    int64_t before = 0;
+    for (int64_t base = 0; base < b; base += THREADS) {
+        const int64_t i = base + tid;
+        const int64_t n = i < b ? tiles_of(i) : 0;
+        int64_t incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        __syncthreads();
+        if (lane == 31) sh[warp] = incl;
+        __syncthreads();
+        int64_t off = before;
+        for (int w = 0; w < warp; ++w) off += sh[w];
+        if (off + incl - n <= p.at && p.at < off + incl) {
+            sh_at[0] = i;
+            sh_at[1] = p.at - (off + incl - n);
+        }
+#pragma unroll
+        for (int w = 0; w < W; ++w) before += sh[w];
+        if (before > p.at) break;
+    }
+    __syncthreads();
+    p.bi = sh_at[0];
+    p.rem = sh_at[1];
+    return p;
+}
+
+// Finishes E features (from c) of a row: O and, with its first feature, LSE.
+// `top` is the reference of the row's exponentials (log2), -inf for no key.
+template <bool BF16, int E>
+__device__ __forceinline__ void store_row(const CacheFwdArgs& a, int64_t bi, int tok, int64_t h, int c, bool in_rows,
+                                          float top, float sum, const float (&x)[E])
+{
+    const bool sunk = a.sink != nullptr && in_rows;
+    float mf = top, lt = sum;
+    if (sunk) {
+        const float sk = a.sink[h] * kLog2e;
+        mf = fmaxf(top, sk);
+        lt = (top == -INFINITY ? 0.f : sum * ex2_approx(top - mf)) + ex2_approx(sk - mf);
+    }
+    const float mul = top == -INFINITY ? 0.f : ex2_approx(top - mf) / lt;
+    uint16_t* o = a.o + bi * a.o_stride[0] + tok * a.o_stride[1] + h * a.o_stride[2] + c;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) w[e] = pack2<BF16>(x[2 * e] * mul, x[2 * e + 1] * mul);
+    if constexpr (E == 8) *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (E == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(o) = w[0];
+    if (c == 0) {
+        // a row without a key: the sink itself, or -inf
+        const float lse = top == -INFINITY ? (sunk ? a.sink[h] : -INFINITY) : (mf + log2f(lt)) * kLn2;
+        a.lse[(bi * a.h_q + h) * a.s_q + tok] = lse;
+    }
+}
+
+}  // namespace swa

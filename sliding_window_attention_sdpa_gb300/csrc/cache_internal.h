@@ -33,7 +33,7 @@ struct CacheFwdCut {
 
 // Kernel for a head dimension and a kv-head's number of rows: rows of a unit,
 // keys of a tile, CTAs per SM.
-enum CacheFwdVariant { kRows128x8, kRows128x16, kRows64x8, kRows64x16, kRows64x32 };
+enum CacheFwdVariant { kRows128x8, kRows128x16, kRows64x8, kRows64x16, kRows64x32, kTiles128, kTiles64 };
 struct CacheFwdPlan {
     int variant, rows, tile, occ;
 };
@@ -54,6 +54,7 @@ struct CacheFwdArgs {
     // workspace: per part two partials [rows][d] with their (reference, sum),
     // and the cut that the part names
     int32_t parts, whole;   // whole: one unit per CTA, no workspace
+    int64_t timeout_ns;     // limit of a wait inside the tile kernel
     float *part_o, *part_ml;
     CacheFwdCut* cuts;
 };
@@ -88,6 +89,7 @@ struct CacheEvictArgs {
 };
 
 cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_cache_fwd_tiles(const CacheFwdArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheAppendArgs& a, cudaStream_t s);
 cudaError_t launch_cache_weigh(const CacheWeighArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_cache_evict(const CacheEvictArgs& a, cudaStream_t s);

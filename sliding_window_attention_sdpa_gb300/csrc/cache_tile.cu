@@ -1,0 +1,696 @@
+// cache_tile.cu -- the cache forward for many rows per kv-head: tcgen05 tiles.
+//
+// A unit is a kv-head's block of up to 256 rows. Rows are the M dimension (128
+// per tile), keys the N dimension of S = Q K^T and the K dimension of O += P V:
+//   S  [128 rows x 128 keys]  TMEM, one buffer for each of two slots
+//   P  16-bit, written over S's columns, the A operand of P V from TMEM
+//   O  [128 rows x d]         TMEM, one for each slot
+// Two slots keep the tensor core and the softmax warps busy in turn: S of one
+// slot is issued before P V of the other. With more than 128 rows the slots
+// are the unit's two row tiles and share each K/V tile; with fewer they take
+// the same rows and every other key tile, and their sums are joined at the end.
+// So K and V are read once per 256 rows, and a short row block loses no overlap.
+//
+// Roles (384 threads): warps 0-2 gather K and V rows from the pages into two
+// rings in the 128-byte swizzle (a page may end anywhere, so each 16 bytes are
+// copied on their own, rows that are not held are filled with zeros), 32 keys
+// per warp in turn; warp 3 issues the MMAs; warps 4-7 and 8-11 are the slots'
+// softmax groups, one row per thread. A row's reference moves only when a score exceeds it by 2^8, so O is
+// seldom rescaled. P is rounded to the I/O dtype, as the prompt's forward does.
+//
+// The steps of all units form one line that the persistent CTAs cut evenly, as
+// in cache_fwd.cu; partials of cut units go to the same join.
+// Every wait is bounded; one that runs out ends the kernel with
+// SDPA_ERR_TIMEOUT in the cache's status.
+#include <type_traits>
+
+#include "cache_fwd.cuh"
+
+namespace swa {
+
+namespace {
+
+constexpr int kTileThreads = 384;
+constexpr int kLoadWarps = 3;
+constexpr int kMmaWarp = 3;
+constexpr int kSoftWarp0 = 4;
+constexpr uint32_t kBlk = 128 * 128;   // one 64-column block of a 128-row 16-bit tile
+constexpr int kRing = 8;               // key tiles whose validity and positions are kept
+
+template <int HD>
+struct TileCfg {
+    static constexpr uint32_t kTile = 128 * HD * 2;
+    static constexpr int kStages = HD == 128 ? 2 : 4;
+    static constexpr uint32_t kQ = 0;                           // 2 slots
+    static constexpr uint32_t kK = kQ + 2 * kTile;
+    static constexpr uint32_t kV = kK + kStages * kTile;
+    static constexpr uint32_t kPos = kV + kStages * kTile;      // int32 [kRing][128]
+    static constexpr uint32_t kOk = kPos + kRing * 512;         // uint32 [kRing][4]
+    static constexpr uint32_t kMask = kOk + kRing * 16;         // uint64 [64]
+    static constexpr uint32_t kMl = kMask + 512;                // float2 [2][128]
+    static constexpr uint32_t kBars = kMl + 2048;
+    static constexpr uint32_t kMisc = kBars + 256;
+    static constexpr uint32_t kBytes = kMisc + 256;
+    static_assert(kBytes <= 232448, "shared memory above the 227 KB a CTA may opt into");
+};
+
+// mbarriers; per-stage and per-slot ones at index + stage or slot
+enum TBar : int { tKFull = 0, tKEmpty = 4, tVFull = 8, tVEmpty = 12, tSFull = 16, tPFull = 18, tPvDone = 20, tQFull = 22,
+                  tSegDone = 24, tDrain, tNumBars };
+static_assert(tNumBars * 8 <= 256, "mbarrier area");
+
+__device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t chunk)
+{
+    return (chunk >> 3) * kBlk + (row >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+// 16 bytes to shared memory; zeros (nothing read) if not `have`.
+__device__ __forceinline__ void cp16(uint32_t dst, const uint16_t* src, bool have)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void named_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// How a sequence's steps are laid out: per kv-head `na` blocks of 256 rows
+// with two row tiles (a step is one key tile), then perhaps one block with one
+// row tile (a step is two key tiles).
+struct Shape {
+    int32_t ta, tb;       // steps of a two-tile block, of a one-tile block
+    int64_t per_head;
+};
+
+__device__ __forceinline__ Shape shape_of(const SeqView& v, int na, int nb)
+{
+    Shape s;
+    s.ta = v.tiles;
+    s.tb = (v.tiles + 1) >> 1;
+    s.per_head = static_cast<int64_t>(na) * s.ta + static_cast<int64_t>(nb) * s.tb;
+    return s;
+}
+
+// One stretch of a CTA's part that lies in one unit.
+struct Seg {
+    int64_t bi, gk;
+    int32_t blk;          // row block
+    bool two;             // two row tiles
+    int32_t step0, steps, of;   // its steps, and how many the unit has
+};
+
+struct Walk {
+    int64_t at, end, bi, rem;
+    int na, nb;
+    SeqView sv;
+    Shape sh;
+    bool loaded;
+
+    __device__ __forceinline__ Seg next(const CacheFwdArgs& a)
+    {
+        if (!loaded) {
+            sv = seq_view(a, bi, 128);
+            sh = shape_of(sv, na, nb);
+            loaded = true;
+        }
+        Seg g;
+        g.bi = bi;
+        g.gk = rem / sh.per_head;
+        const int64_t r = rem - g.gk * sh.per_head;
+        const int64_t a_steps = static_cast<int64_t>(na) * sh.ta;
+        g.two = r < a_steps;
+        g.blk = g.two ? static_cast<int32_t>(r / sh.ta) : na;
+        g.step0 = static_cast<int32_t>(g.two ? r - static_cast<int64_t>(g.blk) * sh.ta : r - a_steps);
+        g.of = g.two ? sh.ta : sh.tb;
+        g.steps = static_cast<int32_t>(imin64(g.of - g.step0, end - at));
+        return g;
+    }
+    __device__ __forceinline__ void advance(const CacheFwdArgs& a, const Seg& g)
+    {
+        at += g.steps;
+        rem += g.steps;
+        if (rem == sh.per_head * a.c.h_kv) {
+            ++bi;
+            rem = 0;
+            loaded = false;
+        }
+    }
+};
+
+// Sub-step i of a segment: slot i & 1. Two row tiles: key tile of step i / 2;
+// one: every key tile in turn (the last step may have only one).
+__device__ __forceinline__ int32_t sub_steps(const Seg& g, int32_t tiles)
+{
+    if (g.two) return 2 * g.steps;
+    return min(2 * (g.step0 + g.steps), tiles) - 2 * g.step0;
+}
+__device__ __forceinline__ int32_t sub_tile(const Seg& g, int32_t i) { return g.two ? g.step0 + (i >> 1) : 2 * g.step0 + i; }
+
+}  // namespace
+
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const __grid_constant__ CacheFwdArgs a)
+{
+    using C = TileCfg<HD>;
+    constexpr int NS = C::kStages;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ int64_t sh_sum[kTileThreads / 32], sh_at[2];
+    if (smem_u32(smem_raw) & 1023u) {
+        if (threadIdx.x == 0) set_status(a.c.status, SDPA_ERR_UNSUPPORTED);
+        if (threadIdx.x == 0 && !a.whole) a.cuts[blockIdx.x] = CacheFwdCut{-1, 0, 0, 0};
+        return;
+    }
+    uint8_t* sm = smem_raw;
+    const uint32_t sbase = smem_u32(sm);
+    auto bar = [&](int i) -> uint32_t { return sbase + C::kBars + 8u * i; };
+    uint32_t* misc = reinterpret_cast<uint32_t*>(sm + C::kMisc);   // [0] tmem base, [1] abort flag
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint64_t tmo = static_cast<uint64_t>(a.timeout_ns);
+
+    const int R = a.s_q * a.group;
+    const int blocks = (R + 255) / 256;
+    const int nb = (R - 1) % 256 < 128 ? 1 : 0;   // the last block has one row tile
+    const int na = blocks - nb;
+    Walk walk{};
+    walk.na = na;
+    walk.nb = nb;
+    Part part{1, 0, 0, 0, 0, Line{0}};
+    CacheFwdCut cut{-1, 0, 0, 0};
+    if (a.whole) {
+        const int64_t units = a.c.h_kv * blocks;
+        part.bi = blockIdx.x / units;
+        const int64_t un = blockIdx.x - part.bi * units, gk = un / blocks, blk = un - gk * blocks;
+        const Shape s = shape_of(seq_view(a, part.bi, 128), na, nb);
+        part.rem = gk * s.per_head + blk * s.ta;
+        part.end = blk < na ? s.ta : s.tb;
+    } else {
+        part = find_part<kTileThreads>(
+            a.c.b, [&](int64_t i) { return a.c.h_kv * shape_of(seq_view(a, i, 128), na, nb).per_head; }, sh_sum, sh_at);
+        if (part.end == 0) {
+            if (tid == 0) a.cuts[blockIdx.x] = cut;
+            grid_dep_launch();
+            return;
+        }
+    }
+    walk.at = part.at;
+    walk.end = part.end;
+    walk.bi = part.bi;
+    walk.rem = part.rem;
+
+    if (tid == 0) {
+        misc[1] = 0;
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(bar(tKFull + i), 128);
+            mbar_init(bar(tKEmpty + i), 1);
+            mbar_init(bar(tVFull + i), 128);
+            mbar_init(bar(tVEmpty + i), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(tSFull + s), 2);    // the MMAs' commit, and the issuer's own arrival
+            mbar_init(bar(tPFull + s), 128);
+            mbar_init(bar(tPvDone + s), 1);
+            mbar_init(bar(tQFull + s), 128);
+        }
+        mbar_init(bar(tSegDone), 256);
+        mbar_init(bar(tDrain), 1);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(sbase + C::kMisc, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    const uint32_t tm_s0 = tmem, tm_o0 = tmem + 256;     // slot s: S at + 128 s, O at + HD s
+    volatile uint32_t* abort_flag = misc + 1;
+
+    auto wait = [&](int b, uint32_t parity) -> bool {
+        if (*abort_flag) return false;
+        if (mbar_wait(bar(b), parity, tmo)) return true;
+        *abort_flag = 1;
+        set_status(a.c.status, SDPA_ERR_TIMEOUT);
+        return false;
+    };
+    auto wait_warp = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
+
+    if (warp < kLoadWarps) {
+        // ------------------------------------------------------------ gather K and V
+        // The line's keys in groups of 32, group q to warp q % 3. A warp's copies
+        // are committed per group, K and V one each; a group is handed over
+        // (writes made visible to the async proxy, barrier) when LAG later ones
+        // of the warp are on their way, or before the warp has to wait.
+        constexpr int CPR = HD / 8;           // 16-byte chunks of a row
+        constexpr int RPI = 32 / CPR;         // rows that a warp copies at once
+        constexpr int LAG = 2 * NS;
+        uint32_t issued = 0, handed = 0;      // this warp's groups
+        uint32_t it0 = 0;                     // key tiles before the segment
+        bool ok = true;
+        // group number n of this warp (K: even, V: odd) lies in key tile (3 (n / 2) + warp) / 4 of the CTA's run
+        auto hand_over = [&](uint32_t upto) {
+            fence_proxy_async_smem();
+            for (; handed < upto; ++handed) {
+                const uint32_t t = (3 * (handed >> 1) + warp) >> 2;
+                mbar_arrive(bar(((handed & 1) ? tVFull : tKFull) + t % NS));
+            }
+        };
+        auto acquire = [&](int b, uint32_t parity) -> bool {
+            for (;;) {
+                if (__all_sync(0xffffffffu, mbar_test(bar(b), parity))) return true;
+                const uint32_t pending = issued - handed;
+                if (pending == 0) return wait_warp(b, parity);
+                // the oldest group, as soon as it is there
+                if (pending > 4) cp_wait<4>();
+                else if (pending == 4) cp_wait<3>();
+                else if (pending == 3) cp_wait<2>();
+                else if (pending == 2) cp_wait<1>();
+                else cp_wait<0>();
+                hand_over(pending > 4 ? issued - 4 : issued - (pending - 1));
+            }
+        };
+        const int c = lane % CPR, sub = lane / CPR;
+        uint32_t q = warp;                    // next group of this warp in the CTA's run
+        while (walk.at < walk.end && ok) {
+            const Seg g = walk.next(a);
+            const SeqView& sv = walk.sv;
+            const int32_t* kpos = a.c.positions ? a.c.positions + (g.bi * a.c.h_kv + g.gk) * a.c.cap : nullptr;
+            const int32_t t0 = sub_tile(g, 0);
+            const uint32_t tiles = static_cast<uint32_t>(sub_tile(g, sub_steps(g, sv.tiles) - 1) - t0 + 1);
+            const uint32_t q_end = (it0 + tiles) * 4;
+            // place of this lane's key of group q in the unit's line of keys
+            auto place = [&](uint32_t qq) -> int32_t { return (t0 * 4 + static_cast<int32_t>(qq - it0 * 4)) * 32 + lane; };
+            auto entry_of = [&](uint32_t qq) -> int32_t {
+                if (qq >= q_end || a.c.page_table == nullptr) return 0;
+                const int32_t x = place(qq), j = sv.lo + x;
+                if (x >= sv.new0 || j >= sv.len) return 0;
+                return a.c.page_table[g.bi * a.c.max_pages + (a.c.page_shift >= 0 ? static_cast<uint32_t>(j) >> a.c.page_shift
+                                                                                  : static_cast<uint32_t>(j) / a.c.page_size)];
+            };
+            int32_t entry = entry_of(q);
+            for (; q < q_end; q += kLoadWarps) {
+                const uint32_t it = q >> 2, part32 = q & 3;
+                // this lane's key
+                const int32_t x = place(q);
+                bool have = false;
+                const uint16_t *kp = a.k, *vp = a.v;
+                int32_t pos = 0;
+                if (x < sv.new0) {
+                    const int32_t j = sv.lo + x;
+                    if (j < sv.len) {
+                        int64_t page = g.bi;
+                        uint32_t row = j;
+                        have = true;
+                        if (a.c.page_table) {
+                            page = entry;
+                            row = a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)
+                                                      : static_cast<uint32_t>(j) % a.c.page_size;
+                            have = page >= 0 && page < a.c.n_pages;
+                            if (!have) set_status(a.c.status, SDPA_ERR_BOUNDS);
+                        }
+                        if (have) {
+                            kp = a.c.k + page * a.c.k_stride[0] + row * a.c.k_stride[1] + g.gk * a.c.k_stride[2];
+                            vp = a.c.v + page * a.c.v_stride[0] + row * a.c.v_stride[1] + g.gk * a.c.v_stride[2];
+                        }
+                        pos = kpos && a.window_left >= 0 ? kpos[j] : j;
+                    }
+                } else if (x - sv.new0 < sv.nq) {
+                    have = true;
+                    kp = a.k + g.bi * a.k_stride[0] + (x - sv.new0) * a.k_stride[1] + g.gk * a.k_stride[2];
+                    vp = a.v + g.bi * a.v_stride[0] + (x - sv.new0) * a.v_stride[1] + g.gk * a.v_stride[2];
+                }
+                entry = entry_of(q + kLoadWarps);
+                const uint32_t held = __ballot_sync(0xffffffffu, have);
+                const uint32_t st = it % NS, par = (it / NS) & 1;
+                auto copy_rows = [&](const uint16_t* base, uint32_t dst) {
+#pragma unroll 8
+                    for (int i = 0; i < 32 / RPI; ++i) {
+                        const int r = i * RPI + sub;
+                        const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(base), r);
+                        cp16(dst + swz(part32 * 32 + r, c), reinterpret_cast<const uint16_t*>(p) + c * 8, (held >> r) & 1);
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    ++issued;
+                    if (issued - handed > LAG) {
+                        cp_wait<LAG>();
+                        hand_over(issued - LAG);
+                    }
+                };
+                if (!(ok = acquire(tKEmpty + st, par ^ 1))) break;
+                reinterpret_cast<int32_t*>(sm + C::kPos)[(it % kRing) * 128 + part32 * 32 + lane] = pos;
+                if (lane == 0) reinterpret_cast<uint32_t*>(sm + C::kOk)[(it % kRing) * 4 + part32] = held;
+                copy_rows(kp, sbase + C::kK + st * C::kTile);
+                if (!(ok = acquire(tVEmpty + st, par ^ 1))) break;
+                copy_rows(vp, sbase + C::kV + st * C::kTile);
+            }
+            it0 += tiles;
+            walk.advance(a, g);
+        }
+        cp_wait<0>();
+        if (ok) hand_over(issued);
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuer
+        constexpr uint32_t kIdS = idesc_f16(BF16, 128, 128, false, false);
+        constexpr uint32_t kIdPV = idesc_f16(BF16, 128, HD, false, true);
+        uint32_t it0 = 0, seg = 0;
+        uint32_t p_cnt[2] = {0u, 0u}, q_cnt[2] = {0u, 0u};
+        bool ok = true;
+        while (walk.at < walk.end && ok) {
+            const Seg g = walk.next(a);
+            const int32_t n = sub_steps(g, walk.sv.tiles);
+            const int nslots = g.two ? 2 : 1;      // row tiles
+            for (int s = 0; s < nslots && ok; ++s) {
+                ok = wait_warp(tQFull + s, q_cnt[s] & 1);
+                ++q_cnt[s];
+            }
+            // ring index of sub-step i's key tile
+            auto ring = [&](int32_t i) -> uint32_t { return it0 + (g.two ? i >> 1 : i); };
+            auto issue_s = [&](int32_t i) -> bool {
+                const uint32_t r = ring(i), st = r % NS;
+                const int sl = i & 1;
+                if ((!g.two || sl == 0) && !wait_warp(tKFull + st, (r / NS) & 1)) return false;
+                tc_fence_after();
+                const uint64_t dq = sdesc_sw128(sbase + C::kQ + (g.two ? sl : 0) * C::kTile, 16, 1024);
+                const uint64_t dk = sdesc_sw128(sbase + C::kK + st * C::kTile, 16, 1024);
+#pragma unroll
+                for (int b = 0; b < HD / 64; ++b)
+                    umma_f16_ss_x4(tm_s0 + sl * 128, sdesc_at(dq, b * kBlk), 2, sdesc_at(dk, b * kBlk), 2, kIdS, b > 0);
+                umma_commit(bar(tSFull + sl));
+                if (lane == 0) mbar_arrive(bar(tSFull + sl));
+                if (!g.two || sl == 1) umma_commit(bar(tKEmpty + st));
+                __syncwarp();
+                return true;
+            };
+            ok = ok && issue_s(0);
+            for (int32_t i = 0; i < n && ok; ++i) {
+                if (i + 1 < n && !(ok = issue_s(i + 1))) break;
+                const uint32_t r = ring(i), st = r % NS;
+                const int sl = i & 1;
+                if ((!g.two || sl == 0) && !(ok = wait_warp(tVFull + st, (r / NS) & 1))) break;
+                if (!(ok = wait_warp(tPFull + sl, p_cnt[sl] & 1))) break;
+                ++p_cnt[sl];
+                // the first P V of a segment overwrites an O that has been read
+                if (i == 0 && seg > 0 && !(ok = wait_warp(tSegDone, (seg - 1) & 1))) break;
+                tc_fence_after();
+                const uint64_t dv = sdesc_sw128(sbase + C::kV + st * C::kTile, kBlk, 1024);
+                umma_f16_ts_x4(tm_o0 + sl * HD, tm_s0 + sl * 128, 8, dv, 2048 >> 4, kIdPV, i >= 2);
+                umma_f16_ts_x4(tm_o0 + sl * HD, tm_s0 + sl * 128 + 32, 8, sdesc_at(dv, 4 * 2048), 2048 >> 4, kIdPV, 1);
+                umma_commit(bar(tPvDone + sl));
+                if (!g.two || sl == 1) umma_commit(bar(tVEmpty + st));
+                __syncwarp();
+            }
+            it0 += g.two ? g.steps : n;
+            ++seg;
+            walk.advance(a, g);
+        }
+        // after a wait that ran out: MMAs in flight end before TMEM is freed
+        if (!ok) {
+            umma_commit(bar(tDrain));
+            mbar_wait(bar(tDrain), 0, tmo);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax and epilogue
+        const int sl = (warp - kSoftWarp0) >> 2;
+        const int r = tid - (kSoftWarp0 + 4 * sl) * 32;     // index in the group
+        // a warp reads the quarter of the TMEM lanes of its number modulo 4
+        const int row = ((warp & 3) << 5) + lane;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tm_s = tm_s0 + sl * 128 + lane_off, tm_o = tm_o0 + sl * HD + lane_off;
+        float2* ml = reinterpret_cast<float2*>(sm + C::kMl);
+        uint64_t* masks = reinterpret_cast<uint64_t*>(sm + C::kMask);
+        uint32_t it0 = 0, cnt = 0;            // ring index at the segment's start; this slot's sub-steps so far
+        bool ok = true;
+        const int64_t part0 = walk.at;
+        while (walk.at < walk.end) {
+            const Seg g = walk.next(a);
+            const SeqView& sv = walk.sv;
+            const int32_t n = sub_steps(g, sv.tiles);
+            named_sync(3, 256);               // the last segment's masks and statistics have been read
+            if (sl == 0 && r < 64) {
+                const uint64_t in = sv.nq == 64 ? ~0ull : (1ull << sv.nq) - 1;
+                uint64_t m = 0;
+                if (r < sv.nq) m = in & (a.tree ? static_cast<uint64_t>(a.tree[g.bi * a.s_q + r]) : (2ull << r) - 1);
+                masks[r] = (m >> r) & 1 ? m : 0;
+            }
+            if (sl == 0 && r == 0 && walk.at == part0 && g.step0 > 0) {
+                const int64_t u0 = walk.at - g.step0, p0 = part.line.part_of(u0, part.parts);
+                if (p0 + 1 == blockIdx.x)
+                    cut = CacheFwdCut{g.bi, g.gk * blocks + g.blk,
+                                      static_cast<int32_t>(part.line.part_of(u0 + g.of - 1, part.parts)),
+                                      part.line.start(p0, part.parts) == u0 ? 0 : 1};
+            }
+            // this thread's row
+            const int rr = g.blk * 256 + (g.two ? sl * 128 : 0) + row;
+            const int tok = rr < R ? rr / a.group : 0;
+            const int64_t h = g.gk * a.group + (rr - tok * a.group);
+            if (g.two || sl == 0) {
+                const bool real = rr < R && tok < sv.nq;
+                const uint16_t* qp = a.q + g.bi * a.q_stride[0] + tok * a.q_stride[1] + h * a.q_stride[2];
+#pragma unroll
+                for (int c = 0; c < HD / 8; ++c) {
+                    const uint4 x = real ? ld_nc_v4(qp + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(sm + C::kQ + sl * C::kTile + swz(row, c)) = x;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(bar(tQFull + sl));
+            }
+            named_sync(3, 256);
+            const uint64_t mask = rr < R ? masks[tok] : 0;
+            const int64_t npos = a.c.next_pos ? a.c.next_pos[g.bi] : sv.len;
+            int32_t low = INT32_MIN;
+            if (a.window_left >= 0)
+                low = static_cast<int32_t>(imax64(INT32_MIN, imin64(INT32_MAX, npos + __popcll(mask) - 1 - a.window_left)));
+            const bool windowed = a.window_left >= 0;
+            const bool by_pos = windowed && a.c.positions != nullptr;
+
+            float m = -INFINITY, l = 0.f;
+            for (int32_t i = sl; i < n; i += 2, ++cnt) {
+                ok = ok && wait(tSFull + sl, cnt & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) continue;
+                tc_fence_after();
+                const int32_t t = sub_tile(g, i);
+                const uint32_t ring = (it0 + (g.two ? i >> 1 : i)) % kRing;
+                const int32_t x0 = t * 128;
+                const uint32_t* held = reinterpret_cast<const uint32_t*>(sm + C::kOk) + ring * 4;
+                // every key is cached, held and in the row's window, in all of the warp's rows
+                const bool all_held = (held[0] & held[1] & held[2] & held[3]) == 0xffffffffu;
+                const bool plain = x0 + 128 <= sv.new0 && all_held && !by_pos &&
+                                   !__any_sync(0xffffffffu, windowed && mask != 0 && sv.lo + x0 < low);
+                uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                if (!plain) {
+                    const int32_t* pos = reinterpret_cast<const int32_t*>(sm + C::kPos) + ring * 128;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t s = held[w];
+                        const int32_t xw = x0 + w * 32;
+                        if (mask == 0) s = 0;
+                        if (xw < sv.new0 ? windowed : false) {
+#pragma unroll 1
+                            for (int e = 0; e < 32; ++e)
+                                if (xw + e < sv.new0 && pos[w * 32 + e] < low) s &= ~(1u << e);
+                        }
+                        if (xw + 31 >= sv.new0) {
+#pragma unroll 1
+                            for (int e = 0; e < 32; ++e) {
+                                const int32_t u = xw + e - sv.new0;
+                                if (u < 0) continue;
+                                const bool in = u < 64 && ((mask >> (u & 63)) & 1) &&
+                                                (!windowed || __popcll(mask) - __popcll(masks[u & 63]) <= a.window_left);
+                                if (!in) s &= ~(1u << e);
+                            }
+                        }
+                        see[w] = s;
+                    }
+                }
+                auto softmax = [&](auto masked) {
+                    constexpr bool M = decltype(masked)::value;
+                    float mt = -INFINITY;
+#pragma unroll
+                    for (int cb = 0; cb < 4; ++cb) {
+                        uint32_t v[32];
+                        tmem_ld32(tm_s + cb * 32, v);
+                        tmem_ld_wait();
+                        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float f = __uint_as_float(v[e]);
+                            x[e & 3] = fmaxf(x[e & 3], !M || ((see[cb] >> e) & 1) ? f : -INFINITY);
+                        }
+                        mt = fmaxf(mt, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+                    }
+                    const float top = mt * a.scale_log2;
+                    const bool up = top > m + 8.f;
+                    if (__any_sync(0xffffffffu, up)) {
+                        const float mn = up ? top : m;
+                        const float al = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+                        const float f = up ? al : 1.f;
+                        l *= f;
+                        m = mn;
+                        if (i >= 2) {
+                            // O holds the P V of this slot's earlier key tiles: they are done before it changes
+                            ok = __all_sync(0xffffffffu, wait(tPvDone + sl, (cnt - 1) & 1));
+                            tc_fence_after();
+                            if (ok) {
+#pragma unroll 1
+                                for (int cb = 0; cb < HD / 32; ++cb) {
+                                    uint32_t v[32];
+                                    tmem_ld32(tm_o + cb * 32, v);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) {
+                                        uint32_t w8[8];
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e)
+                                            w8[e] = __float_as_uint(__uint_as_float(v[8 * q + e]) * f);
+                                        tmem_st8(tm_o + cb * 32 + 8 * q, w8);
+                                    }
+                                }
+                                tmem_st_wait();
+                            }
+                        }
+                    }
+                    // P over the columns of S that have been read
+                    const float mr = m == -INFINITY ? 0.f : m;
+                    float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int cb = 0; cb < 4; ++cb) {
+                        uint32_t v[32], pk[16];
+                        tmem_ld32(tm_s + cb * 32, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float p0 = ex2_approx(fmaf(__uint_as_float(v[e]), a.scale_log2, -mr));
+                            float p1 = ex2_approx(fmaf(__uint_as_float(v[e + 1]), a.scale_log2, -mr));
+                            if (M) {
+                                p0 = (see[cb] >> e) & 1 ? p0 : 0.f;
+                                p1 = (see[cb] >> (e + 1)) & 1 ? p1 : 0.f;
+                            }
+                            ps[(e >> 1) & 3] += p0 + p1;
+                            pk[e >> 1] = pack2<BF16>(p0, p1);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t w8[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w8[e] = pk[8 * q + e];
+                            tmem_st8(tm_s + cb * 16 + 8 * q, w8);
+                        }
+                    }
+                    l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                    tmem_st_wait();
+                };
+                if (plain) softmax(std::false_type{});
+                else softmax(std::true_type{});
+                tc_fence_before();
+                mbar_arrive(bar(tPFull + sl));
+            }
+            // the slot's last P V is done
+            const bool any = n > sl;
+            if (any) {
+                ok = ok && wait(tPvDone + sl, (cnt - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            tc_fence_after();
+            if (mask == 0) {
+                m = -INFINITY;
+                l = 0.f;
+            }
+            ml[sl * 128 + row] = make_float2(m, l);
+            tc_fence_before();
+            named_sync(3, 256);
+            tc_fence_after();
+            // two row tiles: each slot its rows; one: both slots the same rows,
+            // each half of the features, from both slots' sums
+            const bool whole = g.steps == g.of;
+            const int64_t slot = blockIdx.x * int64_t(2) + (walk.at == part0 ? 0 : 1);
+            const int urow = (g.two ? sl * 128 : 0) + row;         // row in the unit
+            float top = m, sum = l, f0 = 1.f, f1 = 0.f;
+            if (!g.two) {
+                const float2 x = ml[row], y = ml[128 + row];
+                top = fmaxf(x.x, y.x);
+                f0 = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top);
+                f1 = n < 2 || y.x == -INFINITY ? 0.f : ex2_approx(y.x - top);
+                sum = f0 * x.y + f1 * y.y;
+            }
+            const int cb0 = g.two ? 0 : sl * (HD / 64), cb1 = g.two ? HD / 32 : cb0 + HD / 64;
+            const bool dead = top == -INFINITY;
+            if (ok) {
+#pragma unroll 1
+                for (int cb = cb0; cb < cb1; ++cb) {
+                    uint32_t v[32];
+                    float x[32];
+                    tmem_ld32((g.two ? tm_o : tm_o0 + lane_off) + cb * 32, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = dead || f0 == 0.f ? 0.f : f0 * __uint_as_float(v[e]);
+                    if (!g.two && n > 1) {
+                        tmem_ld32(tm_o0 + HD + lane_off + cb * 32, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!dead && f1 != 0.f) x[e] += f1 * __uint_as_float(v[e]);
+                    }
+                    if (!whole) {
+                        float* po = a.part_o + (slot * 256 + urow) * HD + cb * 32;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(po + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                        if (cb == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * 256 + urow) * 2) = make_float2(top, sum);
+                    } else if (rr < R) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            float y[8];
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) y[q] = x[e + q];
+                            store_row<BF16, 8>(a, g.bi, tok, h, cb * 32 + e, tok < sv.nq, top, sum, y);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(bar(tSegDone));
+            it0 += g.two ? g.steps : n;
+            walk.advance(a, g);
+        }
+        if (sl == 0 && r == 0 && !a.whole) a.cuts[blockIdx.x] = cut;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (!a.whole) grid_dep_launch();
+}
+
+namespace {
+
+template <int HD, bool BF16>
+cudaError_t launch_tile_typed(const CacheFwdArgs& a, cudaStream_t s)
+{
+    auto kern = cache_fwd_tile_kernel<HD, BF16>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<HD>::kBytes);
+    if (e != cudaSuccess) return e;
+    kern<<<a.parts, kTileThreads, TileCfg<HD>::kBytes, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_fwd_tiles(const CacheFwdArgs& a, int dtype, cudaStream_t s)
+{
+    if (a.c.d == 128)
+        return dtype == SDPA_BF16 ? launch_tile_typed<128, true>(a, s) : launch_tile_typed<128, false>(a, s);
+    return dtype == SDPA_BF16 ? launch_tile_typed<64, true>(a, s) : launch_tile_typed<64, false>(a, s);
+}
+
+}  // namespace swa
