@@ -387,6 +387,31 @@ sdpa_status_t make_map(CUtensorMap* m, const char* name, const void* base, int d
     return make_map(m, name, base, dt, 2, 64, thd, d, h, rows, b, st);
 }
 
+}  // namespace
+
+bool swa::api::make_rows_map(CUtensorMap* m, const void* base, int dtype, int64_t d, int64_t h, int64_t rows, int64_t n,
+                             const int64_t* st, uint32_t box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t u = 1;
+    cuuint64_t dims[4] = {u * d, u * h, u * rows, u * n};
+    // a size of 1 gets a stride that a descriptor accepts
+    const cuuint64_t hs = h > 1 ? u * st[2] * 2 : u * d * 2;
+    const cuuint64_t rs = rows > 1 ? u * st[1] * 2 : hs * h;
+    const cuuint64_t ns = n > 1 ? u * st[0] * 2 : rs * rows;
+    cuuint64_t strides[3] = {hs, rs, ns};
+    cuuint32_t box[4] = {64, 1, box_rows, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    if (hs == 0 || rs == 0 || ns == 0) return false;
+    return fn(m, dtype == SDPA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
 // The dQ convert kernel zero-fills rows past a sequence's length and q-tiles
 // no kv-tile visits, converts q-tiles whose visitors added with unordered
 // atomics (three or more, not deterministic) and finishes dSink. For a BSHD

@@ -4,6 +4,7 @@
 
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/sdpa_bwd.h"
@@ -20,6 +21,12 @@ void clear_error();
 sdpa_status_t check_device_ptr(const char* name, const void* ptr, bool required, int device, unsigned align = 16);
 
 sdpa_status_t cuda_status(cudaError_t e, const char* what);
+
+// TMA descriptor of a 16-bit tensor [n][rows][h][d] (strides in elements: n,
+// row, head) in boxes of 64 features x 1 head x box_rows rows with the 128-byte
+// swizzle. False if the driver takes no such descriptor.
+bool make_rows_map(CUtensorMap* m, const void* base, int dtype, int64_t d, int64_t h, int64_t rows, int64_t n,
+                   const int64_t* st, uint32_t box_rows);
 
 }  // namespace api
 }  // namespace swa

@@ -15,6 +15,7 @@ using swa::api::check_device_ptr;
 using swa::api::clear_error;
 using swa::api::cuda_status;
 using swa::api::fail;
+using swa::api::make_rows_map;
 
 constexpr int64_t kWaitLimitNs = 2000000000LL;
 constexpr int64_t kMax31 = int64_t(1) << 31;
@@ -167,8 +168,8 @@ FwdSize fwd_size(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa:
     if (p->window_left >= 0 && c->positions == nullptr && p->window_left < keys) keys = p->window_left;
     const int64_t rows = p->s_q * (p->h_q / c->h_kv);
     z.blocks = (rows + plan.rows - 1) / plan.rows;
-    // the reach begins and the new tokens end up to 15 keys off a group of 16
-    z.tiles = (keys + 30 + ((p->s_q + 15) & ~int64_t(15)) + plan.tile - 1) / plan.tile;
+    // the reach begins up to 15 keys before (127 in the tile kernel), the new tokens end up to 15 off a group of 16
+    z.tiles = (keys + (plan.variant >= swa::kTiles128 ? 142 : 30) + ((p->s_q + 15) & ~int64_t(15)) + plan.tile - 1) / plan.tile;
     z.units = double(c->b) * double(c->h_kv) * double(z.blocks);
     z.total = z.units * double(z.tiles);
     return z;
@@ -305,7 +306,8 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
 {
     sdpa_status_t st = check_fwd(c, p);
     if (st != SDPA_OK) return st;
-    const FwdLayout l = fwd_layout(c, p, swa::cache_fwd_plan(c->d, p->s_q * (p->h_q / c->h_kv)));
+    const swa::CacheFwdPlan plan = swa::cache_fwd_plan(c->d, p->s_q * (p->h_q / c->h_kv));
+    const FwdLayout l = fwd_layout(c, p, plan);
     if ((st = check_ws(ws, ws_bytes, l.total)) != SDPA_OK) return st;
     int dev = 0;
     if ((st = current_device(&dev)) != SDPA_OK) return st;
@@ -315,7 +317,8 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
                         {"sink", p->sink, false, 4}, {"seq_q_lens", p->seq_q_lens, false, 4}, {"workspace", ws, l.total > 0, 256}};
     if ((st = check_cache_ptrs(c, dev)) != SDPA_OK || (st = check_ptrs(ptrs, dev)) != SDPA_OK) return st;
     if (!rows) return SDPA_OK;
-    swa::CacheFwdArgs a{};
+    swa::CacheTileArgs ta{};
+    swa::CacheFwdArgs& a = ta.f;
     a.c = view_of(c);
     a.s_q = static_cast<int32_t>(p->s_q);
     a.h_q = static_cast<int32_t>(p->h_q);
@@ -341,7 +344,15 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.part_o = at<float>(ws, l.part_o);
     a.part_ml = at<float>(ws, l.part_ml);
     a.cuts = at<swa::CacheFwdCut>(ws, l.cuts);
-    return cuda_status(swa::launch_cache_fwd(a, c->dtype, static_cast<cudaStream_t>(stream)), "cache forward launch");
+    if (plan.variant >= swa::kTiles128 && c->n_pages > 0) {
+        // boxes of up to 128 rows that divide a page; an unpaged sequence's keys follow one another
+        int32_t rows = 128;
+        while (c->page_table != nullptr && c->page_size % rows != 0) rows >>= 1;
+        if (rows >= 8 && make_rows_map(&ta.tm_k, c->k, c->dtype, c->d, c->h_kv, c->page_size, c->n_pages, c->k_stride, rows) &&
+            make_rows_map(&ta.tm_v, c->v, c->dtype, c->d, c->h_kv, c->page_size, c->n_pages, c->v_stride, rows))
+            ta.box_rows = rows;
+    }
+    return cuda_status(swa::launch_cache_fwd(ta, c->dtype, static_cast<cudaStream_t>(stream)), "cache forward launch");
 }
 
 sdpa_status_t sdpa_cache_append(const sdpa_cache* c, const sdpa_cache_append_params* p, void* stream)

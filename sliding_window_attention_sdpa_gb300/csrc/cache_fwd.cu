@@ -589,23 +589,24 @@ cudaError_t launch_rows(const CacheFwdArgs& a, cudaStream_t s)
 }
 
 template <int HD, bool BF16>
-cudaError_t launch_tiles(const CacheFwdArgs& a, cudaStream_t s)
+cudaError_t launch_tiles(const CacheTileArgs& ta, cudaStream_t s)
 {
-    const cudaError_t e = launch_cache_fwd_tiles(a, BF16 ? SDPA_BF16 : SDPA_F16, s);
-    return e != cudaSuccess ? e : launch_join<HD, BF16, 256>(a, s);
+    const cudaError_t e = launch_cache_fwd_tiles(ta, BF16 ? SDPA_BF16 : SDPA_F16, s);
+    return e != cudaSuccess ? e : launch_join<HD, BF16, 256>(ta.f, s);
 }
 
 template <bool BF16>
-cudaError_t launch_fwd_typed(const CacheFwdArgs& a, cudaStream_t s)
+cudaError_t launch_fwd_typed(const CacheTileArgs& ta, cudaStream_t s)
 {
+    const CacheFwdArgs& a = ta.f;
     switch (cache_fwd_plan(a.c.d, a.s_q * a.group).variant) {
         case kRows128x8: return launch_rows<128, BF16, 1, 3>(a, s);
         case kRows128x16: return launch_rows<128, BF16, 2, 2>(a, s);
         case kRows64x8: return launch_rows<64, BF16, 1, 4>(a, s);
         case kRows64x16: return launch_rows<64, BF16, 2, 3>(a, s);
         case kRows64x32: return launch_rows<64, BF16, 4, 2>(a, s);
-        case kTiles128: return launch_tiles<128, BF16>(a, s);
-        default: return launch_tiles<64, BF16>(a, s);
+        case kTiles128: return launch_tiles<128, BF16>(ta, s);
+        default: return launch_tiles<64, BF16>(ta, s);
     }
 }
 
@@ -624,7 +625,7 @@ CacheFwdPlan cache_fwd_plan(int64_t d, int64_t rows)
     return CacheFwdPlan{kTiles64, 256, 128, 1};
 }
 
-cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int dtype, cudaStream_t s)
+cudaError_t launch_cache_fwd(const CacheTileArgs& a, int dtype, cudaStream_t s)
 {
     return dtype == SDPA_BF16 ? launch_fwd_typed<true>(a, s) : launch_fwd_typed<false>(a, s);
 }

@@ -33,12 +33,13 @@ __device__ __forceinline__ float2 unpack2(uint32_t x)
 // One sequence as the rows and keys of this call see it.
 struct SeqView {
     int32_t len, nq;    // cached keys, new tokens
-    int32_t lo;         // first cached key in reach of any row, a multiple of 16
+    int32_t lo;         // first cached key in reach of any row, rounded down to `align`
     int32_t new0;       // place of new token 0 in the line of keys (lo ... ), a multiple of 16 from lo
     int32_t tiles;
 };
 
-__device__ __forceinline__ SeqView seq_view(const CacheFwdArgs& a, int64_t bi, int tk)
+// tk keys a tile; align is a power of two, at least 16.
+__device__ __forceinline__ SeqView seq_view(const CacheFwdArgs& a, int64_t bi, int tk, int align = 16)
 {
     SeqView v;
     bool bad;
@@ -54,7 +55,7 @@ __device__ __forceinline__ SeqView seq_view(const CacheFwdArgs& a, int64_t bi, i
     // without positions the lowest row's window starts at len - W
     v.lo = 0;
     if (a.window_left >= 0 && a.c.positions == nullptr)
-        v.lo = static_cast<int32_t>(imax64(0, v.len - a.window_left)) & ~15;
+        v.lo = static_cast<int32_t>(imax64(0, v.len - a.window_left)) & ~(align - 1);
     const int64_t cached = ((static_cast<int64_t>(v.len) + 15) & ~int64_t(15)) - v.lo;
     v.new0 = static_cast<int32_t>(cached);
     v.tiles = static_cast<int32_t>((cached + ((max(v.nq, 1) + 15) & ~15) + tk - 1) / tk);

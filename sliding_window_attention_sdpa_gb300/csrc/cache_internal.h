@@ -4,6 +4,7 @@
 
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace swa {
@@ -59,6 +60,15 @@ struct CacheFwdArgs {
     CacheFwdCut* cuts;
 };
 
+// The tile kernel's: TMA descriptors of the pools' pages (4-D: d, head, row,
+// page) in boxes of 64 features x box_rows rows with the 128-byte swizzle;
+// box_rows 0: none, every row is gathered.
+struct CacheTileArgs {
+    CUtensorMap tm_k, tm_v;
+    CacheFwdArgs f;
+    int32_t box_rows;
+};
+
 struct CacheAppendArgs {
     CacheView c;
     int32_t thd;
@@ -88,8 +98,8 @@ struct CacheEvictArgs {
     int32_t* counts;       // [b * h_kv] rows to move; -1: the sequence is not touched
 };
 
-cudaError_t launch_cache_fwd(const CacheFwdArgs& a, int dtype, cudaStream_t s);
-cudaError_t launch_cache_fwd_tiles(const CacheFwdArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_cache_fwd(const CacheTileArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_cache_fwd_tiles(const CacheTileArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheAppendArgs& a, cudaStream_t s);
 cudaError_t launch_cache_weigh(const CacheWeighArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_cache_evict(const CacheEvictArgs& a, cudaStream_t s);

@@ -11,11 +11,9 @@
 // the same rows and every other key tile, and their sums are joined at the end.
 // So K and V are read once per 256 rows, and a short row block loses no overlap.
 //
-// Roles (384 threads): warps 0-2 gather K and V rows from the pages into two
-// rings in the 128-byte swizzle (a page may end anywhere, so each 16 bytes are
-// copied on their own, rows that are not held are filled with zeros), 32 keys
-// per warp in turn; warp 3 issues the MMAs; warps 4-7 and 8-11 are the slots'
-// softmax groups, one row per thread. A row's reference moves only when a score exceeds it by 2^8, so O is
+// Roles (384 threads): warp 0 loads K, warp 1 V into two rings in the 128-byte
+// swizzle; warp 2 is idle; warp 3 issues the MMAs; warps 4-7 and 8-11 are the
+// slots' softmax groups, one row per thread. A row's reference moves only when a score exceeds it by 2^8, so O is
 // seldom rescaled. P is rounded to the I/O dtype, as the prompt's forward does.
 //
 // The steps of all units form one line that the persistent CTAs cut evenly, as
@@ -70,6 +68,17 @@ __device__ __forceinline__ void cp16(uint32_t dst, const uint16_t* src, bool hav
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
 }
 
+// A box of 64 features x box_rows rows of one head of a page.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int head, int row,
+                                        int page)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(head), "r"(row), "r"(page)
+        : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void cp_wait()
 {
@@ -116,7 +125,7 @@ struct Walk {
     __device__ __forceinline__ Seg next(const CacheFwdArgs& a)
     {
         if (!loaded) {
-            sv = seq_view(a, bi, 128);
+            sv = seq_view(a, bi, 128, 128);
             sh = shape_of(sv, na, nb);
             loaded = true;
         }
@@ -156,8 +165,9 @@ __device__ __forceinline__ int32_t sub_tile(const Seg& g, int32_t i) { return g.
 }  // namespace
 
 template <int HD, bool BF16>
-__global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const __grid_constant__ CacheFwdArgs a)
+__global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const __grid_constant__ CacheTileArgs ta)
 {
+    const CacheFwdArgs& a = ta.f;
     using C = TileCfg<HD>;
     constexpr int NS = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -187,12 +197,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         const int64_t units = a.c.h_kv * blocks;
         part.bi = blockIdx.x / units;
         const int64_t un = blockIdx.x - part.bi * units, gk = un / blocks, blk = un - gk * blocks;
-        const Shape s = shape_of(seq_view(a, part.bi, 128), na, nb);
+        const Shape s = shape_of(seq_view(a, part.bi, 128, 128), na, nb);
         part.rem = gk * s.per_head + blk * s.ta;
         part.end = blk < na ? s.ta : s.tb;
     } else {
         part = find_part<kTileThreads>(
-            a.c.b, [&](int64_t i) { return a.c.h_kv * shape_of(seq_view(a, i, 128), na, nb).per_head; }, sh_sum, sh_at);
+            a.c.b, [&](int64_t i) { return a.c.h_kv * shape_of(seq_view(a, i, 128, 128), na, nb).per_head; }, sh_sum, sh_at);
         if (part.end == 0) {
             if (tid == 0) a.cuts[blockIdx.x] = cut;
             grid_dep_launch();
@@ -207,9 +217,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
     if (tid == 0) {
         misc[1] = 0;
         for (int i = 0; i < NS; ++i) {
-            mbar_init(bar(tKFull + i), 128);
+            mbar_init(bar(tKFull + i), 4);
             mbar_init(bar(tKEmpty + i), 1);
-            mbar_init(bar(tVFull + i), 128);
+            mbar_init(bar(tVFull + i), 4);
             mbar_init(bar(tVEmpty + i), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -244,117 +254,149 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
 
     if (warp < kLoadWarps) {
         // ------------------------------------------------------------ gather K and V
-        // The line's keys in groups of 32, group q to warp q % 3. A warp's copies
-        // are committed per group, K and V one each; a group is handed over
-        // (writes made visible to the async proxy, barrier) when LAG later ones
-        // of the warp are on their way, or before the warp has to wait.
+        // Warp 0 fills the K ring, warp 1 the V ring, each as its stages become
+        // free. A tile whose 128 keys are all cached comes by TMA, in boxes that
+        // lie within a page (box_rows, a power of two that divides the page size);
+        // the last tiles of a unit, and all of them where pages have no such
+        // divisor, are gathered 16 bytes at a time, 32 keys a group, zeros in the
+        // rows that are not held. A gathered group is handed over (writes made
+        // visible to the async proxy, barrier) when LAG later ones are on their
+        // way, or while the warp has to wait for a stage. A stage is full after
+        // four arrivals, one for each 32 keys.
+        const bool is_v = warp == 1;
         constexpr int CPR = HD / 8;           // 16-byte chunks of a row
         constexpr int RPI = 32 / CPR;         // rows that a warp copies at once
-        constexpr int LAG = 2 * NS;
-        uint32_t issued = 0, handed = 0;      // this warp's groups
-        uint32_t it0 = 0;                     // key tiles before the segment
-        bool ok = true;
-        // group number n of this warp (K: even, V: odd) lies in key tile (3 (n / 2) + warp) / 4 of the CTA's run
-        auto hand_over = [&](uint32_t upto) {
+        constexpr uint32_t LAG = 5;
+        uint64_t queue = 0;                   // stages of the groups on their way, 8 bits each, oldest lowest
+        uint32_t pending = 0;
+        uint32_t it = 0;                      // key tiles so far
+        bool ok = warp < 2;
+        const int full0 = is_v ? tVFull : tKFull, empty0 = is_v ? tVEmpty : tKEmpty;
+        const uint32_t ring0 = sbase + (is_v ? C::kV : C::kK);
+        auto hand_over = [&](uint32_t keep) {     // the groups that are there, all but the last `keep`
             fence_proxy_async_smem();
-            for (; handed < upto; ++handed) {
-                const uint32_t t = (3 * (handed >> 1) + warp) >> 2;
-                mbar_arrive(bar(((handed & 1) ? tVFull : tKFull) + t % NS));
+            __syncwarp();
+            for (; pending > keep; --pending, queue >>= 8)
+                if (lane == 0) mbar_arrive(bar(full0 + static_cast<int>(queue & 255)));
+        };
+        auto wait_oldest = [&]() {
+            switch (pending) {
+                case 6: cp_wait<5>(); break;
+                case 5: cp_wait<4>(); break;
+                case 4: cp_wait<3>(); break;
+                case 3: cp_wait<2>(); break;
+                case 2: cp_wait<1>(); break;
+                default: cp_wait<0>(); break;
             }
+            hand_over(pending > 6 ? 0 : pending - 1);
         };
         auto acquire = [&](int b, uint32_t parity) -> bool {
             for (;;) {
                 if (__all_sync(0xffffffffu, mbar_test(bar(b), parity))) return true;
-                const uint32_t pending = issued - handed;
                 if (pending == 0) return wait_warp(b, parity);
-                // the oldest group, as soon as it is there
-                if (pending > 4) cp_wait<4>();
-                else if (pending == 4) cp_wait<3>();
-                else if (pending == 3) cp_wait<2>();
-                else if (pending == 2) cp_wait<1>();
-                else cp_wait<0>();
-                hand_over(pending > 4 ? issued - 4 : issued - (pending - 1));
+                wait_oldest();
             }
         };
         const int c = lane % CPR, sub = lane / CPR;
-        uint32_t q = warp;                    // next group of this warp in the CTA's run
-        while (walk.at < walk.end && ok) {
+        while (ok && walk.at < walk.end) {
             const Seg g = walk.next(a);
             const SeqView& sv = walk.sv;
-            const int32_t* kpos = a.c.positions ? a.c.positions + (g.bi * a.c.h_kv + g.gk) * a.c.cap : nullptr;
-            const int32_t t0 = sub_tile(g, 0);
-            const uint32_t tiles = static_cast<uint32_t>(sub_tile(g, sub_steps(g, sv.tiles) - 1) - t0 + 1);
-            const uint32_t q_end = (it0 + tiles) * 4;
-            // place of this lane's key of group q in the unit's line of keys
-            auto place = [&](uint32_t qq) -> int32_t { return (t0 * 4 + static_cast<int32_t>(qq - it0 * 4)) * 32 + lane; };
-            auto entry_of = [&](uint32_t qq) -> int32_t {
-                if (qq >= q_end || a.c.page_table == nullptr) return 0;
-                const int32_t x = place(qq), j = sv.lo + x;
-                if (x >= sv.new0 || j >= sv.len) return 0;
+            const int32_t* kpos = a.c.positions && a.window_left >= 0 ? a.c.positions + (g.bi * a.c.h_kv + g.gk) * a.c.cap
+                                                                      : nullptr;
+            const int32_t t0 = sub_tile(g, 0), t1 = sub_tile(g, sub_steps(g, sv.tiles) - 1);
+            const uint16_t* pool = (is_v ? a.c.v : a.c.k) + g.gk * (is_v ? a.c.v_stride[2] : a.c.k_stride[2]);
+            const int64_t st_page = is_v ? a.c.v_stride[0] : a.c.k_stride[0], st_row = is_v ? a.c.v_stride[1] : a.c.k_stride[1];
+            const uint16_t* fresh = (is_v ? a.v + g.bi * a.v_stride[0] + g.gk * a.v_stride[2]
+                                          : a.k + g.bi * a.k_stride[0] + g.gk * a.k_stride[2]);
+            const int64_t st_new = is_v ? a.v_stride[1] : a.k_stride[1];
+            auto entry_of = [&](int32_t j) -> int32_t {       // of a held key
+                if (a.c.page_table == nullptr) return static_cast<int32_t>(g.bi);
                 return a.c.page_table[g.bi * a.c.max_pages + (a.c.page_shift >= 0 ? static_cast<uint32_t>(j) >> a.c.page_shift
                                                                                   : static_cast<uint32_t>(j) / a.c.page_size)];
             };
-            int32_t entry = entry_of(q);
-            for (; q < q_end; q += kLoadWarps) {
-                const uint32_t it = q >> 2, part32 = q & 3;
-                // this lane's key
-                const int32_t x = place(q);
-                bool have = false;
-                const uint16_t *kp = a.k, *vp = a.v;
-                int32_t pos = 0;
-                if (x < sv.new0) {
-                    const int32_t j = sv.lo + x;
-                    if (j < sv.len) {
-                        int64_t page = g.bi;
-                        uint32_t row = j;
-                        have = true;
-                        if (a.c.page_table) {
-                            page = entry;
-                            row = a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)
-                                                      : static_cast<uint32_t>(j) % a.c.page_size;
+            auto row_of = [&](int32_t j) -> uint32_t {
+                if (a.c.page_table == nullptr) return j;
+                return a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)
+                                           : static_cast<uint32_t>(j) % a.c.page_size;
+            };
+            const int boxes = ta.box_rows ? 128 / ta.box_rows : 0;
+            // a TMA tile's page of lane's box, a tile ahead
+            auto box_entry = [&](int32_t t) -> int32_t {
+                const int32_t j = sv.lo + t * 128 + lane * ta.box_rows;
+                return lane < boxes && t <= t1 && j < sv.len ? entry_of(j) : 0;
+            };
+            int32_t entry = box_entry(t0);
+            for (int32_t t = t0; t <= t1; ++t, ++it) {
+                const uint32_t st = it % NS, par = (it / NS) & 1;
+                const int32_t x0 = t * 128, j0 = sv.lo + x0;
+                const int32_t mine = entry;
+                entry = box_entry(t + 1);
+                const bool good = lane >= boxes || (mine >= 0 && mine < a.c.n_pages);
+                const bool by_tma = boxes > 0 && x0 + 128 <= sv.new0 && j0 + 128 <= sv.len && __all_sync(0xffffffffu, good);
+                if (!(ok = acquire(empty0 + st, par ^ 1))) break;
+                const uint32_t stage = ring0 + st * C::kTile;
+                if (!is_v && a.window_left >= 0) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int32_t j = j0 + k * 32 + lane;
+                        reinterpret_cast<int32_t*>(sm + C::kPos)[(it % kRing) * 128 + k * 32 + lane] =
+                            kpos && j < sv.len ? kpos[j] : j;
+                    }
+                }
+                if (by_tma) {
+                    if (!is_v && lane < 4) reinterpret_cast<uint32_t*>(sm + C::kOk)[(it % kRing) * 4 + lane] = 0xffffffffu;
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar(full0 + st), C::kTile);
+                        mbar_arrive(bar(full0 + st));
+                        mbar_arrive(bar(full0 + st));
+                        mbar_arrive(bar(full0 + st));
+                    }
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const CUtensorMap* map = is_v ? &ta.tm_v : &ta.tm_k;
+                        const uint32_t dst = stage + lane * ta.box_rows * 128;
+                        const int row = static_cast<int>(row_of(j0 + lane * ta.box_rows));
+#pragma unroll
+                        for (int cb = 0; cb < HD / 64; ++cb)
+                            tma_box(dst + cb * kBlk, map, bar(full0 + st), cb * 64, static_cast<int>(g.gk), row, mine);
+                    }
+                    continue;
+                }
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    // this lane's key
+                    const int32_t x = x0 + k * 32 + lane, j = sv.lo + x;
+                    const uint16_t* p = fresh;
+                    bool have = false;
+                    if (x < sv.new0) {
+                        if (j < sv.len) {
+                            const int32_t page = entry_of(j);
                             have = page >= 0 && page < a.c.n_pages;
                             if (!have) set_status(a.c.status, SDPA_ERR_BOUNDS);
+                            else p = pool + page * st_page + row_of(j) * st_row;
                         }
-                        if (have) {
-                            kp = a.c.k + page * a.c.k_stride[0] + row * a.c.k_stride[1] + g.gk * a.c.k_stride[2];
-                            vp = a.c.v + page * a.c.v_stride[0] + row * a.c.v_stride[1] + g.gk * a.c.v_stride[2];
-                        }
-                        pos = kpos && a.window_left >= 0 ? kpos[j] : j;
+                    } else if (x - sv.new0 < sv.nq) {
+                        have = true;
+                        p = fresh + (x - sv.new0) * st_new;
                     }
-                } else if (x - sv.new0 < sv.nq) {
-                    have = true;
-                    kp = a.k + g.bi * a.k_stride[0] + (x - sv.new0) * a.k_stride[1] + g.gk * a.k_stride[2];
-                    vp = a.v + g.bi * a.v_stride[0] + (x - sv.new0) * a.v_stride[1] + g.gk * a.v_stride[2];
-                }
-                entry = entry_of(q + kLoadWarps);
-                const uint32_t held = __ballot_sync(0xffffffffu, have);
-                const uint32_t st = it % NS, par = (it / NS) & 1;
-                auto copy_rows = [&](const uint16_t* base, uint32_t dst) {
+                    const uint32_t held = __ballot_sync(0xffffffffu, have);
+                    if (!is_v && lane == 0) reinterpret_cast<uint32_t*>(sm + C::kOk)[(it % kRing) * 4 + k] = held;
 #pragma unroll 8
                     for (int i = 0; i < 32 / RPI; ++i) {
                         const int r = i * RPI + sub;
-                        const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(base), r);
-                        cp16(dst + swz(part32 * 32 + r, c), reinterpret_cast<const uint16_t*>(p) + c * 8, (held >> r) & 1);
+                        const uint64_t q = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(p), r);
+                        cp16(stage + swz(k * 32 + r, c), reinterpret_cast<const uint16_t*>(q) + c * 8, (held >> r) & 1);
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
-                    ++issued;
-                    if (issued - handed > LAG) {
-                        cp_wait<LAG>();
-                        hand_over(issued - LAG);
-                    }
-                };
-                if (!(ok = acquire(tKEmpty + st, par ^ 1))) break;
-                reinterpret_cast<int32_t*>(sm + C::kPos)[(it % kRing) * 128 + part32 * 32 + lane] = pos;
-                if (lane == 0) reinterpret_cast<uint32_t*>(sm + C::kOk)[(it % kRing) * 4 + part32] = held;
-                copy_rows(kp, sbase + C::kK + st * C::kTile);
-                if (!(ok = acquire(tVEmpty + st, par ^ 1))) break;
-                copy_rows(vp, sbase + C::kV + st * C::kTile);
+                    queue |= static_cast<uint64_t>(st) << (8 * pending);
+                    if (++pending > LAG) wait_oldest();
+                }
             }
-            it0 += tiles;
             walk.advance(a, g);
         }
         cp_wait<0>();
-        if (ok) hand_over(issued);
+        if (ok) hand_over(0);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
         constexpr uint32_t kIdS = idesc_f16(BF16, 128, 128, false, false);
@@ -390,7 +432,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             };
             ok = ok && issue_s(0);
             for (int32_t i = 0; i < n && ok; ++i) {
-                if (i + 1 < n && !(ok = issue_s(i + 1))) break;
+                // S of the next sub-step goes first, unless its K is not there yet
+                const uint32_t rn = ring(i + 1);
+                const bool first = i + 1 < n && ((g.two && !(i & 1)) ||
+                                                 __all_sync(0xffffffffu, mbar_test(bar(tKFull + rn % NS), (rn / NS) & 1)));
+                if (first && !(ok = issue_s(i + 1))) break;
                 const uint32_t r = ring(i), st = r % NS;
                 const int sl = i & 1;
                 if ((!g.two || sl == 0) && !(ok = wait_warp(tVFull + st, (r / NS) & 1))) break;
@@ -405,6 +451,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 umma_commit(bar(tPvDone + sl));
                 if (!g.two || sl == 1) umma_commit(bar(tVEmpty + st));
                 __syncwarp();
+                if (!first && i + 1 < n) ok = issue_s(i + 1);
             }
             it0 += g.two ? g.steps : n;
             ++seg;
@@ -675,20 +722,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
 namespace {
 
 template <int HD, bool BF16>
-cudaError_t launch_tile_typed(const CacheFwdArgs& a, cudaStream_t s)
+cudaError_t launch_tile_typed(const CacheTileArgs& a, cudaStream_t s)
 {
     auto kern = cache_fwd_tile_kernel<HD, BF16>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<HD>::kBytes);
     if (e != cudaSuccess) return e;
-    kern<<<a.parts, kTileThreads, TileCfg<HD>::kBytes, s>>>(a);
+    kern<<<a.f.parts, kTileThreads, TileCfg<HD>::kBytes, s>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_cache_fwd_tiles(const CacheFwdArgs& a, int dtype, cudaStream_t s)
+cudaError_t launch_cache_fwd_tiles(const CacheTileArgs& a, int dtype, cudaStream_t s)
 {
-    if (a.c.d == 128)
+    if (a.f.c.d == 128)
         return dtype == SDPA_BF16 ? launch_tile_typed<128, true>(a, s) : launch_tile_typed<128, false>(a, s);
     return dtype == SDPA_BF16 ? launch_tile_typed<64, true>(a, s) : launch_tile_typed<64, false>(a, s);
 }
