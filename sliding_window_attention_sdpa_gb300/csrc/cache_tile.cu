@@ -2,18 +2,19 @@
 //
 // A unit is a kv-head's block of up to 256 rows. Rows are the M dimension (128
 // per tile), keys the N dimension of S = Q K^T and the K dimension of O += P V:
-//   S  [128 rows x 128 keys]  TMEM, one buffer for each of two slots
-//   P  16-bit, written over S's columns, the A operand of P V from TMEM
-//   O  [128 rows x d]         TMEM, one for each slot
-// Two slots keep the tensor core and the softmax warps busy in turn: S of one
-// slot is issued before P V of the other. With more than 128 rows the slots
+//   S  [128 rows x 64 keys]  TMEM, two buffers for each of two slots
+//   P  16-bit, written over its S's columns, the A operand of P V from TMEM
+//   O  [128 rows x d]        TMEM, one for each slot
+// A slot's next S is computed while its softmax works on this one, and the two
+// slots keep the tensor core and the softmax warps busy in turn. With more than 128 rows the slots
 // are the unit's two row tiles and share each K/V tile; with fewer they take
 // the same rows and every other key tile, and their sums are joined at the end.
 // So K and V are read once per 256 rows, and a short row block loses no overlap.
 //
 // Roles (384 threads): warp 0 loads K, warp 1 V into two rings in the 128-byte
-// swizzle; warp 2 is idle; warp 3 issues the MMAs; warps 4-7 and 8-11 are the
-// slots' softmax groups, one row per thread. A row's reference moves only when a score exceeds it by 2^8, so O is
+// swizzle; warps 2 and 3 issue a slot's MMAs each (one warp for both was the
+// bottleneck: its issue of a sub-step's 12 MMAs takes longer than they run);
+// warps 4-7 and 8-11 are the slots' softmax groups, one row per thread. A row's reference moves only when a score exceeds it by 2^8, so O is
 // seldom rescaled. P is rounded to the I/O dtype, as the prompt's forward does.
 //
 // The steps of all units form one line that the persistent CTAs cut evenly, as
@@ -29,8 +30,7 @@ namespace swa {
 namespace {
 
 constexpr int kTileThreads = 384;
-constexpr int kLoadWarps = 3;
-constexpr int kMmaWarp = 3;
+constexpr int kMmaWarp = 2;            // and 3
 constexpr int kSoftWarp0 = 4;
 constexpr uint32_t kBlk = 128 * 128;   // one 64-column block of a 128-row 16-bit tile
 constexpr int kRing = 8;               // key tiles whose validity and positions are kept
@@ -47,15 +47,16 @@ struct TileCfg {
     static constexpr uint32_t kMask = kOk + kRing * 16;         // uint64 [64]
     static constexpr uint32_t kMl = kMask + 512;                // float2 [2][128]
     static constexpr uint32_t kBars = kMl + 2048;
-    static constexpr uint32_t kMisc = kBars + 256;
+    static constexpr uint32_t kMisc = kBars + 320;
     static constexpr uint32_t kBytes = kMisc + 256;
     static_assert(kBytes <= 232448, "shared memory above the 227 KB a CTA may opt into");
 };
 
 // mbarriers; per-stage and per-slot ones at index + stage or slot
-enum TBar : int { tKFull = 0, tKEmpty = 4, tVFull = 8, tVEmpty = 12, tSFull = 16, tPFull = 18, tPvDone = 20, tQFull = 22,
-                  tSegDone = 24, tDrain, tNumBars };
-static_assert(tNumBars * 8 <= 256, "mbarrier area");
+// (S, P and P V: slot * 2 + half of the key tile)
+enum TBar : int { tKFull = 0, tKEmpty = 4, tVFull = 8, tVEmpty = 12, tSFull = 16, tPFull = 20, tPvDone = 24, tQFull = 28,
+                  tSegDone = 30, tDrain = 31, tNumBars = 33 };
+static_assert(tNumBars * 8 <= 320, "mbarrier area");
 
 __device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t chunk)
 {
@@ -153,14 +154,16 @@ struct Walk {
     }
 };
 
-// Sub-step i of a segment: slot i & 1. Two row tiles: key tile of step i / 2;
-// one: every key tile in turn (the last step may have only one).
-__device__ __forceinline__ int32_t sub_steps(const Seg& g, int32_t tiles)
+// Key tiles of a segment: one for each step with two row tiles, two with one
+// (the unit's last step may have only one).
+__device__ __forceinline__ int32_t seg_tile0(const Seg& g) { return g.two ? g.step0 : 2 * g.step0; }
+__device__ __forceinline__ int32_t seg_tiles(const Seg& g, int32_t tiles)
 {
-    if (g.two) return 2 * g.steps;
-    return min(2 * (g.step0 + g.steps), tiles) - 2 * g.step0;
+    return g.two ? g.steps : min(2 * (g.step0 + g.steps), tiles) - 2 * g.step0;
 }
-__device__ __forceinline__ int32_t sub_tile(const Seg& g, int32_t i) { return g.two ? g.step0 + (i >> 1) : 2 * g.step0 + i; }
+// Sub-step i of a segment: slot i & 1, half (i >> 1) & 1 of the key tile that
+// this gives (counted from the segment's first).
+__device__ __forceinline__ int32_t sub_tile(const Seg& g, int32_t i) { return g.two ? i >> 2 : 2 * (i >> 2) + (i & 1); }
 
 }  // namespace
 
@@ -218,18 +221,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         misc[1] = 0;
         for (int i = 0; i < NS; ++i) {
             mbar_init(bar(tKFull + i), 4);
-            mbar_init(bar(tKEmpty + i), 1);
+            mbar_init(bar(tKEmpty + i), 2);
             mbar_init(bar(tVFull + i), 4);
-            mbar_init(bar(tVEmpty + i), 1);
+            mbar_init(bar(tVEmpty + i), 2);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 4; ++s) {
             mbar_init(bar(tSFull + s), 2);    // the MMAs' commit, and the issuer's own arrival
             mbar_init(bar(tPFull + s), 128);
             mbar_init(bar(tPvDone + s), 1);
-            mbar_init(bar(tQFull + s), 128);
         }
+        mbar_init(bar(tQFull), 128);
+        mbar_init(bar(tQFull + 1), 128);
         mbar_init(bar(tSegDone), 256);
         mbar_init(bar(tDrain), 1);
+        mbar_init(bar(tDrain + 1), 1);
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -244,6 +249,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
     volatile uint32_t* abort_flag = misc + 1;
 
     auto wait = [&](int b, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar(b), parity)) return true;
         if (*abort_flag) return false;
         if (mbar_wait(bar(b), parity, tmo)) return true;
         *abort_flag = 1;
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
     };
     auto wait_warp = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
 
-    if (warp < kLoadWarps) {
+    if (warp < kMmaWarp) {
         // ------------------------------------------------------------ gather K and V
         // Warp 0 fills the K ring, warp 1 the V ring, each as its stages become
         // free. A tile whose 128 keys are all cached comes by TMA, in boxes that
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         uint64_t queue = 0;                   // stages of the groups on their way, 8 bits each, oldest lowest
         uint32_t pending = 0;
         uint32_t it = 0;                      // key tiles so far
-        bool ok = warp < 2;
+        bool ok = true;
         const int full0 = is_v ? tVFull : tKFull, empty0 = is_v ? tVEmpty : tKEmpty;
         const uint32_t ring0 = sbase + (is_v ? C::kV : C::kK);
         auto hand_over = [&](uint32_t keep) {     // the groups that are there, all but the last `keep`
@@ -303,7 +309,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             const SeqView& sv = walk.sv;
             const int32_t* kpos = a.c.positions && a.window_left >= 0 ? a.c.positions + (g.bi * a.c.h_kv + g.gk) * a.c.cap
                                                                       : nullptr;
-            const int32_t t0 = sub_tile(g, 0), t1 = sub_tile(g, sub_steps(g, sv.tiles) - 1);
+            const int32_t t0 = seg_tile0(g), t1 = t0 + seg_tiles(g, sv.tiles) - 1;
             const uint16_t* pool = (is_v ? a.c.v : a.c.k) + g.gk * (is_v ? a.c.v_stride[2] : a.c.k_stride[2]);
             const int64_t st_page = is_v ? a.c.v_stride[0] : a.c.k_stride[0], st_row = is_v ? a.c.v_stride[1] : a.c.k_stride[1];
             const uint16_t* fresh = (is_v ? a.v + g.bi * a.v_stride[0] + g.gk * a.v_stride[2]
@@ -397,70 +403,90 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         }
         cp_wait<0>();
         if (ok) hand_over(0);
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA issuer
-        constexpr uint32_t kIdS = idesc_f16(BF16, 128, 128, false, false);
+    } else if (warp < kSoftWarp0) {
+        // ------------------------------------------------------------ MMA issuer of slot `sl`
+        constexpr uint32_t kIdS = idesc_f16(BF16, 128, 64, false, false);
         constexpr uint32_t kIdPV = idesc_f16(BF16, 128, HD, false, true);
-        uint32_t it0 = 0, seg = 0;
-        uint32_t p_cnt[2] = {0u, 0u}, q_cnt[2] = {0u, 0u};
+        const int sl = warp - kMmaWarp;
+        uint32_t it0 = 0, seg = 0, twos = 0, p_par = 0;      // p_par: the parity of the next tile's P
         bool ok = true;
+        const uint32_t ts = tm_s0 + sl * 128, to = tm_o0 + sl * HD;
+        const uint64_t dk0 = sdesc_sw128(sbase + C::kK, 16, 1024);
+        const uint64_t dv0 = sdesc_sw128(sbase + C::kV, kBlk, 1024);
         while (walk.at < walk.end && ok) {
             const Seg g = walk.next(a);
-            const int32_t n = sub_steps(g, walk.sv.tiles);
-            const int nslots = g.two ? 2 : 1;      // row tiles
-            for (int s = 0; s < nslots && ok; ++s) {
-                ok = wait_warp(tQFull + s, q_cnt[s] & 1);
-                ++q_cnt[s];
-            }
-            // ring index of sub-step i's key tile
-            auto ring = [&](int32_t i) -> uint32_t { return it0 + (g.two ? i >> 1 : i); };
-            auto issue_s = [&](int32_t i) -> bool {
-                const uint32_t r = ring(i), st = r % NS;
-                const int sl = i & 1;
-                if ((!g.two || sl == 0) && !wait_warp(tKFull + st, (r / NS) & 1)) return false;
+            const int32_t tiles = seg_tiles(g, walk.sv.tiles);
+            const bool two = g.two;
+            // this slot's key tiles: all, or every other one
+            const int32_t first = two ? 0 : sl, step = two ? 1 : 2;
+            const uint64_t dq = sdesc_sw128(sbase + C::kQ + (two ? sl : 0) * C::kTile, 16, 1024);
+            // slot 0's rows come in every segment, slot 1's in those with two row tiles
+            if (first < tiles) ok = two && sl ? wait_warp(tQFull + 1, twos & 1) : wait_warp(tQFull, seg & 1);
+            twos += two ? 1 : 0;
+            auto k_wait = [&](int32_t t) -> bool {
+                const uint32_t r = it0 + t;
+                return wait_warp(tKFull + r % NS, (r / NS) & 1);
+            };
+            // S of a half: its buffer held the P whose product was issued before
+            auto issue_s = [&](int32_t t, int half) {
+                const uint32_t st = (it0 + t) % NS;
+                const uint64_t dk = sdesc_at(dk0, st * C::kTile + half * 8192);
                 tc_fence_after();
-                const uint64_t dq = sdesc_sw128(sbase + C::kQ + (g.two ? sl : 0) * C::kTile, 16, 1024);
-                const uint64_t dk = sdesc_sw128(sbase + C::kK + st * C::kTile, 16, 1024);
 #pragma unroll
                 for (int b = 0; b < HD / 64; ++b)
-                    umma_f16_ss_x4(tm_s0 + sl * 128, sdesc_at(dq, b * kBlk), 2, sdesc_at(dk, b * kBlk), 2, kIdS, b > 0);
-                umma_commit(bar(tSFull + sl));
-                if (lane == 0) mbar_arrive(bar(tSFull + sl));
-                if (!g.two || sl == 1) umma_commit(bar(tKEmpty + st));
-                __syncwarp();
-                return true;
+                    umma_f16_ss_x4(ts + half * 64, sdesc_at(dq, b * kBlk), 2, sdesc_at(dk, b * kBlk), 2, kIdS, b > 0);
+                umma_commit(bar(tSFull + sl * 2 + half));
+                if (lane == 0) mbar_arrive(bar(tSFull + sl * 2 + half));
+                if (half == 1) {
+                    // a K tile has two readers; a lone one counts twice
+                    umma_commit(bar(tKEmpty + st));
+                    if (!two) umma_commit(bar(tKEmpty + st));
+                }
             };
-            ok = ok && issue_s(0);
-            for (int32_t i = 0; i < n && ok; ++i) {
-                // S of the next sub-step goes first, unless its K is not there yet
-                const uint32_t rn = ring(i + 1);
-                const bool first = i + 1 < n && ((g.two && !(i & 1)) ||
-                                                 __all_sync(0xffffffffu, mbar_test(bar(tKFull + rn % NS), (rn / NS) & 1)));
-                if (first && !(ok = issue_s(i + 1))) break;
-                const uint32_t r = ring(i), st = r % NS;
-                const int sl = i & 1;
-                if ((!g.two || sl == 0) && !(ok = wait_warp(tVFull + st, (r / NS) & 1))) break;
-                if (!(ok = wait_warp(tPFull + sl, p_cnt[sl] & 1))) break;
-                ++p_cnt[sl];
-                // the first P V of a segment overwrites an O that has been read
-                if (i == 0 && seg > 0 && !(ok = wait_warp(tSegDone, (seg - 1) & 1))) break;
+            auto issue_pv = [&](int32_t t, int half, bool add) {
+                const uint32_t st = (it0 + t) % NS;
                 tc_fence_after();
-                const uint64_t dv = sdesc_sw128(sbase + C::kV + st * C::kTile, kBlk, 1024);
-                umma_f16_ts_x4(tm_o0 + sl * HD, tm_s0 + sl * 128, 8, dv, 2048 >> 4, kIdPV, i >= 2);
-                umma_f16_ts_x4(tm_o0 + sl * HD, tm_s0 + sl * 128 + 32, 8, sdesc_at(dv, 4 * 2048), 2048 >> 4, kIdPV, 1);
-                umma_commit(bar(tPvDone + sl));
-                if (!g.two || sl == 1) umma_commit(bar(tVEmpty + st));
-                __syncwarp();
-                if (!first && i + 1 < n) ok = issue_s(i + 1);
+                umma_f16_ts_x4(to, ts + half * 64, 8, sdesc_at(dv0, st * C::kTile + half * 8192), 2048 >> 4, kIdPV, add);
+                umma_commit(bar(tPvDone + sl * 2 + half));
+                if (half == 1) {
+                    umma_commit(bar(tVEmpty + st));
+                    if (!two) umma_commit(bar(tVEmpty + st));
+                }
+            };
+            if (ok && first < tiles && (ok = k_wait(first))) {
+                issue_s(first, 0);
+                issue_s(first, 1);
             }
-            it0 += g.two ? g.steps : n;
+            for (int32_t t = first; t < tiles && ok; t += step) {
+                const bool more = t + step < tiles;
+                const uint32_t r = it0 + t;
+                if (!(ok = wait_warp(tVFull + r % NS, (r / NS) & 1))) break;
+                if (!(ok = wait_warp(tPFull + sl * 2, p_par))) break;
+                // the first product of a segment overwrites an O that has been read
+                if (t == first && seg > 0 && !(ok = wait_warp(tSegDone, (seg - 1) & 1))) break;
+                issue_pv(t, 0, t != first);
+                const uint32_t rn = r + step;
+                const bool ahead = more && __all_sync(0xffffffffu, mbar_test(bar(tKFull + rn % NS), (rn / NS) & 1));
+                if (ahead) issue_s(t + step, 0);
+                if (!(ok = wait_warp(tPFull + sl * 2 + 1, p_par))) break;
+                issue_pv(t, 1, true);
+                p_par ^= 1;
+                if (more) {
+                    if (!ahead) {
+                        if (!(ok = k_wait(t + step))) break;
+                        issue_s(t + step, 0);
+                    }
+                    issue_s(t + step, 1);
+                }
+            }
+            it0 += tiles;
             ++seg;
             walk.advance(a, g);
         }
         // after a wait that ran out: MMAs in flight end before TMEM is freed
         if (!ok) {
-            umma_commit(bar(tDrain));
-            mbar_wait(bar(tDrain), 0, tmo);
+            umma_commit(bar(tDrain + sl));
+            mbar_wait(bar(tDrain + sl), 0, tmo);
         }
         __syncwarp();
     } else {
@@ -473,13 +499,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         const uint32_t tm_s = tm_s0 + sl * 128 + lane_off, tm_o = tm_o0 + sl * HD + lane_off;
         float2* ml = reinterpret_cast<float2*>(sm + C::kMl);
         uint64_t* masks = reinterpret_cast<uint64_t*>(sm + C::kMask);
-        uint32_t it0 = 0, cnt = 0;            // ring index at the segment's start; this slot's sub-steps so far
+        uint32_t it0 = 0, cnt = 0;            // ring index at the segment's start; this slot's sub-steps so far (two a tile)
         bool ok = true;
         const int64_t part0 = walk.at;
         while (walk.at < walk.end) {
             const Seg g = walk.next(a);
             const SeqView& sv = walk.sv;
-            const int32_t n = sub_steps(g, sv.tiles);
+            const int32_t tiles = seg_tiles(g, sv.tiles), t0 = seg_tile0(g), n = 4 * g.steps;
             named_sync(3, 256);               // the last segment's masks and statistics have been read
             if (sl == 0 && r < 64) {
                 const uint64_t in = sv.nq == 64 ? ~0ull : (1ull << sv.nq) - 1;
@@ -519,24 +545,31 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             const bool by_pos = windowed && a.c.positions != nullptr;
 
             float m = -INFINITY, l = 0.f;
-            for (int32_t i = sl; i < n; i += 2, ++cnt) {
-                ok = ok && wait(tSFull + sl, cnt & 1);
+            const uint32_t cnt0 = cnt;
+            for (int32_t i = sl; i < n; i += 2) {
+                const int32_t tt = sub_tile(g, i);
+                if (tt >= tiles) break;
+                const int half = (i >> 1) & 1, pb = sl * 2 + half;
+                const uint32_t my = cnt++;
+                ok = ok && wait(tSFull + pb, (my >> 1) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) continue;
                 tc_fence_after();
-                const int32_t t = sub_tile(g, i);
-                const uint32_t ring = (it0 + (g.two ? i >> 1 : i)) % kRing;
-                const int32_t x0 = t * 128;
-                const uint32_t* held = reinterpret_cast<const uint32_t*>(sm + C::kOk) + ring * 4;
-                // every key is cached, held and in the row's window, in all of the warp's rows
-                const bool all_held = (held[0] & held[1] & held[2] & held[3]) == 0xffffffffu;
-                const bool plain = x0 + 128 <= sv.new0 && all_held && !by_pos &&
+                const uint32_t ts = tm_s + half * 64;
+                uint32_t v[64];
+                tmem_ld32(ts, *reinterpret_cast<uint32_t(*)[32]>(v));
+                tmem_ld32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+                const uint32_t ring = (it0 + tt) % kRing;
+                const int32_t x0 = (t0 + tt) * 128 + half * 64;
+                const uint32_t* held = reinterpret_cast<const uint32_t*>(sm + C::kOk) + ring * 4 + half * 2;
+                // every key is cached, held and in the window of all of the warp's rows
+                const bool plain = x0 + 64 <= sv.new0 && (held[0] & held[1]) == 0xffffffffu && !by_pos &&
                                    !__any_sync(0xffffffffu, windowed && mask != 0 && sv.lo + x0 < low);
-                uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                uint32_t see[2] = {0xffffffffu, 0xffffffffu};
                 if (!plain) {
-                    const int32_t* pos = reinterpret_cast<const int32_t*>(sm + C::kPos) + ring * 128;
+                    const int32_t* pos = reinterpret_cast<const int32_t*>(sm + C::kPos) + ring * 128 + half * 64;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
+                    for (int w = 0; w < 2; ++w) {
                         uint32_t s = held[w];
                         const int32_t xw = x0 + w * 32;
                         if (mask == 0) s = 0;
@@ -558,92 +591,68 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                         see[w] = s;
                     }
                 }
-                auto softmax = [&](auto masked) {
-                    constexpr bool M = decltype(masked)::value;
-                    float mt = -INFINITY;
+                tmem_ld_wait();
+                if (!plain) {
 #pragma unroll
-                    for (int cb = 0; cb < 4; ++cb) {
-                        uint32_t v[32];
-                        tmem_ld32(tm_s + cb * 32, v);
-                        tmem_ld_wait();
-                        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    for (int e = 0; e < 64; ++e)
+                        if (!((see[e >> 5] >> (e & 31)) & 1)) v[e] = 0xff800000u;   // -inf
+                }
+                float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float f = __uint_as_float(v[e]);
-                            x[e & 3] = fmaxf(x[e & 3], !M || ((see[cb] >> e) & 1) ? f : -INFINITY);
-                        }
-                        mt = fmaxf(mt, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-                    }
-                    const float top = mt * a.scale_log2;
-                    const bool up = top > m + 8.f;
-                    if (__any_sync(0xffffffffu, up)) {
-                        const float mn = up ? top : m;
-                        const float al = m == -INFINITY ? 0.f : ex2_approx(m - mn);
-                        const float f = up ? al : 1.f;
-                        l *= f;
-                        m = mn;
-                        if (i >= 2) {
-                            // O holds the P V of this slot's earlier key tiles: they are done before it changes
-                            ok = __all_sync(0xffffffffu, wait(tPvDone + sl, (cnt - 1) & 1));
-                            tc_fence_after();
-                            if (ok) {
+                for (int e = 0; e < 64; ++e) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(v[e]));
+                const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.scale_log2;
+                const bool up = top > m + 8.f;
+                if (__any_sync(0xffffffffu, up)) {
+                    const float f = !up ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - top);
+                    l *= f;
+                    m = up ? top : m;
+                    if (my != cnt0) {
+                        // O holds the P V of this slot's earlier keys: they are done before it changes
+                        ok = __all_sync(0xffffffffu, wait(tPvDone + (pb ^ 1), ((my - 1) >> 1) & 1));
+                        tc_fence_after();
+                        if (ok) {
 #pragma unroll 1
-                                for (int cb = 0; cb < HD / 32; ++cb) {
-                                    uint32_t v[32];
-                                    tmem_ld32(tm_o + cb * 32, v);
-                                    tmem_ld_wait();
+                            for (int cb = 0; cb < HD / 16; ++cb) {
+                                uint32_t o16[16];
+                                tmem_ld16(tm_o + cb * 16, o16);
+                                tmem_ld_wait();
 #pragma unroll
-                                    for (int q = 0; q < 4; ++q) {
-                                        uint32_t w8[8];
+                                for (int q = 0; q < 2; ++q) {
+                                    uint32_t w8[8];
 #pragma unroll
-                                        for (int e = 0; e < 8; ++e)
-                                            w8[e] = __float_as_uint(__uint_as_float(v[8 * q + e]) * f);
-                                        tmem_st8(tm_o + cb * 32 + 8 * q, w8);
-                                    }
+                                    for (int e = 0; e < 8; ++e)
+                                        w8[e] = __float_as_uint(__uint_as_float(o16[8 * q + e]) * f);
+                                    tmem_st8(tm_o + cb * 16 + 8 * q, w8);
                                 }
-                                tmem_st_wait();
                             }
+                            tmem_st_wait();
                         }
                     }
-                    // P over the columns of S that have been read
-                    const float mr = m == -INFINITY ? 0.f : m;
-                    float ps[4] = {0.f, 0.f, 0.f, 0.f};
+                }
+                // P over the first columns of its S
+                const float mr = m == -INFINITY ? 0.f : m;
+                float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int cb = 0; cb < 4; ++cb) {
-                        uint32_t v[32], pk[16];
-                        tmem_ld32(tm_s + cb * 32, v);
-                        tmem_ld_wait();
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w8[8];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float p0 = ex2_approx(fmaf(__uint_as_float(v[e]), a.scale_log2, -mr));
-                            float p1 = ex2_approx(fmaf(__uint_as_float(v[e + 1]), a.scale_log2, -mr));
-                            if (M) {
-                                p0 = (see[cb] >> e) & 1 ? p0 : 0.f;
-                                p1 = (see[cb] >> (e + 1)) & 1 ? p1 : 0.f;
-                            }
-                            ps[(e >> 1) & 3] += p0 + p1;
-                            pk[e >> 1] = pack2<BF16>(p0, p1);
-                        }
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t w8[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) w8[e] = pk[8 * q + e];
-                            tmem_st8(tm_s + cb * 16 + 8 * q, w8);
-                        }
+                    for (int e = 0; e < 8; ++e) {
+                        // a masked score is -inf, its P is 0
+                        const float p0 = ex2_approx(fmaf(__uint_as_float(v[16 * q + 2 * e]), a.scale_log2, -mr));
+                        const float p1 = ex2_approx(fmaf(__uint_as_float(v[16 * q + 2 * e + 1]), a.scale_log2, -mr));
+                        ps[e & 3] += p0 + p1;
+                        w8[e] = pack2<BF16>(p0, p1);
                     }
-                    l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-                    tmem_st_wait();
-                };
-                if (plain) softmax(std::false_type{});
-                else softmax(std::true_type{});
+                    tmem_st8(ts + 8 * q, w8);
+                }
+                l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(bar(tPFull + sl));
+                mbar_arrive(bar(tPFull + pb));
             }
             // the slot's last P V is done
-            const bool any = n > sl;
-            if (any) {
-                ok = ok && wait(tPvDone + sl, (cnt - 1) & 1);
+            if (cnt != cnt0) {
+                ok = ok && wait(tPvDone + sl * 2 + 1, ((cnt - 1) >> 1) & 1);
                 ok = __all_sync(0xffffffffu, ok);
             }
             tc_fence_after();
@@ -665,7 +674,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 const float2 x = ml[row], y = ml[128 + row];
                 top = fmaxf(x.x, y.x);
                 f0 = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top);
-                f1 = n < 2 || y.x == -INFINITY ? 0.f : ex2_approx(y.x - top);
+                f1 = tiles < 2 || y.x == -INFINITY ? 0.f : ex2_approx(y.x - top);
                 sum = f0 * x.y + f1 * y.y;
             }
             const int cb0 = g.two ? 0 : sl * (HD / 64), cb1 = g.two ? HD / 32 : cb0 + HD / 64;
@@ -679,7 +688,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = dead || f0 == 0.f ? 0.f : f0 * __uint_as_float(v[e]);
-                    if (!g.two && n > 1) {
+                    if (!g.two && tiles > 1) {
                         tmem_ld32(tm_o0 + HD + lane_off + cb * 32, v);
                         tmem_ld_wait();
 #pragma unroll
@@ -705,7 +714,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             }
             tc_fence_before();
             mbar_arrive(bar(tSegDone));
-            it0 += g.two ? g.steps : n;
+            it0 += tiles;
             walk.advance(a, g);
         }
         if (sl == 0 && r == 0 && !a.whole) a.cuts[blockIdx.x] = cut;
