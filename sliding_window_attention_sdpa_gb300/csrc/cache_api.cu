@@ -168,8 +168,8 @@ FwdSize fwd_size(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa:
     if (p->window_left >= 0 && c->positions == nullptr && p->window_left < keys) keys = p->window_left;
     const int64_t rows = p->s_q * (p->h_q / c->h_kv);
     z.blocks = (rows + plan.rows - 1) / plan.rows;
-    // the reach begins up to 15 keys before (127 in the tile kernel), the new tokens end up to 15 off a group of 16
-    z.tiles = (keys + (plan.variant >= swa::kTiles128 ? 142 : 30) + ((p->s_q + 15) & ~int64_t(15)) + plan.tile - 1) / plan.tile;
+    // the reach begins up to 15 keys before (63 in the tile kernel), the new tokens end up to 15 off a group of 16
+    z.tiles = (keys + (plan.variant >= swa::kTiles128 ? 78 : 30) + ((p->s_q + 15) & ~int64_t(15)) + plan.tile - 1) / plan.tile;
     z.units = double(c->b) * double(c->h_kv) * double(z.blocks);
     z.total = z.units * double(z.tiles);
     return z;
@@ -180,16 +180,16 @@ struct FwdLayout {
     size_t part_o, part_ml, cuts, total;
 };
 
-// Units of up to kWholeTiles tiles go to one CTA each. Else the work is cut into
+// Units of up to kWholeKeys keys go to one CTA each. Else the work is cut into
 // as many parts as CTAs are resident on a GB300 (152 SMs), fewer if there are
 // fewer tiles; each has two partials.
-constexpr int64_t kWholeTiles = 4;
+constexpr int64_t kWholeKeys = 512;
 
 FwdLayout fwd_layout(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa::CacheFwdPlan& plan)
 {
     FwdLayout l{};
     const FwdSize z = fwd_size(c, p, plan);
-    if (z.tiles <= kWholeTiles && z.units < double(kMax31)) {
+    if (z.tiles * plan.tile <= kWholeKeys && z.units < double(kMax31)) {
         l.parts = static_cast<int32_t>(z.units);
         l.whole = 1;
         return l;
@@ -345,8 +345,8 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.part_ml = at<float>(ws, l.part_ml);
     a.cuts = at<swa::CacheFwdCut>(ws, l.cuts);
     if (plan.variant >= swa::kTiles128 && c->n_pages > 0) {
-        // boxes of up to 128 rows that divide a page; an unpaged sequence's keys follow one another
-        int32_t rows = 128;
+        // boxes of up to 64 rows (a key tile) that divide a page; an unpaged sequence's keys follow one another
+        int32_t rows = 64;
         while (c->page_table != nullptr && c->page_size % rows != 0) rows >>= 1;
         if (rows >= 8 && make_rows_map(&ta.tm_k, c->k, c->dtype, c->d, c->h_kv, c->page_size, c->n_pages, c->k_stride, rows) &&
             make_rows_map(&ta.tm_v, c->v, c->dtype, c->d, c->h_kv, c->page_size, c->n_pages, c->v_stride, rows))

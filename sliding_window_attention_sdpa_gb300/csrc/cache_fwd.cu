@@ -617,12 +617,12 @@ CacheFwdPlan cache_fwd_plan(int64_t d, int64_t rows)
     if (d == 128) {
         if (rows <= 8) return CacheFwdPlan{kRows128x8, 8, 64, 3};
         if (rows <= 16) return CacheFwdPlan{kRows128x16, 16, 64, 2};
-        return CacheFwdPlan{kTiles128, 256, 128, 1};
+        return CacheFwdPlan{kTiles128, 256, 64, 1};
     }
     if (rows <= 8) return CacheFwdPlan{kRows64x8, 8, 128, 4};
     if (rows <= 16) return CacheFwdPlan{kRows64x16, 16, 128, 3};
     if (rows <= 32) return CacheFwdPlan{kRows64x32, 32, 128, 2};
-    return CacheFwdPlan{kTiles64, 256, 128, 1};
+    return CacheFwdPlan{kTiles64, 256, 64, 1};
 }
 
 cudaError_t launch_cache_fwd(const CacheTileArgs& a, int dtype, cudaStream_t s)

@@ -13,7 +13,7 @@
 //
 // Roles (384 threads): warp 0 loads K, warp 1 V into two rings in the 128-byte
 // swizzle; warps 2 and 3 issue a slot's MMAs each (one warp for both was the
-// bottleneck: its issue of a sub-step's 12 MMAs takes longer than they run);
+// bottleneck: its issue of a tile's 12 MMAs takes longer than they run);
 // warps 4-7 and 8-11 are the slots' softmax groups, one row per thread. A row's reference moves only when a score exceeds it by 2^8, so O is
 // seldom rescaled. P is rounded to the I/O dtype, as the prompt's forward does.
 //
@@ -32,35 +32,40 @@ namespace {
 constexpr int kTileThreads = 384;
 constexpr int kMmaWarp = 2;            // and 3
 constexpr int kSoftWarp0 = 4;
-constexpr uint32_t kBlk = 128 * 128;   // one 64-column block of a 128-row 16-bit tile
-constexpr int kRing = 8;               // key tiles whose validity and positions are kept
+constexpr int kKeys = 64;              // keys of a tile
+constexpr uint32_t kQBlk = 128 * 128;  // one 64-column block of a 128-row 16-bit tile
+constexpr uint32_t kBlk = kKeys * 128; // the same of a key tile
+constexpr int kRing = 16;              // key tiles whose validity and positions are kept
 
 template <int HD>
 struct TileCfg {
-    static constexpr uint32_t kTile = 128 * HD * 2;
-    static constexpr int kStages = HD == 128 ? 2 : 4;
+    static constexpr uint32_t kQTile = 128 * HD * 2;
+    static constexpr uint32_t kTile = kKeys * HD * 2;
+    static constexpr int kStages = HD == 128 ? 4 : 8;
     static constexpr uint32_t kQ = 0;                           // 2 slots
-    static constexpr uint32_t kK = kQ + 2 * kTile;
+    static constexpr uint32_t kK = kQ + 2 * kQTile;
     static constexpr uint32_t kV = kK + kStages * kTile;
-    static constexpr uint32_t kPos = kV + kStages * kTile;      // int32 [kRing][128]
-    static constexpr uint32_t kOk = kPos + kRing * 512;         // uint32 [kRing][4]
-    static constexpr uint32_t kMask = kOk + kRing * 16;         // uint64 [64]
+    static constexpr uint32_t kPos = kV + kStages * kTile;      // int32 [kRing][64]
+    static constexpr uint32_t kOk = kPos + kRing * 256;         // uint32 [kRing][2]
+    static constexpr uint32_t kMask = kOk + kRing * 8;          // uint64 [64]
     static constexpr uint32_t kMl = kMask + 512;                // float2 [2][128]
     static constexpr uint32_t kBars = kMl + 2048;
-    static constexpr uint32_t kMisc = kBars + 320;
+    static constexpr uint32_t kMisc = kBars + 448;
     static constexpr uint32_t kBytes = kMisc + 256;
     static_assert(kBytes <= 232448, "shared memory above the 227 KB a CTA may opt into");
 };
 
-// mbarriers; per-stage and per-slot ones at index + stage or slot
-// (S, P and P V: slot * 2 + half of the key tile)
-enum TBar : int { tKFull = 0, tKEmpty = 4, tVFull = 8, tVEmpty = 12, tSFull = 16, tPFull = 20, tPvDone = 24, tQFull = 28,
-                  tSegDone = 30, tDrain = 31, tNumBars = 33 };
-static_assert(tNumBars * 8 <= 320, "mbarrier area");
+// mbarriers; per-stage and per-slot ones at index + stage or slot (S, P and
+// P V: slot * 2 + buffer)
+enum TBar : int { tKFull = 0, tKEmpty = 8, tVFull = 16, tVEmpty = 24, tSFull = 32, tPFull = 36, tPvDone = 40, tQFull = 44,
+                  tSegDone = 46, tDrain = 47, tNumBars = 49 };
+static_assert(tNumBars * 8 <= 448, "mbarrier area");
 
+// 16-byte chunk of a row of a swizzled tile whose 64-column blocks are BLK bytes.
+template <uint32_t BLK>
 __device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t chunk)
 {
-    return (chunk >> 3) * kBlk + (row >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+    return (chunk >> 3) * BLK + (row >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
 // 16 bytes to shared memory; zeros (nothing read) if not `have`.
@@ -84,6 +89,41 @@ template <int N>
 __device__ __forceinline__ void cp_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The MMAs below are issued by one elected thread (elect.sync tells the
+// compiler that the branch holds one): back to back 64 cycles each at N = 128,
+// 48 (A from shared memory) or 32 (from TMEM) at N = 64, against 87, 71 and 52
+// with the whole warp running the code and a predicate on the instruction.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+// Arrives once on `bar` when this thread's MMAs so far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads)
@@ -126,7 +166,7 @@ struct Walk {
     __device__ __forceinline__ Seg next(const CacheFwdArgs& a)
     {
         if (!loaded) {
-            sv = seq_view(a, bi, 128, 128);
+            sv = seq_view(a, bi, kKeys, kKeys);
             sh = shape_of(sv, na, nb);
             loaded = true;
         }
@@ -161,10 +201,6 @@ __device__ __forceinline__ int32_t seg_tiles(const Seg& g, int32_t tiles)
 {
     return g.two ? g.steps : min(2 * (g.step0 + g.steps), tiles) - 2 * g.step0;
 }
-// Sub-step i of a segment: slot i & 1, half (i >> 1) & 1 of the key tile that
-// this gives (counted from the segment's first).
-__device__ __forceinline__ int32_t sub_tile(const Seg& g, int32_t i) { return g.two ? i >> 2 : 2 * (i >> 2) + (i & 1); }
-
 }  // namespace
 
 template <int HD, bool BF16>
@@ -200,12 +236,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         const int64_t units = a.c.h_kv * blocks;
         part.bi = blockIdx.x / units;
         const int64_t un = blockIdx.x - part.bi * units, gk = un / blocks, blk = un - gk * blocks;
-        const Shape s = shape_of(seq_view(a, part.bi, 128, 128), na, nb);
+        const Shape s = shape_of(seq_view(a, part.bi, kKeys, kKeys), na, nb);
         part.rem = gk * s.per_head + blk * s.ta;
         part.end = blk < na ? s.ta : s.tb;
     } else {
         part = find_part<kTileThreads>(
-            a.c.b, [&](int64_t i) { return a.c.h_kv * shape_of(seq_view(a, i, 128, 128), na, nb).per_head; }, sh_sum, sh_at);
+            a.c.b, [&](int64_t i) { return a.c.h_kv * shape_of(seq_view(a, i, kKeys, kKeys), na, nb).per_head; }, sh_sum, sh_at);
         if (part.end == 0) {
             if (tid == 0) a.cuts[blockIdx.x] = cut;
             grid_dep_launch();
@@ -220,9 +256,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
     if (tid == 0) {
         misc[1] = 0;
         for (int i = 0; i < NS; ++i) {
-            mbar_init(bar(tKFull + i), 4);
+            mbar_init(bar(tKFull + i), 2);
             mbar_init(bar(tKEmpty + i), 2);
-            mbar_init(bar(tVFull + i), 4);
+            mbar_init(bar(tVFull + i), 2);
             mbar_init(bar(tVEmpty + i), 2);
         }
         for (int s = 0; s < 4; ++s) {
@@ -261,14 +297,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
     if (warp < kMmaWarp) {
         // ------------------------------------------------------------ gather K and V
         // Warp 0 fills the K ring, warp 1 the V ring, each as its stages become
-        // free. A tile whose 128 keys are all cached comes by TMA, in boxes that
+        // free. A tile whose keys are all cached comes by TMA, in boxes that
         // lie within a page (box_rows, a power of two that divides the page size);
         // the last tiles of a unit, and all of them where pages have no such
         // divisor, are gathered 16 bytes at a time, 32 keys a group, zeros in the
         // rows that are not held. A gathered group is handed over (writes made
         // visible to the async proxy, barrier) when LAG later ones are on their
         // way, or while the warp has to wait for a stage. A stage is full after
-        // four arrivals, one for each 32 keys.
+        // two arrivals, one for each 32 keys.
         const bool is_v = warp == 1;
         constexpr int CPR = HD / 8;           // 16-byte chunks of a row
         constexpr int RPI = 32 / CPR;         // rows that a warp copies at once
@@ -325,37 +361,35 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 return a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)
                                            : static_cast<uint32_t>(j) % a.c.page_size;
             };
-            const int boxes = ta.box_rows ? 128 / ta.box_rows : 0;
+            const int boxes = ta.box_rows ? kKeys / ta.box_rows : 0;
             // a TMA tile's page of lane's box, a tile ahead
             auto box_entry = [&](int32_t t) -> int32_t {
-                const int32_t j = sv.lo + t * 128 + lane * ta.box_rows;
+                const int32_t j = sv.lo + t * kKeys + lane * ta.box_rows;
                 return lane < boxes && t <= t1 && j < sv.len ? entry_of(j) : 0;
             };
             int32_t entry = box_entry(t0);
             for (int32_t t = t0; t <= t1; ++t, ++it) {
                 const uint32_t st = it % NS, par = (it / NS) & 1;
-                const int32_t x0 = t * 128, j0 = sv.lo + x0;
+                const int32_t x0 = t * kKeys, j0 = sv.lo + x0;
                 const int32_t mine = entry;
                 entry = box_entry(t + 1);
                 const bool good = lane >= boxes || (mine >= 0 && mine < a.c.n_pages);
-                const bool by_tma = boxes > 0 && x0 + 128 <= sv.new0 && j0 + 128 <= sv.len && __all_sync(0xffffffffu, good);
+                const bool by_tma = boxes > 0 && x0 + kKeys <= sv.new0 && j0 + kKeys <= sv.len && __all_sync(0xffffffffu, good);
                 if (!(ok = acquire(empty0 + st, par ^ 1))) break;
                 const uint32_t stage = ring0 + st * C::kTile;
                 if (!is_v && a.window_left >= 0) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 2; ++k) {
                         const int32_t j = j0 + k * 32 + lane;
-                        reinterpret_cast<int32_t*>(sm + C::kPos)[(it % kRing) * 128 + k * 32 + lane] =
+                        reinterpret_cast<int32_t*>(sm + C::kPos)[(it % kRing) * kKeys + k * 32 + lane] =
                             kpos && j < sv.len ? kpos[j] : j;
                     }
                 }
                 if (by_tma) {
-                    if (!is_v && lane < 4) reinterpret_cast<uint32_t*>(sm + C::kOk)[(it % kRing) * 4 + lane] = 0xffffffffu;
+                    if (!is_v && lane < 2) reinterpret_cast<uint32_t*>(sm + C::kOk)[(it % kRing) * 2 + lane] = 0xffffffffu;
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar(full0 + st), C::kTile);
-                        mbar_arrive(bar(full0 + st));
-                        mbar_arrive(bar(full0 + st));
                         mbar_arrive(bar(full0 + st));
                     }
                     __syncwarp();
@@ -370,7 +404,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                     continue;
                 }
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 2; ++k) {
                     // this lane's key
                     const int32_t x = x0 + k * 32 + lane, j = sv.lo + x;
                     const uint16_t* p = fresh;
@@ -387,12 +421,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                         p = fresh + (x - sv.new0) * st_new;
                     }
                     const uint32_t held = __ballot_sync(0xffffffffu, have);
-                    if (!is_v && lane == 0) reinterpret_cast<uint32_t*>(sm + C::kOk)[(it % kRing) * 4 + k] = held;
+                    if (!is_v && lane == 0) reinterpret_cast<uint32_t*>(sm + C::kOk)[(it % kRing) * 2 + k] = held;
 #pragma unroll 8
                     for (int i = 0; i < 32 / RPI; ++i) {
                         const int r = i * RPI + sub;
                         const uint64_t q = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(p), r);
-                        cp16(stage + swz(k * 32 + r, c), reinterpret_cast<const uint16_t*>(q) + c * 8, (held >> r) & 1);
+                        cp16(stage + swz<kBlk>(k * 32 + r, c), reinterpret_cast<const uint16_t*>(q) + c * 8, (held >> r) & 1);
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
                     queue |= static_cast<uint64_t>(st) << (8 * pending);
@@ -408,85 +442,71 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         constexpr uint32_t kIdS = idesc_f16(BF16, 128, 64, false, false);
         constexpr uint32_t kIdPV = idesc_f16(BF16, 128, HD, false, true);
         const int sl = warp - kMmaWarp;
-        uint32_t it0 = 0, seg = 0, twos = 0, p_par = 0;      // p_par: the parity of the next tile's P
+        uint32_t it0 = 0, seg = 0, twos = 0, done = 0;       // done: this slot's key tiles before the segment
         bool ok = true;
         const uint32_t ts = tm_s0 + sl * 128, to = tm_o0 + sl * HD;
         const uint64_t dk0 = sdesc_sw128(sbase + C::kK, 16, 1024);
         const uint64_t dv0 = sdesc_sw128(sbase + C::kV, kBlk, 1024);
+        if (elect_one()) {
         while (walk.at < walk.end && ok) {
             const Seg g = walk.next(a);
             const int32_t tiles = seg_tiles(g, walk.sv.tiles);
             const bool two = g.two;
             // this slot's key tiles: all, or every other one
             const int32_t first = two ? 0 : sl, step = two ? 1 : 2;
-            const uint64_t dq = sdesc_sw128(sbase + C::kQ + (two ? sl : 0) * C::kTile, 16, 1024);
+            const int32_t n = tiles > first ? (tiles - first + step - 1) / step : 0;
+            const uint64_t dq = sdesc_sw128(sbase + C::kQ + (two ? sl : 0) * C::kQTile, 16, 1024);
             // slot 0's rows come in every segment, slot 1's in those with two row tiles
-            if (first < tiles) ok = two && sl ? wait_warp(tQFull + 1, twos & 1) : wait_warp(tQFull, seg & 1);
+            if (n > 0) ok = two && sl ? wait(tQFull + 1, twos & 1) : wait(tQFull, seg & 1);
             twos += two ? 1 : 0;
-            auto k_wait = [&](int32_t t) -> bool {
-                const uint32_t r = it0 + t;
-                return wait_warp(tKFull + r % NS, (r / NS) & 1);
-            };
-            // S of a half: its buffer held the P whose product was issued before
-            auto issue_s = [&](int32_t t, int half) {
-                const uint32_t st = (it0 + t) % NS;
-                const uint64_t dk = sdesc_at(dk0, st * C::kTile + half * 8192);
+            // S of the slot's i-th tile goes two ahead, into the buffer whose P V was issued last; it is put
+            // off while its K is not there and a product can go first
+            int32_t si = 0;
+            for (int32_t i = 0; i < n && ok; ++i) {
+                for (; si < n && si <= i + 1; ++si) {
+                    const uint32_t r = it0 + first + si * step, st = r % NS;
+                    if (si == i) {
+                        if (!(ok = wait(tKFull + st, (r / NS) & 1))) break;
+                    } else if (!mbar_test(bar(tKFull + st), (r / NS) & 1)) {
+                        break;
+                    }
+                    const uint32_t b = (done + si) & 1;
+                    const uint64_t dk = sdesc_at(dk0, st * C::kTile);
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k)
+                        mma_ss(ts + b * 64, sdesc_at(dq, (k >> 2) * kQBlk + (k & 3) * 32),
+                               sdesc_at(dk, (k >> 2) * kBlk + (k & 3) * 32), kIdS, k > 0);
+                    mma_commit(bar(tSFull + sl * 2 + b));
+                    mbar_arrive(bar(tSFull + sl * 2 + b));
+                    // a K tile has two readers; a lone one counts twice
+                    mma_commit(bar(tKEmpty + st));
+                    if (!two) mma_commit(bar(tKEmpty + st));
+                }
+                if (!ok) break;
+                const uint32_t r = it0 + first + i * step, st = r % NS, b = (done + i) & 1;
+                if (!(ok = wait(tVFull + st, (r / NS) & 1))) break;
+                if (!(ok = wait(tPFull + sl * 2 + b, ((done + i) >> 1) & 1))) break;
+                // the first product of a segment overwrites an O that has been read
+                if (i == 0 && seg > 0 && !(ok = wait(tSegDone, (seg - 1) & 1))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int b = 0; b < HD / 64; ++b)
-                    umma_f16_ss_x4(ts + half * 64, sdesc_at(dq, b * kBlk), 2, sdesc_at(dk, b * kBlk), 2, kIdS, b > 0);
-                umma_commit(bar(tSFull + sl * 2 + half));
-                if (lane == 0) mbar_arrive(bar(tSFull + sl * 2 + half));
-                if (half == 1) {
-                    // a K tile has two readers; a lone one counts twice
-                    umma_commit(bar(tKEmpty + st));
-                    if (!two) umma_commit(bar(tKEmpty + st));
-                }
-            };
-            auto issue_pv = [&](int32_t t, int half, bool add) {
-                const uint32_t st = (it0 + t) % NS;
-                tc_fence_after();
-                umma_f16_ts_x4(to, ts + half * 64, 8, sdesc_at(dv0, st * C::kTile + half * 8192), 2048 >> 4, kIdPV, add);
-                umma_commit(bar(tPvDone + sl * 2 + half));
-                if (half == 1) {
-                    umma_commit(bar(tVEmpty + st));
-                    if (!two) umma_commit(bar(tVEmpty + st));
-                }
-            };
-            if (ok && first < tiles && (ok = k_wait(first))) {
-                issue_s(first, 0);
-                issue_s(first, 1);
+                for (int k = 0; k < kKeys / 16; ++k)
+                    mma_ts(to, ts + b * 64 + k * 8, sdesc_at(dv0, st * C::kTile + k * 2048), kIdPV, i > 0 || k > 0);
+                mma_commit(bar(tPvDone + sl * 2 + b));
+                mma_commit(bar(tVEmpty + st));
+                if (!two) mma_commit(bar(tVEmpty + st));
             }
-            for (int32_t t = first; t < tiles && ok; t += step) {
-                const bool more = t + step < tiles;
-                const uint32_t r = it0 + t;
-                if (!(ok = wait_warp(tVFull + r % NS, (r / NS) & 1))) break;
-                if (!(ok = wait_warp(tPFull + sl * 2, p_par))) break;
-                // the first product of a segment overwrites an O that has been read
-                if (t == first && seg > 0 && !(ok = wait_warp(tSegDone, (seg - 1) & 1))) break;
-                issue_pv(t, 0, t != first);
-                const uint32_t rn = r + step;
-                const bool ahead = more && __all_sync(0xffffffffu, mbar_test(bar(tKFull + rn % NS), (rn / NS) & 1));
-                if (ahead) issue_s(t + step, 0);
-                if (!(ok = wait_warp(tPFull + sl * 2 + 1, p_par))) break;
-                issue_pv(t, 1, true);
-                p_par ^= 1;
-                if (more) {
-                    if (!ahead) {
-                        if (!(ok = k_wait(t + step))) break;
-                        issue_s(t + step, 0);
-                    }
-                    issue_s(t + step, 1);
-                }
-            }
+            done += n;
             it0 += tiles;
             ++seg;
             walk.advance(a, g);
         }
         // after a wait that ran out: MMAs in flight end before TMEM is freed
         if (!ok) {
-            umma_commit(bar(tDrain + sl));
+            mma_commit(bar(tDrain + sl));
             mbar_wait(bar(tDrain + sl), 0, tmo);
+        }
         }
         __syncwarp();
     } else {
@@ -499,13 +519,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         const uint32_t tm_s = tm_s0 + sl * 128 + lane_off, tm_o = tm_o0 + sl * HD + lane_off;
         float2* ml = reinterpret_cast<float2*>(sm + C::kMl);
         uint64_t* masks = reinterpret_cast<uint64_t*>(sm + C::kMask);
-        uint32_t it0 = 0, cnt = 0;            // ring index at the segment's start; this slot's sub-steps so far (two a tile)
+        uint32_t it0 = 0, cnt = 0;            // ring index at the segment's start; this slot's key tiles so far
         bool ok = true;
         const int64_t part0 = walk.at;
         while (walk.at < walk.end) {
             const Seg g = walk.next(a);
             const SeqView& sv = walk.sv;
-            const int32_t tiles = seg_tiles(g, sv.tiles), t0 = seg_tile0(g), n = 4 * g.steps;
+            const int32_t tiles = seg_tiles(g, sv.tiles), t0 = seg_tile0(g);
             named_sync(3, 256);               // the last segment's masks and statistics have been read
             if (sl == 0 && r < 64) {
                 const uint64_t in = sv.nq == 64 ? ~0ull : (1ull << sv.nq) - 1;
@@ -530,7 +550,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
 #pragma unroll
                 for (int c = 0; c < HD / 8; ++c) {
                     const uint4 x = real ? ld_nc_v4(qp + c * 8) : make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(sm + C::kQ + sl * C::kTile + swz(row, c)) = x;
+                    *reinterpret_cast<uint4*>(sm + C::kQ + sl * C::kQTile + swz<kQBlk>(row, c)) = x;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(bar(tQFull + sl));
@@ -546,28 +566,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
 
             float m = -INFINITY, l = 0.f;
             const uint32_t cnt0 = cnt;
-            for (int32_t i = sl; i < n; i += 2) {
-                const int32_t tt = sub_tile(g, i);
-                if (tt >= tiles) break;
-                const int half = (i >> 1) & 1, pb = sl * 2 + half;
-                const uint32_t my = cnt++;
+            for (int32_t tt = g.two ? 0 : sl; tt < tiles; tt += g.two ? 1 : 2) {
+                const uint32_t my = cnt++, pb = sl * 2 + (my & 1);
                 ok = ok && wait(tSFull + pb, (my >> 1) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) continue;
                 tc_fence_after();
-                const uint32_t ts = tm_s + half * 64;
+                const uint32_t ts = tm_s + (my & 1) * 64;
                 uint32_t v[64];
                 tmem_ld32(ts, *reinterpret_cast<uint32_t(*)[32]>(v));
                 tmem_ld32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
                 const uint32_t ring = (it0 + tt) % kRing;
-                const int32_t x0 = (t0 + tt) * 128 + half * 64;
-                const uint32_t* held = reinterpret_cast<const uint32_t*>(sm + C::kOk) + ring * 4 + half * 2;
+                const int32_t x0 = (t0 + tt) * kKeys;
+                const uint32_t* held = reinterpret_cast<const uint32_t*>(sm + C::kOk) + ring * 2;
                 // every key is cached, held and in the window of all of the warp's rows
-                const bool plain = x0 + 64 <= sv.new0 && (held[0] & held[1]) == 0xffffffffu && !by_pos &&
+                const bool plain = x0 + kKeys <= sv.new0 && (held[0] & held[1]) == 0xffffffffu && !by_pos &&
                                    !__any_sync(0xffffffffu, windowed && mask != 0 && sv.lo + x0 < low);
                 uint32_t see[2] = {0xffffffffu, 0xffffffffu};
                 if (!plain) {
-                    const int32_t* pos = reinterpret_cast<const int32_t*>(sm + C::kPos) + ring * 128 + half * 64;
+                    const int32_t* pos = reinterpret_cast<const int32_t*>(sm + C::kPos) + ring * kKeys;
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         uint32_t s = held[w];
@@ -652,7 +669,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             }
             // the slot's last P V is done
             if (cnt != cnt0) {
-                ok = ok && wait(tPvDone + sl * 2 + 1, ((cnt - 1) >> 1) & 1);
+                ok = ok && wait(tPvDone + sl * 2 + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1);
                 ok = __all_sync(0xffffffffu, ok);
             }
             tc_fence_after();
