@@ -2,6 +2,7 @@
 // argument checks and the launches on the caller's stream. Nothing here
 // allocates or synchronises (except sdpa_cache_check_status).
 #include <cstring>
+#include <cstdlib>
 
 #include <cuda_runtime.h>
 
@@ -340,15 +341,20 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.lse = p->lse;
     a.parts = l.parts;
     a.whole = l.whole;
+    a.cut_by_unit = fwd_size(c, p, plan).units <= l.parts;
+    a.min_tiles = getenv("MT") ? atoi(getenv("MT")) : 1;
     a.timeout_ns = kWaitLimitNs;
     a.part_o = at<float>(ws, l.part_o);
     a.part_ml = at<float>(ws, l.part_ml);
     a.cuts = at<swa::CacheFwdCut>(ws, l.cuts);
-    if (plan.variant >= swa::kTiles128 && c->n_pages > 0) {
-        // boxes of up to 64 rows (a key tile) that divide a page; an unpaged sequence's keys follow one another
-        int32_t rows = 64;
+    if (c->n_pages > 0) {
+        // boxes that divide a page: up to 64 rows (a key tile) for the tile kernel, 16 for the other; an unpaged
+        // sequence's keys follow one another
+        const bool tiles = plan.variant >= swa::kTiles128;
+        int32_t rows = tiles ? 64 : 16;
         while (c->page_table != nullptr && c->page_size % rows != 0) rows >>= 1;
-        if (rows >= 8 && make_rows_map(&ta.tm_k, c->k, c->dtype, c->d, c->h_kv, c->page_size, c->n_pages, c->k_stride, rows) &&
+        if (rows >= (tiles ? 8 : 16) &&
+            make_rows_map(&ta.tm_k, c->k, c->dtype, c->d, c->h_kv, c->page_size, c->n_pages, c->k_stride, rows) &&
             make_rows_map(&ta.tm_v, c->v, c->dtype, c->d, c->h_kv, c->page_size, c->n_pages, c->v_stride, rows))
             ta.box_rows = rows;
     }
@@ -460,8 +466,6 @@ sdpa_status_t sdpa_cache_check_status(const sdpa_cache* c, void* stream)
         return fail(SDPA_ERR_BAD_LENGTHS, "a length, count or row index of the cache is out of its range");
     if (host == SDPA_ERR_BOUNDS) return fail(SDPA_ERR_BOUNDS, "a page-table entry is outside [0, n_pages)");
     if (host == SDPA_ERR_TIMEOUT) return fail(SDPA_ERR_TIMEOUT, "a wait of the cache forward ran out on the device");
-    if (host == SDPA_ERR_UNSUPPORTED)
-        return fail(SDPA_ERR_UNSUPPORTED, "the device gave the cache forward shared memory not 1024-byte aligned");
     return fail(SDPA_ERR_CUDA, "unknown cache status %d", host);
 }
 

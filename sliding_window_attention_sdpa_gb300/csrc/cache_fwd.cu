@@ -6,15 +6,18 @@
 // cached ones in reach, then its new ones, in groups of 16 that hold one kind.
 //
 // Few rows (cache_fwd_rows_kernel): the call is bound by reading K and V once,
-// so every row of a kv-head is computed by the warp that reads a key, and keys
-// go from global memory into the registers that the matrix instruction reads,
-// without a stage in shared memory:
+// so every row of a kv-head is computed by the warp that reads a key. A warp
+// fetches 16 keys of 128 features (32 of 64) a step into a ring of its own:
+// one bulk copy per key and tensor, or TMA boxes of 16 keys where a page's size
+// allows them and the rows are short (a copy of 128 bytes costs the engine what
+// one of 256 does: 4.3 TB/s in all, against 7.0). Through registers (LDG) or
+// cp.async the same loads reached 6.0 and 4.3 TB/s at d = 128: 16 instructions
+// a step and warp instead of one. A warp waits for no other.
 //   S^T = K Q^T   m16n8k16, M = 16 keys, N = 8 rows. A dot product does not
 //                 depend on the order of the features, so the instruction's k
 //                 index is mapped to features such that a thread's operand
-//                 registers are the 16-byte pieces that it loads (a quad of
-//                 threads reads 64 consecutive bytes of a key).
-//   O^T += V^T P^T   M = 16 features, N = 8 rows, K = 16 keys. A thread loads 8
+//                 registers are 16-byte pieces of a key.
+//   O^T += V^T P^T   M = 16 features, N = 8 rows, K = 16 keys. A thread reads 8
 //                 consecutive features of the 4 keys of its k indexes and pairs
 //                 two keys' values by byte permutes; P^T comes from the S^T
 //                 registers by an 8 x 8 transpose (movmatrix).
@@ -63,31 +66,67 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 bytes that this kernel reads once.
-__device__ __forceinline__ uint4 ld_stream(const uint16_t* p)
+// 16 bytes to shared memory; zeros (nothing read) if not `have`.
+__device__ __forceinline__ void cp16(uint32_t dst, const uint16_t* src, bool have)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr)
 {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
+}
+
+constexpr int kStages = 3;              // steps of a warp that are on their way or worked on
+
+// A step's K, then its V: rows of the keys, 16 bytes apart more than they are
+// long, or (boxes of 64 features) 128 bytes of them in the 128-byte swizzle.
+template <int HD>
+struct RowsCfg {
+    static constexpr int KG = 128 / HD;                   // 16-key groups of a step
+    static constexpr int GK = 16 * KG;
+    static constexpr uint32_t kPitch = HD * 2 + 16;
+    static constexpr uint32_t kStage = 9216;              // both forms, and boxes begin on 1024 bytes
+    static constexpr uint32_t kRings = 4 * kStages * kStage;
+    static constexpr uint32_t kBytes = kRings + 1024;
+    static_assert(2 * GK * kPitch <= kStage, "");
+};
+
+// A box of 16 keys x 64 features (from c0) of one head of a page.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int head, int row,
+                                        int page)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(head), "r"(row), "r"(page)
+        : "memory");
 }
 
 }  // namespace
 
-// Features per thread and step: see the comment at the top of the file.
-template <int HD, bool BF16, int NT, int OCC>
-__global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __grid_constant__ CacheFwdArgs a)
+template <int HD, bool BF16, int NT>
+__global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __grid_constant__ CacheTileArgs ta)
 {
-    constexpr int KG = 128 / HD;       // 16-key groups per warp and step: 8 KB of K and V in flight either way
-    constexpr int GK = 16 * KG;
+    const CacheFwdArgs& a = ta.f;
+    using C = RowsCfg<HD>;
+    constexpr int KG = C::KG, GK = C::GK;
     constexpr int TK = 4 * GK;
     constexpr int CH = HD / 32;        // 16-byte pieces of a key's K per thread
     constexpr int VJ = HD / 64;        // 16-byte pieces of a key's V per thread
     constexpr int MT = HD / 16;        // feature tiles of O^T
     constexpr int ROWS = 8 * NT;
     constexpr int PAD = HD + 4;
-    __shared__ float sh_o[4][ROWS][PAD];
+    extern __shared__ __align__(1024) uint8_t raw[];
+    // the warps' rings; at a unit's end their O. Boxes begin on 1024 bytes (kBytes has the slack)
+    uint8_t* dyn = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    __shared__ __align__(8) uint64_t sh_bar[4][kStages];
+    float (*sh_o)[ROWS][PAD] = reinterpret_cast<float (*)[ROWS][PAD]>(dyn);
+    static_assert(4 * ROWS * PAD * 4 <= C::kRings, "the warps' O in the rings' place");
+    __shared__ int32_t sh_pos[4][kStages][GK];         // per step of a ring: the keys' positions,
+    __shared__ uint32_t sh_ok[4][kStages];             // and which are there
     __shared__ float sh_m[4][ROWS], sh_l[4][ROWS];
     __shared__ uint64_t sh_mask[64];
     __shared__ int64_t sh_sum[4];
@@ -99,32 +138,44 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
     const int blocks = (R + ROWS - 1) / ROWS;
     const int64_t units = a.c.h_kv * blocks;      // per sequence
 
-    // ---- this CTA's part of the line
-    Part part{1, 0, 0, 0, 0, Line{0}};
-    CacheFwdCut cut{-1, 0, 0, 0};
-    if (a.whole) {
-        // short units: a CTA takes one from end to end, nothing is cut
-        part.bi = blockIdx.x / units;
-        part.end = seq_view(a, part.bi, TK).tiles;
-        part.rem = (blockIdx.x - part.bi * units) * part.end;
-    } else {
-        part = find_part<kThreads>(a.c.b, [&](int64_t i) { return seq_view(a, i, TK).tiles * units; }, sh_sum, sh_at);
-        if (part.end == 0) {
-            if (tid == 0) a.cuts[blockIdx.x] = cut;
-            grid_dep_launch();
-            return;
+    // ---- this CTA's part of the line; where it stands is kept in shared memory,
+    // the registers are for the keys
+    __shared__ Part sh_part;
+    __shared__ int32_t sh_done, sh_count;      // tiles of the part: done, all
+    {
+        Part part{1, 0, 0, 0, 0, Line{0}};
+        if (a.whole) {
+            // short units: a CTA takes one from end to end, nothing is cut
+            part.bi = blockIdx.x / units;
+            part.end = seq_view(a, part.bi, TK).tiles;
+            part.rem = (blockIdx.x - part.bi * units) * part.end;
+        } else {
+            part = find_part<kThreads>(a.c.b, a.min_tiles, [&](int64_t i) { return seq_view(a, i, TK).tiles * units; }, sh_sum,
+                                       sh_at);
+            if (part.end == 0) {
+                if (tid == 0 && !a.cut_by_unit) a.cuts[blockIdx.x].bi = -1;
+                grid_dep_launch();
+                return;
+            }
         }
+        if (tid == 0) {
+            sh_part = part;
+            sh_done = 0;
+            sh_count = static_cast<int32_t>(part.end - part.at);
+        }
+        __syncthreads();
     }
-    const Line& line = part.line;
-    const int64_t parts = part.parts, end = part.end, part0 = part.at;
-    int64_t at = part.at, bi = part.bi, rem = part.rem;
 
-    SeqView sv{};
+    if (tid < 4 * kStages) mbar_init(smem_u32(&sh_bar[0][0]) + tid * 8, 1);
+    fence_mbar_init();
+    __syncthreads();
+    uint32_t sent = 0;        // per stage: the parity of its next step
+    bool good = true;         // no wait has run out
     int64_t cur = -1;
-    while (at < end) {
+    for (;;) {
+        const int64_t bi = sh_part.bi, rem = sh_part.rem;
+        const SeqView sv = seq_view(a, bi, TK);
         if (cur != bi) {
-            sv = seq_view(a, bi, TK);
-            __syncthreads();
             if (tid < 64) {
                 const uint64_t in = sv.nq == 64 ? ~0ull : (1ull << sv.nq) - 1;
                 uint64_t m = 0;
@@ -136,16 +187,10 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
         }
         const int64_t un = rem / sv.tiles;
         const int32_t tile0 = static_cast<int32_t>(rem - un * sv.tiles);
-        const int32_t nt = static_cast<int32_t>(imin64(sv.tiles - tile0, end - at));
+        const int32_t nt = min(sv.tiles - tile0, sh_count - sh_done);
         const int64_t gk = un / blocks;                     // kv-head
         const int r0 = static_cast<int>(un - gk * blocks) * ROWS;
-        // the part that holds the first cut of a unit names the join's work
-        if (at == part0 && tile0 > 0) {
-            const int64_t u0 = at - tile0, p0 = line.part_of(u0, parts);
-            if (p0 + 1 == blockIdx.x)
-                cut = CacheFwdCut{bi, un, static_cast<int32_t>(line.part_of(u0 + sv.tiles - 1, parts)),
-                                  line.start(p0, parts) == u0 ? 0 : 1};
-        }
+        if (tid == 0 && !a.whole) name_cut(a, sh_part, sh_part.at + sh_done, bi, un, units, tile0, nt, sv.tiles);
         const int64_t npos = a.c.next_pos ? a.c.next_pos[bi] : sv.len;
         const int32_t* kpos = a.c.positions ? a.c.positions + (bi * a.c.h_kv + gk) * a.c.cap : nullptr;
 
@@ -181,16 +226,16 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
 
         // ---- the line of keys of this unit: groups of GK per warp
         auto step_x = [&](int32_t s) -> int32_t { return (tile0 + s) * TK + warp * GK; };
-        // Lane l's key of step s: whether it is held, the cached key's page entry
-        // (loaded a step ahead of its use) and position.
+        // Lane l's key (l % GK) of step s, if it is a cached one: its page entry,
+        // loaded a step ahead of its use, and its position.
         struct Key {
             int32_t entry;    // page-table entry
             int32_t pos;      // cached key's position
         };
         auto fetch_key = [&](int32_t s) -> Key {
             Key k{0, 0};
-            const int32_t x = step_x(s) + lane;
-            if (lane < GK && x < sv.new0) {
+            const int32_t x = step_x(s) + lane % GK;
+            if (x < sv.new0) {
                 const int32_t j = sv.lo + x;
                 if (j < sv.len) {
                     if (a.c.page_table)
@@ -202,40 +247,6 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
             }
             return k;
         };
-        // Offsets of lane l's key in K and V, and whether the key is there.
-        auto place = [&](int32_t s, const Key& k, int64_t& ko, int64_t& vo, bool& ok) {
-            const int32_t x = step_x(s) + lane;
-            ok = false;
-            ko = vo = 0;
-            if (lane < GK) {
-                if (x < sv.new0) {
-                    const int32_t j = sv.lo + x;
-                    if (j < sv.len) {
-                        int64_t page = bi;
-                        uint32_t row = j;
-                        ok = true;
-                        if (a.c.page_table) {
-                            page = k.entry;
-                            row = a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)
-                                                      : static_cast<uint32_t>(j) % a.c.page_size;
-                            ok = page >= 0 && page < a.c.n_pages;
-                            if (!ok) set_status(a.c.status, SDPA_ERR_BOUNDS);
-                        }
-                        ko = page * a.c.k_stride[0] + row * a.c.k_stride[1];
-                        vo = page * a.c.v_stride[0] + row * a.c.v_stride[1];
-                    }
-                } else if (x - sv.new0 < sv.nq) {
-                    ok = true;
-                    ko = (x - sv.new0) * a.k_stride[1];
-                    vo = (x - sv.new0) * a.v_stride[1];
-                }
-            }
-        };
-        const uint16_t* kc = a.c.k + gk * a.c.k_stride[2] + t * 8;
-        const uint16_t* vc = a.c.v + gk * a.c.v_stride[2] + g * 8;
-        const uint16_t* kn = a.k + bi * a.k_stride[0] + gk * a.k_stride[2] + t * 8;
-        const uint16_t* vn = a.v + bi * a.v_stride[0] + gk * a.v_stride[2] + g * 8;
-
         float o[NT][MT][4];
         float m[NT][2], l[NT][2];
 #pragma unroll
@@ -248,121 +259,175 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
                 for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
         }
 
-        uint4 kr[KG][2][CH];      // K of keys g, g + 8 of each group
-        uint4 vr[KG][4][VJ];      // V of keys 2t, 2t + 1, 2t + 8, 2t + 9
-        int64_t vo_next = 0;
-        uint32_t ok_next = 0;
-        auto load_k = [&](int32_t s, const Key& k) {
-            int64_t ko;
-            bool ok;
-            place(s, k, ko, vo_next, ok);
-            ok_next = __ballot_sync(0xffffffffu, ok);
-#pragma unroll
-            for (int u = 0; u < KG; ++u)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int x = u * 16 + h * 8 + g;
-                    const int64_t off = __shfl_sync(0xffffffffu, ko, x);
-                    const uint16_t* p = (step_x(s) + u * 16 < sv.new0 ? kc : kn) + off;
-                    const bool have = (ok_next >> x) & 1;
-#pragma unroll
-                    for (int i = 0; i < CH; ++i)
-                        kr[u][h][i] = have ? ld_stream(p + i * 32) : make_uint4(0u, 0u, 0u, 0u);
-                }
+        const uint32_t ring = smem_u32(dyn) + warp * (kStages * C::kStage);
+        const uint32_t bars = smem_u32(&sh_bar[warp][0]);
+        // 16-byte piece c of a key of a step, relative to the step's K or V
+        const bool boxed = ta.box_rows != 0;
+        const uint32_t half = boxed ? 4096 : GK * C::kPitch;           // where V begins
+        const uint32_t pitch = boxed ? 128 : C::kPitch, swz = boxed ? 7 : 0, blk = boxed ? GK * 128 - 128 : 0;
+        auto piece = [&](uint32_t key_row, uint32_t c) -> uint32_t {
+            return key_row * pitch + ((c ^ (key_row & swz)) << 4) + (c >> 3) * blk;
         };
-        auto load_v = [&](int32_t s) {
-#pragma unroll
-            for (int u = 0; u < KG; ++u)
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int x = u * 16 + (h >> 1) * 8 + 2 * t + (h & 1);
-                    const int64_t off = __shfl_sync(0xffffffffu, vo_next, x);
-                    const uint16_t* p = (step_x(s) + u * 16 < sv.new0 ? vc : vn) + off;
-                    const bool have = (ok_next >> x) & 1;
-#pragma unroll
-                    for (int j = 0; j < VJ; ++j)
-                        vr[u][h][j] = have ? ld_stream(p + j * 64) : make_uint4(0u, 0u, 0u, 0u);
+        // Sends step s's copies on their way: lane l looks after key l % GK.
+        auto issue = [&](int32_t s, const Key& k) {
+            const uint32_t st = static_cast<uint32_t>(s) % kStages, at = ring + st * C::kStage, bar = bars + st * 8;
+            const int32_t x = step_x(s) + lane % GK, j = sv.lo + x;
+            const uint32_t key_row = lane % GK;
+            bool ok = x < sv.new0 && j < sv.len;        // a cached key
+            int64_t page = bi;
+            uint32_t row = j;
+            if (ok && a.c.page_table) {
+                page = k.entry;
+                row = a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)
+                                          : static_cast<uint32_t>(j) % a.c.page_size;
+                ok = page >= 0 && page < a.c.n_pages;
+                if (!ok) set_status(a.c.status, SDPA_ERR_BOUNDS);
+            }
+            const uint32_t oks = __ballot_sync(0xffffffffu, ok);
+            if (lane < GK) sh_pos[warp][st][lane] = k.pos;
+            if (boxed) {
+                // a group's boxes (2 KB each: features 0-63, 64-127 of K, of V) begin at its first key; rows of the
+                // page behind the last key come along
+                constexpr int BOXES = 2 * (HD / 64) * KG;
+                const uint32_t groups = __popc(oks & (KG == 2 ? 0x10001u : 1u));
+                if (lane == 0) {
+                    sh_ok[warp][st] = oks;
+                    mbar_arrive_expect_tx(bar, groups * (2 * (HD / 64) * 2048));
                 }
+                __syncwarp();
+                // one lane a box
+                const int u = lane % KG, b = lane / KG, is_v = b / (HD / 64), cb = b % (HD / 64);
+                const int row0 = __shfl_sync(0xffffffffu, static_cast<int>(row), u * 16);
+                const int page0 = __shfl_sync(0xffffffffu, static_cast<int>(page), u * 16);
+                if (lane < BOXES && ((oks >> (u * 16)) & 1))
+                    tma_box(at + (is_v ? half : 0u) + cb * (GK * 128) + u * 2048, is_v ? &ta.tm_v : &ta.tm_k, bar, cb * 64,
+                            static_cast<int>(gk), row0, page0);
+            } else {
+                if (lane == 0) {
+                    sh_ok[warp][st] = oks;
+                    mbar_arrive_expect_tx(bar, __popc(GK == 32 ? oks : oks & 0xffffu) * 2 * HD * 2);
+                }
+                __syncwarp();
+                if (ok) {
+                    const uint16_t* kp = a.c.k + page * a.c.k_stride[0] + row * a.c.k_stride[1] + gk * a.c.k_stride[2];
+                    const uint16_t* vp = a.c.v + page * a.c.v_stride[0] + row * a.c.v_stride[1] + gk * a.c.v_stride[2];
+                    // 32 keys: both by each lane; 16: K by the lower lanes, V by the upper
+                    if (GK == 32 || lane < 16) bulk_load(at + key_row * C::kPitch, kp, HD * 2, bar);
+                    if (GK == 32 || lane >= 16) bulk_load(at + half + key_row * C::kPitch, vp, HD * 2, bar);
+                }
+            }
+            // new tokens: 16 bytes at a time, zeros in the rows of their group that hold none
+#pragma unroll
+            for (int u = 0; u < KG; ++u) {
+                const int32_t w0 = step_x(s) + u * 16 - sv.new0;      // the group's first new token
+                if (w0 < 0 || w0 >= sv.nq) continue;
+                for (int i = lane; i < 16 * (HD / 8); i += 32) {
+                    const int r = i / (HD / 8), c = i % (HD / 8);
+                    const bool have = w0 + r < sv.nq;
+                    const int64_t tok = have ? w0 + r : 0;
+                    cp16(at + piece(u * 16 + r, c), a.k + bi * a.k_stride[0] + tok * a.k_stride[1] + gk * a.k_stride[2] + c * 8,
+                         have);
+                    cp16(at + half + piece(u * 16 + r, c),
+                         a.v + bi * a.v_stride[0] + tok * a.v_stride[1] + gk * a.v_stride[2] + c * 8, have);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
 
-        Key key = fetch_key(0), key1 = fetch_key(1);
-        load_k(0, key);
-        load_v(0);
+        // (rings hold the last unit's O: its reads are done, and known to the copy engine)
+        fence_proxy_async_smem();
+        __syncwarp();
+        Key key = fetch_key(0);
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) {
+            const Key next = fetch_key(s + 1);
+            if (s < nt) issue(s, key);
+            key = next;
+        }
 #pragma unroll 1
         for (int32_t s = 0; s < nt; ++s) {
-            const uint32_t ok = ok_next;
+            {
+                const Key next = fetch_key(s + kStages);
+                if (s + kStages - 1 < nt) issue(s + kStages - 1, key);
+                key = next;
+            }
+            const uint32_t st = static_cast<uint32_t>(s) % kStages, at = ring + st * C::kStage;
+            if (good && !mbar_wait(bars + st * 8, (sent >> st) & 1, a.timeout_ns)) {
+                good = false;
+                set_status(a.c.status, SDPA_ERR_TIMEOUT);
+            }
+            good = __all_sync(0xffffffffu, good);
+            sent ^= 1u << st;
             const int32_t x0 = step_x(s);
-            const int32_t my_pos = key.pos;
+            const bool some_new = x0 + GK > sv.new0;
+            if (some_new) asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            if (!good) continue;
+            // keys that are there: cached ones, new tokens
+            uint32_t ok = sh_ok[warp][st];
+            if (some_new)
+#pragma unroll
+                for (int u = 0; u < KG; ++u) {
+                    const int32_t w0 = x0 + u * 16 - sv.new0;
+                    if (w0 >= 0) ok |= (w0 < sv.nq ? (sv.nq - w0 >= 16 ? 0xffffu : (1u << (sv.nq - w0)) - 1) : 0u) << (16 * u);
+                }
+            const bool full = GK == 32 ? ok == 0xffffffffu : (ok & 0xffffu) == 0xffffu;
             // S^T
             float sc[NT][KG][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int u = 0; u < KG; ++u) {
 #pragma unroll
-                for (int u = 0; u < KG; ++u) {
-                    sc[n][u][0] = sc[n][u][1] = sc[n][u][2] = sc[n][u][3] = 0.f;
+                for (int n = 0; n < NT; ++n) sc[n][u][0] = sc[n][u][1] = sc[n][u][2] = sc[n][u][3] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < CH; ++i) {
-                        mma_16816<BF16>(sc[n][u], kr[u][0][i].x, kr[u][1][i].x, kr[u][0][i].y, kr[u][1][i].y, q[n][i].x,
-                                        q[n][i].y);
-                        mma_16816<BF16>(sc[n][u], kr[u][0][i].z, kr[u][1][i].z, kr[u][0][i].w, kr[u][1][i].w, q[n][i].z,
-                                        q[n][i].w);
+                for (int i = 0; i < CH; ++i) {
+                    const uint4 k0 = lds16(at + piece(u * 16 + g, t + 4 * i)), k1 = lds16(at + piece(u * 16 + 8 + g, t + 4 * i));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_16816<BF16>(sc[n][u], k0.x, k1.x, k0.y, k1.y, q[n][i].x, q[n][i].y);
+                        mma_16816<BF16>(sc[n][u], k0.z, k1.z, k0.w, k1.w, q[n][i].z, q[n][i].w);
                     }
                 }
-            // the next step's keys start their way
-            key = key1;
-            if (s + 1 < nt) {
-                load_k(s + 1, key);
-                key1 = fetch_key(s + 2);
             }
-            // masks, the row's reference, P
+            // masks (a step whose keys are all there and in every row's window needs none; rows that admit nothing
+            // are left out at the end), the row's reference, P
             uint32_t hi[NT][KG][2], lo[NT][KG][2];
             float mx[NT][2];
             bool up = false;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mx[n][0] = mx[n][1] = -INFINITY;
+            const bool windowed = a.window_left >= 0 && x0 < sv.new0 && (kpos != nullptr || sv.lo + x0 < low_max);
+            if (!full || some_new || windowed) {
 #pragma unroll
                 for (int u = 0; u < KG; ++u) {
                     const bool fresh = x0 + u * 16 >= sv.new0;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int x = u * 16 + (e >> 1) * 8 + g;
-                        bool in = (ok >> x) & 1;
-                        if (fresh) {
-                            const int w = x0 + x - sv.new0;      // the new token
-                            const uint64_t rm = row_tok[n][e & 1] < 0 ? 0 : sh_mask[row_tok[n][e & 1]];
-                            in = in && ((rm >> (w & 63)) & 1) &&
-                                 (a.window_left < 0 || __popcll(rm) - __popcll(sh_mask[w & 63]) <= a.window_left);
-                        } else {
-                            in = in && row_tok[n][e & 1] >= 0;
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int x = u * 16 + (e >> 1) * 8 + g;
+                            bool in = (ok >> x) & 1;
+                            if (fresh) {
+                                const int w = (x0 + x - sv.new0) & 63;      // the new token
+                                const uint64_t rm = row_tok[n][e & 1] < 0 ? 0 : sh_mask[row_tok[n][e & 1]];
+                                in = in && ((rm >> w) & 1) &&
+                                     (a.window_left < 0 || __popcll(rm) - __popcll(sh_mask[w]) <= a.window_left);
+                            } else if (windowed) {
+                                in = in && sh_pos[warp][st][x] >= row_low[n][e & 1];
+                            }
+                            if (!in) sc[n][u][e] = -INFINITY;
                         }
-                        const float v = in ? sc[n][u][e] * a.scale_log2 : -INFINITY;
-                        sc[n][u][e] = v;
-                    }
-                }
-            }
-            // the window over cached keys, where any of the step's keys is below the highest row's
-            if (a.window_left >= 0 && x0 < sv.new0 && (kpos != nullptr || sv.lo + x0 < low_max)) {
-#pragma unroll
-                for (int u = 0; u < KG; ++u) {
-                    const int32_t p0 = __shfl_sync(0xffffffffu, my_pos, u * 16 + g);
-                    const int32_t p1 = __shfl_sync(0xffffffffu, my_pos, u * 16 + 8 + g);
-                    if (x0 + u * 16 < sv.new0) {
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if ((e < 2 ? p0 : p1) < row_low[n][e & 1]) sc[n][u][e] = -INFINITY;
-                    }
                 }
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+                mx[n][0] = mx[n][1] = -INFINITY;
 #pragma unroll
                 for (int u = 0; u < KG; ++u)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) mx[n][e & 1] = fmaxf(mx[n][e & 1], sc[n][u][e]);
-                up = up || mx[n][0] > m[n][0] + 8.f || mx[n][1] > m[n][1] + 8.f;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[n][e] *= a.scale_log2;
+                    up = up || mx[n][e] > m[n][e] + 8.f;
+                }
             }
             if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
@@ -391,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
                     float p[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        p[e] = sc[n][u][e] == -INFINITY ? 0.f : ex2_approx(sc[n][u][e] - m[n][e & 1]);
+                        // a masked score is -inf, its P is 0 (a row's reference is finite here, or 0)
+                        p[e] = ex2_approx(fmaf(sc[n][u][e], a.scale_log2, m[n][e & 1] == -INFINITY ? 0.f : -m[n][e & 1]));
                         l[n][e & 1] += p[e];
                     }
 #pragma unroll
@@ -406,12 +472,19 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
 #pragma unroll
             for (int u = 0; u < KG; ++u)
 #pragma unroll
-                for (int j = 0; j < VJ; ++j)
+                for (int j = 0; j < VJ; ++j) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const int x = u * 16 + (h >> 1) * 8 + 2 * t + (h & 1);
+                        v[h] = lds16(at + half + piece(x, g + 8 * j));
+                        // what stands in the place of a key that is not there meets a P of 0: it has to be finite
+                        if (!full && !((ok >> x) & 1)) v[h] = make_uint4(0u, 0u, 0u, 0u);
+                    }
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         auto reg = [&](int h) -> uint32_t {
-                            const uint4& v = vr[u][h][j];
-                            return p == 0 ? v.x : p == 1 ? v.y : p == 2 ? v.z : v.w;
+                            return p == 0 ? v[h].x : p == 1 ? v[h].y : p == 2 ? v[h].z : v[h].w;
                         };
                         const uint32_t a0 = __byte_perm(reg(0), reg(1), 0x5410), a1 = __byte_perm(reg(0), reg(1), 0x7632);
                         const uint32_t a2 = __byte_perm(reg(2), reg(3), 0x5410), a3 = __byte_perm(reg(2), reg(3), 0x7632);
@@ -421,10 +494,11 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
                             mma_16816<BF16>(o[n][j * 4 + p], a0, a1, a2, a3, lo[n][u][0], lo[n][u][1]);
                         }
                     }
-            if (s + 1 < nt) load_v(s + 1);
+                }
         }
 
         // ---- the CTA's warps join their rows
+        __syncthreads();
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -433,23 +507,24 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
                 const int r = n * 8 + 2 * t + e;
+                const bool live = row_tok[n][e] >= 0;
                 if (g == 0) {
-                    sh_m[warp][r] = m[n][e];
-                    sh_l[warp][r] = x;
+                    sh_m[warp][r] = live ? m[n][e] : -INFINITY;
+                    sh_l[warp][r] = live ? x : 0.f;
                 }
 #pragma unroll
                 for (int j = 0; j < VJ; ++j) {
                     float* dst = &sh_o[warp][r][(g + 8 * j) * 8];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        dst[2 * p] = o[n][j * 4 + p][e];
-                        dst[2 * p + 1] = o[n][j * 4 + p][2 + e];
+                        dst[2 * p] = live ? o[n][j * 4 + p][e] : 0.f;
+                        dst[2 * p + 1] = live ? o[n][j * 4 + p][2 + e] : 0.f;
                     }
                 }
             }
         __syncthreads();
         const bool whole = nt == sv.tiles;
-        const int64_t slot = blockIdx.x * 2 + (at == part0 ? 0 : 1);
+        const int64_t slot = blockIdx.x * 2 + (sh_done == 0 ? 0 : 1);
         for (int u = tid; u < ROWS * (HD / 8); u += kThreads) {
             const int r = u / (HD / 8), c = (u % (HD / 8)) * 8;
             float top = fmaxf(fmaxf(sh_m[0][r], sh_m[1][r]), fmaxf(sh_m[2][r], sh_m[3][r]));
@@ -478,21 +553,22 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_fwd_rows_kernel(const __g
             store_row<BF16, 8>(a, bi, tok, h, c, tok < sv.nq, top, sum, x);
         }
         __syncthreads();
-
-        at += nt;
-        rem += nt;
-        if (rem == sv.tiles * units) {
-            ++bi;
-            rem = 0;
+        if (tid == 0) {
+            sh_done += nt;
+            sh_part.rem = rem + nt;
+            if (rem + nt == sv.tiles * units) {
+                ++sh_part.bi;
+                sh_part.rem = 0;
+            }
         }
+        __syncthreads();
+        if (sh_done == sh_count) break;
     }
-    if (a.whole) return;
-    if (tid == 0) a.cuts[blockIdx.x] = cut;
-    grid_dep_launch();
+    if (!a.whole) grid_dep_launch();
 }
 
 // Adds the partials of a unit that was cut between parts, in the order of the
-// parts. CTA x looks after the unit whose first cut is at part x's start.
+// parts. CTA x looks after cuts[x].
 // SPREAD: CTA y takes row y, its warps every eighth part (few units, many
 // parts each); else CTA y takes 8 rows, a warp each with all its parts.
 template <int HD, bool BF16, int ROWS, bool SPREAD>
@@ -507,7 +583,7 @@ __global__ void __launch_bounds__(256) cache_fwd_join_kernel(const __grid_consta
     const int R = a.s_q * a.group, blocks = (R + ROWS - 1) / ROWS;
     const int64_t gk = cut.un / blocks;
     const int r0 = static_cast<int>(cut.un - gk * blocks) * ROWS;
-    const int c0 = static_cast<int>(blockIdx.x) - 1, n = cut.last - c0 + 1;
+    const int c0 = cut.first, n = cut.last - c0 + 1;
     // parts behind the first begin with this unit
     auto slot = [&](int i) -> int64_t { return i == 0 ? c0 * int64_t(2) + cut.slot0 : (c0 + i) * int64_t(2); };
     int nq = a.s_q;
@@ -564,11 +640,12 @@ template <int HD, bool BF16, int ROWS>
 cudaError_t launch_join(const CacheFwdArgs& a, cudaStream_t s)
 {
     if (a.whole || a.parts == 1) return cudaSuccess;
-    const int blocks = (a.s_q * a.group + ROWS - 1) / ROWS;
-    // with an eighth as many units as parts a unit has few cuts
-    const bool spread = a.c.b * a.c.h_kv * blocks * 8 < a.parts;
+    const int rows = a.s_q * a.group, blocks = (rows + ROWS - 1) / ROWS, most = rows < ROWS ? rows : ROWS;
+    const int64_t units = a.c.b * a.c.h_kv * blocks;
+    // with fewer units than an eighth of the parts a unit has many parts
+    const bool spread = units * 8 < a.parts;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.parts), spread ? ROWS : ROWS / 8);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.cut_by_unit ? units : a.parts), spread ? most : (most + 7) / 8);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -580,12 +657,16 @@ cudaError_t launch_join(const CacheFwdArgs& a, cudaStream_t s)
                   : cudaLaunchKernelEx(&cfg, cache_fwd_join_kernel<HD, BF16, ROWS, false>, a);
 }
 
-template <int HD, bool BF16, int NT, int OCC>
-cudaError_t launch_rows(const CacheFwdArgs& a, cudaStream_t s)
+template <int HD, bool BF16, int NT>
+cudaError_t launch_rows(const CacheTileArgs& ta, cudaStream_t s)
 {
-    cache_fwd_rows_kernel<HD, BF16, NT, OCC><<<a.parts, kThreads, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_join<HD, BF16, 8 * NT>(a, s);
+    auto kern = cache_fwd_rows_kernel<HD, BF16, NT>;
+    const uint32_t bytes = RowsCfg<HD>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kern<<<ta.f.parts, kThreads, bytes, s>>>(ta);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join<HD, BF16, 8 * NT>(ta.f, s);
 }
 
 template <int HD, bool BF16>
@@ -598,13 +679,10 @@ cudaError_t launch_tiles(const CacheTileArgs& ta, cudaStream_t s)
 template <bool BF16>
 cudaError_t launch_fwd_typed(const CacheTileArgs& ta, cudaStream_t s)
 {
-    const CacheFwdArgs& a = ta.f;
-    switch (cache_fwd_plan(a.c.d, a.s_q * a.group).variant) {
-        case kRows128x8: return launch_rows<128, BF16, 1, 3>(a, s);
-        case kRows128x16: return launch_rows<128, BF16, 2, 2>(a, s);
-        case kRows64x8: return launch_rows<64, BF16, 1, 4>(a, s);
-        case kRows64x16: return launch_rows<64, BF16, 2, 3>(a, s);
-        case kRows64x32: return launch_rows<64, BF16, 4, 2>(a, s);
+    switch (cache_fwd_plan(ta.f.c.d, ta.f.s_q * ta.f.group).variant) {
+        case kRows128x8: return launch_rows<128, BF16, 1>(ta, s);
+        case kRows64x8: return launch_rows<64, BF16, 1>(ta, s);
+        case kRows64x16: return launch_rows<64, BF16, 2>(ta, s);
         case kTiles128: return launch_tiles<128, BF16>(ta, s);
         default: return launch_tiles<64, BF16>(ta, s);
     }
@@ -614,14 +692,9 @@ cudaError_t launch_fwd_typed(const CacheTileArgs& ta, cudaStream_t s)
 
 CacheFwdPlan cache_fwd_plan(int64_t d, int64_t rows)
 {
-    if (d == 128) {
-        if (rows <= 8) return CacheFwdPlan{kRows128x8, 8, 64, 3};
-        if (rows <= 16) return CacheFwdPlan{kRows128x16, 16, 64, 2};
-        return CacheFwdPlan{kTiles128, 256, 64, 1};
-    }
-    if (rows <= 8) return CacheFwdPlan{kRows64x8, 8, 128, 4};
-    if (rows <= 16) return CacheFwdPlan{kRows64x16, 16, 128, 3};
-    if (rows <= 32) return CacheFwdPlan{kRows64x32, 32, 128, 2};
+    if (d == 128) return rows <= 8 ? CacheFwdPlan{kRows128x8, 8, 64, 2} : CacheFwdPlan{kTiles128, 256, 64, 1};
+    if (rows <= 8) return CacheFwdPlan{kRows64x8, 8, 128, 2};
+    if (rows <= 16) return CacheFwdPlan{kRows64x16, 16, 128, 2};
     return CacheFwdPlan{kTiles64, 256, 64, 1};
 }
 

@@ -25,16 +25,18 @@ struct CacheView {
 };
 
 // A unit of the forward's work that is cut between parts: its sequence (-1:
-// none), its number in the sequence, the last part that has some of it, and
-// which of the first part's two partials is the unit's.
+// none), its number in the sequence, the parts that have some of it, and which
+// of the first part's two partials is the unit's. Kept by unit where there are
+// no more units than parts (so that the join has a CTA per unit), else by the
+// part at whose start the unit's first cut is.
 struct CacheFwdCut {
     int64_t bi, un;
-    int32_t last, slot0;
+    int32_t first, last, slot0;
 };
 
 // Kernel for a head dimension and a kv-head's number of rows: rows of a unit,
 // keys of a tile, CTAs per SM.
-enum CacheFwdVariant { kRows128x8, kRows128x16, kRows64x8, kRows64x16, kRows64x32, kTiles128, kTiles64 };
+enum CacheFwdVariant { kRows128x8, kRows64x8, kRows64x16, kTiles128, kTiles64 };
 struct CacheFwdPlan {
     int variant, rows, tile, occ;
 };
@@ -54,13 +56,15 @@ struct CacheFwdArgs {
     float* lse;
     // workspace: per part two partials [rows][d] with their (reference, sum),
     // and the cut that the part names
+    int32_t min_tiles;      // least tiles of a part
     int32_t parts, whole;   // whole: one unit per CTA, no workspace
+    int32_t cut_by_unit;
     int64_t timeout_ns;     // limit of a wait inside the tile kernel
     float *part_o, *part_ml;
     CacheFwdCut* cuts;
 };
 
-// The tile kernel's: TMA descriptors of the pools' pages (4-D: d, head, row,
+// The tile kernel's, and the rows kernel's at d = 64: TMA descriptors of the pools' pages (4-D: d, head, row,
 // page) in boxes of 64 features x box_rows rows with the 128-byte swizzle;
 // box_rows 0: none, every row is gathered.
 struct CacheTileArgs {

@@ -51,7 +51,7 @@ struct TileCfg {
     static constexpr uint32_t kMl = kMask + 512;                // float2 [2][128]
     static constexpr uint32_t kBars = kMl + 2048;
     static constexpr uint32_t kMisc = kBars + 448;
-    static constexpr uint32_t kBytes = kMisc + 256;
+    static constexpr uint32_t kBytes = kMisc + 256 + 1024;
     static_assert(kBytes <= 232448, "shared memory above the 227 KB a CTA may opt into");
 };
 
@@ -211,12 +211,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
     constexpr int NS = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ int64_t sh_sum[kTileThreads / 32], sh_at[2];
-    if (smem_u32(smem_raw) & 1023u) {
-        if (threadIdx.x == 0) set_status(a.c.status, SDPA_ERR_UNSUPPORTED);
-        if (threadIdx.x == 0 && !a.whole) a.cuts[blockIdx.x] = CacheFwdCut{-1, 0, 0, 0};
-        return;
-    }
-    uint8_t* sm = smem_raw;
+    // the swizzle needs 1024-byte boundaries (kBytes has the slack)
+    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(sm);
     auto bar = [&](int i) -> uint32_t { return sbase + C::kBars + 8u * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(sm + C::kMisc);   // [0] tmem base, [1] abort flag
@@ -231,7 +227,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
     walk.na = na;
     walk.nb = nb;
     Part part{1, 0, 0, 0, 0, Line{0}};
-    CacheFwdCut cut{-1, 0, 0, 0};
     if (a.whole) {
         const int64_t units = a.c.h_kv * blocks;
         part.bi = blockIdx.x / units;
@@ -241,9 +236,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         part.end = blk < na ? s.ta : s.tb;
     } else {
         part = find_part<kTileThreads>(
-            a.c.b, [&](int64_t i) { return a.c.h_kv * shape_of(seq_view(a, i, kKeys, kKeys), na, nb).per_head; }, sh_sum, sh_at);
+            a.c.b, a.min_tiles, [&](int64_t i) { return a.c.h_kv * shape_of(seq_view(a, i, kKeys, kKeys), na, nb).per_head; }, sh_sum, sh_at);
         if (part.end == 0) {
-            if (tid == 0) a.cuts[blockIdx.x] = cut;
+            if (tid == 0 && !a.cut_by_unit) a.cuts[blockIdx.x].bi = -1;
             grid_dep_launch();
             return;
         }
@@ -533,13 +528,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 if (r < sv.nq) m = in & (a.tree ? static_cast<uint64_t>(a.tree[g.bi * a.s_q + r]) : (2ull << r) - 1);
                 masks[r] = (m >> r) & 1 ? m : 0;
             }
-            if (sl == 0 && r == 0 && walk.at == part0 && g.step0 > 0) {
-                const int64_t u0 = walk.at - g.step0, p0 = part.line.part_of(u0, part.parts);
-                if (p0 + 1 == blockIdx.x)
-                    cut = CacheFwdCut{g.bi, g.gk * blocks + g.blk,
-                                      static_cast<int32_t>(part.line.part_of(u0 + g.of - 1, part.parts)),
-                                      part.line.start(p0, part.parts) == u0 ? 0 : 1};
-            }
+            if (sl == 0 && r == 0 && !a.whole)
+                name_cut(a, part, walk.at, g.bi, g.gk * blocks + g.blk, a.c.h_kv * blocks, g.step0, g.steps, g.of);
             // this thread's row
             const int rr = g.blk * 256 + (g.two ? sl * 128 : 0) + row;
             const int tok = rr < R ? rr / a.group : 0;
@@ -712,13 +702,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                         for (int e = 0; e < 32; ++e)
                             if (!dead && f1 != 0.f) x[e] += f1 * __uint_as_float(v[e]);
                     }
+                    if (rr >= R) continue;
                     if (!whole) {
                         float* po = a.part_o + (slot * 256 + urow) * HD + cb * 32;
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             *reinterpret_cast<float4*>(po + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
                         if (cb == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * 256 + urow) * 2) = make_float2(top, sum);
-                    } else if (rr < R) {
+                    } else {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
                             float y[8];
@@ -734,7 +725,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             it0 += tiles;
             walk.advance(a, g);
         }
-        if (sl == 0 && r == 0 && !a.whole) a.cuts[blockIdx.x] = cut;
     }
     tc_fence_before();
     __syncthreads();
