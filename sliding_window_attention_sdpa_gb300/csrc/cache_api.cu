@@ -342,7 +342,7 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.parts = l.parts;
     a.whole = l.whole;
     a.cut_by_unit = fwd_size(c, p, plan).units <= l.parts;
-    a.min_tiles = getenv("MT") ? atoi(getenv("MT")) : 1;
+    a.unit_cost = getenv("MT") ? atoi(getenv("MT")) : 1;
     a.timeout_ns = kWaitLimitNs;
     a.part_o = at<float>(ws, l.part_o);
     a.part_ml = at<float>(ws, l.part_ml);

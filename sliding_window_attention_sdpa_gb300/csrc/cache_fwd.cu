@@ -141,19 +141,19 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
     // ---- this CTA's part of the line; where it stands is kept in shared memory,
     // the registers are for the keys
     __shared__ Part sh_part;
-    __shared__ int32_t sh_done, sh_count;      // tiles of the part: done, all
+    __shared__ int32_t sh_done, sh_count;      // places of the part in the line: done, all
     {
         Part part{1, 0, 0, 0, 0, Line{0}};
         if (a.whole) {
             // short units: a CTA takes one from end to end, nothing is cut
             part.bi = blockIdx.x / units;
             part.end = seq_view(a, part.bi, TK).tiles;
-            part.rem = (blockIdx.x - part.bi * units) * part.end;
+            part.rem = (blockIdx.x - part.bi * units) * (part.end + a.unit_cost) + a.unit_cost;
         } else {
-            part = find_part<kThreads>(a.c.b, a.min_tiles, [&](int64_t i) { return seq_view(a, i, TK).tiles * units; }, sh_sum,
-                                       sh_at);
+            part = find_part<kThreads>(
+                a.c.b, [&](int64_t i) { return (seq_view(a, i, TK).tiles + a.unit_cost) * units; }, sh_sum, sh_at);
+            if (tid == 0 && !a.cut_by_unit) a.cuts[blockIdx.x].bi = -1;
             if (part.end == 0) {
-                if (tid == 0 && !a.cut_by_unit) a.cuts[blockIdx.x].bi = -1;
                 grid_dep_launch();
                 return;
             }
@@ -185,12 +185,15 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
             __syncthreads();
             cur = bi;
         }
-        const int64_t un = rem / sv.tiles;
-        const int32_t tile0 = static_cast<int32_t>(rem - un * sv.tiles);
-        const int32_t nt = min(sv.tiles - tile0, sh_count - sh_done);
+        const Segment seg = segment_at(rem, sv.tiles, a.unit_cost, sh_count - sh_done);
+        const int64_t un = seg.un;
+        const int32_t tile0 = seg.tile0, nt = seg.n;
+        if (nt == 0) break;                                 // the part ends before the unit's first tile
         const int64_t gk = un / blocks;                     // kv-head
         const int r0 = static_cast<int>(un - gk * blocks) * ROWS;
-        if (tid == 0 && !a.whole) name_cut(a, sh_part, sh_part.at + sh_done, bi, un, units, tile0, nt, sv.tiles);
+        if (tid == 0 && !a.whole)
+            name_cut(a, sh_part, sh_done == 0, sh_part.at + sh_done + seg.line_n - tile0 - nt, a.unit_cost, bi, un, units, tile0,
+                     nt, sv.tiles);
         const int64_t npos = a.c.next_pos ? a.c.next_pos[bi] : sv.len;
         const int32_t* kpos = a.c.positions ? a.c.positions + (bi * a.c.h_kv + gk) * a.c.cap : nullptr;
 
@@ -341,22 +344,28 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
 #pragma unroll
         for (int s = 0; s < kStages - 1; ++s) {
             const Key next = fetch_key(s + 1);
-            if (s < nt) issue(s, key);
+            if (good && s < nt) issue(s, key);
             key = next;
         }
 #pragma unroll 1
         for (int32_t s = 0; s < nt; ++s) {
             {
                 const Key next = fetch_key(s + kStages);
-                if (s + kStages - 1 < nt) issue(s + kStages - 1, key);
+                if (good && s + kStages - 1 < nt) issue(s + kStages - 1, key);
                 key = next;
             }
             const uint32_t st = static_cast<uint32_t>(s) % kStages, at = ring + st * C::kStage;
-            if (good && !mbar_wait(bars + st * 8, (sent >> st) & 1, a.timeout_ns)) {
-                good = false;
-                set_status(a.c.status, SDPA_ERR_TIMEOUT);
+            if (good) {
+                good = __all_sync(0xffffffffu, mbar_wait(bars + st * 8, (sent >> st) & 1, a.timeout_ns));
+                if (!good) {
+                    // nothing more is sent; what is on its way ends before the CTA does
+                    set_status(a.c.status, SDPA_ERR_TIMEOUT);
+                    for (int32_t q = s; q < nt && q < s + kStages; ++q)
+                        mbar_wait(bars + (q % kStages) * 8, (sent >> (q % kStages)) & 1, a.timeout_ns);
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    __syncwarp();
+                }
             }
-            good = __all_sync(0xffffffffu, good);
             sent ^= 1u << st;
             const int32_t x0 = step_x(s);
             const bool some_new = x0 + GK > sv.new0;
@@ -554,9 +563,9 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
         }
         __syncthreads();
         if (tid == 0) {
-            sh_done += nt;
-            sh_part.rem = rem + nt;
-            if (rem + nt == sv.tiles * units) {
+            sh_done += seg.line_n;
+            sh_part.rem = rem + seg.line_n;
+            if (rem + seg.line_n == (sv.tiles + a.unit_cost) * units) {
                 ++sh_part.bi;
                 sh_part.rem = 0;
             }

@@ -99,10 +99,10 @@ struct Part {
 };
 
 // Cuts the line of all sequences' tiles (tiles_of(i), each more than 0) into
-// one part per CTA, fewer if a part would have fewer than min_tiles tiles. Every thread calls it; sh
+// one part per CTA, fewer if there are fewer tiles. Every thread calls it; sh
 // has a place per warp, sh_at two.
 template <int THREADS, class F>
-__device__ __forceinline__ Part find_part(int64_t b, int64_t min_tiles, F tiles_of, int64_t* sh, int64_t* sh_at)
+__device__ __forceinline__ Part find_part(int64_t b, F tiles_of, int64_t* sh, int64_t* sh_at)
 {
     constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -110,7 +110,7 @@ __device__ __forceinline__ Part find_part(int64_t b, int64_t min_tiles, F tiles_
     int64_t s = 0;
     for (int64_t i = tid; i < b; i += THREADS) s += tiles_of(i);
     p.line.total = block_sum64<THREADS>(s, sh);
-    p.parts = imin64(gridDim.x, imax64(1, p.line.total / min_tiles));
+    p.parts = imin64(gridDim.x, p.line.total);
     if (blockIdx.x >= p.parts) return p;
     p.at = p.line.start(blockIdx.x, p.parts);
     p.end = p.line.start(blockIdx.x + 1, p.parts);
@@ -143,23 +143,40 @@ __device__ __forceinline__ Part find_part(int64_t b, int64_t min_tiles, F tiles_
     return p;
 }
 
-// Names the join's work for a segment of `n` tiles from tile0 (of `tiles`) of
-// unit `un` of sequence bi, which begins at tile `at` of the line (one thread
-// calls it, for each segment of a part). `units`: per sequence.
-__device__ __forceinline__ void name_cut(const CacheFwdArgs& a, const Part& p, int64_t at, int64_t bi, int64_t un,
-                                         int64_t units, int32_t tile0, int32_t n, int32_t tiles)
+// A unit's place in the line: kUnitCost tiles' worth of its fixed cost (rows in,
+// pipeline filled and drained, O out), then its tiles. A part that ends within
+// the first has none of the unit's tiles. A segment: what a part has of a unit.
+struct Segment {
+    int64_t un;                 // the unit's number in its sequence
+    int32_t tile0, n, line_n;   // first tile, tiles (0: none), places in the line
+};
+
+__device__ __forceinline__ Segment segment_at(int64_t rem, int32_t tiles, int32_t cost, int64_t left)
 {
-    if (a.cut_by_unit ? tile0 != 0 : at != p.at) return;
+    Segment g;
+    g.un = rem / (tiles + cost);
+    const int32_t y = static_cast<int32_t>(rem - g.un * (tiles + cost));
+    g.tile0 = max(0, y - cost);
+    g.line_n = static_cast<int32_t>(imin64(tiles + cost - y, left));
+    g.n = max(0, y + g.line_n - cost) - g.tile0;
+    return g;
+}
+
+// Names the join's work for a segment of g.n > 0 tiles of unit `un` (of
+// `tiles`) of sequence bi; `pos0` is the place of the unit's tile 0 in the line
+// (one thread calls it, for each segment of a part). `units`: per sequence.
+__device__ __forceinline__ void name_cut(const CacheFwdArgs& a, const Part& p, bool first_of_part, int64_t pos0, int32_t cost,
+                                         int64_t bi, int64_t un, int64_t units, int32_t tile0, int32_t n, int32_t tiles)
+{
+    if (a.cut_by_unit ? tile0 != 0 : !first_of_part || tile0 == 0) return;
     CacheFwdCut cut{-1, 0, 0, 0, 0};
-    const int64_t u0 = at - tile0;
-    if (n != tiles) {
-        const int64_t first = p.line.part_of(u0, p.parts);
-        // by part: only the one right behind the unit's first names it
-        if (a.cut_by_unit || (tile0 > 0 && first + 1 == blockIdx.x))
-            cut = CacheFwdCut{bi, un, static_cast<int32_t>(first), static_cast<int32_t>(p.line.part_of(u0 + tiles - 1, p.parts)),
-                              p.line.start(first, p.parts) == u0 ? 0 : 1};
-    }
-    a.cuts[a.cut_by_unit ? bi * units + un : blockIdx.x] = cut;
+    const int64_t first = p.line.part_of(pos0, p.parts);
+    if (n != tiles)
+        cut = CacheFwdCut{bi, un, static_cast<int32_t>(first), static_cast<int32_t>(p.line.part_of(pos0 + tiles - 1, p.parts)),
+                          p.line.start(first, p.parts) >= pos0 - cost ? 0 : 1};
+    if (a.cut_by_unit) a.cuts[bi * units + un] = cut;
+    // by part (a part's entry holds no cut at first): the one right behind the unit's first part names it
+    else if (first + 1 == blockIdx.x) a.cuts[blockIdx.x] = cut;
 }
 
 // Finishes E features (from c) of a row: O and, with its first feature, LSE.

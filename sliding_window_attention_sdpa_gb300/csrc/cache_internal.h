@@ -56,7 +56,7 @@ struct CacheFwdArgs {
     float* lse;
     // workspace: per part two partials [rows][d] with their (reference, sum),
     // and the cut that the part names
-    int32_t min_tiles;      // least tiles of a part
+    int32_t unit_cost;      // a unit's fixed cost in tiles
     int32_t parts, whole;   // whole: one unit per CTA, no workspace
     int32_t cut_by_unit;
     int64_t timeout_ns;     // limit of a wait inside the tile kernel

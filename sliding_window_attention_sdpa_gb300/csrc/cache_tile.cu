@@ -57,8 +57,8 @@ struct TileCfg {
 
 // mbarriers; per-stage and per-slot ones at index + stage or slot (S, P and
 // P V: slot * 2 + buffer)
-enum TBar : int { tKFull = 0, tKEmpty = 8, tVFull = 16, tVEmpty = 24, tSFull = 32, tPFull = 36, tPvDone = 40, tQFull = 44,
-                  tSegDone = 46, tDrain = 47, tNumBars = 49 };
+enum TBar : int { tKFull = 0, tKEmpty = 8, tVFull = 16, tVEmpty = 24, tSFull = 32, tPFull = 36, tPvDone = 40, tDrain = 44,
+                  tNumBars = 46 };
 static_assert(tNumBars * 8 <= 448, "mbarrier area");
 
 // 16-byte chunk of a row of a swizzled tile whose 64-column blocks are BLK bytes.
@@ -133,18 +133,18 @@ __device__ __forceinline__ void named_sync(int id, int threads)
 
 // How a sequence's steps are laid out: per kv-head `na` blocks of 256 rows
 // with two row tiles (a step is one key tile), then perhaps one block with one
-// row tile (a step is two key tiles).
+// row tile (a step is two key tiles), each with its fixed cost before it.
 struct Shape {
     int32_t ta, tb;       // steps of a two-tile block, of a one-tile block
     int64_t per_head;
 };
 
-__device__ __forceinline__ Shape shape_of(const SeqView& v, int na, int nb)
+__device__ __forceinline__ Shape shape_of(const SeqView& v, int na, int nb, int32_t cost)
 {
     Shape s;
     s.ta = v.tiles;
     s.tb = (v.tiles + 1) >> 1;
-    s.per_head = static_cast<int64_t>(na) * s.ta + static_cast<int64_t>(nb) * s.tb;
+    s.per_head = static_cast<int64_t>(na) * (s.ta + cost) + static_cast<int64_t>(nb) * (s.tb + cost);
     return s;
 }
 
@@ -153,7 +153,7 @@ struct Seg {
     int64_t bi, gk;
     int32_t blk;          // row block
     bool two;             // two row tiles
-    int32_t step0, steps, of;   // its steps, and how many the unit has
+    int32_t step0, steps, of, line_n;   // its steps, how many the unit has, its places in the line
 };
 
 struct Walk {
@@ -163,29 +163,32 @@ struct Walk {
     Shape sh;
     bool loaded;
 
-    __device__ __forceinline__ Seg next(const CacheFwdArgs& a)
+    // The next segment with steps; false at the part's end.
+    __device__ __forceinline__ bool next(const CacheFwdArgs& a, Seg& g)
     {
+        if (at >= end) return false;
         if (!loaded) {
             sv = seq_view(a, bi, kKeys, kKeys);
-            sh = shape_of(sv, na, nb);
+            sh = shape_of(sv, na, nb, a.unit_cost);
             loaded = true;
         }
-        Seg g;
         g.bi = bi;
         g.gk = rem / sh.per_head;
         const int64_t r = rem - g.gk * sh.per_head;
-        const int64_t a_steps = static_cast<int64_t>(na) * sh.ta;
-        g.two = r < a_steps;
-        g.blk = g.two ? static_cast<int32_t>(r / sh.ta) : na;
-        g.step0 = static_cast<int32_t>(g.two ? r - static_cast<int64_t>(g.blk) * sh.ta : r - a_steps);
+        const int64_t a_line = static_cast<int64_t>(na) * (sh.ta + a.unit_cost);
+        g.two = r < a_line;
         g.of = g.two ? sh.ta : sh.tb;
-        g.steps = static_cast<int32_t>(imin64(g.of - g.step0, end - at));
-        return g;
+        const Segment s = segment_at(g.two ? r : r - a_line, g.of, a.unit_cost, end - at);
+        g.blk = g.two ? static_cast<int32_t>(s.un) : na;
+        g.step0 = s.tile0;
+        g.steps = s.n;
+        g.line_n = s.line_n;
+        return s.n > 0;       // a part that ends before a unit's first step has no more
     }
     __device__ __forceinline__ void advance(const CacheFwdArgs& a, const Seg& g)
     {
-        at += g.steps;
-        rem += g.steps;
+        at += g.line_n;
+        rem += g.line_n;
         if (rem == sh.per_head * a.c.h_kv) {
             ++bi;
             rem = 0;
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(sm);
     auto bar = [&](int i) -> uint32_t { return sbase + C::kBars + 8u * i; };
-    uint32_t* misc = reinterpret_cast<uint32_t*>(sm + C::kMisc);   // [0] tmem base, [1] abort flag
+    uint32_t* misc = reinterpret_cast<uint32_t*>(sm + C::kMisc);   // [0] tmem base, [1] abort flag, [2] segments begun
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t tmo = static_cast<uint64_t>(a.timeout_ns);
 
@@ -231,14 +234,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         const int64_t units = a.c.h_kv * blocks;
         part.bi = blockIdx.x / units;
         const int64_t un = blockIdx.x - part.bi * units, gk = un / blocks, blk = un - gk * blocks;
-        const Shape s = shape_of(seq_view(a, part.bi, kKeys, kKeys), na, nb);
-        part.rem = gk * s.per_head + blk * s.ta;
+        const Shape s = shape_of(seq_view(a, part.bi, kKeys, kKeys), na, nb, a.unit_cost);
+        part.rem = gk * s.per_head + blk * (s.ta + a.unit_cost) + a.unit_cost;
         part.end = blk < na ? s.ta : s.tb;
     } else {
         part = find_part<kTileThreads>(
-            a.c.b, a.min_tiles, [&](int64_t i) { return a.c.h_kv * shape_of(seq_view(a, i, kKeys, kKeys), na, nb).per_head; }, sh_sum, sh_at);
+            a.c.b, [&](int64_t i) { return a.c.h_kv * shape_of(seq_view(a, i, kKeys, kKeys), na, nb, a.unit_cost).per_head; }, sh_sum, sh_at);
+        if (tid == 0 && !a.cut_by_unit) a.cuts[blockIdx.x].bi = -1;
         if (part.end == 0) {
-            if (tid == 0 && !a.cut_by_unit) a.cuts[blockIdx.x].bi = -1;
             grid_dep_launch();
             return;
         }
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
     walk.rem = part.rem;
 
     if (tid == 0) {
-        misc[1] = 0;
+        misc[1] = misc[2] = 0;
         for (int i = 0; i < NS; ++i) {
             mbar_init(bar(tKFull + i), 2);
             mbar_init(bar(tKEmpty + i), 2);
@@ -261,9 +264,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             mbar_init(bar(tPFull + s), 128);
             mbar_init(bar(tPvDone + s), 1);
         }
-        mbar_init(bar(tQFull), 128);
-        mbar_init(bar(tQFull + 1), 128);
-        mbar_init(bar(tSegDone), 256);
         mbar_init(bar(tDrain), 1);
         mbar_init(bar(tDrain + 1), 1);
         fence_mbar_init();
@@ -286,6 +286,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         *abort_flag = 1;
         set_status(a.c.status, SDPA_ERR_TIMEOUT);
         return false;
+    };
+    // until the softmax groups have begun n segments
+    auto wait_count = [&](uint32_t n) -> bool {
+        const uint64_t t0 = globaltimer_ns();
+        for (;;) {
+            uint32_t x;
+            asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(x) : "r"(sbase + C::kMisc + 8) : "memory");
+            if (x >= n) return true;
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > tmo) {
+                *abort_flag = 1;
+                set_status(a.c.status, SDPA_ERR_TIMEOUT);
+                return false;
+            }
+        }
     };
     auto wait_warp = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
 
@@ -335,8 +350,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             }
         };
         const int c = lane % CPR, sub = lane / CPR;
-        while (ok && walk.at < walk.end) {
-            const Seg g = walk.next(a);
+        Seg g;
+        while (ok && walk.next(a, g)) {
             const SeqView& sv = walk.sv;
             const int32_t* kpos = a.c.positions && a.window_left >= 0 ? a.c.positions + (g.bi * a.c.h_kv + g.gk) * a.c.cap
                                                                       : nullptr;
@@ -430,30 +445,36 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             }
             walk.advance(a, g);
         }
+        // copies in flight end before the CTA does, whatever wait has run out
         cp_wait<0>();
-        if (ok) hand_over(0);
+        hand_over(0);
+        for (uint32_t k = 0; k < NS && k < it; ++k) {
+            const uint32_t r = it - 1 - k;
+            mbar_wait(bar(full0 + r % NS), (r / NS) & 1, tmo);
+        }
+        __syncwarp();
     } else if (warp < kSoftWarp0) {
         // ------------------------------------------------------------ MMA issuer of slot `sl`
         constexpr uint32_t kIdS = idesc_f16(BF16, 128, 64, false, false);
         constexpr uint32_t kIdPV = idesc_f16(BF16, 128, HD, false, true);
         const int sl = warp - kMmaWarp;
-        uint32_t it0 = 0, seg = 0, twos = 0, done = 0;       // done: this slot's key tiles before the segment
+        uint32_t it0 = 0, seg = 0, done = 0;       // done: this slot's key tiles before the segment
         bool ok = true;
         const uint32_t ts = tm_s0 + sl * 128, to = tm_o0 + sl * HD;
         const uint64_t dk0 = sdesc_sw128(sbase + C::kK, 16, 1024);
         const uint64_t dv0 = sdesc_sw128(sbase + C::kV, kBlk, 1024);
         if (elect_one()) {
-        while (walk.at < walk.end && ok) {
-            const Seg g = walk.next(a);
+        Seg g;
+        while (ok && walk.next(a, g)) {
             const int32_t tiles = seg_tiles(g, walk.sv.tiles);
             const bool two = g.two;
             // this slot's key tiles: all, or every other one
             const int32_t first = two ? 0 : sl, step = two ? 1 : 2;
             const int32_t n = tiles > first ? (tiles - first + step - 1) / step : 0;
             const uint64_t dq = sdesc_sw128(sbase + C::kQ + (two ? sl : 0) * C::kQTile, 16, 1024);
-            // slot 0's rows come in every segment, slot 1's in those with two row tiles
-            if (n > 0) ok = two && sl ? wait(tQFull + 1, twos & 1) : wait(tQFull, seg & 1);
-            twos += two ? 1 : 0;
+            // The softmax groups have read the last segment's O and put this one's rows in place. A count, not a
+            // barrier's parity: a slot may have no tile in a segment, and be two phases ahead or behind
+            ok = wait_count(seg + 1);
             // S of the slot's i-th tile goes two ahead, into the buffer whose P V was issued last; it is put
             // off while its K is not there and a product can go first
             int32_t si = 0;
@@ -482,8 +503,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 const uint32_t r = it0 + first + i * step, st = r % NS, b = (done + i) & 1;
                 if (!(ok = wait(tVFull + st, (r / NS) & 1))) break;
                 if (!(ok = wait(tPFull + sl * 2 + b, ((done + i) >> 1) & 1))) break;
-                // the first product of a segment overwrites an O that has been read
-                if (i == 0 && seg > 0 && !(ok = wait(tSegDone, (seg - 1) & 1))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
@@ -497,11 +516,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             ++seg;
             walk.advance(a, g);
         }
-        // after a wait that ran out: MMAs in flight end before TMEM is freed
-        if (!ok) {
-            mma_commit(bar(tDrain + sl));
-            mbar_wait(bar(tDrain + sl), 0, tmo);
-        }
+        // MMAs in flight end before TMEM is freed, whatever wait has run out
+        mma_commit(bar(tDrain + sl));
+        mbar_wait(bar(tDrain + sl), 0, tmo);
         }
         __syncwarp();
     } else {
@@ -517,8 +534,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         uint32_t it0 = 0, cnt = 0;            // ring index at the segment's start; this slot's key tiles so far
         bool ok = true;
         const int64_t part0 = walk.at;
-        while (walk.at < walk.end) {
-            const Seg g = walk.next(a);
+        uint32_t segs = 0;
+        Seg g;
+        while (walk.next(a, g)) {
             const SeqView& sv = walk.sv;
             const int32_t tiles = seg_tiles(g, sv.tiles), t0 = seg_tile0(g);
             named_sync(3, 256);               // the last segment's masks and statistics have been read
@@ -529,7 +547,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 masks[r] = (m >> r) & 1 ? m : 0;
             }
             if (sl == 0 && r == 0 && !a.whole)
-                name_cut(a, part, walk.at, g.bi, g.gk * blocks + g.blk, a.c.h_kv * blocks, g.step0, g.steps, g.of);
+                name_cut(a, part, walk.at == part0, walk.at + g.line_n - g.step0 - g.steps, a.unit_cost, g.bi,
+                         g.gk * blocks + g.blk, a.c.h_kv * blocks, g.step0, g.steps, g.of);
             // this thread's row
             const int rr = g.blk * 256 + (g.two ? sl * 128 : 0) + row;
             const int tok = rr < R ? rr / a.group : 0;
@@ -543,9 +562,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                     *reinterpret_cast<uint4*>(sm + C::kQ + sl * C::kQTile + swz<kQBlk>(row, c)) = x;
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(bar(tQFull + sl));
             }
             named_sync(3, 256);
+            if (sl == 0 && r == 0)
+                asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(sbase + C::kMisc + 8), "r"(++segs) : "memory");
             const uint64_t mask = rr < R ? masks[tok] : 0;
             const int64_t npos = a.c.next_pos ? a.c.next_pos[g.bi] : sv.len;
             int32_t low = INT32_MIN;
@@ -721,7 +741,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 }
             }
             tc_fence_before();
-            mbar_arrive(bar(tSegDone));
             it0 += tiles;
             walk.advance(a, g);
         }

@@ -98,6 +98,12 @@ FORWARD = {
     "long": ([9000, 11], 1, 4, 2, 64, "bf16", 64, -1, {}),
     "long_d128_rows": ([5000], 3, 8, 2, 128, "f16", 128, -1, {}),
     "long_tree": ([4100, 700], 20, 8, 1, 128, "bf16", 64, 4000, dict(tree=True, sink=True)),
+    # units of one key tile and of many in one part: a slot of the tile kernel without work, segment after segment
+    "short_units": ([(37 * i) % 90 for i in range(60)] + [1500], 5, 16, 2, 64, "bf16", 16, -1, dict(tree=True)),
+    "short_units_d128": ([3, 60, 64, 65, 1, 0, 7, 130, 20, 5] * 6 + [900], 3, 8, 1, 128, "f16", 64, -1, {}),
+    "short_units_two_tiles": ([3, 60, 64, 65, 1, 0, 7, 130, 20, 5] * 2 + [900], 20, 8, 1, 64, "bf16", 64, -1, dict(tree=True)),
+    "short_units_three_tiles": ([3, 60, 1, 0, 130, 5, 700], 37, 8, 1, 128, "bf16", 16, -1, dict(tree=True)),
+    "short_units_few_rows": ([3, 60, 64, 65, 1, 0, 7, 130, 20, 5] * 6 + [900], 1, 8, 2, 128, "bf16", 64, -1, {}),
     "mha_many_rows": ([333, 130], 48, 3, 3, 64, "bf16", 64, -1, dict(tree=True)),
 }
 
