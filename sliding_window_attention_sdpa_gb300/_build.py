@@ -21,7 +21,7 @@ LIB = os.path.join(BUILD, "libswa_sdpa_bwd.so")
 LIB_DBG = os.path.join(BUILD, "libswa_sdpa_bwd_dbg.so")
 DEBUG_BOUNDS = ("-DSDPA_DEBUG_BOUNDS",)
 SOURCES = ["api.cu", "aux_kernels.cu", "main_kernel.cu", "fwd_kernel.cu", "cache_api.cu", "cache_kernels.cu",
-           "cache_fwd.cu", "cache_tile.cu"]
+           "cache_fwd.cu", "cache_tile.cu", "cache_weigh.cu"]
 HEADERS = ["ptx.cuh", "seq.cuh", "sdpa_internal.h", "api_util.h", "cache_internal.h", "cache.cuh",
            "cache_fwd.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -2,7 +2,6 @@
 // argument checks and the launches on the caller's stream. Nothing here
 // allocates or synchronises (except sdpa_cache_check_status).
 #include <cstring>
-#include <cstdlib>
 
 #include <cuda_runtime.h>
 
@@ -342,7 +341,7 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.parts = l.parts;
     a.whole = l.whole;
     a.cut_by_unit = fwd_size(c, p, plan).units <= l.parts;
-    a.unit_cost = getenv("MT") ? atoi(getenv("MT")) : 1;
+    a.unit_cost = plan.unit_cost;
     a.timeout_ns = kWaitLimitNs;
     a.part_o = at<float>(ws, l.part_o);
     a.part_ml = at<float>(ws, l.part_ml);
@@ -403,8 +402,8 @@ sdpa_status_t sdpa_cache_weigh(const sdpa_cache* c, const sdpa_cache_weigh_param
     if ((st = check_strides("q", p->q_stride)) != SDPA_OK) return st;
     int dev = 0;
     if ((st = current_device(&dev)) != SDPA_OK) return st;
-    const bool rows = c->b > 0;
-    const Ptr ptrs[] = {{"q", p->q, rows, 16}, {"lse", p->lse, rows, 4}, {"q_pos", p->q_pos, false, 4}};
+    const bool rows = holds_keys(c);
+    const Ptr ptrs[] = {{"q", p->q, c->b > 0, 16}, {"lse", p->lse, c->b > 0, 4}, {"q_pos", p->q_pos, false, 4}};
     if ((st = check_cache_ptrs(c, dev)) != SDPA_OK || (st = check_ptrs(ptrs, dev)) != SDPA_OK) return st;
     if (!rows) return SDPA_OK;
     swa::CacheWeighArgs a{};
@@ -412,12 +411,22 @@ sdpa_status_t sdpa_cache_weigh(const sdpa_cache* c, const sdpa_cache_weigh_param
     a.s_q = static_cast<int32_t>(p->s_q);
     a.h_q = static_cast<int32_t>(p->h_q);
     a.group = static_cast<int32_t>(p->h_q / c->h_kv);
-    a.window_left = p->window_left;
+    a.window_left = p->window_left < (int64_t(1) << 32) ? p->window_left : -1;
     a.scale_log2 = p->scale * 1.4426950408889634f;
     a.q = static_cast<const uint16_t*>(p->q);
     copy3(a.q_stride, p->q_stride);
     a.lse = p->lse;
     a.q_pos = p->q_pos;
+    a.timeout_ns = kWaitLimitNs;
+    // a CTA per SM, fewer if there are fewer tiles of 128 keys
+    const double tiles = double(c->b) * double(c->h_kv) * double((c->page_size * c->max_pages + 127) / 128);
+    a.parts = tiles < 152 ? static_cast<int32_t>(tiles) : 152;
+    if (c->n_pages > 0) {
+        int32_t box = 128;
+        while (c->page_table != nullptr && c->page_size % box != 0) box >>= 1;
+        if (box >= 8 && make_rows_map(&a.tm_k, c->k, c->dtype, c->d, c->h_kv, c->page_size, c->n_pages, c->k_stride, box))
+            a.box_rows = box;
+    }
     return cuda_status(swa::launch_cache_weigh(a, c->dtype, static_cast<cudaStream_t>(stream)), "cache weigh launch");
 }
 

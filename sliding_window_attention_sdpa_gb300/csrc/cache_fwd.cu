@@ -66,12 +66,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 bytes to shared memory; zeros (nothing read) if not `have`.
-__device__ __forceinline__ void cp16(uint32_t dst, const uint16_t* src, bool have)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
-}
-
 __device__ __forceinline__ uint4 lds16(uint32_t addr)
 {
     uint4 v;
@@ -699,12 +693,18 @@ cudaError_t launch_fwd_typed(const CacheTileArgs& ta, cudaStream_t s)
 
 }  // namespace
 
+// Rows per kv-head above which the tile kernel is ahead (12 sequences of 16484
+// keys, 6 kv-heads): d = 128, 16 rows 116 us against 131 for a rows kernel of 16
+// (8 rows: 107 against the tile kernel's 113); d = 64, 32 rows 98 us against 138
+// (16 rows: 75 against 98). A unit's cost (64 ragged sequences of 5 to 16484
+// keys): rows kernel 123, 89, 79, 79, 84 us at 0, 2, 4, 8, 16; tile kernel with
+// 24 rows 228, 127, 104, 126 us at 0, 4, 8, 16.
 CacheFwdPlan cache_fwd_plan(int64_t d, int64_t rows)
 {
-    if (d == 128) return rows <= 8 ? CacheFwdPlan{kRows128x8, 8, 64, 2} : CacheFwdPlan{kTiles128, 256, 64, 1};
-    if (rows <= 8) return CacheFwdPlan{kRows64x8, 8, 128, 2};
-    if (rows <= 16) return CacheFwdPlan{kRows64x16, 16, 128, 2};
-    return CacheFwdPlan{kTiles64, 256, 64, 1};
+    if (d == 128) return rows <= 8 ? CacheFwdPlan{kRows128x8, 8, 64, 2, 4} : CacheFwdPlan{kTiles128, 256, 64, 1, 8};
+    if (rows <= 8) return CacheFwdPlan{kRows64x8, 8, 128, 2, 4};
+    if (rows <= 16) return CacheFwdPlan{kRows64x16, 16, 128, 2, 4};
+    return CacheFwdPlan{kTiles64, 256, 64, 1, 8};
 }
 
 cudaError_t launch_cache_fwd(const CacheTileArgs& a, int dtype, cudaStream_t s)

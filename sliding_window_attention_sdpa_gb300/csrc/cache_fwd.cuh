@@ -30,6 +30,71 @@ __device__ __forceinline__ float2 unpack2(uint32_t x)
     return __half22float2(h);
 }
 
+// 16-byte chunk of a row of a swizzled tile whose 64-column blocks are BLK bytes.
+template <uint32_t BLK>
+__device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t chunk)
+{
+    return (chunk >> 3) * BLK + (row >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+// 16 bytes to shared memory; zeros (nothing read) if not `have`.
+__device__ __forceinline__ void cp16(uint32_t dst, const uint16_t* src, bool have)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+
+// The MMAs below are issued by one elected thread (elect.sync tells the
+// compiler that the branch holds one): back to back 64 cycles each at N = 128,
+// 48 (A from shared memory) or 32 (from TMEM) at N = 64, against 87, 71 and 52
+// with the whole warp running the code and a predicate on the instruction.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+// After tmem_ld_wait: the values of a load that other work was put behind are
+// used from here on (the compiler may not move that use before the wait).
+__device__ __forceinline__ void loaded(uint32_t (&r)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                     "+r"(r[i + 6]), "+r"(r[i + 7])
+                     :
+                     : "memory");
+}
+
+// Arrives once on `bar` when this thread's MMAs so far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void named_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // One sequence as the rows and keys of this call see it.
 struct SeqView {
     int32_t len, nq;    // cached keys, new tokens

@@ -35,10 +35,10 @@ struct CacheFwdCut {
 };
 
 // Kernel for a head dimension and a kv-head's number of rows: rows of a unit,
-// keys of a tile, CTAs per SM.
+// keys of a tile, CTAs per SM, a unit's fixed cost in tiles.
 enum CacheFwdVariant { kRows128x8, kRows64x8, kRows64x16, kTiles128, kTiles64 };
 struct CacheFwdPlan {
-    int variant, rows, tile, occ;
+    int variant, rows, tile, occ, unit_cost;
 };
 CacheFwdPlan cache_fwd_plan(int64_t d, int64_t rows);
 
@@ -84,6 +84,9 @@ struct CacheAppendArgs {
 };
 
 struct CacheWeighArgs {
+    CUtensorMap tm_k;      // as in CacheTileArgs, boxes of up to 128 rows
+    int32_t box_rows, parts;
+    int64_t timeout_ns;
     CacheView c;
     int32_t s_q, h_q, group;
     int64_t window_left;

@@ -1,75 +1,8 @@
-// cache_kernels.cu -- append, evict and weigh on the paged cache.
+// cache_kernels.cu -- append and evict on the paged cache.
 #include "cache.cuh"
 #include "ptx.cuh"
 
 namespace swa {
-
-namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float warp_sum(float x)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
-}  // namespace
-
-// ---------------------------------------------------------------- weigh
-
-template <int HD, bool BF16>
-__global__ void __launch_bounds__(128) cache_weigh_kernel(const CacheWeighArgs a)
-{
-    constexpr int E = HD / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t bi = blockIdx.x / a.c.h_kv, g = blockIdx.x % a.c.h_kv;
-    bool bad;
-    const int32_t len = cache_length(a.c, bi, bad);
-    const int64_t np = a.c.next_pos ? a.c.next_pos[bi] : len;
-    for (int64_t j = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) >> 5; j < len;
-         j += (static_cast<int64_t>(gridDim.y) * blockDim.x) >> 5) {
-        uint32_t r;
-        const int64_t page = cache_page(a.c, bi, static_cast<uint32_t>(j), r);
-        if (page < 0) continue;
-        const uint16_t* kp = a.c.k + page * a.c.k_stride[0] + r * a.c.k_stride[1] + g * a.c.k_stride[2];
-        float k[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) k[e] = to_float<BF16>(kp[lane * E + e]);
-        const int64_t at = (bi * a.c.h_kv + g) * a.c.cap + j;
-        const int64_t kpos = a.c.positions ? a.c.positions[at] : j;
-        float sum = 0.f;
-        for (int64_t t = 0; t < a.s_q; ++t) {
-            const int64_t qp = a.q_pos ? a.q_pos[bi * a.s_q + t] : np - a.s_q + t;
-            if (qp < 0 || kpos > qp || (a.window_left >= 0 && qp - kpos > a.window_left)) continue;
-            for (int64_t h = g * a.group; h < (g + 1) * a.group; ++h) {
-                const uint16_t* q = a.q + bi * a.q_stride[0] + t * a.q_stride[1] + h * a.q_stride[2];
-                float s = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) s += k[e] * to_float<BF16>(q[lane * E + e]);
-                const float lse = a.lse[(bi * a.h_q + h) * a.s_q + t];
-                s = warp_sum(s);
-                if (fabsf(lse) < INFINITY) sum += exp2f(s * a.scale_log2 - lse * kLog2e);
-            }
-        }
-        if (lane == 0) a.c.weights[at] += sum;
-    }
-}
-
-cudaError_t launch_cache_weigh(const CacheWeighArgs& a, int dtype, cudaStream_t s)
-{
-    if (a.c.b * a.c.h_kv == 0 || a.c.cap == 0) return cudaSuccess;
-    const dim3 grid(static_cast<unsigned>(a.c.b * a.c.h_kv), static_cast<unsigned>(imin64((a.c.cap + 3) / 4, 1024)));
-    if (a.c.d == 64) {
-        if (dtype == SDPA_BF16) cache_weigh_kernel<64, true><<<grid, 128, 0, s>>>(a);
-        else cache_weigh_kernel<64, false><<<grid, 128, 0, s>>>(a);
-    } else {
-        if (dtype == SDPA_BF16) cache_weigh_kernel<128, true><<<grid, 128, 0, s>>>(a);
-        else cache_weigh_kernel<128, false><<<grid, 128, 0, s>>>(a);
-    }
-    return cudaGetLastError();
-}
 
 // ---------------------------------------------------------------- append
 

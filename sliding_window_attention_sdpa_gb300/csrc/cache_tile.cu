@@ -61,19 +61,6 @@ enum TBar : int { tKFull = 0, tKEmpty = 8, tVFull = 16, tVEmpty = 24, tSFull = 3
                   tNumBars = 46 };
 static_assert(tNumBars * 8 <= 448, "mbarrier area");
 
-// 16-byte chunk of a row of a swizzled tile whose 64-column blocks are BLK bytes.
-template <uint32_t BLK>
-__device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t chunk)
-{
-    return (chunk >> 3) * BLK + (row >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-}
-
-// 16 bytes to shared memory; zeros (nothing read) if not `have`.
-__device__ __forceinline__ void cp16(uint32_t dst, const uint16_t* src, bool have)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
-}
-
 // A box of 64 features x box_rows rows of one head of a page.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int head, int row,
                                         int page)
@@ -91,49 +78,10 @@ __device__ __forceinline__ void cp_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The MMAs below are issued by one elected thread (elect.sync tells the
-// compiler that the branch holds one): back to back 64 cycles each at N = 128,
-// 48 (A from shared memory) or 32 (from TMEM) at N = 64, against 87, 71 and 52
-// with the whole warp running the code and a predicate on the instruction.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
-        : "memory");
-}
-
-// Arrives once on `bar` when this thread's MMAs so far are done.
-__device__ __forceinline__ void mma_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void named_sync(int id, int threads)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // How a sequence's steps are laid out: per kv-head `na` blocks of 256 rows
 // with two row tiles (a step is one key tile), then perhaps one block with one
-// row tile (a step is two key tiles), each with its fixed cost before it.
+// row tile (a step is two key tiles), each with its fixed cost before it (by its
+// row tiles: Q in, O out).
 struct Shape {
     int32_t ta, tb;       // steps of a two-tile block, of a one-tile block
     int64_t per_head;
@@ -144,7 +92,7 @@ __device__ __forceinline__ Shape shape_of(const SeqView& v, int na, int nb, int3
     Shape s;
     s.ta = v.tiles;
     s.tb = (v.tiles + 1) >> 1;
-    s.per_head = static_cast<int64_t>(na) * (s.ta + cost) + static_cast<int64_t>(nb) * (s.tb + cost);
+    s.per_head = static_cast<int64_t>(na) * (s.ta + 2 * cost) + static_cast<int64_t>(nb) * (s.tb + cost);
     return s;
 }
 
@@ -153,7 +101,7 @@ struct Seg {
     int64_t bi, gk;
     int32_t blk;          // row block
     bool two;             // two row tiles
-    int32_t step0, steps, of, line_n;   // its steps, how many the unit has, its places in the line
+    int32_t step0, steps, of, line_n, cost;   // its steps, how many the unit has, its places in the line, the unit's cost
 };
 
 struct Walk {
@@ -175,10 +123,11 @@ struct Walk {
         g.bi = bi;
         g.gk = rem / sh.per_head;
         const int64_t r = rem - g.gk * sh.per_head;
-        const int64_t a_line = static_cast<int64_t>(na) * (sh.ta + a.unit_cost);
+        const int64_t a_line = static_cast<int64_t>(na) * (sh.ta + 2 * a.unit_cost);
         g.two = r < a_line;
         g.of = g.two ? sh.ta : sh.tb;
-        const Segment s = segment_at(g.two ? r : r - a_line, g.of, a.unit_cost, end - at);
+        g.cost = g.two ? 2 * a.unit_cost : a.unit_cost;
+        const Segment s = segment_at(g.two ? r : r - a_line, g.of, g.cost, end - at);
         g.blk = g.two ? static_cast<int32_t>(s.un) : na;
         g.step0 = s.tile0;
         g.steps = s.n;
@@ -235,7 +184,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         part.bi = blockIdx.x / units;
         const int64_t un = blockIdx.x - part.bi * units, gk = un / blocks, blk = un - gk * blocks;
         const Shape s = shape_of(seq_view(a, part.bi, kKeys, kKeys), na, nb, a.unit_cost);
-        part.rem = gk * s.per_head + blk * (s.ta + a.unit_cost) + a.unit_cost;
+        part.rem = gk * s.per_head + blk * (s.ta + 2 * a.unit_cost) + (blk < na ? 2 : 1) * a.unit_cost;
         part.end = blk < na ? s.ta : s.tb;
     } else {
         part = find_part<kTileThreads>(
@@ -436,7 +385,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                     for (int i = 0; i < 32 / RPI; ++i) {
                         const int r = i * RPI + sub;
                         const uint64_t q = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(p), r);
-                        cp16(stage + swz<kBlk>(k * 32 + r, c), reinterpret_cast<const uint16_t*>(q) + c * 8, (held >> r) & 1);
+                        cp16(stage + swizzled<kBlk>(k * 32 + r, c), reinterpret_cast<const uint16_t*>(q) + c * 8, (held >> r) & 1);
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
                     queue |= static_cast<uint64_t>(st) << (8 * pending);
@@ -547,7 +496,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 masks[r] = (m >> r) & 1 ? m : 0;
             }
             if (sl == 0 && r == 0 && !a.whole)
-                name_cut(a, part, walk.at == part0, walk.at + g.line_n - g.step0 - g.steps, a.unit_cost, g.bi,
+                name_cut(a, part, walk.at == part0, walk.at + g.line_n - g.step0 - g.steps, g.cost, g.bi,
                          g.gk * blocks + g.blk, a.c.h_kv * blocks, g.step0, g.steps, g.of);
             // this thread's row
             const int rr = g.blk * 256 + (g.two ? sl * 128 : 0) + row;
@@ -559,7 +508,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
 #pragma unroll
                 for (int c = 0; c < HD / 8; ++c) {
                     const uint4 x = real ? ld_nc_v4(qp + c * 8) : make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(sm + C::kQ + sl * C::kQTile + swz<kQBlk>(row, c)) = x;
+                    *reinterpret_cast<uint4*>(sm + C::kQ + sl * C::kQTile + swizzled<kQBlk>(row, c)) = x;
                 }
                 fence_proxy_async_smem();
             }
@@ -619,6 +568,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                     }
                 }
                 tmem_ld_wait();
+                loaded(*reinterpret_cast<uint32_t(*)[32]>(v));
+                loaded(*reinterpret_cast<uint32_t(*)[32]>(v + 32));
                 if (!plain) {
 #pragma unroll
                     for (int e = 0; e < 64; ++e)

@@ -1,0 +1,471 @@
+// cache_weigh.cu -- each cached key's attention weight, summed over given rows
+// (sdpa_cache_weigh).
+//
+// With the rows' LSE known, a key's sum needs no other key: S^T = K Q^T puts
+// the keys in the M dimension (128 per tile, a TMEM lane each) and a kv-head's
+// rows in N (up to 256 at once), so the thread that owns a lane adds
+//   exp2(s_r * scale * log2(e) - LSE_r * log2(e))
+// over its lane's columns in registers: one reader and writer per key, no
+// atomics, a fixed order. Two accumulators of up to 256 columns alternate: the
+// MMAs of a key tile run while the other's columns are being summed.
+//
+// Few rows: bound by reading K once (a 4-stage ring of 128 keys by TMA). Many
+// rows: by the exponentials (one per key and row).
+//
+// Roles (384 threads): warp 0 loads K; warp 1 issues the MMAs; warps 4-7 and
+// 8-11 sum every other key tile each, and put the rows (Q, LSE, positions) in
+// place, 256 at a time; more rows take another round over the part's keys.
+// The key tiles of all (sequence, kv-head) units form one line that the CTAs
+// cut evenly. Every wait is bounded (SDPA_ERR_TIMEOUT in the cache's status).
+#include "cache_fwd.cuh"
+
+namespace swa {
+
+namespace {
+
+constexpr int kWThreads = 384;
+constexpr int kWKeys = 128;
+constexpr int kWRows = 256;
+constexpr int kWCost = 4;             // a unit's fixed cost in key tiles
+
+template <int HD>
+struct WeighCfg {
+    static constexpr uint32_t kTile = kWKeys * HD * 2;
+    static constexpr uint32_t kBlk = kWKeys * 128;            // a 64-column block of a key tile
+    static constexpr uint32_t kQBlk = kWRows * 128;           // and of the rows
+    static constexpr int kStages = HD == 128 ? 4 : 8;
+    static constexpr uint32_t kQ = 0;
+    static constexpr uint32_t kK = kQ + kWRows * HD * 2;
+    static constexpr uint32_t kCst = kK + kStages * kTile;    // float [256]: -LSE * log2(e), -inf for a row that does not count
+    static constexpr uint32_t kPos = kCst + kWRows * 4;       // int32 [256]: positions
+    static constexpr uint32_t kBars = kPos + kWRows * 4;
+    static constexpr uint32_t kMisc = kBars + 192;
+    static constexpr uint32_t kBytes = kMisc + 128 + 1024;
+    static_assert(kBytes <= 232448, "shared memory above the 227 KB a CTA may opt into");
+};
+
+enum WBar : int { wKFull = 0, wKEmpty = 8, wDFull = 16, wDEmpty = 18, wDrain = 20, wNumBars };
+static_assert(wNumBars * 8 <= 192, "mbarrier area");
+
+// Two fp32 values in one 64-bit register, and the packed arithmetic on them.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+
+// A chunk of rows and the key tiles [t0, t1) of a segment that it reaches.
+__device__ __forceinline__ void reach(int32_t qmin, int32_t qmax, int64_t window, int32_t len, int32_t t0, int32_t t1, int32_t& a,
+                                      int32_t& b)
+{
+    if (qmax < 0) {          // no row counts
+        a = b = t0;
+        return;
+    }
+    const int64_t lo = window >= 0 ? imax64(0, qmin - window) : 0;
+    const int64_t hi = imin64(qmax, static_cast<int64_t>(len) - 1);
+    a = static_cast<int32_t>(imax64(t0, lo / kWKeys));
+    b = static_cast<int32_t>(imin64(t1, hi / kWKeys + 1));
+    if (b < a) b = a;
+}
+
+}  // namespace
+
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_constant__ CacheWeighArgs a)
+{
+    using C = WeighCfg<HD>;
+    constexpr int NS = C::kStages;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    __shared__ int64_t sh_sum[kWThreads / 32], sh_at[2];
+    uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_u32(sm);
+    auto bar = [&](int i) -> uint32_t { return sbase + C::kBars + 8u * i; };
+    // [0] tmem base, [1] abort flag, [2] chunks begun, [3] smallest and [4] largest position of the chunk's rows,
+    // [5], [6] chunks whose positions warps 0, 1 have read
+    uint32_t* misc = reinterpret_cast<uint32_t*>(sm + C::kMisc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint64_t tmo = static_cast<uint64_t>(a.timeout_ns);
+
+    const int R = a.s_q * a.group;
+    const int chunks = (R + kWRows - 1) / kWRows;
+    auto tiles_of = [&](int64_t i) -> int32_t {
+        bool bad;
+        return (cache_length(a.c, i, bad) + kWKeys - 1) / kWKeys;
+    };
+    // (a sequence without keys keeps its units' cost, so that every sequence has a place in the line)
+    const Part part = find_part<kWThreads>(a.c.b, [&](int64_t i) { return (tiles_of(i) + kWCost) * a.c.h_kv; }, sh_sum, sh_at);
+    if (part.end == 0) return;
+
+    if (tid == 0) {
+        misc[1] = misc[2] = misc[5] = misc[6] = 0;
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(bar(wKFull + i), 1);
+            mbar_init(bar(wKEmpty + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(wDFull + i), 1);
+            mbar_init(bar(wDEmpty + i), 128);
+        }
+        mbar_init(bar(wDrain), 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(sbase + C::kMisc, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    volatile uint32_t* abort_flag = misc + 1;
+    volatile int32_t* qrange = reinterpret_cast<volatile int32_t*>(misc + 3);
+
+    auto give_up = [&]() -> bool {
+        *abort_flag = 1;
+        set_status(a.c.status, SDPA_ERR_TIMEOUT);
+        return false;
+    };
+    auto wait = [&](int b, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar(b), parity)) return true;
+        if (*abort_flag) return false;
+        if (mbar_wait(bar(b), parity, tmo)) return true;
+        return give_up();
+    };
+    // until n chunks of rows are in place (word 2; 5, 6: have been seen)
+    auto wait_count = [&](uint32_t n, int word = 2) -> bool {
+        const uint64_t t0 = globaltimer_ns();
+        for (;;) {
+            uint32_t x;
+            asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(x) : "r"(sbase + C::kMisc + 4 * word) : "memory");
+            if (x >= n) return true;
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > tmo) return give_up();
+        }
+    };
+    auto put_count = [&](int word, uint32_t n) {
+        asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(sbase + C::kMisc + 4 * word), "r"(n) : "memory");
+    };
+    auto seen = [&](int who, uint32_t n) { put_count(5 + who, n); };
+    // Keys that a chunk cannot reach are left out where slots are positions and the rows may be far from some keys.
+    const bool skips = a.c.positions == nullptr && (a.window_left >= 0 || chunks > 1);
+
+    // Walks the part: f(sequence, kv-head, its keys, first key tile, number of key tiles) until it returns false.
+    auto walk = [&](auto f) {
+        int64_t at = part.at, bi = part.bi, rem = part.rem;
+        while (at < part.end) {
+            bool bad;
+            const int32_t len = cache_length(a.c, bi, bad), tiles = (len + kWKeys - 1) / kWKeys;
+            const Segment g = segment_at(rem, tiles, kWCost, part.end - at);
+            if (g.n > 0 && !f(bi, g.un, len, g.tile0, g.n)) return;
+            at += g.line_n;
+            rem += g.line_n;
+            if (rem == (static_cast<int64_t>(tiles) + kWCost) * a.c.h_kv) {
+                ++bi;
+                rem = 0;
+            }
+        }
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ K
+        uint32_t it = 0, cnt = 0;
+        bool ok = true;
+        walk([&](int64_t bi, int64_t gk, int32_t len, int32_t tile0, int32_t n) -> bool {
+            auto entry_of = [&](int32_t j) -> int32_t {
+                if (a.c.page_table == nullptr) return static_cast<int32_t>(bi);
+                return a.c.page_table[bi * a.c.max_pages + (a.c.page_shift >= 0 ? static_cast<uint32_t>(j) >> a.c.page_shift
+                                                                                : static_cast<uint32_t>(j) / a.c.page_size)];
+            };
+            auto row_of = [&](int32_t j) -> uint32_t {
+                if (a.c.page_table == nullptr) return j;
+                return a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)
+                                           : static_cast<uint32_t>(j) % a.c.page_size;
+            };
+            const int boxes = a.box_rows ? kWKeys / a.box_rows : 0;
+            for (int ch = 0; ch < chunks && ok; ++ch) {
+                int32_t ta = tile0, tb = tile0 + n;
+                ++cnt;
+                if (skips) {
+                    if (!(ok = __all_sync(0xffffffffu, wait_count(cnt)))) break;
+                    reach(qrange[0], qrange[1], a.window_left, len, tile0, tile0 + n, ta, tb);
+                    __syncwarp();
+                    if (lane == 0) seen(0, cnt);
+                }
+                auto box_entry = [&](int32_t t) -> int32_t {
+                    const int32_t j = t * kWKeys + lane * a.box_rows;
+                    return lane < boxes && t < tb && j < len ? entry_of(j) : -1;
+                };
+                int32_t entry = box_entry(ta);
+                for (int32_t t = ta; t < tb; ++t, ++it) {
+                    const uint32_t st = it % NS;
+                    const uint32_t stage = sbase + C::kK + st * C::kTile;
+                    const int32_t mine = entry;
+                    entry = box_entry(t + 1);
+                    if (!(ok = __all_sync(0xffffffffu, wait(wKEmpty + st, ((it / NS) & 1) ^ 1)))) break;
+                    const int32_t j0 = t * kWKeys;
+                    if (boxes > 0) {
+                        // boxes without a key, or on a page out of range, stay as they were: their lanes are not used
+                        const bool good = mine >= 0 && mine < a.c.n_pages;
+                        if (lane < boxes && j0 + lane * a.box_rows < len && !good) set_status(a.c.status, SDPA_ERR_BOUNDS);
+                        const uint32_t have = __popc(__ballot_sync(0xffffffffu, good));
+                        if (lane == 0) mbar_arrive_expect_tx(bar(wKFull + st), have * a.box_rows * HD * 2);
+                        __syncwarp();
+                        if (good) {
+                            const int row = static_cast<int>(row_of(j0 + lane * a.box_rows));
+#pragma unroll
+                            for (int cb = 0; cb < HD / 64; ++cb)
+                                asm volatile(
+                                    "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                                    "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(stage + cb * C::kBlk + lane * a.box_rows * 128),
+                                    "l"(reinterpret_cast<uint64_t>(&a.tm_k)), "r"(bar(wKFull + st)), "r"(cb * 64),
+                                    "r"(static_cast<int>(gk)), "r"(row), "r"(mine)
+                                    : "memory");
+                        }
+                        continue;
+                    }
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        const int32_t j = j0 + k * 32 + lane;
+                        const uint16_t* p = a.c.k;
+                        bool have = j < len;
+                        if (have) {
+                            const int32_t page = entry_of(j);
+                            have = page >= 0 && page < a.c.n_pages;
+                            if (!have) set_status(a.c.status, SDPA_ERR_BOUNDS);
+                            else p += page * a.c.k_stride[0] + row_of(j) * a.c.k_stride[1] + gk * a.c.k_stride[2];
+                        }
+                        const uint32_t held = __ballot_sync(0xffffffffu, have);
+                        constexpr int CPR = HD / 8, RPI = 32 / CPR;
+#pragma unroll 8
+                        for (int i = 0; i < 32 / RPI; ++i) {
+                            const int r = i * RPI + lane / CPR, c = lane % CPR;
+                            const uint64_t q = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(p), r);
+                            cp16(stage + swizzled<C::kBlk>(k * 32 + r, c), reinterpret_cast<const uint16_t*>(q) + c * 8,
+                                 (held >> r) & 1);
+                        }
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(wKFull + st));
+                }
+            }
+            return ok;
+        });
+        // copies in flight end before the CTA does
+        for (uint32_t k = 0; k < NS && k < it; ++k) {
+            const uint32_t r = it - 1 - k;
+            mbar_wait(bar(wKFull + r % NS), (r / NS) & 1, tmo);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        if (elect_one()) {
+            uint32_t it = 0, cnt = 0;
+            bool ok = true;
+            const uint64_t dk0 = sdesc_sw128(sbase + C::kK, 16, 1024);
+            const uint64_t dq0 = sdesc_sw128(sbase + C::kQ, 16, 1024);
+            walk([&](int64_t, int64_t, int32_t len, int32_t tile0, int32_t n) -> bool {
+                for (int ch = 0; ch < chunks && ok; ++ch) {
+                    if (!(ok = wait_count(++cnt))) break;
+                    int32_t ta = tile0, tb = tile0 + n;
+                    if (skips) {
+                        reach(qrange[0], qrange[1], a.window_left, len, tile0, tile0 + n, ta, tb);
+                        seen(1, cnt);
+                    }
+                    const int rows = (min(kWRows, R - ch * kWRows) + 31) & ~31;
+                    const uint32_t idesc = idesc_f16(BF16, 128, 0, false, false) | static_cast<uint32_t>(rows >> 3) << 17;
+                    for (int32_t t = ta; t < tb; ++t, ++it) {
+                        const uint32_t st = it % NS, b = it & 1;
+                        if (!(ok = wait(wKFull + st, (it / NS) & 1))) break;
+                        if (!(ok = wait(wDEmpty + b, ((it >> 1) & 1) ^ 1))) break;
+                        tc_fence_after();
+                        const uint64_t dk = sdesc_at(dk0, st * C::kTile);
+#pragma unroll
+                        for (int k = 0; k < HD / 16; ++k)
+                            mma_ss(tmem + b * kWRows, sdesc_at(dk, (k >> 2) * C::kBlk + (k & 3) * 32),
+                                   sdesc_at(dq0, (k >> 2) * C::kQBlk + (k & 3) * 32), idesc, k > 0);
+                        mma_commit(bar(wDFull + b));
+                        mma_commit(bar(wKEmpty + st));
+                    }
+                }
+                return ok;
+            });
+            // MMAs in flight end before TMEM is freed
+            mma_commit(bar(wDrain));
+            mbar_wait(bar(wDrain), 0, tmo);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ rows, sums
+        const int grp = (warp - 4) >> 2;
+        const int et = tid - 128;                           // 0..255: a row each
+        const int key_lane = ((warp & 3) << 5) + lane;      // key of the tile
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const float* cst = reinterpret_cast<const float*>(sm + C::kCst);
+        const int32_t* qpos = reinterpret_cast<const int32_t*>(sm + C::kPos);
+        uint32_t it = 0, cnt = 0;
+        bool ok = true;
+        const uint64_t scale2 = pair(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
+        walk([&](int64_t bi, int64_t gk, int32_t len, int32_t tile0, int32_t n) -> bool {
+            const int64_t npos = a.c.next_pos ? a.c.next_pos[bi] : len;
+            const int64_t unit = (bi * a.c.h_kv + gk) * a.c.cap;
+            for (int ch = 0; ch < chunks; ++ch) {
+                named_sync(3, 256);         // both groups are done with the last chunk's rows
+                const int r = ch * kWRows + et;
+                const int rows = (min(kWRows, R - ch * kWRows) + 31) & ~31;
+                {
+                    int64_t p = -1;
+                    float c = -INFINITY;
+                    const int tok = r < R ? r / a.group : 0;
+                    const int64_t h = gk * a.group + (r - tok * a.group);
+                    if (r < R) {
+                        p = a.q_pos ? a.q_pos[bi * a.s_q + tok] : npos - a.s_q + tok;
+                        const float z = a.lse[(bi * a.h_q + h) * a.s_q + tok];
+                        if (p >= 0 && fabsf(z) < INFINITY) c = -z * kLog2e;
+                    }
+                    const bool live = c != -INFINITY;
+                    const int32_t pos = live ? static_cast<int32_t>(imin64(p, INT32_MAX)) : -1;
+                    reinterpret_cast<float*>(sm + C::kCst)[et] = c;
+                    reinterpret_cast<int32_t*>(sm + C::kPos)[et] = pos;
+                    if (et < rows) {
+                        const uint16_t* qp = a.q + bi * a.q_stride[0] + tok * a.q_stride[1] + h * a.q_stride[2];
+#pragma unroll
+                        for (int k = 0; k < HD / 8; ++k) {
+                            const uint4 x = live ? ld_nc_v4(qp + k * 8) : make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4*>(sm + C::kQ + swizzled<C::kQBlk>(et, k)) = x;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                named_sync(3, 256);
+                // smallest and largest position of the rows that count (each group's warps alike)
+                int32_t lo = INT32_MAX, hi = -1;
+                for (int i = lane; i < rows; i += 32) {
+                    const int32_t p = qpos[i];
+                    if (p >= 0) lo = min(lo, p);
+                    hi = max(hi, p);
+                }
+                lo = __reduce_min_sync(0xffffffffu, lo);
+                hi = __reduce_max_sync(0xffffffffu, hi);
+                ++cnt;
+                if (et == 0) {
+                    // a chunk without tiles is over at once: its positions stay until both readers have seen them
+                    if (skips) ok = ok && wait_count(cnt - 1, 5) && wait_count(cnt - 1, 6);
+                    qrange[0] = lo;
+                    qrange[1] = hi;
+                    put_count(2, cnt);
+                }
+                int32_t ta = tile0, tb = tile0 + n;
+                if (skips) reach(lo, hi, a.window_left, len, tile0, tile0 + n, ta, tb);
+                for (int32_t t = ta; t < tb; ++t, ++it) {
+                    if (static_cast<int>(it & 1) != grp) continue;
+                    // this thread's key: held, on a page of the cache
+                    const int32_t j = t * kWKeys + key_lane;
+                    bool held = j < len;
+                    if (held && a.c.page_table) {
+                        const int32_t page =
+                            a.c.page_table[bi * a.c.max_pages + (a.c.page_shift >= 0 ? static_cast<uint32_t>(j) >> a.c.page_shift
+                                                                                     : static_cast<uint32_t>(j) / a.c.page_size)];
+                        held = page >= 0 && page < a.c.n_pages;
+                    }
+                    const int32_t kp = !held ? 0 : a.c.positions ? a.c.positions[unit + j] : j;
+                    const float w = held ? a.c.weights[unit + j] : 0.f;
+                    // does every row that counts admit every key of the warp?
+                    const bool plain = __all_sync(0xffffffffu, !held || (kp <= lo && (a.window_left < 0 ||
+                                                                                      hi - static_cast<int64_t>(kp) <= a.window_left)));
+                    ok = ok && wait(wDFull + grp, (it >> 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    const uint32_t td = tmem + grp * kWRows + lane_off;
+                    // 32 columns at a time, the next ones on their way
+                    uint64_t s2[4] = {0u, 0u, 0u, 0u};
+                    uint32_t v[2][32];
+                    tmem_ld32(td, v[0]);
+                    tmem_ld_wait();
+                    loaded(v[0]);
+                    auto add = [&](uint32_t (&x)[32], int cb) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(cst + cb + e);
+                            uint64_t y0 = fma2(pair(x[e], x[e + 1]), scale2, c.x);
+                            uint64_t y1 = fma2(pair(x[e + 2], x[e + 3]), scale2, c.y);
+                            float p[4] = {ex2_approx(lo_of(y0)), ex2_approx(hi_of(y0)), ex2_approx(lo_of(y1)), ex2_approx(hi_of(y1))};
+                            if (!plain) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const int64_t at = qpos[cb + e + q];
+                                    if (kp > at || (a.window_left >= 0 && at - kp > a.window_left)) p[q] = 0.f;
+                                }
+                            }
+                            s2[(e >> 1) & 3] = add2(s2[(e >> 1) & 3], pair(__float_as_uint(p[0]), __float_as_uint(p[1])));
+                            s2[((e >> 1) & 3) + 1] = add2(s2[((e >> 1) & 3) + 1], pair(__float_as_uint(p[2]), __float_as_uint(p[3])));
+                        }
+                    };
+#pragma unroll 1
+                    for (int cb = 0; cb < rows; cb += 64) {
+                        if (cb + 32 < rows) tmem_ld32(td + cb + 32, v[1]);
+                        add(v[0], cb);
+                        tmem_ld_wait();
+                        loaded(v[1]);
+                        if (cb + 32 >= rows) break;
+                        if (cb + 64 < rows) tmem_ld32(td + cb + 64, v[0]);
+                        add(v[1], cb + 32);
+                        tmem_ld_wait();
+                        loaded(v[0]);
+                    }
+                    const uint64_t sum2 = add2(add2(s2[0], s2[1]), add2(s2[2], s2[3]));
+                    tc_fence_before();
+                    mbar_arrive(bar(wDEmpty + grp));
+                    if (held) a.c.weights[unit + j] = w + (lo_of(sum2) + hi_of(sum2));
+                }
+            }
+            return true;
+        });
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+namespace {
+
+template <int HD, bool BF16>
+cudaError_t launch_typed(const CacheWeighArgs& a, cudaStream_t s)
+{
+    auto kern = cache_weigh_kernel<HD, BF16>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WeighCfg<HD>::kBytes);
+    if (e != cudaSuccess) return e;
+    kern<<<a.parts, kWThreads, WeighCfg<HD>::kBytes, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_weigh(const CacheWeighArgs& a, int dtype, cudaStream_t s)
+{
+    if (a.c.d == 128) return dtype == SDPA_BF16 ? launch_typed<128, true>(a, s) : launch_typed<128, false>(a, s);
+    return dtype == SDPA_BF16 ? launch_typed<64, true>(a, s) : launch_typed<64, false>(a, s);
+}
+
+}  // namespace swa

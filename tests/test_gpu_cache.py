@@ -374,6 +374,13 @@ WEIGH = {
     "evicted_window": ([90, 257, 0], 5, 40, 2, 128, "bf16", 32, 100, dict(evicted=True, pos=True)),
     "group_5_mqa": ([1100], 1, 5, 1, 128, "f16", 0, -1, {}),
     "long": ([9000, 11], 1, 4, 2, 64, "bf16", 64, -1, {}),
+    # several rounds of 256 rows, some of which reach no key of a part
+    "rounds": ([1500, 0, 40], 200, 8, 2, 64, "bf16", 64, -1, dict(pos=True)),
+    "rounds_window": ([1500, 300, 40], 200, 8, 2, 64, "bf16", 24, 64, dict(pos=True)),
+    "rounds_window_odd_pages": ([700, 300], 90, 8, 1, 128, "f16", 7, 30, dict(pos=True)),
+    "rounds_evicted": ([300, 500], 70, 8, 1, 128, "bf16", 64, 100, dict(evicted=True, pos=True)),
+    "short_units": ([(37 * i) % 90 for i in range(70)] + [1500], 2, 8, 4, 64, "bf16", 16, -1, {}),
+    "short_units_window": ([(37 * i) % 90 for i in range(70)] + [1500], 3, 8, 4, 128, "bf16", 16, 5, dict(pos=True)),
 }
 
 
