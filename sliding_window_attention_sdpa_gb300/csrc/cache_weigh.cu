@@ -6,8 +6,8 @@
 // rows in N (up to 256 at once), so the thread that owns a lane adds
 //   exp2(s_r * scale * log2(e) - LSE_r * log2(e))
 // over its lane's columns in registers: one reader and writer per key, no
-// atomics, a fixed order. Two accumulators of up to 256 columns alternate: the
-// MMAs of a key tile run while the other's columns are being summed.
+// atomics, a fixed order. Four accumulators of up to 128 columns: each of two
+// groups of warps sums one while its other one is computed.
 //
 // Few rows: bound by reading K once (a 4-stage ring of 128 keys by TMA). Many
 // rows: by the exponentials (one per key and row).
@@ -26,6 +26,7 @@ namespace {
 constexpr int kWThreads = 384;
 constexpr int kWKeys = 128;
 constexpr int kWRows = 256;
+constexpr int kWHalf = 128;           // rows of an accumulator
 constexpr int kWCost = 4;             // a unit's fixed cost in key tiles
 
 template <int HD>
@@ -39,13 +40,14 @@ struct WeighCfg {
     static constexpr uint32_t kCst = kK + kStages * kTile;    // float [256]: -LSE * log2(e), -inf for a row that does not count
     static constexpr uint32_t kPos = kCst + kWRows * 4;       // int32 [256]: positions
     static constexpr uint32_t kBars = kPos + kWRows * 4;
-    static constexpr uint32_t kMisc = kBars + 192;
+    static constexpr uint32_t kMisc = kBars + 256;
     static constexpr uint32_t kBytes = kMisc + 128 + 1024;
     static_assert(kBytes <= 232448, "shared memory above the 227 KB a CTA may opt into");
 };
 
-enum WBar : int { wKFull = 0, wKEmpty = 8, wDFull = 16, wDEmpty = 18, wDrain = 20, wNumBars };
-static_assert(wNumBars * 8 <= 192, "mbarrier area");
+// (accumulators: group * 2 + buffer)
+enum WBar : int { wKFull = 0, wKEmpty = 8, wDFull = 16, wDEmpty = 20, wDrain = 24, wNumBars };
+static_assert(wNumBars * 8 <= 256, "mbarrier area");
 
 // Two fp32 values in one 64-bit register, and the packed arithmetic on them.
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi)
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
             mbar_init(bar(wKFull + i), 1);
             mbar_init(bar(wKEmpty + i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(bar(wDFull + i), 1);
             mbar_init(bar(wDEmpty + i), 128);
         }
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         if (elect_one()) {
-            uint32_t it = 0, cnt = 0;
+            uint32_t it = 0, cnt = 0, made0 = 0, made1 = 0;    // accumulators of each group so far
             bool ok = true;
             const uint64_t dk0 = sdesc_sw128(sbase + C::kK, 16, 1024);
             const uint64_t dq0 = sdesc_sw128(sbase + C::kQ, 16, 1024);
@@ -290,18 +292,23 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                         seen(1, cnt);
                     }
                     const int rows = (min(kWRows, R - ch * kWRows) + 31) & ~31;
-                    const uint32_t idesc = idesc_f16(BF16, 128, 0, false, false) | static_cast<uint32_t>(rows >> 3) << 17;
-                    for (int32_t t = ta; t < tb; ++t, ++it) {
-                        const uint32_t st = it % NS, b = it & 1;
+                    for (int32_t t = ta; t < tb && ok; ++t, ++it) {
+                        const uint32_t st = it % NS, grp = it & 1;
                         if (!(ok = wait(wKFull + st, (it / NS) & 1))) break;
-                        if (!(ok = wait(wDEmpty + b, ((it >> 1) & 1) ^ 1))) break;
-                        tc_fence_after();
                         const uint64_t dk = sdesc_at(dk0, st * C::kTile);
+                        for (int r0 = 0; r0 < rows; r0 += kWHalf) {
+                            const uint32_t m = grp ? made1++ : made0++, b = grp * 2 + (m & 1);
+                            if (!(ok = wait(wDEmpty + b, ((m >> 1) & 1) ^ 1))) break;
+                            tc_fence_after();
+                            const uint32_t idesc = idesc_f16(BF16, 128, 0, false, false) |
+                                                   static_cast<uint32_t>(min(kWHalf, rows - r0) >> 3) << 17;
+                            const uint64_t dq = sdesc_at(dq0, r0 * 128);
 #pragma unroll
-                        for (int k = 0; k < HD / 16; ++k)
-                            mma_ss(tmem + b * kWRows, sdesc_at(dk, (k >> 2) * C::kBlk + (k & 3) * 32),
-                                   sdesc_at(dq0, (k >> 2) * C::kQBlk + (k & 3) * 32), idesc, k > 0);
-                        mma_commit(bar(wDFull + b));
+                            for (int k = 0; k < HD / 16; ++k)
+                                mma_ss(tmem + b * kWHalf, sdesc_at(dk, (k >> 2) * C::kBlk + (k & 3) * 32),
+                                       sdesc_at(dq, (k >> 2) * C::kQBlk + (k & 3) * 32), idesc, k > 0);
+                            mma_commit(bar(wDFull + b));
+                        }
                         mma_commit(bar(wKEmpty + st));
                     }
                 }
@@ -320,8 +327,10 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float* cst = reinterpret_cast<const float*>(sm + C::kCst);
         const int32_t* qpos = reinterpret_cast<const int32_t*>(sm + C::kPos);
-        uint32_t it = 0, cnt = 0;
+        uint32_t it = 0, cnt = 0, taken = 0;                // taken: this group's accumulators
         bool ok = true;
+        // widest distance of a key behind a row
+        const uint32_t wide = a.window_left < 0 || a.window_left > INT32_MAX ? INT32_MAX : static_cast<uint32_t>(a.window_left);
         const uint64_t scale2 = pair(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
         walk([&](int64_t bi, int64_t gk, int32_t len, int32_t tile0, int32_t n) -> bool {
             const int64_t npos = a.c.next_pos ? a.c.next_pos[bi] : len;
@@ -387,54 +396,66 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                     }
                     const int32_t kp = !held ? 0 : a.c.positions ? a.c.positions[unit + j] : j;
                     const float w = held ? a.c.weights[unit + j] : 0.f;
-                    // does every row that counts admit every key of the warp?
-                    const bool plain = __all_sync(0xffffffffu, !held || (kp <= lo && (a.window_left < 0 ||
-                                                                                      hi - static_cast<int64_t>(kp) <= a.window_left)));
-                    ok = ok && wait(wDFull + grp, (it >> 1) & 1);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) continue;
-                    tc_fence_after();
-                    const uint32_t td = tmem + grp * kWRows + lane_off;
-                    // 32 columns at a time, the next ones on their way
+                    // does every row that counts admit every key of the warp, or none any?
+                    const bool plain = __all_sync(0xffffffffu, !held || (kp <= lo && static_cast<uint32_t>(hi - kp) <= wide));
+                    const bool none = __all_sync(0xffffffffu, !held || kp > hi || (kp < lo && static_cast<uint32_t>(lo - kp) > wide));
                     uint64_t s2[4] = {0u, 0u, 0u, 0u};
-                    uint32_t v[2][32];
-                    tmem_ld32(td, v[0]);
-                    tmem_ld_wait();
-                    loaded(v[0]);
-                    auto add = [&](uint32_t (&x)[32], int cb) {
+                    for (int r0 = 0; r0 < rows; r0 += kWHalf) {
+                        const uint32_t b = grp * 2 + (taken & 1);
+                        ok = ok && wait(wDFull + b, (taken >> 1) & 1);
+                        ++taken;
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) continue;
+                        tc_fence_after();
+                        const uint32_t td = tmem + b * kWHalf + lane_off;
+                        const int n32 = min(kWHalf, rows - r0);
+                        // 32 columns at a time, the next ones on their way
+                        uint32_t v[2][32];
+                        auto add = [&](uint32_t (&x)[32], int cb) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(cst + cb + e);
-                            uint64_t y0 = fma2(pair(x[e], x[e + 1]), scale2, c.x);
-                            uint64_t y1 = fma2(pair(x[e + 2], x[e + 3]), scale2, c.y);
-                            float p[4] = {ex2_approx(lo_of(y0)), ex2_approx(hi_of(y0)), ex2_approx(lo_of(y1)), ex2_approx(hi_of(y1))};
-                            if (!plain) {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int64_t at = qpos[cb + e + q];
-                                    if (kp > at || (a.window_left >= 0 && at - kp > a.window_left)) p[q] = 0.f;
+                            for (int e = 0; e < 32; e += 4) {
+                                const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(cst + r0 + cb + e);
+                                const uint64_t y0 = fma2(pair(x[e], x[e + 1]), scale2, c.x);
+                                const uint64_t y1 = fma2(pair(x[e + 2], x[e + 3]), scale2, c.y);
+                                float p[4] = {ex2_approx(lo_of(y0)), ex2_approx(hi_of(y0)), ex2_approx(lo_of(y1)),
+                                              ex2_approx(hi_of(y1))};
+                                if (!plain) {
+                                    // (a row that does not count is at -1: below every key)
+                                    const int4 at = *reinterpret_cast<const int4*>(qpos + r0 + cb + e);
+                                    if (static_cast<uint32_t>(at.x - kp) > wide) p[0] = 0.f;
+                                    if (static_cast<uint32_t>(at.y - kp) > wide) p[1] = 0.f;
+                                    if (static_cast<uint32_t>(at.z - kp) > wide) p[2] = 0.f;
+                                    if (static_cast<uint32_t>(at.w - kp) > wide) p[3] = 0.f;
                                 }
+                                uint64_t& sa = s2[(e >> 1) & 2];
+                                uint64_t& sb = s2[((e >> 1) & 2) + 1];
+                                sa = add2(sa, pair(__float_as_uint(p[0]), __float_as_uint(p[1])));
+                                sb = add2(sb, pair(__float_as_uint(p[2]), __float_as_uint(p[3])));
                             }
-                            s2[(e >> 1) & 3] = add2(s2[(e >> 1) & 3], pair(__float_as_uint(p[0]), __float_as_uint(p[1])));
-                            s2[((e >> 1) & 3) + 1] = add2(s2[((e >> 1) & 3) + 1], pair(__float_as_uint(p[2]), __float_as_uint(p[3])));
-                        }
-                    };
+                        };
+                        if (!none) {
+                            tmem_ld32(td, v[0]);
+                            tmem_ld_wait();
+                            loaded(v[0]);
 #pragma unroll 1
-                    for (int cb = 0; cb < rows; cb += 64) {
-                        if (cb + 32 < rows) tmem_ld32(td + cb + 32, v[1]);
-                        add(v[0], cb);
-                        tmem_ld_wait();
-                        loaded(v[1]);
-                        if (cb + 32 >= rows) break;
-                        if (cb + 64 < rows) tmem_ld32(td + cb + 64, v[0]);
-                        add(v[1], cb + 32);
-                        tmem_ld_wait();
-                        loaded(v[0]);
+                            for (int cb = 0;; cb += 64) {
+                                if (cb + 32 < n32) tmem_ld32(td + cb + 32, v[1]);
+                                add(v[0], cb);
+                                if (cb + 32 >= n32) break;
+                                tmem_ld_wait();
+                                loaded(v[1]);
+                                if (cb + 64 < n32) tmem_ld32(td + cb + 64, v[0]);
+                                add(v[1], cb + 32);
+                                if (cb + 64 >= n32) break;
+                                tmem_ld_wait();
+                                loaded(v[0]);
+                            }
+                        }
+                        tc_fence_before();
+                        mbar_arrive(bar(wDEmpty + b));
                     }
                     const uint64_t sum2 = add2(add2(s2[0], s2[1]), add2(s2[2], s2[3]));
-                    tc_fence_before();
-                    mbar_arrive(bar(wDEmpty + grp));
-                    if (held) a.c.weights[unit + j] = w + (lo_of(sum2) + hi_of(sum2));
+                    if (held && ok) a.c.weights[unit + j] = w + (lo_of(sum2) + hi_of(sum2));
                 }
             }
             return true;
