@@ -12,9 +12,12 @@
 // Few rows: bound by reading K once (a 4-stage ring of 128 keys by TMA). Many
 // rows: by the exponentials (one per key and row).
 //
-// Roles (384 threads): warp 0 loads K; warp 1 issues the MMAs; warps 4-7 and
-// 8-11 sum every other key tile each, and put the rows (Q, LSE, positions) in
-// place, 256 at a time; more rows take another round over the part's keys.
+// Roles (640 threads): warp 0 loads K; warp 1 issues the MMAs; warps 4-11 and
+// 12-19 sum every other key tile each, two threads a key (64 of an
+// accumulator's columns each; 8 warps instead of 16 left the SM waiting on
+// latencies: 116 us against 102 at 12 sequences of 16484 keys, 6 kv-heads, 256 rows), and
+// put the rows (Q, LSE, positions) in place, 256 at a time; more rows take
+// another round over the part's keys.
 // The key tiles of all (sequence, kv-head) units form one line that the CTAs
 // cut evenly. Every wait is bounded (SDPA_ERR_TIMEOUT in the cache's status).
 #include "cache_fwd.cuh"
@@ -23,7 +26,7 @@ namespace swa {
 
 namespace {
 
-constexpr int kWThreads = 384;
+constexpr int kWThreads = 640;
 constexpr int kWKeys = 128;
 constexpr int kWRows = 256;
 constexpr int kWHalf = 128;           // rows of an accumulator
@@ -39,7 +42,8 @@ struct WeighCfg {
     static constexpr uint32_t kK = kQ + kWRows * HD * 2;
     static constexpr uint32_t kCst = kK + kStages * kTile;    // float [256]: -LSE * log2(e), -inf for a row that does not count
     static constexpr uint32_t kPos = kCst + kWRows * 4;       // int32 [256]: positions
-    static constexpr uint32_t kBars = kPos + kWRows * 4;
+    static constexpr uint32_t kSum = kPos + kWRows * 4;       // float [2 groups][2 tiles][128]: second threads' sums
+    static constexpr uint32_t kBars = kSum + 2048;
     static constexpr uint32_t kMisc = kBars + 256;
     static constexpr uint32_t kBytes = kMisc + 128 + 1024;
     static_assert(kBytes <= 232448, "shared memory above the 227 KB a CTA may opt into");
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(wDFull + i), 1);
-            mbar_init(bar(wDEmpty + i), 128);
+            mbar_init(bar(wDEmpty + i), 256);
         }
         mbar_init(bar(wDrain), 1);
         fence_mbar_init();
@@ -321,13 +325,13 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
         __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ rows, sums
-        const int grp = (warp - 4) >> 2;
-        const int et = tid - 128;                           // 0..255: a row each
+        const int grp = (warp - 4) >> 3, second = ((warp - 4) >> 2) & 1;
+        const int et = tid - 128;                           // the first 256: a row each
         const int key_lane = ((warp & 3) << 5) + lane;      // key of the tile
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float* cst = reinterpret_cast<const float*>(sm + C::kCst);
         const int32_t* qpos = reinterpret_cast<const int32_t*>(sm + C::kPos);
-        uint32_t it = 0, cnt = 0, taken = 0;                // taken: this group's accumulators
+        uint32_t it = 0, cnt = 0, taken = 0, tile_par = 0;  // taken: this group's accumulators
         bool ok = true;
         // widest distance of a key behind a row
         const uint32_t wide = a.window_left < 0 || a.window_left > INT32_MAX ? INT32_MAX : static_cast<uint32_t>(a.window_left);
@@ -336,10 +340,10 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
             const int64_t npos = a.c.next_pos ? a.c.next_pos[bi] : len;
             const int64_t unit = (bi * a.c.h_kv + gk) * a.c.cap;
             for (int ch = 0; ch < chunks; ++ch) {
-                named_sync(3, 256);         // both groups are done with the last chunk's rows
+                named_sync(3, 512);         // both groups are done with the last chunk's rows
                 const int r = ch * kWRows + et;
                 const int rows = (min(kWRows, R - ch * kWRows) + 31) & ~31;
-                {
+                if (et < kWRows) {
                     int64_t p = -1;
                     float c = -INFINITY;
                     const int tok = r < R ? r / a.group : 0;
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                     }
                     fence_proxy_async_smem();
                 }
-                named_sync(3, 256);
+                named_sync(3, 512);
                 // smallest and largest position of the rows that count (each group's warps alike)
                 int32_t lo = INT32_MAX, hi = -1;
                 for (int i = lane; i < rows; i += 32) {
@@ -383,19 +387,32 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                 }
                 int32_t ta = tile0, tb = tile0 + n;
                 if (skips) reach(lo, hi, a.window_left, len, tile0, tile0 + n, ta, tb);
+                // this thread's key of a tile: its page entry, position and weight are loaded a tile of the group ahead
+                struct Mine {
+                    int32_t entry, pos;
+                    float w;
+                };
+                auto fetch = [&](int32_t t) -> Mine {
+                    Mine k{static_cast<int32_t>(bi), 0, 0.f};
+                    const int32_t j = t * kWKeys + key_lane;
+                    if (t < tb && j < len) {
+                        if (a.c.page_table)
+                            k.entry = a.c.page_table[bi * a.c.max_pages + (a.c.page_shift >= 0 ? static_cast<uint32_t>(j) >> a.c.page_shift
+                                                                                               : static_cast<uint32_t>(j) / a.c.page_size)];
+                        k.pos = a.c.positions ? a.c.positions[unit + j] : j;
+                        k.w = a.c.weights[unit + j];
+                    }
+                    return k;
+                };
+                const int32_t mine0 = ta + static_cast<int32_t>((it & 1) != static_cast<uint32_t>(grp));   // the group's first tile
+                Mine next = fetch(mine0);
                 for (int32_t t = ta; t < tb; ++t, ++it) {
                     if (static_cast<int>(it & 1) != grp) continue;
-                    // this thread's key: held, on a page of the cache
+                    const Mine me = next;
+                    next = fetch(t + 2);
                     const int32_t j = t * kWKeys + key_lane;
-                    bool held = j < len;
-                    if (held && a.c.page_table) {
-                        const int32_t page =
-                            a.c.page_table[bi * a.c.max_pages + (a.c.page_shift >= 0 ? static_cast<uint32_t>(j) >> a.c.page_shift
-                                                                                     : static_cast<uint32_t>(j) / a.c.page_size)];
-                        held = page >= 0 && page < a.c.n_pages;
-                    }
-                    const int32_t kp = !held ? 0 : a.c.positions ? a.c.positions[unit + j] : j;
-                    const float w = held ? a.c.weights[unit + j] : 0.f;
+                    const bool held = j < len && me.entry >= 0 && me.entry < a.c.n_pages;
+                    const int32_t kp = held ? me.pos : 0;
                     // does every row that counts admit every key of the warp, or none any?
                     const bool plain = __all_sync(0xffffffffu, !held || (kp <= lo && static_cast<uint32_t>(hi - kp) <= wide));
                     const bool none = __all_sync(0xffffffffu, !held || kp > hi || (kp < lo && static_cast<uint32_t>(lo - kp) > wide));
@@ -409,8 +426,8 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                         tc_fence_after();
                         const uint32_t td = tmem + b * kWHalf + lane_off;
                         const int n32 = min(kWHalf, rows - r0);
-                        // 32 columns at a time, the next ones on their way
-                        uint32_t v[2][32];
+                        // this thread's columns, 32 at a time
+                        const int c1 = min(n32, 64 * (second + 1));
                         auto add = [&](uint32_t (&x)[32], int cb) {
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
@@ -433,29 +450,26 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                                 sb = add2(sb, pair(__float_as_uint(p[2]), __float_as_uint(p[3])));
                             }
                         };
-                        if (!none) {
-                            tmem_ld32(td, v[0]);
-                            tmem_ld_wait();
-                            loaded(v[0]);
+                        if (!none)
 #pragma unroll 1
-                            for (int cb = 0;; cb += 64) {
-                                if (cb + 32 < n32) tmem_ld32(td + cb + 32, v[1]);
-                                add(v[0], cb);
-                                if (cb + 32 >= n32) break;
+                            for (int cb = 64 * second; cb < c1; cb += 32) {
+                                uint32_t v[32];
+                                tmem_ld32(td + cb, v);
                                 tmem_ld_wait();
-                                loaded(v[1]);
-                                if (cb + 64 < n32) tmem_ld32(td + cb + 64, v[0]);
-                                add(v[1], cb + 32);
-                                if (cb + 64 >= n32) break;
-                                tmem_ld_wait();
-                                loaded(v[0]);
+                                loaded(v);
+                                add(v, cb);
                             }
-                        }
                         tc_fence_before();
                         mbar_arrive(bar(wDEmpty + b));
                     }
                     const uint64_t sum2 = add2(add2(s2[0], s2[1]), add2(s2[2], s2[3]));
-                    if (held && ok) a.c.weights[unit + j] = w + (lo_of(sum2) + hi_of(sum2));
+                    float sum = lo_of(sum2) + hi_of(sum2);
+                    // the key's two threads: the second hands its sum to the first
+                    float* slot = reinterpret_cast<float*>(sm + C::kSum) + (grp * 2 + (tile_par & 1)) * kWKeys + key_lane;
+                    tile_par ^= 1;
+                    if (second) *slot = sum;
+                    named_sync(4 + grp * 4 + (warp & 3), 64);
+                    if (!second && held && ok) a.c.weights[unit + j] = me.w + (sum + *slot);
                 }
             }
             return true;
