@@ -457,6 +457,7 @@ sdpa_status_t sdpa_cache_evict(const sdpa_cache* c, const sdpa_cache_evict_param
     a.holes = at<int32_t>(ws, l.holes);
     a.tails = at<int32_t>(ws, l.tails);
     a.counts = at<int32_t>(ws, l.counts);
+    a.timeout_ns = kWaitLimitNs;
     return cuda_status(swa::launch_cache_evict(a, static_cast<cudaStream_t>(stream)), "cache evict launch");
 }
 
@@ -474,7 +475,7 @@ sdpa_status_t sdpa_cache_check_status(const sdpa_cache* c, void* stream)
     if (host == SDPA_ERR_BAD_LENGTHS)
         return fail(SDPA_ERR_BAD_LENGTHS, "a length, count or row index of the cache is out of its range");
     if (host == SDPA_ERR_BOUNDS) return fail(SDPA_ERR_BOUNDS, "a page-table entry is outside [0, n_pages)");
-    if (host == SDPA_ERR_TIMEOUT) return fail(SDPA_ERR_TIMEOUT, "a wait of the cache forward ran out on the device");
+    if (host == SDPA_ERR_TIMEOUT) return fail(SDPA_ERR_TIMEOUT, "a wait of a cache call ran out on the device");
     return fail(SDPA_ERR_CUDA, "unknown cache status %d", host);
 }
 

@@ -1,4 +1,6 @@
 // cache_kernels.cu -- append and evict on the paged cache.
+#include <cooperative_groups.h>
+
 #include "cache.cuh"
 #include "ptx.cuh"
 
@@ -130,6 +132,16 @@ cudaError_t launch_cache_append(const CacheAppendArgs& a0, cudaStream_t s)
 }
 
 // ---------------------------------------------------------------- evict
+//
+// A head's kept keys are the `keep` of the highest rank (protected ones above
+// every weight). A cluster of up to 16 CTAs takes a (sequence, kv-head): each
+// CTA reads its slice of weights and positions once and keeps the ranks in
+// shared memory; four passes of 8 bits find the keep-th largest rank, the CTAs'
+// histograms added through distributed shared memory; then each warp, in slot
+// order, lists the free slots below `keep` and the kept ones from there on. A
+// histogram has a column per lane (256 x 32 counters): lanes never meet on a
+// counter or a bank, whatever the weights. The second kernel moves the rows,
+// bound by reading and writing each moved row once.
 
 namespace {
 
@@ -143,127 +155,310 @@ __device__ __forceinline__ uint32_t evict_rank(const CacheEvictArgs& a, float w,
     return x & 0x80000000u ? ~x : x | 0x80000000u;
 }
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;      // two CTAs an SM
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr uint32_t kSelFixed = 256 * 32 * 4;       // the histogram; the ranks follow it
 
 }  // namespace
 
-// One CTA per (sequence, kv-head): the keep-th largest rank by four passes of
-// 8 bits, then the free slots below keep and the kept ones behind it, in order.
-__global__ void __launch_bounds__(kSelThreads) cache_evict_select_kernel(const CacheEvictArgs a)
+__global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(const __grid_constant__ CacheEvictArgs a)
 {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t sh_prefix, sh_need;
-    __shared__ uint32_t warp_cnt[3][32];
-    __shared__ uint32_t base[3];   // ties, holes, tails so far
-    const int64_t u = blockIdx.x, bi = u / a.c.h_kv;
+    namespace cg = cooperative_groups;
+    extern __shared__ uint32_t dyn32[];
+    uint32_t* hist = dyn32;
+    uint32_t* ranks = dyn32 + kSelFixed / 4;
+    __shared__ uint32_t tot[2][256];        // this CTA's histogram of a pass
+    __shared__ uint32_t mine[3];            // this CTA's ties, free slots, kept slots behind
+    __shared__ uint32_t per_warp[3][kSelWarps];
+    __shared__ uint32_t sums[256];          // all CTAs' histogram of a pass
+    __shared__ uint32_t digit, left, equal;
+    cg::cluster_group cl = cg::this_cluster();
+    const uint32_t cs = static_cast<uint32_t>(a.cluster), c = blockIdx.x % cs;
+    const int64_t u = blockIdx.x / cs, bi = u / a.c.h_kv;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     bool bad;
     const int32_t len = cache_length(a.c, bi, bad);
-    if (bad || len <= a.keep) {
-        if (tid == 0) a.counts[u] = -1;
+    if (bad || len <= a.keep) {             // (the whole cluster)
+        if (c == 0 && tid == 0) a.counts[u] = -1;
+        grid_dep_launch();
         return;
     }
+    const int32_t keep = static_cast<int32_t>(a.keep);
     const float* w = a.c.weights + u * a.c.cap;
     const int32_t* pos = a.c.positions + u * a.c.cap;
     const int64_t next = a.c.next_pos[bi];
-    uint32_t prefix = 0, need = static_cast<uint32_t>(a.keep);
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
+    // this CTA's slots [lo, hi), a multiple of 32 per warp
+    const int32_t slice = static_cast<int32_t>((((static_cast<int64_t>(len) + cs - 1) / cs) + kSelThreads - 1) / kSelThreads * kSelThreads);
+    const int32_t lo = static_cast<int32_t>(imin64(len, static_cast<int64_t>(c) * slice));
+    const int32_t hi = static_cast<int32_t>(imin64(len, static_cast<int64_t>(lo) + slice)), n = hi - lo;
+    const bool cached = slice <= a.slice_max;
+    auto rank_of = [&](int32_t i) -> uint32_t { return cached ? ranks[i] : evict_rank(a, w[lo + i], pos[lo + i], next); };
+    if (cached) {
+#pragma unroll 8
+        for (int32_t i = tid; i < n; i += kSelThreads) ranks[i] = evict_rank(a, w[lo + i], pos[lo + i], next);
+    }
+    uint32_t prefix = 0, need = static_cast<uint32_t>(keep);
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) hist[i * kSelThreads + tid] = 0;
         __syncthreads();
-        for (int32_t j = tid; j < len; j += kSelThreads) {
-            const uint32_t r = evict_rank(a, w[j], pos[j], next);
-            if (shift == 24 || (r >> (shift + 8)) == prefix) atomicAdd(&hist[(r >> shift) & 255], 1u);
+#pragma unroll 4
+        for (int32_t i = tid; i < n; i += kSelThreads) {
+            const uint32_t r = rank_of(i);
+            if (pass == 0 || (r >> (shift + 8)) == prefix) atomicAdd(&hist[((r >> shift) & 255) * 32 + lane], 1u);
         }
         __syncthreads();
-        if (tid == 0) {
-            uint32_t left = need;
-            int d = 255;
-            for (; d > 0 && hist[d] < left; --d) left -= hist[d];
-            sh_prefix = (prefix << 8) | static_cast<uint32_t>(d);
-            sh_need = left;
+        {
+            // two threads a bin, sixteen columns each (each bin from another bank on)
+            const int bin = tid >> 1, q = tid & 1;
+            uint32_t s = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s += hist[bin * 32 + ((q * 16 + i + bin) & 31)];
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            if (q == 0) tot[pass & 1][bin] = s;
+        }
+        // (a buffer is written again two passes on: every CTA has read it by the barrier between)
+        cl.sync();
+        if (tid < 256) {
+            uint32_t x = 0;
+#pragma unroll
+            for (uint32_t k = 0; k < 16; ++k)
+                if (k < cs) x += *cl.map_shared_rank(&tot[pass & 1][tid], k);
+            sums[tid] = x;
         }
         __syncthreads();
-        prefix = sh_prefix;
-        need = sh_need;
+        if (warp == 0) {
+            // lane l: bins 255 - 8l down to 248 - 8l
+            uint32_t b[8], s = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += b[i] = sums[255 - 8 * lane - i];
+            uint32_t incl = s;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += x;
+            }
+            // the first bin, from the top, by which `need` are reached (there are at least `need` in all)
+            uint32_t before = incl - s;
+            if (before < need ? need <= incl : need == 0 && lane == 0) {
+                uint32_t d = 255 - 8 * lane;
+#pragma unroll
+                for (int i = 0; i < 7; ++i)
+                    if (before + b[i] < need && d == 255u - 8 * lane - i) {
+                        before += b[i];
+                        --d;
+                    }
+                digit = d;
+                left = need - before;
+                equal = sums[d];
+            }
+        }
+        __syncthreads();
+        prefix = (prefix << 8) | digit;
+        need = left;
         __syncthreads();
     }
-    // ranks above `prefix` stay, and the first `need` that equal it
-    if (tid < 3) base[tid] = 0;
+    // Ranks above `prefix` stay, and the first `need` (in slot order) that equal it; where those are all, their
+    // order does not matter. Each warp looks after consecutive slots.
+    if (need == equal) need = 0xffffffffu;
+    const int32_t seg = slice / kSelWarps, i0 = warp * seg, i1 = min(n, i0 + seg);
+    const uint32_t below = (1u << lane) - 1;
+    // sum of what comes before this warp: earlier CTAs' counts, earlier warps'
+    auto before_me = [&](int what) -> uint32_t {
+        uint32_t s = lane < warp ? per_warp[what][lane] : 0;
+        if (lane < static_cast<int>(c)) s += *cl.map_shared_rank(&mine[what], lane);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
+    };
+    auto count = [&](int what, uint32_t v) {     // of this warp
+        if (lane == 0) per_warp[what][warp] = v;
+    };
+    auto total = [&](int what) {
+        if (warp == what) {
+            uint32_t s = lane < kSelWarps ? per_warp[what][lane] : 0;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane == 0) mine[what] = s;
+        }
+    };
+    uint32_t tie0 = 0;
+    if (need != 0xffffffffu) {              // (the same in every CTA of the cluster)
+        uint32_t ties = 0;
+        for (int32_t i = i0 + lane; i - lane < i1; i += 32)
+            ties += __popc(__ballot_sync(0xffffffffu, i < i1 && rank_of(i) == prefix));
+        count(0, ties);
+        __syncthreads();
+        total(0);
+        cl.sync();
+        tie0 = before_me(0);
+    }
+    // f(slot, free below keep, kept behind it) in slot order, whole warps
+    auto walk = [&](auto f) {
+        uint32_t t = tie0;
+        for (int32_t i = i0 + lane; i - lane < i1; i += 32) {
+            const bool in = i < i1;
+            const uint32_t r = in ? rank_of(i) : 0;
+            const uint32_t bt = __ballot_sync(0xffffffffu, in && r == prefix);
+            const bool kept = in && (r > prefix || (r == prefix && t + __popc(bt & below) < need));
+            t += __popc(bt);
+            const int32_t j = lo + i;
+            f(j, __ballot_sync(0xffffffffu, in && !kept && j < keep), __ballot_sync(0xffffffffu, kept && j >= keep));
+        }
+    };
+    uint32_t holes = 0, tails = 0;
+    walk([&](int32_t, uint32_t h, uint32_t t) {
+        holes += __popc(h);
+        tails += __popc(t);
+    });
+    count(1, holes);
+    count(2, tails);
     __syncthreads();
-    for (int32_t j0 = 0; j0 < len; j0 += kSelThreads) {
-        const int32_t j = j0 + tid;
-        const uint32_t r = j < len ? evict_rank(a, w[j], pos[j], next) : 0;
-        const bool tie = j < len && r == prefix;
-        const uint32_t below = (1u << lane) - 1;
-        const uint32_t bt = __ballot_sync(0xffffffffu, tie);
-        if (lane == 0) warp_cnt[0][warp] = __popc(bt);
-        __syncthreads();
-        uint32_t before = base[0];
-        for (int i = 0; i < warp; ++i) before += warp_cnt[0][i];
-        const bool kept = j < len && (r > prefix || (tie && before + __popc(bt & below) < need));
-        const bool hole = j < len && !kept && j < a.keep, tail = kept && j >= a.keep;
-        const uint32_t bh = __ballot_sync(0xffffffffu, hole), bl = __ballot_sync(0xffffffffu, tail);
-        if (lane == 0) {
-            warp_cnt[1][warp] = __popc(bh);
-            warp_cnt[2][warp] = __popc(bl);
-        }
-        __syncthreads();
-        uint32_t hb = base[1], lb = base[2];
-        for (int i = 0; i < warp; ++i) {
-            hb += warp_cnt[1][i];
-            lb += warp_cnt[2][i];
-        }
-        if (hole) a.holes[u * a.m + hb + __popc(bh & below)] = j;
-        if (tail) a.tails[u * a.m + lb + __popc(bl & below)] = j;
-        __syncthreads();
-        if (tid < 3)
-            for (int i = 0; i < 32; ++i) base[tid] += warp_cnt[tid][i];
-        __syncthreads();
-    }
-    if (tid == 0) a.counts[u] = static_cast<int32_t>(base[1]);
+    total(1);
+    total(2);
+    cl.sync();
+    uint32_t h0 = before_me(1), t0 = before_me(2);
+    if (c == cs - 1 && warp == kSelWarps - 1 && lane == 0) a.counts[u] = static_cast<int32_t>(h0 + holes);
+    walk([&](int32_t j, uint32_t h, uint32_t t) {
+        if ((h >> lane) & 1) a.holes[u * a.m + h0 + __popc(h & below)] = j;
+        if ((t >> lane) & 1) a.tails[u * a.m + t0 + __popc(t & below)] = j;
+        h0 += __popc(h);
+        t0 += __popc(t);
+    });
+    grid_dep_launch();
+    cl.sync();      // no CTA ends while another reads its counts
 }
 
+// Moves kept rows into free slots: a lane looks after a row (K and V of 64
+// features) or half of one (K or V of 128), one bulk copy into shared memory
+// and one out of it; a warp's 8 KB of rows come in while the 8 KB before go out.
 template <int HD>
-__global__ void __launch_bounds__(256) cache_evict_move_kernel(const CacheEvictArgs a)
+__global__ void __launch_bounds__(128) cache_evict_move_kernel(const __grid_constant__ CacheEvictArgs a)
 {
-    constexpr uint32_t C = HD / 8;
+    constexpr int GP = HD == 64 ? 32 : 16;             // rows of a warp's round
+    constexpr uint32_t RB = HD * 2;                    // bytes of a row of K or V
+    extern __shared__ __align__(128) uint8_t dyn8[];   // [warp][2 rounds][8 KB]
+    __shared__ __align__(8) uint64_t bars[4][2];
     const int64_t u = blockIdx.x, bi = u / a.c.h_kv, g = u - bi * a.c.h_kv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x < 8) mbar_init(smem_u32(&bars[0][0]) + threadIdx.x * 8, 1);
+    fence_mbar_init();
+    __syncthreads();
+    grid_dep_wait();
     const int32_t n = a.counts[u];
     if (n < 0) return;
     if (blockIdx.y == 0 && g == 0 && threadIdx.x == 0) a.c.lengths[bi] = static_cast<int32_t>(a.keep);
-    for (int64_t x = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x; x < static_cast<int64_t>(n) * C;
-         x += static_cast<int64_t>(gridDim.y) * blockDim.x) {
-        const uint32_t c = static_cast<uint32_t>(x % C);
-        const int64_t i = x / C;
-        const uint32_t dst = a.holes[u * a.m + i], src = a.tails[u * a.m + i];
-        if (c == 0) {
-            a.c.positions[u * a.c.cap + dst] = a.c.positions[u * a.c.cap + src];
-            a.c.weights[u * a.c.cap + dst] = a.c.weights[u * a.c.cap + src];
+    const int64_t step = static_cast<int64_t>(gridDim.y) * 4 * GP;
+    int64_t i0 = (static_cast<int64_t>(blockIdx.y) * 4 + warp) * GP;
+    const uint32_t ring = smem_u32(dyn8) + warp * 16384;
+    // this lane's part of the rounds on their way: where it goes
+    uint16_t *kd[2] = {nullptr, nullptr}, *vd[2] = {nullptr, nullptr};
+    auto send = [&](int r, int64_t first) {
+        const int64_t i = first + lane % GP;
+        bool ok = i < n;
+        const uint16_t *ks = nullptr, *vs = nullptr;
+        if (ok) {
+            const uint32_t dst = a.holes[u * a.m + i], src = a.tails[u * a.m + i];
+            if (lane < GP) {
+                a.c.positions[u * a.c.cap + dst] = a.c.positions[u * a.c.cap + src];
+                a.c.weights[u * a.c.cap + dst] = a.c.weights[u * a.c.cap + src];
+            }
+            uint32_t sr, dr;
+            const int64_t sp = cache_page(a.c, bi, src, sr), dp = cache_page(a.c, bi, dst, dr);
+            ok = sp >= 0 && dp >= 0;
+            ks = a.c.k + sp * a.c.k_stride[0] + sr * a.c.k_stride[1] + g * a.c.k_stride[2];
+            vs = a.c.v + sp * a.c.v_stride[0] + sr * a.c.v_stride[1] + g * a.c.v_stride[2];
+            kd[r] = a.c.k + dp * a.c.k_stride[0] + dr * a.c.k_stride[1] + g * a.c.k_stride[2];
+            vd[r] = a.c.v + dp * a.c.v_stride[0] + dr * a.c.v_stride[1] + g * a.c.v_stride[2];
         }
-        uint32_t sr, dr;
-        const int64_t sp = cache_page(a.c, bi, src, sr), dp = cache_page(a.c, bi, dst, dr);
-        if (sp < 0 || dp < 0) continue;
-        *reinterpret_cast<uint4*>(a.c.k + dp * a.c.k_stride[0] + dr * a.c.k_stride[1] + g * a.c.k_stride[2] + c * 8) =
-            *reinterpret_cast<const uint4*>(a.c.k + sp * a.c.k_stride[0] + sr * a.c.k_stride[1] +
-                                            g * a.c.k_stride[2] + c * 8);
-        *reinterpret_cast<uint4*>(a.c.v + dp * a.c.v_stride[0] + dr * a.c.v_stride[1] + g * a.c.v_stride[2] + c * 8) =
-            *reinterpret_cast<const uint4*>(a.c.v + sp * a.c.v_stride[0] + sr * a.c.v_stride[1] +
-                                            g * a.c.v_stride[2] + c * 8);
+        // 64 features: K and V by each lane; 128: K by the lower lanes, V by the upper
+        const bool k_mine = ok && (HD == 64 || lane < 16), v_mine = ok && (HD == 64 || lane >= 16);
+        if (!k_mine) kd[r] = nullptr;
+        if (!v_mine) vd[r] = nullptr;
+        const uint32_t bar = smem_u32(&bars[warp][r]);
+        const uint32_t copies = __popc(__ballot_sync(0xffffffffu, k_mine)) + __popc(__ballot_sync(0xffffffffu, v_mine));
+        if (lane == 0) mbar_arrive_expect_tx(bar, copies * RB);
+        __syncwarp();
+        const uint32_t at = ring + r * 8192 + (lane % GP) * RB;
+        if (k_mine) bulk_load(at, ks, RB, bar);
+        if (v_mine) bulk_load(at + 4096, vs, RB, bar);
+    };
+    auto store = [&](uint16_t* dst, uint32_t src) {
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(RB) : "memory");
+    };
+    uint32_t par[2] = {0u, 0u};
+    if (i0 < n) send(0, i0);
+    int r = 0;
+    for (; i0 < n; i0 += step, r ^= 1) {
+        // the other half's rows have left it: the next round may come in
+        bulk_wait_read0();
+        __syncwarp();
+        if (i0 + step < n) send(r ^ 1, i0 + step);
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[warp][r]), par[r], a.timeout_ns))) {
+            set_status(a.c.status, SDPA_ERR_TIMEOUT);
+            if (i0 + step < n) mbar_wait(smem_u32(&bars[warp][r ^ 1]), par[r ^ 1], a.timeout_ns);
+            break;
+        }
+        par[r] ^= 1;
+        const uint32_t at = ring + r * 8192 + (lane % GP) * RB;
+        fence_proxy_async_smem();
+        if (kd[r] != nullptr) store(kd[r], at);
+        if (vd[r] != nullptr) store(vd[r], at + 4096);
+        bulk_commit();
     }
+    bulk_wait0();
 }
 
-cudaError_t launch_cache_evict(const CacheEvictArgs& a, cudaStream_t s)
+cudaError_t launch_cache_evict(const CacheEvictArgs& a0, cudaStream_t s)
 {
+    CacheEvictArgs a = a0;
     const int64_t units = a.c.b * a.c.h_kv;
     if (units == 0 || a.c.cap <= a.keep) return cudaSuccess;
-    cache_evict_select_kernel<<<static_cast<unsigned>(units), kSelThreads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    // CTAs per head: as many as two per SM allow, with 2048 slots each at least
+    a.cluster = 1;
+    while (a.cluster < 16 && units * a.cluster * 2 <= 304 && a.c.cap / (a.cluster * 2) >= 2048) a.cluster *= 2;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e;
+    for (;; a.cluster = 8) {
+        // a slice's ranks are kept as far as shared memory goes; a longer one's are computed in each pass
+        const int64_t most = (a.c.cap + a.cluster - 1) / a.cluster + kSelThreads;
+        a.slice_max = static_cast<int32_t>(imin64(most, (200 * 1024 - kSelFixed) / 4));
+        cfg.dynamicSmemBytes = kSelFixed + static_cast<uint32_t>(a.slice_max) * 4;
+        cfg.gridDim = dim3(static_cast<unsigned>(units * a.cluster));
+        attr[0].val.clusterDim.x = a.cluster;
+        e = cudaFuncSetAttribute(cache_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(cfg.dynamicSmemBytes));
+        if (e != cudaSuccess) return e;
+        if (a.cluster < 16) break;
+        // 16 CTAs of a cluster are not promised by every partition of a GPU
+        e = cudaFuncSetAttribute(cache_evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        int fit = 0;
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, cache_evict_select_kernel, &cfg);
+        if (e == cudaSuccess && fit > 0) break;
+        cudaGetLastError();
+    }
+    if ((e = cudaLaunchKernelEx(&cfg, cache_evict_select_kernel, a)) != cudaSuccess) return e;
+    const int64_t rows = a.c.d == 64 ? 128 : 64;      // of a CTA's round
+    cfg.gridDim = dim3(static_cast<unsigned>(units),
+                       static_cast<unsigned>(imax64(1, imin64((a.m + rows - 1) / rows, 152 * 3 / units))));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 65536;
+    e = a.c.d == 64 ? cudaFuncSetAttribute(cache_evict_move_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536)
+                    : cudaFuncSetAttribute(cache_evict_move_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(units),
-                    static_cast<unsigned>(imax64(1, imin64((a.m * (a.c.d / 8) + 255) / 256, 256))));
-    if (a.c.d == 64) cache_evict_move_kernel<64><<<grid, 256, 0, s>>>(a);
-    else cache_evict_move_kernel<128><<<grid, 256, 0, s>>>(a);
-    return cudaGetLastError();
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    return a.c.d == 64 ? cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<64>, a)
+                       : cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<128>, a);
 }
 
 }  // namespace swa
