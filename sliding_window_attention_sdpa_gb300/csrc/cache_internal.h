@@ -104,7 +104,7 @@ struct CacheEvictArgs {
     int32_t *holes, *tails;  // [b * h_kv][m] free slots below keep, kept slots from keep on
     int32_t* counts;       // [b * h_kv] rows to move; -1: the sequence is not touched
     int64_t timeout_ns;
-    int32_t cluster, slice_max;   // CTAs per head, slots of a CTA whose ranks it keeps (set by the launcher)
+    int32_t cluster;       // CTAs per head (set by the launcher)
 };
 
 cudaError_t launch_cache_fwd(const CacheTileArgs& a, int dtype, cudaStream_t s);

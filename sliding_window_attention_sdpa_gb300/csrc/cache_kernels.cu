@@ -161,10 +161,12 @@ constexpr uint32_t kSelFixed = 256 * 32 * 4;       // the histogram; the ranks f
 
 }  // namespace
 
+// CACHED: a slice's ranks fit shared memory; else each pass computes them.
+template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(const __grid_constant__ CacheEvictArgs a)
 {
     namespace cg = cooperative_groups;
-    extern __shared__ uint32_t dyn32[];
+    extern __shared__ __align__(16) uint32_t dyn32[];
     uint32_t* hist = dyn32;
     uint32_t* ranks = dyn32 + kSelFixed / 4;
     __shared__ uint32_t tot[2][256];        // this CTA's histogram of a pass
@@ -191,9 +193,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
     const int32_t slice = static_cast<int32_t>((((static_cast<int64_t>(len) + cs - 1) / cs) + kSelThreads - 1) / kSelThreads * kSelThreads);
     const int32_t lo = static_cast<int32_t>(imin64(len, static_cast<int64_t>(c) * slice));
     const int32_t hi = static_cast<int32_t>(imin64(len, static_cast<int64_t>(lo) + slice)), n = hi - lo;
-    const bool cached = slice <= a.slice_max;
-    auto rank_of = [&](int32_t i) -> uint32_t { return cached ? ranks[i] : evict_rank(a, w[lo + i], pos[lo + i], next); };
-    if (cached) {
+    auto rank_of = [&](int32_t i) -> uint32_t {
+        if constexpr (CACHED) return ranks[i];
+        return evict_rank(a, w[lo + i], pos[lo + i], next);
+    };
+    if constexpr (CACHED) {
 #pragma unroll 8
         for (int32_t i = tid; i < n; i += kSelThreads) ranks[i] = evict_rank(a, w[lo + i], pos[lo + i], next);
     }
@@ -204,10 +208,21 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
 #pragma unroll
         for (int i = 0; i < 16; ++i) hist[i * kSelThreads + tid] = 0;
         __syncthreads();
-#pragma unroll 4
-        for (int32_t i = tid; i < n; i += kSelThreads) {
-            const uint32_t r = rank_of(i);
+        auto put = [&](uint32_t r) {
             if (pass == 0 || (r >> (shift + 8)) == prefix) atomicAdd(&hist[((r >> shift) & 255) * 32 + lane], 1u);
+        };
+        if constexpr (CACHED) {
+#pragma unroll 2
+            for (int32_t i = tid * 4; i < n; i += kSelThreads * 4) {
+                const uint4 r = *reinterpret_cast<const uint4*>(ranks + i);      // (the room is a multiple of 4)
+                put(r.x);
+                if (i + 1 < n) put(r.y);
+                if (i + 2 < n) put(r.z);
+                if (i + 3 < n) put(r.w);
+            }
+        } else {
+#pragma unroll 4
+            for (int32_t i = tid; i < n; i += kSelThreads) put(rank_of(i));
         }
         __syncthreads();
         {
@@ -298,14 +313,20 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
     // f(slot, free below keep, kept behind it) in slot order, whole warps
     auto walk = [&](auto f) {
         uint32_t t = tie0;
-        for (int32_t i = i0 + lane; i - lane < i1; i += 32) {
-            const bool in = i < i1;
-            const uint32_t r = in ? rank_of(i) : 0;
-            const uint32_t bt = __ballot_sync(0xffffffffu, in && r == prefix);
-            const bool kept = in && (r > prefix || (r == prefix && t + __popc(bt & below) < need));
-            t += __popc(bt);
-            const int32_t j = lo + i;
-            f(j, __ballot_sync(0xffffffffu, in && !kept && j < keep), __ballot_sync(0xffffffffu, kept && j >= keep));
+        for (int32_t i = i0 + lane; i - lane < i1; i += 128) {
+            uint32_t rs[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) rs[q] = i + 32 * q < i1 ? rank_of(i + 32 * q) : 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const bool in = i + 32 * q < i1;
+                const uint32_t r = rs[q];
+                const uint32_t bt = __ballot_sync(0xffffffffu, in && r == prefix);
+                const bool kept = in && (r > prefix || (r == prefix && t + __popc(bt & below) < need));
+                t += __popc(bt);
+                const int32_t j = lo + i + 32 * q;
+                f(j, __ballot_sync(0xffffffffu, in && !kept && j < keep), __ballot_sync(0xffffffffu, kept && j >= keep));
+            }
         }
     };
     uint32_t holes = 0, tails = 0;
@@ -428,25 +449,27 @@ cudaError_t launch_cache_evict(const CacheEvictArgs& a0, cudaStream_t s)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t e;
+    void (*select)(CacheEvictArgs);
     for (;; a.cluster = 8) {
         // a slice's ranks are kept as far as shared memory goes; a longer one's are computed in each pass
         const int64_t most = (a.c.cap + a.cluster - 1) / a.cluster + kSelThreads;
-        a.slice_max = static_cast<int32_t>(imin64(most, (200 * 1024 - kSelFixed) / 4));
-        cfg.dynamicSmemBytes = kSelFixed + static_cast<uint32_t>(a.slice_max) * 4;
+        const bool cached = most <= (200 * 1024 - kSelFixed) / 4;
+        select = cached ? cache_evict_select_kernel<true> : cache_evict_select_kernel<false>;
+        cfg.dynamicSmemBytes = kSelFixed + (cached ? static_cast<uint32_t>((most + 3) / 4 * 16) : 0u);
         cfg.gridDim = dim3(static_cast<unsigned>(units * a.cluster));
         attr[0].val.clusterDim.x = a.cluster;
-        e = cudaFuncSetAttribute(cache_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(cfg.dynamicSmemBytes));
         if (e != cudaSuccess) return e;
         if (a.cluster < 16) break;
         // 16 CTAs of a cluster are not promised by every partition of a GPU
-        e = cudaFuncSetAttribute(cache_evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         int fit = 0;
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, cache_evict_select_kernel, &cfg);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, select, &cfg);
         if (e == cudaSuccess && fit > 0) break;
         cudaGetLastError();
     }
-    if ((e = cudaLaunchKernelEx(&cfg, cache_evict_select_kernel, a)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, select, a)) != cudaSuccess) return e;
     const int64_t rows = a.c.d == 64 ? 128 : 64;      // of a CTA's round
     cfg.gridDim = dim3(static_cast<unsigned>(units),
                        static_cast<unsigned>(imax64(1, imin64((a.m + rows - 1) / rows, 152 * 3 / units))));
