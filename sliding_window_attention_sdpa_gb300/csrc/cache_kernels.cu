@@ -149,10 +149,10 @@ namespace {
 // above every weight, NaN above every number; -0 counts as 0.
 __device__ __forceinline__ uint32_t evict_rank(const CacheEvictArgs& a, float w, int64_t pos, int64_t next)
 {
-    if (pos < a.first || pos >= next - a.recent) return 0xffffffffu;
-    if (w != w) return 0xfffffffeu;
-    const uint32_t x = __float_as_uint(w + 0.f);
-    return x & 0x80000000u ? ~x : x | 0x80000000u;
+    // (no branches: the loads of several keys are on their way at once)
+    const uint32_t x = __float_as_uint(w + 0.f), flip = static_cast<uint32_t>(static_cast<int32_t>(x) >> 31) | 0x80000000u;
+    const uint32_t r = w != w ? 0xfffffffeu : x ^ flip;
+    return (pos < a.first) | (pos >= next - a.recent) ? 0xffffffffu : r;
 }
 
 constexpr int kSelThreads = 512;      // two CTAs an SM
@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
         cl.sync();
         tie0 = before_me(0);
     }
-    // f(slot, free below keep, kept behind it) in slot order, whole warps
+    // f(slot, free below keep, kept behind it) in slot order, whole warps; a warp's slots mostly lie on one side of
+    // `keep`
     auto walk = [&](auto f) {
         uint32_t t = tie0;
         for (int32_t i = i0 + lane; i - lane < i1; i += 128) {
@@ -321,11 +322,15 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
             for (int q = 0; q < 4; ++q) {
                 const bool in = i + 32 * q < i1;
                 const uint32_t r = rs[q];
-                const uint32_t bt = __ballot_sync(0xffffffffu, in && r == prefix);
-                const bool kept = in && (r > prefix || (r == prefix && t + __popc(bt & below) < need));
-                t += __popc(bt);
-                const int32_t j = lo + i + 32 * q;
-                f(j, __ballot_sync(0xffffffffu, in && !kept && j < keep), __ballot_sync(0xffffffffu, kept && j >= keep));
+                bool kept = in && r >= prefix;
+                if (need != 0xffffffffu) {
+                    const uint32_t bt = __ballot_sync(0xffffffffu, in && r == prefix);
+                    kept = in && (r > prefix || (r == prefix && t + __popc(bt & below) < need));
+                    t += __popc(bt);
+                }
+                const int32_t j = lo + i + 32 * q, j0 = j - lane;
+                f(j, j0 < keep ? __ballot_sync(0xffffffffu, in && !kept && j < keep) : 0u,
+                  j0 + 31 >= keep ? __ballot_sync(0xffffffffu, kept && j >= keep) : 0u);
             }
         }
     };
