@@ -10,16 +10,21 @@
 // groups of warps sums one while its other one is computed.
 //
 // Few rows: bound by reading K once (a 4-stage ring of 128 keys by TMA). Many
-// rows: by the exponentials (one per key and row).
+// rows: by the exponentials (one per key and row): 93 us at 12 sequences of
+// 16484 keys, 6 kv-heads and 256 rows in bf16, d = 128. The loop over columns
+// exists twice, with and without the mask (102 us with one loop that asked per
+// 32 columns), and is not unrolled: both stay within the registers.
 //
 // Roles (640 threads): warp 0 loads K; warp 1 issues the MMAs; warps 4-11 and
 // 12-19 sum every other key tile each, two threads a key (64 of an
-// accumulator's columns each; 8 warps instead of 16 left the SM waiting on
-// latencies: 116 us against 102 at 12 sequences of 16484 keys, 6 kv-heads, 256 rows), and
+// accumulator's columns each; with one, 8 warps left the SM waiting on
+// latencies: 116 us against 102 then), and
 // put the rows (Q, LSE, positions) in place, 256 at a time; more rows take
 // another round over the part's keys.
 // The key tiles of all (sequence, kv-head) units form one line that the CTAs
 // cut evenly. Every wait is bounded (SDPA_ERR_TIMEOUT in the cache's status).
+#include <type_traits>
+
 #include "cache_fwd.cuh"
 
 namespace swa {
@@ -428,37 +433,38 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                         const int n32 = min(kWHalf, rows - r0);
                         // this thread's columns, 32 at a time
                         const int c1 = min(n32, 64 * (second + 1));
-                        auto add = [&](uint32_t (&x)[32], int cb) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(cst + r0 + cb + e);
-                                const uint64_t y0 = fma2(pair(x[e], x[e + 1]), scale2, c.x);
-                                const uint64_t y1 = fma2(pair(x[e + 2], x[e + 3]), scale2, c.y);
-                                float p[4] = {ex2_approx(lo_of(y0)), ex2_approx(hi_of(y0)), ex2_approx(lo_of(y1)),
-                                              ex2_approx(hi_of(y1))};
-                                if (!plain) {
-                                    // (a row that does not count is at -1: below every key)
-                                    const int4 at = *reinterpret_cast<const int4*>(qpos + r0 + cb + e);
-                                    if (static_cast<uint32_t>(at.x - kp) > wide) p[0] = 0.f;
-                                    if (static_cast<uint32_t>(at.y - kp) > wide) p[1] = 0.f;
-                                    if (static_cast<uint32_t>(at.z - kp) > wide) p[2] = 0.f;
-                                    if (static_cast<uint32_t>(at.w - kp) > wide) p[3] = 0.f;
-                                }
-                                uint64_t& sa = s2[(e >> 1) & 2];
-                                uint64_t& sb = s2[((e >> 1) & 2) + 1];
-                                sa = add2(sa, pair(__float_as_uint(p[0]), __float_as_uint(p[1])));
-                                sb = add2(sb, pair(__float_as_uint(p[2]), __float_as_uint(p[3])));
-                            }
-                        };
-                        if (!none)
+                        auto columns = [&](auto masked) {
+                            constexpr bool M = decltype(masked)::value;
 #pragma unroll 1
                             for (int cb = 64 * second; cb < c1; cb += 32) {
-                                uint32_t v[32];
-                                tmem_ld32(td + cb, v);
+                                uint32_t x[32];
+                                tmem_ld32(td + cb, x);
                                 tmem_ld_wait();
-                                loaded(v);
-                                add(v, cb);
+                                loaded(x);
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4) {
+                                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(cst + r0 + cb + e);
+                                    const uint64_t y0 = fma2(pair(x[e], x[e + 1]), scale2, c.x);
+                                    const uint64_t y1 = fma2(pair(x[e + 2], x[e + 3]), scale2, c.y);
+                                    float p0 = ex2_approx(lo_of(y0)), p1 = ex2_approx(hi_of(y0));
+                                    float p2 = ex2_approx(lo_of(y1)), p3 = ex2_approx(hi_of(y1));
+                                    if constexpr (M) {
+                                        // (a row that does not count is at -1: below every key)
+                                        const int4 at = *reinterpret_cast<const int4*>(qpos + r0 + cb + e);
+                                        p0 = static_cast<uint32_t>(at.x - kp) > wide ? 0.f : p0;
+                                        p1 = static_cast<uint32_t>(at.y - kp) > wide ? 0.f : p1;
+                                        p2 = static_cast<uint32_t>(at.z - kp) > wide ? 0.f : p2;
+                                        p3 = static_cast<uint32_t>(at.w - kp) > wide ? 0.f : p3;
+                                    }
+                                    uint64_t& sa = s2[(e >> 1) & 2];
+                                    uint64_t& sb = s2[((e >> 1) & 2) + 1];
+                                    sa = add2(sa, pair(__float_as_uint(p0), __float_as_uint(p1)));
+                                    sb = add2(sb, pair(__float_as_uint(p2), __float_as_uint(p3)));
+                                }
                             }
+                        };
+                        if (plain) columns(std::false_type{});
+                        else if (!none) columns(std::true_type{});
                         tc_fence_before();
                         mbar_arrive(bar(wDEmpty + b));
                     }
