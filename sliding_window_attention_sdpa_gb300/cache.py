@@ -260,6 +260,12 @@ class KVCache:
         self._ref, self._key, self._index = ctypes.addressof(c), (b, h_kv, d, dev, k.dtype), dev.index or 0
         self._ws_bytes = {}     # workspace bytes of the calls made so far, by their sizes
 
+    def __setattr__(self, name, value):
+        # the calls use the addresses taken by the constructor: another tensor under the name would not be seen
+        if "_ws_bytes" in self.__dict__:
+            raise AttributeError(f"{name}: a cache's tensors are changed in place (or make another KVCache)")
+        super().__setattr__(name, value)
+
     @classmethod
     def empty(cls, b: int, h_kv: int, d: int, max_len: int, *, dtype, device, page_size: int = 64,
               track: bool = False) -> "KVCache":
@@ -298,6 +304,8 @@ def _workspace(cache, key, size, workspace, c):
             from . import SDPA_ERR_INVALID_ARG, SdpaError, last_error
             if last_error():
                 raise SdpaError(SDPA_ERR_INVALID_ARG, f"sdpa_cache_{key[0]}_workspace_bytes", last_error())
+        if len(cache._ws_bytes) >= 256:
+            cache._ws_bytes.clear()
         cache._ws_bytes[key] = n
     return c.empty(n, dtype=c.uint8, device=cache.device) if n else None
 
@@ -375,11 +383,11 @@ def cache_append(cache: KVCache, k, v, *, index=None, counts=None, offsets=None,
         if index.dim() != 2:
             raise ValueError("index: expected [b, n]")
         n = index.shape[1]
+        if n == 0:
+            s = 0       # no row of any sequence (and no address of an empty index)
     p = _APPEND.pack(layout, 0, s, n, total, k.data_ptr(), v.data_ptr(), *sk, *sv,
                      _flat("index", index, (b, n), dev, c.int32), _flat("counts", counts, (b,), dev, c.int32),
                      _flat("offsets", offsets, (b + 1,), dev, c.int32))
-    if index is not None and n == 0:
-        return      # no row of any sequence
     _check(c.append(cache._ref, p, c.stream(cache._index)), "sdpa_cache_append")
     if check_status:
         cache.check_status()

@@ -21,6 +21,10 @@ constexpr int64_t kWaitLimitNs = 2000000000LL;
 constexpr int64_t kMax31 = int64_t(1) << 31;
 // a sequence's keys, rounded up to tiles, are numbered in 32 bits
 constexpr int64_t kMaxCap = kMax31 - (int64_t(1) << 16);
+// rows of a call, in 32 bits up to the next multiple of a block of rows
+constexpr int64_t kMaxRows = kMax31 - 1024;
+// 16-byte pieces of an append's CTA (32769 rows at most), in 32 bits
+constexpr int64_t kMaxHeads = 4096;
 
 void copy3(int64_t* dst, const int64_t* src) { memcpy(dst, src, 3 * sizeof(int64_t)); }
 
@@ -60,9 +64,9 @@ sdpa_status_t check_cache(const sdpa_cache* c)
     if (c->page_size >= kMax31 || c->max_pages >= kMax31 || c->page_size * c->max_pages > kMaxCap)
         return fail(SDPA_ERR_UNSUPPORTED, "cache capacity max_pages * page_size = %lld * %lld: at most 2^31 - 2^16 keys",
                     (long long)c->max_pages, (long long)c->page_size);
-    if (c->b >= kMax31 || c->h_kv >= kMax31 || c->b * c->h_kv >= kMax31)
-        return fail(SDPA_ERR_UNSUPPORTED, "cache b * h_kv = %lld * %lld: at most 2^31 - 1", (long long)c->b,
-                    (long long)c->h_kv);
+    if (c->h_kv > kMaxHeads || c->b >= kMax31 || c->b * c->h_kv >= kMax31)
+        return fail(SDPA_ERR_UNSUPPORTED, "cache b * h_kv = %lld * %lld: at most 2^31 - 1, h_kv at most 4096",
+                    (long long)c->b, (long long)c->h_kv);
     if (holds_keys(c) && c->page_table == nullptr && (c->max_pages != 1 || c->n_pages < c->b))
         return fail(SDPA_ERR_INVALID_ARG,
                     "cache without a page_table: max_pages=%lld n_pages=%lld (need one page per sequence)",
@@ -143,8 +147,8 @@ sdpa_status_t check_rows(const sdpa_cache* c, int64_t s_q, int64_t h_q, int64_t 
     if (h_q <= 0 || h_q % c->h_kv != 0)
         return fail(SDPA_ERR_INVALID_ARG, "h_q=%lld is not a positive multiple of h_kv=%lld", (long long)h_q,
                     (long long)c->h_kv);
-    if (h_q >= kMax31 || s_q >= kMax31 || c->b * s_q >= kMax31 || c->b * s_q * h_q >= kMax31)
-        return fail(SDPA_ERR_UNSUPPORTED, "b * s_q * h_q = %lld * %lld * %lld rows: at most 2^31 - 1", (long long)c->b,
+    if (h_q > kMaxRows || s_q > kMaxRows || s_q * h_q > kMaxRows || c->b * s_q * h_q > kMaxRows)
+        return fail(SDPA_ERR_UNSUPPORTED, "b * s_q * h_q = %lld * %lld * %lld rows: at most 2^31 - 1024", (long long)c->b,
                     (long long)s_q, (long long)h_q);
     if (window_left < -1)
         return fail(SDPA_ERR_INVALID_ARG, "window_left=%lld: must be >= -1", (long long)window_left);
@@ -253,6 +257,8 @@ sdpa_status_t check_evict(const sdpa_cache* c, const sdpa_cache_evict_params* p)
         return fail(SDPA_ERR_INVALID_ARG,
                     "keep=%lld first=%lld recent=%lld: need keep >= first + recent, all >= 0, keep < 2^31",
                     (long long)p->keep, (long long)p->first, (long long)p->recent);
+    if (double(c->b) * double(c->h_kv) * double(c->page_size * c->max_pages) >= double(int64_t(1) << 50))
+        return fail(SDPA_ERR_UNSUPPORTED, "evict: b * h_kv * capacity passes 2^50");
     return SDPA_OK;
 }
 
@@ -367,6 +373,7 @@ sdpa_status_t sdpa_cache_append(const sdpa_cache* c, const sdpa_cache_append_par
     int dev = 0;
     if ((st = current_device(&dev)) != SDPA_OK) return st;
     const bool thd = p->layout == SDPA_THD;
+    // (without rows to take, counts and offsets are still looked at)
     const bool rows = c->b > 0 && p->s > 0 && (thd ? p->total > 0 : true) && (p->index == nullptr || p->n > 0);
     const Ptr ptrs[] = {{"k", p->k, rows, 16},
                         {"v", p->v, rows, 16},
@@ -374,7 +381,7 @@ sdpa_status_t sdpa_cache_append(const sdpa_cache* c, const sdpa_cache_append_par
                         {"counts", p->counts, false, 4},
                         {"offsets", p->offsets, thd, 4}};
     if ((st = check_cache_ptrs(c, dev)) != SDPA_OK || (st = check_ptrs(ptrs, dev)) != SDPA_OK) return st;
-    if (!rows) return SDPA_OK;
+    if (c->b == 0 || (!rows && !thd && p->counts == nullptr && (p->index == nullptr || p->n == 0))) return SDPA_OK;
     swa::CacheAppendArgs a{};
     a.c = view_of(c);
     a.thd = thd ? 1 : 0;
@@ -471,7 +478,10 @@ sdpa_status_t sdpa_cache_check_status(const sdpa_cache* c, void* stream)
     if ((st = cuda_status(cudaMemcpy(&host, c->status, sizeof(host), cudaMemcpyDeviceToHost), "status read")) != SDPA_OK)
         return st;
     if (host == 0) return SDPA_OK;
-    if ((st = cuda_status(cudaMemset(c->status, 0, sizeof(int32_t)), "status reset")) != SDPA_OK) return st;
+    // (on the stream: ordered before the calls that follow)
+    if ((st = cuda_status(cudaMemsetAsync(c->status, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)),
+                          "status reset")) != SDPA_OK)
+        return st;
     if (host == SDPA_ERR_BAD_LENGTHS)
         return fail(SDPA_ERR_BAD_LENGTHS, "a length, count or row index of the cache is out of its range");
     if (host == SDPA_ERR_BOUNDS) return fail(SDPA_ERR_BOUNDS, "a page-table entry is outside [0, n_pages)");

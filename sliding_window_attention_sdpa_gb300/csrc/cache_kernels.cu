@@ -122,9 +122,10 @@ cudaError_t launch_cache_append(const CacheAppendArgs& a0, cudaStream_t s)
 {
     CacheAppendArgs a = a0;
     const int64_t most = a.index ? a.n : a.s;
-    if (a.c.b == 0 || most == 0) return cudaSuccess;
+    if (a.c.b == 0) return cudaSuccess;
     a.rows_per_cta = static_cast<int32_t>(imax64(64, (most + 65534) / 65535));
-    const dim3 grid(static_cast<unsigned>(a.c.b), static_cast<unsigned>((most + a.rows_per_cta - 1) / a.rows_per_cta));
+    const dim3 grid(static_cast<unsigned>(a.c.b),
+                    static_cast<unsigned>(imax64(1, (most + a.rows_per_cta - 1) / a.rows_per_cta)));
     if (a.c.d == 64) cache_append_kernel<64><<<grid, 256, 0, s>>>(a);
     else cache_append_kernel<128><<<grid, 256, 0, s>>>(a);
     if (grid.y > 1) cache_advance_kernel<<<static_cast<unsigned>(a.c.b), 256, 0, s>>>(a);

@@ -84,6 +84,7 @@ def refused(code, got, needle):
     (dict(max_pages=2 ** 20, page_size=2 ** 11), UNSUP, "capacity"),
     (dict(max_pages=2 ** 40, page_size=2 ** 40), UNSUP, "capacity"),
     (dict(b=2 ** 30), UNSUP, "b * h_kv"),
+    (dict(h_kv=4097), UNSUP, "b * h_kv"),
     (dict(page_table=0), INVALID, "without a page_table"),
     (dict(page_table=0, max_pages=1, n_pages=1), INVALID, "without a page_table"),
     (dict(positions=0), INVALID, "positions and next_pos"),
@@ -244,6 +245,25 @@ def test_calls_refuse_wrong_tensors():
             swa.cache_weigh(c, *args, scale=0.1, **kw)
     with pytest.raises(swa.SdpaError, match="weights"):
         swa.cache_evict(c, 4)
+
+
+def test_cache_attributes_are_not_replaced():
+    """The calls use the addresses that the constructor took."""
+    c = tensors()
+    for name in ("k", "v", "lengths", "page_table", "positions", "weights", "status", "anything"):
+        with pytest.raises(AttributeError, match=name):
+            setattr(c, name, torch.zeros(2, dtype=torch.int32))
+    c.lengths[0] = 3
+    assert c.lengths.tolist() == [3, 0]
+
+
+def test_rows_up_to_the_32_bit_limit():
+    refused(UNSUP, swa.sdpa_cache_weigh(cache(b=1, h_kv=1), weigh(s_q=2 ** 31 - 1023, h_q=1), 0), "rows")
+    refused(UNSUP, swa.sdpa_cache_weigh(cache(b=0, h_kv=1), weigh(s_q=2 ** 31 - 1, h_q=2 ** 31 - 1), 0), "rows")
+    p = swa.SdpaCacheEvictParams(2 ** 30, 0, 0)
+    big = cache(b=2 ** 20, h_kv=1, max_pages=2 ** 20, page_size=2 ** 10 + 1)
+    refused(UNSUP, swa.sdpa_cache_evict(big, p, 4096, 1 << 62, 0), "2^50")
+    assert swa.sdpa_cache_evict_workspace_bytes(big, p) == 0
 
 
 def test_empty_cache_helper():
