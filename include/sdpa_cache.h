@@ -23,8 +23,10 @@
  *
  * Problems found on the device are recorded in cache->status, first one wins:
  * SDPA_ERR_BAD_LENGTHS (a length, count or row index out of its range),
- * SDPA_ERR_BOUNDS (a page-table entry outside [0, n_pages)). Nothing outside
- * the buffers is accessed then: each call says below what it leaves out.
+ * SDPA_ERR_BOUNDS (a page-table entry outside [0, n_pages)), SDPA_ERR_TIMEOUT
+ * (a wait inside a kernel ran out; the call's outputs are not to be used).
+ * Nothing outside the buffers is accessed then: each call says below what it
+ * leaves out.
  */
 #ifndef SDPA_CACHE_H
 #define SDPA_CACHE_H
@@ -43,7 +45,7 @@ extern "C" {
 typedef struct sdpa_cache {
     int32_t dtype;              /* SDPA_BF16 | SDPA_F16 for K, V and the calls' tensors */
     int32_t reserved0;
-    int64_t b, h_kv, d;         /* sequences, kv-heads, head dimension (64 or 128) */
+    int64_t b, h_kv, d;         /* sequences, kv-heads (up to 4096), head dimension (64 or 128) */
     int64_t n_pages, page_size; /* pages in k and v, rows of a page (any number >= 1) */
     int64_t max_pages;          /* entries of a page-table row; a sequence has room for
                                    max_pages * page_size keys (its capacity, at most
@@ -52,7 +54,9 @@ typedef struct sdpa_cache {
     int64_t k_stride[3], v_stride[3]; /* page, row, head */
     const int32_t *page_table;  /* device [b][max_pages]; NULL: page i is sequence i's only one
                                    (max_pages = 1, n_pages >= b). Entries behind a sequence's
-                                   keys are not read. No page is in two places of the table. */
+                                   keys are not read. A page may be in several places (a common
+                                   prefix) as long as no call writes it: append writes the slots
+                                   behind a sequence's keys, evict any slot below its length. */
     int32_t *lengths;           /* device [b] */
     int32_t *next_pos;          /* device [b] with positions, else NULL (equal to lengths) */
     int32_t *positions;         /* device [b][h_kv][capacity] or NULL (the slot's number) */
@@ -84,11 +88,15 @@ size_t sdpa_cache_evict_params_bytes(void);
  * A row that admits no key gets O = 0 and LSE = -inf, or LSE = sink_h with a
  * sink. Rows at or behind seq_q_lens[i] get O = 0, LSE = -inf, and their keys
  * are not admitted by any row; bits at or behind it are ignored.
- * Sums, maxima and O are kept in fp32; P is split into a 16-bit value and a
- * 16-bit remainder for the P V product where rows are few, and rounded to the
- * I/O dtype (as sdpa_fwd does) where a tile of 128 rows is filled.
+ * Sums, maxima and O are kept in fp32. For the P V product P is split into a
+ * 16-bit value and its 16-bit remainder where a kv-head has up to 8 rows (s_q *
+ * h_q / h_kv; d = 64: up to 16), and rounded to the I/O dtype, as sdpa_fwd
+ * does, where it has more.
  * Keys on pages out of range are left out; lengths out of [0, capacity] are
- * taken as the nearer end.
+ * taken as the nearer end. Not read, or without effect whatever they hold, are
+ * slots behind a sequence's keys, without positions those in front of every
+ * row's window, and new tokens that no row admits. The other keys' K and V have
+ * to be finite, those too that only some rows admit: a masked V meets a P of 0.
  */
 typedef struct sdpa_cache_fwd_params {
     int64_t s_q, h_q;                    /* new tokens per sequence (1..64), q-heads */
@@ -146,7 +154,8 @@ sdpa_status_t sdpa_cache_append(const sdpa_cache *cache, const sdpa_cache_append
  * pos_j <= q_pos, and q_pos - pos_j <= window_left (if >= 0). Without q_pos the
  * rows are the last s_q tokens: q_pos = next_pos - s_q + r. The sum over a
  * key's rows is formed in fp32 in a fixed order (bitwise repeatable). Keys on
- * pages out of range keep their weight.
+ * pages out of range keep their weight. A key's K has to be finite, and the q of
+ * rows that count.
  */
 typedef struct sdpa_cache_weigh_params {
     int64_t s_q, h_q;             /* rows per sequence (>= 1), q-heads */
@@ -170,7 +179,8 @@ sdpa_status_t sdpa_cache_weigh(const sdpa_cache *cache, const sdpa_cache_weigh_p
  * free slots below `keep` in slot order, with their positions and weights.
  * Slots from `keep` on are left as they were. Sequences that hold no more than
  * `keep` keys are not touched. Needs positions and weights. A sequence whose
- * length is out of range is left alone; keys on pages out of range do not move.
+ * length is out of range is left alone; K and V on pages out of range do not
+ * move (their positions and weights do).
  */
 typedef struct sdpa_cache_evict_params {
     int64_t keep, first, recent;  /* keep >= first + recent, all >= 0 */

@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
     __shared__ uint32_t sh_ok[4][kStages];             // and which are there
     __shared__ float sh_m[4][ROWS], sh_l[4][ROWS];
     __shared__ uint64_t sh_mask[64];
+    __shared__ uint32_t sh_used[2];        // new tokens that some row admits
     __shared__ int64_t sh_sum[4];
     __shared__ int64_t sh_at[2];
 
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
     // ---- this CTA's part of the line; where it stands is kept in shared memory,
     // the registers are for the keys
     __shared__ Part sh_part;
-    __shared__ int32_t sh_done, sh_count;      // places of the part in the line: done, all
+    __shared__ int64_t sh_done, sh_count;      // places of the part in the line: done, all
     {
         Part part{1, 0, 0, 0, 0, Line{0}};
         if (a.whole) {
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
         if (tid == 0) {
             sh_part = part;
             sh_done = 0;
-            sh_count = static_cast<int32_t>(part.end - part.at);
+            sh_count = part.end - part.at;
         }
         __syncthreads();
     }
@@ -174,7 +175,19 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
                 const uint64_t in = sv.nq == 64 ? ~0ull : (1ull << sv.nq) - 1;
                 uint64_t m = 0;
                 if (tid < sv.nq) m = in & (a.tree ? static_cast<uint64_t>(a.tree[bi * a.s_q + tid]) : (2ull << tid) - 1);
-                sh_mask[tid] = (m >> tid) & 1 ? m : 0;   // without its own bit: an empty row
+                m = (m >> tid) & 1 ? m : 0;   // without its own bit: an empty row
+                sh_mask[tid] = m;
+            }
+            if (tid < 2) sh_used[tid] = 0;
+            __syncthreads();
+            if (warp < 2) {
+                const uint64_t m = sh_mask[tid];
+                const uint32_t lo32 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m));
+                const uint32_t hi32 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m >> 32));
+                if (lane == 0) {
+                    atomicOr(&sh_used[0], lo32);
+                    atomicOr(&sh_used[1], hi32);
+                }
             }
             __syncthreads();
             cur = bi;
@@ -273,20 +286,22 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
             bool ok = x < sv.new0 && j < sv.len;        // a cached key
             int64_t page = bi;
             uint32_t row = j;
+            const bool reach = ok && j >= sv.first;
             if (ok && a.c.page_table) {
                 page = k.entry;
                 row = a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)
                                           : static_cast<uint32_t>(j) % a.c.page_size;
                 ok = page >= 0 && page < a.c.n_pages;
-                if (!ok) set_status(a.c.status, SDPA_ERR_BOUNDS);
+                if (reach && !ok) set_status(a.c.status, SDPA_ERR_BOUNDS);
             }
+            ok = ok && reach;
             const uint32_t oks = __ballot_sync(0xffffffffu, ok);
             if (lane < GK) sh_pos[warp][st][lane] = k.pos;
             if (boxed) {
                 // a group's boxes (2 KB each: features 0-63, 64-127 of K, of V) begin at its first key; rows of the
                 // page behind the last key come along
                 constexpr int BOXES = 2 * (HD / 64) * KG;
-                const uint32_t groups = __popc(oks & (KG == 2 ? 0x10001u : 1u));
+                const uint32_t groups = ((oks & 0xffffu) != 0) + (KG == 2 && oks >> 16 != 0);
                 if (lane == 0) {
                     sh_ok[warp][st] = oks;
                     mbar_arrive_expect_tx(bar, groups * (2 * (HD / 64) * 2048));
@@ -296,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
                 const int u = lane % KG, b = lane / KG, is_v = b / (HD / 64), cb = b % (HD / 64);
                 const int row0 = __shfl_sync(0xffffffffu, static_cast<int>(row), u * 16);
                 const int page0 = __shfl_sync(0xffffffffu, static_cast<int>(page), u * 16);
-                if (lane < BOXES && ((oks >> (u * 16)) & 1))
+                if (lane < BOXES && ((oks >> (u * 16)) & 0xffffu))
                     tma_box(at + (is_v ? half : 0u) + cb * (GK * 128) + u * 2048, is_v ? &ta.tm_v : &ta.tm_k, bar, cb * 64,
                             static_cast<int>(gk), row0, page0);
             } else {
@@ -313,14 +328,15 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
                     if (GK == 32 || lane >= 16) bulk_load(at + half + key_row * C::kPitch, vp, HD * 2, bar);
                 }
             }
-            // new tokens: 16 bytes at a time, zeros in the rows of their group that hold none
+            // new tokens: 16 bytes at a time, zeros in the rows of their group that hold none or one that no row
+            // admits (padding may be anything, and meets a P of 0)
 #pragma unroll
             for (int u = 0; u < KG; ++u) {
                 const int32_t w0 = step_x(s) + u * 16 - sv.new0;      // the group's first new token
                 if (w0 < 0 || w0 >= sv.nq) continue;
                 for (int i = lane; i < 16 * (HD / 8); i += 32) {
                     const int r = i / (HD / 8), c = i % (HD / 8);
-                    const bool have = w0 + r < sv.nq;
+                    const bool have = w0 + r < sv.nq && (sh_used[(w0 + r) >> 5] >> ((w0 + r) & 31)) & 1;
                     const int64_t tok = have ? w0 + r : 0;
                     cp16(at + piece(u * 16 + r, c), a.k + bi * a.k_stride[0] + tok * a.k_stride[1] + gk * a.k_stride[2] + c * 8,
                          have);

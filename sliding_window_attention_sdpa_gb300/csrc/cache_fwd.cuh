@@ -98,7 +98,8 @@ __device__ __forceinline__ void named_sync(int id, int threads)
 // One sequence as the rows and keys of this call see it.
 struct SeqView {
     int32_t len, nq;    // cached keys, new tokens
-    int32_t lo;         // first cached key in reach of any row, rounded down to `align`
+    int32_t first;      // first cached key in reach of any row; the ones before it are not there
+    int32_t lo;         // the same, rounded down to `align`
     int32_t new0;       // place of new token 0 in the line of keys (lo ... ), a multiple of 16 from lo
     int32_t tiles;
 };
@@ -118,9 +119,9 @@ __device__ __forceinline__ SeqView seq_view(const CacheFwdArgs& a, int64_t bi, i
         }
     }
     // without positions the lowest row's window starts at len - W
-    v.lo = 0;
-    if (a.window_left >= 0 && a.c.positions == nullptr)
-        v.lo = static_cast<int32_t>(imax64(0, v.len - a.window_left)) & ~(align - 1);
+    v.first = 0;
+    if (a.window_left >= 0 && a.c.positions == nullptr) v.first = static_cast<int32_t>(imax64(0, v.len - a.window_left));
+    v.lo = v.first & ~(align - 1);
     const int64_t cached = ((static_cast<int64_t>(v.len) + 15) & ~int64_t(15)) - v.lo;
     v.new0 = static_cast<int32_t>(cached);
     v.tiles = static_cast<int32_t>((cached + ((max(v.nq, 1) + 15) & ~15) + tk - 1) / tk);

@@ -320,11 +320,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 return a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)
                                            : static_cast<uint32_t>(j) % a.c.page_size;
             };
+            // new tokens that some row admits: padding may be anything, and would meet a P of 0
+            uint32_t used[2] = {0u, 0u};
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int r = w * 32 + lane;
+                const uint64_t in = sv.nq == 64 ? ~0ull : (1ull << sv.nq) - 1;
+                uint64_t m = 0;
+                if (r < sv.nq) m = in & (a.tree ? static_cast<uint64_t>(a.tree[g.bi * a.s_q + r]) : (2ull << r) - 1);
+                if (!((m >> r) & 1)) m = 0;
+                used[0] |= __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m));
+                used[1] |= __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m >> 32));
+            }
             const int boxes = ta.box_rows ? kKeys / ta.box_rows : 0;
             // a TMA tile's page of lane's box, a tile ahead
             auto box_entry = [&](int32_t t) -> int32_t {
                 const int32_t j = sv.lo + t * kKeys + lane * ta.box_rows;
-                return lane < boxes && t <= t1 && j < sv.len ? entry_of(j) : 0;
+                return lane < boxes && t <= t1 && j >= sv.first && j < sv.len ? entry_of(j) : 0;
             };
             int32_t entry = box_entry(t0);
             for (int32_t t = t0; t <= t1; ++t, ++it) {
@@ -333,7 +345,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 const int32_t mine = entry;
                 entry = box_entry(t + 1);
                 const bool good = lane >= boxes || (mine >= 0 && mine < a.c.n_pages);
-                const bool by_tma = boxes > 0 && x0 + kKeys <= sv.new0 && j0 + kKeys <= sv.len && __all_sync(0xffffffffu, good);
+                const bool by_tma = boxes > 0 && j0 >= sv.first && x0 + kKeys <= sv.new0 && j0 + kKeys <= sv.len &&
+                                    __all_sync(0xffffffffu, good);
                 if (!(ok = acquire(empty0 + st, par ^ 1))) break;
                 const uint32_t stage = ring0 + st * C::kTile;
                 if (!is_v && a.window_left >= 0) {
@@ -369,14 +382,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                     const uint16_t* p = fresh;
                     bool have = false;
                     if (x < sv.new0) {
-                        if (j < sv.len) {
+                        if (j >= sv.first && j < sv.len) {
                             const int32_t page = entry_of(j);
                             have = page >= 0 && page < a.c.n_pages;
                             if (!have) set_status(a.c.status, SDPA_ERR_BOUNDS);
                             else p = pool + page * st_page + row_of(j) * st_row;
                         }
                     } else if (x - sv.new0 < sv.nq) {
-                        have = true;
+                        have = ((x - sv.new0 < 32 ? used[0] : used[1]) >> ((x - sv.new0) & 31)) & 1;
                         p = fresh + (x - sv.new0) * st_new;
                     }
                     const uint32_t held = __ballot_sync(0xffffffffu, have);

@@ -207,6 +207,69 @@ def test_forward_extreme_scores(t, d):
     close("o", o, ref.o, ref.tol_o)
 
 
+@pytest.mark.parametrize("t,d,h_q", [(11, 64, 2), (7, 128, 2), (11, 128, 8), (40, 64, 4), (64, 128, 4)])
+def test_forward_padding_tokens_hold_anything(t, d, h_q):
+    """Tokens that no row admits (masks without their own bit): NaN in them
+    reaches no output."""
+    lens, h_kv = [90, 10, 0], 2
+    lay = R.make(61, lens, h_kv, d, "bf16", 16)
+    q, k, v = inputs(62, len(lens), t, h_q, h_kv, d, "bf16")
+    tree = R.tree_masks(63, len(lens), t, 0.4)
+    for i in range(len(lens)):
+        pad = [r for r in range(t) if not int(tree[i, r]) >> r & 1]
+        assert 0 < len(pad) < t
+        q[i, pad], k[i, pad], v[i, pad] = math.nan, math.nan, math.inf
+    kw = dict(scale=d ** -0.5, window=-1, tree=tree, q_lens=None, sink=None)
+    o, lse = call_forward(gpu_cache(lay), dev(q), dev(k), dev(v), kw, check_status=True)
+    ref = R.forward(lay, q, k, v, **kw)
+    close("lse", lse, ref.lse, ref.tol_lse)
+    close("o", o, ref.o, ref.tol_o)
+
+
+@pytest.mark.parametrize("page", [4, 16, 64, 0])
+@pytest.mark.parametrize("t,d", [(1, 64), (2, 64), (2, 128), (40, 128), (40, 64)])
+def test_forward_in_front_of_the_window(t, d, page):
+    """Keys in front of every row's window may hold anything, pages in front of
+    it may be on no page at all (freed ones)."""
+    lens, h_q, h_kv, window = [301, 100, 77, 1000], 4, 2, 77
+    lay = R.make(64, lens, h_kv, d, "bf16", page)
+    for i, n in enumerate(lens):
+        if n > window:
+            pg, at = lay.where(i, list(range(n - window)))
+            lay.k[pg, at], lay.v[pg, at] = math.nan, math.nan
+            if page:
+                lay.table[i, :(n - window) // page] = -1
+    q, k, v = inputs(65, len(lens), t, h_q, h_kv, d, "bf16")
+    kw = dict(scale=d ** -0.5, window=window, tree=None, q_lens=None, sink=None)
+    o, lse = call_forward(gpu_cache(lay), dev(q), dev(k), dev(v), kw, check_status=True)
+    ref = R.forward(lay, q, k, v, **kw)
+    close("lse", lse, ref.lse, ref.tol_lse)
+    close("o", o, ref.o, ref.tol_o)
+
+
+@pytest.mark.parametrize("t,d", [(1, 64), (40, 128)])
+def test_forward_pages_shared_by_sequences(t, d):
+    """A common prefix on the same pages, read by all of its sequences; what is
+    appended goes behind it."""
+    import sliding_window_attention_sdpa_gb300 as swa
+    lens, h_q, h_kv, page = [128, 150, 131], 4, 2, 64
+    lay = R.make(66, lens, h_kv, d, "bf16", page, room=3 * t)
+    for i in (1, 2):
+        lay.real[i][:2] = lay.real[0][:2]
+        lay.table[i, :2] = lay.table[0, :2]
+    q, k, v = inputs(67, len(lens), t, h_q, h_kv, d, "bf16")
+    kw = dict(scale=d ** -0.5, window=-1, tree=None, q_lens=None, sink=None)
+    c = gpu_cache(lay)
+    for _ in range(2):
+        o, lse = call_forward(c, dev(q), dev(k), dev(v), kw, check_status=True)
+        ref = R.forward(lay, q, k, v, **kw)
+        close("lse", lse, ref.lse, ref.tol_lse)
+        close("o", o, ref.o, ref.tol_o)
+        swa.cache_append(c, dev(k), dev(v), check_status=True)
+        lay = R.append(lay, k, v)
+        same_cache(c, lay)
+
+
 @pytest.mark.parametrize("t,d", [(1, 64), (4, 128), (40, 128), (40, 64)])
 def test_forward_reports_bad_pages_and_lengths(t, d):
     """Found on the device, reported, nothing outside the buffers read; the
@@ -302,6 +365,29 @@ def test_append_forms(d, dtype, page, tracked):
         swa.cache_append(c, dev(kp)[:, 1:, :d], dev(vp)[:, 1:, :d], offsets=dev(off), max_seqlen=6, counts=dev(cnt),
                          check_status=True)
         same_cache(c, R.append(lay, kp[:, 1:, :d], vp[:, 1:, :d], offsets=off, counts=cnt))
+
+
+def test_append_without_rows_looks_at_the_counts():
+    import sliding_window_attention_sdpa_gb300 as swa
+    lay = R.make(45, [3, 5], 2, 64, "bf16", 16, room=9, tracked=True)
+    none = torch.zeros(2, 0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    some = torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    no_index = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    c = gpu_cache(lay)
+    for kw in ({}, dict(counts=i32(0, 0))):
+        swa.cache_append(c, none, none, check_status=True, **kw)
+        swa.cache_append(c, some, some, index=no_index, check_status=True, **kw)
+        swa.cache_append(c, none[0], none[0], offsets=i32(0, 0, 0), max_seqlen=0, check_status=True, **kw)
+    for args, kw in (((none, none), dict(counts=i32(0, 1))), ((some, some), dict(index=no_index, counts=i32(0, 1))),
+                     ((none, none), dict(index=i32(0, 0).view(2, 1))),
+                     ((some[0], some[0]), dict(offsets=i32(0, 1, 3), max_seqlen=0)),
+                     ((none[0], none[0]), dict(offsets=i32(0, 0, 1), max_seqlen=2))):
+        swa.cache_append(c, *args, **kw)
+        with pytest.raises(swa.SdpaError) as e:
+            c.check_status()
+        assert e.value.code == swa.SDPA_ERR_BAD_LENGTHS
+    same_cache(c, lay)
 
 
 @pytest.mark.parametrize("page", [64, 100])
