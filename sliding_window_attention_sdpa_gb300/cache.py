@@ -184,9 +184,18 @@ def _strides(name, t, shape, device, dtype):
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}: the feature dimension must be contiguous (stride 1)")
-    if 1 in shape:
-        return [s if n > 1 else 0 for s, n in zip(st[:-1], shape)]
-    return st[:-1]
+    return [s if n > 1 else 0 for s, n in zip(st[:-1], shape)]
+
+
+def _strides4(name, t, shape, device, dtype):
+    """The same of a call's tensor [.., .., .., d]: any stride serves where
+    there is no second entry, as long as the library's check takes it."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        _wrong(name, t, shape, device, dtype)
+    x, y, z, feature = t.stride()
+    if feature != 1 or (x | y | z) & 7:
+        return _strides(name, t, shape, device, dtype)
+    return x, y, z
 
 
 def _flat(name, t, shape, device, dtype):
@@ -290,24 +299,24 @@ class KVCache:
                "sdpa_cache_check_status")
 
 
-def _workspace(cache, key, size, workspace, c):
-    """Address and bytes of the workspace: the caller's, or a new tensor of the
-    bytes that `size()` says (kept by `key`, the arguments it depends on)."""
-    if workspace is not None:
-        if workspace.dtype is not c.uint8 or not workspace.is_contiguous():
-            raise ValueError("workspace: expected a contiguous uint8 tensor")
-        return workspace
-    n = cache._ws_bytes.get(key)
-    if n is None:
-        n = size()
-        if n == 0:
-            from . import SDPA_ERR_INVALID_ARG, SdpaError, last_error
-            if last_error():
-                raise SdpaError(SDPA_ERR_INVALID_ARG, f"sdpa_cache_{key[0]}_workspace_bytes", last_error())
-        if len(cache._ws_bytes) >= 256:
-            cache._ws_bytes.clear()
-        cache._ws_bytes[key] = n
-    return c.empty(n, dtype=c.uint8, device=cache.device) if n else None
+def _ws_size(cache, key, size, params, p):
+    """Workspace bytes of a call, kept by `key`, the arguments they depend on."""
+    n = size(cache.params, params.from_buffer_copy(p))
+    if n == 0:
+        from . import SDPA_ERR_INVALID_ARG, SdpaError, last_error
+        if last_error():
+            raise SdpaError(SDPA_ERR_INVALID_ARG, size.__name__, last_error())
+    if len(cache._ws_bytes) >= 256:
+        cache._ws_bytes.clear()
+    cache._ws_bytes[key] = n
+    return n
+
+
+def _given(workspace, c):
+    """Bytes of the caller's workspace."""
+    if workspace.dtype is not c.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous uint8 tensor")
+    return workspace.numel()
 
 
 def cache_forward(cache: KVCache, q, k, v, *, scale: float, window_left: int = -1, tree=None, seq_q_lens=None,
@@ -327,9 +336,9 @@ def cache_forward(cache: KVCache, q, k, v, *, scale: float, window_left: int = -
     _, s_q, h_q, _ = q.shape
     b, h_kv, d, dev, dt = cache._key
     rows, kv = (b, s_q, h_q, d), (b, s_q, h_kv, d)
-    sq = _strides("q", q, rows, dev, dt)
-    sk = _strides("k", k, kv, dev, dt)
-    sv = _strides("v", v, kv, dev, dt)
+    sq = _strides4("q", q, rows, dev, dt)
+    sk = _strides4("k", k, kv, dev, dt)
+    sv = _strides4("v", v, kv, dev, dt)
     if out is None:
         out = c.empty(rows, dtype=dt, device=dev)
         so = (s_q * h_q * d, h_q * d, d)
@@ -338,15 +347,25 @@ def cache_forward(cache: KVCache, q, k, v, *, scale: float, window_left: int = -
         so = _strides("out", out, rows, dev, dt)
     if lse is None:
         lse = c.empty((b, h_q, s_q), dtype=c.float32, device=dev)
+        lse_at = lse.data_ptr()
+    else:
+        lse_at = _flat("lse", lse, (b, h_q, s_q), dev, c.float32)
     p = _FWD.pack(s_q, h_q, window_left, scale, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(), *sq, *sk, *sv, *so,
-                  _flat("tree", tree, (b, s_q), dev, c.int64), _flat("seq_q_lens", seq_q_lens, (b,), dev, c.int32),
-                  _flat("sink", sink, (h_q,), dev, c.float32), out.data_ptr(),
-                  _flat("lse", lse, (b, h_q, s_q), dev, c.float32))
-    ws = _workspace(cache, ("fwd", s_q, h_q, window_left),
-                    lambda: sdpa_cache_fwd_workspace_bytes(cache.params, SdpaCacheFwdParams.from_buffer_copy(p)),
-                    workspace, c)
-    _check(c.fwd(cache._ref, p, ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0,
-                 c.stream(cache._index)), "sdpa_cache_fwd")
+                  0 if tree is None else _flat("tree", tree, (b, s_q), dev, c.int64),
+                  0 if seq_q_lens is None else _flat("seq_q_lens", seq_q_lens, (b,), dev, c.int32),
+                  0 if sink is None else _flat("sink", sink, (h_q,), dev, c.float32), out.data_ptr(), lse_at)
+    if workspace is None:
+        key = s_q, h_q, window_left
+        n = cache._ws_bytes.get(key)
+        if n is None:
+            n = _ws_size(cache, key, sdpa_cache_fwd_workspace_bytes, SdpaCacheFwdParams, p)
+        if n:
+            workspace = c.empty(n, dtype=c.uint8, device=dev)
+    else:
+        n = _given(workspace, c)
+    code = c.fwd(cache._ref, p, workspace.data_ptr() if n else 0, n, c.stream(cache._index))
+    if code:
+        _check(code, "sdpa_cache_fwd")
     if check_status:
         cache.check_status()
     return out, lse
@@ -378,7 +397,7 @@ def cache_append(cache: KVCache, k, v, *, index=None, counts=None, offsets=None,
             raise ValueError(f"k: expected [b, s, h_kv, d] or [total, h_kv, d], got {tuple(k.shape)}")
         layout, s = 0, k.shape[1]
         shape = (b, s, h_kv, d)
-        sk, sv = _strides("k", k, shape, dev, dt), _strides("v", v, shape, dev, dt)
+        sk, sv = _strides4("k", k, shape, dev, dt), _strides4("v", v, shape, dev, dt)
     if index is not None:
         if index.dim() != 2:
             raise ValueError("index: expected [b, n]")
@@ -386,8 +405,9 @@ def cache_append(cache: KVCache, k, v, *, index=None, counts=None, offsets=None,
         if n == 0:
             s = 0       # no row of any sequence (and no address of an empty index)
     p = _APPEND.pack(layout, 0, s, n, total, k.data_ptr(), v.data_ptr(), *sk, *sv,
-                     _flat("index", index, (b, n), dev, c.int32), _flat("counts", counts, (b,), dev, c.int32),
-                     _flat("offsets", offsets, (b + 1,), dev, c.int32))
+                     0 if index is None else _flat("index", index, (b, n), dev, c.int32),
+                     0 if counts is None else _flat("counts", counts, (b,), dev, c.int32),
+                     0 if offsets is None else _flat("offsets", offsets, (b + 1,), dev, c.int32))
     _check(c.append(cache._ref, p, c.stream(cache._index)), "sdpa_cache_append")
     if check_status:
         cache.check_status()
@@ -406,8 +426,9 @@ def cache_weigh(cache: KVCache, q, lse, *, scale: float, window_left: int = -1, 
         raise ValueError(f"q: expected [b, s_q, h_q, d], got {tuple(q.shape)}")
     _, s_q, h_q, _ = q.shape
     b, _, d, dev, dt = cache._key
-    p = _WEIGH.pack(s_q, h_q, window_left, scale, 0, q.data_ptr(), *_strides("q", q, (b, s_q, h_q, d), dev, dt),
-                    _flat("lse", lse, (b, h_q, s_q), dev, c.float32), _flat("q_pos", q_pos, (b, s_q), dev, c.int32))
+    p = _WEIGH.pack(s_q, h_q, window_left, scale, 0, q.data_ptr(), *_strides4("q", q, (b, s_q, h_q, d), dev, dt),
+                    _flat("lse", lse, (b, h_q, s_q), dev, c.float32),
+                    0 if q_pos is None else _flat("q_pos", q_pos, (b, s_q), dev, c.int32))
     _check(c.weigh(cache._ref, p, c.stream(cache._index)), "sdpa_cache_weigh")
     if check_status:
         cache.check_status()
@@ -420,10 +441,15 @@ def cache_evict(cache: KVCache, keep: int, *, first: int = 0, recent: int = 0, w
     heaviest of the others stay, for each kv-head on its own."""
     c = _calls or _c()
     p = _EVICT.pack(keep, first, recent)
-    ws = _workspace(cache, ("evict", keep, first, recent),
-                    lambda: sdpa_cache_evict_workspace_bytes(cache.params, SdpaCacheEvictParams.from_buffer_copy(p)),
-                    workspace, c)
-    _check(c.evict(cache._ref, p, ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0,
-                   c.stream(cache._index)), "sdpa_cache_evict")
+    if workspace is None:
+        key = "evict", keep, first, recent
+        n = cache._ws_bytes.get(key)
+        if n is None:
+            n = _ws_size(cache, key, sdpa_cache_evict_workspace_bytes, SdpaCacheEvictParams, p)
+        if n:
+            workspace = c.empty(n, dtype=c.uint8, device=cache.device)
+    else:
+        n = _given(workspace, c)
+    _check(c.evict(cache._ref, p, workspace.data_ptr() if n else 0, n, c.stream(cache._index)), "sdpa_cache_evict")
     if check_status:
         cache.check_status()

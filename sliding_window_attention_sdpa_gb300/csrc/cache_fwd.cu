@@ -681,7 +681,8 @@ cudaError_t launch_rows(const CacheTileArgs& ta, cudaStream_t s)
 {
     auto kern = cache_fwd_rows_kernel<HD, BF16, NT>;
     const uint32_t bytes = RowsCfg<HD>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(kern, bytes, allowed);
     if (e != cudaSuccess) return e;
     kern<<<ta.f.parts, kThreads, bytes, s>>>(ta);
     e = cudaGetLastError();

@@ -2,6 +2,7 @@
 // (cache_api.cu) and its kernels. Plain structs passed by value.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda.h>
@@ -106,6 +107,21 @@ struct CacheEvictArgs {
     int64_t timeout_ns;
     int32_t cluster;       // CTAs per head (set by the launcher)
 };
+
+// Lets a kernel have `bytes` of dynamic shared memory: asked of the driver once
+// per device (`done`: a bit each).
+template <class F>
+cudaError_t allow_smem(F* kern, int bytes, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 cudaError_t launch_cache_fwd(const CacheTileArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_cache_fwd_tiles(const CacheTileArgs& a, int dtype, cudaStream_t s);

@@ -438,6 +438,85 @@ __global__ void __launch_bounds__(128) cache_evict_move_kernel(const __grid_cons
     bulk_wait0();
 }
 
+namespace {
+
+constexpr uint32_t kSelMost = 200 * 1024;      // shared memory of a select CTA, at most
+constexpr uint32_t kMoveBytes = 65536;
+
+// Whether clusters of 16 run on the current device (not every partition of a
+// GPU promises them): asked once per device.
+template <bool CACHED>
+bool clusters_of_16()
+{
+    static std::atomic<uint64_t> known{0}, yes{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
+    const uint64_t bit = uint64_t(1) << dev;
+    if (!(known.load(std::memory_order_acquire) & bit)) {
+        auto kern = cache_evict_select_kernel<CACHED>;
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 16;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(kSelThreads);
+        cfg.dynamicSmemBytes = kSelMost;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int fit = 0;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) == cudaSuccess && fit > 0)
+            yes.fetch_or(bit, std::memory_order_relaxed);
+        cudaGetLastError();
+        known.fetch_or(bit, std::memory_order_release);
+    }
+    return yes.load(std::memory_order_relaxed) & bit;
+}
+
+template <bool CACHED>
+cudaError_t launch_select(CacheEvictArgs& a, uint32_t bytes, int64_t units, cudaStream_t s)
+{
+    auto kern = cache_evict_select_kernel<CACHED>;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(units * a.cluster));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(kern, kSelMost, allowed);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int HD>
+cudaError_t launch_move(const CacheEvictArgs& a, int64_t units, cudaStream_t s)
+{
+    auto kern = cache_evict_move_kernel<HD>;
+    constexpr int64_t rows = HD == 64 ? 128 : 64;      // of a CTA's round
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(units),
+                       static_cast<unsigned>(imax64(1, imin64((a.m + rows - 1) / rows, 152 * 3 / units))));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = kMoveBytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(kern, kMoveBytes, allowed);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace
+
 cudaError_t launch_cache_evict(const CacheEvictArgs& a0, cudaStream_t s)
 {
     CacheEvictArgs a = a0;
@@ -446,48 +525,14 @@ cudaError_t launch_cache_evict(const CacheEvictArgs& a0, cudaStream_t s)
     // CTAs per head: as many as two per SM allow, with 2048 slots each at least
     a.cluster = 1;
     while (a.cluster < 16 && units * a.cluster * 2 <= 304 && a.c.cap / (a.cluster * 2) >= 2048) a.cluster *= 2;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e;
-    void (*select)(CacheEvictArgs);
-    for (;; a.cluster = 8) {
-        // a slice's ranks are kept as far as shared memory goes; a longer one's are computed in each pass
-        const int64_t most = (a.c.cap + a.cluster - 1) / a.cluster + kSelThreads;
-        const bool cached = most <= (200 * 1024 - kSelFixed) / 4;
-        select = cached ? cache_evict_select_kernel<true> : cache_evict_select_kernel<false>;
-        cfg.dynamicSmemBytes = kSelFixed + (cached ? static_cast<uint32_t>((most + 3) / 4 * 16) : 0u);
-        cfg.gridDim = dim3(static_cast<unsigned>(units * a.cluster));
-        attr[0].val.clusterDim.x = a.cluster;
-        e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(cfg.dynamicSmemBytes));
-        if (e != cudaSuccess) return e;
-        if (a.cluster < 16) break;
-        // 16 CTAs of a cluster are not promised by every partition of a GPU
-        e = cudaFuncSetAttribute(select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        int fit = 0;
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&fit, select, &cfg);
-        if (e == cudaSuccess && fit > 0) break;
-        cudaGetLastError();
-    }
-    if ((e = cudaLaunchKernelEx(&cfg, select, a)) != cudaSuccess) return e;
-    const int64_t rows = a.c.d == 64 ? 128 : 64;      // of a CTA's round
-    cfg.gridDim = dim3(static_cast<unsigned>(units),
-                       static_cast<unsigned>(imax64(1, imin64((a.m + rows - 1) / rows, 152 * 3 / units))));
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 65536;
-    e = a.c.d == 64 ? cudaFuncSetAttribute(cache_evict_move_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536)
-                    : cudaFuncSetAttribute(cache_evict_move_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+    // a slice's ranks are kept as far as shared memory goes; a longer one's are computed in each pass
+    auto most = [&]() { return (a.c.cap + a.cluster - 1) / a.cluster + kSelThreads; };
+    auto cached = [&]() { return most() <= (kSelMost - kSelFixed) / 4; };
+    if (a.cluster == 16 && !(cached() ? clusters_of_16<true>() : clusters_of_16<false>())) a.cluster = 8;
+    const cudaError_t e = cached() ? launch_select<true>(a, kSelFixed + static_cast<uint32_t>((most() + 3) / 4 * 16), units, s)
+                                   : launch_select<false>(a, kSelFixed, units, s);
     if (e != cudaSuccess) return e;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    return a.c.d == 64 ? cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<64>, a)
-                       : cudaLaunchKernelEx(&cfg, cache_evict_move_kernel<128>, a);
+    return a.c.d == 64 ? launch_move<64>(a, units, s) : launch_move<128>(a, units, s);
 }
 
 }  // namespace swa

@@ -724,7 +724,8 @@ template <int HD, bool BF16>
 cudaError_t launch_tile_typed(const CacheTileArgs& a, cudaStream_t s)
 {
     auto kern = cache_fwd_tile_kernel<HD, BF16>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<HD>::kBytes);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(kern, TileCfg<HD>::kBytes, allowed);
     if (e != cudaSuccess) return e;
     kern<<<a.f.parts, kTileThreads, TileCfg<HD>::kBytes, s>>>(a);
     return cudaGetLastError();

@@ -495,7 +495,8 @@ template <int HD, bool BF16>
 cudaError_t launch_typed(const CacheWeighArgs& a, cudaStream_t s)
 {
     auto kern = cache_weigh_kernel<HD, BF16>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WeighCfg<HD>::kBytes);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(kern, WeighCfg<HD>::kBytes, allowed);
     if (e != cudaSuccess) return e;
     kern<<<a.parts, kWThreads, WeighCfg<HD>::kBytes, s>>>(a);
     return cudaGetLastError();
