@@ -6,21 +6,27 @@
 // rows in N (up to 256 at once), so the thread that owns a lane adds
 //   exp2(s_r * scale * log2(e) - LSE_r * log2(e))
 // over its lane's columns in registers: one reader and writer per key, no
-// atomics, a fixed order. Four accumulators of up to 128 columns: each of two
-// groups of warps sums one while its other one is computed.
+// atomics, a fixed order. Each group of warps has two accumulators and sums one
+// while its other one is computed.
 //
-// Few rows: bound by reading K once (a 4-stage ring of 128 keys by TMA). Many
-// rows: by the exponentials (one per key and row): 93 us at 12 sequences of
-// 16484 keys, 6 kv-heads and 256 rows in bf16, d = 128. The loop over columns
-// exists twice, with and without the mask (102 us with one loop that asked per
-// 32 columns), and is not unrolled: both stay within the registers.
+// Few rows: bound by reading K once (a 4-stage ring of 128 keys by TMA, 8 at
+// d = 64): 55 us at 12 sequences of 16484 keys, 6 kv-heads, 8 rows in bf16,
+// d = 128 (5.5 TB/s). Many rows: by the exponentials (one per key and row):
+// 88 us for 256 rows. The loop over columns exists twice, with and without the
+// mask (102 us against 93 with one loop that asked per 32 columns), and is not
+// unrolled: both stay within the registers. Weights and positions come into L2
+// ahead of their use (93 us against 89).
 //
-// Roles (640 threads): warp 0 loads K; warp 1 issues the MMAs; warps 4-11 and
-// 12-19 sum every other key tile each, two threads a key (64 of an
-// accumulator's columns each; with one, 8 warps left the SM waiting on
-// latencies: 116 us against 102 then), and
-// put the rows (Q, LSE, positions) in place, 256 at a time; more rows take
-// another round over the part's keys.
+// Roles (640 threads): warp 0 loads K; warp 1 issues the MMAs; warps 4-19 sum,
+// and put the rows (Q, LSE, positions) in place, 256 at a time; more rows take
+// another round over the part's keys. More than 64 rows: two groups of eight
+// warps take every other key tile, two threads a key (64 of an accumulator's
+// columns each; with one, 8 warps in all left the SM waiting on latencies: 116
+// us against 102 then). Up to 64 rows the second thread would have nothing to
+// do, and a tile's chain of waits, not its work, is what a group takes: four
+// groups take every fourth tile, a thread a key (16 sequences of 8000 keys, 8
+// kv-heads, 8 rows, d = 64: 33 us against 39; 8 rows and d = 128 above: 55
+// against 56).
 // The key tiles of all (sequence, kv-head) units form one line that the CTAs
 // cut evenly. Every wait is bounded (SDPA_ERR_TIMEOUT in the cache's status).
 #include <type_traits>
@@ -35,6 +41,7 @@ constexpr int kWThreads = 640;
 constexpr int kWKeys = 128;
 constexpr int kWRows = 256;
 constexpr int kWHalf = 128;           // rows of an accumulator
+constexpr int kAhead = 6;             // tiles that weights and positions are brought into L2 before their use
 constexpr int kWCost = 4;             // a unit's fixed cost in key tiles
 
 template <int HD>
@@ -49,14 +56,14 @@ struct WeighCfg {
     static constexpr uint32_t kPos = kCst + kWRows * 4;       // int32 [256]: positions
     static constexpr uint32_t kSum = kPos + kWRows * 4;       // float [2 groups][2 tiles][128]: second threads' sums
     static constexpr uint32_t kBars = kSum + 2048;
-    static constexpr uint32_t kMisc = kBars + 256;
+    static constexpr uint32_t kMisc = kBars + 384;
     static constexpr uint32_t kBytes = kMisc + 128 + 1024;
     static_assert(kBytes <= 232448, "shared memory above the 227 KB a CTA may opt into");
 };
 
 // (accumulators: group * 2 + buffer)
-enum WBar : int { wKFull = 0, wKEmpty = 8, wDFull = 16, wDEmpty = 20, wDrain = 24, wNumBars };
-static_assert(wNumBars * 8 <= 256, "mbarrier area");
+enum WBar : int { wKFull = 0, wKEmpty = 8, wDFull = 16, wDEmpty = 24, wDrain = 32, wNumBars };
+static_assert(wNumBars * 8 <= 384, "mbarrier area");
 
 // Two fp32 values in one 64-bit register, and the packed arithmetic on them.
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi)
@@ -97,11 +104,15 @@ __device__ __forceinline__ void reach(int32_t qmin, int32_t qmax, int64_t window
 
 }  // namespace
 
-template <int HD, bool BF16>
+// FEW: up to 64 rows; four groups of warps take every fourth key tile each, a
+// thread a key, two accumulators of 64 columns each.
+template <int HD, bool BF16, bool FEW>
 __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_constant__ CacheWeighArgs a)
 {
     using C = WeighCfg<HD>;
     constexpr int NS = C::kStages;
+    constexpr uint32_t NG = FEW ? 4 : 2;               // groups
+    constexpr uint32_t AC = FEW ? 64 : kWHalf;         // columns of an accumulator
     extern __shared__ __align__(1024) uint8_t raw[];
     __shared__ int64_t sh_sum[kWThreads / 32], sh_at[2];
     uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -129,9 +140,9 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
             mbar_init(bar(wKFull + i), 1);
             mbar_init(bar(wKEmpty + i), 1);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (uint32_t i = 0; i < 2 * NG; ++i) {
             mbar_init(bar(wDFull + i), 1);
-            mbar_init(bar(wDEmpty + i), 256);
+            mbar_init(bar(wDEmpty + i), FEW ? 128 : 256);
         }
         mbar_init(bar(wDrain), 1);
         fence_mbar_init();
@@ -302,11 +313,11 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                     }
                     const int rows = (min(kWRows, R - ch * kWRows) + 31) & ~31;
                     for (int32_t t = ta; t < tb && ok; ++t, ++it) {
-                        const uint32_t st = it % NS, grp = it & 1;
+                        const uint32_t st = it % NS, grp = it % NG;
                         if (!(ok = wait(wKFull + st, (it / NS) & 1))) break;
                         const uint64_t dk = sdesc_at(dk0, st * C::kTile);
                         for (int r0 = 0; r0 < rows; r0 += kWHalf) {
-                            const uint32_t m = grp ? made1++ : made0++, b = grp * 2 + (m & 1);
+                            const uint32_t m = FEW ? it / NG : grp ? made1++ : made0++, b = grp * 2 + (m & 1);
                             if (!(ok = wait(wDEmpty + b, ((m >> 1) & 1) ^ 1))) break;
                             tc_fence_after();
                             const uint32_t idesc = idesc_f16(BF16, 128, 0, false, false) |
@@ -314,7 +325,7 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                             const uint64_t dq = sdesc_at(dq0, r0 * 128);
 #pragma unroll
                             for (int k = 0; k < HD / 16; ++k)
-                                mma_ss(tmem + b * kWHalf, sdesc_at(dk, (k >> 2) * C::kBlk + (k & 3) * 32),
+                                mma_ss(tmem + b * AC, sdesc_at(dk, (k >> 2) * C::kBlk + (k & 3) * 32),
                                        sdesc_at(dq, (k >> 2) * C::kQBlk + (k & 3) * 32), idesc, k > 0);
                             mma_commit(bar(wDFull + b));
                         }
@@ -330,7 +341,7 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
         __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ rows, sums
-        const int grp = (warp - 4) >> 3, second = ((warp - 4) >> 2) & 1;
+        const int grp = (warp - 4) >> (FEW ? 2 : 3), second = FEW ? 0 : ((warp - 4) >> 2) & 1;
         const int et = tid - 128;                           // the first 256: a row each
         const int key_lane = ((warp & 3) << 5) + lane;      // key of the tile
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -406,15 +417,21 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                                                                                                : static_cast<uint32_t>(j) / a.c.page_size)];
                         k.pos = a.c.positions ? a.c.positions[unit + j] : j;
                         k.w = a.c.weights[unit + j];
+                        // (a group's tile takes less than memory's latency: later ones come into L2 before)
+                        const int32_t later = j + kAhead * kWKeys;
+                        if (later < len) {
+                            if (!second) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.weights + unit + later));
+                            if ((FEW || second) && a.c.positions) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.positions + unit + later));
+                        }
                     }
                     return k;
                 };
-                const int32_t mine0 = ta + static_cast<int32_t>((it & 1) != static_cast<uint32_t>(grp));   // the group's first tile
+                const int32_t mine0 = ta + static_cast<int32_t>((grp - it) % NG);   // the group's first tile
                 Mine next = fetch(mine0);
                 for (int32_t t = ta; t < tb; ++t, ++it) {
-                    if (static_cast<int>(it & 1) != grp) continue;
+                    if (it % NG != static_cast<uint32_t>(grp)) continue;
                     const Mine me = next;
-                    next = fetch(t + 2);
+                    next = fetch(t + NG);
                     const int32_t j = t * kWKeys + key_lane;
                     const bool held = j < len && me.entry >= 0 && me.entry < a.c.n_pages;
                     const int32_t kp = held ? me.pos : 0;
@@ -429,7 +446,7 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) continue;
                         tc_fence_after();
-                        const uint32_t td = tmem + b * kWHalf + lane_off;
+                        const uint32_t td = tmem + b * AC + lane_off;
                         const int n32 = min(kWHalf, rows - r0);
                         // this thread's columns, 32 at a time
                         const int c1 = min(n32, 64 * (second + 1));
@@ -470,12 +487,16 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                     }
                     const uint64_t sum2 = add2(add2(s2[0], s2[1]), add2(s2[2], s2[3]));
                     float sum = lo_of(sum2) + hi_of(sum2);
-                    // the key's two threads: the second hands its sum to the first
-                    float* slot = reinterpret_cast<float*>(sm + C::kSum) + (grp * 2 + (tile_par & 1)) * kWKeys + key_lane;
-                    tile_par ^= 1;
-                    if (second) *slot = sum;
-                    named_sync(4 + grp * 4 + (warp & 3), 64);
-                    if (!second && held && ok) a.c.weights[unit + j] = me.w + (sum + *slot);
+                    if constexpr (FEW) {
+                        if (held && ok) a.c.weights[unit + j] = me.w + sum;
+                    } else {
+                        // the key's two threads: the second hands its sum to the first
+                        float* slot = reinterpret_cast<float*>(sm + C::kSum) + (grp * 2 + (tile_par & 1)) * kWKeys + key_lane;
+                        tile_par ^= 1;
+                        if (second) *slot = sum;
+                        named_sync(4 + grp * 4 + (warp & 3), 64);
+                        if (!second && held && ok) a.c.weights[unit + j] = me.w + (sum + *slot);
+                    }
                 }
             }
             return true;
@@ -491,10 +512,10 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
 
 namespace {
 
-template <int HD, bool BF16>
+template <int HD, bool BF16, bool FEW>
 cudaError_t launch_typed(const CacheWeighArgs& a, cudaStream_t s)
 {
-    auto kern = cache_weigh_kernel<HD, BF16>;
+    auto kern = cache_weigh_kernel<HD, BF16, FEW>;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(kern, WeighCfg<HD>::kBytes, allowed);
     if (e != cudaSuccess) return e;
@@ -502,12 +523,18 @@ cudaError_t launch_typed(const CacheWeighArgs& a, cudaStream_t s)
     return cudaGetLastError();
 }
 
+template <int HD, bool BF16>
+cudaError_t launch_rows(const CacheWeighArgs& a, cudaStream_t s)
+{
+    return static_cast<int64_t>(a.s_q) * a.group <= 64 ? launch_typed<HD, BF16, true>(a, s) : launch_typed<HD, BF16, false>(a, s);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_weigh(const CacheWeighArgs& a, int dtype, cudaStream_t s)
 {
-    if (a.c.d == 128) return dtype == SDPA_BF16 ? launch_typed<128, true>(a, s) : launch_typed<128, false>(a, s);
-    return dtype == SDPA_BF16 ? launch_typed<64, true>(a, s) : launch_typed<64, false>(a, s);
+    if (a.c.d == 128) return dtype == SDPA_BF16 ? launch_rows<128, true>(a, s) : launch_rows<128, false>(a, s);
+    return dtype == SDPA_BF16 ? launch_rows<64, true>(a, s) : launch_rows<64, false>(a, s);
 }
 
 }  // namespace swa
