@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         const uint32_t tm_s = tm_s0 + sl * 128 + lane_off, tm_o = tm_o0 + sl * HD + lane_off;
         float2* ml = reinterpret_cast<float2*>(sm + C::kMl);
         uint64_t* masks = reinterpret_cast<uint64_t*>(sm + C::kMask);
+        const uint64_t scale2 = pair(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
         uint32_t it0 = 0, cnt = 0;            // ring index at the segment's start; this slot's key tiles so far
         bool ok = true;
         const int64_t part0 = walk.at;
@@ -590,7 +591,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 }
                 float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < 64; ++e) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(v[e]));
+                for (int e = 0; e < 64; e += 2)
+                    x[(e >> 1) & 3] = max3(x[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
                 const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.scale_log2;
                 const bool up = top > m + 8.f;
                 if (__any_sync(0xffffffffu, up)) {
@@ -622,21 +624,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 }
                 // P over the first columns of its S
                 const float mr = m == -INFINITY ? 0.f : m;
-                float ps[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t mr2 = pair(__float_as_uint(-mr), __float_as_uint(-mr));
+                uint64_t ps[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t w8[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         // a masked score is -inf, its P is 0
-                        const float p0 = ex2_approx(fmaf(__uint_as_float(v[16 * q + 2 * e]), a.scale_log2, -mr));
-                        const float p1 = ex2_approx(fmaf(__uint_as_float(v[16 * q + 2 * e + 1]), a.scale_log2, -mr));
-                        ps[e & 3] += p0 + p1;
+                        const uint64_t y = fma2(pair(v[16 * q + 2 * e], v[16 * q + 2 * e + 1]), scale2, mr2);
+                        const float p0 = ex2_approx(lo_of(y)), p1 = ex2_approx(hi_of(y));
+                        ps[e & 3] = add2(ps[e & 3], pair(__float_as_uint(p0), __float_as_uint(p1)));
                         w8[e] = pack2<BF16>(p0, p1);
                     }
                     tmem_st8(ts + 8 * q, w8);
                 }
-                l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                const uint64_t pt = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
+                l += lo_of(pt) + hi_of(pt);
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(bar(tPFull + pb));

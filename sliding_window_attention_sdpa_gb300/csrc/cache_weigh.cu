@@ -65,28 +65,6 @@ struct WeighCfg {
 enum WBar : int { wKFull = 0, wKEmpty = 8, wDFull = 16, wDEmpty = 24, wDrain = 32, wNumBars };
 static_assert(wNumBars * 8 <= 384, "mbarrier area");
 
-// Two fp32 values in one 64-bit register, and the packed arithmetic on them.
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
-__device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-
 // A chunk of rows and the key tiles [t0, t1) of a segment that it reaches.
 __device__ __forceinline__ void reach(int32_t qmin, int32_t qmax, int64_t window, int32_t len, int32_t t0, int32_t t1, int32_t& a,
                                       int32_t& b)
