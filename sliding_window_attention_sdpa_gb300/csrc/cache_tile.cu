@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         }
         for (int s = 0; s < 4; ++s) {
             mbar_init(bar(tSFull + s), 2);    // the MMAs' commit, and the issuer's own arrival
-            mbar_init(bar(tPFull + s), 128);
+            mbar_init(bar(tPFull + s), 4);        // a warp each
             mbar_init(bar(tPvDone + s), 1);
         }
         mbar_init(bar(tDrain), 1);
@@ -643,7 +643,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 l += lo_of(pt) + hi_of(pt);
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(bar(tPFull + pb));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(tPFull + pb));
             }
             // the slot's last P V is done
             if (cnt != cnt0) {

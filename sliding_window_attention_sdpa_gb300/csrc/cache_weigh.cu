@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
         }
         for (uint32_t i = 0; i < 2 * NG; ++i) {
             mbar_init(bar(wDFull + i), 1);
-            mbar_init(bar(wDEmpty + i), FEW ? 128 : 256);
+            mbar_init(bar(wDEmpty + i), FEW ? 4 : 8);      // a warp each
         }
         mbar_init(bar(wDrain), 1);
         fence_mbar_init();
@@ -461,7 +461,8 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                         if (plain) columns(std::false_type{});
                         else if (!none) columns(std::true_type{});
                         tc_fence_before();
-                        mbar_arrive(bar(wDEmpty + b));
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(wDEmpty + b));
                     }
                     const uint64_t sum2 = add2(add2(s2[0], s2[1]), add2(s2[2], s2[3]));
                     float sum = lo_of(sum2) + hi_of(sum2);
