@@ -113,6 +113,21 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32])
                      : "memory");
 }
 
+// Whether the phase with the given parity has completed, without suspending the
+// thread (try_wait may hold it for a while).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Arrives once on `bar` when this thread's MMAs so far are done.
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
