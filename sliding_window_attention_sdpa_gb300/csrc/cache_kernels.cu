@@ -155,7 +155,7 @@ cudaError_t launch_cache_append(const CacheAppendArgs& a0, cudaStream_t s)
 // order, lists the free slots below `keep` and the kept ones from there on. A
 // histogram has a column per lane (256 x 32 counters): lanes never meet on a
 // counter or a bank, whatever the weights. It is bound by its chain of barriers
-// and cluster barriers, not by its reads: 21.6 us for 72 heads of 16484 keys, 44
+// and cluster barriers, not by its reads: 21.6 us for 72 heads of 16484 keys, 42
 // for 8 heads of 262161 (slices of 16385 keys, 16 CTAs a head). The second
 // kernel moves the rows, bound by reading and writing each moved row once.
 
@@ -171,23 +171,23 @@ __device__ __forceinline__ uint32_t evict_rank(const CacheEvictArgs& a, float w,
     return (pos < a.first) | (pos >= next - a.recent) ? 0xffffffffu : r;
 }
 
-constexpr int kSelThreads = 512;      // two CTAs an SM
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr uint32_t kSelFixed = 256 * 32 * 4;       // the histogram; the ranks follow it
 
 }  // namespace
 
 // CACHED: a slice's ranks fit shared memory; else each pass computes them.
-template <bool CACHED>
-__global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(const __grid_constant__ CacheEvictArgs a)
+// T: threads.
+template <bool CACHED, int T>
+__global__ void __launch_bounds__(T, 1024 / T) cache_evict_select_kernel(const __grid_constant__ CacheEvictArgs a)
 {
     namespace cg = cooperative_groups;
+    constexpr int W = T / 32;
     extern __shared__ __align__(16) uint32_t dyn32[];
     uint32_t* hist = dyn32;
     uint32_t* ranks = dyn32 + kSelFixed / 4;
     __shared__ uint32_t tot[2][256];        // this CTA's histogram of a pass
     __shared__ uint32_t mine[3];            // this CTA's ties, free slots, kept slots behind
-    __shared__ uint32_t per_warp[3][kSelWarps];
+    __shared__ uint32_t per_warp[3][W];
     __shared__ uint32_t sums[256];          // all CTAs' histogram of a pass
     __shared__ uint32_t digit, left, equal;
     cg::cluster_group cl = cg::this_cluster();
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
     const int32_t* pos = a.c.positions + u * a.c.cap;
     const int64_t next = a.c.next_pos[bi];
     // this CTA's slots [lo, hi), a multiple of 32 per warp
-    const int32_t slice = static_cast<int32_t>((((static_cast<int64_t>(len) + cs - 1) / cs) + kSelThreads - 1) / kSelThreads * kSelThreads);
+    const int32_t slice = static_cast<int32_t>((((static_cast<int64_t>(len) + cs - 1) / cs) + T - 1) / T * T);
     const int32_t lo = static_cast<int32_t>(imin64(len, static_cast<int64_t>(c) * slice));
     const int32_t hi = static_cast<int32_t>(imin64(len, static_cast<int64_t>(lo) + slice)), n = hi - lo;
     auto rank_of = [&](int32_t i) -> uint32_t {
@@ -215,21 +215,21 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
     };
     if constexpr (CACHED) {
 #pragma unroll 8
-        for (int32_t i = tid; i < n; i += kSelThreads) ranks[i] = evict_rank(a, w[lo + i], pos[lo + i], next);
+        for (int32_t i = tid; i < n; i += T) ranks[i] = evict_rank(a, w[lo + i], pos[lo + i], next);
     }
     uint32_t prefix = 0, need = static_cast<uint32_t>(keep);
 #pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = 24 - 8 * pass;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) hist[i * kSelThreads + tid] = 0;
+        for (int i = 0; i < 8192 / T; ++i) hist[i * T + tid] = 0;
         __syncthreads();
         auto put = [&](uint32_t r) {
             if (pass == 0 || (r >> (shift + 8)) == prefix) atomicAdd(&hist[((r >> shift) & 255) * 32 + lane], 1u);
         };
         if constexpr (CACHED) {
 #pragma unroll 2
-            for (int32_t i = tid * 4; i < n; i += kSelThreads * 4) {
+            for (int32_t i = tid * 4; i < n; i += T * 4) {
                 const uint4 r = *reinterpret_cast<const uint4*>(ranks + i);      // (the room is a multiple of 4)
                 put(r.x);
                 if (i + 1 < n) put(r.y);
@@ -238,16 +238,18 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
             }
         } else {
 #pragma unroll 4
-            for (int32_t i = tid; i < n; i += kSelThreads) put(rank_of(i));
+            for (int32_t i = tid; i < n; i += T) put(rank_of(i));
         }
         __syncthreads();
         {
-            // two threads a bin, sixteen columns each (each bin from another bank on)
-            const int bin = tid >> 1, q = tid & 1;
+            // two or four threads a bin, 16 or 8 columns each (each bin from another bank on)
+            constexpr int Q = T / 256, N = 32 / Q;
+            const int bin = tid / Q, q = tid % Q;
             uint32_t s = 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s += hist[bin * 32 + ((q * 16 + i + bin) & 31)];
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            for (int i = 0; i < N; ++i) s += hist[bin * 32 + ((q * N + i + bin) & 31)];
+#pragma unroll
+            for (int o = 1; o < Q; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             if (q == 0) tot[pass & 1][bin] = s;
         }
         // (a buffer is written again two passes on: every CTA has read it by the barrier between)
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
     // Ranks above `prefix` stay, and the first `need` (in slot order) that equal it; where those are all, their
     // order does not matter. Each warp looks after consecutive slots.
     if (need == equal) need = 0xffffffffu;
-    const int32_t seg = slice / kSelWarps, i0 = warp * seg, i1 = min(n, i0 + seg);
+    const int32_t seg = slice / W, i0 = warp * seg, i1 = min(n, i0 + seg);
     const uint32_t below = (1u << lane) - 1;
     // sum of what comes before this warp: earlier CTAs' counts, earlier warps'
     auto before_me = [&](int what) -> uint32_t {
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
     };
     auto total = [&](int what) {
         if (warp == what) {
-            uint32_t s = lane < kSelWarps ? per_warp[what][lane] : 0;
+            uint32_t s = lane < W ? per_warp[what][lane] : 0;
 #pragma unroll
             for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             if (lane == 0) mine[what] = s;
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) cache_evict_select_kernel(cons
     total(2);
     cl.sync();
     uint32_t h0 = before_me(1), t0 = before_me(2);
-    if (c == cs - 1 && warp == kSelWarps - 1 && lane == 0) a.counts[u] = static_cast<int32_t>(h0 + holes);
+    if (c == cs - 1 && warp == W - 1 && lane == 0) a.counts[u] = static_cast<int32_t>(h0 + holes);
     walk([&](int32_t j, uint32_t h, uint32_t t) {
         if ((h >> lane) & 1) a.holes[u * a.m + h0 + __popc(h & below)] = j;
         if ((t >> lane) & 1) a.tails[u * a.m + t0 + __popc(t & below)] = j;
@@ -479,10 +481,11 @@ namespace {
 
 constexpr uint32_t kSelMost = 200 * 1024;      // shared memory of a select CTA, at most
 constexpr uint32_t kMoveBytes = 65536;
+constexpr int64_t kWideSlice = 4096;
 
 // Whether clusters of 16 run on the current device (not every partition of a
 // GPU promises them): asked once per device.
-template <bool CACHED>
+template <bool CACHED, int T>
 bool clusters_of_16()
 {
     static std::atomic<uint64_t> known{0}, yes{0};
@@ -490,14 +493,14 @@ bool clusters_of_16()
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
     const uint64_t bit = uint64_t(1) << dev;
     if (!(known.load(std::memory_order_acquire) & bit)) {
-        auto kern = cache_evict_select_kernel<CACHED>;
+        auto kern = cache_evict_select_kernel<CACHED, T>;
         cudaLaunchConfig_t cfg{};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 16;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3(16);
-        cfg.blockDim = dim3(kSelThreads);
+        cfg.blockDim = dim3(T);
         cfg.dynamicSmemBytes = kSelMost;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
@@ -511,18 +514,23 @@ bool clusters_of_16()
     return yes.load(std::memory_order_relaxed) & bit;
 }
 
-template <bool CACHED>
-cudaError_t launch_select(CacheEvictArgs& a, uint32_t bytes, int64_t units, cudaStream_t s)
+// CTAs of T threads, a cluster of a.cluster for each of `units` heads.
+template <bool CACHED, int T>
+cudaError_t launch_select(CacheEvictArgs& a, int64_t units, cudaStream_t s)
 {
-    auto kern = cache_evict_select_kernel<CACHED>;
+    if (a.cluster == 16 && !clusters_of_16<CACHED, T>()) a.cluster = 8;
+    const int64_t most = (a.c.cap + a.cluster - 1) / a.cluster + T;
+    // a slice's ranks are kept as far as shared memory goes; a longer one's are computed in each pass
+    if (CACHED && most > (kSelMost - kSelFixed) / 4) return launch_select<false, T>(a, units, s);
+    auto kern = cache_evict_select_kernel<CACHED, T>;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = a.cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(units * a.cluster));
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = bytes;
+    cfg.blockDim = dim3(T);
+    cfg.dynamicSmemBytes = kSelFixed + (CACHED ? static_cast<uint32_t>((most + 3) / 4 * 16) : 0u);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -562,12 +570,11 @@ cudaError_t launch_cache_evict(const CacheEvictArgs& a0, cudaStream_t s)
     // CTAs per head: as many as two per SM allow, with 2048 slots each at least
     a.cluster = 1;
     while (a.cluster < 16 && units * a.cluster * 2 <= 304 && a.c.cap / (a.cluster * 2) >= 2048) a.cluster *= 2;
-    // a slice's ranks are kept as far as shared memory goes; a longer one's are computed in each pass
-    auto most = [&]() { return (a.c.cap + a.cluster - 1) / a.cluster + kSelThreads; };
-    auto cached = [&]() { return most() <= (kSelMost - kSelFixed) / 4; };
-    if (a.cluster == 16 && !(cached() ? clusters_of_16<true>() : clusters_of_16<false>())) a.cluster = 8;
-    const cudaError_t e = cached() ? launch_select<true>(a, kSelFixed + static_cast<uint32_t>((most() + 3) / 4 * 16), units, s)
-                                   : launch_select<false>(a, kSelFixed, units, s);
+    // Long slices with an SM each get 1024 threads, else two CTAs of 512 share one: slices of 16385 slots (8 heads,
+    // clusters of 16) 42 us against 44 to 50, of 32770 (16 heads, 8) 73 against 98, of 4096 19.5 against 20.4, of
+    // 2048 16.5 against 15.5.
+    const bool wide = units * a.cluster <= 152 && a.c.cap / a.cluster >= kWideSlice;
+    const cudaError_t e = wide ? launch_select<true, 1024>(a, units, s) : launch_select<true, 512>(a, units, s);
     if (e != cudaSuccess) return e;
     return a.c.d == 64 ? launch_move<64>(a, units, s) : launch_move<128>(a, units, s);
 }
