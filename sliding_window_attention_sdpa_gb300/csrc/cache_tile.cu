@@ -568,7 +568,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                             for (int e = 0; e < 32; ++e)
                                 if (xw + e < sv.new0 && pos[w * 32 + e] < low) s &= ~(1u << e);
                         }
-                        if (xw + 31 >= sv.new0) {
+                        if (xw + 31 >= sv.new0 && !windowed) {
+                            // the mask's bits from the word's first new token on, behind cached keys
+                            const int32_t u = xw - sv.new0;
+                            s &= u >= 64 ? 0u : u >= 0 ? static_cast<uint32_t>(mask >> u)
+                                                       : static_cast<uint32_t>(mask << -u) | ((1u << -u) - 1);
+                        } else if (xw + 31 >= sv.new0) {
 #pragma unroll 1
                             for (int e = 0; e < 32; ++e) {
                                 const int32_t u = xw + e - sv.new0;
