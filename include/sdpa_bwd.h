@@ -57,7 +57,8 @@ typedef enum {
     SDPA_ERR_WORKSPACE = 6,    /* workspace NULL, misaligned or too small */
     SDPA_ERR_BOUNDS = 7        /* device-side, range-checked build only (compiled with
                                   -DSDPA_DEBUG_BOUNDS): a computed index fell outside its
-                                  buffer; the access was skipped */
+                                  buffer; the access was skipped. In a cache's status
+                                  (sdpa_cache.h): a page-table entry out of its range */
 } sdpa_status_t;
 
 enum { SDPA_BF16 = 0, SDPA_F16 = 1 };

@@ -65,9 +65,9 @@ struct CacheFwdArgs {
     CacheFwdCut* cuts;
 };
 
-// The tile kernel's, and the rows kernel's at d = 64: TMA descriptors of the pools' pages (4-D: d, head, row,
-// page) in boxes of 64 features x box_rows rows with the 128-byte swizzle;
-// box_rows 0: none, every row is gathered.
+// The tile and the rows kernel's: TMA descriptors of the pools' pages (4-D: d,
+// head, row, page) in boxes of 64 features x box_rows rows with the 128-byte
+// swizzle; box_rows 0: none, every row is gathered.
 struct CacheTileArgs {
     CUtensorMap tm_k, tm_v;
     CacheFwdArgs f;

@@ -567,7 +567,8 @@ cudaError_t launch_cache_evict(const CacheEvictArgs& a0, cudaStream_t s)
     CacheEvictArgs a = a0;
     const int64_t units = a.c.b * a.c.h_kv;
     if (units == 0 || a.c.cap <= a.keep) return cudaSuccess;
-    // CTAs per head: as many as two per SM allow, with 2048 slots each at least
+    // CTAs per head: as many as two per SM allow, with 2048 slots each at least (8 heads of 16384 slots: 13.8 us,
+    // 18.4 with 1024 at least, 15.3 with 4096; 12 of 16484: 15.8, 18.9, 17.3)
     a.cluster = 1;
     while (a.cluster < 16 && units * a.cluster * 2 <= 304 && a.c.cap / (a.cluster * 2) >= 2048) a.cluster *= 2;
     // Long slices with an SM each get 1024 threads, else two CTAs of 512 share one: slices of 16385 slots (8 heads,

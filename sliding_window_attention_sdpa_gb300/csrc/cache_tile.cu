@@ -6,16 +6,29 @@
 //   P  16-bit, written over its S's columns, the A operand of P V from TMEM
 //   O  [128 rows x d]        TMEM, one for each slot
 // A slot's next S is computed while its softmax works on this one, and the two
-// slots keep the tensor core and the softmax warps busy in turn. With more than 128 rows the slots
-// are the unit's two row tiles and share each K/V tile; with fewer they take
-// the same rows and every other key tile, and their sums are joined at the end.
-// So K and V are read once per 256 rows, and a short row block loses no overlap.
+// slots keep the tensor core and the softmax warps busy in turn. With more than
+// 128 rows the slots are the unit's two row tiles and share each K/V tile; with
+// fewer they take the same rows and every other key tile, and their sums are
+// joined at the end. So K and V are read once per 256 rows, and a short row
+// block loses no overlap.
+//
+// Bound by reading K and V up to 128 rows (12 sequences of 16484 keys, 6
+// kv-heads, d = 128: 113 us at 128 rows, 5.4 TB/s), then by the softmax groups'
+// chain from a tile's S to its P (256 rows 142 us; 512, each half reading K and V
+// again, 255 us, 1.2 PFLOP/s): its phases wait on the tensor memory's loads and
+// the exponentials in turn, with the tensor core a third of the time idle. Two
+// threads a row and 640 threads did not shorten it (256 rows: 161 us against 147
+// then), and splitting P as the rows kernel does costs 16 % (512 rows: 304 us
+// against 263 then).
 //
 // Roles (384 threads): warp 0 loads K, warp 1 V into two rings in the 128-byte
 // swizzle; warps 2 and 3 issue a slot's MMAs each (one warp for both was the
 // bottleneck: its issue of a tile's 12 MMAs takes longer than they run);
-// warps 4-7 and 8-11 are the slots' softmax groups, one row per thread. A row's reference moves only when a score exceeds it by 2^8, so O is
-// seldom rescaled. P is rounded to the I/O dtype, as the prompt's forward does.
+// warps 4-7 and 8-11 are the slots' softmax groups, one row per thread. A row's
+// reference moves only when a score exceeds it by 2^8, so O is seldom rescaled.
+// P is rounded to the I/O dtype, as the prompt's forward does: half a step of a
+// P next to a sum that stays in fp32, which leaves O's error within 1.4 times
+// that of rounding O alone.
 //
 // The steps of all units form one line that the persistent CTAs cut evenly, as
 // in cache_fwd.cu; partials of cut units go to the same join.
