@@ -591,10 +591,12 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
 // Adds the partials of a unit that was cut between parts, in the order of the
 // parts. CTA x looks after cuts[x].
 // SPREAD: CTA y takes row y, its warps every eighth part (few units, many
-// parts each); else CTA y takes 8 rows, a warp each with all its parts.
-template <int HD, bool BF16, int ROWS, bool SPREAD>
+// parts each); else a warp takes RW rows, all their parts, with the rows' loads
+// on their way together.
+template <int HD, bool BF16, int ROWS, bool SPREAD, int RW>
 __global__ void __launch_bounds__(256) cache_fwd_join_kernel(const __grid_constant__ CacheFwdArgs a)
 {
+    static_assert(RW == 1 || !SPREAD, "");
     constexpr int E = HD / 32;
     __shared__ float sh_x[8][HD], sh_s[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -609,49 +611,63 @@ __global__ void __launch_bounds__(256) cache_fwd_join_kernel(const __grid_consta
     auto slot = [&](int i) -> int64_t { return i == 0 ? c0 * int64_t(2) + cut.slot0 : (c0 + i) * int64_t(2); };
     int nq = a.s_q;
     if (a.seq_q_lens) nq = max(0, min(a.seq_q_lens[cut.bi], a.s_q));
-    {
-        const int r = SPREAD ? blockIdx.y : blockIdx.y * 8 + warp;
-        const int rr = r0 + r;
-        if (rr >= R) return;
-        float top = -INFINITY;
-        for (int i = lane; i < n; i += 32) top = fmaxf(top, a.part_ml[(slot(i) * ROWS + r) * 2]);
+    // this warp's rows (of a unit's ROWS: the partials of all of them are there, whatever the last real one)
+    const int r = SPREAD ? blockIdx.y : (blockIdx.y * 8 + warp) * RW;
+    if (r0 + r >= R) return;
+    float top[RW], sum[RW], x[RW][E];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float sum = 0.f, x[E];
+    for (int j = 0; j < RW; ++j) {
+        top[j] = -INFINITY;
+        sum[j] = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = 0.f;
-#pragma unroll 8
-        for (int i = SPREAD ? warp : 0; i < n; i += SPREAD ? 8 : 1) {
-            const int64_t at = slot(i) * ROWS + r;
-            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-            const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
-            sum += f * ml.y;
-            const float* p = a.part_o + at * HD + lane * E;
+        for (int e = 0; e < E; ++e) x[j][e] = 0.f;
+    }
+    for (int i = lane; i < n; i += 32) {
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 v = *reinterpret_cast<const float2*>(p + e);
-                x[e] += f * v.x;
-                x[e + 1] += f * v.y;
-            }
+        for (int j = 0; j < RW; ++j) top[j] = fmaxf(top[j], a.part_ml[(slot(i) * ROWS + r + j) * 2]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < RW; ++j) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+#pragma unroll(RW == 1 ? 8 : 2)
+    for (int i = SPREAD ? warp : 0; i < n; i += SPREAD ? 8 : 1) {
+        const int64_t at = slot(i) * ROWS + r;
+#pragma unroll
+        for (int j = 0; j < RW; ++j) {
+            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (at + j) * 2);
+            const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top[j]);
+            sum[j] += f * ml.y;
+            const float* p = a.part_o + (at + j) * HD + lane * E;
+            float v[E];
+            if constexpr (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
+            else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p);
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[j][e] += f * v[e];
         }
-        if (SPREAD) {
+    }
+    if (SPREAD) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) sh_x[warp][lane * E + e] = x[e];
-            if (lane == 0) sh_s[warp] = sum;
-            __syncthreads();
-            if (warp > 0) return;
-            sum = 0.f;
+        for (int e = 0; e < E; ++e) sh_x[warp][lane * E + e] = x[0][e];
+        if (lane == 0) sh_s[warp] = sum[0];
+        __syncthreads();
+        if (warp > 0) return;
+        sum[0] = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = 0.f;
+        for (int e = 0; e < E; ++e) x[0][e] = 0.f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                sum += sh_s[w];
+        for (int w = 0; w < 8; ++w) {
+            sum[0] += sh_s[w];
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[e] += sh_x[w][lane * E + e];
-            }
+            for (int e = 0; e < E; ++e) x[0][e] += sh_x[w][lane * E + e];
         }
+    }
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+        const int rr = r0 + r + j;
+        if (rr >= R) break;
         const int tok = rr / a.group;
-        store_row<BF16, E>(a, cut.bi, tok, gk * a.group + (rr - tok * a.group), lane * E, tok < nq, top, sum, x);
+        store_row<BF16, E>(a, cut.bi, tok, gk * a.group + (rr - tok * a.group), lane * E, tok < nq, top[j], sum[j], x[j]);
     }
 }
 
@@ -666,7 +682,8 @@ cudaError_t launch_join(const CacheFwdArgs& a, cudaStream_t s)
     // with fewer units than an eighth of the parts a unit has many parts
     const bool spread = units * 8 < a.parts;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.cut_by_unit ? units : a.parts), spread ? most : (most + 7) / 8);
+    constexpr int RW = ROWS == 8 ? 1 : 4, CR = 8 * RW;      // rows of a warp, of a CTA
+    cfg.gridDim = dim3(static_cast<unsigned>(a.cut_by_unit ? units : a.parts), spread ? most : (most + CR - 1) / CR);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -674,8 +691,8 @@ cudaError_t launch_join(const CacheFwdArgs& a, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return spread ? cudaLaunchKernelEx(&cfg, cache_fwd_join_kernel<HD, BF16, ROWS, true>, a)
-                  : cudaLaunchKernelEx(&cfg, cache_fwd_join_kernel<HD, BF16, ROWS, false>, a);
+    return spread ? cudaLaunchKernelEx(&cfg, cache_fwd_join_kernel<HD, BF16, ROWS, true, 1>, a)
+                  : cudaLaunchKernelEx(&cfg, cache_fwd_join_kernel<HD, BF16, ROWS, false, RW>, a);
 }
 
 template <int HD, bool BF16, int NT>
