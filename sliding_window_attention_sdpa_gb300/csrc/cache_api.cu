@@ -356,12 +356,12 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.part_ml = at<float>(ws, l.part_ml);
     a.cuts = at<swa::CacheFwdCut>(ws, l.cuts);
     if (c->n_pages > 0) {
-        // boxes that divide a page: up to 64 rows (a key tile) for the tile kernel, 16 for the other; an unpaged
+        // boxes that divide a page, of 8 rows at least: up to 64 (a key tile) for the tile kernel, 16 for the other; an unpaged
         // sequence's keys follow one another
         const bool tiles = plan.variant >= swa::kTiles128;
         int32_t rows = tiles ? 64 : 16;
         while (c->page_table != nullptr && c->page_size % rows != 0) rows >>= 1;
-        if (rows >= (tiles ? 8 : 16) &&
+        if (rows >= 8 &&
             make_rows_map(&ta.tm_k, c->k, c->dtype, c->d, c->h_kv, c->page_size, c->n_pages, c->k_stride, rows) &&
             make_rows_map(&ta.tm_v, c->v, c->dtype, c->d, c->h_kv, c->page_size, c->n_pages, c->v_stride, rows))
             ta.box_rows = rows;

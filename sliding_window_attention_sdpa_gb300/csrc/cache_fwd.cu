@@ -8,8 +8,8 @@
 // Few rows (cache_fwd_rows_kernel): the call is bound by reading K and V once,
 // so every row of a kv-head is computed by the warp that reads a key. A warp
 // fetches 16 keys of 128 features (32 of 64) a step into a ring of its own: by
-// TMA boxes of 16 keys where a page's size is a multiple of 16 (or the keys are
-// one run), else by one bulk copy per key and tensor. A copy of a single row of
+// TMA boxes of 16 or 8 keys where a page's size is a multiple of it (or the keys
+// are one run), else by one bulk copy per key and tensor. A copy of a single row of
 // 128 bytes costs the engine what one of 256 does (4.3 TB/s in all, against
 // 7.0). Through registers (LDG) or cp.async the same loads reached 6.0 and 4.3
 // TB/s at d = 128: 16 instructions a step and warp instead of one. A warp waits
@@ -90,7 +90,7 @@ struct RowsCfg {
     static_assert(2 * GK * kPitch <= kStage, "");
 };
 
-// A box of 16 keys x 64 features (from c0) of one head of a page.
+// A box of box_rows keys x 64 features (from c0) of one head of a page.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int head, int row,
                                         int page)
 {
@@ -300,21 +300,23 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
             const uint32_t oks = __ballot_sync(0xffffffffu, ok);
             if (lane < GK) sh_pos[warp][st][lane] = k.pos;
             if (boxed) {
-                // a group's boxes (2 KB each: features 0-63, 64-127 of K, of V) begin at its first key; rows of the
-                // page behind the last key come along
-                constexpr int BOXES = 2 * (HD / 64) * KG;
-                const uint32_t groups = ((oks & 0xffffu) != 0) + (KG == 2 && oks >> 16 != 0);
+                // boxes of 16 or 8 keys (2 or 1 KB each: features 0-63, 64-127 of K, of V); rows of the page in front
+                // of the first key in reach and behind the last one come along
+                const int bk = ta.box_rows, nu = GK / bk;                 // keys of a box, boxes over a step's keys
+                const uint32_t of_box = (1u << bk) - 1;
+                // one lane a box
+                const int u = lane % nu, b = lane / nu, is_v = b / (HD / 64), cb = b % (HD / 64);
+                const int row0 = __shfl_sync(0xffffffffu, static_cast<int>(row), u * bk);
+                const int page0 = __shfl_sync(0xffffffffu, static_cast<int>(page), u * bk);
+                const bool mine = b < 2 * (HD / 64) && ((oks >> (u * bk)) & of_box) != 0;
+                const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
                 if (lane == 0) {
                     sh_ok[warp][st] = oks;
-                    mbar_arrive_expect_tx(bar, groups * (2 * (HD / 64) * 2048));
+                    mbar_arrive_expect_tx(bar, boxes * bk * 128);
                 }
                 __syncwarp();
-                // one lane a box
-                const int u = lane % KG, b = lane / KG, is_v = b / (HD / 64), cb = b % (HD / 64);
-                const int row0 = __shfl_sync(0xffffffffu, static_cast<int>(row), u * 16);
-                const int page0 = __shfl_sync(0xffffffffu, static_cast<int>(page), u * 16);
-                if (lane < BOXES && ((oks >> (u * 16)) & 0xffffu))
-                    tma_box(at + (is_v ? half : 0u) + cb * (GK * 128) + u * 2048, is_v ? &ta.tm_v : &ta.tm_k, bar, cb * 64,
+                if (mine)
+                    tma_box(at + (is_v ? half : 0u) + cb * (GK * 128) + u * bk * 128, is_v ? &ta.tm_v : &ta.tm_k, bar, cb * 64,
                             static_cast<int>(gk), row0, page0);
             } else {
                 if (lane == 0) {

@@ -74,6 +74,10 @@ FORWARD = {
     "page_of_one": ([5, 40], 2, 2, 2, 64, "f16", 1, -1, {}),
     "odd_pages": ([100, 7, 213], 3, 6, 2, 128, "bf16", 7, -1, {}),
     "pages_of_24": ([100, 24, 213, 48], 1, 16, 2, 64, "bf16", 24, -1, {}),
+    "pages_of_8": ([100, 8, 213, 47, 0, 130], 1, 8, 2, 64, "bf16", 8, -1, {}),
+    "pages_of_8_d128": ([100, 8, 213, 47, 0, 130], 2, 4, 1, 128, "f16", 8, 77, dict(sink=True)),
+    "pages_of_24_d128": ([100, 24, 213, 47], 1, 8, 2, 128, "bf16", 24, -1, dict(evicted=True)),
+    "pages_of_40": ([1100, 24, 213, 47], 3, 10, 2, 64, "f16", 40, 500, {}),
     "one_run": ([100, 7, 213], 4, 6, 2, 64, "bf16", 0, -1, {}),
     "window": ([5, 130, 700, 129, 128], 1, 8, 2, 64, "bf16", 64, 128, {}),
     "window_zero": ([0, 130, 64], 3, 4, 2, 64, "bf16", 16, 0, {}),
@@ -226,7 +230,7 @@ def test_forward_padding_tokens_hold_anything(t, d, h_q):
     close("o", o, ref.o, ref.tol_o)
 
 
-@pytest.mark.parametrize("page", [4, 16, 64, 0])
+@pytest.mark.parametrize("page", [4, 8, 16, 64, 0])
 @pytest.mark.parametrize("t,d", [(1, 64), (2, 64), (2, 128), (40, 128), (40, 64)])
 def test_forward_in_front_of_the_window(t, d, page):
     """Keys in front of every row's window may hold anything, pages in front of
