@@ -109,6 +109,9 @@ FORWARD = {
     "short_units_three_tiles": ([3, 60, 1, 0, 130, 5, 700], 37, 8, 1, 128, "bf16", 16, -1, dict(tree=True)),
     "short_units_few_rows": ([3, 60, 64, 65, 1, 0, 7, 130, 20, 5] * 6 + [900], 1, 8, 2, 128, "bf16", 64, -1, {}),
     "mha_many_rows": ([333, 130], 48, 3, 3, 64, "bf16", 64, -1, dict(tree=True)),
+    # more sequences than a CTA has threads
+    "b_700": ([(37 * i) % 40 for i in range(700)] + [600], 1, 2, 1, 64, "bf16", 64, -1, {}),
+    "b_700_many_rows": ([(37 * i) % 40 for i in range(700)] + [600], 3, 8, 1, 128, "bf16", 64, -1, {}),
 }
 
 
@@ -471,6 +474,8 @@ WEIGH = {
     "rounds_evicted": ([300, 500], 70, 8, 1, 128, "bf16", 64, 100, dict(evicted=True, pos=True)),
     "short_units": ([(37 * i) % 90 for i in range(70)] + [1500], 2, 8, 4, 64, "bf16", 16, -1, {}),
     "short_units_window": ([(37 * i) % 90 for i in range(70)] + [1500], 3, 8, 4, 128, "bf16", 16, 5, dict(pos=True)),
+    "b_700": ([(37 * i) % 40 for i in range(700)] + [600], 1, 2, 1, 64, "bf16", 64, -1, {}),
+    "b_700_many_rows": ([(37 * i) % 40 for i in range(700)] + [600], 17, 4, 1, 64, "f16", 64, -1, dict(pos=True)),
 }
 
 
@@ -572,6 +577,23 @@ def test_evict(lens, keep, first, recent, d, page):
     # at the budget: a second call changes nothing
     swa.cache_evict(c, keep, first=first, recent=recent, check_status=True)
     same_cache(c, want)
+
+
+@pytest.mark.parametrize("lens,cap", [([5000], 900000), ([20, 100, 101, 300] * 20, 50000), ([20, 100, 101, 300] * 20, 40000)])
+def test_evict_with_room_for_many_keys(lens, cap):
+    """The room, not the keys, says how a head is cut and whether its ranks are
+    kept: few heads with much room, many heads with more than shared memory
+    holds and with less."""
+    import sliding_window_attention_sdpa_gb300 as swa
+    lay = R.make(90, lens, 2, 64, "bf16", 64, evicted=True)
+    more = -(-cap // 64) - lay.table.shape[1]
+    b, h_kv = len(lens), 2
+    lay.table = torch.cat([lay.table, torch.full((b, more), -1, dtype=torch.int32)], 1)
+    lay.positions = torch.cat([lay.positions, torch.full((b, h_kv, more * 64), -5, dtype=torch.int32)], 2)
+    lay.weights = torch.cat([lay.weights, torch.full((b, h_kv, more * 64), math.nan)], 2)
+    c = gpu_cache(lay)
+    swa.cache_evict(c, 100, first=4, recent=20, check_status=True)
+    same_cache(c, R.evict(lay, 100, 4, 20))
 
 
 @pytest.mark.parametrize("kind", ["all_equal", "special", "close", "negative"])
