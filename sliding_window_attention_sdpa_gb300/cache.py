@@ -269,9 +269,12 @@ class KVCache:
         self._ref, self._key, self._index = ctypes.addressof(c), (b, h_kv, d, dev, k.dtype), dev.index or 0
         self._ws_bytes = {}     # workspace bytes of the calls made so far, by their sizes
 
+    _own = frozenset(("k", "v", "lengths", "page_table", "next_pos", "positions", "weights", "status", "params", "capacity",
+                      "b", "h_kv", "d", "dtype", "device"))
+
     def __setattr__(self, name, value):
         # the calls use the addresses taken by the constructor: another tensor under the name would not be seen
-        if "_ws_bytes" in self.__dict__:
+        if name in self._own and "_ws_bytes" in self.__dict__:
             raise AttributeError(f"{name}: a cache's tensors are changed in place (or make another KVCache)")
         super().__setattr__(name, value)
 

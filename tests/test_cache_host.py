@@ -250,11 +250,13 @@ def test_calls_refuse_wrong_tensors():
 def test_cache_attributes_are_not_replaced():
     """The calls use the addresses that the constructor took."""
     c = tensors()
-    for name in ("k", "v", "lengths", "page_table", "positions", "weights", "status", "anything"):
+    for name in ("k", "v", "lengths", "page_table", "positions", "weights", "status", "capacity"):
         with pytest.raises(AttributeError, match=name):
             setattr(c, name, torch.zeros(2, dtype=torch.int32))
     c.lengths[0] = 3
     assert c.lengths.tolist() == [3, 0]
+    c.layer = 7                             # a user's own names are free
+    assert c.layer == 7
 
 
 def test_rows_up_to_the_32_bit_limit():
