@@ -94,9 +94,9 @@ size_t sdpa_cache_evict_params_bytes(void);
  * does, where it has more.
  * Keys on pages out of range are left out; lengths out of [0, capacity] are
  * taken as the nearer end. Not read, or without effect whatever they hold, are
- * slots behind a sequence's keys, without positions those in front of every
- * row's window, and new tokens that no row admits. The other keys' K and V have
- * to be finite, those too that only some rows admit: a masked V meets a P of 0.
+ * slots behind a sequence's keys, keys that no row's window has, and new tokens
+ * that no row admits. The other keys' K and V have to be finite, those too that
+ * only some rows admit: a masked V meets a P of 0.
  */
 typedef struct sdpa_cache_fwd_params {
     int64_t s_q, h_q;                    /* new tokens per sequence (1..64), q-heads */

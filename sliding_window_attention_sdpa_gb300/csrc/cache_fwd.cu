@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
         uint4 q[NT][CH];
         int row_tok[NT][2];           // the row's token, -1: admits nothing
         int32_t row_low[NT][2];       // lowest position in the row's window
-        int32_t low_max = INT32_MIN;  // the highest of them (this CTA's rows)
+        int32_t low_max = INT32_MIN, low_min = INT32_MAX;  // the highest and the lowest of them (this CTA's rows)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = r0 + n * 8 + g;
@@ -230,11 +230,17 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
                 if (a.window_left >= 0)
                     row_low[n][e] = static_cast<int32_t>(
                         imax64(INT32_MIN, imin64(INT32_MAX, npos + __popcll(m) - 1 - a.window_left)));
-                if (m) low_max = max(low_max, row_low[n][e]);
+                if (m) {
+                    low_max = max(low_max, row_low[n][e]);
+                    low_min = min(low_min, row_low[n][e]);
+                }
             }
         }
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) low_max = max(low_max, __shfl_xor_sync(0xffffffffu, low_max, o));
+        for (int o = 1; o < 4; o <<= 1) {
+            low_max = max(low_max, __shfl_xor_sync(0xffffffffu, low_max, o));
+            low_min = min(low_min, __shfl_xor_sync(0xffffffffu, low_min, o));
+        }
 
         // ---- the line of keys of this unit: groups of GK per warp
         auto step_x = [&](int32_t s) -> int32_t { return (tile0 + s) * TK + warp * GK; };
@@ -244,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
             int32_t entry;    // page-table entry
             int32_t pos;      // cached key's position
         };
+        const bool by_pos = kpos != nullptr && a.window_left >= 0;
         auto fetch_key = [&](int32_t s) -> Key {
             Key k{0, 0};
             const int32_t x = step_x(s) + lane % GK;
@@ -254,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
                         k.entry = a.c.page_table[bi * a.c.max_pages +
                                                  (a.c.page_shift >= 0 ? static_cast<uint32_t>(j) >> a.c.page_shift
                                                                       : static_cast<uint32_t>(j) / a.c.page_size)];
-                    k.pos = kpos && a.window_left >= 0 ? kpos[j] : j;
+                    k.pos = by_pos ? kpos[j] : j;
                 }
             }
             return k;
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
             bool ok = x < sv.new0 && j < sv.len;        // a cached key
             int64_t page = bi;
             uint32_t row = j;
-            const bool reach = ok && j >= sv.first;
+            const bool reach = ok && (by_pos ? k.pos >= low_min : j >= sv.first);
             if (ok && a.c.page_table) {
                 page = k.entry;
                 row = a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)

@@ -254,6 +254,35 @@ def test_forward_in_front_of_the_window(t, d, page):
     close("o", o, ref.o, ref.tol_o)
 
 
+@pytest.mark.parametrize("page", [7, 8, 64])
+@pytest.mark.parametrize("t,d,tree", [(1, 64, False), (2, 128, False), (13, 64, True), (40, 128, False), (40, 64, True)])
+def test_forward_out_of_the_window_by_position(t, d, tree, page):
+    """The same where positions say which keys the windows have: keys in any
+    slot that no row's window has may hold anything."""
+    lens, h_q, h_kv, window = [301, 100, 77, 700], 4, 2, 60
+    lay = R.make(68, lens, h_kv, d, "bf16", page, evicted=True)
+    gone = 0
+    for i, n in enumerate(lens):
+        for h in range(h_kv):
+            out = [j for j in range(n) if int(lay.positions[i, h, j]) < int(lay.next_pos[i]) - window]
+            pg, at = lay.where(i, out)
+            lay.k[pg, at, h], lay.v[pg, at, h] = math.nan, math.nan
+            gone += len(out)
+        # a page of which no head's windows have a key may be gone
+        if page:
+            for p in range(-(-n // page)):
+                if int(lay.positions[i, :, p * page:min(n, (p + 1) * page)].max()) < int(lay.next_pos[i]) - window:
+                    lay.table[i, p] = -1
+    assert gone > 1000
+    q, k, v = inputs(69, len(lens), t, h_q, h_kv, d, "bf16")
+    masks = R.tree_masks(70, len(lens), t) if tree else None
+    kw = dict(scale=d ** -0.5, window=window, tree=masks, q_lens=None, sink=None)
+    o, lse = call_forward(gpu_cache(lay), dev(q), dev(k), dev(v), kw, check_status=True)
+    ref = R.forward(lay, q, k, v, **kw)
+    close("lse", lse, ref.lse, ref.tol_lse)
+    close("o", o, ref.o, ref.tol_o)
+
+
 @pytest.mark.parametrize("t,d", [(1, 64), (40, 128)])
 def test_forward_pages_shared_by_sequences(t, d):
     """A common prefix on the same pages, read by all of its sequences; what is
