@@ -348,15 +348,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 used[1] |= __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m >> 32));
             }
             // lowest position in any row's window
-            const int64_t npos = a.c.next_pos ? a.c.next_pos[g.bi] : sv.len;
-            const int32_t low = static_cast<int32_t>(imax64(INT32_MIN, imin64(INT32_MAX,
-                npos + static_cast<int32_t>(__reduce_min_sync(0xffffffffu, shallow)) - 1 - a.window_left)));
-            // the positions of the lane's keys, a tile ahead (the K warp puts them down for the softmax)
-            auto pos_of = [&](int32_t t, int k) -> int32_t {
-                const int32_t j = sv.lo + t * kKeys + k * 32 + lane;
-                return kpos && t <= t1 && j < sv.len ? kpos[j] : j;
-            };
-            int32_t pos_a = pos_of(t0, 0), pos_b = pos_of(t0, 1);
+            int32_t low = INT32_MIN;
+            if (kpos != nullptr) {
+                const int64_t npos = a.c.next_pos[g.bi];
+                low = static_cast<int32_t>(imax64(INT32_MIN, imin64(INT32_MAX,
+                    npos + static_cast<int32_t>(__reduce_min_sync(0xffffffffu, shallow)) - 1 - a.window_left)));
+            }
             const int boxes = ta.box_rows ? kKeys / ta.box_rows : 0;
             // a TMA tile's page of lane's box, a tile ahead
             auto box_entry = [&](int32_t t) -> int32_t {
@@ -369,12 +366,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 const int32_t x0 = t * kKeys, j0 = sv.lo + x0;
                 const int32_t mine = entry;
                 entry = box_entry(t + 1);
-                const int32_t pos[2] = {pos_a, pos_b};
-                pos_a = pos_of(t + 1, 0);
-                pos_b = pos_of(t + 1, 1);
+                // the positions of the lane's keys (the K warp puts them down for the softmax)
+                int32_t pos[2] = {INT32_MAX, INT32_MAX};
+                if (kpos != nullptr) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int32_t j = j0 + k * 32 + lane;
+                        pos[k] = j < sv.len ? kpos[j] : j;
+                    }
+                }
                 // (a V that no row's window has may be anything, and would meet a P of 0)
-                const bool good = (lane >= boxes || (mine >= 0 && mine < a.c.n_pages)) &&
-                                  (!is_v || kpos == nullptr || (pos[0] >= low && pos[1] >= low));
+                const bool good = (lane >= boxes || (mine >= 0 && mine < a.c.n_pages)) && (!is_v || (pos[0] >= low && pos[1] >= low));
                 const bool by_tma = boxes > 0 && j0 >= sv.first && x0 + kKeys <= sv.new0 && j0 + kKeys <= sv.len &&
                                     __all_sync(0xffffffffu, good);
                 if (!(ok = acquire(empty0 + st, par ^ 1))) break;
@@ -382,7 +384,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 if (!is_v && a.window_left >= 0) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        reinterpret_cast<int32_t*>(sm + C::kPos)[(it % kRing) * kKeys + k * 32 + lane] = pos[k];
+                        reinterpret_cast<int32_t*>(sm + C::kPos)[(it % kRing) * kKeys + k * 32 + lane] =
+                            kpos != nullptr ? pos[k] : j0 + k * 32 + lane;
                     }
                 }
                 if (by_tma) {
@@ -410,7 +413,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                     const uint16_t* p = fresh;
                     bool have = false;
                     if (x < sv.new0) {
-                        if (j >= sv.first && j < sv.len && (kpos == nullptr || (k ? pos[1] : pos[0]) >= low)) {
+                        if (j >= sv.first && j < sv.len && (k ? pos[1] : pos[0]) >= low) {
                             const int32_t page = entry_of(j);
                             have = page >= 0 && page < a.c.n_pages;
                             if (!have) set_status(a.c.status, SDPA_ERR_BOUNDS);
