@@ -189,6 +189,19 @@ size_t sdpa_cache_evict_workspace_bytes(const sdpa_cache *cache, const sdpa_cach
 sdpa_status_t sdpa_cache_evict(const sdpa_cache *cache, const sdpa_cache_evict_params *params, void *workspace,
                                size_t workspace_bytes, void *stream);
 
+/*
+ * Test-only hook of the bounded waits (defaults: 2 s, no flags). A wait that
+ * runs out records SDPA_ERR_TIMEOUT: the kernel sends no more copies, lets
+ * those and the products in flight finish, frees its tensor memory and returns.
+ * This call changes, for the calling thread's later calls on any cache:
+ *   wait_limit_ns  the bound of every device wait (<= 0: the default);
+ *   flags          bit 0: an early copy of each stretch of work is left out, so
+ *                  that the wait for it runs out; 0: normal operation.
+ * Returns SDPA_ERR_INVALID_ARG for undefined flag bits. Call it with (0, 0) to
+ * restore normal operation.
+ */
+sdpa_status_t sdpa_cache_test_hook(int64_t wait_limit_ns, int32_t flags);
+
 /* Synchronises `stream`, returns the cache's status word and clears it. */
 sdpa_status_t sdpa_cache_check_status(const sdpa_cache *cache, void *stream);
 

@@ -70,7 +70,7 @@ ENTRY_POINTS = ("sdpa_cache_bytes", "sdpa_cache_fwd_params_bytes", "sdpa_cache_a
                 "sdpa_cache_weigh_params_bytes", "sdpa_cache_evict_params_bytes",
                 "sdpa_cache_fwd_workspace_bytes", "sdpa_cache_fwd", "sdpa_cache_append",
                 "sdpa_cache_weigh", "sdpa_cache_evict_workspace_bytes", "sdpa_cache_evict",
-                "sdpa_cache_check_status")
+                "sdpa_cache_check_status", "sdpa_cache_test_hook")
 
 
 def bind(lib) -> None:
@@ -88,6 +88,7 @@ def bind(lib) -> None:
         f = getattr(lib, f"sdpa_cache_{name}")
         f.argtypes, f.restype = [C, ctypes.POINTER(params), _vp], st
     lib.sdpa_cache_check_status.argtypes, lib.sdpa_cache_check_status.restype = [C, _vp], st
+    lib.sdpa_cache_test_hook.argtypes, lib.sdpa_cache_test_hook.restype = [_i64, _i32], st
 
 
 def _lib():
@@ -164,6 +165,12 @@ def sdpa_cache_evict(cache, params, workspace: int, workspace_bytes: int, stream
 
 def sdpa_cache_check_status(cache, stream: int) -> int:
     return _lib().sdpa_cache_check_status(cache, stream)
+
+
+def sdpa_cache_test_hook(wait_limit_ns: int, flags: int) -> int:
+    """Test-only: device wait limit, and copies left out so that waits run out,
+    for this thread's later cache calls ((0, 0) restores normal operation)."""
+    return _lib().sdpa_cache_test_hook(wait_limit_ns, flags)
 
 
 # ------------------------------------------------------------- torch helpers

@@ -17,7 +17,13 @@ using swa::api::cuda_status;
 using swa::api::fail;
 using swa::api::make_rows_map;
 
+// sdpa_cache_test_hook's settings for this thread's next calls.
 constexpr int64_t kWaitLimitNs = 2000000000LL;
+thread_local int64_t g_test_wait_ns = 0;
+thread_local int32_t g_test_stall = 0;
+
+int64_t wait_limit() { return g_test_wait_ns > 0 ? g_test_wait_ns : kWaitLimitNs; }
+
 constexpr int64_t kMax31 = int64_t(1) << 31;
 // a sequence's keys, rounded up to tiles, are numbered in 32 bits
 constexpr int64_t kMaxCap = kMax31 - (int64_t(1) << 16);
@@ -139,6 +145,7 @@ swa::CacheView view_of(const sdpa_cache* c)
     v.positions = c->positions;
     v.weights = c->weights;
     v.status = c->status;
+    v.stall = g_test_stall;
     return v;
 }
 
@@ -351,7 +358,7 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.whole = l.whole;
     a.cut_by_unit = fwd_size(c, p, plan).units <= l.parts;
     a.unit_cost = plan.unit_cost;
-    a.timeout_ns = kWaitLimitNs;
+    a.timeout_ns = wait_limit();
     a.part_o = at<float>(ws, l.part_o);
     a.part_ml = at<float>(ws, l.part_ml);
     a.cuts = at<swa::CacheFwdCut>(ws, l.cuts);
@@ -427,7 +434,7 @@ sdpa_status_t sdpa_cache_weigh(const sdpa_cache* c, const sdpa_cache_weigh_param
     copy3(a.q_stride, p->q_stride);
     a.lse = p->lse;
     a.q_pos = p->q_pos;
-    a.timeout_ns = kWaitLimitNs;
+    a.timeout_ns = wait_limit();
     // a CTA per SM, fewer if there are fewer tiles of 128 keys
     const double tiles = double(c->b) * double(c->h_kv) * double((c->page_size * c->max_pages + 127) / 128);
     a.parts = tiles < 152 ? static_cast<int32_t>(tiles) : 152;
@@ -467,8 +474,17 @@ sdpa_status_t sdpa_cache_evict(const sdpa_cache* c, const sdpa_cache_evict_param
     a.holes = at<int32_t>(ws, l.holes);
     a.tails = at<int32_t>(ws, l.tails);
     a.counts = at<int32_t>(ws, l.counts);
-    a.timeout_ns = kWaitLimitNs;
+    a.timeout_ns = wait_limit();
     return cuda_status(swa::launch_cache_evict(a, static_cast<cudaStream_t>(stream)), "cache evict launch");
+}
+
+sdpa_status_t sdpa_cache_test_hook(int64_t wait_limit_ns, int32_t flags)
+{
+    if (flags & ~1) return fail(SDPA_ERR_INVALID_ARG, "test hook flags=%d: only bit 0 is defined", flags);
+    g_test_wait_ns = wait_limit_ns > 0 ? wait_limit_ns : 0;
+    g_test_stall = flags;
+    clear_error();
+    return SDPA_OK;
 }
 
 sdpa_status_t sdpa_cache_check_status(const sdpa_cache* c, void* stream)

@@ -23,6 +23,7 @@ struct CacheView {
     int32_t *lengths, *next_pos, *positions;
     float* weights;
     int32_t* status;
+    int32_t stall;                  // test hook: a copy that a wait is for is left out
 };
 
 // A unit of the forward's work that is cut between parts: its sequence (-1:

@@ -454,6 +454,8 @@ __global__ void __launch_bounds__(128) cache_evict_move_kernel(const __grid_cons
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(RB) : "memory");
     };
     uint32_t par[2] = {0u, 0u};
+    // (test hook: this warp's second round never comes)
+    const int64_t never = a.c.stall ? i0 + step : -1;
     look(i0);
     if (i0 < n) send(0, i0);
     int r = 0;
@@ -461,9 +463,11 @@ __global__ void __launch_bounds__(128) cache_evict_move_kernel(const __grid_cons
         // the other half's rows have left it: the next round may come in
         bulk_wait_read0();
         __syncwarp();
-        if (i0 + step < n) send(r ^ 1, i0 + step);
+        if (i0 + step < n && i0 + step != never) send(r ^ 1, i0 + step);
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[warp][r]), par[r], a.timeout_ns))) {
+            // no more rounds; both that are on their way end before the CTA does
             set_status(a.c.status, SDPA_ERR_TIMEOUT);
+            mbar_wait(smem_u32(&bars[warp][r]), par[r], a.timeout_ns);
             if (i0 + step < n) mbar_wait(smem_u32(&bars[warp][r ^ 1]), par[r ^ 1], a.timeout_ns);
             break;
         }
