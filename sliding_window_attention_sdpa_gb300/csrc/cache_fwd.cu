@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
 #pragma unroll
         for (int s = 0; s < kStages - 1; ++s) {
             const Key next = fetch_key(s + 1);
-            if (good && s < nt) issue(s, key);
+            if (good && s < nt && !(a.c.stall && s == 1)) issue(s, key);      // (test hook: a step that never comes)
             key = next;
         }
 #pragma unroll 1
