@@ -284,8 +284,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         uint64_t queue = 0;                   // stages of the groups on their way, 8 bits each, oldest lowest
         uint32_t pending = 0;
         uint32_t it = 0;                      // key tiles so far
-        const uint32_t never = a.c.stall && !is_v ? 2 : ~0u;     // test hook: a K tile that never comes
-        bool ok = true;
+        bool ok = is_v || !a.c.stall;         // (test hook: no K comes)
         const int full0 = is_v ? tVFull : tKFull, empty0 = is_v ? tVEmpty : tKEmpty;
         const uint32_t ring0 = sbase + (is_v ? C::kV : C::kK);
         auto hand_over = [&](uint32_t keep) {     // the groups that are there, all but the last `keep`
@@ -380,7 +379,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 const bool good = (lane >= boxes || (mine >= 0 && mine < a.c.n_pages)) && (!is_v || (pos[0] >= low && pos[1] >= low));
                 const bool by_tma = boxes > 0 && j0 >= sv.first && x0 + kKeys <= sv.new0 && j0 + kKeys <= sv.len &&
                                     __all_sync(0xffffffffu, good);
-                if (!(ok = it != never && acquire(empty0 + st, par ^ 1))) break;
+                if (!(ok = acquire(empty0 + st, par ^ 1))) break;
                 const uint32_t stage = ring0 + st * C::kTile;
                 if (!is_v && a.window_left >= 0) {
 #pragma unroll

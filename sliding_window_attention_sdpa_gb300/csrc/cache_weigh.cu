@@ -185,7 +185,6 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
     if (warp == 0) {
         // ------------------------------------------------------------ K
         uint32_t it = 0, cnt = 0;
-        const uint32_t never = a.c.stall ? 1 : ~0u;     // test hook: a tile that never comes
         bool ok = true;
         walk([&](int64_t bi, int64_t gk, int32_t len, int32_t tile0, int32_t n) -> bool {
             auto entry_of = [&](int32_t j) -> int32_t {
@@ -218,7 +217,7 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                     const uint32_t stage = sbase + C::kK + st * C::kTile;
                     const int32_t mine = entry;
                     entry = box_entry(t + 1);
-                    if (!(ok = it != never && __all_sync(0xffffffffu, wait(wKEmpty + st, ((it / NS) & 1) ^ 1)))) break;
+                    if (!(ok = __all_sync(0xffffffffu, wait(wKEmpty + st, ((it / NS) & 1) ^ 1)))) break;
                     const int32_t j0 = t * kWKeys;
                     if (boxes > 0) {
                         // boxes without a key, or on a page out of range, stay as they were: their lanes are not used
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                     if (lane == 0) mbar_arrive(bar(wKFull + st));
                 }
             }
-            return ok;
+            return ok && !a.c.stall;        // (test hook: no second stretch of keys comes)
         });
         // copies in flight end before the CTA does
         for (uint32_t k = 0; k < NS && k < it; ++k) {

@@ -57,14 +57,16 @@ def test_forward_waits_run_out(name):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("lens,t,d,page,window", [([60000, 40], 1, 64, 64, -1), ([60000, 40], 1, 128, 7, -1), ([60000, 40], 40, 128, 64, -1),
-                                                  ([60000, 40], 70, 64, 64, 30000)])
+@pytest.mark.parametrize("lens,t,d,page,window", [([700] * 300, 1, 64, 64, -1), ([700] * 300, 1, 128, 7, -1),
+                                                  ([700] * 300, 40, 128, 64, -1), ([3000] * 160, 70, 64, 64, 1500)])
 def test_weigh_waits_run_out(lens, t, d, page, window):
+    """More sequences than CTAs: each has several to look after."""
     from test_gpu_cache import dev, gpu_cache, randn
     lay = R.make(621, lens, 1, d, "bf16", page, tracked=True)
     if window >= 0:
         lay.positions = lay.next_pos = None       # rows that reach some tiles only
-    q, lse = dev(randn(622, 2, t, 8, d, dtype=torch.bfloat16)), dev(randn(623, 2, 8, t) + 4)
+    q, lse = (dev(x) for x in (randn(622, len(lens), t, 8, d, dtype=torch.bfloat16),
+                           randn(623, len(lens), 8, t) + 4))
 
     def weighed(stall=False):
         c = gpu_cache(lay)
