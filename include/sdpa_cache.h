@@ -91,7 +91,8 @@ size_t sdpa_cache_evict_params_bytes(void);
  * Sums, maxima and O are kept in fp32. For the P V product P is split into a
  * 16-bit value and its 16-bit remainder where a kv-head has up to 8 rows (s_q *
  * h_q / h_kv; d = 64: up to 16), and rounded to the I/O dtype, as sdpa_fwd
- * does, where it has more.
+ * does, where it has more. In f16 P is held on a grid of 2^-31 of the row's
+ * heaviest key, or finer: a lighter key counts in LSE alone.
  * Keys on pages out of range are left out; lengths out of [0, capacity] are
  * taken as the nearer end. Not read, or without effect whatever they hold, are
  * slots behind a sequence's keys, keys that no row's window has, and new tokens

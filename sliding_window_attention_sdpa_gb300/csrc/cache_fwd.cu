@@ -25,10 +25,12 @@
 //                 registers by an 8 x 8 transpose (movmatrix).
 // Both keep a row in one column: its maximum and its scale are per-thread
 // values. The reference of a row's exponentials moves only when a score exceeds
-// it by more than 2^8 (one vote per step instead of shuffles); P up to 2^8 costs
-// no precision in floating point. P is split into a 16-bit value and its 16-bit
-// remainder, two products: O then has the error of its own rounding only, and
-// the second product runs in the shadow of the loads.
+// it by more than 2^8 (one vote per step instead of shuffles; f16: 2^15, from 2^7
+// on, see kBelow); a P above 1 costs no precision in floating point. P is split
+// into a 16-bit value and its 16-bit remainder, two products: O then has the
+// error of its own rounding only (in f16 also half of 2^-24 a key next to a
+// largest P of 2^7 at least), and the second product runs in the shadow of the
+// loads.
 //
 // Work: the 64- or 128-key tiles of all (sequence, kv-head, row block) units
 // form one line that the persistent CTAs cut into equal parts, whatever the
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mx[n][e] *= a.scale_log2;
-                    up = up || mx[n][e] > m[n][e] + 8.f;
+                    up = up || mx[n][e] > m[n][e] + kMoves<BF16>;
                 }
             }
             if (__any_sync(0xffffffffu, up)) {
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
                         float x = mx[n][e];
 #pragma unroll
                         for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
-                        x = fmaxf(x, m[n][e]);
+                        x = fmaxf(x - kBelow<BF16>, m[n][e]);
                         al[e] = m[n][e] == -INFINITY ? 0.f : ex2_approx(m[n][e] - x);
                         m[n][e] = x;
                         l[n][e] *= al[e];

@@ -139,6 +139,15 @@ __device__ __forceinline__ void named_sync(int id, int threads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// How far, in powers of two, a row's reference lies below the score that set it, and how far above the reference a
+// score may lie before it moves. f16 has no exponent below 2^-24: with its largest P at 2^7 to 2^15 (of 65504), keys
+// down to 2^-31 of the heaviest keep a P, of 2^-21 all 11 bits of it (a reference at the score itself: 2^-24 and 2^-14).
+// bf16 has fp32's exponents.
+template <bool BF16>
+constexpr float kBelow = BF16 ? 0.f : 7.f;
+template <bool BF16>
+constexpr float kMoves = 8.f + kBelow<BF16>;
+
 // One sequence as the rows and keys of this call see it.
 struct SeqView {
     int32_t len, nq;    // cached keys, new tokens

@@ -25,7 +25,8 @@
 // swizzle; warps 2 and 3 issue a slot's MMAs each (one warp for both was the
 // bottleneck: its issue of a tile's 12 MMAs takes longer than they run);
 // warps 4-7 and 8-11 are the slots' softmax groups, one row per thread. A row's
-// reference moves only when a score exceeds it by 2^8, so O is seldom rescaled.
+// reference moves only when a score exceeds it by 2^8 (f16: by 2^15, and then
+// lies 2^7 below it, see kBelow), so O is seldom rescaled.
 // P is rounded to the I/O dtype, as the prompt's forward does: half a step of a
 // P next to a sum that stays in fp32, which leaves O's error within 1.4 times
 // that of rounding O alone.
@@ -630,11 +631,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 for (int e = 0; e < 64; e += 2)
                     x[(e >> 1) & 3] = max3(x[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
                 const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.scale_log2;
-                const bool up = top > m + 8.f;
+                const bool up = top > m + kMoves<BF16>;
                 if (__any_sync(0xffffffffu, up)) {
-                    const float f = !up ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - top);
+                    const float f = !up ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - (top - kBelow<BF16>));
                     l *= f;
-                    m = up ? top : m;
+                    m = up ? top - kBelow<BF16> : m;
                     if (my != cnt0) {
                         // O holds the P V of this slot's earlier keys: they are done before it changes
                         ok = __all_sync(0xffffffffu, wait(tPvDone + (pb ^ 1), ((my - 1) >> 1) & 1));

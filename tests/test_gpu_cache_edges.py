@@ -1,0 +1,123 @@
+"""Edges of the key/value cache's calls on the GPU: masks that list padding
+tokens, keys that only the shallowest rows could see, light keys in f16, NaN
+queries and infinite sinks, the precision that each forward kernel promises,
+and every form in which the forward's work is cut and joined."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cache_ref as R
+from test_gpu_cache import close, dev, gpu_cache, inputs
+
+pytestmark = pytest.mark.gpu
+
+F64 = torch.float64
+
+
+def admitted(lay, i, g, t, tree, window):
+    """Which cached keys [t, n] and new tokens [t, t] each row admits, by the
+    header's words: a token's position counts all bits of its mask; a mask
+    without its own bit admits nothing, but others may list its token."""
+    n = int(lay.lengths[i])
+    line = R.chain(t) if tree is None else [int(x) % 2 ** 64 & ((1 << t) - 1) for x in tree[i].tolist()]
+    deep = torch.tensor([bin(x).count("1") - 1 for x in line])
+    real = torch.tensor([x >> r & 1 for r, x in enumerate(line)], dtype=torch.bool)
+    bit = torch.tensor([[x >> u & 1 for u in range(t)] for x in line], dtype=torch.bool)
+    old = real[:, None].expand(t, n)
+    new = bit & real[:, None]
+    if window >= 0:
+        pos = torch.from_numpy(lay.pos(i, g, n))
+        old = old & (lay.next(i) + deep[:, None] - pos <= window)
+        new = new & (deep[:, None] - deep <= window)
+    return old, new
+
+
+def form(lay, q, k, v, *, scale, window=-1, tree=None, sink=None, dtype="bf16", split=False):
+    """O, LSE and their bounds in 64 bits, a (sequence, kv-head) at a time.
+    `split`: P enters the product as a 16-bit value and its 16-bit remainder."""
+    b, t, h_q, d = q.shape
+    h_kv, u = k.shape[2], R.U[dtype]
+    grp = h_q // h_kv
+    o, tol_o = torch.zeros(b, t, h_q, d, dtype=F64), torch.zeros(b, t, h_q, d, dtype=F64)
+    lse, tol_l = torch.full((b, h_q, t), -math.inf, dtype=F64), torch.zeros(b, h_q, t, dtype=F64)
+    for i in range(b):
+        n = int(lay.lengths[i])
+        for g in range(h_kv):
+            old, new = admitted(lay, i, g, t, tree, window)
+            see = torch.cat([old, new], 1)
+            ks, vs = lay.rows(i, g, n)
+            kk, vv = torch.cat([ks, k[i, :, g]]).to(F64), torch.cat([vs, v[i, :, g]]).to(F64)
+            none = ~see.any(0)
+            kk[none], vv[none] = 0.0, 0.0
+            for h in range(g * grp, (g + 1) * grp):
+                qq = q[i, :, h].to(F64)
+                s = (qq @ kk.T * scale).masked_fill(~see, -math.inf)
+                z = torch.logsumexp(s, 1)
+                if sink is not None:
+                    z = torch.logaddexp(z, sink[h].to(F64))
+                rows = see.any(1)
+                p = torch.exp(s - z[:, None])
+                p[~rows] = 0
+                m = see.sum(1).to(F64) + 8
+                mag = torch.where(see, (qq.abs() @ kk.abs().T) * scale, 0.0).amax(1)
+                top = torch.where(see, s.abs(), 0.0).amax(1)
+                # as in cache_ref.forward: scores off by es, exponentials within 2^-21, sums of m terms within m steps
+                es = mag * (d + 8) * 2.0 ** -23 + top * 2.0 ** -22
+                rel = (2 * es + 2.0 ** -20 + m * 2.0 ** -23)[:, None]
+                o[i, :, h], lse[i, h] = p @ vv, z
+                zf = torch.where(torch.isfinite(z), z.abs(), 0.0)
+                tol_l[i, h] = es + 2.0 ** -20 + m * 2.0 ** -23 + zf * 2.0 ** -22
+                # P in 16 bits (and its remainder: u of u); f16's smallest P is 2^-24 of which half is lost, next to a
+                # largest P of 2^7 at least
+                up = u * u if split else u
+                small = 2.0 ** -32 * (m * p.amax(1))[:, None] * vv.abs().max() if dtype == "f16" and len(vv) else 0.0
+                tol_o[i, :, h] = u * o[i, :, h].abs() + (up + rel) * (1 + u) * (p @ vv.abs()) + small + 2.0 ** -24
+    return R.Forward(o, lse, tol_o, tol_l)
+
+
+def few(t, h_q, h_kv, d):
+    """Whether the kernel for few rows per kv-head takes the call (it splits P)."""
+    return t * (h_q // h_kv) <= (8 if d == 128 else 16)
+
+
+def call(c, q, k, v, **kw):
+    import sliding_window_attention_sdpa_gb300 as swa
+    kw = {n: dev(x) if torch.is_tensor(x) else x for n, x in kw.items()}
+    return swa.cache_forward(c, dev(q), dev(k), dev(v), check_status=True, **kw)
+
+
+# ------------------------------------------------------------------------- values
+
+def ladder(lay, i, powers, values):
+    """Keys of sequence i whose scores, with q = (1, 0, ..) and scale 1, are
+    log(2) times `powers` (rounded to the type), and V of `values` in every
+    feature."""
+    n = len(powers)
+    dt = lay.k.dtype
+    pg, at = lay.where(i, np.arange(n))
+    x = (torch.tensor(powers, dtype=F64) * math.log(2)).to(dt)
+    lay.k[pg, at], lay.v[pg, at] = 0, torch.tensor(values, dtype=dt)[:, None, None]
+    lay.k[pg, at, :, 0] = x[:, None]
+
+
+@pytest.mark.parametrize("heavy", ["first", "last", "amid"])
+@pytest.mark.parametrize("light", [-15.0, -24.3, -26.1, -29.6])
+@pytest.mark.parametrize("t,d,n", [(1, 64, 2000), (1, 128, 300), (1, 128, 5000), (20, 128, 300), (20, 64, 5000)])
+def test_light_keys_in_f16(t, d, n, light, heavy):
+    """One heavy key whose V is 0 next to many light ones whose V is 1: O is the
+    light ones' mass, far below f16's smallest number relative to the heavy P."""
+    lay = R.make(431, [n], 1, d, "f16", 16)
+    q, k, v = inputs(432, 1, t, 1, 1, d, "f16")
+    q[:], k[:], v[:] = 0, 0, 0
+    q[..., 0] = 1
+    k[..., 0] = light * math.log(2)
+    powers, values = [light] * n, [1.0] * n
+    at = dict(first=0, last=n - 1, amid=n // 2 + 5)[heavy]
+    powers[at], values[at] = 0.0, 0.0
+    ladder(lay, 0, powers, values)
+    o, lse = call(gpu_cache(lay), q, k, v, scale=1.0)
+    ref = form(lay, q, k, v, scale=1.0, dtype="f16", split=few(t, 1, 1, d))
+    close("lse", lse, ref.lse, ref.tol_lse)
+    close("o", o, ref.o, ref.tol_o)
