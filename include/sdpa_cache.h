@@ -86,7 +86,7 @@ size_t sdpa_cache_evict_params_bytes(void);
  *     LSE = log( sum exp(s) + exp(sink_h) )     (sink term only with a sink)
  *     O   = sum exp(s - LSE) v.
  * A row that admits no key gets O = 0 and LSE = -inf, or LSE = sink_h with a
- * sink. Rows at or behind seq_q_lens[i] get O = 0, LSE = -inf, and their keys
+ * sink. A row that admits one and has a NaN in its q gets NaN for both. Rows at or behind seq_q_lens[i] get O = 0, LSE = -inf, and their keys
  * are not admitted by any row; bits at or behind it are ignored.
  * Sums, maxima and O are kept in fp32. For the P V product P is split into a
  * 16-bit value and its 16-bit remainder where a kv-head has up to 8 rows (s_q *

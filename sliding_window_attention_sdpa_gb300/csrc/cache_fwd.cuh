@@ -299,11 +299,13 @@ __device__ __forceinline__ void name_cut(const CacheFwdArgs& a, const Part& p, b
 }
 
 // Finishes E features (from c) of a row: O and, with its first feature, LSE.
-// `top` is the reference of the row's exponentials (log2), -inf for no key.
+// `ref` is the reference of the row's exponentials (log2), -inf for no key. The
+// maxima pass over NaN: of a row with NaN scores (a NaN in its q) the sum tells.
 template <bool BF16, int E>
 __device__ __forceinline__ void store_row(const CacheFwdArgs& a, int64_t bi, int tok, int64_t h, int c, bool in_rows,
-                                          float top, float sum, const float (&x)[E])
+                                          float ref, float sum, const float (&x)[E])
 {
+    const float top = sum == sum ? ref : sum;
     const bool sunk = a.sink != nullptr && in_rows;
     float mf = top, lt = sum;
     if (sunk) {

@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 sum = f0 * x.y + f1 * y.y;
             }
             const int cb0 = g.two ? 0 : sl * (HD / 64), cb1 = g.two ? HD / 32 : cb0 + HD / 64;
-            const bool dead = top == -INFINITY;
+            const bool dead = top == -INFINITY;          // (no key, or NaN scores: store_row sees it by the sum)
             if (ok) {
 #pragma unroll 1
                 for (int cb = cb0; cb < cb1; ++cb) {

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import cache_ref as R
-from test_gpu_cache import close, dev, gpu_cache, inputs
+from test_gpu_cache import close, dev, gpu_cache, inputs, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +121,27 @@ def test_light_keys_in_f16(t, d, n, light, heavy):
     ref = form(lay, q, k, v, scale=1.0, dtype="f16", split=few(t, 1, 1, d))
     close("lse", lse, ref.lse, ref.tol_lse)
     close("o", o, ref.o, ref.tol_o)
+
+
+@pytest.mark.parametrize("sink", [False, True])
+@pytest.mark.parametrize("t,d,lens", [(2, 64, [90, 0, 300]), (2, 128, [90, 0, 5000]), (9, 128, [90, 0, 300]),
+                                      (40, 64, [90, 0, 5000]), (40, 128, [90, 3, 700])])
+def test_nan_queries_are_seen(t, d, lens, sink):
+    """A row whose q holds a NaN has NaN for every score: O and LSE are NaN,
+    those of the other rows what they are; a padding row is still empty."""
+    h_q, h_kv, b = 4, 2, len(lens)
+    lay = R.make(441, lens, h_kv, d, "bf16", 16)
+    q, k, v = inputs(442, b, t, h_q, h_kv, d, "bf16")
+    tree = R.tree_masks(443, b, t)
+    tree[0, 1] = 0                                     # an empty row, NaN or not
+    s = randn(444, h_q) if sink else None
+    ref = form(lay, q, k, v, scale=d ** -0.5, tree=tree, sink=s, split=few(t, h_q, h_kv, d))
+    bad = torch.zeros(b, t, h_q, dtype=torch.bool)
+    bad[0, 0, 1] = bad[1, t - 1, 3] = bad[2, 0, 0] = bad[2, t // 2, 2] = True
+    q[bad, d - 1] = math.nan
+    q[0, 1, 2] = math.nan
+    o, lse = call(gpu_cache(lay), q, k, v, scale=d ** -0.5, tree=tree, sink=s)
+    o, lse = o.cpu(), lse.cpu()
+    assert torch.isnan(o[bad]).all() and torch.isnan(lse.transpose(1, 2)[bad]).all()
+    close("lse", lse.transpose(1, 2)[~bad], ref.lse.transpose(1, 2)[~bad], ref.tol_lse.transpose(1, 2)[~bad])
+    close("o", o[~bad], ref.o[~bad], ref.tol_o[~bad])
