@@ -78,8 +78,9 @@ size_t sdpa_cache_evict_params_bytes(void);
  * tree[i][r] says which of sequence i's new tokens token r descends from: bit u
  * is set for u = r and for every token on the way from the root to r. Token r's
  * position is next_pos[i] + (number of set bits - 1). A mask without its own bit
- * is an empty row (padding): it admits no key. Without masks the tokens are a
- * chain. Token r admits
+ * is an empty row (padding): it admits no key, while its token keeps the position
+ * that its bits say for rows that list it. Without masks the tokens are a chain.
+ * Token r admits
  *     cached key j    iff  pos_r - pos_j <= window_left  (if window_left >= 0)
  *     new key u       iff  bit u is set and pos_r - pos_u <= window_left
  * and, with s over the admitted keys (scale * q . k),

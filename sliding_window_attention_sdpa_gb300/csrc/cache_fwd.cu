@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
     __shared__ int32_t sh_pos[4][kStages][GK];         // per step of a ring: the keys' positions,
     __shared__ uint32_t sh_ok[4][kStages];             // and which are there
     __shared__ float sh_m[4][ROWS], sh_l[4][ROWS];
-    __shared__ uint64_t sh_mask[64];
+    __shared__ uint64_t sh_mask[64];       // new tokens that each one's rows admit
+    __shared__ int32_t sh_bits[64];        // and its mask's number of bits
     __shared__ uint32_t sh_used[2];        // new tokens that some row admits
     __shared__ int64_t sh_sum[4];
     __shared__ int64_t sh_at[2];
@@ -176,11 +177,9 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
         const SeqView sv = seq_view(a, bi, TK);
         if (cur != bi) {
             if (tid < 64) {
-                const uint64_t in = sv.nq == 64 ? ~0ull : (1ull << sv.nq) - 1;
-                uint64_t m = 0;
-                if (tid < sv.nq) m = in & (a.tree ? static_cast<uint64_t>(a.tree[bi * a.s_q + tid]) : (2ull << tid) - 1);
-                m = (m >> tid) & 1 ? m : 0;   // without its own bit: an empty row
-                sh_mask[tid] = m;
+                int bits;
+                sh_mask[tid] = admitted_tokens(a, bi, sv.nq, tid, bits);
+                sh_bits[tid] = bits;
             }
             if (tid < 2) sh_used[tid] = 0;
             __syncthreads();
@@ -231,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
                 row_low[n][e] = INT32_MIN;
                 if (a.window_left >= 0)
                     row_low[n][e] = static_cast<int32_t>(
-                        imax64(INT32_MIN, imin64(INT32_MAX, npos + __popcll(m) - 1 - a.window_left)));
+                        imax64(INT32_MIN, imin64(INT32_MAX, npos + sh_bits[tk] - 1 - a.window_left)));
                 if (m) {
                     low_max = max(low_max, row_low[n][e]);
                     low_min = min(low_min, row_low[n][e]);
@@ -439,8 +438,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
                             if (fresh) {
                                 const int w = (x0 + x - sv.new0) & 63;      // the new token
                                 const uint64_t rm = row_tok[n][e & 1] < 0 ? 0 : sh_mask[row_tok[n][e & 1]];
-                                in = in && ((rm >> w) & 1) &&
-                                     (a.window_left < 0 || __popcll(rm) - __popcll(sh_mask[w]) <= a.window_left);
+                                in = in && ((rm >> w) & 1);
                             } else if (windowed) {
                                 in = in && sh_pos[warp][st][x] >= row_low[n][e & 1];
                             }

@@ -181,6 +181,31 @@ __device__ __forceinline__ SeqView seq_view(const CacheFwdArgs& a, int64_t bi, i
     return v;
 }
 
+// New token r's mask as it is given (r < nq), without the bits from nq on.
+__device__ __forceinline__ uint64_t given_mask(const CacheFwdArgs& a, int64_t bi, int32_t nq, int r)
+{
+    const uint64_t in = nq == 64 ? ~0ull : (1ull << nq) - 1;
+    return in & (a.tree ? static_cast<uint64_t>(a.tree[bi * a.s_q + r]) : (2ull << r) - 1);
+}
+
+// The new tokens that row r admits, and (`bits`) the number of its mask's bits,
+// which is its position + 1 behind next_pos: none without its own bit, and none
+// out of the window (a row only looks for those if it is deeper than the window).
+__device__ __forceinline__ uint64_t admitted_tokens(const CacheFwdArgs& a, int64_t bi, int32_t nq, int r, int& bits)
+{
+    bits = 0;
+    if (r >= nq) return 0;
+    uint64_t m = given_mask(a, bi, nq, r);
+    bits = __popcll(m);
+    if (!((m >> r) & 1)) return 0;
+    if (a.window_left >= 0 && bits > a.window_left)
+        for (uint64_t rest = m; rest; rest &= rest - 1) {
+            const int u = __ffsll(static_cast<long long>(rest)) - 1;
+            if (bits - __popcll(given_mask(a, bi, nq, u)) > a.window_left) m &= ~(1ull << u);
+        }
+    return m;
+}
+
 // The line of tiles: all sequences' units, cut evenly between the parts.
 struct Line {
     int64_t total;

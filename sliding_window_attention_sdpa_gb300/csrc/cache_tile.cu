@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(sm);
     auto bar = [&](int i) -> uint32_t { return sbase + C::kBars + 8u * i; };
-    uint32_t* misc = reinterpret_cast<uint32_t*>(sm + C::kMisc);   // [0] tmem base, [1] abort flag, [2] segments begun
+    // [0] tmem base, [1] abort flag, [2] segments begun, [16] on: the masks' numbers of bits, a byte each
+    uint32_t* misc = reinterpret_cast<uint32_t*>(sm + C::kMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t tmo = static_cast<uint64_t>(a.timeout_ns);
 
@@ -336,15 +337,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             };
             // new tokens that some row admits: padding may be anything, and would meet a P of 0
             uint32_t used[2] = {0u, 0u};
-            int32_t shallow = 64;                 // least bits of a row's mask
+            int32_t shallow = 64;                 // least bits of a mask whose row admits a key
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                const int r = w * 32 + lane;
-                const uint64_t in = sv.nq == 64 ? ~0ull : (1ull << sv.nq) - 1;
-                uint64_t m = 0;
-                if (r < sv.nq) m = in & (a.tree ? static_cast<uint64_t>(a.tree[g.bi * a.s_q + r]) : (2ull << r) - 1);
-                if (!((m >> r) & 1)) m = 0;
-                if (m) shallow = min(shallow, __popcll(m));
+                int bits;
+                const uint64_t m = admitted_tokens(a, g.bi, sv.nq, w * 32 + lane, bits);
+                if (m) shallow = min(shallow, bits);
                 used[0] |= __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m));
                 used[1] |= __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m >> 32));
             }
@@ -524,7 +522,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tm_s = tm_s0 + sl * 128 + lane_off, tm_o = tm_o0 + sl * HD + lane_off;
         float2* ml = reinterpret_cast<float2*>(sm + C::kMl);
-        uint64_t* masks = reinterpret_cast<uint64_t*>(sm + C::kMask);
+        uint64_t* masks = reinterpret_cast<uint64_t*>(sm + C::kMask);     // new tokens that each one's rows admit
+        uint8_t* bits = reinterpret_cast<uint8_t*>(misc + 16);            // and its mask's number of bits
         const uint64_t scale2 = pair(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
         uint32_t it0 = 0, cnt = 0;            // ring index at the segment's start; this slot's key tiles so far
         bool ok = true;
@@ -536,10 +535,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             const int32_t tiles = seg_tiles(g, sv.tiles), t0 = seg_tile0(g);
             named_sync(3, 256);               // the last segment's masks and statistics have been read
             if (sl == 0 && r < 64) {
-                const uint64_t in = sv.nq == 64 ? ~0ull : (1ull << sv.nq) - 1;
-                uint64_t m = 0;
-                if (r < sv.nq) m = in & (a.tree ? static_cast<uint64_t>(a.tree[g.bi * a.s_q + r]) : (2ull << r) - 1);
-                masks[r] = (m >> r) & 1 ? m : 0;
+                int n;
+                masks[r] = admitted_tokens(a, g.bi, sv.nq, r, n);
+                bits[r] = static_cast<uint8_t>(n);
             }
             if (sl == 0 && r == 0 && !a.whole)
                 name_cut(a, part, walk.at == part0, walk.at + g.line_n - g.step0 - g.steps, g.cost, g.bi,
@@ -565,7 +563,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             const int64_t npos = a.c.next_pos ? a.c.next_pos[g.bi] : sv.len;
             int32_t low = INT32_MIN;
             if (a.window_left >= 0)
-                low = static_cast<int32_t>(imax64(INT32_MIN, imin64(INT32_MAX, npos + __popcll(mask) - 1 - a.window_left)));
+                low = static_cast<int32_t>(imax64(INT32_MIN, imin64(INT32_MAX, npos + bits[tok] - 1 - a.window_left)));
             const bool windowed = a.window_left >= 0;
             const bool by_pos = windowed && a.c.positions != nullptr;
 
@@ -600,20 +598,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                             for (int e = 0; e < 32; ++e)
                                 if (xw + e < sv.new0 && pos[w * 32 + e] < low) s &= ~(1u << e);
                         }
-                        if (xw + 31 >= sv.new0 && !windowed) {
+                        if (xw + 31 >= sv.new0) {
                             // the mask's bits from the word's first new token on, behind cached keys
                             const int32_t u = xw - sv.new0;
                             s &= u >= 64 ? 0u : u >= 0 ? static_cast<uint32_t>(mask >> u)
                                                        : static_cast<uint32_t>(mask << -u) | ((1u << -u) - 1);
-                        } else if (xw + 31 >= sv.new0) {
-#pragma unroll 1
-                            for (int e = 0; e < 32; ++e) {
-                                const int32_t u = xw + e - sv.new0;
-                                if (u < 0) continue;
-                                const bool in = u < 64 && ((mask >> (u & 63)) & 1) &&
-                                                (!windowed || __popcll(mask) - __popcll(masks[u & 63]) <= a.window_left);
-                                if (!in) s &= ~(1u << e);
-                            }
                         }
                         see[w] = s;
                     }

@@ -88,6 +88,61 @@ def call(c, q, k, v, **kw):
     return swa.cache_forward(c, dev(q), dev(k), dev(v), check_status=True, **kw)
 
 
+# ------------------------------------------------------------------------- masks
+
+def listed_padding(seed, b, t, share):
+    """Trees of which some tokens' masks lack their own bit: those rows are
+    empty, while the rows behind them list them as before."""
+    tree = R.tree_masks(seed, b, t)
+    rs = np.random.RandomState(seed + 1)
+    for i in range(b):
+        for r in range(t - 1):
+            if rs.rand() < share:
+                tree[i, r] = int(tree[i, r]) & ~(1 << r)
+    return tree
+
+
+@pytest.mark.parametrize("window", [-1, 2, 0, 40])
+@pytest.mark.parametrize("t,d,h_q", [(7, 64, 2), (4, 128, 4), (11, 128, 8), (40, 64, 4), (63, 128, 4)])
+def test_padding_tokens_that_others_list(t, d, h_q, window):
+    """A mask without its own bit makes an empty row, and its token keeps the
+    position that its bits say: others that list it admit it by that."""
+    lens, h_kv = [90, 10, 0], 2
+    lay = R.make(401, lens, h_kv, d, "bf16", 16)
+    q, k, v = inputs(402, len(lens), t, h_q, h_kv, d, "bf16")
+    tree = listed_padding(403, len(lens), t, 0.4)
+    # the smallest such case in sequence 0: token 1 descends from 0 but is empty, token 2 lists both
+    tree[0, 0], tree[0, 1], tree[0, 2] = 1, 1, 7
+    kw = dict(scale=d ** -0.5, window=window, tree=tree)
+    o, lse = call(gpu_cache(lay), q, k, v, scale=kw["scale"], window_left=window, tree=tree)
+    ref = form(lay, q, k, v, split=few(t, h_q, h_kv, d), **kw)
+    close("lse", lse, ref.lse, ref.tol_lse)
+    close("o", o, ref.o, ref.tol_o)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("t,d,h_q", [(7, 64, 2), (4, 128, 4), (8, 64, 4), (30, 128, 4), (64, 64, 4)])
+def test_tokens_out_of_every_window_hold_anything(t, d, h_q, wide):
+    """Tokens that rows list but no row's window has, on a chain whose first
+    ones are empty rows: NaN in them reaches no output."""
+    lens, h_kv, gone = [90, 10, 0], 2, t // 2
+    b, window = len(lens), gone - 1 if wide else 0
+    lay = R.make(411, lens, h_kv, d, "bf16", 16)
+    q, k, v = inputs(412, b, t, h_q, h_kv, d, "bf16")
+    line = R.chain(t)
+    for r in range(gone):
+        line[r] &= ~(1 << r)
+    tree = torch.tensor([[x - 2 ** 64 if x >= 2 ** 63 else x for x in line]] * b, dtype=torch.int64)
+    new = admitted(lay, 0, 0, t, tree, window)[1]
+    out = torch.nonzero(~new.any(0)).flatten().tolist()
+    assert out
+    k[:, out], v[:, out] = math.nan, math.inf
+    o, lse = call(gpu_cache(lay), q, k, v, scale=d ** -0.5, window_left=window, tree=tree)
+    ref = form(lay, q, k, v, split=few(t, h_q, h_kv, d), scale=d ** -0.5, window=window, tree=tree)
+    close("lse", lse, ref.lse, ref.tol_lse)
+    close("o", o, ref.o, ref.tol_o)
+
+
 # ------------------------------------------------------------------------- values
 
 def ladder(lay, i, powers, values):
