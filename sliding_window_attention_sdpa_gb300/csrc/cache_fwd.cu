@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
             bool ok = x < sv.new0 && j < sv.len;        // a cached key
             int64_t page = bi;
             uint32_t row = j;
-            const bool reach = ok && (by_pos ? k.pos >= low_min : j >= sv.first);
+            const bool reach = ok && k.pos >= low_min;
             if (ok && a.c.page_table) {
                 page = k.entry;
                 row = a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)

@@ -151,7 +151,7 @@ constexpr float kMoves = 8.f + kBelow<BF16>;
 // One sequence as the rows and keys of this call see it.
 struct SeqView {
     int32_t len, nq;    // cached keys, new tokens
-    int32_t first;      // first cached key in reach of any row; the ones before it are not there
+    int32_t first;      // first cached key in the window of a row at next_pos (the loads know the rows' own depths)
     int32_t lo;         // the same, rounded down to `align`
     int32_t new0;       // place of new token 0 in the line of keys (lo ... ), a multiple of 16 from lo
     int32_t tiles;
@@ -171,7 +171,7 @@ __device__ __forceinline__ SeqView seq_view(const CacheFwdArgs& a, int64_t bi, i
             v.nq = v.nq < 0 ? 0 : a.s_q;
         }
     }
-    // without positions the lowest row's window starts at len - W
+    // without positions the window of a row at next_pos starts at len - W
     v.first = 0;
     if (a.window_left >= 0 && a.c.positions == nullptr) v.first = static_cast<int32_t>(imax64(0, v.len - a.window_left));
     v.lo = v.first & ~(align - 1);

@@ -346,18 +346,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 used[0] |= __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m));
                 used[1] |= __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m >> 32));
             }
-            // lowest position in any row's window
+            // lowest position in any row's window, and without positions the first slot there
             int32_t low = INT32_MIN;
-            if (kpos != nullptr) {
-                const int64_t npos = a.c.next_pos[g.bi];
+            if (a.window_left >= 0) {
+                const int64_t npos = a.c.next_pos ? a.c.next_pos[g.bi] : sv.len;
                 low = static_cast<int32_t>(imax64(INT32_MIN, imin64(INT32_MAX,
                     npos + static_cast<int32_t>(__reduce_min_sync(0xffffffffu, shallow)) - 1 - a.window_left)));
             }
+            const int32_t first = kpos != nullptr ? 0 : max(sv.first, low);
             const int boxes = ta.box_rows ? kKeys / ta.box_rows : 0;
             // a TMA tile's page of lane's box, a tile ahead
             auto box_entry = [&](int32_t t) -> int32_t {
                 const int32_t j = sv.lo + t * kKeys + lane * ta.box_rows;
-                return lane < boxes && t <= t1 && j >= sv.first && j < sv.len ? entry_of(j) : 0;
+                return lane < boxes && t <= t1 && j >= first && j < sv.len ? entry_of(j) : 0;
             };
             int32_t entry = box_entry(t0);
             for (int32_t t = t0; t <= t1; ++t, ++it) {
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 }
                 // (a V that no row's window has may be anything, and would meet a P of 0)
                 const bool good = (lane >= boxes || (mine >= 0 && mine < a.c.n_pages)) && (!is_v || (pos[0] >= low && pos[1] >= low));
-                const bool by_tma = boxes > 0 && j0 >= sv.first && x0 + kKeys <= sv.new0 && j0 + kKeys <= sv.len &&
+                const bool by_tma = boxes > 0 && j0 >= first && x0 + kKeys <= sv.new0 && j0 + kKeys <= sv.len &&
                                     __all_sync(0xffffffffu, good);
                 if (!(ok = acquire(empty0 + st, par ^ 1))) break;
                 const uint32_t stage = ring0 + st * C::kTile;
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                     const uint16_t* p = fresh;
                     bool have = false;
                     if (x < sv.new0) {
-                        if (j >= sv.first && j < sv.len && (k ? pos[1] : pos[0]) >= low) {
+                        if (j >= first && j < sv.len && (k ? pos[1] : pos[0]) >= low) {
                             const int32_t page = entry_of(j);
                             have = page >= 0 && page < a.c.n_pages;
                             if (!have) set_status(a.c.status, SDPA_ERR_BOUNDS);

@@ -143,6 +143,32 @@ def test_tokens_out_of_every_window_hold_anything(t, d, h_q, wide):
     close("o", o, ref.o, ref.tol_o)
 
 
+@pytest.mark.parametrize("page", [0, 7, 16, 64])
+@pytest.mark.parametrize("t,d,h_q", [(5, 64, 2), (3, 128, 4), (21, 128, 4), (40, 64, 4)])
+def test_in_front_of_the_shallowest_window(t, d, h_q, page):
+    """Rows whose shallowest is not at the next position (the tokens before it
+    are padding): keys that only the padding's windows would have hold anything,
+    and their pages may be gone."""
+    lens, h_kv, window, gone = [301, 100, 76, 1000], 2, 77, t // 2
+    b = len(lens)
+    lay = R.make(421, lens, h_kv, d, "bf16", page)
+    q, k, v = inputs(422, b, t, h_q, h_kv, d, "bf16")
+    line = R.chain(t)
+    for r in range(gone):
+        line[r] = 0
+    tree = torch.tensor([[x - 2 ** 64 if x >= 2 ** 63 else x for x in line]] * b, dtype=torch.int64)
+    for i, n in enumerate(lens):
+        first = max(0, min(n, n + gone - window))
+        pg, at = lay.where(i, np.arange(first))
+        lay.k[pg, at], lay.v[pg, at] = math.nan, math.nan
+        if page:
+            lay.table[i, :first // page] = -1
+    o, lse = call(gpu_cache(lay), q, k, v, scale=d ** -0.5, window_left=window, tree=tree)
+    ref = form(lay, q, k, v, split=few(t, h_q, h_kv, d), scale=d ** -0.5, window=window, tree=tree)
+    close("lse", lse, ref.lse, ref.tol_lse)
+    close("o", o, ref.o, ref.tol_o)
+
+
 # ------------------------------------------------------------------------- values
 
 def ladder(lay, i, powers, values):
