@@ -570,7 +570,12 @@ cudaError_t launch_cache_evict(const CacheEvictArgs& a0, cudaStream_t s)
 {
     CacheEvictArgs a = a0;
     const int64_t units = a.c.b * a.c.h_kv;
-    if (units == 0 || a.c.cap <= a.keep) return cudaSuccess;
+    if (units == 0) return cudaSuccess;
+    if (a.c.cap <= a.keep) {
+        // nothing can move: lengths out of range are recorded
+        a.cluster = 1;
+        return launch_select<false, 512>(a, units, s);
+    }
     // CTAs per head: as many as two per SM allow, with 2048 slots each at least (8 heads of 16384 slots: 13.8 us,
     // 18.4 with 1024 at least, 15.3 with 4096; 12 of 16484: 15.8, 18.9, 17.3)
     a.cluster = 1;

@@ -226,3 +226,23 @@ def test_nan_queries_are_seen(t, d, lens, sink):
     assert torch.isnan(o[bad]).all() and torch.isnan(lse.transpose(1, 2)[bad]).all()
     close("lse", lse.transpose(1, 2)[~bad], ref.lse.transpose(1, 2)[~bad], ref.tol_lse.transpose(1, 2)[~bad])
     close("o", o[~bad], ref.o[~bad], ref.tol_o[~bad])
+
+
+# ------------------------------------------------------------------------- lengths
+
+@pytest.mark.parametrize("keep", [64, 65, 2 ** 31 - 1])
+def test_evict_looks_at_lengths_whatever_the_budget(keep):
+    """A budget of all of the room moves nothing; lengths out of range are
+    reported all the same."""
+    import sliding_window_attention_sdpa_gb300 as swa
+    lay = R.make(471, [64, 30], 2, 64, "bf16", 16, evicted=True)
+    c = gpu_cache(lay)
+    swa.cache_evict(c, keep, check_status=True)
+    assert c.lengths.tolist() == [64, 30]
+    for wrong in (-1, 65, 2 ** 31 - 1):
+        c.lengths[1] = wrong
+        swa.cache_evict(c, keep)
+        with pytest.raises(swa.SdpaError) as e:
+            c.check_status()
+        assert e.value.code == swa.SDPA_ERR_BAD_LENGTHS
+        assert c.lengths.tolist() == [64, wrong]
