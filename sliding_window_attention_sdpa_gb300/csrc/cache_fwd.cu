@@ -620,7 +620,9 @@ __global__ void __launch_bounds__(256) cache_fwd_join_kernel(const __grid_consta
     auto slot = [&](int i) -> int64_t { return i == 0 ? c0 * int64_t(2) + cut.slot0 : (c0 + i) * int64_t(2); };
     int nq = a.s_q;
     if (a.seq_q_lens) nq = max(0, min(a.seq_q_lens[cut.bi], a.s_q));
-    // this warp's rows (of a unit's ROWS: the partials of all of them are there, whatever the last real one)
+    // this warp's rows; their partials are there up to the next multiple of RW behind the last real one (loads without
+    // a bound on them are on their way together: 296 rows 11 us, 15 to 16 with one)
+    static_assert(kPartialRows % RW == 0, "");
     const int r = SPREAD ? blockIdx.y : (blockIdx.y * 8 + warp) * RW;
     if (r0 + r >= R) return;
     float top[RW], sum[RW], x[RW][E];

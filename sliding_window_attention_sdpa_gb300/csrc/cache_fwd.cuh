@@ -206,6 +206,10 @@ __device__ __forceinline__ uint64_t admitted_tokens(const CacheFwdArgs& a, int64
     return m;
 }
 
+// A cut unit leaves partials of its rows up to a multiple of this (the join's
+// warps take as many).
+constexpr int kPartialRows = 4;
+
 // The line of tiles: all sequences' units, cut evenly between the parts.
 struct Line {
     int64_t total;
@@ -287,7 +291,7 @@ __device__ __forceinline__ Part find_part(int64_t b, F tiles_of, int64_t* sh, in
     return p;
 }
 
-// A unit's place in the line: kUnitCost tiles' worth of its fixed cost (rows in,
+// A unit's place in the line: `cost` tiles' worth of its fixed cost (rows in,
 // pipeline filled and drained, O out), then its tiles. A part that ends within
 // the first has none of the unit's tiles. A segment: what a part has of a unit.
 struct Segment {

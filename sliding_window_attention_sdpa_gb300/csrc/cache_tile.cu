@@ -701,6 +701,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 sum = f0 * x.y + f1 * y.y;
             }
             const int cb0 = g.two ? 0 : sl * (HD / 64), cb1 = g.two ? HD / 32 : cb0 + HD / 64;
+            // (rows behind the last one, empty, as far as the join reads)
+            const int stored = whole ? R : (R + kPartialRows - 1) / kPartialRows * kPartialRows;
             const bool dead = top == -INFINITY;          // (no key, or NaN scores: store_row sees it by the sum)
             if (ok) {
 #pragma unroll 1
@@ -718,7 +720,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                         for (int e = 0; e < 32; ++e)
                             if (!dead && f1 != 0.f) x[e] += f1 * __uint_as_float(v[e]);
                     }
-                    if (rr >= R) continue;
+                    if (rr >= stored) continue;
                     if (!whole) {
                         float* po = a.part_o + (slot * 256 + urow) * HD + cb * 32;
 #pragma unroll
