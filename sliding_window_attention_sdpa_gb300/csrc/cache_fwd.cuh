@@ -340,7 +340,8 @@ __device__ __forceinline__ void store_row(const CacheFwdArgs& a, int64_t bi, int
     if (sunk) {
         const float sk = a.sink[h] * kLog2e;
         mf = fmaxf(top, sk);
-        lt = (top == -INFINITY ? 0.f : sum * ex2_approx(top - mf)) + ex2_approx(sk - mf);
+        // (a sink of +inf is its own reference, and all of the sum)
+        lt = (top == -INFINITY ? 0.f : sum * ex2_approx(top - mf)) + (sk == mf ? 1.f : ex2_approx(sk - mf));
     }
     const float mul = top == -INFINITY ? 0.f : ex2_approx(top - mf) / lt;
     uint16_t* o = a.o + bi * a.o_stride[0] + tok * a.o_stride[1] + h * a.o_stride[2] + c;

@@ -228,6 +228,20 @@ def test_nan_queries_are_seen(t, d, lens, sink):
     close("o", o[~bad], ref.o[~bad], ref.tol_o[~bad])
 
 
+@pytest.mark.parametrize("t,d,n", [(1, 64, 90), (2, 128, 3000), (40, 64, 90), (40, 128, 3000), (1, 64, 0)])
+def test_infinite_sinks(t, d, n):
+    """exp(-inf) = 0: no sink; a sink of +inf takes all of the weight."""
+    h_q, h_kv = 4, 2
+    lay = R.make(451, [n, 30], h_kv, d, "bf16", 16)
+    q, k, v = inputs(452, 2, t, h_q, h_kv, d, "bf16")
+    sink = torch.tensor([math.inf, -math.inf, 0.3, math.inf])
+    o, lse = call(gpu_cache(lay), q, k, v, scale=d ** -0.5, sink=sink)
+    ref = form(lay, q, k, v, scale=d ** -0.5, sink=sink, split=few(t, h_q, h_kv, d))
+    assert torch.isinf(ref.lse[:, [0, 3]]).all() and (ref.o[:, :, [0, 3]] == 0).all()
+    close("lse", lse, ref.lse, ref.tol_lse)
+    close("o", o, ref.o, ref.tol_o)
+
+
 # ------------------------------------------------------------------------- lengths
 
 @pytest.mark.parametrize("keep", [64, 65, 2 ** 31 - 1])
