@@ -397,6 +397,8 @@ def cache_append(cache: KVCache, k, v, *, index=None, counts=None, offsets=None,
     if k.dim() == 3:
         if offsets is None or max_seqlen is None:
             raise ValueError("packed k, v need offsets and max_seqlen")
+        if index is not None:
+            raise ValueError("index: only with k, v of [b, s, h_kv, d]")
         layout, s, total = 1, max_seqlen, k.shape[0]
         shape = (total, h_kv, d)
         sk, sv = (0, *_strides("k", k, shape, dev, dt)), (0, *_strides("v", v, shape, dev, dt))
