@@ -709,6 +709,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
                 for (int cb = cb0; cb < cb1; ++cb) {
                     uint32_t v[32];
                     float x[32];
+                    __syncwarp();       // rows behind the last one have left the last turn early
                     tmem_ld32((g.two ? tm_o : tm_o0 + lane_off) + cb * 32, v);
                     tmem_ld_wait();
 #pragma unroll

@@ -242,6 +242,72 @@ def test_infinite_sinks(t, d, n):
     close("o", o, ref.o, ref.tol_o)
 
 
+def rms_ratio(got, exact, dtype):
+    """Root mean square error relative to that of rounding the exact O."""
+    rms = lambda x: float(x.double().square().mean().sqrt())  # noqa: E731
+    return rms(got.cpu().double() - exact) / rms(exact.to(R.DT[dtype]).double() - exact)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("t,d,h_q", [(2, 64, 8), (4, 64, 8), (2, 128, 8), (4, 128, 8), (37, 128, 16)])
+def test_precision_of_each_kernel(t, d, h_q, dtype):
+    """With V of zero mean both O and the sum of P's rounding errors are random
+    walks over p v: P in 16 bits adds an error of the size of O's own rounding,
+    1.41 times it together; with P's remainder O's own rounding is all (the next
+    term is u of it). The bounds are apart from both by a few per cent of 10^4
+    samples and more."""
+    b, h_kv, n = 2, 2, 900
+    split = few(t, h_q, h_kv, d)
+    lay = R.make(461, [n] * b, h_kv, d, dtype, 64)
+    q, k, v = inputs(462, b, t, h_q, h_kv, d, dtype)
+    o, lse = call(gpu_cache(lay), q, k, v, scale=d ** -0.5)
+    exact = form(lay, q, k, v, scale=d ** -0.5, dtype=dtype, split=split).o
+    assert rms_ratio(o, exact, dtype) < (1.01 if split else 1.5)
+    # and that a lost remainder would show: the same sums with P rounded once
+    i, g = 0, 0
+    ks, vs = lay.rows(i, g, n)
+    qq = q[i, :, :h_q // h_kv].transpose(0, 1).reshape(-1, d).double()
+    s = qq @ ks.double().T * d ** -0.5
+    p = torch.exp(s - s.amax(1, keepdim=True))
+    whole, once = (x @ vs.double() / p.sum(1, keepdim=True) for x in (p, p.to(R.DT[dtype]).double()))
+    assert rms_ratio(once.to(R.DT[dtype]), whole, dtype) > 1.2
+
+
+# ------------------------------------------------------------------------- work cut between parts
+
+# lens, t, h_q, h_kv, d, dtype: more units (sequence, kv-head, block of 256 or 8 rows) than parts (152, few rows 304)
+# and room for more than 512 keys, so that cut units are named by their part
+PARTS = {
+    "blocks_of_two_and_one": ([(37 * i) % 90 for i in range(42)] + [1500, 700], 37, 16, 2, 128, "bf16"),
+    "blocks_of_two_and_one_d64": ([(37 * i) % 90 for i in range(42)] + [1500, 700], 37, 16, 2, 64, "f16"),
+    "two_blocks_of_two": ([(53 * i) % 70 for i in range(40)] + [900, 1300], 64, 16, 2, 128, "f16"),
+    "two_blocks_of_two_d64": ([(53 * i) % 70 for i in range(40)] + [900, 1300], 64, 16, 2, 64, "bf16"),
+    "one_block_of_two": ([(37 * i) % 90 for i in range(60)] + [1500], 32, 24, 3, 64, "bf16"),
+    "one_block_of_one": ([(37 * i) % 90 for i in range(90)] + [1500, 40, 2000], 5, 16, 2, 128, "bf16"),
+    "three_blocks": ([(37 * i) % 90 for i in range(30)] + [1500], 60, 18, 2, 64, "bf16"),
+    "few_rows": ([(37 * i) % 90 for i in range(170)] + [900, 5, 2500], 1, 8, 2, 128, "bf16"),
+    "few_rows_d64": ([(37 * i) % 90 for i in range(110)] + [900, 5, 2500], 2, 24, 3, 64, "f16"),
+    # and by unit: several kv-heads, mixed blocks, fewer units than parts
+    "by_unit_mixed": ([1500, 3, 700, 4000], 37, 16, 2, 128, "bf16"),
+    "by_unit_three_blocks": ([1500, 3, 700], 60, 18, 2, 64, "f16"),
+}
+
+
+@pytest.mark.parametrize("name", PARTS)
+def test_units_cut_between_parts(name):
+    lens, t, h_q, h_kv, d, dtype = PARTS[name]
+    seed, b, rows = 500 + 7 * list(PARTS).index(name), len(lens), t * (h_q // h_kv)
+    units = b * h_kv * -(-rows // (256 if not few(t, h_q, h_kv, d) else rows))
+    assert name.startswith("by_unit") == (units <= (304 if few(t, h_q, h_kv, d) else 152))
+    lay = R.make(seed, lens, h_kv, d, dtype, 64)
+    q, k, v = inputs(seed + 1, b, t, h_q, h_kv, d, dtype)
+    tree = R.tree_masks(seed + 2, b, t)
+    o, lse = call(gpu_cache(lay), q, k, v, scale=d ** -0.5, tree=tree)
+    ref = form(lay, q, k, v, scale=d ** -0.5, tree=tree, dtype=dtype, split=few(t, h_q, h_kv, d))
+    close("lse", lse, ref.lse, ref.tol_lse)
+    close("o", o, ref.o, ref.tol_o)
+
+
 # ------------------------------------------------------------------------- lengths
 
 @pytest.mark.parametrize("keep", [64, 65, 2 ** 31 - 1])
