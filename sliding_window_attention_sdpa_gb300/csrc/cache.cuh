@@ -10,6 +10,18 @@
 
 namespace swa {
 
+// The page-table entry of a slot of sequence bi, and the slot's row in its page
+// (a cache with a page table).
+__device__ __forceinline__ int32_t cache_entry(const CacheView& c, int64_t bi, uint32_t slot)
+{
+    return c.page_table[bi * c.max_pages + (c.page_shift >= 0 ? slot >> c.page_shift : slot / c.page_size)];
+}
+
+__device__ __forceinline__ uint32_t cache_row(const CacheView& c, uint32_t slot)
+{
+    return c.page_shift >= 0 ? slot & ((1u << c.page_shift) - 1) : slot % c.page_size;
+}
+
 // The page that holds `slot` of sequence bi, or -1 (recorded) if the table's
 // entry is outside [0, n_pages); `row` becomes the slot's row in it.
 __device__ __forceinline__ int64_t cache_page(const CacheView& c, int64_t bi, uint32_t slot, uint32_t& row)

@@ -92,17 +92,6 @@ struct RowsCfg {
     static_assert(2 * GK * kPitch <= kStage, "");
 };
 
-// A box of box_rows keys x 64 features (from c0) of one head of a page.
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int head, int row,
-                                        int page)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(head), "r"(row), "r"(page)
-        : "memory");
-}
-
 }  // namespace
 
 template <int HD, bool BF16, int NT>
@@ -258,10 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
             if (x < sv.new0) {
                 const int32_t j = sv.lo + x;
                 if (j < sv.len) {
-                    if (a.c.page_table)
-                        k.entry = a.c.page_table[bi * a.c.max_pages +
-                                                 (a.c.page_shift >= 0 ? static_cast<uint32_t>(j) >> a.c.page_shift
-                                                                      : static_cast<uint32_t>(j) / a.c.page_size)];
+                    if (a.c.page_table) k.entry = cache_entry(a.c, bi, j);
                     k.pos = by_pos ? kpos[j] : j;
                 }
             }
@@ -299,8 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_rows_kernel(const __gri
             const bool reach = ok && k.pos >= low_min;
             if (ok && a.c.page_table) {
                 page = k.entry;
-                row = a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)
-                                          : static_cast<uint32_t>(j) % a.c.page_size;
+                row = cache_row(a.c, j);
                 ok = page >= 0 && page < a.c.n_pages;
                 if (reach && !ok) set_status(a.c.status, SDPA_ERR_BOUNDS);
             }

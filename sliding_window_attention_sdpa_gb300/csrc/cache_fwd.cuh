@@ -66,6 +66,17 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t chunk)
     return (chunk >> 3) * BLK + (row >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
+// A box of 64 features (from c0) x the map's rows of one head of a page.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int head, int row,
+                                        int page)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(head), "r"(row), "r"(page)
+        : "memory");
+}
+
 // 16 bytes to shared memory; zeros (nothing read) if not `have`.
 __device__ __forceinline__ void cp16(uint32_t dst, const uint16_t* src, bool have)
 {

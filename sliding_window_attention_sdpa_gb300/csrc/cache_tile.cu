@@ -75,17 +75,6 @@ enum TBar : int { tKFull = 0, tKEmpty = 8, tVFull = 16, tVEmpty = 24, tSFull = 3
                   tNumBars = 46 };
 static_assert(tNumBars * 8 <= 448, "mbarrier area");
 
-// A box of 64 features x box_rows rows of one head of a page.
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int head, int row,
-                                        int page)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(head), "r"(row), "r"(page)
-        : "memory");
-}
-
 template <int N>
 __device__ __forceinline__ void cp_wait()
 {
@@ -330,13 +319,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const _
             const int64_t st_new = is_v ? a.v_stride[1] : a.k_stride[1];
             auto entry_of = [&](int32_t j) -> int32_t {       // of a held key
                 if (a.c.page_table == nullptr) return static_cast<int32_t>(g.bi);
-                return a.c.page_table[g.bi * a.c.max_pages + (a.c.page_shift >= 0 ? static_cast<uint32_t>(j) >> a.c.page_shift
-                                                                                  : static_cast<uint32_t>(j) / a.c.page_size)];
+                return cache_entry(a.c, g.bi, j);
             };
             auto row_of = [&](int32_t j) -> uint32_t {
-                if (a.c.page_table == nullptr) return j;
-                return a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)
-                                           : static_cast<uint32_t>(j) % a.c.page_size;
+                return a.c.page_table == nullptr ? j : cache_row(a.c, j);
             };
             // new tokens that some row admits: padding may be anything, and would meet a P of 0
             uint32_t used[2] = {0u, 0u};

@@ -189,13 +189,10 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
         walk([&](int64_t bi, int64_t gk, int32_t len, int32_t tile0, int32_t n) -> bool {
             auto entry_of = [&](int32_t j) -> int32_t {
                 if (a.c.page_table == nullptr) return static_cast<int32_t>(bi);
-                return a.c.page_table[bi * a.c.max_pages + (a.c.page_shift >= 0 ? static_cast<uint32_t>(j) >> a.c.page_shift
-                                                                                : static_cast<uint32_t>(j) / a.c.page_size)];
+                return cache_entry(a.c, bi, j);
             };
             auto row_of = [&](int32_t j) -> uint32_t {
-                if (a.c.page_table == nullptr) return j;
-                return a.c.page_shift >= 0 ? static_cast<uint32_t>(j) & ((1u << a.c.page_shift) - 1)
-                                           : static_cast<uint32_t>(j) % a.c.page_size;
+                return a.c.page_table == nullptr ? j : cache_row(a.c, j);
             };
             const int boxes = a.box_rows ? kWKeys / a.box_rows : 0;
             for (int ch = 0; ch < chunks && ok; ++ch) {
@@ -230,12 +227,8 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                             const int row = static_cast<int>(row_of(j0 + lane * a.box_rows));
 #pragma unroll
                             for (int cb = 0; cb < HD / 64; ++cb)
-                                asm volatile(
-                                    "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
-                                    "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(stage + cb * C::kBlk + lane * a.box_rows * 128),
-                                    "l"(reinterpret_cast<uint64_t>(&a.tm_k)), "r"(bar(wKFull + st)), "r"(cb * 64),
-                                    "r"(static_cast<int>(gk)), "r"(row), "r"(mine)
-                                    : "memory");
+                                tma_box(stage + cb * C::kBlk + lane * a.box_rows * 128, &a.tm_k, bar(wKFull + st), cb * 64,
+                                        static_cast<int>(gk), row, mine);
                         }
                         continue;
                     }
@@ -390,9 +383,7 @@ __global__ void __launch_bounds__(kWThreads, 1) cache_weigh_kernel(const __grid_
                     Mine k{static_cast<int32_t>(bi), 0, 0.f};
                     const int32_t j = t * kWKeys + key_lane;
                     if (t < tb && j < len) {
-                        if (a.c.page_table)
-                            k.entry = a.c.page_table[bi * a.c.max_pages + (a.c.page_shift >= 0 ? static_cast<uint32_t>(j) >> a.c.page_shift
-                                                                                               : static_cast<uint32_t>(j) / a.c.page_size)];
+                        if (a.c.page_table) k.entry = cache_entry(a.c, bi, j);
                         k.pos = a.c.positions ? a.c.positions[unit + j] : j;
                         k.w = a.c.weights[unit + j];
                         // (a group's tile takes less than memory's latency: later ones come into L2 before)
