@@ -156,7 +156,8 @@ sdpa_status_t sdpa_cache_append(const sdpa_cache *cache, const sdpa_cache_append
  * pos_j <= q_pos, and q_pos - pos_j <= window_left (if >= 0). Without q_pos the
  * rows are the last s_q tokens: q_pos = next_pos - s_q + r. The sum over a
  * key's rows is formed in fp32 in a fixed order (bitwise repeatable). Keys on
- * pages out of range keep their weight. A key's K has to be finite, and the q of
+ * pages out of range keep their weight; such a page may be reported although no
+ * row's window has a key on it. A key's K has to be finite, and the q of
  * rows that count.
  */
 typedef struct sdpa_cache_weigh_params {

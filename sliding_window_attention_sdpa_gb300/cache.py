@@ -338,7 +338,8 @@ def cache_forward(cache: KVCache, q, k, v, *, scale: float, window_left: int = -
     cache yet); tree: int64 [b, s_q], bit u of tree[i, r] set for r itself and
     each token u that r descends from (0: a padding row; None: a chain);
     seq_q_lens: int32 [b] real rows of each sequence; sink: fp32 [h_q].
-    Returns (o, lse) with o like q and lse fp32 [b, h_q, s_q].
+    Returns (o, lse) with o like q and lse fp32 [b, h_q, s_q]. Tensors that
+    require a gradient are taken, and nothing is recorded for one.
     """
     c = _calls or _c()
     if q.dim() != 4:

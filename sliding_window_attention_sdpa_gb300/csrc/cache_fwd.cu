@@ -728,7 +728,8 @@ cudaError_t launch_fwd_typed(const CacheTileArgs& ta, cudaStream_t s)
 // Rows per kv-head above which the tile kernel is ahead (12 sequences of 16484
 // keys, 6 kv-heads): d = 128, 16 rows 116 us against 131 for a rows kernel of 16
 // (8 rows: 107 against the tile kernel's 113); d = 64, 32 rows 98 us against 138
-// (16 rows: 75 against 98). A unit's cost (64 ragged sequences of 5 to 16484
+// (16 rows: 75 against 98), as measured together (the tile kernel's 16 and 32
+// rows are 105 and 81 us now). A unit's cost (64 ragged sequences of 5 to 16484
 // keys): rows kernel 123, 89, 79, 79, 84 us at 0, 2, 4, 8, 16; tile kernel with
 // 24 rows 228, 127, 104, 126 us at 0, 4, 8, 16.
 CacheFwdPlan cache_fwd_plan(int64_t d, int64_t rows)

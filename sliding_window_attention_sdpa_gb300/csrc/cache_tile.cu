@@ -13,13 +13,14 @@
 // block loses no overlap.
 //
 // Bound by reading K and V up to 128 rows (12 sequences of 16484 keys, 6
-// kv-heads, d = 128: 113 us at 128 rows, 5.4 TB/s), then by the softmax groups'
-// chain from a tile's S to its P (256 rows 142 us; 512, each half reading K and V
-// again, 255 us, 1.2 PFLOP/s): its phases wait on the tensor memory's loads and
+// kv-heads, d = 128: 112 us at 128 rows, 5.4 TB/s), then by the softmax groups'
+// chain from a tile's S to its P (256 rows 138 us; 512, each half reading K and V
+// again, 247 us, 1.26 PFLOP/s): its phases wait on the tensor memory's loads and
 // the exponentials in turn, with the tensor core a third of the time idle. Two
 // threads a row and 640 threads did not shorten it (256 rows: 161 us against 147
-// then), and splitting P as the rows kernel does costs 16 % (512 rows: 304 us
-// against 263 then).
+// then), and splitting P as the rows kernel does costs the kernel 3 % at 24 to 128
+// rows of even lengths, 11 % of ragged ones, and 16 to 19 % above (512 rows: 283
+// us against 238).
 //
 // Roles (384 threads): warp 0 loads K, warp 1 V into two rings in the 128-byte
 // swizzle; warps 2 and 3 issue a slot's MMAs each (one warp for both was the
@@ -158,10 +159,11 @@ __device__ __forceinline__ int32_t seg_tiles(const Seg& g, int32_t tiles)
 }
 }  // namespace
 
-// POS: a window over keys that have positions. An instance of its own: with one
-// for both the loaders' checks of positions made two row blocks' CTAs share less
-// of their reads (12 sequences of 16484 keys, 6 kv-heads, 296 rows: 255 us
-// against 223, d = 64 230 against 193; other row counts 1 to 2 %).
+// POS: a window over keys that have positions. An instance of its own: the
+// checks of positions lengthen the loaders' way to a tile (12 sequences of 16484
+// keys, 6 kv-heads, 296 rows: 255 us with one instance for both, 223 without the
+// checks; d = 64 230 and 193; 16 to 512 rows of one kind of block 1 to 2 %. It is
+// the pace, not the reads: 223 and 217 MB from DRAM for 3 of the sequences).
 template <int HD, bool BF16, bool POS>
 __global__ void __launch_bounds__(kTileThreads, 1) cache_fwd_tile_kernel(const __grid_constant__ CacheTileArgs ta)
 {

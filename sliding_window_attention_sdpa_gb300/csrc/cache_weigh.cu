@@ -11,8 +11,10 @@
 //
 // Few rows: bound by reading K once (a 4-stage ring of 128 keys by TMA, 8 at
 // d = 64): 55 us at 12 sequences of 16484 keys, 6 kv-heads, 8 rows in bf16,
-// d = 128 (5.5 TB/s). Many rows: by the exponentials (one per key and row):
-// 88 us for 256 rows. The loop over columns exists twice, with and without the
+// d = 128 (5.5 TB/s). Many rows (88 us for 256): by none of its units' rates
+// (exponential pipe 29 % busy, tensor pipe 28 %; the exponentials alone would take
+// 30 us); its warps wait at barriers first of all, where a key's two threads meet
+// behind every tile. The loop over columns exists twice, with and without the
 // mask (102 us against 93 with one loop that asked per 32 columns), and is not
 // unrolled: both stay within the registers. Weights and positions come into L2
 // ahead of their use (93 us against 89).
