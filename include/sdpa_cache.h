@@ -73,7 +73,9 @@ size_t sdpa_cache_evict_params_bytes(void);
 
 /*
  * Attention of up to 64 new tokens per sequence over the cached keys and over
- * each other. The new tokens' own keys and values are not in the cache yet.
+ * each other. The new tokens' own keys and values are not in the cache yet. More
+ * tokens take several calls, each followed by an append; a whole prompt is
+ * sdpa_fwd's, whose keys lie in one run.
  *
  * tree[i][r] says which of sequence i's new tokens token r descends from: bit u
  * is set for u = r and for every token on the way from the root to r. Token r's
@@ -87,13 +89,14 @@ size_t sdpa_cache_evict_params_bytes(void);
  *     LSE = log( sum exp(s) + exp(sink_h) )     (sink term only with a sink)
  *     O   = sum exp(s - LSE) v.
  * A row that admits no key gets O = 0 and LSE = -inf, or LSE = sink_h with a
- * sink. A row that admits one and has a NaN in its q gets NaN for both. Rows at or behind seq_q_lens[i] get O = 0, LSE = -inf, and their keys
- * are not admitted by any row; bits at or behind it are ignored.
+ * sink. A row that admits one and has a NaN in its q gets NaN for both. Rows at
+ * or behind seq_q_lens[i] get O = 0, LSE = -inf, and their keys are not admitted
+ * by any row; bits at or behind it are ignored.
  * Sums, maxima and O are kept in fp32. For the P V product P is split into a
  * 16-bit value and its 16-bit remainder where a kv-head has up to 8 rows (s_q *
  * h_q / h_kv; d = 64: up to 16), and rounded to the I/O dtype, as sdpa_fwd
  * does, where it has more. In f16 P is held on a grid of 2^-31 of the row's
- * heaviest key, or finer: a lighter key counts in LSE alone.
+ * heaviest key, or finer: keys lighter than half of that count in LSE alone.
  * Keys on pages out of range are left out; lengths out of [0, capacity] are
  * taken as the nearer end. Not read, or without effect whatever they hold, are
  * slots behind a sequence's keys, keys that no row's window has, and new tokens
@@ -198,8 +201,8 @@ sdpa_status_t sdpa_cache_evict(const sdpa_cache *cache, const sdpa_cache_evict_p
  * those and the products in flight finish, frees its tensor memory and returns.
  * This call changes, for the calling thread's later calls on any cache:
  *   wait_limit_ns  the bound of every device wait (<= 0: the default);
- *   flags          bit 0: an early copy of each stretch of work is left out, so
- *                  that the wait for it runs out; 0: normal operation.
+ *   flags          bit 0: forward, weigh and evict leave out copies that a
+ *                  wait is for, so that it runs out; 0: normal operation.
  * Returns SDPA_ERR_INVALID_ARG for undefined flag bits. Call it with (0, 0) to
  * restore normal operation.
  */

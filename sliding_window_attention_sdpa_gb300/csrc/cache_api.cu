@@ -224,7 +224,8 @@ sdpa_status_t check_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p)
     if (st != SDPA_OK) return st;
     if (p == nullptr) return fail(SDPA_ERR_INVALID_ARG, "params is NULL");
     if (p->s_q < 1 || p->s_q > 64)
-        return fail(SDPA_ERR_UNSUPPORTED, "s_q=%lld: 1 to 64 new tokens per sequence (longer ones: sdpa_fwd)",
+        return fail(SDPA_ERR_UNSUPPORTED,
+                    "s_q=%lld: 1 to 64 new tokens per sequence (more: up to 64 a call, appended in between)",
                     (long long)p->s_q);
     if ((st = check_rows(c, p->s_q, p->h_q, p->window_left, p->scale)) != SDPA_OK) return st;
     const struct { const char* n; const int64_t* s; } strides[] = {

@@ -310,6 +310,26 @@ def test_units_cut_between_parts(name):
 
 # ------------------------------------------------------------------------- lengths
 
+@pytest.mark.parametrize("d,window", [(64, -1), (128, 100)])
+def test_more_than_64_tokens_in_several_calls(d, window):
+    """A call refuses them and says how: in calls of up to 64, appended in between."""
+    import sliding_window_attention_sdpa_gb300 as swa
+    t, h_q, h_kv, lens = 150, 8, 2, [90, 0]
+    lay = R.make(481, lens, h_kv, d, "bf16", 16, room=t)
+    q, k, v = inputs(482, 2, t, h_q, h_kv, d, "bf16")
+    c = gpu_cache(lay)
+    with pytest.raises(swa.SdpaError, match="appended in between"):
+        call(c, q, k, v, scale=d ** -0.5, window_left=window)
+    for a in range(0, t, 64):
+        x = [y[:, a:a + 64].contiguous() for y in (q, k, v)]
+        o, lse = call(c, *x, scale=d ** -0.5, window_left=window)
+        swa.cache_append(c, dev(x[1]), dev(x[2]), check_status=True)
+        ref = form(lay, *x, scale=d ** -0.5, window=window)
+        close("lse", lse, ref.lse, ref.tol_lse)
+        close("o", o, ref.o, ref.tol_o)
+        lay = R.append(lay, x[1], x[2])
+
+
 @pytest.mark.parametrize("keep", [64, 65, 2 ** 31 - 1])
 def test_evict_looks_at_lengths_whatever_the_budget(keep):
     """A budget of all of the room moves nothing; lengths out of range are
