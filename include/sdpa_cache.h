@@ -44,14 +44,15 @@ extern "C" {
  */
 typedef struct sdpa_cache {
     int32_t dtype;              /* SDPA_BF16 | SDPA_F16 for K, V and the calls' tensors */
-    int32_t reserved0;
+    int32_t bits;               /* 0 or 16: K and V are held in dtype; 4: in 4 bits (below) */
     int64_t b, h_kv, d;         /* sequences, kv-heads (up to 4096), head dimension (64 or 128) */
     int64_t n_pages, page_size; /* pages in k and v, rows of a page (any number >= 1) */
     int64_t max_pages;          /* entries of a page-table row; a sequence has room for
                                    max_pages * page_size keys (its capacity, at most
                                    2^31 - 2^16) */
-    void *k, *v;                /* device [n_pages][page_size][h_kv][d] */
-    int64_t k_stride[3], v_stride[3]; /* page, row, head */
+    void *k, *v;                /* device [n_pages][page_size][h_kv][d]; bits = 4: bytes
+                                   [n_pages][h_kv][page_size / 16][9 d] */
+    int64_t k_stride[3], v_stride[3]; /* page, row, head; bits = 4, in bytes: page, group (9 d), head */
     const int32_t *page_table;  /* device [b][max_pages]; NULL: page i is sequence i's only one
                                    (max_pages = 1, n_pages >= b). Entries behind a sequence's
                                    keys are not read. A page may be in several places (a common
@@ -64,10 +65,28 @@ typedef struct sdpa_cache {
     int32_t *status;            /* device [1], zero at first: the first problem found */
 } sdpa_cache;
 
+/*
+ * A cache in 4 bits (bits = 4). sdpa_cache_append quantises the rows as they go in,
+ * sdpa_cache_read gives them back, sdpa_cache_fwd attends over them; weigh and
+ * evict are not done on it (SDPA_ERR_UNSUPPORTED). 16 neighbouring features x of a
+ * key are held as whole numbers c and a scale s, and stand for c * s, which dtype
+ * holds exactly:
+ *     s = max|x| / 7, rounded to 3 mantissa bits (ties to even): a normal number
+ *         from 2^-14 on, a multiple of 2^-17 below, 240 at most;
+ *     c = x / s rounded to a whole number (ties to even), -8 to 7; 0 where s = 0.
+ * So magnitudes above 1680 are cut off there (negative ones at 1920). 16 features
+ * with an infinity or a NaN among them come back as NaN, all 16. 16 keys of a head
+ * (a group: slots 16 i to 16 i + 15) take 9 d bytes, in an order of the library's
+ * own; page_size is a multiple of 16, the groups of a page's head follow one
+ * another, the page and head strides are non-negative multiples of 16 bytes. Pages
+ * may be moved and shared as a whole.
+ */
+
 /* sizeof of the structs as compiled into the library, for binding checks. */
 size_t sdpa_cache_bytes(void);
 size_t sdpa_cache_fwd_params_bytes(void);
 size_t sdpa_cache_append_params_bytes(void);
+size_t sdpa_cache_read_params_bytes(void);
 size_t sdpa_cache_weigh_params_bytes(void);
 size_t sdpa_cache_evict_params_bytes(void);
 
@@ -97,6 +116,11 @@ size_t sdpa_cache_evict_params_bytes(void);
  * h_q / h_kv; d = 64: up to 16), and rounded to the I/O dtype, as sdpa_fwd
  * does, where it has more. In f16 P is held on a grid of 2^-31 of the row's
  * heaviest key, or finer: keys lighter than half of that count in LSE alone.
+ * Over a cache in 4 bits the new tokens' keys and values count as they are, not
+ * as they will be held; all products are of f16 numbers: bf16 rows of q are scaled
+ * by a power of two for them, the new tokens' k and v are rounded to f16 (which
+ * changes none between 2^-17 and 65504 in magnitude; beyond, 65504 counts). P is
+ * f16, with its remainder for f16 output in units of up to 16 rows of a kv-head.
  * Keys on pages out of range are left out; lengths out of [0, capacity] are
  * taken as the nearer end. Not read, or without effect whatever they hold, are
  * slots behind a sequence's keys, keys that no row's window has, and new tokens
@@ -150,6 +174,29 @@ typedef struct sdpa_cache_append_params {
     const int32_t *offsets;       /* device [b+1], THD only */
 } sdpa_cache_append_params;
 sdpa_status_t sdpa_cache_append(const sdpa_cache *cache, const sdpa_cache_append_params *params, void *stream);
+
+/*
+ * The cached rows of each sequence in dtype, in slot order: output row j of
+ * sequence i is its slot start[i] + j (start: 0 without the array).
+ *  SDPA_BSHD: k, v [b][s][h_kv][d];
+ *  SDPA_THD: k, v [total][h_kv][d], offsets [b+1] with offsets[0] = 0 and
+ *    offsets[b] = total; a sequence's rows are those of its slot.
+ * counts[i] rows come out (all without counts); rows behind them and behind the
+ * sequence's last key are zeros. Of a cache in 4 bits the values are those that the
+ * codes stand for. A start outside [0, length], a count outside the rows there are
+ * and a row of no sequence are reported; rows on pages out of range are zeros.
+ */
+typedef struct sdpa_cache_read_params {
+    int32_t layout;
+    int32_t reserved0;
+    int64_t s, total;             /* rows per sequence (BSHD), THD rows */
+    const int32_t *start;         /* device [b] or NULL */
+    const int32_t *counts;        /* device [b] or NULL */
+    const int32_t *offsets;       /* device [b+1], THD only */
+    void *k, *v;
+    int64_t k_stride[3], v_stride[3];   /* batch (THD: ignored), token, head */
+} sdpa_cache_read_params;
+sdpa_status_t sdpa_cache_read(const sdpa_cache* cache, const sdpa_cache_read_params* params, void* stream);
 
 /*
  * Adds to each cached key's weight the attention that it gets from given rows:

@@ -21,10 +21,11 @@ from typing import Optional
 from . import _build
 from . import cache as _cache
 from .cache import (KVCache, SdpaCache, SdpaCacheAppendParams, SdpaCacheEvictParams, SdpaCacheFwdParams,
-                    SdpaCacheWeighParams, cache_append, cache_evict, cache_forward, cache_weigh,
+                    SdpaCacheReadParams, SdpaCacheWeighParams, cache_append, cache_evict, cache_forward, cache_read,
+                    cache_weigh,
                     sdpa_cache_append, sdpa_cache_check_status, sdpa_cache_evict,
                     sdpa_cache_evict_workspace_bytes, sdpa_cache_fwd, sdpa_cache_fwd_workspace_bytes,
-                    sdpa_cache_test_hook, sdpa_cache_weigh)
+                    sdpa_cache_read, sdpa_cache_test_hook, sdpa_cache_weigh)
 
 SDPA_OK, SDPA_ERR_INVALID_ARG, SDPA_ERR_UNSUPPORTED, SDPA_ERR_CUDA = 0, 1, 2, 3
 SDPA_ERR_TIMEOUT, SDPA_ERR_BAD_LENGTHS, SDPA_ERR_WORKSPACE, SDPA_ERR_BOUNDS = 4, 5, 6, 7

@@ -1,8 +1,8 @@
 """Key/value cache: binding of ``include/sdpa_cache.h``.
 
-``KVCache`` names the tensors of a cache; ``cache_forward``, ``cache_append``,
-``cache_weigh`` and ``cache_evict`` are the calls a PyTorch user makes, each
-over the C entry point of the same name. All work runs in the CUDA library on
+``KVCache`` names the tensors of a cache, in 16 bits or in 4; ``cache_forward``,
+``cache_append``, ``cache_read``, ``cache_weigh`` and ``cache_evict`` are the
+calls a PyTorch user makes, each over the C entry point of the same name. All work runs in the CUDA library on
 torch's current stream; the calls can be captured into a CUDA graph. They serve
 decoding: none of them records a gradient.
 
@@ -27,7 +27,7 @@ _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 class SdpaCache(ctypes.Structure):
     """Mirror of ``sdpa_cache`` (field order and types as in the header)."""
     _fields_ = [
-        ("dtype", _i32), ("reserved0", _i32),
+        ("dtype", _i32), ("bits", _i32),
         ("b", _i64), ("h_kv", _i64), ("d", _i64),
         ("n_pages", _i64), ("page_size", _i64), ("max_pages", _i64),
         ("k", _vp), ("v", _vp), ("k_stride", _i64x3), ("v_stride", _i64x3),
@@ -54,6 +54,14 @@ class SdpaCacheAppendParams(ctypes.Structure):
     ]
 
 
+class SdpaCacheReadParams(ctypes.Structure):
+    _fields_ = [
+        ("layout", _i32), ("reserved0", _i32), ("s", _i64), ("total", _i64),
+        ("start", _vp), ("counts", _vp), ("offsets", _vp),
+        ("k", _vp), ("v", _vp), ("k_stride", _i64x3), ("v_stride", _i64x3),
+    ]
+
+
 class SdpaCacheWeighParams(ctypes.Structure):
     _fields_ = [
         ("s_q", _i64), ("h_q", _i64), ("window_left", _i64),
@@ -67,8 +75,8 @@ class SdpaCacheEvictParams(ctypes.Structure):
 
 
 ENTRY_POINTS = ("sdpa_cache_bytes", "sdpa_cache_fwd_params_bytes", "sdpa_cache_append_params_bytes",
-                "sdpa_cache_weigh_params_bytes", "sdpa_cache_evict_params_bytes",
-                "sdpa_cache_fwd_workspace_bytes", "sdpa_cache_fwd", "sdpa_cache_append",
+                "sdpa_cache_read_params_bytes", "sdpa_cache_weigh_params_bytes", "sdpa_cache_evict_params_bytes",
+                "sdpa_cache_fwd_workspace_bytes", "sdpa_cache_fwd", "sdpa_cache_append", "sdpa_cache_read",
                 "sdpa_cache_weigh", "sdpa_cache_evict_workspace_bytes", "sdpa_cache_evict",
                 "sdpa_cache_check_status", "sdpa_cache_test_hook")
 
@@ -76,7 +84,7 @@ ENTRY_POINTS = ("sdpa_cache_bytes", "sdpa_cache_fwd_params_bytes", "sdpa_cache_a
 def bind(lib) -> None:
     """Argument and result types of the cache's entry points."""
     C, sz, st = ctypes.POINTER(SdpaCache), ctypes.c_size_t, ctypes.c_int
-    for name in ENTRY_POINTS[:5]:
+    for name in ENTRY_POINTS[:6]:
         getattr(lib, name).argtypes = []
         getattr(lib, name).restype = sz
     for name, params in (("fwd", SdpaCacheFwdParams), ("evict", SdpaCacheEvictParams)):
@@ -84,7 +92,7 @@ def bind(lib) -> None:
         f.argtypes, f.restype = [C, ctypes.POINTER(params)], sz
         f = getattr(lib, f"sdpa_cache_{name}")
         f.argtypes, f.restype = [C, ctypes.POINTER(params), _vp, sz, _vp], st
-    for name, params in (("append", SdpaCacheAppendParams), ("weigh", SdpaCacheWeighParams)):
+    for name, params in (("append", SdpaCacheAppendParams), ("read", SdpaCacheReadParams), ("weigh", SdpaCacheWeighParams)):
         f = getattr(lib, f"sdpa_cache_{name}")
         f.argtypes, f.restype = [C, ctypes.POINTER(params), _vp], st
     lib.sdpa_cache_check_status.argtypes, lib.sdpa_cache_check_status.restype = [C, _vp], st
@@ -114,7 +122,7 @@ class _Calls:
             f = lib[f"sdpa_cache_{name}"]
             f.argtypes, f.restype = [_vp, ctypes.c_char_p, _vp, ctypes.c_size_t, _vp], ctypes.c_int
             setattr(self, name, f)
-        for name in ("append", "weigh"):
+        for name in ("append", "read", "weigh"):
             f = lib[f"sdpa_cache_{name}"]
             f.argtypes, f.restype = [_vp, ctypes.c_char_p, _vp], ctypes.c_int
             setattr(self, name, f)
@@ -125,6 +133,7 @@ class _Calls:
 
 _FWD = struct.Struct("3qfi3Q12q5Q")
 _APPEND = struct.Struct("2i3q2Q6q3Q")
+_READ = struct.Struct("2i2q5Q6q")
 _WEIGH = struct.Struct("3qfiQ3q2Q")
 _EVICT = struct.Struct("3q")
 _calls = None
@@ -149,6 +158,10 @@ def sdpa_cache_fwd(cache, params, workspace: int, workspace_bytes: int, stream: 
 
 def sdpa_cache_append(cache, params, stream: int) -> int:
     return _lib().sdpa_cache_append(cache, params, stream)
+
+
+def sdpa_cache_read(cache, params, stream: int) -> int:
+    return _lib().sdpa_cache_read(cache, params, stream)
 
 
 def sdpa_cache_weigh(cache, params, stream: int) -> int:
@@ -231,23 +244,47 @@ class KVCache:
     neither; weights: fp32 [b, h_kv, capacity]. All on one CUDA device, and
     changed in place by the calls. `status` is the int32 word that holds the
     first problem found on the device (see check_status).
+
+    A cache in 4 bits: k, v are uint8 [n_pages, h_kv, page_size / 16, 9 d], as
+    cache_append fills them (16 features of a key as whole numbers with one
+    scale, in an order of the library's own), and `dtype` is that of the calls'
+    tensors. It takes cache_append, cache_read and cache_forward.
     """
 
-    def __init__(self, k, v, lengths, *, page_table=None, next_pos=None, positions=None, weights=None):
+    def __init__(self, k, v, lengths, *, page_table=None, next_pos=None, positions=None, weights=None, dtype=None):
         import torch
         from . import SDPA_BF16, SDPA_F16
+        bits = 4 if k.dtype == torch.uint8 else 16
         if k.dim() != 4:
-            raise ValueError(f"k: expected [n_pages, page_size, h_kv, d], got {tuple(k.shape)}")
-        if k.dtype not in (torch.bfloat16, torch.float16):
-            raise ValueError(f"unsupported dtype {k.dtype}")
-        n_pages, page_size, h_kv, d = k.shape
+            raise ValueError(f"k: expected [n_pages, page_size, h_kv, d], or uint8 [n_pages, h_kv, page_size / 16, 9 d]; "
+                             f"got {tuple(k.shape)}")
+        if bits == 4 and dtype is None:
+            raise ValueError("dtype: a cache in 4 bits needs that of the calls' tensors")
+        if bits == 16 and dtype not in (None, k.dtype):
+            raise ValueError(f"dtype: k is {k.dtype}, got {dtype}")
+        dtype = dtype or k.dtype
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"unsupported dtype {dtype}")
+        if bits == 4:
+            n_pages, h_kv, groups, nine_d = k.shape
+            if nine_d % 9:
+                raise ValueError(f"k: groups of 9 d bytes, got {nine_d}")
+            page_size, d = groups * 16, nine_d // 9
+        else:
+            n_pages, page_size, h_kv, d = k.shape
         dev, b = k.device, lengths.numel()
         i32 = torch.int32
         c = SdpaCache()
-        c.dtype = SDPA_BF16 if k.dtype == torch.bfloat16 else SDPA_F16
+        c.dtype = SDPA_BF16 if dtype == torch.bfloat16 else SDPA_F16
+        c.bits = bits
         c.b, c.h_kv, c.d, c.n_pages, c.page_size = b, h_kv, d, n_pages, page_size
-        c.k_stride = _i64x3(*_strides("k", k, tuple(k.shape), dev, k.dtype))
-        c.v_stride = _i64x3(*_strides("v", v, tuple(k.shape), dev, k.dtype))
+        for name, t in (("k", k), ("v", v)):
+            x, y, z = _strides(name, t, tuple(k.shape), dev, k.dtype)
+            if bits == 4:
+                if groups > 1 and z != nine_d:
+                    raise ValueError(f"{name}: the groups of a page's head must follow one another")
+                x, y, z = x, nine_d, y
+            setattr(c, name + "_stride", _i64x3(x, y, z))
         _apart("k", k)
         _apart("v", v)
         if page_table is not None:
@@ -271,13 +308,13 @@ class KVCache:
         c.status = self.status.data_ptr()
         self.k, self.v, self.lengths, self.page_table = k, v, lengths, page_table
         self.next_pos, self.positions, self.weights = next_pos, positions, weights
-        self.b, self.h_kv, self.d, self.dtype, self.device = b, h_kv, d, k.dtype, dev
+        self.b, self.h_kv, self.d, self.dtype, self.device, self.bits = b, h_kv, d, dtype, dev, bits
         self.params = c
-        self._ref, self._key, self._index = ctypes.addressof(c), (b, h_kv, d, dev, k.dtype), dev.index or 0
+        self._ref, self._key, self._index = ctypes.addressof(c), (b, h_kv, d, dev, dtype), dev.index or 0
         self._ws_bytes = {}     # workspace bytes of the calls made so far, by their sizes
 
     _own = frozenset(("k", "v", "lengths", "page_table", "next_pos", "positions", "weights", "status", "params", "capacity",
-                      "b", "h_kv", "d", "dtype", "device"))
+                      "b", "h_kv", "d", "dtype", "device", "bits"))
 
     def __setattr__(self, name, value):
         # the calls use the addresses taken by the constructor: another tensor under the name would not be seen
@@ -287,18 +324,28 @@ class KVCache:
 
     @classmethod
     def empty(cls, b: int, h_kv: int, d: int, max_len: int, *, dtype, device, page_size: int = 64,
-              track: bool = False) -> "KVCache":
+              track: bool = False, bits: int = 16) -> "KVCache":
         """An empty cache with room for max_len keys in each of b sequences;
-        `track`: with positions and weights, as weighing and eviction need."""
+        `track`: with positions and weights, as weighing and eviction need;
+        bits: 16 (K and V in dtype) or 4 (page_size: a multiple of 16)."""
         import torch
+        if bits not in (4, 16):
+            raise ValueError(f"bits={bits}: 4 or 16")
+        if bits == 4 and page_size % 16:
+            raise ValueError(f"page_size={page_size}: a multiple of 16 in a cache of 4 bits")
         per = -(-max_len // page_size)
         kw = dict(dtype=torch.int32, device=device)
-        k, v = (torch.zeros(b * per, page_size, h_kv, d, dtype=dtype, device=device) for _ in range(2))
+        if bits == 4:
+            shape, held = (b * per, h_kv, page_size // 16, 9 * d), torch.uint8
+        else:
+            shape, held = (b * per, page_size, h_kv, d), dtype
+        k, v = (torch.zeros(shape, dtype=held, device=device) for _ in range(2))
         extra = {}
         if track:
             extra = dict(next_pos=torch.zeros(b, **kw), positions=torch.full((b, h_kv, per * page_size), -1, **kw),
                          weights=torch.zeros(b, h_kv, per * page_size, device=device))
-        return cls(k, v, torch.zeros(b, **kw), page_table=torch.arange(b * per, **kw).view(b, per), **extra)
+        return cls(k, v, torch.zeros(b, **kw), page_table=torch.arange(b * per, **kw).view(b, per), dtype=dtype,
+                   **extra)
 
     def check_status(self) -> None:
         """Synchronises torch's current stream and raises if a call found a
@@ -424,6 +471,49 @@ def cache_append(cache: KVCache, k, v, *, index=None, counts=None, offsets=None,
     _check(c.append(cache._ref, p, c.stream(cache._index)), "sdpa_cache_append")
     if check_status:
         cache.check_status()
+
+
+def cache_read(cache: KVCache, *, start=None, counts=None, max_rows: Optional[int] = None, offsets=None,
+               total: Optional[int] = None, out=None, check_status: bool = False):
+    """The cached keys and values of each sequence in cache.dtype, in slot order.
+
+    Row j of sequence i is its slot start[i] + j (int32 [b]; from 0 without
+    start), counts[i] rows of it (int32 [b]; all of them without counts); rows
+    behind those and behind its last key are zeros. Returns (k, v) of
+    [b, max_rows, h_kv, d] (max_rows: the capacity unless given), or packed,
+    [total, h_kv, d], with offsets (int32 [b + 1]): the next part of a prompt
+    attends over them with `forward`.
+    """
+    c = _calls or _c()
+    b, h_kv, d, dev, dt = cache._key
+    if offsets is not None:
+        if total is None:
+            raise ValueError("packed rows need offsets and total")
+        if max_rows is not None:
+            raise ValueError("max_rows: only without offsets")
+        layout, s, shape = 1, 0, (total, h_kv, d)
+    else:
+        if total is not None:
+            raise ValueError("total: only with offsets")
+        layout, s, total = 0, cache.capacity if max_rows is None else max_rows, 0
+        shape = (b, s, h_kv, d)
+    if min(shape) < 0:
+        raise ValueError(f"rows: expected max_rows or total >= 0, got {s or total}")
+    if out is None:
+        k, v = c.empty(shape, dtype=dt, device=dev), c.empty(shape, dtype=dt, device=dev)
+    else:
+        k, v = out
+        _apart("out k", k)
+        _apart("out v", v)
+    sk, sv = (([0] if layout else []) + _strides(n, t, shape, dev, dt) for n, t in (("out k", k), ("out v", v)))
+    p = _READ.pack(layout, 0, s, total, 0 if start is None else _flat("start", start, (b,), dev, c.int32),
+                   0 if counts is None else _flat("counts", counts, (b,), dev, c.int32),
+                   0 if offsets is None else _flat("offsets", offsets, (b + 1,), dev, c.int32),
+                   k.data_ptr(), v.data_ptr(), *sk, *sv)
+    _check(c.read(cache._ref, p, c.stream(cache._index)), "sdpa_cache_read")
+    if check_status:
+        cache.check_status()
+    return k, v
 
 
 def cache_weigh(cache: KVCache, q, lse, *, scale: float, window_left: int = -1, q_pos=None,

@@ -1,0 +1,157 @@
+// cache4.cuh -- the cache in 4 bits: how 16 features of a key are held, and how
+// they come back.
+//
+// A block of 16 features x is held as whole numbers c = rint(x / s), -8 to 7, and a
+// scale s = max|x| / 7 rounded to a floating-point number of 5 exponent and 3
+// mantissa bits without a sign: the byte's value is that of the f16 with the bits
+// byte << 7. So its range (normal from 2^-14 on, steps of 2^-17 below) needs no
+// second scale, and c * s has 7 significant bits: it is exact in f16 and in bf16.
+// Scales end at 240: the constants that bring a value back (-264 s) stay within
+// f16. A block that holds an infinity or a NaN has the byte 0xff, a NaN.
+//
+// Whole numbers of 4 bits next to the same bits as a floating-point number (e2m1)
+// with a scale per 16: normal values come back 7.6 % off against 9.4 % (rms), and
+// in 2.75 instructions a pair against 4.
+//
+// 16 keys of a head ("group") are 9 d bytes in one run: their codes in the order
+// in which the lanes of a matrix instruction take them, then their scales.
+//   K: lane (g, t) of S^T = K Q^T has the features [t d/4, (t + 1) d/4) of the keys
+//      kappa(g) and kappa(g) + 2, kappa(g) = 4 (g / 2) + g % 2
+//   V: lane (g, t) of O^T = V^T P^T has the features [g d/8, (g + 1) d/8) of the
+//      keys 4t, 4t + 1 (first part) and 4t + 2, 4t + 3 (second)
+// Two 16-bit halves of a 32-bit word are the two values of a register: K's the even
+// and odd features of 8, V's two keys' values of the same 4 features. In a half
+// the codes c + 8 lie at bits 6-9 and 2-5, and the other two there after a swap of
+// its bytes, where an "or" with the bits of 16 and of 256 makes them the numbers
+// 16 + c + 8 and 256 + c + 8.
+#pragma once
+
+#include "cache.cuh"
+#include "ptx.cuh"
+
+namespace swa {
+
+constexpr float kMaxScale4 = 240.f;
+constexpr uint32_t kNanScale4 = 0xffu;
+
+template <int HD>
+struct Group4 {
+    static constexpr uint32_t kCodes = 8 * HD, kBytes = 9 * HD;
+};
+
+// Byte of a group at which K's word (8 features, from 8 * w8) of key x lies.
+template <int HD>
+__device__ __forceinline__ uint32_t k4_word(uint32_t x, uint32_t w8)
+{
+    const uint32_t g = 2 * (x >> 2) + (x & 1), h = (x >> 1) & 1;
+    constexpr uint32_t W = HD / 32;                 // words of a lane and key
+    const uint32_t t = w8 / W, w = w8 % W;
+    return HD == 128 ? h * 512 + (g * 4 + t) * 16 + w * 4 : (g * 4 + t) * 16 + h * 8 + w * 4;
+}
+
+// Byte of K's scale of key x, block f16 (16 features).
+template <int HD>
+__device__ __forceinline__ uint32_t k4_scale(uint32_t x, uint32_t f16)
+{
+    const uint32_t g = 2 * (x >> 2) + (x & 1), h = (x >> 1) & 1;
+    return Group4<HD>::kCodes + (HD == 128 ? (g * 4 + (f16 >> 1)) * 4 + h * 2 + (f16 & 1) : (g * 4 + f16) * 2 + h);
+}
+
+// Byte of V's half word of key x that has the 4 features from 4 * f4.
+template <int HD>
+__device__ __forceinline__ uint32_t v4_half(uint32_t x, uint32_t f4)
+{
+    constexpr uint32_t W = HD / 32;                 // words of a lane and part
+    const uint32_t t = x >> 2, part = (x >> 1) & 1, g = f4 / W, w = f4 % W;
+    return (HD == 128 ? part * 512 + (g * 4 + t) * 16 + w * 4 : (g * 4 + t) * 16 + part * 8 + w * 4) + (x & 1) * 2;
+}
+
+template <int HD>
+__device__ __forceinline__ uint32_t v4_scale(uint32_t x, uint32_t f16)
+{
+    return Group4<HD>::kCodes + f16 * 16 + x;
+}
+
+// Four codes (c + 8, 0 to 15) as the 16 bits of a half word, and back.
+__device__ __forceinline__ uint32_t pack_half4(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3)
+{
+    return c0 << 6 | c1 << 2 | c3 << 10 | (c2 & 3) << 14 | c2 >> 2;
+}
+
+__device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Two scales as f16 (both exact), and the offsets that go with them.
+struct Scale4 {
+    uint32_t s, n24, n264;
+};
+
+// SEL: byte_perm selector that puts the two scale bytes of w at bytes 1 and 3,
+// zeros (byte 4) at 0 and 2.
+template <uint32_t SEL>
+__device__ __forceinline__ Scale4 scale4(uint32_t w)
+{
+    Scale4 r;
+    r.s = __byte_perm(w, 0u, SEL) >> 1;
+    r.n24 = h2mul(r.s, 0xce00ce00u);        // -24
+    r.n264 = h2mul(r.s, 0xdc20dc20u);       // -264
+    return r;
+}
+
+// The 8 values of a word as 4 registers of two f16 (register j: code j of the low and of the high half).
+__device__ __forceinline__ void values4(uint32_t w, const Scale4& s, uint32_t (&r)[4])
+{
+    const uint32_t b = __byte_perm(w, 0u, 0x2301);
+    r[0] = h2fma((w & 0x03c003c0u) | 0x4c004c00u, s.s, s.n24);
+    r[1] = h2fma((w & 0x003c003cu) | 0x5c005c00u, s.s, s.n264);
+    r[2] = h2fma((b & 0x03c003c0u) | 0x4c004c00u, s.s, s.n24);
+    r[3] = h2fma((b & 0x003c003cu) | 0x5c005c00u, s.s, s.n264);
+}
+
+// The scale byte of a block whose largest magnitude is `most` (the bits of an
+// fp32; those of an infinity or a NaN are above every number's), and 1 / s (0
+// where the scale is 0: every code is 0 then).
+// The border between two scales, 7 times a number of 5 bits, and the inputs' 11
+// bits are on one grid: most / 7 is at least 2^-11 of itself away from a border
+// that it is not on, so that the fp32 quotient's rounding decides as the
+// exact one would; a quotient that is a border is exact.
+__device__ __forceinline__ uint32_t scale_byte4(uint32_t most_bits, float& inv)
+{
+    if (most_bits >= 0x7f800000u) {
+        inv = 0.f;
+        return kNanScale4;
+    }
+    const float v = fminf(__fdiv_rn(__uint_as_float(most_bits), 7.f), kMaxScale4);
+    // adding and taking away 2^20 times v's power of two, whose unit in the last place is an eighth of that power,
+    // rounds to the scales' grid (below 2^-14 it is that of 2^-14), ties to even
+    const uint32_t e = max(__float_as_uint(v) >> 23, 113u);
+    const float big = __uint_as_float((e + 20) << 23);
+    const float s = __fsub_rn(__fadd_rn(v, big), big);
+    inv = s > 0.f ? __frcp_rn(s) : 0.f;
+    return __half_as_ushort(__float2half_rn(s)) >> 7;
+}
+
+// rint(x / s), -8 to 7, + 8. A border (k + 1/2) s, 8 bits, is on the grid of x: x / s
+// is at least 2^-12 away from a border that it is not on, and x * inv within 2^-23 of itself;
+// rounding the product to multiples of 2^-14 puts what is on a border there, and then
+// ties go to even.
+__device__ __forceinline__ uint32_t code4(float x, float inv)
+{
+    constexpr float kGrid = 512.f + 256.f;      // its unit in the last place: 2^-14
+    const float y = fminf(fmaxf(__fmul_rn(x, inv), -16.f), 16.f);
+    const float z = __fsub_rn(__fadd_rn(y, kGrid), kGrid);
+    return static_cast<uint32_t>(min(max(__float2int_rn(z), -8), 7) + 8);
+}
+
+}  // namespace swa

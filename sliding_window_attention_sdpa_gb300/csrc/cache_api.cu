@@ -22,6 +22,8 @@ constexpr int64_t kWaitLimitNs = 2000000000LL;
 thread_local int64_t g_test_wait_ns = 0;
 thread_local int32_t g_test_stall = 0;
 
+int64_t imin(int64_t x, int64_t y) { return x < y ? x : y; }
+
 int64_t wait_limit() { return g_test_wait_ns > 0 ? g_test_wait_ns : kWaitLimitNs; }
 
 constexpr int64_t kMax31 = int64_t(1) << 31;
@@ -52,6 +54,31 @@ sdpa_status_t check_strides(const char* name, const int64_t* st, int first = 0)
 // Whether any sequence has room for a key; without, the arrays may be empty (NULL).
 bool holds_keys(const sdpa_cache* c) { return c->b > 0 && c->max_pages > 0; }
 
+// A cache in 4 bits: pages of whole groups of 16 keys, one behind the other; strides in bytes.
+sdpa_status_t check_groups(const sdpa_cache* c)
+{
+    if (c->page_size % 16 != 0)
+        return fail(SDPA_ERR_UNSUPPORTED, "cache page_size=%lld: a multiple of 16 in a cache of 4 bits", (long long)c->page_size);
+    const struct { const char* n; const int64_t* s; } strides[] = {{"cache k", c->k_stride}, {"cache v", c->v_stride}};
+    for (const auto& x : strides) {
+        if (x.s[1] != 9 * c->d)
+            return fail(SDPA_ERR_INVALID_ARG, "%s_stride[1]=%lld: groups of 16 keys follow one another, 9 d = %lld bytes each",
+                        x.n, (long long)x.s[1], (long long)(9 * c->d));
+        for (int i = 0; i < 3; i += 2)
+            if (x.s[i] < 0 || x.s[i] % 16 != 0)
+                return fail(SDPA_ERR_INVALID_ARG, "%s_stride[%d]=%lld: strides must be non-negative multiples of 16 bytes", x.n, i,
+                            (long long)x.s[i]);
+    }
+    return SDPA_OK;
+}
+
+// What a cache in 4 bits does not do.
+sdpa_status_t refuse_groups(const sdpa_cache* c, const char* what)
+{
+    if (c->bits != 4) return SDPA_OK;
+    return fail(SDPA_ERR_UNSUPPORTED, "%s: not of a cache in 4 bits (bits=4); one in its dtype is weighed and evicted", what);
+}
+
 // The cache's fields, without device access.
 sdpa_status_t check_cache(const sdpa_cache* c)
 {
@@ -79,6 +106,9 @@ sdpa_status_t check_cache(const sdpa_cache* c)
                     (long long)c->max_pages, (long long)c->n_pages);
     if (holds_keys(c) && (c->positions == nullptr) != (c->next_pos == nullptr))
         return fail(SDPA_ERR_INVALID_ARG, "cache positions and next_pos must both be set or both be NULL");
+    if (c->bits != 0 && c->bits != 4 && c->bits != 16)
+        return fail(SDPA_ERR_INVALID_ARG, "cache bits=%d: expected 0 or 16 (K and V in dtype) or 4", c->bits);
+    if (c->bits == 4) return check_groups(c);
     sdpa_status_t st;
     if ((st = check_strides("cache k", c->k_stride)) != SDPA_OK) return st;
     return check_strides("cache v", c->v_stride);
@@ -134,6 +164,7 @@ swa::CacheView view_of(const sdpa_cache* c)
     v.page_shift = -1;
     for (int i = 0; i < 31; ++i)
         if (c->page_size == int64_t(1) << i) v.page_shift = i;
+    v.bits = c->bits == 4 ? 4 : 16;
     v.cap = c->page_size * c->max_pages;
     v.k = static_cast<uint16_t*>(c->k);
     v.v = static_cast<uint16_t*>(c->v);
@@ -176,14 +207,26 @@ FwdSize fwd_size(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa:
 {
     FwdSize z{};
     int64_t keys = c->page_size * c->max_pages;
+    const int64_t room = keys;
     if (p->window_left >= 0 && c->positions == nullptr && p->window_left < keys) keys = p->window_left;
     const int64_t rows = p->s_q * (p->h_q / c->h_kv);
     z.blocks = (rows + plan.rows - 1) / plan.rows;
     // the reach begins up to 15 keys before (63 in the tile kernel), the new tokens end up to 15 off a group of 16
     z.tiles = (keys + (plan.variant >= swa::kTiles128 ? 78 : 30) + ((p->s_q + 15) & ~int64_t(15)) + plan.tile - 1) / plan.tile;
+    if (c->bits == 4) {
+        // the reach begins up to a warp's step - 1 before, ends as far behind, and the new tokens are a step
+        const int64_t gk = plan.tile / 4;
+        z.tiles = (imin((keys + 2 * (gk - 1)), (room + gk - 1) / gk * gk) + gk + plan.tile - 1) / plan.tile;
+    }
     z.units = double(c->b) * double(c->h_kv) * double(z.blocks);
     z.total = z.units * double(z.tiles);
     return z;
+}
+
+swa::CacheFwdPlan fwd_plan(const sdpa_cache* c, const sdpa_cache_fwd_params* p)
+{
+    const int64_t rows = p->s_q * (p->h_q / c->h_kv);
+    return c->bits == 4 ? swa::cache4_fwd_plan(c->d, rows) : swa::cache_fwd_plan(c->d, rows);
 }
 
 struct FwdLayout {
@@ -198,12 +241,13 @@ struct FwdLayout {
 // a join of 1.5 cut; 900 keys 13.4 whole, 7.6 and 4.1 cut; 1800 keys 20.5 whole,
 // 8.0 and 3.4 cut.
 constexpr int64_t kWholeKeys = 512;
+constexpr int64_t kWholeKeys4 = 1024;
 
 FwdLayout fwd_layout(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa::CacheFwdPlan& plan)
 {
     FwdLayout l{};
     const FwdSize z = fwd_size(c, p, plan);
-    if (z.tiles * plan.tile <= kWholeKeys && z.units < double(kMax31)) {
+    if (z.tiles * plan.tile <= (c->bits == 4 ? kWholeKeys4 : kWholeKeys) && z.units < double(kMax31)) {
         l.parts = static_cast<int32_t>(z.units);
         l.whole = 1;
         return l;
@@ -232,7 +276,7 @@ sdpa_status_t check_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p)
         {"q", p->q_stride}, {"k", p->k_stride}, {"v", p->v_stride}, {"o", p->o_stride}};
     for (const auto& x : strides)
         if ((st = check_strides(x.n, x.s)) != SDPA_OK) return st;
-    const swa::CacheFwdPlan plan = swa::cache_fwd_plan(c->d, p->s_q * (p->h_q / c->h_kv));
+    const swa::CacheFwdPlan plan = fwd_plan(c, p);
     if (fwd_size(c, p, plan).total >= double(int64_t(1) << 50))
         return fail(SDPA_ERR_UNSUPPORTED, "the forward's tiles (b * h_kv * row blocks * keys) pass 2^50");
     return SDPA_OK;
@@ -261,6 +305,7 @@ sdpa_status_t check_evict(const sdpa_cache* c, const sdpa_cache_evict_params* p)
     sdpa_status_t st = check_cache(c);
     if (st != SDPA_OK) return st;
     if (p == nullptr) return fail(SDPA_ERR_INVALID_ARG, "params is NULL");
+    if ((st = refuse_groups(c, "evict")) != SDPA_OK) return st;
     if (holds_keys(c) && (c->positions == nullptr || c->weights == nullptr))
         return fail(SDPA_ERR_INVALID_ARG, "evict needs a cache with positions and weights");
     if (p->keep < 0 || p->first < 0 || p->recent < 0 || p->keep >= kMax31 || p->first > p->keep ||
@@ -308,6 +353,7 @@ extern "C" {
 size_t sdpa_cache_bytes(void) { return sizeof(sdpa_cache); }
 size_t sdpa_cache_fwd_params_bytes(void) { return sizeof(sdpa_cache_fwd_params); }
 size_t sdpa_cache_append_params_bytes(void) { return sizeof(sdpa_cache_append_params); }
+size_t sdpa_cache_read_params_bytes(void) { return sizeof(sdpa_cache_read_params); }
 size_t sdpa_cache_weigh_params_bytes(void) { return sizeof(sdpa_cache_weigh_params); }
 size_t sdpa_cache_evict_params_bytes(void) { return sizeof(sdpa_cache_evict_params); }
 
@@ -315,7 +361,7 @@ size_t sdpa_cache_fwd_workspace_bytes(const sdpa_cache* c, const sdpa_cache_fwd_
 {
     if (check_fwd(c, p) != SDPA_OK) return 0;
     clear_error();
-    return fwd_layout(c, p, swa::cache_fwd_plan(c->d, p->s_q * (p->h_q / c->h_kv))).total;
+    return fwd_layout(c, p, fwd_plan(c, p)).total;
 }
 
 sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p, void* ws, size_t ws_bytes,
@@ -323,7 +369,7 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
 {
     sdpa_status_t st = check_fwd(c, p);
     if (st != SDPA_OK) return st;
-    const swa::CacheFwdPlan plan = swa::cache_fwd_plan(c->d, p->s_q * (p->h_q / c->h_kv));
+    const swa::CacheFwdPlan plan = fwd_plan(c, p);
     const FwdLayout l = fwd_layout(c, p, plan);
     if ((st = check_ws(ws, ws_bytes, l.total)) != SDPA_OK) return st;
     int dev = 0;
@@ -363,6 +409,13 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.part_o = at<float>(ws, l.part_o);
     a.part_ml = at<float>(ws, l.part_ml);
     a.cuts = at<swa::CacheFwdCut>(ws, l.cuts);
+    if (c->bits == 4) {
+        swa::Cache4FwdArgs qa{};
+        qa.f = a;
+        qa.copy_keys = plan.tile / 4;
+        while (c->page_size % qa.copy_keys != 0) qa.copy_keys >>= 1;
+        return cuda_status(swa::launch_cache4_fwd(qa, c->dtype, static_cast<cudaStream_t>(stream)), "cache forward launch");
+    }
     if (c->n_pages > 0) {
         // boxes that divide a page, of 8 rows at least: up to 64 (a key tile) for the tile kernel, 16 for the other; an unpaged
         // sequence's keys follow one another
@@ -406,7 +459,47 @@ sdpa_status_t sdpa_cache_append(const sdpa_cache* c, const sdpa_cache_append_par
     a.index = p->index;
     a.counts = p->counts;
     a.offsets = thd ? p->offsets : nullptr;
-    return cuda_status(swa::launch_cache_append(a, static_cast<cudaStream_t>(stream)), "cache append launch");
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return cuda_status(c->bits == 4 ? swa::launch_cache4_append(a, c->dtype, cs) : swa::launch_cache_append(a, cs),
+                       "cache append launch");
+}
+
+sdpa_status_t sdpa_cache_read(const sdpa_cache* c, const sdpa_cache_read_params* p, void* stream)
+{
+    sdpa_status_t st = check_cache(c);
+    if (st != SDPA_OK) return st;
+    if (p == nullptr) return fail(SDPA_ERR_INVALID_ARG, "params is NULL");
+    if (p->layout != SDPA_BSHD && p->layout != SDPA_THD)
+        return fail(SDPA_ERR_INVALID_ARG, "layout: expected SDPA_BSHD or SDPA_THD, got %d", p->layout);
+    const bool thd = p->layout == SDPA_THD;
+    if (!thd && (p->s < 0 || p->s >= kMax31)) return fail(SDPA_ERR_INVALID_ARG, "s=%lld: must be 0 to 2^31 - 1", (long long)p->s);
+    if (thd && (p->total < 0 || p->total >= kMax31))
+        return fail(SDPA_ERR_INVALID_ARG, "total=%lld: must be 0 to 2^31 - 1", (long long)p->total);
+    if (thd && p->offsets == nullptr) return fail(SDPA_ERR_INVALID_ARG, "THD layout needs offsets");
+    if ((st = check_strides("k", p->k_stride, thd ? 1 : 0)) != SDPA_OK) return st;
+    if ((st = check_strides("v", p->v_stride, thd ? 1 : 0)) != SDPA_OK) return st;
+    int dev = 0;
+    if ((st = current_device(&dev)) != SDPA_OK) return st;
+    const int64_t rows = c->b == 0 ? 0 : thd ? p->total : c->b * p->s;
+    const Ptr ptrs[] = {{"k", p->k, rows > 0, 16},
+                        {"v", p->v, rows > 0, 16},
+                        {"start", p->start, false, 4},
+                        {"counts", p->counts, false, 4},
+                        {"offsets", p->offsets, thd, 4}};
+    if ((st = check_cache_ptrs(c, dev)) != SDPA_OK || (st = check_ptrs(ptrs, dev)) != SDPA_OK) return st;
+    if (rows == 0) return SDPA_OK;
+    swa::CacheReadArgs a{};
+    a.c = view_of(c);
+    a.s = p->s;
+    a.rows = rows;
+    a.start = p->start;
+    a.counts = p->counts;
+    a.offsets = thd ? p->offsets : nullptr;
+    a.k = static_cast<uint16_t*>(p->k);
+    a.v = static_cast<uint16_t*>(p->v);
+    copy3(a.k_stride, p->k_stride);
+    copy3(a.v_stride, p->v_stride);
+    return cuda_status(swa::launch_cache_read(a, c->dtype, static_cast<cudaStream_t>(stream)), "cache read launch");
 }
 
 sdpa_status_t sdpa_cache_weigh(const sdpa_cache* c, const sdpa_cache_weigh_params* p, void* stream)
@@ -414,6 +507,7 @@ sdpa_status_t sdpa_cache_weigh(const sdpa_cache* c, const sdpa_cache_weigh_param
     sdpa_status_t st = check_cache(c);
     if (st != SDPA_OK) return st;
     if (p == nullptr) return fail(SDPA_ERR_INVALID_ARG, "params is NULL");
+    if ((st = refuse_groups(c, "weigh")) != SDPA_OK) return st;
     if (holds_keys(c) && c->weights == nullptr) return fail(SDPA_ERR_INVALID_ARG, "weigh needs a cache with weights");
     if (p->s_q < 1) return fail(SDPA_ERR_INVALID_ARG, "s_q=%lld: must be >= 1", (long long)p->s_q);
     if ((st = check_rows(c, p->s_q, p->h_q, p->window_left, p->scale)) != SDPA_OK) return st;

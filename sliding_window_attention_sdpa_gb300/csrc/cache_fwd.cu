@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(256) cache_fwd_join_kernel(const __grid_consta
     // a bound on them are on their way together: 296 rows 11 us, 15 to 16 with one)
     static_assert(kPartialRows % RW == 0, "");
     const int r = SPREAD ? blockIdx.y : (blockIdx.y * 8 + warp) * RW;
-    if (r0 + r >= R) return;
+    if ((ROWS % (8 * RW) != 0 && r >= ROWS) || r0 + r >= R) return;
     float top[RW], sum[RW], x[RW][E];
 #pragma unroll
     for (int j = 0; j < RW; ++j) {
@@ -738,6 +738,19 @@ CacheFwdPlan cache_fwd_plan(int64_t d, int64_t rows)
     if (rows <= 8) return CacheFwdPlan{kRows64x8, 8, 128, 2, 4};
     if (rows <= 16) return CacheFwdPlan{kRows64x16, 16, 128, 2, 4};
     return CacheFwdPlan{kTiles64, 256, 64, 1, 8};
+}
+
+cudaError_t launch_cache_fwd_join(const CacheFwdArgs& a, int dtype, int rows, cudaStream_t s)
+{
+    const bool bf16 = dtype == SDPA_BF16;
+    if (a.c.d == 128) {
+        if (rows == 8) return bf16 ? launch_join<128, true, 8>(a, s) : launch_join<128, false, 8>(a, s);
+        if (rows == 16) return bf16 ? launch_join<128, true, 16>(a, s) : launch_join<128, false, 16>(a, s);
+        return bf16 ? launch_join<128, true, 256>(a, s) : launch_join<128, false, 256>(a, s);
+    }
+    if (rows == 8) return bf16 ? launch_join<64, true, 8>(a, s) : launch_join<64, false, 8>(a, s);
+    if (rows == 16) return bf16 ? launch_join<64, true, 16>(a, s) : launch_join<64, false, 16>(a, s);
+    return bf16 ? launch_join<64, true, 256>(a, s) : launch_join<64, false, 256>(a, s);
 }
 
 cudaError_t launch_cache_fwd(const CacheTileArgs& a, int dtype, cudaStream_t s)

@@ -192,6 +192,16 @@ __device__ __forceinline__ SeqView seq_view(const CacheFwdArgs& a, int64_t bi, i
     return v;
 }
 
+// The same of a cache in 4 bits: the line starts at a multiple of gk keys, and so
+// do the new tokens behind it (at most gk of them).
+__device__ __forceinline__ SeqView seq_view4(const CacheFwdArgs& a, int64_t bi, int tk, int gk)
+{
+    SeqView v = seq_view(a, bi, tk, gk);
+    v.new0 = static_cast<int32_t>(((static_cast<int64_t>(v.len) + gk - 1) & ~static_cast<int64_t>(gk - 1)) - v.lo);
+    v.tiles = (v.new0 + gk + tk - 1) / tk;
+    return v;
+}
+
 // New token r's mask as it is given (r < nq), without the bits from nq on.
 __device__ __forceinline__ uint64_t given_mask(const CacheFwdArgs& a, int64_t bi, int32_t nq, int r)
 {

@@ -17,6 +17,7 @@ struct CacheView {
     uint32_t page_size, max_pages;
     int32_t page_shift;             // log2 of page_size if it is a power of two, else -1
     int64_t cap;                    // max_pages * page_size, < 2^31
+    int32_t bits;                   // 4: groups as in cache4.cuh, strides in bytes (page, -, head)
     uint16_t *k, *v;
     int64_t k_stride[3], v_stride[3];   // page, row, head
     const int32_t* page_table;
@@ -43,6 +44,10 @@ struct CacheFwdPlan {
     int variant, rows, tile, occ, unit_cost;
 };
 CacheFwdPlan cache_fwd_plan(int64_t d, int64_t rows);
+
+// The same for a cache in 4 bits.
+enum Cache4FwdVariant { kQ4Rows128x8, kQ4Rows128x16, kQ4Rows64x8, kQ4Rows64x16 };
+CacheFwdPlan cache4_fwd_plan(int64_t d, int64_t rows);
 
 struct CacheFwdArgs {
     CacheView c;
@@ -75,6 +80,11 @@ struct CacheTileArgs {
     int32_t box_rows;
 };
 
+struct Cache4FwdArgs {
+    CacheFwdArgs f;
+    int32_t copy_keys;      // keys of a copy: a power of two from 16 that divides a page, at most a warp's step
+};
+
 struct CacheAppendArgs {
     CacheView c;
     int32_t thd;
@@ -83,6 +93,14 @@ struct CacheAppendArgs {
     int64_t k_stride[3], v_stride[3];
     const int32_t *index, *counts, *offsets;
     int32_t rows_per_cta;
+};
+
+struct CacheReadArgs {
+    CacheView c;
+    int64_t s, rows;        // rows per sequence (without offsets), all output rows
+    const int32_t *start, *counts, *offsets;
+    uint16_t *k, *v;
+    int64_t k_stride[3], v_stride[3];   // batch, token, head
 };
 
 struct CacheWeighArgs {
@@ -126,6 +144,12 @@ cudaError_t allow_smem(F* kern, int bytes, std::atomic<uint64_t>& done)
 
 cudaError_t launch_cache_fwd(const CacheTileArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_cache_fwd_tiles(const CacheTileArgs& a, int dtype, cudaStream_t s);
+// The join behind a forward kernel whose units have `rows` rows (8, 16 or 256).
+cudaError_t launch_cache_fwd_join(const CacheFwdArgs& a, int dtype, int rows, cudaStream_t s);
+cudaError_t launch_cache4_fwd(const Cache4FwdArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_cache4_append(const CacheAppendArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_cache_advance(const CacheAppendArgs& a, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheReadArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheAppendArgs& a, cudaStream_t s);
 cudaError_t launch_cache_weigh(const CacheWeighArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_cache_evict(const CacheEvictArgs& a, cudaStream_t s);

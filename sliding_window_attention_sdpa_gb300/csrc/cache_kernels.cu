@@ -2,67 +2,12 @@
 #include <cooperative_groups.h>
 
 #include "cache.cuh"
+#include "cache_append.cuh"
 #include "ptx.cuh"
 
 namespace swa {
 
 // ---------------------------------------------------------------- append
-
-namespace {
-
-// Rows that sequence bi appends, from which source row, behind how many keys;
-// -1 rows (recorded) if they cannot be appended. Every thread of the CTA calls it.
-struct AppendPlan {
-    int64_t src0;
-    int32_t n, len;
-};
-
-__device__ __forceinline__ AppendPlan append_plan(const CacheAppendArgs& a, int64_t bi)
-{
-    AppendPlan p;
-    p.len = a.c.lengths[bi];
-    p.src0 = 0;
-    int64_t most = a.index ? a.n : a.s;
-    bool ok = p.len >= 0 && p.len <= a.c.cap;
-    if (a.thd) {
-        p.src0 = a.offsets[bi];
-        const int64_t end = a.offsets[bi + 1];
-        most = end - p.src0;
-        ok = ok && p.src0 >= 0 && most >= 0 && most <= a.s && end <= a.total;
-    }
-    int64_t n = a.counts ? a.counts[bi] : most;
-    ok = ok && n >= 0 && n <= most && p.len + n <= a.c.cap;
-    if (a.c.next_pos) ok = ok && a.c.next_pos[bi] >= 0 && a.c.next_pos[bi] + n <= 0x7fffffff;
-    bool fine = true;
-    if (ok && a.index)
-        for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
-            const int32_t x = a.index[bi * a.n + i];
-            fine = fine && x >= 0 && x < a.s;
-        }
-    if (!__syncthreads_and(ok && fine)) {
-        if (threadIdx.x == 0) set_status(a.c.status, SDPA_ERR_BAD_LENGTHS);
-        p.n = -1;
-        return p;
-    }
-    bool paged = true;
-    if (n > 0 && a.c.page_table != nullptr) {
-        const uint32_t p0 = static_cast<uint32_t>(p.len) / a.c.page_size;
-        const uint32_t p1 = static_cast<uint32_t>(p.len + n - 1) / a.c.page_size;
-        for (uint32_t i = p0 + threadIdx.x; i <= p1; i += blockDim.x) {
-            const int32_t page = a.c.page_table[bi * a.c.max_pages + i];
-            paged = paged && page >= 0 && page < a.c.n_pages;
-        }
-    }
-    if (!__syncthreads_and(paged)) {
-        if (threadIdx.x == 0) set_status(a.c.status, SDPA_ERR_BOUNDS);
-        p.n = -1;
-        return p;
-    }
-    p.n = static_cast<int32_t>(n);
-    return p;
-}
-
-}  // namespace
 
 // Bound by reading and writing each row once: prompts of 16 sequences (68,000
 // rows of 8 kv-heads, d = 128, in bf16) 89 us, 6.2 TB/s. A thread copies 16
@@ -141,7 +86,13 @@ cudaError_t launch_cache_append(const CacheAppendArgs& a0, cudaStream_t s)
                     static_cast<unsigned>(imax64(1, (most + a.rows_per_cta - 1) / a.rows_per_cta)));
     if (a.c.d == 64) cache_append_kernel<64><<<grid, 256, 0, s>>>(a);
     else cache_append_kernel<128><<<grid, 256, 0, s>>>(a);
-    if (grid.y > 1) cache_advance_kernel<<<static_cast<unsigned>(a.c.b), 256, 0, s>>>(a);
+    if (grid.y > 1) return launch_cache_advance(a, s);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_advance(const CacheAppendArgs& a, cudaStream_t s)
+{
+    cache_advance_kernel<<<static_cast<unsigned>(a.c.b), 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 
