@@ -7,7 +7,8 @@ functions ``sdpa_bwd_workspace_bytes``, ``sdpa_bwd_preprocess``, ``sdpa_bwd``,
 mirror the C entry points one to one; ``backward()`` is the convenience call a
 PyTorch user makes (it allocates outputs and the workspace with torch and runs
 the four kernels on the current stream). The key/value cache's calls
-(``include/sdpa_cache.h``) are in ``cache.py`` and offered here by name.
+(``include/sdpa_cache.h``) are in ``cache.py``, the norm and rotation of queries
+and keys (``include/sdpa_rope.h``) in ``rope.py``, and offered here by name.
 
 If the compiled library is missing this module raises: there is no fallback.
 """
@@ -20,12 +21,15 @@ from typing import Optional
 
 from . import _build
 from . import cache as _cache
+from . import rope as _rope
 from .cache import (KVCache, SdpaCache, SdpaCacheAppendParams, SdpaCacheEvictParams, SdpaCacheFwdParams,
                     SdpaCacheReadParams, SdpaCacheWeighParams, cache_append, cache_evict, cache_forward, cache_read,
                     cache_weigh,
                     sdpa_cache_append, sdpa_cache_check_status, sdpa_cache_evict,
                     sdpa_cache_evict_workspace_bytes, sdpa_cache_fwd, sdpa_cache_fwd_workspace_bytes,
                     sdpa_cache_read, sdpa_cache_test_hook, sdpa_cache_weigh)
+from .rope import (SdpaRopeParams, qk_rotate, qk_rotate_backward, sdpa_rope_bwd, sdpa_rope_bwd_workspace_bytes,
+                   sdpa_rope_fwd)
 
 SDPA_OK, SDPA_ERR_INVALID_ARG, SDPA_ERR_UNSUPPORTED, SDPA_ERR_CUDA = 0, 1, 2, 3
 SDPA_ERR_TIMEOUT, SDPA_ERR_BAD_LENGTHS, SDPA_ERR_WORKSPACE, SDPA_ERR_BOUNDS = 4, 5, 6, 7
@@ -38,7 +42,7 @@ ENTRY_POINTS = ("sdpa_bwd_workspace_bytes", "sdpa_bwd_preprocess", "sdpa_bwd",
                 "sdpa_bwd_last_error", "sdpa_bwd_params_bytes", "sdpa_bwd_tile_kv",
                 "sdpa_bwd_tile_q", "sdpa_bwd_no_alloc", "sdpa_bwd_kernel_launches",
                 "sdpa_fwd", "sdpa_fwd_check_status", "sdpa_fwd_params_bytes",
-                "sdpa_bwd_test_hook", "sdpa_bwd_no_alloc_check_status", *_cache.ENTRY_POINTS)
+                "sdpa_bwd_test_hook", "sdpa_bwd_no_alloc_check_status", *_cache.ENTRY_POINTS, *_rope.ENTRY_POINTS)
 
 _i64x3 = ctypes.c_int64 * 3
 
@@ -139,6 +143,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.sdpa_fwd_check_status.restype = st
         lib.sdpa_fwd_params_bytes.restype = sz
         _cache.bind(lib)
+        _rope.bind(lib)
         _lib = lib
         return lib
 
