@@ -21,10 +21,10 @@ LIB = os.path.join(BUILD, "libswa_sdpa_bwd.so")
 LIB_DBG = os.path.join(BUILD, "libswa_sdpa_bwd_dbg.so")
 DEBUG_BOUNDS = ("-DSDPA_DEBUG_BOUNDS",)
 SOURCES = ["api.cu", "aux_kernels.cu", "main_kernel.cu", "fwd_kernel.cu", "cache_api.cu", "cache_kernels.cu",
-           "cache_fwd.cu", "cache_tile.cu", "cache_weigh.cu", "cache4_kernels.cu", "cache4_fwd.cu",
+           "cache_fwd.cu", "cache_tile.cu", "cache_weigh.cu", "cache4_kernels.cu", "cache4_fwd.cu", "cache4_tile.cu",
            "rope_api.cu", "rope_kernels.cu"]
 HEADERS = ["ptx.cuh", "seq.cuh", "sdpa_internal.h", "api_util.h", "cache_internal.h", "cache.cuh",
-           "cache_fwd.cuh", "cache_append.cuh", "cache4.cuh", "rope_internal.h"]
+           "cache_fwd.cuh", "cache_append.cuh", "cache4.cuh", "cache_tile.cuh", "rope_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

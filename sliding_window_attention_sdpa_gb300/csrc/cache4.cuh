@@ -119,6 +119,72 @@ __device__ __forceinline__ void values4(uint32_t w, const Scale4& s, uint32_t (&
     r[3] = h2fma((b & 0x003c003cu) | 0x5c005c00u, s.s, s.n264);
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
+}
+
+// Lane (g, t)'s words of a group: K's of the keys kappa(g), kappa(g) + 2, or V's of the keys 4t, 4t + 1 and 4t + 2, 4t + 3.
+template <int HD>
+struct Words4 {
+    uint32_t w[2][HD / 32];
+};
+
+template <int HD>
+__device__ __forceinline__ Words4<HD> words4(uint32_t group, int lane)
+{
+    Words4<HD> r;
+    const uint4 x = lds128(group + lane * 16);
+    if constexpr (HD == 128) {
+        const uint4 y = lds128(group + 512 + lane * 16);
+        r.w[0][0] = x.x, r.w[0][1] = x.y, r.w[0][2] = x.z, r.w[0][3] = x.w;
+        r.w[1][0] = y.x, r.w[1][1] = y.y, r.w[1][2] = y.z, r.w[1][3] = y.w;
+    } else {
+        r.w[0][0] = x.x, r.w[0][1] = x.y;
+        r.w[1][0] = x.z, r.w[1][1] = x.w;
+    }
+    return r;
+}
+
+// Two 16-bit values of the I/O type as f16 (bf16: what f16 does not reach is taken as its largest number).
+template <bool BF16>
+__device__ __forceinline__ uint32_t to_f16x2(uint32_t x)
+{
+    if constexpr (!BF16) return x;
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(x & 0xffff0000u)), "f"(__uint_as_float(x << 16)));
+    return r;
+}
+
+// The power of two that a bf16 row is multiplied by on its way to f16, and the
+// one that brings its products back, from the bits of its largest magnitude: that comes to lie
+// between 2^14 and 2^15.
+struct QScale4 {
+    float mul, back;
+};
+
+__device__ __forceinline__ QScale4 q_scale4(uint32_t most)
+{
+    const int e = min(max(static_cast<int>(most >> 7) - 14, 1), 253);
+    return QScale4{__uint_as_float(static_cast<uint32_t>(254 - e) << 23), __uint_as_float(static_cast<uint32_t>(e) << 23)};
+}
+
 // The scale byte of a block whose largest magnitude is `most` (the bits of an
 // fp32; those of an infinity or a NaN are above every number's), and 1 / s (0
 // where the scale is 0: every code is 0 then).

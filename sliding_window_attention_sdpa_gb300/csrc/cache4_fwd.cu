@@ -55,63 +55,10 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr)
-{
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-    return v;
-}
-
-// Lane (g, t)'s words of a group: K's of the keys kappa(g), kappa(g) + 2, or V's of the keys 4t, 4t + 1 and 4t + 2, 4t + 3.
-template <int HD>
-struct Words4 {
-    uint32_t w[2][HD / 32];
-};
-
-template <int HD>
-__device__ __forceinline__ Words4<HD> words4(uint32_t group, int lane)
-{
-    Words4<HD> r;
-    const uint4 x = lds128(group + lane * 16);
-    if constexpr (HD == 128) {
-        const uint4 y = lds128(group + 512 + lane * 16);
-        r.w[0][0] = x.x, r.w[0][1] = x.y, r.w[0][2] = x.z, r.w[0][3] = x.w;
-        r.w[1][0] = y.x, r.w[1][1] = y.y, r.w[1][2] = y.z, r.w[1][3] = y.w;
-    } else {
-        r.w[0][0] = x.x, r.w[0][1] = x.y;
-        r.w[1][0] = x.z, r.w[1][1] = x.w;
-    }
-    return r;
-}
-
-// Two 16-bit values of the I/O type as f16 (bf16: what f16 does not reach is taken as its largest number).
-template <bool BF16>
-__device__ __forceinline__ uint32_t to_f16x2(uint32_t x)
-{
-    if constexpr (!BF16) return x;
-    uint32_t r;
-    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(x & 0xffff0000u)), "f"(__uint_as_float(x << 16)));
-    return r;
-}
-
 }  // namespace
 
 template <int HD, bool BF16, int NT>
-__global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __grid_constant__ Cache4FwdArgs qa)
+__global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __grid_constant__ CacheTileArgs qa)
 {
     const CacheFwdArgs& a = qa.f;
     using C = Rows4Cfg<HD>;
@@ -233,15 +180,14 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
                     for (int j = 0; j < 4; ++j) most = max(most, max(q[n][w][j] & 0x7fffu, (q[n][w][j] >> 16) & 0x7fffu));
                 most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
                 most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                const int e = min(max(static_cast<int>(most >> 7) - 14, 1), 253);
-                back = __uint_as_float(static_cast<uint32_t>(e) << 23);
-                const float mul = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+                const QScale4 scale = q_scale4(most);
+                back = scale.back;
 #pragma unroll
                 for (int w = 0; w < KW; ++w)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 f = unpack2<true>(q[n][w][j]);
-                        q[n][w][j] = pack2<false>(f.x * mul, f.y * mul);
+                        q[n][w][j] = pack2<false>(f.x * scale.mul, f.y * scale.mul);
                     }
             }
 #pragma unroll
@@ -345,7 +291,7 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
         // ---- cached keys: steps of GK per warp
         auto step_x = [&](int32_t s) -> int32_t { return (tile0 + s) * TK + warp * GK; };
         const int32_t cached = max(0, min(nt, (sv.new0 - step_x(0) + TK - 1) / TK));     // this warp's steps with cached keys
-        const int ck = qa.copy_keys, nu = GK / ck;                  // keys of a copy, copies of a step's K
+        const int ck = qa.box_rows, nu = GK / ck;                  // keys of a copy, copies of a step's K
         // the page of lane's copy (lane % nu), a step ahead
         auto fetch_entry = [&](int32_t s) -> int32_t {
             if (a.c.page_table == nullptr) return static_cast<int32_t>(bi);
@@ -637,7 +583,7 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
 namespace {
 
 template <int HD, bool BF16, int NT>
-cudaError_t launch_rows4(const Cache4FwdArgs& qa, cudaStream_t s)
+cudaError_t launch_rows4(const CacheTileArgs& qa, cudaStream_t s)
 {
     auto kern = cache4_fwd_rows_kernel<HD, BF16, NT>;
     const uint32_t bytes = Rows4Cfg<HD>::kBytes;
@@ -650,13 +596,14 @@ cudaError_t launch_rows4(const Cache4FwdArgs& qa, cudaStream_t s)
 }
 
 template <bool BF16>
-cudaError_t launch_fwd4(const Cache4FwdArgs& qa, cudaStream_t s)
+cudaError_t launch_fwd4(const CacheTileArgs& qa, cudaStream_t s)
 {
     switch (cache4_fwd_plan(qa.f.c.d, qa.f.s_q * qa.f.group).variant) {
         case kQ4Rows128x8: return launch_rows4<128, BF16, 1>(qa, s);
         case kQ4Rows128x16: return launch_rows4<128, BF16, 2>(qa, s);
         case kQ4Rows64x8: return launch_rows4<64, BF16, 1>(qa, s);
-        default: return launch_rows4<64, BF16, 2>(qa, s);
+        case kQ4Rows64x16: return launch_rows4<64, BF16, 2>(qa, s);
+        default: return launch_cache4_fwd_tiles(qa, BF16 ? SDPA_BF16 : SDPA_F16, s);
     }
 }
 
@@ -664,11 +611,12 @@ cudaError_t launch_fwd4(const Cache4FwdArgs& qa, cudaStream_t s)
 
 CacheFwdPlan cache4_fwd_plan(int64_t d, int64_t rows)
 {
+    if (rows > 16) return CacheFwdPlan{kQ4Tiles, 256, 64, 1, 8};
     if (d == 128) return rows <= 8 ? CacheFwdPlan{kQ4Rows128x8, 8, 256, 2, 1} : CacheFwdPlan{kQ4Rows128x16, 16, 256, 2, 1};
     return rows <= 8 ? CacheFwdPlan{kQ4Rows64x8, 8, 512, 2, 1} : CacheFwdPlan{kQ4Rows64x16, 16, 512, 2, 1};
 }
 
-cudaError_t launch_cache4_fwd(const Cache4FwdArgs& a, int dtype, cudaStream_t s)
+cudaError_t launch_cache4_fwd(const CacheTileArgs& a, int dtype, cudaStream_t s)
 {
     return dtype == SDPA_BF16 ? launch_fwd4<true>(a, s) : launch_fwd4<false>(a, s);
 }

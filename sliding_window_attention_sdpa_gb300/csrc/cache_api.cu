@@ -214,8 +214,8 @@ FwdSize fwd_size(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa:
     // the reach begins up to 15 keys before (63 in the tile kernel), the new tokens end up to 15 off a group of 16
     z.tiles = (keys + (plan.variant >= swa::kTiles128 ? 78 : 30) + ((p->s_q + 15) & ~int64_t(15)) + plan.tile - 1) / plan.tile;
     if (c->bits == 4) {
-        // the reach begins up to a warp's step - 1 before, ends as far behind, and the new tokens are a step
-        const int64_t gk = plan.tile / 4;
+        // the reach begins up to a step - 1 before (a warp's, or a tile), ends as far behind, and the new tokens are a step
+        const int64_t gk = plan.variant == swa::kQ4Tiles ? plan.tile : plan.tile / 4;
         z.tiles = (imin((keys + 2 * (gk - 1)), (room + gk - 1) / gk * gk) + gk + plan.tile - 1) / plan.tile;
     }
     z.units = double(c->b) * double(c->h_kv) * double(z.blocks);
@@ -410,11 +410,9 @@ sdpa_status_t sdpa_cache_fwd(const sdpa_cache* c, const sdpa_cache_fwd_params* p
     a.part_ml = at<float>(ws, l.part_ml);
     a.cuts = at<swa::CacheFwdCut>(ws, l.cuts);
     if (c->bits == 4) {
-        swa::Cache4FwdArgs qa{};
-        qa.f = a;
-        qa.copy_keys = plan.tile / 4;
-        while (c->page_size % qa.copy_keys != 0) qa.copy_keys >>= 1;
-        return cuda_status(swa::launch_cache4_fwd(qa, c->dtype, static_cast<cudaStream_t>(stream)), "cache forward launch");
+        ta.box_rows = plan.variant == swa::kQ4Tiles ? plan.tile : plan.tile / 4;
+        while (c->page_size % ta.box_rows != 0) ta.box_rows >>= 1;
+        return cuda_status(swa::launch_cache4_fwd(ta, c->dtype, static_cast<cudaStream_t>(stream)), "cache forward launch");
     }
     if (c->n_pages > 0) {
         // boxes that divide a page, of 8 rows at least: up to 64 (a key tile) for the tile kernel, 16 for the other; an unpaged

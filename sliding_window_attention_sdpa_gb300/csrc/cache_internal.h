@@ -46,7 +46,7 @@ struct CacheFwdPlan {
 CacheFwdPlan cache_fwd_plan(int64_t d, int64_t rows);
 
 // The same for a cache in 4 bits.
-enum Cache4FwdVariant { kQ4Rows128x8, kQ4Rows128x16, kQ4Rows64x8, kQ4Rows64x16 };
+enum Cache4FwdVariant { kQ4Rows128x8, kQ4Rows128x16, kQ4Rows64x8, kQ4Rows64x16, kQ4Tiles };
 CacheFwdPlan cache4_fwd_plan(int64_t d, int64_t rows);
 
 struct CacheFwdArgs {
@@ -73,16 +73,13 @@ struct CacheFwdArgs {
 
 // The tile and the rows kernel's: TMA descriptors of the pools' pages (4-D: d,
 // head, row, page) in boxes of 64 features x box_rows rows with the 128-byte
-// swizzle; box_rows 0: none, every row is gathered.
+// swizzle; box_rows 0: none, every row is gathered. Of a cache in 4 bits there are
+// no descriptors, and box_rows is the keys of a bulk copy: a power of two from 16
+// that divides a page, at most a warp's step.
 struct CacheTileArgs {
     CUtensorMap tm_k, tm_v;
     CacheFwdArgs f;
     int32_t box_rows;
-};
-
-struct Cache4FwdArgs {
-    CacheFwdArgs f;
-    int32_t copy_keys;      // keys of a copy: a power of two from 16 that divides a page, at most a warp's step
 };
 
 struct CacheAppendArgs {
@@ -146,7 +143,8 @@ cudaError_t launch_cache_fwd(const CacheTileArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_cache_fwd_tiles(const CacheTileArgs& a, int dtype, cudaStream_t s);
 // The join behind a forward kernel whose units have `rows` rows (8, 16 or 256).
 cudaError_t launch_cache_fwd_join(const CacheFwdArgs& a, int dtype, int rows, cudaStream_t s);
-cudaError_t launch_cache4_fwd(const Cache4FwdArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_cache4_fwd_tiles(const CacheTileArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_cache4_fwd(const CacheTileArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_cache4_append(const CacheAppendArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_cache_advance(const CacheAppendArgs& a, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheReadArgs& a, int dtype, cudaStream_t s);
