@@ -109,35 +109,23 @@ __device__ __forceinline__ Scale4 scale4(uint32_t w)
     return r;
 }
 
+// (x & M) | C as one instruction: it takes one of the two constants as such, the other in a register.
+template <uint32_t M, uint32_t C>
+__device__ __forceinline__ uint32_t and_or(uint32_t x)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(M), "n"(C));
+    return r;
+}
+
 // The 8 values of a word as 4 registers of two f16 (register j: code j of the low and of the high half).
 __device__ __forceinline__ void values4(uint32_t w, const Scale4& s, uint32_t (&r)[4])
 {
     const uint32_t b = __byte_perm(w, 0u, 0x2301);
-    r[0] = h2fma((w & 0x03c003c0u) | 0x4c004c00u, s.s, s.n24);
-    r[1] = h2fma((w & 0x003c003cu) | 0x5c005c00u, s.s, s.n264);
-    r[2] = h2fma((b & 0x03c003c0u) | 0x4c004c00u, s.s, s.n24);
-    r[3] = h2fma((b & 0x003c003cu) | 0x5c005c00u, s.s, s.n264);
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr)
-{
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-    return v;
+    r[0] = h2fma(and_or<0x03c003c0u, 0x4c004c00u>(w), s.s, s.n24);
+    r[1] = h2fma(and_or<0x003c003cu, 0x5c005c00u>(w), s.s, s.n264);
+    r[2] = h2fma(and_or<0x03c003c0u, 0x4c004c00u>(b), s.s, s.n24);
+    r[3] = h2fma(and_or<0x003c003cu, 0x5c005c00u>(b), s.s, s.n264);
 }
 
 // Lane (g, t)'s words of a group: K's of the keys kappa(g), kappa(g) + 2, or V's of the keys 4t, 4t + 1 and 4t + 2, 4t + 3.
@@ -147,12 +135,12 @@ struct Words4 {
 };
 
 template <int HD>
-__device__ __forceinline__ Words4<HD> words4(uint32_t group, int lane)
+__device__ __forceinline__ Words4<HD> words4(const uint8_t* group, int lane)
 {
     Words4<HD> r;
-    const uint4 x = lds128(group + lane * 16);
+    const uint4 x = *reinterpret_cast<const uint4*>(group + lane * 16);
     if constexpr (HD == 128) {
-        const uint4 y = lds128(group + 512 + lane * 16);
+        const uint4 y = *reinterpret_cast<const uint4*>(group + 512 + lane * 16);
         r.w[0][0] = x.x, r.w[0][1] = x.y, r.w[0][2] = x.z, r.w[0][3] = x.w;
         r.w[1][0] = y.x, r.w[1][1] = y.y, r.w[1][2] = y.z, r.w[1][3] = y.w;
     } else {
@@ -160,6 +148,20 @@ __device__ __forceinline__ Words4<HD> words4(uint32_t group, int lane)
         r.w[1][0] = x.z, r.w[1][1] = x.w;
     }
     return r;
+}
+
+// The scale bytes that go with them: K's of key kappa(g), then kappa(g) + 2 (d = 128: two blocks each), V's of keys 4t to 4t + 3.
+template <int HD>
+__device__ __forceinline__ uint32_t k_scales4(const uint8_t* group, int lane)
+{
+    if constexpr (HD == 128) return *reinterpret_cast<const uint32_t*>(group + Group4<HD>::kCodes + lane * 4);
+    else return *reinterpret_cast<const uint16_t*>(group + Group4<HD>::kCodes + lane * 2);
+}
+
+template <int HD>
+__device__ __forceinline__ uint32_t v_scales4(const uint8_t* group, int lane)
+{
+    return *reinterpret_cast<const uint32_t*>(group + Group4<HD>::kCodes + (HD == 128 ? lane >> 2 : lane >> 3) * 16 + (lane & 3) * 4);
 }
 
 // Two 16-bit values of the I/O type as f16 (bf16: what f16 does not reach is taken as its largest number).

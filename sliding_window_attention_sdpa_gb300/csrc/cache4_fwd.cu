@@ -26,16 +26,19 @@ namespace swa {
 
 namespace {
 
-constexpr int kThreads4 = 128;
-constexpr int kStages4 = 3;
+constexpr int kWarps4 = 4;                          // that compute; one more brings the keys
+constexpr int kThreads4 = 32 * (kWarps4 + 1);
+constexpr int kStep4 = 64, kGroups4 = kStep4 / 16;  // keys, groups of a warp's step
+constexpr int kTile4 = kWarps4 * kStep4;            // keys of a CTA's step
 
-template <int HD>
+template <int HD, int NT>
 struct Rows4Cfg {
-    static constexpr int GK = 8192 / HD, KG = GK / 16;          // keys, groups of a warp's step
-    static constexpr int TK = 4 * GK;
-    static constexpr uint32_t kHalf = KG * Group4<HD>::kBytes;  // a step's K
-    static constexpr uint32_t kStage = 2 * kHalf;
-    static constexpr uint32_t kBytes = 4 * kStages4 * kStage;
+    static constexpr int kOcc = 2;
+    static constexpr int kSub = HD == 128 && NT == 2 ? 2 : 4;            // groups whose scores are in registers together
+    static constexpr uint32_t kHalf = kGroups4 * Group4<HD>::kBytes;     // a warp's K of a step
+    static constexpr uint32_t kStage = 2 * kWarps4 * kHalf;              // the CTA's K, then its V
+    static constexpr int kStages = static_cast<int>(110 * 1024 / kStage);
+    static constexpr uint32_t kBytes = kStages * kStage;
 };
 
 __device__ __forceinline__ uint32_t movm_trans4(uint32_t x)
@@ -55,29 +58,42 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with a sum of 0 to begin with.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 }  // namespace
 
 template <int HD, bool BF16, int NT>
-__global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __grid_constant__ CacheTileArgs qa)
+__global__ void __launch_bounds__(kThreads4, Rows4Cfg<HD, NT>::kOcc) cache4_fwd_rows_kernel(const __grid_constant__ CacheTileArgs qa)
 {
     const CacheFwdArgs& a = qa.f;
-    using C = Rows4Cfg<HD>;
+    using C = Rows4Cfg<HD, NT>;
+    constexpr int ST = C::kStages;
     constexpr bool SPLIT = !BF16;
-    constexpr int GK = C::GK, KG = C::KG, TK = C::TK, OKW = GK / 32;
+    constexpr int GK = kStep4, KG = kGroups4, TK = kTile4, OKW = GK / 32;
     constexpr int KW = HD / 32;        // words of a lane, key and tensor
     constexpr int MT = HD / 16;        // feature tiles of O^T
     constexpr int ROWS = 8 * NT;
     constexpr int PAD = HD + 4;
     extern __shared__ __align__(128) uint8_t dyn[];
-    __shared__ __align__(8) uint64_t sh_bar[4][kStages4];
+    __shared__ __align__(8) uint64_t sh_full[ST], sh_empty[ST];
     float (*sh_o)[ROWS][PAD] = reinterpret_cast<float (*)[ROWS][PAD]>(dyn);     // at a unit's end
     static_assert(4 * ROWS * PAD * 4 <= C::kBytes, "the warps' O in the rings' place");
-    __shared__ uint32_t sh_ok[4][kStages4][OKW];       // per step of a ring: which keys count
+    __shared__ uint32_t sh_ok[ST][TK / 32];            // per stage: which keys count,
+    __shared__ uint32_t sh_all[ST];                    // and whether all of them do
     __shared__ float sh_m[4][ROWS], sh_l[4][ROWS];
     __shared__ uint64_t sh_mask[64];       // new tokens that each one's rows admit
     __shared__ int32_t sh_bits[64];        // and its mask's number of bits
     __shared__ uint32_t sh_used[2];        // new tokens that some row admits
-    __shared__ int64_t sh_sum[4], sh_at[2];
+    __shared__ int64_t sh_sum[kThreads4 / 32], sh_at[2];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -111,16 +127,117 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
         __syncthreads();
     }
 
-    if (tid < 4 * kStages4) mbar_init(smem_u32(&sh_bar[0][0]) + tid * 8, 1);
+    if (tid < ST) {
+        mbar_init(smem_u32(&sh_full[tid]), 1);
+        mbar_init(smem_u32(&sh_empty[tid]), kWarps4);
+    }
     fence_mbar_init();
     __syncthreads();
-    const uint32_t ring = smem_u32(dyn) + warp * (kStages4 * C::kStage), bars = smem_u32(&sh_bar[warp][0]);
-    uint32_t it = 0;          // steps of this warp's ring so far
+    const uint32_t full = smem_u32(&sh_full[0]), empty = smem_u32(&sh_empty[0]);
+    uint32_t stage = 0, par = 0;      // the ring's stage to fill or to read, and its phase
     bool good = true;         // no wait has run out
     int64_t cur = -1;
     for (;;) {
         const int64_t bi = sh_part.bi, rem = sh_part.rem;
         const SeqView sv = view(bi);
+        const Segment seg = segment_at(rem, sv.tiles, a.unit_cost, sh_count - sh_done);
+        const int64_t un = seg.un;
+        const int32_t tile0 = seg.tile0, nt = seg.n;
+        if (nt == 0) break;                                 // the part ends before the unit's first tile
+        const int64_t gk = blocks == 1 ? un : un / blocks;  // kv-head
+        const int r0 = static_cast<int>(un - gk * blocks) * ROWS;
+        const int64_t npos = a.c.next_pos ? a.c.next_pos[bi] : sv.len;
+        const int32_t* kpos = a.c.positions && a.window_left >= 0 ? a.c.positions + (bi * a.c.h_kv + gk) * a.c.cap : nullptr;
+
+        // a step is TK cached keys of the CTA, GK of each warp; the new tokens are the unit's last GK
+        const int32_t cached = max(0, min(nt, (sv.new0 - tile0 * TK + TK - 1) / TK));    // steps with cached keys
+        if (warp == kWarps4) {
+            // ---- brings the steps: bulk copies of as many keys as a page and a warp's step allow, lane u K's copy u, lane
+            // nu + u V's. Keys in front of every row's window are not fetched
+            int32_t low_min = INT32_MIN;
+            if (a.window_left >= 0) {
+                int32_t shallow = 64;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    int bits;
+                    if (admitted_tokens(a, bi, sv.nq, w * 32 + lane, bits)) shallow = min(shallow, bits);
+                }
+                low_min = static_cast<int32_t>(imax64(INT32_MIN, imin64(INT32_MAX,
+                    npos + static_cast<int32_t>(__reduce_min_sync(0xffffffffu, shallow)) - 1 - a.window_left)));
+            }
+            const int ck = qa.box_rows, nu = TK / ck;           // keys of a copy, copies of a step's K (16 at most)
+            const uint32_t bytes = ck / 16 * Group4<HD>::kBytes;
+            const bool is_v = lane >= nu;
+            const int mine = lane < 2 * nu ? lane % nu : 0;
+            const int64_t st_page = is_v ? a.c.v_stride[0] : a.c.k_stride[0];
+            const uint8_t* pool = reinterpret_cast<const uint8_t*>(is_v ? a.c.v : a.c.k) + gk * (is_v ? a.c.v_stride[2] : a.c.k_stride[2]);
+            const uint32_t dst = smem_u32(dyn) + (is_v ? C::kStage / 2 : 0u) + mine * bytes;
+            // the page of the lane's copy of a step
+            auto fetch_entry = [&](int32_t s) -> int32_t {
+                if (a.c.page_table == nullptr) return static_cast<int32_t>(bi);
+                const int32_t j = sv.lo + (tile0 + s) * TK + mine * ck;
+                return s < cached && j < sv.len ? cache_entry(a.c, bi, j) : 0;
+            };
+            // (the ring holds the last unit's O: its reads are done, and known to the copy engine)
+            fence_proxy_async_smem();
+            int32_t entry = fetch_entry(0);
+            int32_t sent = 0;
+#pragma unroll 1
+            for (; sent < cached && good; ++sent) {
+                const uint32_t bar = full + stage * 8;
+                const int32_t j0 = sv.lo + (tile0 + sent) * TK, j = j0 + mine * ck;
+                const bool paged = entry >= 0 && entry < a.c.n_pages;
+                bool go = lane < 2 * nu;
+                uint32_t copies = 2 * nu;
+                good = __all_sync(0xffffffffu, mbar_wait(empty + stage * 8, par ^ 1, a.timeout_ns));
+                if (!good) {
+                    set_status(a.c.status, SDPA_ERR_TIMEOUT);
+                    break;
+                }
+                // (every key of every copy is there and in reach, mostly)
+                const bool all = __all_sync(0xffffffffu, paged && j + ck <= sv.len && kpos == nullptr && j >= low_min);
+                if (!all) {
+                    uint32_t any = 0;
+#pragma unroll 1
+                    for (int w = 0; w < TK / 32; ++w) {
+                        const int32_t x = w * 32 + lane, jx = j0 + x;
+                        const bool there = __shfl_sync(0xffffffffu, paged ? 1 : 0, x / ck) != 0;
+                        bool in = jx < sv.len;
+                        if (in && a.window_left >= 0) in = (kpos ? kpos[jx] : jx) >= low_min;
+                        if (in && !there) set_status(a.c.status, SDPA_ERR_BOUNDS);
+                        const uint32_t oks = __ballot_sync(0xffffffffu, in && there);
+                        if (lane == 0) sh_ok[stage][w] = oks;
+                        const int first = mine * ck - w * 32;                // the copy's keys in this word
+                        if (ck >= 32 ? first <= 0 && first + ck > 0 : first >= 0 && first < 32)
+                            any |= ck >= 32 ? oks : (oks >> first) & 0xffffu;
+                    }
+                    go = go && any != 0;
+                    copies = __popc(__ballot_sync(0xffffffffu, go));
+                }
+                if (lane == 0) {
+                    sh_all[stage] = all;
+                    mbar_arrive_expect_tx(bar, copies * bytes);
+                }
+                __syncwarp();
+                if (go && !(a.c.stall && sent == 1)) {       // (test hook: a step that never comes)
+                    const uint32_t row = a.c.page_table == nullptr ? j : cache_row(a.c, j);
+                    bulk_load(dst + stage * C::kStage, pool + entry * st_page + static_cast<int64_t>(row >> 4) * Group4<HD>::kBytes, bytes,
+                              bar);
+                }
+                entry = fetch_entry(sent + 1);
+                if (++stage == ST) stage = 0, par ^= 1;
+            }
+            if (lane == 0 && !a.whole)
+                name_cut(a, sh_part, sh_done == 0, sh_part.at + sh_done + seg.line_n - tile0 - nt, a.unit_cost, bi, un, units, tile0,
+                         nt, sv.tiles);
+            // what is on its way ends before the unit does, whatever wait has run out
+            uint32_t q = stage, ph = par;
+            for (int32_t r = 0; r < ST && r < sent; ++r) {
+                if (q-- == 0) q = ST - 1, ph ^= 1;
+                if (!mbar_wait(full + q * 8, ph, a.timeout_ns)) good = false;
+            }
+            good = __all_sync(0xffffffffu, good);
+        } else {
         if (cur != bi) {
             if (tid < 64) {
                 int bits;
@@ -128,7 +245,7 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
                 sh_bits[tid] = bits;
             }
             if (tid < 2) sh_used[tid] = 0;
-            __syncthreads();
+            named_sync(1, 32 * kWarps4);
             if (warp < 2) {
                 const uint64_t m = sh_mask[tid];
                 const uint32_t lo32 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m));
@@ -138,27 +255,34 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
                     atomicOr(&sh_used[1], hi32);
                 }
             }
-            __syncthreads();
+            named_sync(1, 32 * kWarps4);
             cur = bi;
         }
-        const Segment seg = segment_at(rem, sv.tiles, a.unit_cost, sh_count - sh_done);
-        const int64_t un = seg.un;
-        const int32_t tile0 = seg.tile0, nt = seg.n;
-        if (nt == 0) break;                                 // the part ends before the unit's first tile
-        const int64_t gk = un / blocks;                     // kv-head
-        const int r0 = static_cast<int>(un - gk * blocks) * ROWS;
-        if (tid == 0 && !a.whole)
-            name_cut(a, sh_part, sh_done == 0, sh_part.at + sh_done + seg.line_n - tile0 - nt, a.unit_cost, bi, un, units, tile0,
-                     nt, sv.tiles);
-        const int64_t npos = a.c.next_pos ? a.c.next_pos[bi] : sv.len;
-        const int32_t* kpos = a.c.positions && a.window_left >= 0 ? a.c.positions + (bi * a.c.h_kv + gk) * a.c.cap : nullptr;
-
-        // ---- rows: Q in f16 (row g of each 8), masks, windows and factors (rows 2t, 2t + 1)
-        uint32_t q[NT][KW][4];
-        float row_scale[NT][2];       // the row's scores to powers of two
+        auto step_x = [&](int32_t s) -> int32_t { return (tile0 + s) * TK + warp * GK; };
+        // ---- rows: masks and windows (rows 2t, 2t + 1)
         int row_tok[NT][2];           // the row's token, -1: admits nothing
         int32_t row_low[NT][2];       // lowest position in the row's window
-        int32_t low_max = INT32_MIN, low_min = INT32_MAX;  // the highest and the lowest of them (this CTA's rows)
+        int32_t low_max = INT32_MIN;  // the highest of them (this CTA's rows)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int rr = r0 + n * 8 + 2 * t + e;
+                const int tk = rr < R ? rr / a.group : 0;
+                const uint64_t m = rr < R ? sh_mask[tk] : 0;
+                row_tok[n][e] = m ? tk : -1;
+                row_low[n][e] = INT32_MIN;
+                if (a.window_left >= 0)
+                    row_low[n][e] = static_cast<int32_t>(
+                        imax64(INT32_MIN, imin64(INT32_MAX, npos + sh_bits[tk] - 1 - a.window_left)));
+                if (m) low_max = max(low_max, row_low[n][e]);
+            }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) low_max = max(low_max, __shfl_xor_sync(0xffffffffu, low_max, o));
+
+        // ---- Q in f16 (row g of each 8) and its factors (rows 2t, 2t + 1), while the first keys are on their way
+        uint32_t q[NT][KW][4];
+        float row_scale[NT][2];       // the row's scores to powers of two
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = r0 + n * 8 + g;
@@ -194,24 +318,7 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
             for (int e = 0; e < 2; ++e) {
                 // (not 0: masked scores are -inf)
                 row_scale[n][e] = fmaxf(a.scale_log2 * __shfl_sync(0xffffffffu, back, (2 * t + e) * 4), 1e-38f);
-                const int rr = r0 + n * 8 + 2 * t + e;
-                const int tk = rr < R ? rr / a.group : 0;
-                const uint64_t m = rr < R ? sh_mask[tk] : 0;
-                row_tok[n][e] = m ? tk : -1;
-                row_low[n][e] = INT32_MIN;
-                if (a.window_left >= 0)
-                    row_low[n][e] = static_cast<int32_t>(
-                        imax64(INT32_MIN, imin64(INT32_MAX, npos + sh_bits[tk] - 1 - a.window_left)));
-                if (m) {
-                    low_max = max(low_max, row_low[n][e]);
-                    low_min = min(low_min, row_low[n][e]);
-                }
             }
-        }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            low_max = max(low_max, __shfl_xor_sync(0xffffffffu, low_max, o));
-            low_min = min(low_min, __shfl_xor_sync(0xffffffffu, low_min, o));
         }
 
         float o[NT][MT][4];
@@ -288,112 +395,41 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
                 }
         };
 
-        // ---- cached keys: steps of GK per warp
-        auto step_x = [&](int32_t s) -> int32_t { return (tile0 + s) * TK + warp * GK; };
-        const int32_t cached = max(0, min(nt, (sv.new0 - step_x(0) + TK - 1) / TK));     // this warp's steps with cached keys
-        const int ck = qa.box_rows, nu = GK / ck;                  // keys of a copy, copies of a step's K
-        // the page of lane's copy (lane % nu), a step ahead
-        auto fetch_entry = [&](int32_t s) -> int32_t {
-            if (a.c.page_table == nullptr) return static_cast<int32_t>(bi);
-            const int32_t j = sv.lo + step_x(s) + (lane % nu) * ck;
-            return s < cached && j < sv.len ? cache_entry(a.c, bi, j) : 0;
-        };
-        auto issue = [&](int32_t s, int32_t entry) {
-            const uint32_t st = (it + s) % kStages4, at = ring + st * C::kStage, bar = bars + st * 8;
-            const int32_t x0 = step_x(s), j0 = sv.lo + x0;
-            const bool paged = entry >= 0 && entry < a.c.n_pages;
-            uint32_t oks[OKW];
-#pragma unroll
-            for (int w = 0; w < OKW; ++w) {
-                const int32_t x = w * 32 + lane, j = j0 + x;
-                const bool there = __shfl_sync(0xffffffffu, paged ? 1 : 0, x / ck) != 0;
-                bool ok = j < sv.len;
-                if (ok && a.window_left >= 0) ok = (kpos ? kpos[j] : j) >= low_min;
-                if (ok && !there) set_status(a.c.status, SDPA_ERR_BOUNDS);
-                oks[w] = __ballot_sync(0xffffffffu, ok && there);
-            }
-            // lane u brings K's copy u, lane nu + u V's
-            const int u = lane % nu;
-            uint32_t mine = 0;
-#pragma unroll
-            for (int w = 0; w < OKW; ++w) {
-                const int first = u * ck - w * 32;                   // the copy's keys in this word
-                if (ck >= 32 ? first <= 0 && first + ck > 0 : first >= 0 && first < 32)
-                    mine |= ck >= 32 ? oks[w] : (oks[w] >> first) & 0xffffu;
-            }
-            const bool go = lane < 2 * nu && mine != 0;
-            const uint32_t bytes = ck / 16 * Group4<HD>::kBytes;
-            const uint32_t copies = __popc(__ballot_sync(0xffffffffu, go));
-            if (lane == 0) {
-#pragma unroll
-                for (int w = 0; w < OKW; ++w) sh_ok[warp][st][w] = oks[w];
-                mbar_arrive_expect_tx(bar, copies * bytes);
-            }
-            __syncwarp();
-            if (go) {
-                const bool is_v = lane >= nu;
-                const int32_t j = j0 + u * ck;
-                const uint32_t row = a.c.page_table == nullptr ? j : cache_row(a.c, j);
-                const int64_t* sd = is_v ? a.c.v_stride : a.c.k_stride;
-                const uint8_t* src = reinterpret_cast<const uint8_t*>(is_v ? a.c.v : a.c.k) + entry * sd[0] + gk * sd[2] +
-                                     static_cast<int64_t>(row >> 4) * Group4<HD>::kBytes;
-                bulk_load(at + (is_v ? C::kHalf : 0u) + u * bytes, src, bytes, bar);
-            }
-        };
-
-        // (rings hold the last unit's O: its reads are done, and known to the copy engine)
-        fence_proxy_async_smem();
-        __syncwarp();
-        int32_t entry = fetch_entry(0);
-#pragma unroll
-        for (int s = 0; s < kStages4 - 1; ++s) {
-            const int32_t next = fetch_entry(s + 1);
-            if (good && s < cached && !(a.c.stall && s == 1)) issue(s, entry);      // (test hook: a step that never comes)
-            entry = next;
-        }
 #pragma unroll 1
         for (int32_t s = 0; s < cached; ++s) {
-            {
-                const int32_t next = fetch_entry(s + kStages4);
-                if (good && s + kStages4 - 1 < cached) issue(s + kStages4 - 1, entry);
-                entry = next;
-            }
-            const uint32_t st = (it + s) % kStages4, at = ring + st * C::kStage;
+            const uint32_t st = stage;
+            const uint8_t* step = dyn + st * C::kStage + warp * C::kHalf;
             if (good) {
-                good = __all_sync(0xffffffffu, mbar_wait(bars + st * 8, ((it + s) / kStages4) & 1, a.timeout_ns));
-                if (!good) {
-                    // nothing more is sent; what is on its way ends before the CTA does
-                    set_status(a.c.status, SDPA_ERR_TIMEOUT);
-                    for (int32_t r = s; r < cached && r < s + kStages4; ++r)
-                        mbar_wait(bars + ((it + r) % kStages4) * 8, ((it + r) / kStages4) & 1, a.timeout_ns);
-                    __syncwarp();
-                }
+                good = __all_sync(0xffffffffu, mbar_wait(full + st * 8, par, a.timeout_ns));
+                if (!good) set_status(a.c.status, SDPA_ERR_TIMEOUT);
             }
+            if (++stage == ST) stage = 0, par ^= 1;
             if (!good) continue;
             const int32_t x0 = step_x(s);
+            const bool all = sh_all[st] != 0;
             uint32_t ok[OKW];
-            bool full = true;
 #pragma unroll
-            for (int w = 0; w < OKW; ++w) {
-                ok[w] = sh_ok[warp][st][w];
-                full = full && ok[w] == 0xffffffffu;
-            }
+            for (int w = 0; w < OKW; ++w) ok[w] = all ? 0xffffffffu : sh_ok[st][warp * OKW + w];
+            if (all || (ok[0] | ok[1]) != 0) {
+            constexpr int KS = C::kSub;
+            auto okw = [&](int u) -> uint32_t { return u < 2 ? ok[0] : ok[1]; };
+            static_assert(OKW == 2, "");
+#pragma unroll 1
+            for (int u0 = 0; u0 < KG; u0 += KS) {
             // S^T
-            float sc[NT][KG][4];
+            float sc[NT][KS][4];
 #pragma unroll
-            for (int u = 0; u < KG; ++u) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) sc[n][u][0] = sc[n][u][1] = sc[n][u][2] = sc[n][u][3] = 0.f;
-                const uint32_t grp = at + u * Group4<HD>::kBytes;
+            for (int u = 0; u < KS; ++u) {
+                const uint8_t* grp = step + (u0 + u) * Group4<HD>::kBytes;
                 const Words4<HD> kw = words4<HD>(grp, lane);
+                const uint32_t x = k_scales4<HD>(grp, lane);
                 Scale4 ks[2][HD / 64];
+                ks[0][0] = scale4<0x0404>(x);
                 if constexpr (HD == 128) {
-                    const uint32_t x = lds32(grp + Group4<HD>::kCodes + lane * 4);
-                    ks[0][0] = scale4<0x0404>(x), ks[0][1] = scale4<0x1414>(x);
+                    ks[0][1] = scale4<0x1414>(x);
                     ks[1][0] = scale4<0x2424>(x), ks[1][1] = scale4<0x3434>(x);
                 } else {
-                    const uint32_t x = lds_u16(grp + Group4<HD>::kCodes + lane * 2);
-                    ks[0][0] = scale4<0x0404>(x), ks[1][0] = scale4<0x1414>(x);
+                    ks[1][0] = scale4<0x1414>(x);
                 }
 #pragma unroll
                 for (int w = 0; w < KW; ++w) {
@@ -402,7 +438,8 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
                     values4(kw.w[1][w], ks[1][w / 2], k1);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        mma_f16(sc[n][u], k0[0], k1[0], k0[1], k1[1], q[n][w][0], q[n][w][1]);
+                        if (w == 0) mma_f16_first(sc[n][u], k0[0], k1[0], k0[1], k1[1], q[n][w][0], q[n][w][1]);
+                        else mma_f16(sc[n][u], k0[0], k1[0], k0[1], k1[1], q[n][w][0], q[n][w][1]);
                         mma_f16(sc[n][u], k0[2], k1[2], k0[3], k1[3], q[n][w][2], q[n][w][3]);
                     }
                 }
@@ -410,13 +447,13 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
             // masks (a step whose keys are all there and in every row's window needs none; rows that admit nothing
             // are left out at the end)
             const bool windowed = a.window_left >= 0 && (kpos != nullptr || sv.lo + x0 < low_max);
-            if (!full || windowed) {
+            if (!all || windowed) {
 #pragma unroll
-                for (int u = 0; u < KG; ++u)
+                for (int u = 0; u < KS; ++u)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int x = u * 16 + kappa + 2 * h, j = sv.lo + x0 + x;
-                        const bool in = (ok[u / 2] >> (x & 31)) & 1;
+                        const int x = (u0 + u) * 16 + kappa + 2 * h, j = sv.lo + x0 + x;
+                        const bool in = (okw(u0 + u) >> (x & 31)) & 1;
                         const int32_t pos = in && kpos ? kpos[j] : j;
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
@@ -425,16 +462,16 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
                                 if (!in || (windowed && pos < row_low[n][e])) sc[n][u][2 * h + e] = -INFINITY;
                     }
             }
-            uint32_t hi[NT][KG][2], lo[NT][KG][2];
+            uint32_t hi[NT][KS][2], lo[NT][KS][2];
             softmax(sc, hi, lo);
             // O^T += V^T P^T
 #pragma unroll
-            for (int u = 0; u < KG; ++u) {
-                const uint32_t grp = at + C::kHalf + u * Group4<HD>::kBytes;
+            for (int u = 0; u < KS; ++u) {
+                const uint8_t* grp = step + C::kStage / 2 + (u0 + u) * Group4<HD>::kBytes;
                 const Words4<HD> vw = words4<HD>(grp, lane);
-                uint32_t x = lds32(grp + Group4<HD>::kCodes + (HD == 128 ? g : g >> 1) * 16 + t * 4);
+                uint32_t x = v_scales4<HD>(grp, lane);
                 // what stands in the place of a key that does not count meets a P of 0: its scale has to be 0
-                if (!full) x &= (((ok[u / 2] >> ((u & 1) * 16 + 4 * t)) & 15) * 0x00204081u & 0x01010101u) * 255u;
+                if (!all) x &= (((okw(u0 + u) >> (((u0 + u) & 1) * 16 + 4 * t)) & 15) * 0x00204081u & 0x01010101u) * 255u;
                 const Scale4 v0 = scale4<0x1404>(x), v1 = scale4<0x3424>(x);
 #pragma unroll
                 for (int w = 0; w < KW; ++w) {
@@ -451,12 +488,18 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
                         }
                 }
             }
+            }
+            }
+            // the stage is free when all four warps are done with it
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + st * 8);
         }
-        it += cached;
 
         // ---- the new tokens, 16 at a time, by the warp whose step they are; of those that no row admits (they may hold
         // anything) nothing is read
-        if (cached < nt && step_x(cached) == sv.new0) {
+        // (they begin with a warp's step, perhaps in a CTA's step that has cached keys as well)
+        const int32_t sn = (sv.new0 / GK - tile0 * kWarps4 - warp) / kWarps4;
+        if (sv.new0 >= step_x(0) && sn < nt && step_x(sn) == sv.new0) {
             const uint16_t* kn = a.k + bi * a.k_stride[0] + gk * a.k_stride[2] + t * (HD / 4);
             const uint16_t* vn = a.v + bi * a.v_stride[0] + gk * a.v_stride[2] + g * (HD / 8);
 #pragma unroll 1
@@ -514,7 +557,7 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
         }
 
         // ---- the CTA's warps join their rows
-        __syncthreads();
+        named_sync(1, 32 * kWarps4);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -535,6 +578,7 @@ __global__ void __launch_bounds__(kThreads4, 2) cache4_fwd_rows_kernel(const __g
                     dst[2 * p + 1] = live ? o[n][p][2 + e] : 0.f;
                 }
             }
+        }
         __syncthreads();
         const bool whole = nt == sv.tiles;
         const int64_t slot = blockIdx.x * 2 + (sh_done == 0 ? 0 : 1);
@@ -586,7 +630,7 @@ template <int HD, bool BF16, int NT>
 cudaError_t launch_rows4(const CacheTileArgs& qa, cudaStream_t s)
 {
     auto kern = cache4_fwd_rows_kernel<HD, BF16, NT>;
-    const uint32_t bytes = Rows4Cfg<HD>::kBytes;
+    const uint32_t bytes = Rows4Cfg<HD, NT>::kBytes;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(kern, bytes, allowed);
     if (e != cudaSuccess) return e;
@@ -612,8 +656,8 @@ cudaError_t launch_fwd4(const CacheTileArgs& qa, cudaStream_t s)
 CacheFwdPlan cache4_fwd_plan(int64_t d, int64_t rows)
 {
     if (rows > 16) return CacheFwdPlan{kQ4Tiles, 256, 64, 1, 8};
-    if (d == 128) return rows <= 8 ? CacheFwdPlan{kQ4Rows128x8, 8, 256, 2, 1} : CacheFwdPlan{kQ4Rows128x16, 16, 256, 2, 1};
-    return rows <= 8 ? CacheFwdPlan{kQ4Rows64x8, 8, 512, 2, 1} : CacheFwdPlan{kQ4Rows64x16, 16, 512, 2, 1};
+    if (d == 128) return rows <= 8 ? CacheFwdPlan{kQ4Rows128x8, 8, kTile4, 2, 3} : CacheFwdPlan{kQ4Rows128x16, 16, kTile4, 2, 3};
+    return rows <= 8 ? CacheFwdPlan{kQ4Rows64x8, 8, kTile4, 2, 3} : CacheFwdPlan{kQ4Rows64x16, 16, kTile4, 2, 3};
 }
 
 cudaError_t launch_cache4_fwd(const CacheTileArgs& a, int dtype, cudaStream_t s)

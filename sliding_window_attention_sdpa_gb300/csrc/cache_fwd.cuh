@@ -231,12 +231,20 @@ __device__ __forceinline__ uint64_t admitted_tokens(const CacheFwdArgs& a, int64
 // warps take as many).
 constexpr int kPartialRows = 4;
 
+// x / y of numbers that are not negative; in 32 bits where they fit (a division in 64 bits is a routine of some 100 cycles,
+// and a kernel's start has several in a row).
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y)
+{
+    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
+}
+
 // The line of tiles: all sequences' units, cut evenly between the parts.
 struct Line {
     int64_t total;
-    __device__ __forceinline__ int64_t start(int64_t c, int64_t parts) const { return c * total / parts; }
+    __device__ __forceinline__ int64_t start(int64_t c, int64_t parts) const { return quotient(c * total, parts); }
     // the part that holds tile t
-    __device__ __forceinline__ int64_t part_of(int64_t t, int64_t parts) const { return ((t + 1) * parts - 1) / total; }
+    __device__ __forceinline__ int64_t part_of(int64_t t, int64_t parts) const { return quotient((t + 1) * parts - 1, total); }
 };
 
 __device__ __forceinline__ int64_t warp_sum64(int64_t x)
@@ -276,8 +284,9 @@ __device__ __forceinline__ Part find_part(int64_t b, F tiles_of, int64_t* sh, in
     constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Part p{};
-    int64_t s = 0;
-    for (int64_t i = tid; i < b; i += THREADS) s += tiles_of(i);
+    const int64_t mine = tid < b ? tiles_of(tid) : 0;      // (of the first THREADS sequences, for both passes)
+    int64_t s = mine;
+    for (int64_t i = tid + THREADS; i < b; i += THREADS) s += tiles_of(i);
     p.line.total = block_sum64<THREADS>(s, sh);
     p.parts = imin64(gridDim.x, p.line.total);
     if (blockIdx.x >= p.parts) return p;
@@ -286,7 +295,7 @@ __device__ __forceinline__ Part find_part(int64_t b, F tiles_of, int64_t* sh, in
     int64_t before = 0;
     for (int64_t base = 0; base < b; base += THREADS) {
         const int64_t i = base + tid;
-        const int64_t n = i < b ? tiles_of(i) : 0;
+        const int64_t n = base == 0 ? mine : i < b ? tiles_of(i) : 0;
         int64_t incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -323,7 +332,7 @@ struct Segment {
 __device__ __forceinline__ Segment segment_at(int64_t rem, int32_t tiles, int32_t cost, int64_t left)
 {
     Segment g;
-    g.un = rem / (tiles + cost);
+    g.un = quotient(rem, tiles + cost);
     const int32_t y = static_cast<int32_t>(rem - g.un * (tiles + cost));
     g.tile0 = max(0, y - cost);
     g.line_n = static_cast<int32_t>(imin64(tiles + cost - y, left));

@@ -317,7 +317,7 @@ __device__ __forceinline__ void tile_convert4(const CacheTileArgs& ta, Walk<true
     volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(sm + C::kMisc) + 1;
     const int full0 = is_v ? tVFull : tKFull, empty0 = is_v ? tVEmpty : tKEmpty;
     const int raw_full0 = is_v ? tRawVFull : tRawKFull, raw_empty0 = is_v ? tRawVEmpty : tRawKEmpty;
-    const uint32_t ring0 = is_v ? C::kV : C::kK, raw0 = sbase + C::kRaw + (is_v ? kRawStages * C::kRaw1 : 0) + p * (C::kRaw1 / 2);
+    const uint32_t ring0 = is_v ? C::kV : C::kK, raw0 = C::kRaw + (is_v ? kRawStages * C::kRaw1 : 0) + p * (C::kRaw1 / 2);
     const uint32_t* const oks0 = reinterpret_cast<const uint32_t*>(sm + C::kRawOk) + (is_v ? kRawStages * 2 : 0) + p;
     const int lg = lane >> 2, lt = lane & 3;
     uint32_t it = 0, got = 0;                                   // tiles so far, those of cached keys
@@ -357,18 +357,17 @@ __device__ __forceinline__ void tile_convert4(const CacheTileArgs& ta, Walk<true
                 }
             }
             if (!fresh) {
-                const uint32_t raw = raw0 + rs * C::kRaw1;
+                const uint8_t* raw = sm + raw0 + rs * C::kRaw1;
                 uint32_t w[2][2][KW], sc[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const uint32_t grp = raw + q * Group4<HD>::kBytes;
+                    const uint8_t* grp = raw + q * Group4<HD>::kBytes;
                     const Words4<HD> x = words4<HD>(grp, lane);
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
                         for (int k = 0; k < KW; ++k) w[q][hh][k] = x.w[hh][k];
-                    const uint32_t at = grp + Group4<HD>::kCodes;
-                    sc[q] = is_v ? lds32(at + (HD == 128 ? lg : lg >> 1) * 16 + lt * 4) : HD == 128 ? lds32(at + lane * 4) : lds_u16(at + lane * 2);
+                    sc[q] = is_v ? v_scales4<HD>(grp, lane) : k_scales4<HD>(grp, lane);
                 }
                 if (!is_v) {
                     // rows of keys: the lane has a quarter of the features of two keys of each group. Lanes two quarters
