@@ -72,12 +72,6 @@ __device__ __forceinline__ uint32_t v4_scale(uint32_t x, uint32_t f16)
     return Group4<HD>::kCodes + f16 * 16 + x;
 }
 
-// Four codes (c + 8, 0 to 15) as the 16 bits of a half word, and back.
-__device__ __forceinline__ uint32_t pack_half4(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3)
-{
-    return c0 << 6 | c1 << 2 | c3 << 10 | (c2 & 3) << 14 | c2 >> 2;
-}
-
 __device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c)
 {
     uint32_t r;
@@ -187,39 +181,64 @@ __device__ __forceinline__ QScale4 q_scale4(uint32_t most)
     return QScale4{__uint_as_float(static_cast<uint32_t>(254 - e) << 23), __uint_as_float(static_cast<uint32_t>(e) << 23)};
 }
 
-// The scale byte of a block whose largest magnitude is `most` (the bits of an
-// fp32; those of an infinity or a NaN are above every number's), and 1 / s (0
-// where the scale is 0: every code is 0 then).
-// The border between two scales, 7 times a number of 5 bits, and the inputs' 11
-// bits are on one grid: most / 7 is at least 2^-11 of itself away from a border
-// that it is not on, so that the fp32 quotient's rounding decides as the
-// exact one would; a quotient that is a border is exact.
-__device__ __forceinline__ uint32_t scale_byte4(uint32_t most_bits, float& inv)
+// The 8 values of a word as bf16 pairs, exactly: 16 + c + 8 in bf16 has the code at bits 3-6. s: the two scales in bf16.
+__device__ __forceinline__ void values4_bf16(uint32_t w, uint32_t s, uint32_t n24, uint32_t (&r)[4])
 {
-    if (most_bits >= 0x7f800000u) {
-        inv = 0.f;
-        return kNanScale4;
-    }
-    const float v = fminf(__fdiv_rn(__uint_as_float(most_bits), 7.f), kMaxScale4);
-    // adding and taking away 2^20 times v's power of two, whose unit in the last place is an eighth of that power,
-    // rounds to the scales' grid (below 2^-14 it is that of 2^-14), ties to even
-    const uint32_t e = max(__float_as_uint(v) >> 23, 113u);
-    const float big = __uint_as_float((e + 20) << 23);
-    const float s = __fsub_rn(__fadd_rn(v, big), big);
-    inv = s > 0.f ? __frcp_rn(s) : 0.f;
-    return __half_as_ushort(__float2half_rn(s)) >> 7;
+    const uint32_t b = __byte_perm(w, 0u, 0x2301);
+    auto fma = [&](uint32_t x) -> uint32_t {
+        uint32_t y;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(and_or<0x00780078u, 0x41804180u>(x)), "r"(s), "r"(n24));
+        return y;
+    };
+    r[0] = fma(w >> 3);
+    r[1] = fma(w << 1);
+    r[2] = fma(b >> 3);
+    r[3] = fma(b << 1);
 }
 
-// rint(x / s), -8 to 7, + 8. A border (k + 1/2) s, 8 bits, is on the grid of x: x / s
-// is at least 2^-12 away from a border that it is not on, and x * inv within 2^-23 of itself;
-// rounding the product to multiples of 2^-14 puts what is on a border there, and then
-// ties go to even.
-__device__ __forceinline__ uint32_t code4(float x, float inv)
+// The scale byte of a block whose largest magnitude is `most` (the bits of an fp32; those of an infinity or a NaN are
+// above every number's), and 1 / s to within 2^-22 (0 where the scale is 0 or NaN: every code is 0 or of no account).
+// The border between two scales, 7 times a number of 5 bits, and the inputs' 11 bits are on one grid: most / 7 is at
+// least 2^-11 of itself away from a border that it is not on, and the product with 1 / 7 within 2^-23 of it. So the
+// product is first rounded to 2^-12 of its power of two, which puts what is on a border there, then to 2^-3 (ties to
+// even). Rounding is done by adding a power of two whose unit in the last place is the grid's.
+// `wide`: codes may pass 7: the scale ends at 240, and is coarse below 2^-14.
+__device__ __forceinline__ uint32_t scale_byte4(uint32_t most, float& inv, bool& wide)
 {
-    constexpr float kGrid = 512.f + 256.f;      // its unit in the last place: 2^-14
-    const float y = fminf(fmaxf(__fmul_rn(x, inv), -16.f), 16.f);
-    const float z = __fsub_rn(__fadd_rn(y, kGrid), kGrid);
-    return static_cast<uint32_t>(min(max(__float2int_rn(z), -8), 7) + 8);
+    const float v = fminf(__fmul_rn(__uint_as_float(most), 0.14285714924335479736f), kMaxScale4);
+    const uint32_t e = max(__float_as_uint(v) >> 23, 113u);     // (below 2^-14: the step of 2^-14)
+    const float fine = __uint_as_float((e + 11) << 23), coarse = __uint_as_float((e + 20) << 23);
+    const float s = __fsub_rn(__fadd_rn(__fadd_rn(v, fine), __fsub_rn(coarse, fine)), coarse);
+    wide = v >= kMaxScale4 || e == 113u;
+    const bool bad = most >= 0x7f800000u;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    inv = s > 0.f && !bad ? r : 0.f;
+    return bad ? kNanScale4 : static_cast<uint32_t>(__half_as_ushort(__float2half_rn(s))) >> 7;
+}
+
+// rint(x / s) + 8 in the low 4 bits of each of two numbers, -8 to 7 where it is in that range; the bits below 16 above
+// them are 0. A border (k + 1/2) s, 8 bits, is on the grid of x: x / s is at least 2^-12 away from a border that it is not
+// on, and x * inv within 2^-19 of itself; rounding the product to multiples of 2^-14 puts what is on a border there, and
+// then ties go to even.
+__device__ __forceinline__ uint64_t code4_2(uint64_t x, uint64_t inv)
+{
+    // 768: unit in the last place 2^-14; 2^23 + 2^22 + 8: units, the code in the lowest bits
+    constexpr uint64_t kFine = 0x4440000044400000ull;
+    constexpr uint32_t kOnes = 0x4b400000u + 8 - 768;           // bits of 12582920 - 768
+    uint64_t y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(x), "l"(inv));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(y) : "l"(kFine));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(y) : "l"((static_cast<uint64_t>(kOnes) << 32) | kOnes));
+    return y;
+}
+
+// Four codes each (low 4 bits; the other bits below 16 are 0) as a word's low and high half.
+__device__ __forceinline__ uint32_t pack_word4(const uint32_t (&lo)[4], const uint32_t (&hi)[4])
+{
+    const uint32_t a = __byte_perm(lo[0] * 16 + lo[1], hi[0] * 16 + hi[1], 0x5410) << 2;
+    const uint32_t b = __byte_perm(lo[2] * 16 + lo[3], hi[2] * 16 + hi[3], 0x5410) << 2;
+    return a | __byte_perm(b, 0u, 0x2301);
 }
 
 }  // namespace swa

@@ -7,32 +7,47 @@ namespace swa {
 
 namespace {
 
-// The 8 features of a 16-byte piece as fp32.
+// 8 features of a block of 16 whose other half the neighbouring lane (^ 1) has, as codes c + 8 (see code4_2); the
+// block's scale byte.
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& x, float (&f)[8])
+__device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t (&c)[8])
 {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    // the largest magnitude, a NaN if there is one
+    uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        if constexpr (BF16) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+        else asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+    }
+    m = max(m & 0xffffu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const uint32_t most = BF16 ? m << 16 : __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(m))));
+    float inv;
+    bool wide;
+    const uint32_t scale = scale_byte4(most, inv, wide);
+    uint64_t inv2;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(inv2) : "f"(inv));
+    float f[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         f[2 * i] = to_float<BF16>(static_cast<uint16_t>(w[i]));
         f[2 * i + 1] = to_float<BF16>(static_cast<uint16_t>(w[i] >> 16));
     }
-}
-
-// 8 features of a block of 16 whose other half the neighbouring lane (^ 1) has, as codes c + 8; the block's scale byte.
-template <bool BF16>
-__device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t (&c)[8])
-{
-    float f[8];
-    unpack8<BF16>(x, f);
-    uint32_t most = 0;
+    if (__any_sync(0xffffffffu, wide)) {
+        // (8 s and 7 s are exact; where s is 0 the codes are anyway)
+        const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(scale << 7)));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(f[i]) & 0x7fffffffu);
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    float inv;
-    const uint32_t scale = scale_byte4(most, inv);
+        for (int i = 0; i < 8; ++i) f[i] = fminf(fmaxf(f[i], -8.f * s), 7.f * s);
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = code4(f[i], inv);
+    for (int i = 0; i < 4; ++i) {
+        uint64_t x2;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(x2) : "f"(f[2 * i]), "f"(f[2 * i + 1]));
+        x2 = code4_2(x2, inv2);
+        c[2 * i] = static_cast<uint32_t>(x2);
+        c[2 * i + 1] = static_cast<uint32_t>(x2 >> 32);
+    }
     return scale;
 }
 
@@ -41,7 +56,7 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t (&c)[8])
 // A warp takes 2 (d = 64: 4) adjacent slots of a head at a time, a lane 8 features
 // of K and of V.
 template <int HD, bool BF16>
-__global__ void __launch_bounds__(256) cache4_append_kernel(const CacheAppendArgs a)
+__global__ void __launch_bounds__(256, 3) cache4_append_kernel(const CacheAppendArgs a)
 {
     constexpr uint32_t LK = HD / 8, KP = 32 / LK;      // lanes of a key, keys of a warp
     const int64_t bi = blockIdx.x;
@@ -54,44 +69,56 @@ __global__ void __launch_bounds__(256) cache4_append_kernel(const CacheAppendArg
         const uint32_t h_kv = static_cast<uint32_t>(a.c.h_kv), c = lane % LK, sub = lane / LK;
         const uint32_t first = static_cast<uint32_t>(s0) / KP, sets = static_cast<uint32_t>(s1 - 1) / KP - first + 1;
         const int64_t b0 = a.thd ? 0 : bi;
-        for (uint32_t u = warp; u < sets * h_kv; u += warps) {
-            const uint32_t set = u / h_kv, g = u - set * h_kv;
-            const uint32_t slot = (first + set) * KP + sub;
-            const bool in = slot >= s0 && slot < s1;
-            uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
-            uint8_t *kg = nullptr, *vg = nullptr;       // the slot's group
-            uint32_t row = 0;
-            if (in) {
-                const int32_t i = static_cast<int32_t>(slot) - p.len;
-                const int64_t src = p.src0 + (a.index ? a.index[bi * a.n + i] : i);
-                kx = ld_nc_v4(a.k + b0 * a.k_stride[0] + src * a.k_stride[1] + g * a.k_stride[2] + c * 8);
-                vx = ld_nc_v4(a.v + b0 * a.v_stride[0] + src * a.v_stride[1] + g * a.v_stride[2] + c * 8);
-                const int64_t page = cache_page(a.c, bi, slot, row);
-                const int64_t at = static_cast<int64_t>(row >> 4) * Group4<HD>::kBytes;
-                kg = reinterpret_cast<uint8_t*>(a.c.k) + page * a.c.k_stride[0] + g * a.c.k_stride[2] + at;
-                vg = reinterpret_cast<uint8_t*>(a.c.v) + page * a.c.v_stride[0] + g * a.c.v_stride[2] + at;
+        constexpr int U = 2;                            // sets whose loads are on their way together
+        for (uint32_t u = warp; u < sets * h_kv; u += warps * U) {
+            uint4 kx[U], vx[U];
+            uint8_t *kg[U], *vg[U];                     // the slots' groups, NULL: not a slot of this call
+            uint32_t x[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const uint32_t uk = u + k * warps, set = uk / h_kv, g = uk - set * h_kv;
+                const uint32_t slot = (first + set) * KP + sub;
+                kx[k] = vx[k] = make_uint4(0u, 0u, 0u, 0u);
+                kg[k] = vg[k] = nullptr;
+                x[k] = slot & 1;
+                if (uk < sets * h_kv && slot >= s0 && slot < s1) {
+                    const int32_t i = static_cast<int32_t>(slot) - p.len;
+                    const int64_t src = p.src0 + (a.index ? a.index[bi * a.n + i] : i);
+                    kx[k] = ld_nc_v4(a.k + b0 * a.k_stride[0] + src * a.k_stride[1] + g * a.k_stride[2] + c * 8);
+                    vx[k] = ld_nc_v4(a.v + b0 * a.v_stride[0] + src * a.v_stride[1] + g * a.v_stride[2] + c * 8);
+                    uint32_t row;
+                    const int64_t page = cache_page(a.c, bi, slot, row);
+                    const int64_t at = static_cast<int64_t>(row >> 4) * Group4<HD>::kBytes;
+                    kg[k] = reinterpret_cast<uint8_t*>(a.c.k) + page * a.c.k_stride[0] + g * a.c.k_stride[2] + at;
+                    vg[k] = reinterpret_cast<uint8_t*>(a.c.v) + page * a.c.v_stride[0] + g * a.c.v_stride[2] + at;
+                    x[k] = row & 15;
+                }
             }
-            const uint32_t x = row & 15;
-            uint32_t q[8];
-            const uint32_t ks = quantise8<BF16>(kx, q);
-            const uint32_t kw = pack_half4(q[0], q[2], q[4], q[6]) | pack_half4(q[1], q[3], q[5], q[7]) << 16;
-            const uint32_t vs = quantise8<BF16>(vx, q);
-            const uint32_t v0 = pack_half4(q[0], q[1], q[2], q[3]), v1 = pack_half4(q[4], q[5], q[6], q[7]);
-            // an even slot's lane writes both keys' first half words, the odd slot's the second ones
-            const bool odd = slot & 1;
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, LK);
-            const bool both = __shfl_xor_sync(0xffffffffu, in ? 1 : 0, LK) != 0 && in;
-            if (!in) continue;
-            *reinterpret_cast<uint32_t*>(kg + k4_word<HD>(x, c)) = kw;
-            if (both) {
-                *reinterpret_cast<uint32_t*>(vg + v4_half<HD>(x & ~1u, 2 * c + (odd ? 1 : 0))) =
-                    odd ? other | v1 << 16 : v0 | other << 16;
-            } else {
-                *reinterpret_cast<uint16_t*>(vg + v4_half<HD>(x, 2 * c)) = static_cast<uint16_t>(v0);
-                *reinterpret_cast<uint16_t*>(vg + v4_half<HD>(x, 2 * c + 1)) = static_cast<uint16_t>(v1);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                uint32_t q[8];
+                const bool in = kg[k] != nullptr, odd = x[k] & 1;
+                const uint32_t ks = quantise8<BF16>(kx[k], q);
+                const uint32_t even4[4] = {q[0], q[2], q[4], q[6]}, odd4[4] = {q[1], q[3], q[5], q[7]};
+                const uint32_t kw = pack_word4(even4, odd4);
+                const uint32_t vs = quantise8<BF16>(vx[k], q);
+                const uint32_t lo4[4] = {q[0], q[1], q[2], q[3]}, hi4[4] = {q[4], q[5], q[6], q[7]};
+                const uint32_t vw = pack_word4(lo4, hi4);       // both half words of this key
+                // an even slot's lane writes both keys' first half words, the odd slot's the second ones
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, vw, LK);
+                const bool both = __shfl_xor_sync(0xffffffffu, in ? 1 : 0, LK) != 0 && in;
+                if (!in) continue;
+                *reinterpret_cast<uint32_t*>(kg[k] + k4_word<HD>(x[k], c)) = kw;
+                if (both) {
+                    *reinterpret_cast<uint32_t*>(vg[k] + v4_half<HD>(x[k] & ~1u, 2 * c + (odd ? 1 : 0))) =
+                        odd ? __byte_perm(other, vw, 0x7632) : __byte_perm(vw, other, 0x5410);
+                } else {
+                    *reinterpret_cast<uint16_t*>(vg[k] + v4_half<HD>(x[k], 2 * c)) = static_cast<uint16_t>(vw);
+                    *reinterpret_cast<uint16_t*>(vg[k] + v4_half<HD>(x[k], 2 * c + 1)) = static_cast<uint16_t>(vw >> 16);
+                }
+                if (c & 1) vg[k][v4_scale<HD>(x[k], c >> 1)] = static_cast<uint8_t>(vs);
+                else kg[k][k4_scale<HD>(x[k], c >> 1)] = static_cast<uint8_t>(ks);
             }
-            if (c & 1) vg[v4_scale<HD>(x, c >> 1)] = static_cast<uint8_t>(vs);
-            else kg[k4_scale<HD>(x, c >> 1)] = static_cast<uint8_t>(ks);
         }
         const uint32_t nr = static_cast<uint32_t>(s1 - s0);
         for (uint32_t u = threadIdx.x; u < nr * h_kv; u += blockDim.x) {
@@ -172,16 +199,17 @@ __device__ __forceinline__ ReadRow read_row(const CacheReadArgs& a, int64_t r)
 
 }  // namespace
 
-// A warp takes 2 (d = 64: 4) adjacent output rows of a head, a lane 8 features
-// of K and of V.
+// A warp takes 2 (d = 64: 4) adjacent output rows, all heads or a share of them, a lane 8 features of K and of V.
 template <int HD, bool BF16, bool Q4>
-__global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadArgs a)
+__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ CacheReadArgs a)
 {
     constexpr uint32_t LK = HD / 8, KP = 32 / LK;
+    constexpr int U = 2;                                // heads whose loads are on their way together
     const uint32_t lane = threadIdx.x & 31, c = lane % LK, sub = lane / LK;
     const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int64_t warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-    const int64_t units = (a.rows + KP - 1) / KP * a.c.h_kv;
+    const int32_t h_kv = static_cast<int32_t>(a.c.h_kv);
+    const int64_t units = (a.rows + KP - 1) / KP * a.splits;
     if (blockIdx.x == 0 && a.offsets) {
         // (rows of no sequence are found below; here offsets that do not ascend from 0 to the end)
         bool ok = a.offsets[0] == 0 && a.offsets[a.c.b] == a.rows;
@@ -189,58 +217,104 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadArgs a)
         if (!ok) set_status(a.c.status, SDPA_ERR_BAD_LENGTHS);
     }
     for (int64_t u = warp; u < units; u += warps) {
-        const int64_t set = u / a.c.h_kv, g = u - set * a.c.h_kv, r = set * KP + sub;
+        const int64_t set = u / a.splits, r = set * KP + sub;
+        const int32_t h0 = static_cast<int32_t>(u - set * a.splits) * a.per_split, h1 = min(h0 + a.per_split, h_kv);
         if (r >= a.rows) continue;
         const ReadRow x = read_row(a, r);
-        uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
         uint32_t row = 0;
         const int64_t page = x.slot < 0 ? -1 : cache_page(a.c, x.bi, static_cast<uint32_t>(x.slot), row);
-        if (page >= 0) {
-            if constexpr (Q4) {
-                const int64_t at = static_cast<int64_t>(row >> 4) * Group4<HD>::kBytes;
-                const uint8_t* kg = reinterpret_cast<const uint8_t*>(a.c.k) + page * a.c.k_stride[0] + g * a.c.k_stride[2] + at;
-                const uint8_t* vg = reinterpret_cast<const uint8_t*>(a.c.v) + page * a.c.v_stride[0] + g * a.c.v_stride[2] + at;
-                const uint32_t i = row & 15;
-                const uint32_t kw = *reinterpret_cast<const uint32_t*>(kg + k4_word<HD>(i, c));
-                const uint2 vw = *reinterpret_cast<const uint2*>(vg + (v4_half<HD>(i, 2 * c) & ~3u));
-                const uint32_t ks = kg[k4_scale<HD>(i, c >> 1)], vs = vg[v4_scale<HD>(i, c >> 1)];
-                uint32_t f[4];
-                values4(kw, scale4<0x0404>(ks), f);
-                kx = make_uint4(f[0], f[1], f[2], f[3]);
-                // V: this key's halves, paired feature by feature
-                const uint32_t two = __byte_perm(vw.x, vw.y, i & 1 ? 0x7632 : 0x5410);
-                values4(two, scale4<0x0404>(vs), f);
-                vx = make_uint4(__byte_perm(f[0], f[1], 0x5410), __byte_perm(f[2], f[3], 0x5410),
-                                __byte_perm(f[0], f[1], 0x7632), __byte_perm(f[2], f[3], 0x7632));
-                if constexpr (BF16) {
-                    auto conv = [](uint32_t h) -> uint32_t {
-                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                        uint32_t z;
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(z) : "f"(y.y), "f"(y.x));
-                        return z;
-                    };
-                    kx = make_uint4(conv(kx.x), conv(kx.y), conv(kx.z), conv(kx.w));
-                    vx = make_uint4(conv(vx.x), conv(vx.y), conv(vx.z), conv(vx.w));
+        const int64_t b0 = a.offsets ? 0 : r / a.s, j = a.offsets ? r : r - b0 * a.s;
+        uint16_t* ko = a.k + b0 * a.k_stride[0] + j * a.k_stride[1] + c * 8;
+        uint16_t* vo = a.v + b0 * a.v_stride[0] + j * a.v_stride[1] + c * 8;
+        if constexpr (Q4) {
+            const uint32_t i = row & 15;
+            const int64_t at = static_cast<int64_t>(row >> 4) * Group4<HD>::kBytes;
+            const uint8_t* kp = reinterpret_cast<const uint8_t*>(a.c.k) + page * a.c.k_stride[0] + at;
+            const uint8_t* vp = reinterpret_cast<const uint8_t*>(a.c.v) + page * a.c.v_stride[0] + at;
+            const uint32_t kw_at = k4_word<HD>(i, c), ks_at = k4_scale<HD>(i, c >> 1);
+            const uint32_t vw_at = v4_half<HD>(i, 2 * c) & ~3u, vs_at = v4_scale<HD>(i, c >> 1);
+#pragma unroll 1
+            for (int32_t h = h0; h < h1; h += U) {
+                uint32_t kw[U], ks[U], vs[U];
+                uint2 vw[U];
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    kw[k] = ks[k] = vs[k] = 0u;
+                    vw[k] = make_uint2(0u, 0u);
+                    if (page >= 0 && h + k < h1) {
+                        const uint8_t* kg = kp + (h + k) * a.c.k_stride[2];
+                        const uint8_t* vg = vp + (h + k) * a.c.v_stride[2];
+                        kw[k] = *reinterpret_cast<const uint32_t*>(kg + kw_at);
+                        vw[k] = *reinterpret_cast<const uint2*>(vg + vw_at);
+                        ks[k] = kg[ks_at];
+                        vs[k] = vg[vs_at];
+                    }
                 }
-            } else {
-                kx = ld_nc_v4(a.c.k + page * a.c.k_stride[0] + row * a.c.k_stride[1] + g * a.c.k_stride[2] + c * 8);
-                vx = ld_nc_v4(a.c.v + page * a.c.v_stride[0] + row * a.c.v_stride[1] + g * a.c.v_stride[2] + c * 8);
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    if (h + k >= h1) break;
+                    // V: this key's half words, whose features go to the low and the high half of a register
+                    const uint32_t two = __byte_perm(vw[k].x, vw[k].y, i & 1 ? 0x7632 : 0x5410);
+                    uint32_t f[4], g[4];
+                    if constexpr (BF16) {
+                        auto scale = [](uint32_t b, uint32_t& n24) -> uint32_t {
+                            const __nv_bfloat162 s = __float2bfloat162_rn(__half2float(__ushort_as_half(static_cast<uint16_t>(b << 7))));
+                            const __nv_bfloat162 n = __hmul2(s, __float2bfloat162_rn(-24.f));
+                            n24 = *reinterpret_cast<const uint32_t*>(&n);
+                            return *reinterpret_cast<const uint32_t*>(&s);
+                        };
+                        uint32_t n24;
+                        uint32_t s = scale(ks[k], n24);
+                        values4_bf16(kw[k], s, n24, f);
+                        s = scale(vs[k], n24);
+                        values4_bf16(two, s, n24, g);
+                    } else {
+                        values4(kw[k], scale4<0x0404>(ks[k]), f);
+                        values4(two, scale4<0x0404>(vs[k]), g);
+                    }
+                    *reinterpret_cast<uint4*>(ko + (h + k) * a.k_stride[2]) = make_uint4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<uint4*>(vo + (h + k) * a.v_stride[2]) =
+                        make_uint4(__byte_perm(g[0], g[1], 0x5410), __byte_perm(g[2], g[3], 0x5410),
+                                   __byte_perm(g[0], g[1], 0x7632), __byte_perm(g[2], g[3], 0x7632));
+                }
+            }
+        } else {
+            const uint16_t* kp = a.c.k + page * a.c.k_stride[0] + row * a.c.k_stride[1] + c * 8;
+            const uint16_t* vp = a.c.v + page * a.c.v_stride[0] + row * a.c.v_stride[1] + c * 8;
+#pragma unroll 1
+            for (int32_t h = h0; h < h1; h += U) {
+                uint4 kx[U], vx[U];
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const bool in = page >= 0 && h + k < h1;
+                    kx[k] = in ? ld_nc_v4(kp + (h + k) * a.c.k_stride[2]) : make_uint4(0u, 0u, 0u, 0u);
+                    vx[k] = in ? ld_nc_v4(vp + (h + k) * a.c.v_stride[2]) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    if (h + k >= h1) break;
+                    *reinterpret_cast<uint4*>(ko + (h + k) * a.k_stride[2]) = kx[k];
+                    *reinterpret_cast<uint4*>(vo + (h + k) * a.v_stride[2]) = vx[k];
+                }
             }
         }
-        const int64_t b0 = a.offsets ? 0 : r / a.s, j = a.offsets ? r : r - b0 * a.s;
-        *reinterpret_cast<uint4*>(a.k + b0 * a.k_stride[0] + j * a.k_stride[1] + g * a.k_stride[2] + c * 8) = kx;
-        *reinterpret_cast<uint4*>(a.v + b0 * a.v_stride[0] + j * a.v_stride[1] + g * a.v_stride[2] + c * 8) = vx;
     }
 }
 
 namespace {
 
 template <int HD, bool BF16, bool Q4>
-cudaError_t launch_read(const CacheReadArgs& a, cudaStream_t s)
+cudaError_t launch_read(const CacheReadArgs& a0, cudaStream_t s)
 {
+    CacheReadArgs a = a0;
     constexpr int64_t KP = 256 / HD;
-    const int64_t units = (a.rows + KP - 1) / KP * a.c.h_kv;
-    const int64_t ctas = imin64((units + 7) / 8, 152 * 8);
+    // a warp takes all heads of its rows (which are looked up once then), a share of them where there are fewer rows than
+    // warps that fit
+    const int64_t sets = (a.rows + KP - 1) / KP, most = 152 * 48;
+    const int64_t splits = imax64(1, imin64(a.c.h_kv, most / sets));
+    a.per_split = static_cast<int32_t>((a.c.h_kv + splits - 1) / splits);
+    a.splits = static_cast<int32_t>((a.c.h_kv + a.per_split - 1) / a.per_split);
+    const int64_t ctas = imin64((sets * a.splits + 7) / 8, 152 * 6);
     cache_read_kernel<HD, BF16, Q4><<<static_cast<unsigned>(ctas), 256, 0, s>>>(a);
     return cudaGetLastError();
 }

@@ -26,7 +26,7 @@ struct RopeArgs {
     float eps, weight_offset, rot_scale;
     const int32_t *positions, *axis, *seq_lens;
     const float* freq;
-    int32_t splits, per_split; // a row's heads are shared between this many warps, this many for each
+    int32_t splits[2], per_split;  // a token's queries, its keys are shared between so many warps, so many heads for each
     float* partial;            // backward with a norm: [ctas][2][d]
     int32_t ctas;
 };

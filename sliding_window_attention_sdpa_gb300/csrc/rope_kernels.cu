@@ -2,10 +2,10 @@
 // its backward pass.
 //
 // Both are bound by reading their inputs and writing their outputs once. A warp
-// takes a token (few tokens: a share of its heads): it computes the token's cosines
-// and sines, which all heads have in common, puts them into its shared memory and
-// keeps those of its lanes' features in registers; then head after head, 8
-// features (16 bytes) a lane, 2 heads at a time (d = 64: 4).
+// takes a token's queries or keys (few tokens: a share of the heads): it computes
+// the token's cosines and sines, which all heads have in common, puts them into its
+// shared memory and keeps those of its lanes' features in registers; then head
+// after head, 8 features (16 bytes) a lane, 2 heads at a time (d = 64: 4).
 //
 // Rotation: feature f becomes y_f cos + y_partner (+-) sin, with the sign kept
 // in the lane's sine and (1, 0) for features that are not rotated. The partner of
@@ -73,11 +73,17 @@ __device__ __forceinline__ float head_sum(float x)
 
 }  // namespace
 
+#ifndef V_FU
+#define V_FU 4
+#define V_FO 3
+#define V_BU 2
+#define V_BO 2
+#endif
 template <int HD, bool BF16, RopeMode MODE, bool NORM, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const __grid_constant__ RopeArgs a)
+__global__ void __launch_bounds__(kRopeThreads, BWD ? V_BO : V_FO) rope_kernel(const __grid_constant__ RopeArgs a)
 {
     constexpr int LK = HD / 8, HP = 32 / LK;       // lanes of a head, heads at a time
-    constexpr int U = BWD ? 2 : 4;                 // of those on their way together
+    constexpr int U = BWD ? V_BU : V_FU;           // of those on their way together
     constexpr int PAIRS = HD / 64;                 // pairs of a lane when angles are computed
     __shared__ float2 sh_turn[kRopeWarps][HD / 2];
     __shared__ float sh_row[MODE == kAnyHalves ? kRopeWarps : 1][MODE == kAnyHalves ? HP : 1][HD];
@@ -99,28 +105,47 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const _
             if (a.axis) axis[i] = min(max(a.axis[p], 0), a.n_axes - 1);
         }
     }
-    float w[2][8];
-    float dw[2][8];
+    // the lane's features of the weights, and of their gradient's sum, of the tensor in hand (queries first, then keys)
+    float w[8], dw[8];
+    int n = -1;
+    auto flush = [&]() {
+        if constexpr (BWD && NORM) {
+            // lanes with the same features
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+            for (int e = 0; e < 8; ++e) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[n][e] = 1.f;
-            dw[n][e] = 0.f;
-            if (NORM && a.t[n].heads > 0) {
-                float v;
-                if (a.weight_f32) v = static_cast<const float*>(a.t[n].weight)[f0 + e];
-                else if constexpr (BF16) v = __bfloat162float(static_cast<const __nv_bfloat16*>(a.t[n].weight)[f0 + e]);
-                else v = __half2float(static_cast<const __half*>(a.t[n].weight)[f0 + e]);
-                w[n][e] = v + a.weight_offset;
+                for (int o = LK; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
+                if (sub == 0) sh_dw[warp][n][f0 + e] = dw[e];
             }
         }
+    };
+    if constexpr (BWD && NORM)
+        for (int i = tid; i < kRopeWarps * 2 * HD; i += kRopeThreads) (&sh_dw[0][0][0])[i] = 0.f;
+    __syncthreads();
 
-    const int64_t units = a.rows * a.splits;
+    const int64_t units_q = a.rows * a.splits[0], units = units_q + a.rows * a.splits[1];
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp; u < units; u += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
-        const int64_t row = u / a.splits;
-        const int h0 = static_cast<int>(u - row * a.splits) * a.per_split, h1 = min(h0 + a.per_split, a.heads);
-        const int64_t bi = row / a.s, j = row - bi * a.s;
+        const int now = u >= units_q ? 1 : 0;
+        const RopeTensor& t = a.t[now];
+        if (now != n) {
+            if (n >= 0) flush();
+            n = now;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dw[e] = 0.f;
+                w[e] = 1.f;
+                if constexpr (NORM) {
+                    float v;
+                    if (a.weight_f32) v = static_cast<const float*>(t.weight)[f0 + e];
+                    else if constexpr (BF16) v = __bfloat162float(static_cast<const __nv_bfloat16*>(t.weight)[f0 + e]);
+                    else v = __half2float(static_cast<const __half*>(t.weight)[f0 + e]);
+                    w[e] = v + a.weight_offset;
+                }
+            }
+        }
+        const int64_t un = now ? u - units_q : u, row = a.splits[now] == 1 ? un : un / a.splits[now];
+        const int first = static_cast<int>(un - row * a.splits[now]) * a.per_split, last = min(first + a.per_split, t.heads);
+        const int64_t bi = a.s == a.rows ? 0 : row / a.s, j = row - bi * a.s;
         const bool real = a.seq_lens == nullptr || j < a.seq_lens[bi];
         // ---- the token's turns
         float cs[8], sn[8];
@@ -175,75 +200,62 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3) rope_kernel(const _
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = f0 + e < a.rot ? fmaf(y[e], cs[e], p[e] * sn[e]) : y[e];
         };
-        // ---- the heads, queries then keys
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const RopeTensor& t = a.t[n];
-            const int off = n ? a.t[0].heads : 0;
-            const int first = max(h0 - off, 0), last = min(h1 - off, t.heads);
-            const uint16_t* xp = t.x + bi * t.x_stride[0] + j * t.x_stride[1] + f0;
-            const uint16_t* gp = t.g + bi * t.g_stride[0] + j * t.g_stride[1] + f0;
-            uint16_t* op = t.o + bi * t.o_stride[0] + j * t.o_stride[1] + f0;
+        // ---- the heads
+        const uint16_t* xp = t.x + bi * t.x_stride[0] + j * t.x_stride[1] + f0;
+        const uint16_t* gp = t.g + bi * t.g_stride[0] + j * t.g_stride[1] + f0;
+        uint16_t* op = t.o + bi * t.o_stride[0] + j * t.o_stride[1] + f0;
 #pragma unroll 1
-            for (int h = first; h < last; h += HP * U) {
-                uint4 xr[U], gr[U];
+        for (int h = first; h < last; h += HP * U) {
+            uint4 xr[U], gr[U];
 #pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int hh = h + k * HP + sub;
-                    const bool in = real && hh < last;
-                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                    xr[k] = (!BWD || NORM) && in ? *reinterpret_cast<const uint4*>(xp + hh * t.x_stride[2]) : z;
-                    gr[k] = BWD && in ? *reinterpret_cast<const uint4*>(gp + hh * t.g_stride[2]) : z;
+            for (int k = 0; k < U; ++k) {
+                const int hh = h + k * HP + sub;
+                const bool in = real && hh < last;
+                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                xr[k] = (!BWD || NORM) && in ? *reinterpret_cast<const uint4*>(xp + hh * t.x_stride[2]) : z;
+                gr[k] = BWD && in ? *reinterpret_cast<const uint4*>(gp + hh * t.g_stride[2]) : z;
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int hh = h + k * HP + sub;
+                if (h + k * HP >= last) break;
+                float x[8], y[8], r = 1.f;
+                unpack8<BF16>(xr[k], x);
+                if constexpr (NORM) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+                    r = rsqrtf(fmaf(head_sum<LK>(ss), 1.f / HD, a.eps));
                 }
+                if constexpr (!BWD) {
 #pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int hh = h + k * HP + sub;
-                    if (h + k * HP >= last) break;
-                    float x[8], y[8], r = 1.f;
-                    unpack8<BF16>(xr[k], x);
+                    for (int e = 0; e < 8; ++e) y[e] = NORM ? x[e] * r * w[e] : x[e];
+                    turned(y);
+                } else {
+                    unpack8<BF16>(gr[k], y);
+                    turned(y);
                     if constexpr (NORM) {
-                        float ss = 0.f;
+                        float dot = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                        r = rsqrtf(fmaf(head_sum<LK>(ss), 1.f / HD, a.eps));
-                    }
-                    if constexpr (!BWD) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = NORM ? x[e] * r * w[n][e] : x[e];
-                        turned(y);
-                    } else {
-                        unpack8<BF16>(gr[k], y);
-                        turned(y);
-                        if constexpr (NORM) {
-                            float dot = 0.f;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                x[e] *= r;
-                                dw[n][e] = fmaf(y[e], x[e], dw[n][e]);
-                                y[e] *= w[n][e];
-                                dot = fmaf(y[e], x[e], dot);
-                            }
-                            dot = head_sum<LK>(dot) * (1.f / HD);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) y[e] = r * fmaf(-x[e], dot, y[e]);
+                        for (int e = 0; e < 8; ++e) {
+                            x[e] *= r;
+                            dw[e] = fmaf(y[e], x[e], dw[e]);
+                            y[e] *= w[e];
+                            dot = fmaf(y[e], x[e], dot);
                         }
+                        dot = head_sum<LK>(dot) * (1.f / HD);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = r * fmaf(-x[e], dot, y[e]);
                     }
-                    if (hh < last)
-                        *reinterpret_cast<uint4*>(op + hh * t.o_stride[2]) = real ? pack8<BF16>(y) : make_uint4(0u, 0u, 0u, 0u);
                 }
+                if (hh < last)
+                    *reinterpret_cast<uint4*>(op + hh * t.o_stride[2]) = real ? pack8<BF16>(y) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
     }
     if constexpr (BWD && NORM) {
-        // the CTA's sums: lanes with the same features, then warps, in order
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-#pragma unroll
-                for (int o = LK; o < 32; o <<= 1) dw[n][e] += __shfl_xor_sync(0xffffffffu, dw[n][e], o);
-                if (sub == 0) sh_dw[warp][n][f0 + e] = dw[n][e];
-            }
+        // the CTA's sums: its warps', in order
+        if (n >= 0) flush();
         __syncthreads();
         for (int i = tid; i < 2 * HD; i += kRopeThreads) {
             float x = 0.f;
@@ -278,16 +290,21 @@ __global__ void __launch_bounds__(256) rope_sum_kernel(const __grid_constant__ R
 
 void rope_plan(RopeArgs& a, bool backward)
 {
-    const int resident = 152 * (backward ? 2 : 3);
+    const int resident = 152 * (backward ? V_BO : V_FO);
     const int hp = 256 / a.d;
-    // a warp for a token, unless there are fewer tokens than warps: then a token's heads are shared out
-    const int64_t warps = static_cast<int64_t>(resident) * kRopeWarps, sets = (a.heads + hp - 1) / hp;
-    int64_t splits = a.rows > 0 ? warps / a.rows : 1;
-    splits = imax64(1, imin64(splits, sets));
-    const int64_t per = (sets + splits - 1) / splits;
-    a.per_split = static_cast<int32_t>(per * hp);
-    a.splits = static_cast<int32_t>((sets + per - 1) / per);
-    a.ctas = static_cast<int32_t>(imax64(1, imin64(resident, (a.rows * a.splits + kRopeWarps - 1) / kRopeWarps)));
+    // a warp for a token's queries and one for its keys, unless there are fewer of those than warps: then heads are shared out
+    const int64_t warps = static_cast<int64_t>(resident) * kRopeWarps;
+    const int64_t sets = (static_cast<int64_t>(a.t[0].heads) + hp - 1) / hp + (static_cast<int64_t>(a.t[1].heads) + hp - 1) / hp;
+    const int64_t shares = a.rows > 0 ? imax64(1, imin64(warps / a.rows, sets)) : 1;
+    const int64_t most = (a.t[0].heads > a.t[1].heads ? a.t[0].heads : a.t[1].heads) + hp - 1;
+    a.per_split = static_cast<int32_t>(imin64(most / hp, (sets + shares - 1) / shares) * hp);
+    if (shares <= 2) a.per_split = static_cast<int32_t>(most / hp * hp);
+    int64_t units = 0;
+    for (int n = 0; n < 2; ++n) {
+        a.splits[n] = (a.t[n].heads + a.per_split - 1) / a.per_split;
+        units += a.rows * a.splits[n];
+    }
+    a.ctas = static_cast<int32_t>(imax64(1, imin64(resident, (units + kRopeWarps - 1) / kRopeWarps)));
 }
 
 namespace {

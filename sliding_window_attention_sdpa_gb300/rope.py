@@ -13,6 +13,9 @@ library on torch's current stream; the calls can be captured into a CUDA graph.
 from __future__ import annotations
 
 import ctypes
+import struct
+
+from .cache import _apart, _flat, _given, _strides, _strides4
 
 _i64x3 = ctypes.c_int64 * 3
 _vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
@@ -66,106 +69,124 @@ def sdpa_rope_bwd(params: SdpaRopeParams, workspace: int, workspace_bytes: int, 
 
 # ------------------------------------------------------------- torch helpers
 
-def _rows(name, t, shape, dev, dt, output=False):
-    """Strides (batch, token, head) of a tensor of this shape; 0 where there is no second entry."""
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dt:
-        raise ValueError(f"{name}: expected dtype {dt}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name}: expected device {dev}, got {t.device}")
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"{name}: the feature dimension must be contiguous (stride 1)")
-    if output and any(s == 0 and n > 1 for s, n in zip(st, t.shape)):
-        raise ValueError(f"{name}: rows share memory (an expanded tensor)")
-    st = [s if n > 1 else 0 for s, n in zip(st[:-1], t.shape)]
-    return _i64x3(*(st if len(st) == 3 else [0, *st]))
+class _Calls:
+    """The entry points with their parameter block as packed bytes (the layout of
+    the struct above), and torch's current stream: see cache._Calls."""
+
+    def __init__(self):
+        import torch
+        from . import SDPA_BF16, SDPA_F16
+        lib = _lib()
+        self.fwd, self.bwd = lib["sdpa_rope_fwd"], lib["sdpa_rope_bwd"]
+        self.fwd.argtypes, self.fwd.restype = [ctypes.c_char_p, _vp], ctypes.c_int
+        self.bwd.argtypes, self.bwd.restype = [ctypes.c_char_p, _vp, ctypes.c_size_t, _vp], ctypes.c_int
+        self.dtypes = {torch.bfloat16: SDPA_BF16, torch.float16: SDPA_F16}
+        self.empty, self.float32, self.int32, self.uint8 = torch.empty, torch.float32, torch.int32, torch.uint8
+        self.stream = torch._C._cuda_getCurrentRawStream
 
 
-def _array(name, t, shape, dev, dtypes):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: expected dtype {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name}: expected device {dev}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+_PARAMS = struct.Struct("4i8q3fi14Q18q")
+assert _PARAMS.size == ctypes.sizeof(SdpaRopeParams)
+_NONE = (0, 0, 0)
+_calls = None
 
 
-def _params(like_q, like_k, positions, freq, q_weight, k_weight, eps, weight_offset, axis, interleaved, rot_scale, seq_lens):
-    """The parameters that the tensors' common shape gives (like_k: None for queries alone)."""
-    import torch
-    from . import SDPA_BF16, SDPA_BSHD, SDPA_F16, SDPA_THD
-    dt, dev = like_q.dtype, like_q.device
-    if dt not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"unsupported dtype {dt}")
-    if like_q.dim() not in (3, 4):
-        raise ValueError(f"q: expected [b, s, h, d] or [total, h, d], got {tuple(like_q.shape)}")
-    p = SdpaRopeParams()
-    p.dtype = SDPA_BF16 if dt == torch.bfloat16 else SDPA_F16
-    *rows, p.h_q, p.d = like_q.shape
-    if like_k is not None:
-        if like_k.dim() != like_q.dim() or list(like_k.shape[:-2]) != rows or like_k.shape[-1] != p.d:
-            raise ValueError(f"k: expected {tuple(rows)} rows of heads of {p.d} features like q's, got {tuple(like_k.shape)}")
-        p.h_kv = like_k.shape[-2]
-    if len(rows) == 1:
-        p.layout, p.total = SDPA_THD, rows[0]
-    else:
-        p.layout, p.b, p.s = SDPA_BSHD, *rows
-    if freq.dim() != 1:
-        raise ValueError(f"freq: expected [rot / 2], got {tuple(freq.shape)}")
-    p.rot = 2 * freq.shape[0]
-    p.freq = _array("freq", freq, freq.shape, dev, (torch.float32,))
-    p.n_axes = 1
-    if positions.dim() == len(rows) + 1:
-        p.n_axes = positions.shape[0]
-        if axis is None and p.n_axes != 1:
-            raise ValueError("axis: positions of several axes need each pair's axis")
-    shape = positions.shape[:1] if positions.dim() == len(rows) + 1 else ()
-    p.positions = _array("positions", positions, (*shape, *rows), dev, (torch.int32,))
-    if axis is not None:
-        p.axis = _array("axis", axis, freq.shape, dev, (torch.int32,))
-    if seq_lens is not None:
-        if len(rows) == 1:
+def _c() -> _Calls:
+    global _calls
+    if _calls is None:
+        _calls = _Calls()
+    return _calls
+
+
+def _rows(name, t, shape, dev, dt):
+    """Strides (batch, token, head) of a tensor of this shape."""
+    if len(shape) == 4:
+        return _strides4(name, t, shape, dev, dt)
+    return 0, *_strides(name, t, shape, dev, dt)
+
+
+def _weight(name, w, d, dev, dt, c):
+    if w.dtype is not dt and w.dtype is not c.float32:
+        raise ValueError(f"{name}: expected dtype {dt} or {c.float32}, got {w.dtype}")
+    return _flat(name, w, (d,), dev, w.dtype)
+
+
+class _Shape:
+    """What the tensors' common shape and the arrays give of a call's parameters."""
+    __slots__ = ("c", "dt", "dev", "qs", "ks", "head", "floats", "arrays", "norm")
+
+    def __init__(self, q, k, positions, freq, q_weight, k_weight, eps, weight_offset, axis, interleaved, rot_scale, seq_lens):
+        c = self.c = _calls or _c()
+        dt, dev = self.dt, self.dev = q.dtype, q.device
+        code = c.dtypes.get(dt)
+        if code is None:
+            raise ValueError(f"unsupported dtype {dt}")
+        qs = self.qs = q.shape
+        n = len(qs)
+        if n not in (3, 4):
+            raise ValueError(f"q: expected [b, s, h, d] or [total, h, d], got {tuple(qs)}")
+        rows, d = qs[:-2], qs[-1]
+        h_kv, self.ks = 0, None
+        if k is not None:
+            ks = self.ks = k.shape
+            if len(ks) != n or ks[:-2] != rows or ks[-1] != d:
+                raise ValueError(f"k: expected {tuple(rows)} rows of heads of {d} features like q's, got {tuple(ks)}")
+            h_kv = ks[-2]
+        if freq.dim() != 1:
+            raise ValueError(f"freq: expected [rot / 2], got {tuple(freq.shape)}")
+        half = freq.shape[0]
+        n_axes, at = 1, positions.shape
+        if len(at) == n - 1:
+            n_axes = at[0]
+            if axis is None and n_axes != 1:
+                raise ValueError("axis: positions of several axes need each pair's axis")
+            want = (n_axes, *rows)
+        else:
+            want = rows
+        if seq_lens is not None and n == 3:
             raise ValueError("seq_lens: only with [b, s, h, d]")
-        p.seq_lens = _array("seq_lens", seq_lens, rows[:1], dev, (torch.int32,))
-    if like_k is None and k_weight is not None:
-        raise ValueError("k_weight: there is no k")
-    if like_k is not None and (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight: both or neither")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            setattr(p, name, _array(name, w, (p.d,), dev, (dt, torch.float32)))
-            if name == "k_weight" and w.dtype != q_weight.dtype:
-                raise ValueError(f"k_weight: expected dtype {q_weight.dtype}, got {w.dtype}")
-            p.weight_f32 = int(w.dtype == torch.float32)
-    p.eps, p.weight_offset, p.rot_scale, p.interleaved = eps, weight_offset, rot_scale, int(bool(interleaved))
-    return p, dt, dev
+        wq = wk = f32 = 0
+        self.norm = q_weight is not None
+        if k is None:
+            if k_weight is not None:
+                raise ValueError("k_weight: there is no k")
+        elif self.norm != (k_weight is not None):
+            raise ValueError("q_weight and k_weight: both or neither")
+        if self.norm:
+            wq = _weight("q_weight", q_weight, d, dev, dt, c)
+            f32 = int(q_weight.dtype is c.float32)
+            if k is not None:
+                if k_weight.dtype is not q_weight.dtype:
+                    raise ValueError(f"k_weight: expected dtype {q_weight.dtype}, got {k_weight.dtype}")
+                wk = _weight("k_weight", k_weight, d, dev, dt, c)
+        b, s, total = (0, 0, rows[0]) if n == 3 else (*rows, 0)
+        self.head = (code, int(n == 3), int(bool(interleaved)), f32, b, s, total, qs[-2], h_kv, d, 2 * half, n_axes, eps, weight_offset,
+                     rot_scale, 0)
+        self.arrays = (_flat("positions", positions, want, dev, c.int32),
+                       0 if axis is None else _flat("axis", axis, (half,), dev, c.int32), _flat("freq", freq, (half,), dev, c.float32),
+                       0 if seq_lens is None else _flat("seq_lens", seq_lens, rows[:1], dev, c.int32), wq, wk)
 
-
-def _stream(dev):
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev.index or 0)
+    def outputs(self, out):
+        """The tensors to write to, their addresses, their strides."""
+        qs, ks, dt, dev = self.qs, self.ks, self.dt, self.dev
+        if out is None:
+            oq = self.c.empty(qs, dtype=dt, device=dev)
+            ok = None if ks is None else self.c.empty(ks, dtype=dt, device=dev)
+        else:
+            oq, ok = out
+            _apart("out q", oq)
+            if ks is not None:
+                _apart("out k", ok)
+        sq = _rows("out q", oq, qs, dev, dt)
+        if ks is None:
+            return oq, None, oq.data_ptr(), 0, sq, _NONE
+        return oq, ok, oq.data_ptr(), ok.data_ptr(), sq, _rows("out k", ok, ks, dev, dt)
 
 
 def _check(code, where):
     if code:
         from . import SdpaError, last_error
         raise SdpaError(code, where, last_error())
-
-
-def _outputs(p, q, k, out, dt, dev):
-    import torch
-    if out is None:
-        out = torch.empty(q.shape, dtype=dt, device=dev), None if k is None else torch.empty(k.shape, dtype=dt, device=dev)
-    oq, ok = out
-    p.oq, p.oq_stride = oq.data_ptr(), _rows("out q", oq, q.shape, dev, dt, True)
-    if k is not None:
-        p.ok, p.ok_stride = ok.data_ptr(), _rows("out k", ok, k.shape, dev, dt, True)
-    return oq, ok
 
 
 def qk_rotate(q, k, positions, freq, *, q_weight=None, k_weight=None, eps: float = 1e-6, weight_offset: float = 0.0, axis=None,
@@ -182,12 +203,14 @@ def qk_rotate(q, k, positions, freq, *, q_weight=None, k_weight=None, eps: float
     write to, q and k themselves too. No gradient is recorded
     (qk_rotate_backward computes it).
     """
-    p, dt, dev = _params(q, k, positions, freq, q_weight, k_weight, eps, weight_offset, axis, interleaved, rot_scale, seq_lens)
-    p.q, p.q_stride = q.data_ptr(), _rows("q", q, q.shape, dev, dt)
-    if k is not None:
-        p.k, p.k_stride = k.data_ptr(), _rows("k", k, k.shape, dev, dt)
-    oq, ok = _outputs(p, q, k, out, dt, dev)
-    _check(sdpa_rope_fwd(p, _stream(dev)), "sdpa_rope_fwd")
+    x = _Shape(q, k, positions, freq, q_weight, k_weight, eps, weight_offset, axis, interleaved, rot_scale, seq_lens)
+    sq = _rows("q", q, x.qs, x.dev, x.dt)
+    kp, sk = (0, _NONE) if k is None else (k.data_ptr(), _rows("k", k, x.ks, x.dev, x.dt))
+    oq, ok, oqp, okp, soq, sok = x.outputs(out)
+    p = _PARAMS.pack(*x.head, *x.arrays, q.data_ptr(), kp, 0, 0, oqp, okp, 0, 0, *sq, *sk, 0, 0, 0, 0, 0, 0, *soq, *sok)
+    code = x.c.fwd(p, x.c.stream(x.dev.index or 0))
+    if code:
+        _check(code, "sdpa_rope_fwd")
     return oq, ok
 
 
@@ -199,31 +222,33 @@ def qk_rotate_backward(dq, dk, q, k, positions, freq, *, q_weight=None, k_weight
     weights). The other arguments are qk_rotate's; the weights' gradients are fp32
     [d] (None without weights). out: (dq, dk) to write to, the given ones too.
     """
-    import torch
-    p, dt, dev = _params(dq, dk, positions, freq, q_weight, k_weight, eps, weight_offset, axis, interleaved, rot_scale, seq_lens)
-    p.gq, p.gq_stride = dq.data_ptr(), _rows("dq", dq, dq.shape, dev, dt)
-    if dk is not None:
-        p.gk, p.gk_stride = dk.data_ptr(), _rows("dk", dk, dk.shape, dev, dt)
+    x = _Shape(dq, dk, positions, freq, q_weight, k_weight, eps, weight_offset, axis, interleaved, rot_scale, seq_lens)
+    c, dev, dt = x.c, x.dev, x.dt
+    sgq = _rows("dq", dq, x.qs, dev, dt)
+    gkp, sgk = (0, _NONE) if dk is None else (dk.data_ptr(), _rows("dk", dk, x.ks, dev, dt))
     wq = wk = None
-    n = 0
-    if q_weight is not None:
-        p.q, p.q_stride = q.data_ptr(), _rows("q", q, dq.shape, dev, dt)
-        wq = torch.empty(p.d, dtype=torch.float32, device=dev)
-        p.dq_weight = wq.data_ptr()
+    qp = kp = wqp = wkp = n = 0
+    sq = sk = _NONE
+    if x.norm:
+        qp, sq = q.data_ptr(), _rows("q", q, x.qs, dev, dt)
+        wq = c.empty(x.qs[-1], dtype=c.float32, device=dev)
+        wqp = wq.data_ptr()
         if dk is not None:
-            p.k, p.k_stride = k.data_ptr(), _rows("k", k, dk.shape, dev, dt)
-            wk = torch.empty(p.d, dtype=torch.float32, device=dev)
-            p.dk_weight = wk.data_ptr()
-    oq, ok = _outputs(p, dq, dk, out, dt, dev)
-    if q_weight is not None:
+            kp, sk = k.data_ptr(), _rows("k", k, x.ks, dev, dt)
+            wk = c.empty(x.qs[-1], dtype=c.float32, device=dev)
+            wkp = wk.data_ptr()
+    oq, ok, oqp, okp, soq, sok = x.outputs(out)
+    p = _PARAMS.pack(*x.head, *x.arrays, qp, kp, dq.data_ptr(), gkp, oqp, okp, wqp, wkp, *sq, *sk, *sgq, *sgk, *soq, *sok)
+    if x.norm:
         if workspace is None:
-            n = sdpa_rope_bwd_workspace_bytes(p)
+            n = sdpa_rope_bwd_workspace_bytes(SdpaRopeParams.from_buffer_copy(p))
             if n == 0:
-                from . import SDPA_ERR_INVALID_ARG, SdpaError, last_error
-                raise SdpaError(SDPA_ERR_INVALID_ARG, "sdpa_rope_bwd_workspace_bytes", last_error())
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            raise ValueError("workspace: expected a contiguous uint8 tensor")
-        n = workspace.numel()
-    _check(sdpa_rope_bwd(p, workspace.data_ptr() if n else 0, n, _stream(dev)), "sdpa_rope_bwd")
+                from . import SDPA_ERR_INVALID_ARG
+                _check(SDPA_ERR_INVALID_ARG, "sdpa_rope_bwd_workspace_bytes")
+            workspace = c.empty(n, dtype=c.uint8, device=dev)
+        else:
+            n = _given(workspace, c)
+    code = c.bwd(p, workspace.data_ptr() if n else 0, n, c.stream(dev.index or 0))
+    if code:
+        _check(code, "sdpa_rope_bwd")
     return oq, ok, wq, wk
