@@ -16,6 +16,8 @@
 // the product with a 32-bit position modulo 2^64 is the angle's fraction of a turn,
 // exact to 2^-24 of one for every position: fp32 products are off by whole radians
 // far into a text.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -31,35 +33,50 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 
+// CTAs on an SM: more leave too few registers for two batches (backward with 3: 413 us against 288 for 28 k packed rows of
+// 54 heads), fewer too few loads on their way
+template <bool BWD>
+constexpr int kRopeOcc = BWD ? 2 : 3;
+
 enum RopeMode { kNeighbours, kHalves, kAnyHalves };
 
-template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& x, float (&f)[8])
+// Two fp32 values in one 64-bit register, and packed arithmetic on them.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi)
 {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (BF16) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        } else {
-            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            f[2 * i] = y.x;
-            f[2 * i + 1] = y.y;
-        }
-    }
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float lo2(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float hi2(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
 }
 
 template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+__device__ __forceinline__ uint64_t unpack2(uint32_t w)
 {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-        else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (BF16) return pair2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pair2(y.x, y.y);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(uint64_t x)
+{
+    uint32_t w;
+    if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi2(x)), "f"(lo2(x)));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi2(x)), "f"(lo2(x)));
+    return w;
 }
 
 // Sum over the LK lanes of a head, the same in each.
@@ -73,19 +90,14 @@ __device__ __forceinline__ float head_sum(float x)
 
 }  // namespace
 
-#ifndef V_FU
-#define V_FU 4
-#define V_FO 3
-#define V_BU 2
-#define V_BO 2
-#endif
 template <int HD, bool BF16, RopeMode MODE, bool NORM, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads, BWD ? V_BO : V_FO) rope_kernel(const __grid_constant__ RopeArgs a)
+__global__ void __launch_bounds__(kRopeThreads, kRopeOcc<BWD>) rope_kernel(const __grid_constant__ RopeArgs a)
 {
     constexpr int LK = HD / 8, HP = 32 / LK;       // lanes of a head, heads at a time
-    constexpr int U = BWD ? V_BU : V_FU;           // of those on their way together
+    constexpr int U = 2;                           // of those in a batch: one is on its way while one is worked on
     constexpr int PAIRS = HD / 64;                 // pairs of a lane when angles are computed
-    __shared__ float2 sh_turn[kRopeWarps][HD / 2];
+    __shared__ __align__(16) float2 sh_turn[kRopeWarps][HD / 2];
+    __shared__ __align__(16) float sh_w[2][NORM ? HD : 1];       // weights
     __shared__ float sh_row[MODE == kAnyHalves ? kRopeWarps : 1][MODE == kAnyHalves ? HP : 1][HD];
     __shared__ float sh_dw[BWD && NORM ? kRopeWarps : 1][2][HD];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -105,157 +117,247 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? V_BO : V_FO) rope_kernel(c
             if (a.axis) axis[i] = min(max(a.axis[p], 0), a.n_axes - 1);
         }
     }
-    // the lane's features of the weights, and of their gradient's sum, of the tensor in hand (queries first, then keys)
-    float w[8], dw[8];
-    int n = -1;
-    auto flush = [&]() {
+    // the lane's features of the weights' gradient, of the tensor in hand (queries first, then keys)
+    uint64_t dw[4];
+    auto flush = [&](int n) {
         if constexpr (BWD && NORM) {
             // lanes with the same features
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
+                float x = e & 1 ? hi2(dw[e / 2]) : lo2(dw[e / 2]);
 #pragma unroll
-                for (int o = LK; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
-                if (sub == 0) sh_dw[warp][n][f0 + e] = dw[e];
+                for (int o = LK; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                if (sub == 0) sh_dw[warp][n][f0 + e] = x;
             }
         }
     };
-    if constexpr (BWD && NORM)
-        for (int i = tid; i < kRopeWarps * 2 * HD; i += kRopeThreads) (&sh_dw[0][0][0])[i] = 0.f;
+    if constexpr (NORM)
+        for (int i = tid; i < 2 * HD; i += kRopeThreads) {
+            const int f = i % HD;
+            const void* wt = a.t[i / HD].weight;
+            float v = 0.f;
+            if (wt == nullptr) continue;
+            if (a.weight_f32) v = static_cast<const float*>(wt)[f];
+            else if constexpr (BF16) v = __bfloat162float(static_cast<const __nv_bfloat16*>(wt)[f]);
+            else v = __half2float(static_cast<const __half*>(wt)[f]);
+            sh_w[i / HD][f] = v + a.weight_offset;
+        }
     __syncthreads();
 
     const int64_t units_q = a.rows * a.splits[0], units = units_q + a.rows * a.splits[1];
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp; u < units; u += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
-        const int now = u >= units_q ? 1 : 0;
-        const RopeTensor& t = a.t[now];
-        if (now != n) {
-            if (n >= 0) flush();
-            n = now;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kRopeWarps;
+    auto row_of = [&](int64_t u) -> int64_t {
+        const int32_t sp = a.splits[u >= units_q ? 1 : 0];
+        const int64_t un = u >= units_q ? u - units_q : u;
+        return sp == 1 ? un : un >> 32 ? un / sp : static_cast<uint32_t>(un) / static_cast<uint32_t>(sp);
+    };
+    // positions of the lane's pairs, a unit ahead
+    int32_t pos[PAIRS];
+    auto fetch_pos = [&](int64_t u) {
+        if (u >= units) return;
+        const int64_t row = row_of(u);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dw[e] = 0.f;
-                w[e] = 1.f;
-                if constexpr (NORM) {
-                    float v;
-                    if (a.weight_f32) v = static_cast<const float*>(t.weight)[f0 + e];
-                    else if constexpr (BF16) v = __bfloat162float(static_cast<const __nv_bfloat16*>(t.weight)[f0 + e]);
-                    else v = __half2float(static_cast<const __half*>(t.weight)[f0 + e]);
-                    w[e] = v + a.weight_offset;
+        for (int i = 0; i < PAIRS; ++i)
+            if (lane + 32 * i < half) pos[i] = a.positions[axis[i] * a.rows + row];
+    };
+    int64_t u = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
+    fetch_pos(u);
+    // the units of one tensor (a function each, so that its addresses and strides are constants)
+    auto tensor = [&](auto which, int64_t end) {
+    constexpr int now = decltype(which)::value;
+    const RopeTensor& t = a.t[now];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dw[e] = 0;
+#pragma unroll 1
+    for (; u < end; u += stride) {
+        const int64_t un = u - (now ? units_q : 0), row = row_of(u);
+        const int first = static_cast<int>(un - row * a.splits[now]) * a.per_split, last = min(first + a.per_split, t.heads);
+        const int64_t bi = a.s == a.rows ? 0 : static_cast<uint32_t>(row) / static_cast<uint32_t>(a.s), j = row - bi * a.s;
+        const bool real = a.seq_lens == nullptr || j < a.seq_lens[bi];
+        // ---- the heads' loads: a batch of U sets is on its way while the one before is worked on, the first one during the
+        // token's turns
+        const int64_t head0 = first + sub;
+        [[maybe_unused]] const uint16_t* xp = t.x + bi * t.x_stride[0] + j * t.x_stride[1] + head0 * t.x_stride[2] + f0;
+        [[maybe_unused]] const uint16_t* gp = t.g + bi * t.g_stride[0] + j * t.g_stride[1] + head0 * t.g_stride[2] + f0;
+        uint16_t* op = t.o + bi * t.o_stride[0] + j * t.o_stride[1] + head0 * t.o_stride[2] + f0;
+        uint4 xa[U], ga[U], xb[U], gb[U];
+        auto load = [&](int h, uint4 (&xr)[U], uint4 (&gr)[U]) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const bool in = real && h + k * HP + sub < last;
+                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (!BWD || NORM) {
+                    xr[k] = in ? *reinterpret_cast<const uint4*>(xp) : z;
+                    xp += HP * t.x_stride[2];
+                }
+                if constexpr (BWD) {
+                    gr[k] = in ? *reinterpret_cast<const uint4*>(gp) : z;
+                    gp += HP * t.g_stride[2];
                 }
             }
-        }
-        const int64_t un = now ? u - units_q : u, row = a.splits[now] == 1 ? un : un / a.splits[now];
-        const int first = static_cast<int>(un - row * a.splits[now]) * a.per_split, last = min(first + a.per_split, t.heads);
-        const int64_t bi = a.s == a.rows ? 0 : row / a.s, j = row - bi * a.s;
-        const bool real = a.seq_lens == nullptr || j < a.seq_lens[bi];
+        };
+        load(first, xa, ga);
         // ---- the token's turns
-        float cs[8], sn[8];
+        uint64_t cs[4], sn[4];
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
             const int p = lane + 32 * i;
             if (p < half) {
-                const int64_t pos = a.positions[axis[i] * a.rows + row];
-                const int32_t part = static_cast<int32_t>((static_cast<uint64_t>(pos) * turn[i]) >> 32);
+                const int32_t part = static_cast<int32_t>((static_cast<uint64_t>(static_cast<int64_t>(pos[i])) * turn[i]) >> 32);
                 float s, co;
                 sincospif(static_cast<float>(part) * 0x1p-31f, &s, &co);
                 sh_turn[warp][p] = make_float2(co * a.rot_scale, s * a.rot_scale);
             }
         }
         __syncwarp();
+        [[maybe_unused]] const bool on = f0 < a.rot;                     // (halves of a multiple of 8: the lane's features are alike)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int f = f0 + e;
-            cs[e] = 1.f;
-            sn[e] = 0.f;
-            if (f < a.rot) {
-                const bool hi = MODE == kNeighbours ? (e & 1) : f >= half;
-                const float2 x = sh_turn[warp][MODE == kNeighbours ? f >> 1 : hi ? f - half : f];
-                cs[e] = x.x;
-                // the sign of the turn, and of the turn back
-                sn[e] = hi != BWD ? x.y : -x.y;
+        for (int e = 0; e < 4; ++e) {
+            // features f and f + 1: cosines, and sines with the sign of the turn (or of the turn back)
+            const int f = f0 + 2 * e;
+            cs[e] = pair2(1.f, 1.f);
+            sn[e] = 0;
+            if constexpr (MODE == kNeighbours) {
+                if (f < a.rot) {
+                    const float2 x = sh_turn[warp][f >> 1];
+                    cs[e] = pair2(x.x, x.x);
+                    sn[e] = BWD ? pair2(x.y, -x.y) : pair2(-x.y, x.y);
+                }
+            } else if constexpr (MODE == kHalves) {
+                if (on) {
+                    const bool hi = f0 >= half;
+                    const float4 x = *reinterpret_cast<const float4*>(&sh_turn[warp][hi ? f - half : f]);
+                    cs[e] = pair2(x.x, x.z);
+                    sn[e] = hi != BWD ? pair2(x.y, x.w) : pair2(-x.y, -x.w);
+                }
+            } else {
+                float c2[2] = {1.f, 1.f}, s2[2] = {0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (f + k < a.rot) {
+                        const bool hi = f + k >= half;
+                        const float2 x = sh_turn[warp][hi ? f + k - half : f + k];
+                        c2[k] = x.x;
+                        s2[k] = hi != BWD ? x.y : -x.y;
+                    }
+                cs[e] = pair2(c2[0], c2[1]);
+                sn[e] = pair2(s2[0], s2[1]);
+            }
+            if constexpr (NORM && !BWD) {
+                // (with the weights of the features and of their partners)
+                auto partner = [&](int k) -> int {
+                    return k >= a.rot ? k : MODE == kNeighbours ? k ^ 1 : k < half ? k + half : k - half;
+                };
+                const float2 w = *reinterpret_cast<const float2*>(&sh_w[now][f]);
+                cs[e] = mul2(cs[e], pair2(w.x, w.y));
+                sn[e] = mul2(sn[e], pair2(sh_w[now][partner(f)], sh_w[now][partner(f + 1)]));
             }
         }
+        [[maybe_unused]] uint64_t w[4];
+        if constexpr (NORM && BWD)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = *reinterpret_cast<const float2*>(&sh_w[now][f0 + 2 * e]);
+                w[e] = pair2(x.x, x.y);
+            }
         __syncwarp();
+        fetch_pos(u + stride);
         // the lane that has the partners (halves: rot / 16 lanes on or back)
-        const int with = MODE == kHalves ? (f0 < half ? lane + half / 8 : f0 < a.rot ? lane - half / 8 : lane) : lane;
-        auto turned = [&](float (&y)[8]) {
-            float p[8];
+        [[maybe_unused]] const int with = MODE == kHalves && on ? (f0 < half ? lane + half / 8 : lane - half / 8) : lane;
+        [[maybe_unused]] const bool part = a.rot < HD;
+        // the partners' values; 0 where there is none, so that nothing of another feature comes in
+        auto partners = [&](const uint4& raw, const uint64_t (&y)[4], uint64_t (&p)[4]) {
             if constexpr (MODE == kNeighbours) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) p[e] = y[e ^ 1];
+                for (int e = 0; e < 4; ++e) p[e] = part && f0 + 2 * e >= a.rot ? 0 : pair2(hi2(y[e]), lo2(y[e]));
             } else if constexpr (MODE == kHalves) {
+                const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, y[e], with);
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t z = __shfl_sync(0xffffffffu, v[e], with);
+                    p[e] = unpack2<BF16>(part && !on ? 0u : z);
+                }
             } else {
                 __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sh_row[warp][sub][f0 + e] = y[e];
+                for (int e = 0; e < 4; ++e) {
+                    sh_row[warp][sub][f0 + 2 * e] = lo2(y[e]);
+                    sh_row[warp][sub][f0 + 2 * e + 1] = hi2(y[e]);
+                }
                 __syncwarp();
+                auto at = [&](int f) -> float { return f < a.rot ? sh_row[warp][sub][f < half ? f + half : f - half] : 0.f; };
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int f = f0 + e;
-                    p[e] = f < a.rot ? sh_row[warp][sub][f < half ? f + half : f - half] : 0.f;
-                }
+                for (int e = 0; e < 4; ++e) p[e] = pair2(at(f0 + 2 * e), at(f0 + 2 * e + 1));
             }
-            // (what is not rotated stays as it is, whatever its partner is)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = f0 + e < a.rot ? fmaf(y[e], cs[e], p[e] * sn[e]) : y[e];
         };
-        // ---- the heads
-        const uint16_t* xp = t.x + bi * t.x_stride[0] + j * t.x_stride[1] + f0;
-        const uint16_t* gp = t.g + bi * t.g_stride[0] + j * t.g_stride[1] + f0;
-        uint16_t* op = t.o + bi * t.o_stride[0] + j * t.o_stride[1] + f0;
-#pragma unroll 1
-        for (int h = first; h < last; h += HP * U) {
-            uint4 xr[U], gr[U];
+        auto work = [&](int h, const uint4 (&xr)[U], const uint4 (&gr)[U]) {
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                const int hh = h + k * HP + sub;
-                const bool in = real && hh < last;
-                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                xr[k] = (!BWD || NORM) && in ? *reinterpret_cast<const uint4*>(xp + hh * t.x_stride[2]) : z;
-                gr[k] = BWD && in ? *reinterpret_cast<const uint4*>(gp + hh * t.g_stride[2]) : z;
-            }
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int hh = h + k * HP + sub;
                 if (h + k * HP >= last) break;
-                float x[8], y[8], r = 1.f;
-                unpack8<BF16>(xr[k], x);
+                [[maybe_unused]] const uint32_t xw[4] = {xr[k].x, xr[k].y, xr[k].z, xr[k].w};
+                [[maybe_unused]] const uint32_t gw[4] = {gr[k].x, gr[k].y, gr[k].z, gr[k].w};
+                [[maybe_unused]] uint64_t x[4], y[4], p[4];
+                [[maybe_unused]] float r = 1.f;
+                if constexpr (!BWD || NORM)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = unpack2<BF16>(xw[e]);
                 if constexpr (NORM) {
-                    float ss = 0.f;
+                    uint64_t ss = mul2(x[0], x[0]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                    r = rsqrtf(fmaf(head_sum<LK>(ss), 1.f / HD, a.eps));
+                    for (int e = 1; e < 4; ++e) ss = fma2(x[e], x[e], ss);
+                    r = rsqrtf(fmaf(head_sum<LK>(lo2(ss) + hi2(ss)), 1.f / HD, a.eps));
                 }
+                [[maybe_unused]] const uint64_t r2 = pair2(r, r);
                 if constexpr (!BWD) {
+                    // y = r (x w cos + x' w' sin): the weights are in the cosines and sines
+                    partners(xr[k], x, p);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = NORM ? x[e] * r * w[e] : x[e];
-                    turned(y);
+                    for (int e = 0; e < 4; ++e) {
+                        y[e] = fma2(p[e], sn[e], mul2(x[e], cs[e]));
+                        if constexpr (NORM) y[e] = mul2(y[e], r2);
+                    }
                 } else {
-                    unpack8<BF16>(gr[k], y);
-                    turned(y);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = unpack2<BF16>(gw[e]);
+                    partners(gr[k], y, p);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = fma2(p[e], sn[e], mul2(y[e], cs[e]));
                     if constexpr (NORM) {
-                        float dot = 0.f;
+                        // y = u r w; dx = y - x r^2 mean(y x)
+                        uint64_t dot = 0;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            x[e] *= r;
-                            dw[e] = fmaf(y[e], x[e], dw[e]);
-                            y[e] *= w[e];
-                            dot = fmaf(y[e], x[e], dot);
+                        for (int e = 0; e < 4; ++e) {
+                            y[e] = mul2(y[e], r2);
+                            dw[e] = fma2(y[e], x[e], dw[e]);
+                            y[e] = mul2(y[e], w[e]);
+                            dot = fma2(y[e], x[e], dot);
                         }
-                        dot = head_sum<LK>(dot) * (1.f / HD);
+                        const float z = head_sum<LK>(lo2(dot) + hi2(dot)) * (1.f / HD) * -(r * r);
+                        const uint64_t z2 = pair2(z, z);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = r * fmaf(-x[e], dot, y[e]);
+                        for (int e = 0; e < 4; ++e) y[e] = fma2(x[e], z2, y[e]);
                     }
                 }
-                if (hh < last)
-                    *reinterpret_cast<uint4*>(op + hh * t.o_stride[2]) = real ? pack8<BF16>(y) : make_uint4(0u, 0u, 0u, 0u);
+                if (h + k * HP + sub < last)
+                    *reinterpret_cast<uint4*>(op) =
+                        real ? make_uint4(pack2<BF16>(y[0]), pack2<BF16>(y[1]), pack2<BF16>(y[2]), pack2<BF16>(y[3])) : make_uint4(0u, 0u, 0u, 0u);
+                op += HP * t.o_stride[2];
             }
+        };
+#pragma unroll 1
+        for (int h = first; h < last; h += 2 * HP * U) {
+            load(h + HP * U, xb, gb);
+            work(h, xa, ga);
+            load(h + 2 * HP * U, xa, ga);
+            work(h + HP * U, xb, gb);
         }
     }
+    flush(now);
+    };
+    tensor(std::integral_constant<int, 0>{}, units_q);
+    tensor(std::integral_constant<int, 1>{}, units);
     if constexpr (BWD && NORM) {
         // the CTA's sums: its warps', in order
-        if (n >= 0) flush();
         __syncthreads();
         for (int i = tid; i < 2 * HD; i += kRopeThreads) {
             float x = 0.f;
@@ -290,7 +392,7 @@ __global__ void __launch_bounds__(256) rope_sum_kernel(const __grid_constant__ R
 
 void rope_plan(RopeArgs& a, bool backward)
 {
-    const int resident = 152 * (backward ? V_BO : V_FO);
+    const int resident = 152 * (backward ? kRopeOcc<true> : kRopeOcc<false>);
     const int hp = 256 / a.d;
     // a warp for a token's queries and one for its keys, unless there are fewer of those than warps: then heads are shared out
     const int64_t warps = static_cast<int64_t>(resident) * kRopeWarps;
