@@ -582,11 +582,11 @@ __global__ void __launch_bounds__(kTileThreads<Q4>, 1) cache_fwd_tile_kernel(con
     };
     auto wait_warp = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(b, parity)); };
 
-    if constexpr (Q4) {
-        // the softmax groups' registers come out of the other warpgroups' (512 x 128 in all: 2 x 160 + 2 x 96)
-        if (warp >= kSoftWarp0 && warp < kSoftWarp0 + 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    }
+    // (4 bits: the softmax groups' registers come out of the other warpgroups', 512 x 128 in all: 2 x 152 + 2 x 104. Every
+    // warp of a warpgroup runs the same instruction, and it stands in the branch whose registers it sets: behind a branch
+    // that joins again the compiler has to take the lower number for all)
+    if (warp < kSoftWarp0 || warp >= kSoftWarp0 + 8) {
+    if constexpr (Q4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (Q4 && (warp < kMmaWarp || warp >= kSoftWarp0 + 8)) {
         if constexpr (Q4) {
             // warps 12 and 13 load; 0 and 1 convert K, 14 and 15 V: a scheduler has one of these besides the softmax
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(kTileThreads<Q4>, 1) cache_fwd_tile_kernel(con
             mbar_wait(bar(full0 + r % NS), (r / NS) & 1, tmo);
         }
         __syncwarp();
-    } else if (warp < kSoftWarp0) {
+    } else {
         // ------------------------------------------------------------ MMA issuer of slot `sl`
         constexpr uint32_t kIdS = idesc_f16(MB, 128, 64, false, false);
         constexpr uint32_t kIdPV = idesc_f16(MB, 128, HD, false, !Q4);      // (4 bits: V lies transposed)
@@ -837,8 +837,10 @@ __global__ void __launch_bounds__(kTileThreads<Q4>, 1) cache_fwd_tile_kernel(con
         mbar_wait(bar(tDrain + sl), 0, tmo);
         }
         __syncwarp();
+    }
     } else {
         // ------------------------------------------------------------ softmax and epilogue
+        if constexpr (Q4) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         const int sl = (warp - kSoftWarp0) >> 2;
         const int r = tid - (kSoftWarp0 + 4 * sl) * 32;     // index in the group
         // a warp reads the quarter of the TMEM lanes of its number modulo 4
