@@ -69,55 +69,65 @@ __global__ void __launch_bounds__(256, 3) cache4_append_kernel(const CacheAppend
         const uint32_t h_kv = static_cast<uint32_t>(a.c.h_kv), c = lane % LK, sub = lane / LK;
         const uint32_t first = static_cast<uint32_t>(s0) / KP, sets = static_cast<uint32_t>(s1 - 1) / KP - first + 1;
         const int64_t b0 = a.thd ? 0 : bi;
-        constexpr int U = 2;                            // sets whose loads are on their way together
-        for (uint32_t u = warp; u < sets * h_kv; u += warps * U) {
-            uint4 kx[U], vx[U];
-            uint8_t *kg[U], *vg[U];                     // the slots' groups, NULL: not a slot of this call
-            uint32_t x[U];
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const uint32_t uk = u + k * warps, set = uk / h_kv, g = uk - set * h_kv;
-                const uint32_t slot = (first + set) * KP + sub;
-                kx[k] = vx[k] = make_uint4(0u, 0u, 0u, 0u);
-                kg[k] = vg[k] = nullptr;
-                x[k] = slot & 1;
-                if (uk < sets * h_kv && slot >= s0 && slot < s1) {
-                    const int32_t i = static_cast<int32_t>(slot) - p.len;
-                    const int64_t src = p.src0 + (a.index ? a.index[bi * a.n + i] : i);
-                    kx[k] = ld_nc_v4(a.k + b0 * a.k_stride[0] + src * a.k_stride[1] + g * a.k_stride[2] + c * 8);
-                    vx[k] = ld_nc_v4(a.v + b0 * a.v_stride[0] + src * a.v_stride[1] + g * a.v_stride[2] + c * 8);
-                    uint32_t row;
-                    const int64_t page = cache_page(a.c, bi, slot, row);
-                    const int64_t at = static_cast<int64_t>(row >> 4) * Group4<HD>::kBytes;
-                    kg[k] = reinterpret_cast<uint8_t*>(a.c.k) + page * a.c.k_stride[0] + g * a.c.k_stride[2] + at;
-                    vg[k] = reinterpret_cast<uint8_t*>(a.c.v) + page * a.c.v_stride[0] + g * a.c.v_stride[2] + at;
-                    x[k] = row & 15;
-                }
+        // a warp takes all heads of its slots (which are looked up once then), a share of them where there are few slots
+        const uint32_t splits = max(1u, min(h_kv, warps / sets)), per = (h_kv + splits - 1) / splits;
+        constexpr int U = 2;                            // heads whose loads are on their way together
+        for (uint32_t u = warp; u < sets * splits; u += warps) {
+            const uint32_t set = u / splits, h0 = (u - set * splits) * per, h1 = min(h0 + per, h_kv);
+            const uint32_t slot = (first + set) * KP + sub;
+            const bool in = slot >= s0 && slot < s1;
+            const bool both = __shfl_xor_sync(0xffffffffu, in ? 1 : 0, LK) != 0 && in;
+            const uint16_t *kp = nullptr, *vp = nullptr;
+            uint8_t *kg = nullptr, *vg = nullptr;       // the slot's group of head 0
+            uint32_t row = 0;
+            if (in) {
+                const int32_t i = static_cast<int32_t>(slot) - p.len;
+                const int64_t src = p.src0 + (a.index ? a.index[bi * a.n + i] : i);
+                kp = a.k + b0 * a.k_stride[0] + src * a.k_stride[1] + c * 8;
+                vp = a.v + b0 * a.v_stride[0] + src * a.v_stride[1] + c * 8;
+                const int64_t page = cache_page(a.c, bi, slot, row);
+                const int64_t at = static_cast<int64_t>(row >> 4) * Group4<HD>::kBytes;
+                kg = reinterpret_cast<uint8_t*>(a.c.k) + page * a.c.k_stride[0] + at;
+                vg = reinterpret_cast<uint8_t*>(a.c.v) + page * a.c.v_stride[0] + at;
             }
+            const uint32_t x = row & 15;
+            const bool odd = slot & 1;
+            const uint32_t kw_at = k4_word<HD>(x, c), ks_at = k4_scale<HD>(x, c >> 1), vs_at = v4_scale<HD>(x, c >> 1);
+            // an even slot's lane writes both keys' first half words, the odd slot's the second ones
+            const uint32_t two_at = v4_half<HD>(x & ~1u, 2 * c + (odd ? 1 : 0)), one_at = v4_half<HD>(x, 2 * c);
+#pragma unroll 1
+            for (uint32_t h = h0; h < h1; h += U) {
+                uint4 kx[U], vx[U];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                uint32_t q[8];
-                const bool in = kg[k] != nullptr, odd = x[k] & 1;
-                const uint32_t ks = quantise8<BF16>(kx[k], q);
-                const uint32_t even4[4] = {q[0], q[2], q[4], q[6]}, odd4[4] = {q[1], q[3], q[5], q[7]};
-                const uint32_t kw = pack_word4(even4, odd4);
-                const uint32_t vs = quantise8<BF16>(vx[k], q);
-                const uint32_t lo4[4] = {q[0], q[1], q[2], q[3]}, hi4[4] = {q[4], q[5], q[6], q[7]};
-                const uint32_t vw = pack_word4(lo4, hi4);       // both half words of this key
-                // an even slot's lane writes both keys' first half words, the odd slot's the second ones
-                const uint32_t other = __shfl_xor_sync(0xffffffffu, vw, LK);
-                const bool both = __shfl_xor_sync(0xffffffffu, in ? 1 : 0, LK) != 0 && in;
-                if (!in) continue;
-                *reinterpret_cast<uint32_t*>(kg[k] + k4_word<HD>(x[k], c)) = kw;
-                if (both) {
-                    *reinterpret_cast<uint32_t*>(vg[k] + v4_half<HD>(x[k] & ~1u, 2 * c + (odd ? 1 : 0))) =
-                        odd ? __byte_perm(other, vw, 0x7632) : __byte_perm(vw, other, 0x5410);
-                } else {
-                    *reinterpret_cast<uint16_t*>(vg[k] + v4_half<HD>(x[k], 2 * c)) = static_cast<uint16_t>(vw);
-                    *reinterpret_cast<uint16_t*>(vg[k] + v4_half<HD>(x[k], 2 * c + 1)) = static_cast<uint16_t>(vw >> 16);
+                for (int k = 0; k < U; ++k) {
+                    const bool load = in && h + k < h1;
+                    kx[k] = load ? ld_nc_v4(kp + (h + k) * a.k_stride[2]) : make_uint4(0u, 0u, 0u, 0u);
+                    vx[k] = load ? ld_nc_v4(vp + (h + k) * a.v_stride[2]) : make_uint4(0u, 0u, 0u, 0u);
                 }
-                if (c & 1) vg[k][v4_scale<HD>(x[k], c >> 1)] = static_cast<uint8_t>(vs);
-                else kg[k][k4_scale<HD>(x[k], c >> 1)] = static_cast<uint8_t>(ks);
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    if (h + k >= h1) break;
+                    uint32_t q[8];
+                    const uint32_t ks = quantise8<BF16>(kx[k], q);
+                    const uint32_t even4[4] = {q[0], q[2], q[4], q[6]}, odd4[4] = {q[1], q[3], q[5], q[7]};
+                    const uint32_t kw = pack_word4(even4, odd4);
+                    const uint32_t vs = quantise8<BF16>(vx[k], q);
+                    const uint32_t lo4[4] = {q[0], q[1], q[2], q[3]}, hi4[4] = {q[4], q[5], q[6], q[7]};
+                    const uint32_t vw = pack_word4(lo4, hi4);       // both half words of this key
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, vw, LK);
+                    if (!in) continue;
+                    uint8_t* kh = kg + (h + k) * a.c.k_stride[2];
+                    uint8_t* vh = vg + (h + k) * a.c.v_stride[2];
+                    *reinterpret_cast<uint32_t*>(kh + kw_at) = kw;
+                    if (both) {
+                        *reinterpret_cast<uint32_t*>(vh + two_at) = odd ? __byte_perm(other, vw, 0x7632) : __byte_perm(vw, other, 0x5410);
+                    } else {
+                        *reinterpret_cast<uint16_t*>(vh + one_at) = static_cast<uint16_t>(vw);
+                        *reinterpret_cast<uint16_t*>(vh + one_at + 4) = static_cast<uint16_t>(vw >> 16);
+                    }
+                    if (c & 1) vh[vs_at] = static_cast<uint8_t>(vs);
+                    else kh[ks_at] = static_cast<uint8_t>(ks);
+                }
             }
         }
         const uint32_t nr = static_cast<uint32_t>(s1 - s0);
@@ -160,15 +170,15 @@ cudaError_t launch_cache4_append(const CacheAppendArgs& a0, int dtype, cudaStrea
 
 namespace {
 
-// Where an output row's key is: its sequence and slot, or slot -1 (zeros).
-struct ReadRow {
-    int64_t bi, slot;
+// The sequence of an output row, kept for the rows that follow: its first output row and the one behind its last, and
+// of row `first` + j the slot start + j for j < n.
+struct ReadSeq {
+    int64_t bi, first, end, start, n;
 };
 
-__device__ __forceinline__ ReadRow read_row(const CacheReadArgs& a, int64_t r)
+__device__ __forceinline__ ReadSeq read_seq(const CacheReadArgs& a, int64_t r)
 {
-    ReadRow x;
-    int64_t j, room;
+    ReadSeq x;
     if (a.offsets) {
         // the last sequence that begins at or in front of the row
         int64_t lo = 0, hi = a.c.b;
@@ -177,23 +187,26 @@ __device__ __forceinline__ ReadRow read_row(const CacheReadArgs& a, int64_t r)
             if (a.offsets[mid] <= r) lo = mid; else hi = mid;
         }
         x.bi = lo;
-        j = r - a.offsets[lo];
-        room = static_cast<int64_t>(a.offsets[lo + 1]) - a.offsets[lo];
-        if (j < 0 || j >= room) {
+        x.first = a.offsets[lo];
+        x.end = a.offsets[lo + 1];
+        if (r < x.first || r >= x.end) {        // (a row of no sequence: looked up alone)
             set_status(a.c.status, SDPA_ERR_BAD_LENGTHS);
-            x.slot = -1;
+            x.first = r;
+            x.end = r + 1;
+            x.n = 0;
             return x;
         }
     } else {
         x.bi = r / a.s;
-        j = r - x.bi * a.s;
-        room = a.s;
+        x.first = x.bi * a.s;
+        x.end = x.first + a.s;
     }
     bool bad;
-    const int64_t len = cache_length(a.c, x.bi, bad);
-    const int64_t start = a.start ? a.start[x.bi] : 0, n = a.counts ? a.counts[x.bi] : room;
-    if (start < 0 || start > len || n < 0 || n > room) set_status(a.c.status, SDPA_ERR_BAD_LENGTHS);
-    x.slot = start >= 0 && j < n && start + j < len ? start + j : -1;
+    const int64_t len = cache_length(a.c, x.bi, bad), room = x.end - x.first;
+    x.start = a.start ? a.start[x.bi] : 0;
+    x.n = a.counts ? a.counts[x.bi] : room;
+    if (x.start < 0 || x.start > len || x.n < 0 || x.n > room) set_status(a.c.status, SDPA_ERR_BAD_LENGTHS);
+    x.n = x.start < 0 ? 0 : imin64(x.n, len - x.start);
     return x;
 }
 
@@ -201,29 +214,43 @@ __device__ __forceinline__ ReadRow read_row(const CacheReadArgs& a, int64_t r)
 
 // A warp takes 2 (d = 64: 4) adjacent output rows, all heads or a share of them, a lane 8 features of K and of V.
 template <int HD, bool BF16, bool Q4>
-__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ CacheReadArgs a)
+__global__ void __launch_bounds__(256, 4) cache_read_kernel(const __grid_constant__ CacheReadArgs a)
 {
     constexpr uint32_t LK = HD / 8, KP = 32 / LK;
-    constexpr int U = 2;                                // heads whose loads are on their way together
+    constexpr int U = 3;                                // heads whose loads are on their way together
     const uint32_t lane = threadIdx.x & 31, c = lane % LK, sub = lane / LK;
     const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int64_t warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
     const int32_t h_kv = static_cast<int32_t>(a.c.h_kv);
     const int64_t units = (a.rows + KP - 1) / KP * a.splits;
+    // a warp's units follow one another: the look-ups of a sequence and of a page serve many rows
+    const int64_t u0 = warp * a.per_warp, u1 = imin64(units, u0 + a.per_warp);
+    ReadSeq x;
+    x.first = x.end = 0;
+    int64_t page = -1, page0 = -1;                      // of slots [page0, page0 + page_size)
     if (blockIdx.x == 0 && a.offsets) {
         // (rows of no sequence are found below; here offsets that do not ascend from 0 to the end)
         bool ok = a.offsets[0] == 0 && a.offsets[a.c.b] == a.rows;
         for (int64_t i = threadIdx.x; i < a.c.b; i += blockDim.x) ok = ok && a.offsets[i] <= a.offsets[i + 1];
         if (!ok) set_status(a.c.status, SDPA_ERR_BAD_LENGTHS);
     }
-    for (int64_t u = warp; u < units; u += warps) {
-        const int64_t set = u / a.splits, r = set * KP + sub;
+    for (int64_t u = u0; u < u1; ++u) {
+        const int64_t set = a.splits == 1 ? u : u / a.splits, r = set * KP + sub;
         const int32_t h0 = static_cast<int32_t>(u - set * a.splits) * a.per_split, h1 = min(h0 + a.per_split, h_kv);
         if (r >= a.rows) continue;
-        const ReadRow x = read_row(a, r);
-        uint32_t row = 0;
-        const int64_t page = x.slot < 0 ? -1 : cache_page(a.c, x.bi, static_cast<uint32_t>(x.slot), row);
-        const int64_t b0 = a.offsets ? 0 : r / a.s, j = a.offsets ? r : r - b0 * a.s;
+        if (r < x.first || r >= x.end) {
+            x = read_seq(a, r);
+            page0 = -1;
+        }
+        const bool held = r - x.first < x.n;            // (else zeros)
+        const int64_t slot = x.start + r - x.first;
+        if (held && (page0 < 0 || slot < page0 || slot >= page0 + a.c.page_size)) {
+            uint32_t at;
+            page = cache_page(a.c, x.bi, static_cast<uint32_t>(slot), at);
+            page0 = slot - at;
+        }
+        const bool there = held && page >= 0;
+        const uint32_t row = held ? static_cast<uint32_t>(slot - page0) : 0;
+        const int64_t b0 = a.offsets ? 0 : x.bi, j = a.offsets ? r : r - x.first;
         uint16_t* ko = a.k + b0 * a.k_stride[0] + j * a.k_stride[1] + c * 8;
         uint16_t* vo = a.v + b0 * a.v_stride[0] + j * a.v_stride[1] + c * 8;
         if constexpr (Q4) {
@@ -241,7 +268,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
                 for (int k = 0; k < U; ++k) {
                     kw[k] = ks[k] = vs[k] = 0u;
                     vw[k] = make_uint2(0u, 0u);
-                    if (page >= 0 && h + k < h1) {
+                    if (there && h + k < h1) {
                         const uint8_t* kg = kp + (h + k) * a.c.k_stride[2];
                         const uint8_t* vg = vp + (h + k) * a.c.v_stride[2];
                         kw[k] = *reinterpret_cast<const uint32_t*>(kg + kw_at);
@@ -286,7 +313,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
                 uint4 kx[U], vx[U];
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    const bool in = page >= 0 && h + k < h1;
+                    const bool in = there && h + k < h1;
                     kx[k] = in ? ld_nc_v4(kp + (h + k) * a.c.k_stride[2]) : make_uint4(0u, 0u, 0u, 0u);
                     vx[k] = in ? ld_nc_v4(vp + (h + k) * a.c.v_stride[2]) : make_uint4(0u, 0u, 0u, 0u);
                 }
@@ -314,7 +341,10 @@ cudaError_t launch_read(const CacheReadArgs& a0, cudaStream_t s)
     const int64_t splits = imax64(1, imin64(a.c.h_kv, most / sets));
     a.per_split = static_cast<int32_t>((a.c.h_kv + splits - 1) / splits);
     a.splits = static_cast<int32_t>((a.c.h_kv + a.per_split - 1) / a.per_split);
-    const int64_t ctas = imin64((sets * a.splits + 7) / 8, 152 * 6);
+    // (a warp's sets follow one another, 4 of them: 12 x 16484 rows of 6 heads 142 us; 16 of them 167, one 149)
+    const int64_t units = sets * a.splits;
+    a.per_warp = imax64(1, imin64(4, units / most));
+    const int64_t ctas = ((units + a.per_warp - 1) / a.per_warp + 7) / 8;
     cache_read_kernel<HD, BF16, Q4><<<static_cast<unsigned>(ctas), 256, 0, s>>>(a);
     return cudaGetLastError();
 }

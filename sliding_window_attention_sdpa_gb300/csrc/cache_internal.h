@@ -99,6 +99,7 @@ struct CacheReadArgs {
     uint16_t *k, *v;
     int64_t k_stride[3], v_stride[3];   // batch, token, head
     int32_t splits, per_split;          // a row's heads are shared between so many warps, so many each (set by the launcher)
+    int64_t per_warp;                   // rows' sets and shares of a warp
 };
 
 struct CacheWeighArgs {
