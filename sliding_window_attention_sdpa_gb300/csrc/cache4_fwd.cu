@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads4, Rows4Cfg<HD, NT>::kOcc) cache4_fwd_
                     mbar_arrive_expect_tx(bar, copies * bytes);
                 }
                 __syncwarp();
-                if (go && !(a.c.stall && sent == 1)) {       // (test hook: a step that never comes)
+                if (go && !(a.c.stall && sent == min(1, cached - 1))) {       // (test hook: a step that never comes)
                     const uint32_t row = a.c.page_table == nullptr ? j : cache_row(a.c, j);
                     bulk_load(dst + stage * C::kStage, pool + entry * st_page + static_cast<int64_t>(row >> 4) * Group4<HD>::kBytes, bytes,
                               bar);

@@ -474,6 +474,8 @@ sdpa_status_t sdpa_cache_read(const sdpa_cache* c, const sdpa_cache_read_params*
     if (thd && (p->total < 0 || p->total >= kMax31))
         return fail(SDPA_ERR_INVALID_ARG, "total=%lld: must be 0 to 2^31 - 1", (long long)p->total);
     if (thd && p->offsets == nullptr) return fail(SDPA_ERR_INVALID_ARG, "THD layout needs offsets");
+    if (thd && c->b == 0 && p->total > 0)
+        return fail(SDPA_ERR_INVALID_ARG, "total=%lld: there are no sequences", (long long)p->total);
     if ((st = check_strides("k", p->k_stride, thd ? 1 : 0)) != SDPA_OK) return st;
     if ((st = check_strides("v", p->v_stride, thd ? 1 : 0)) != SDPA_OK) return st;
     int dev = 0;
