@@ -2,10 +2,10 @@
 // bits and over each other: up to 16 rows of a kv-head in a unit.
 //
 // Rows, units, the line of tiles and its cut into parts are those of cache_fwd.cu. A
-// step of a warp is 64 keys (d = 64: 128), 9216 bytes of codes and scales in one run
-// for each 16 keys: bulk copies of up to a step's 4608 bytes of K and of V, as long as
-// a page allows, into the warp's own ring of three steps. The new tokens, in their
-// 16-bit form, are the unit's last step; one warp takes them from global memory.
+// step of a CTA is 256 keys, 64 for each of four warps; a fifth warp brings it, 64
+// keys (or as many as a page has in one run) a bulk copy, into a ring of two or more
+// steps. The new tokens, in their 16-bit form, are the unit's last 64 keys; one warp
+// takes them from global memory.
 //
 // The values come out of the codes as f16, exactly (cache4.cuh), straight into the
 // operand registers of m16n8k16:
@@ -17,6 +17,15 @@
 // below f16's last place is 2^-39 of that), and its scores by the inverse.
 // P is f16 for either type, with references as cache_fwd.cu has them for f16; for f16
 // output its remainder is a second product.
+//
+// Reading is 9/16 byte a feature, 25 us for 12 sequences of 16484 keys of 6 kv-heads, d =
+// 128 (8 rows: 47 us, 3.6 TB/s). Without the arithmetic the same kernel takes 42 us: 6 us
+// pass before the first keys are there, 6 in the join's launch and the join. With it,
+// no unit is near its rate (ALU 41 %, fp16 28 %, matrix unit 19 %, DRAM 48 % of the time), and
+// warps wait for operations that have just been issued. A ring for each warp instead
+// (three steps, no fifth warp: the copies' issue takes a warp some 600 cycles a step)
+// was as fast there, and took 55 us against 44 for 64 ragged sequences; twice as many
+// warps with half the step, 30 % more instructions, 50 us against 47.
 #include <type_traits>
 
 #include "cache4.cuh"
@@ -238,346 +247,347 @@ __global__ void __launch_bounds__(kThreads4, Rows4Cfg<HD, NT>::kOcc) cache4_fwd_
             }
             good = __all_sync(0xffffffffu, good);
         } else {
-        if (cur != bi) {
-            if (tid < 64) {
-                int bits;
-                sh_mask[tid] = admitted_tokens(a, bi, sv.nq, tid, bits);
-                sh_bits[tid] = bits;
-            }
-            if (tid < 2) sh_used[tid] = 0;
-            named_sync(1, 32 * kWarps4);
-            if (warp < 2) {
-                const uint64_t m = sh_mask[tid];
-                const uint32_t lo32 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m));
-                const uint32_t hi32 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m >> 32));
-                if (lane == 0) {
-                    atomicOr(&sh_used[0], lo32);
-                    atomicOr(&sh_used[1], hi32);
+            if (cur != bi) {
+                if (tid < 64) {
+                    int bits;
+                    sh_mask[tid] = admitted_tokens(a, bi, sv.nq, tid, bits);
+                    sh_bits[tid] = bits;
                 }
-            }
-            named_sync(1, 32 * kWarps4);
-            cur = bi;
-        }
-        auto step_x = [&](int32_t s) -> int32_t { return (tile0 + s) * TK + warp * GK; };
-        // ---- rows: masks and windows (rows 2t, 2t + 1)
-        int row_tok[NT][2];           // the row's token, -1: admits nothing
-        int32_t row_low[NT][2];       // lowest position in the row's window
-        int32_t low_max = INT32_MIN;  // the highest of them (this CTA's rows)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int rr = r0 + n * 8 + 2 * t + e;
-                const int tk = rr < R ? rr / a.group : 0;
-                const uint64_t m = rr < R ? sh_mask[tk] : 0;
-                row_tok[n][e] = m ? tk : -1;
-                row_low[n][e] = INT32_MIN;
-                if (a.window_left >= 0)
-                    row_low[n][e] = static_cast<int32_t>(
-                        imax64(INT32_MIN, imin64(INT32_MAX, npos + sh_bits[tk] - 1 - a.window_left)));
-                if (m) low_max = max(low_max, row_low[n][e]);
-            }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) low_max = max(low_max, __shfl_xor_sync(0xffffffffu, low_max, o));
-
-        // ---- Q in f16 (row g of each 8) and its factors (rows 2t, 2t + 1), while the first keys are on their way
-        uint32_t q[NT][KW][4];
-        float row_scale[NT][2];       // the row's scores to powers of two
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int r = r0 + n * 8 + g;
-            const int tok = r / a.group;
-            const bool real = r < R && tok < sv.nq;
-            const uint16_t* qp = a.q + bi * a.q_stride[0] + tok * a.q_stride[1] +
-                                 (gk * a.group + (r - tok * a.group)) * a.q_stride[2] + t * (HD / 4);
-#pragma unroll
-            for (int w = 0; w < KW; ++w) {
-                const uint4 x = real ? ld_nc_v4(qp + w * 8) : make_uint4(0u, 0u, 0u, 0u);
-                q[n][w][0] = x.x, q[n][w][1] = x.y, q[n][w][2] = x.z, q[n][w][3] = x.w;
-            }
-            float back = 1.f;
-            if constexpr (BF16) {
-                uint32_t most = 0;
-#pragma unroll
-                for (int w = 0; w < KW; ++w)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) most = max(most, max(q[n][w][j] & 0x7fffu, (q[n][w][j] >> 16) & 0x7fffu));
-                most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                const QScale4 scale = q_scale4(most);
-                back = scale.back;
-#pragma unroll
-                for (int w = 0; w < KW; ++w)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = unpack2<true>(q[n][w][j]);
-                        q[n][w][j] = pack2<false>(f.x * scale.mul, f.y * scale.mul);
+                if (tid < 2) sh_used[tid] = 0;
+                named_sync(1, 32 * kWarps4);
+                if (warp < 2) {
+                    const uint64_t m = sh_mask[tid];
+                    const uint32_t lo32 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m));
+                    const uint32_t hi32 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(m >> 32));
+                    if (lane == 0) {
+                        atomicOr(&sh_used[0], lo32);
+                        atomicOr(&sh_used[1], hi32);
                     }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                // (not 0: masked scores are -inf)
-                row_scale[n][e] = fmaxf(a.scale_log2 * __shfl_sync(0xffffffffu, back, (2 * t + e) * 4), 1e-38f);
-            }
-        }
-
-        float o[NT][MT][4];
-        float m[NT][2], l[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            m[n][0] = m[n][1] = -INFINITY;
-            l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
-        }
-
-        // The softmax of G groups' masked scores: references, sums, and P^T as the second product's operands (hi, and
-        // with SPLIT the remainders lo).
-        auto softmax = [&](auto& sc, auto& hi, auto& lo) {
-            constexpr int G = std::extent<std::remove_reference_t<decltype(sc)>, 1>::value;
-            float mx[NT][2];
-            bool up = false;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mx[n][0] = mx[n][1] = -INFINITY;
-#pragma unroll
-                for (int u = 0; u < G; ++u)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[n][e & 1] = fmaxf(mx[n][e & 1], sc[n][u][e]);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mx[n][e] *= row_scale[n][e];
-                    up = up || mx[n][e] > m[n][e] + kMoves<false>;
                 }
+                named_sync(1, 32 * kWarps4);
+                cur = bi;
             }
-            if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float al[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = mx[n][e];
-#pragma unroll
-                        for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
-                        x = fmaxf(x - kBelow<false>, m[n][e]);
-                        al[e] = m[n][e] == -INFINITY ? 0.f : ex2_approx(m[n][e] - x);
-                        m[n][e] = x;
-                        l[n][e] *= al[e];
-                    }
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[n][i][e] *= al[e & 1];
-                }
-            }
+            auto step_x = [&](int32_t s) -> int32_t { return (tile0 + s) * TK + warp * GK; };
+            // ---- rows: masks and windows (rows 2t, 2t + 1)
+            int row_tok[NT][2];           // the row's token, -1: admits nothing
+            int32_t row_low[NT][2];       // lowest position in the row's window
+            int32_t low_max = INT32_MIN;  // the highest of them (this CTA's rows)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int u = 0; u < G; ++u) {
-                    float p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // a masked score is -inf, its P is 0 (a row's reference is finite here, or 0)
-                        p[e] = ex2_approx(fmaf(sc[n][u][e], row_scale[n][e & 1], m[n][e & 1] == -INFINITY ? 0.f : -m[n][e & 1]));
-                        l[n][e & 1] += p[e];
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        hi[n][u][h] = pack2<false>(p[2 * h], p[2 * h + 1]);
-                        if constexpr (SPLIT) {
-                            const float2 f = unpack2<false>(hi[n][u][h]);
-                            lo[n][u][h] = movm_trans4(pack2<false>(p[2 * h] - f.x, p[2 * h + 1] - f.y));
-                        }
-                        hi[n][u][h] = movm_trans4(hi[n][u][h]);
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    const int rr = r0 + n * 8 + 2 * t + e;
+                    const int tk = rr < R ? rr / a.group : 0;
+                    const uint64_t m = rr < R ? sh_mask[tk] : 0;
+                    row_tok[n][e] = m ? tk : -1;
+                    row_low[n][e] = INT32_MIN;
+                    if (a.window_left >= 0)
+                        row_low[n][e] = static_cast<int32_t>(
+                            imax64(INT32_MIN, imin64(INT32_MAX, npos + sh_bits[tk] - 1 - a.window_left)));
+                    if (m) low_max = max(low_max, row_low[n][e]);
                 }
-        };
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) low_max = max(low_max, __shfl_xor_sync(0xffffffffu, low_max, o));
 
-#pragma unroll 1
-        for (int32_t s = 0; s < cached; ++s) {
-            const uint32_t st = stage;
-            const uint8_t* step = dyn + st * C::kStage + warp * C::kHalf;
-            if (good) {
-                good = __all_sync(0xffffffffu, mbar_wait(full + st * 8, par, a.timeout_ns));
-                if (!good) set_status(a.c.status, SDPA_ERR_TIMEOUT);
-            }
-            if (++stage == ST) stage = 0, par ^= 1;
-            if (!good) continue;
-            const int32_t x0 = step_x(s);
-            const bool all = sh_all[st] != 0;
-            uint32_t ok[OKW];
+            // ---- Q in f16 (row g of each 8) and its factors (rows 2t, 2t + 1), while the first keys are on their way
+            uint32_t q[NT][KW][4];
+            float row_scale[NT][2];       // the row's scores to powers of two
 #pragma unroll
-            for (int w = 0; w < OKW; ++w) ok[w] = all ? 0xffffffffu : sh_ok[st][warp * OKW + w];
-            if (all || (ok[0] | ok[1]) != 0) {
-            constexpr int KS = C::kSub;
-            auto okw = [&](int u) -> uint32_t { return u < 2 ? ok[0] : ok[1]; };
-            static_assert(OKW == 2, "");
-#pragma unroll 1
-            for (int u0 = 0; u0 < KG; u0 += KS) {
-            // S^T
-            float sc[NT][KS][4];
-#pragma unroll
-            for (int u = 0; u < KS; ++u) {
-                const uint8_t* grp = step + (u0 + u) * Group4<HD>::kBytes;
-                const Words4<HD> kw = words4<HD>(grp, lane);
-                const uint32_t x = k_scales4<HD>(grp, lane);
-                Scale4 ks[2][HD / 64];
-                ks[0][0] = scale4<0x0404>(x);
-                if constexpr (HD == 128) {
-                    ks[0][1] = scale4<0x1414>(x);
-                    ks[1][0] = scale4<0x2424>(x), ks[1][1] = scale4<0x3434>(x);
-                } else {
-                    ks[1][0] = scale4<0x1414>(x);
-                }
+            for (int n = 0; n < NT; ++n) {
+                const int r = r0 + n * 8 + g;
+                const int tok = r / a.group;
+                const bool real = r < R && tok < sv.nq;
+                const uint16_t* qp = a.q + bi * a.q_stride[0] + tok * a.q_stride[1] +
+                                     (gk * a.group + (r - tok * a.group)) * a.q_stride[2] + t * (HD / 4);
 #pragma unroll
                 for (int w = 0; w < KW; ++w) {
-                    uint32_t k0[4], k1[4];
-                    values4(kw.w[0][w], ks[0][w / 2], k0);
-                    values4(kw.w[1][w], ks[1][w / 2], k1);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (w == 0) mma_f16_first(sc[n][u], k0[0], k1[0], k0[1], k1[1], q[n][w][0], q[n][w][1]);
-                        else mma_f16(sc[n][u], k0[0], k1[0], k0[1], k1[1], q[n][w][0], q[n][w][1]);
-                        mma_f16(sc[n][u], k0[2], k1[2], k0[3], k1[3], q[n][w][2], q[n][w][3]);
-                    }
+                    const uint4 x = real ? ld_nc_v4(qp + w * 8) : make_uint4(0u, 0u, 0u, 0u);
+                    q[n][w][0] = x.x, q[n][w][1] = x.y, q[n][w][2] = x.z, q[n][w][3] = x.w;
                 }
-            }
-            // masks (a step whose keys are all there and in every row's window needs none; rows that admit nothing
-            // are left out at the end)
-            const bool windowed = a.window_left >= 0 && (kpos != nullptr || sv.lo + x0 < low_max);
-            if (!all || windowed) {
+                float back = 1.f;
+                if constexpr (BF16) {
+                    uint32_t most = 0;
 #pragma unroll
-                for (int u = 0; u < KS; ++u)
+                    for (int w = 0; w < KW; ++w)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int x = (u0 + u) * 16 + kappa + 2 * h, j = sv.lo + x0 + x;
-                        const bool in = (okw(u0 + u) >> (x & 31)) & 1;
-                        const int32_t pos = in && kpos ? kpos[j] : j;
+                        for (int j = 0; j < 4; ++j) most = max(most, max(q[n][w][j] & 0x7fffu, (q[n][w][j] >> 16) & 0x7fffu));
+                    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                    most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                    const QScale4 scale = q_scale4(most);
+                    back = scale.back;
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                    for (int w = 0; w < KW; ++w)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (!in || (windowed && pos < row_low[n][e])) sc[n][u][2 * h + e] = -INFINITY;
-                    }
-            }
-            uint32_t hi[NT][KS][2], lo[NT][KS][2];
-            softmax(sc, hi, lo);
-            // O^T += V^T P^T
-#pragma unroll
-            for (int u = 0; u < KS; ++u) {
-                const uint8_t* grp = step + C::kStage / 2 + (u0 + u) * Group4<HD>::kBytes;
-                const Words4<HD> vw = words4<HD>(grp, lane);
-                uint32_t x = v_scales4<HD>(grp, lane);
-                // what stands in the place of a key that does not count meets a P of 0: its scale has to be 0
-                if (!all) x &= (((okw(u0 + u) >> (((u0 + u) & 1) * 16 + 4 * t)) & 15) * 0x00204081u & 0x01010101u) * 255u;
-                const Scale4 v0 = scale4<0x1404>(x), v1 = scale4<0x3424>(x);
-#pragma unroll
-                for (int w = 0; w < KW; ++w) {
-                    uint32_t r0[4], r1[4];
-                    values4(vw.w[0][w], v0, r0);
-                    values4(vw.w[1][w], v1, r1);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            mma_f16(o[n][w * 2 + p], r0[2 * p], r0[2 * p + 1], r1[2 * p], r1[2 * p + 1], hi[n][u][0], hi[n][u][1]);
-                            if constexpr (SPLIT)
-                                mma_f16(o[n][w * 2 + p], r0[2 * p], r0[2 * p + 1], r1[2 * p], r1[2 * p + 1], lo[n][u][0], lo[n][u][1]);
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 f = unpack2<true>(q[n][w][j]);
+                            q[n][w][j] = pack2<false>(f.x * scale.mul, f.y * scale.mul);
                         }
                 }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    // (not 0: masked scores are -inf)
+                    row_scale[n][e] = fmaxf(a.scale_log2 * __shfl_sync(0xffffffffu, back, (2 * t + e) * 4), 1e-38f);
+                }
             }
-            }
-            }
-            // the stage is free when all four warps are done with it
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + st * 8);
-        }
 
-        // ---- the new tokens, 16 at a time, by the warp whose step they are; of those that no row admits (they may hold
-        // anything) nothing is read
-        // (they begin with a warp's step, perhaps in a CTA's step that has cached keys as well)
-        const int32_t sn = (sv.new0 / GK - tile0 * kWarps4 - warp) / kWarps4;
-        if (sv.new0 >= step_x(0) && sn < nt && step_x(sn) == sv.new0) {
-            const uint16_t* kn = a.k + bi * a.k_stride[0] + gk * a.k_stride[2] + t * (HD / 4);
-            const uint16_t* vn = a.v + bi * a.v_stride[0] + gk * a.v_stride[2] + g * (HD / 8);
-#pragma unroll 1
-            for (int w0 = 0; w0 < sv.nq; w0 += 16) {
-                float sc[NT][1][4];
+            float o[NT][MT][4];
+            float m[NT][2], l[NT][2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) sc[n][0][0] = sc[n][0][1] = sc[n][0][2] = sc[n][0][3] = 0.f;
-                auto there = [&](int w) -> bool { return w < sv.nq && (sh_used[w >> 5] >> (w & 31)) & 1; };
-                const bool in0 = there(w0 + kappa), in1 = there(w0 + kappa + 2);
+            for (int n = 0; n < NT; ++n) {
+                m[n][0] = m[n][1] = -INFINITY;
+                l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-                for (int w = 0; w < KW; ++w) {
-                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                    const uint4 x = in0 ? ld_nc_v4(kn + (w0 + kappa) * a.k_stride[1] + w * 8) : z;
-                    const uint4 y = in1 ? ld_nc_v4(kn + (w0 + kappa + 2) * a.k_stride[1] + w * 8) : z;
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+            }
+
+            // The softmax of G groups' masked scores: references, sums, and P^T as the second product's operands (hi, and
+            // with SPLIT the remainders lo).
+            auto softmax = [&](auto& sc, auto& hi, auto& lo) {
+                constexpr int G = std::extent<std::remove_reference_t<decltype(sc)>, 1>::value;
+                float mx[NT][2];
+                bool up = false;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mx[n][0] = mx[n][1] = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < G; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mx[n][e & 1] = fmaxf(mx[n][e & 1], sc[n][u][e]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        mx[n][e] *= row_scale[n][e];
+                        up = up || mx[n][e] > m[n][e] + kMoves<false>;
+                    }
+                }
+                if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        mma_f16(sc[n][0], to_f16x2<BF16>(x.x), to_f16x2<BF16>(y.x), to_f16x2<BF16>(x.y), to_f16x2<BF16>(y.y),
-                                q[n][w][0], q[n][w][1]);
-                        mma_f16(sc[n][0], to_f16x2<BF16>(x.z), to_f16x2<BF16>(y.z), to_f16x2<BF16>(x.w), to_f16x2<BF16>(y.w),
-                                q[n][w][2], q[n][w][3]);
+                        float al[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = mx[n][e];
+#pragma unroll
+                            for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+                            x = fmaxf(x - kBelow<false>, m[n][e]);
+                            al[e] = m[n][e] == -INFINITY ? 0.f : ex2_approx(m[n][e] - x);
+                            m[n][e] = x;
+                            l[n][e] *= al[e];
+                        }
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[n][i][e] *= al[e & 1];
                     }
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint64_t rm = row_tok[n][e & 1] < 0 ? 0 : sh_mask[row_tok[n][e & 1]];
-                        if (!((rm >> (w0 + kappa + 2 * (e >> 1))) & 1)) sc[n][0][e] = -INFINITY;
+                    for (int u = 0; u < G; ++u) {
+                        float p[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            // a masked score is -inf, its P is 0 (a row's reference is finite here, or 0)
+                            p[e] = ex2_approx(fmaf(sc[n][u][e], row_scale[n][e & 1], m[n][e & 1] == -INFINITY ? 0.f : -m[n][e & 1]));
+                            l[n][e & 1] += p[e];
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            hi[n][u][h] = pack2<false>(p[2 * h], p[2 * h + 1]);
+                            if constexpr (SPLIT) {
+                                const float2 f = unpack2<false>(hi[n][u][h]);
+                                lo[n][u][h] = movm_trans4(pack2<false>(p[2 * h] - f.x, p[2 * h + 1] - f.y));
+                            }
+                            hi[n][u][h] = movm_trans4(hi[n][u][h]);
+                        }
                     }
-                uint32_t hi[NT][1][2], lo[NT][1][2];
-                softmax(sc, hi, lo);
-                // V: 8 features at a time of the keys 4t .. 4t + 3
+            };
+
+#pragma unroll 1
+            for (int32_t s = 0; s < cached; ++s) {
+                const uint32_t st = stage;
+                const uint8_t* step = dyn + st * C::kStage + warp * C::kHalf;
+                if (good) {
+                    good = __all_sync(0xffffffffu, mbar_wait(full + st * 8, par, a.timeout_ns));
+                    if (!good) set_status(a.c.status, SDPA_ERR_TIMEOUT);
+                }
+                if (++stage == ST) stage = 0, par ^= 1;
+                if (!good) continue;
+                const int32_t x0 = step_x(s);
+                const bool all = sh_all[st] != 0;
+                uint32_t ok[OKW];
 #pragma unroll
-                for (int c = 0; c < HD / 64; ++c) {
-                    uint32_t v[4][4];
+                for (int w = 0; w < OKW; ++w) ok[w] = all ? 0xffffffffu : sh_ok[st][warp * OKW + w];
+                if (all || (ok[0] | ok[1]) != 0) {
+                    constexpr int KS = C::kSub;
+                    auto okw = [&](int u) -> uint32_t { return u < 2 ? ok[0] : ok[1]; };
+                    static_assert(OKW == 2, "");
+#pragma unroll 1
+                    for (int u0 = 0; u0 < KG; u0 += KS) {
+                        // S^T
+                        float sc[NT][KS][4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int w = w0 + 4 * t + k;
-                        const uint4 x = there(w) ? ld_nc_v4(vn + w * a.v_stride[1] + c * 8) : make_uint4(0u, 0u, 0u, 0u);
-                        v[k][0] = to_f16x2<BF16>(x.x), v[k][1] = to_f16x2<BF16>(x.y);
-                        v[k][2] = to_f16x2<BF16>(x.z), v[k][3] = to_f16x2<BF16>(x.w);
+                        for (int u = 0; u < KS; ++u) {
+                            const uint8_t* grp = step + (u0 + u) * Group4<HD>::kBytes;
+                            const Words4<HD> kw = words4<HD>(grp, lane);
+                            const uint32_t x = k_scales4<HD>(grp, lane);
+                            Scale4 ks[2][HD / 64];
+                            ks[0][0] = scale4<0x0404>(x);
+                            if constexpr (HD == 128) {
+                                ks[0][1] = scale4<0x1414>(x);
+                                ks[1][0] = scale4<0x2424>(x), ks[1][1] = scale4<0x3434>(x);
+                            } else {
+                                ks[1][0] = scale4<0x1414>(x);
+                            }
+#pragma unroll
+                            for (int w = 0; w < KW; ++w) {
+                                uint32_t k0[4], k1[4];
+                                values4(kw.w[0][w], ks[0][w / 2], k0);
+                                values4(kw.w[1][w], ks[1][w / 2], k1);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    if (w == 0) mma_f16_first(sc[n][u], k0[0], k1[0], k0[1], k1[1], q[n][w][0], q[n][w][1]);
+                                    else mma_f16(sc[n][u], k0[0], k1[0], k0[1], k1[1], q[n][w][0], q[n][w][1]);
+                                    mma_f16(sc[n][u], k0[2], k1[2], k0[3], k1[3], q[n][w][2], q[n][w][3]);
+                                }
+                            }
+                        }
+                        // masks (a step whose keys are all there and in every row's window needs none; rows that admit nothing
+                        // are left out at the end)
+                        const bool windowed = a.window_left >= 0 && (kpos != nullptr || sv.lo + x0 < low_max);
+                        if (!all || windowed) {
+#pragma unroll
+                            for (int u = 0; u < KS; ++u)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int x = (u0 + u) * 16 + kappa + 2 * h, j = sv.lo + x0 + x;
+                                    const bool in = (okw(u0 + u) >> (x & 31)) & 1;
+                                    const int32_t pos = in && kpos ? kpos[j] : j;
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                        for (int e = 0; e < 2; ++e)
+                                            if (!in || (windowed && pos < row_low[n][e])) sc[n][u][2 * h + e] = -INFINITY;
+                                }
+                        }
+                        uint32_t hi[NT][KS][2], lo[NT][KS][2];
+                        softmax(sc, hi, lo);
+                        // O^T += V^T P^T
+#pragma unroll
+                        for (int u = 0; u < KS; ++u) {
+                            const uint8_t* grp = step + C::kStage / 2 + (u0 + u) * Group4<HD>::kBytes;
+                            const Words4<HD> vw = words4<HD>(grp, lane);
+                            uint32_t x = v_scales4<HD>(grp, lane);
+                            // what stands in the place of a key that does not count meets a P of 0: its scale has to be 0
+                            if (!all) x &= (((okw(u0 + u) >> (((u0 + u) & 1) * 16 + 4 * t)) & 15) * 0x00204081u & 0x01010101u) * 255u;
+                            const Scale4 v0 = scale4<0x1404>(x), v1 = scale4<0x3424>(x);
+#pragma unroll
+                            for (int w = 0; w < KW; ++w) {
+                                uint32_t f0[4], f1[4];
+                                values4(vw.w[0][w], v0, f0);
+                                values4(vw.w[1][w], v1, f1);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                    for (int p = 0; p < 2; ++p) {
+                                        mma_f16(o[n][w * 2 + p], f0[2 * p], f0[2 * p + 1], f1[2 * p], f1[2 * p + 1], hi[n][u][0],
+                                                hi[n][u][1]);
+                                        if constexpr (SPLIT)
+                                            mma_f16(o[n][w * 2 + p], f0[2 * p], f0[2 * p + 1], f1[2 * p], f1[2 * p + 1], lo[n][u][0],
+                                                lo[n][u][1]);
+                                    }
+                            }
+                        }
                     }
+                }
+                // the stage is free when all four warps are done with it
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + st * 8);
+            }
+
+            // ---- the new tokens, 16 at a time, by the warp whose step they are (they begin with a warp's step, perhaps in a
+            // CTA's step that has cached keys as well); of those that no row admits, which may hold anything, nothing is read
+            const int32_t sn = (sv.new0 / GK - tile0 * kWarps4 - warp) / kWarps4;
+            if (sv.new0 >= step_x(0) && sn < nt && step_x(sn) == sv.new0) {
+                const uint16_t* kn = a.k + bi * a.k_stride[0] + gk * a.k_stride[2] + t * (HD / 4);
+                const uint16_t* vn = a.v + bi * a.v_stride[0] + gk * a.v_stride[2] + g * (HD / 8);
+#pragma unroll 1
+                for (int w0 = 0; w0 < sv.nq; w0 += 16) {
+                    float sc[NT][1][4];
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const uint32_t a0 = __byte_perm(v[0][p], v[1][p], 0x5410), a1 = __byte_perm(v[0][p], v[1][p], 0x7632);
-                        const uint32_t a2 = __byte_perm(v[2][p], v[3][p], 0x5410), a3 = __byte_perm(v[2][p], v[3][p], 0x7632);
+                    for (int n = 0; n < NT; ++n) sc[n][0][0] = sc[n][0][1] = sc[n][0][2] = sc[n][0][3] = 0.f;
+                    auto there = [&](int w) -> bool { return w < sv.nq && (sh_used[w >> 5] >> (w & 31)) & 1; };
+                    const bool in0 = there(w0 + kappa), in1 = there(w0 + kappa + 2);
+#pragma unroll
+                    for (int w = 0; w < KW; ++w) {
+                        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                        const uint4 x = in0 ? ld_nc_v4(kn + (w0 + kappa) * a.k_stride[1] + w * 8) : z;
+                        const uint4 y = in1 ? ld_nc_v4(kn + (w0 + kappa + 2) * a.k_stride[1] + w * 8) : z;
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            mma_f16(o[n][c * 4 + p], a0, a1, a2, a3, hi[n][0][0], hi[n][0][1]);
-                            if constexpr (SPLIT) mma_f16(o[n][c * 4 + p], a0, a1, a2, a3, lo[n][0][0], lo[n][0][1]);
+                            mma_f16(sc[n][0], to_f16x2<BF16>(x.x), to_f16x2<BF16>(y.x), to_f16x2<BF16>(x.y), to_f16x2<BF16>(y.y),
+                                    q[n][w][0], q[n][w][1]);
+                            mma_f16(sc[n][0], to_f16x2<BF16>(x.z), to_f16x2<BF16>(y.z), to_f16x2<BF16>(x.w), to_f16x2<BF16>(y.w),
+                                    q[n][w][2], q[n][w][3]);
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint64_t rm = row_tok[n][e & 1] < 0 ? 0 : sh_mask[row_tok[n][e & 1]];
+                            if (!((rm >> (w0 + kappa + 2 * (e >> 1))) & 1)) sc[n][0][e] = -INFINITY;
+                        }
+                    uint32_t hi[NT][1][2], lo[NT][1][2];
+                    softmax(sc, hi, lo);
+                    // V: 8 features at a time of the keys 4t .. 4t + 3
+#pragma unroll
+                    for (int c = 0; c < HD / 64; ++c) {
+                        uint32_t v[4][4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int w = w0 + 4 * t + k;
+                            const uint4 x = there(w) ? ld_nc_v4(vn + w * a.v_stride[1] + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+                            v[k][0] = to_f16x2<BF16>(x.x), v[k][1] = to_f16x2<BF16>(x.y);
+                            v[k][2] = to_f16x2<BF16>(x.z), v[k][3] = to_f16x2<BF16>(x.w);
+                        }
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const uint32_t a0 = __byte_perm(v[0][p], v[1][p], 0x5410), a1 = __byte_perm(v[0][p], v[1][p], 0x7632);
+                            const uint32_t a2 = __byte_perm(v[2][p], v[3][p], 0x5410), a3 = __byte_perm(v[2][p], v[3][p], 0x7632);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                mma_f16(o[n][c * 4 + p], a0, a1, a2, a3, hi[n][0][0], hi[n][0][1]);
+                                if constexpr (SPLIT) mma_f16(o[n][c * 4 + p], a0, a1, a2, a3, lo[n][0][0], lo[n][0][1]);
+                            }
                         }
                     }
                 }
             }
-        }
 
-        // ---- the CTA's warps join their rows
-        named_sync(1, 32 * kWarps4);
+            // ---- the CTA's warps join their rows
+            named_sync(1, 32 * kWarps4);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float x = l[n][e];
+                for (int e = 0; e < 2; ++e) {
+                    float x = l[n][e];
 #pragma unroll
-                for (int w = 4; w < 32; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-                const int r = n * 8 + 2 * t + e;
-                const bool live = row_tok[n][e] >= 0;
-                if (g == 0) {
-                    sh_m[warp][r] = live ? m[n][e] : -INFINITY;
-                    sh_l[warp][r] = live ? x : 0.f;
+                    for (int w = 4; w < 32; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+                    const int r = n * 8 + 2 * t + e;
+                    const bool live = row_tok[n][e] >= 0;
+                    if (g == 0) {
+                        sh_m[warp][r] = live ? m[n][e] : -INFINITY;
+                        sh_l[warp][r] = live ? x : 0.f;
+                    }
+                    float* dst = &sh_o[warp][r][g * (HD / 8)];
+#pragma unroll
+                    for (int p = 0; p < MT; ++p) {
+                        dst[2 * p] = live ? o[n][p][e] : 0.f;
+                        dst[2 * p + 1] = live ? o[n][p][2 + e] : 0.f;
+                    }
                 }
-                float* dst = &sh_o[warp][r][g * (HD / 8)];
-#pragma unroll
-                for (int p = 0; p < MT; ++p) {
-                    dst[2 * p] = live ? o[n][p][e] : 0.f;
-                    dst[2 * p + 1] = live ? o[n][p][2 + e] : 0.f;
-                }
-            }
         }
         __syncthreads();
         const bool whole = nt == sv.tiles;

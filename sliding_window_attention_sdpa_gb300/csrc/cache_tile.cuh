@@ -180,6 +180,19 @@ __device__ __forceinline__ int32_t seg_tiles(const Seg& g, int32_t tiles)
 
 // ---- a cache in 4 bits
 //
+// K and V tiles are made in shared memory, as f16, out of the codes: two warps bring
+// them as they are held, two turn K's and two V's (a warp 32 keys of each tile). Q is
+// f16 as well (see cache4_fwd.cu). 12 sequences of 16484 keys, 6 kv-heads, d = 128: 24
+// rows 131 us, 128 rows 136, 256 rows 172, 296 rows 299; of 16 bits 105, 112, 138, 235.
+//
+// Below 128 rows the turning warps' chain is the bound (about 2000 cycles a tile: wait,
+// load, 200 operations, store, fence), above it that of the softmax groups beside it.
+// What costs most there is instructions: with K's and V's turning as functions of their
+// own (more code between the same loops, fewer registers spilled) 296 rows took 370 to
+// 520 us, with all warps' registers set behind one branch (and softmax spilling) 381.
+// Setting them takes whole warpgroups: warps 0-3 and 12-15 the lower number, 4-11 the
+// higher. A softmax of 32 columns at a time: 334 us.
+//
 // A tile's columns (keys of S, and of P and V) are in the order in which V's values come out of their groups in runs of
 // 16 bytes: of each 32 keys, column 8 t + 4 q + e is key 16 q + 4 t + e. V lies transposed, its row 8 i + rho(g) is
 // feature i of lane row g's run of d / 8, rho(g) chosen so that the lanes of a store meet no bank twice.
@@ -589,7 +602,7 @@ __global__ void __launch_bounds__(kTileThreads<Q4>, 1) cache_fwd_tile_kernel(con
     if constexpr (Q4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (Q4 && (warp < kMmaWarp || warp >= kSoftWarp0 + 8)) {
         if constexpr (Q4) {
-            // warps 12 and 13 load; 0 and 1 convert K, 14 and 15 V: a scheduler has one of these besides the softmax
+            // warps 12 and 13 load; 0 and 1 turn K, 14 and 15 V: each of the four schedulers has one of these beside the softmax
             if (warp == kSoftWarp0 + 8 || warp == kSoftWarp0 + 9) tile_load4<HD, POS>(ta, walk, sm, warp & 1, lane);
             else tile_convert4<HD, BF16, POS>(ta, walk, sm, warp >= kSoftWarp0, warp & 1, lane);
         }

@@ -33,7 +33,7 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 
-// CTAs on an SM: more leave too few registers for two batches (backward with 3: 413 us against 288 for 28 k packed rows of
+// CTAs on an SM: more leave too few registers for two batches (backward with 3: 413 us against 288 for 38 k packed rows of
 // 54 heads), fewer too few loads on their way
 template <bool BWD>
 constexpr int kRopeOcc = BWD ? 2 : 3;
@@ -174,6 +174,13 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeOcc<BWD>) rope_kernel(const
         const int first = static_cast<int>(un - row * a.splits[now]) * a.per_split, last = min(first + a.per_split, t.heads);
         const int64_t bi = a.s == a.rows ? 0 : static_cast<uint32_t>(row) / static_cast<uint32_t>(a.s), j = row - bi * a.s;
         const bool real = a.seq_lens == nullptr || j < a.seq_lens[bi];
+        if (!real) {
+            // padding: zeros, and nothing read
+            fetch_pos(u + stride);
+            uint16_t* op = t.o + bi * t.o_stride[0] + j * t.o_stride[1] + f0;
+            for (int h = first + sub; h < last; h += HP) *reinterpret_cast<uint4*>(op + h * t.o_stride[2]) = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+        }
         // ---- the heads' loads: a batch of U sets is on its way while the one before is worked on, the first one during the
         // token's turns
         const int64_t head0 = first + sub;
@@ -184,7 +191,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeOcc<BWD>) rope_kernel(const
         auto load = [&](int h, uint4 (&xr)[U], uint4 (&gr)[U]) {
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                const bool in = real && h + k * HP + sub < last;
+                const bool in = h + k * HP + sub < last;
                 const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                 if constexpr (!BWD || NORM) {
                     xr[k] = in ? *reinterpret_cast<const uint4*>(xp) : z;
@@ -340,7 +347,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeOcc<BWD>) rope_kernel(const
                 }
                 if (h + k * HP + sub < last)
                     *reinterpret_cast<uint4*>(op) =
-                        real ? make_uint4(pack2<BF16>(y[0]), pack2<BF16>(y[1]), pack2<BF16>(y[2]), pack2<BF16>(y[3])) : make_uint4(0u, 0u, 0u, 0u);
+                        make_uint4(pack2<BF16>(y[0]), pack2<BF16>(y[1]), pack2<BF16>(y[2]), pack2<BF16>(y[3]));
                 op += HP * t.o_stride[2];
             }
         };
