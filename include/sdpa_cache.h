@@ -120,7 +120,8 @@ size_t sdpa_cache_evict_params_bytes(void);
  * as they will be held; all products are of f16 numbers: bf16 rows of q are scaled
  * by a power of two for them, the new tokens' k and v are rounded to f16 (which
  * changes none between 2^-17 and 65504 in magnitude; beyond, 65504 counts). P is
- * f16, with its remainder for f16 output in units of up to 16 rows of a kv-head.
+ * f16, with its remainder for f16 output where a kv-head has up to 32 rows (d =
+ * 64: 80).
  * Keys on pages out of range are left out; lengths out of [0, capacity] are
  * taken as the nearer end. Not read, or without effect whatever they hold, are
  * slots behind a sequence's keys, keys that no row's window has, and new tokens

@@ -55,7 +55,7 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t (&c)[8])
 
 // A warp takes 2 (d = 64: 4) adjacent slots, a lane 8 features of K and of V, head
 // after head. Bound by its operations, some 125 for 16 values, with 60 % of the issue
-// slots busy: prompts of 16 sequences (68,000 rows of 8 kv-heads, d = 128) 90 us, of
+// slots busy: prompts of 16 sequences (68,000 rows of 8 kv-heads, d = 128) 84 us, of
 // 52 for their bytes. Two heads' loads are on their way, with 4 CTAs on an SM: one head
 // takes 12 us more, four with 2 CTAs 20; looking rows up for each head took 123.
 template <int HD, bool BF16>
@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(256, 4) cache4_append_kernel(const CacheAppend
         const uint32_t first = static_cast<uint32_t>(s0) / KP, sets = static_cast<uint32_t>(s1 - 1) / KP - first + 1;
         const int64_t b0 = a.thd ? 0 : bi;
         // a warp takes all heads of its slots (which are looked up once then), a share of them where there are few slots
+        // (48 sequences of 1 to 5 rows, 8 heads of d = 64, 6.2 us, 9.4 without shares)
         const uint32_t splits = max(1u, min(h_kv, warps / sets)), per = (h_kv + splits - 1) / splits;
         constexpr int U = 2;                            // heads whose loads are on their way together
         for (uint32_t u = warp; u < sets * splits; u += warps) {
@@ -354,7 +355,7 @@ cudaError_t launch_read(const CacheReadArgs& a0, cudaStream_t s)
     CacheReadArgs a = a0;
     constexpr int64_t KP = 256 / HD;
     // a warp takes all heads of its rows (which are looked up once then), a share of them where there are fewer rows than
-    // warps that fit
+    // warps that fit (4 x 128 rows, 8 heads of d = 64, 5.6 us, 10.3 without shares)
     const int64_t sets = (a.rows + KP - 1) / KP, most = 152 * 48;
     const int64_t splits = imax64(1, imin64(a.c.h_kv, most / sets));
     a.per_split = static_cast<int32_t>((a.c.h_kv + splits - 1) / splits);

@@ -239,15 +239,18 @@ struct FwdLayout {
 // GB300 (152 SMs), fewer if there are fewer tiles; each has two partials. One
 // sequence of 16 kv-heads, d = 64, one row each: 301 keys 7.8 us whole, 8.8 and
 // a join of 1.5 cut; 900 keys 13.4 whole, 7.6 and 4.1 cut; 1800 keys 20.5 whole,
-// 8.0 and 3.4 cut.
-constexpr int64_t kWholeKeys = 512;
-constexpr int64_t kWholeKeys4 = 1024;
+// 8.0 and 3.4 cut. A cache in 4 bits, calls as timed from the host: that shape
+// with 301, 900, 1800 keys 12.4, 14.3, 17.4 us whole and 15.4, 16.6, 17.4 cut; its
+// tile kernel (6 kv-heads of 296 rows, d = 128) 28.7, 38.6, 51.8 whole and 33.8,
+// 37.1, 37.9 cut, 12 such sequences 32.9, 43.0, 59.7 whole and 57.3, 70.3, 87.0 cut.
+constexpr int64_t kWholeKeys = 512, kWholeKeys4 = 2048, kWholeKeys4Tiles = 1024;
 
 FwdLayout fwd_layout(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa::CacheFwdPlan& plan)
 {
     FwdLayout l{};
     const FwdSize z = fwd_size(c, p, plan);
-    if (z.tiles * plan.tile <= (c->bits == 4 ? kWholeKeys4 : kWholeKeys) && z.units < double(kMax31)) {
+    const int64_t whole = c->bits != 4 ? kWholeKeys : plan.variant == swa::kQ4Tiles ? kWholeKeys4Tiles : kWholeKeys4;
+    if (z.tiles * plan.tile <= whole && z.units < double(kMax31)) {
         l.parts = static_cast<int32_t>(z.units);
         l.whole = 1;
         return l;
@@ -476,11 +479,12 @@ sdpa_status_t sdpa_cache_read(const sdpa_cache* c, const sdpa_cache_read_params*
     if (thd && p->offsets == nullptr) return fail(SDPA_ERR_INVALID_ARG, "THD layout needs offsets");
     if (thd && c->b == 0 && p->total > 0)
         return fail(SDPA_ERR_INVALID_ARG, "total=%lld: there are no sequences", (long long)p->total);
+    const int64_t rows = c->b == 0 ? 0 : thd ? p->total : c->b * p->s;
+    if (rows >= int64_t(1) << 36) return fail(SDPA_ERR_UNSUPPORTED, "b * s = %lld: at most 2^36 - 1 rows", (long long)rows);
     if ((st = check_strides("k", p->k_stride, thd ? 1 : 0)) != SDPA_OK) return st;
     if ((st = check_strides("v", p->v_stride, thd ? 1 : 0)) != SDPA_OK) return st;
     int dev = 0;
     if ((st = current_device(&dev)) != SDPA_OK) return st;
-    const int64_t rows = c->b == 0 ? 0 : thd ? p->total : c->b * p->s;
     const Ptr ptrs[] = {{"k", p->k, rows > 0, 16},
                         {"v", p->v, rows > 0, 16},
                         {"start", p->start, false, 4},

@@ -401,7 +401,8 @@ void rope_plan(RopeArgs& a, bool backward)
 {
     const int resident = 152 * (backward ? kRopeOcc<true> : kRopeOcc<false>);
     const int hp = 256 / a.d;
-    // a warp for a token's queries and one for its keys, unless there are fewer of those than warps: then heads are shared out
+    // a warp for a token's queries and one for its keys, unless there are fewer of those than warps: then heads are shared
+    // out (48 + 6 heads of d = 128, one token 6.4 us, 12 for a warp that has all; 64 tokens 7.0 and 12.8)
     const int64_t warps = static_cast<int64_t>(resident) * kRopeWarps;
     const int64_t sets = (static_cast<int64_t>(a.t[0].heads) + hp - 1) / hp + (static_cast<int64_t>(a.t[1].heads) + hp - 1) / hp;
     const int64_t shares = a.rows > 0 ? imax64(1, imin64(warps / a.rows, sets)) : 1;
@@ -446,6 +447,8 @@ cudaError_t launch_mode(const RopeArgs& a, bool backward, cudaStream_t s)
     const bool norm = a.t[0].weight != nullptr;
     if (a.interleaved || a.rot == 0)
         return norm ? launch_norm<HD, BF16, kNeighbours, true>(a, backward, s) : launch_norm<HD, BF16, kNeighbours, false>(a, backward, s);
+    // a lane's partner features are another lane's own 8 (16 x 4096 tokens, all of d = 128 turned, 170 us; through shared
+    // memory, as for halves that end inside 8 features, 335)
     if (a.rot % 16 == 0)
         return norm ? launch_norm<HD, BF16, kHalves, true>(a, backward, s) : launch_norm<HD, BF16, kHalves, false>(a, backward, s);
     return norm ? launch_norm<HD, BF16, kAnyHalves, true>(a, backward, s) : launch_norm<HD, BF16, kAnyHalves, false>(a, backward, s);

@@ -70,6 +70,11 @@ def test_read_refusals(bits, kw, code, needle):
     assert swa.sdpa_cache_read(cache4() if bits == 4 else cache(bits=bits), None, 0) == INVALID
 
 
+def test_read_refuses_more_rows_than_a_launch_has():
+    for c in (cache4(b=1 << 20), cache(b=1 << 20)):
+        refused(UNSUP, swa.sdpa_cache_read(c, read(s=1 << 20), 0), "rows")
+
+
 def test_workspace_follows_the_work():
     """None for short units (one CTA each), else two partials of a part's rows."""
     assert swa.sdpa_cache_fwd_workspace_bytes(cache4(max_pages=20), fwd()) == 0 and swa.last_error() == ""

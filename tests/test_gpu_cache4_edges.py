@@ -39,6 +39,10 @@ FORMS = {
     "tile_padding": ([90, 10, 300], 45, 3, 1, 128, "bf16", 16, 30, dict(tree=True, empty=0.4)),
     "rows_positions": ([1700, 300, 5], 3, 4, 2, 128, "bf16", 32, 150, dict(tree=True, evicted=True)),
     "one_long": ([40000], 1, 4, 2, 64, "f16", 128, -1, {}),
+    "rows_positions_cut": ([3700, 300, 5], 3, 4, 2, 128, "bf16", 32, 150, dict(tree=True, evicted=True)),
+    "rows_ragged_cut": ([4000, 0, 90, 2500], 4, 8, 2, 128, "f16", 64, -1, dict(q_lens=[4, 0, 1, 3], sink=True)),
+    "d64_rows_window_cut": ([9000, 300], 2, 8, 2, 64, "bf16", 16, 5000, {}),
+    "d64_rows_padding_cut": ([6000, 17], 4, 8, 2, 64, "f16", 48, -1, dict(tree=True, empty=0.4)),
 }
 
 
