@@ -121,7 +121,7 @@ size_t sdpa_cache_evict_params_bytes(void);
  * by a power of two for them, the new tokens' k and v are rounded to f16 (which
  * changes none between 2^-17 and 65504 in magnitude; beyond, 65504 counts). P is
  * f16, with its remainder for f16 output where a kv-head has up to 32 rows (d =
- * 64: 80).
+ * 64: 64).
  * Keys on pages out of range are left out; lengths out of [0, capacity] are
  * taken as the nearer end. Not read, or without effect whatever they hold, are
  * slots behind a sequence's keys, keys that no row's window has, and new tokens

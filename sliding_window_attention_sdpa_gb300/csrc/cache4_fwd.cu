@@ -665,13 +665,13 @@ cudaError_t launch_fwd4(const CacheTileArgs& qa, cudaStream_t s)
 
 // Rows per kv-head above which the tile kernel is ahead, though the blocks of 16
 // rows below read K and V again each (12 sequences of 16484 keys, 6 kv-heads):
-// d = 128, 32 rows 109 us against 131, 48 rows 154 against 131; d = 64, 80 rows 127 us
-// against 150, 96 rows 151 against 150. A unit's cost in tiles of 256 keys (64 ragged
+// d = 128, 32 rows 109 us against 131, 48 rows 154 against 131; d = 64, 48 rows 83 us
+// against 106, 64 rows 106 and 106, 80 rows 126 against 106. A unit's cost in tiles of 256 keys (64 ragged
 // sequences of 5 to 16484 keys, 8 rows): 61, 49, 45, 48, 54 us at 1, 2, 3, 4, 6; in
 // the tile kernel's of 64 (24 rows): 214, 178, 166 at 4, 8, 16.
 CacheFwdPlan cache4_fwd_plan(int64_t d, int64_t rows)
 {
-    if (rows > (d == 128 ? 32 : 80)) return CacheFwdPlan{kQ4Tiles, 256, 64, 1, 16};
+    if (rows > (d == 128 ? 32 : 64)) return CacheFwdPlan{kQ4Tiles, 256, 64, 1, 16};
     if (d == 128) return rows <= 8 ? CacheFwdPlan{kQ4Rows128x8, 8, kTile4, 2, 3} : CacheFwdPlan{kQ4Rows128x16, 16, kTile4, 2, 3};
     return rows <= 8 ? CacheFwdPlan{kQ4Rows64x8, 8, kTile4, 2, 3} : CacheFwdPlan{kQ4Rows64x16, 16, kTile4, 2, 3};
 }

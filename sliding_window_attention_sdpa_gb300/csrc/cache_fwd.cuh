@@ -276,9 +276,9 @@ struct Part {
 };
 
 // Cuts the line of all sequences' tiles (tiles_of(i), each more than 0) into
-// one part per CTA, fewer if there are fewer tiles. Every thread calls it; sh
-// has a place per warp, sh_at two.
-template <int THREADS, class F>
+// one part per CTA, fewer if there are fewer tiles; a part has LEAST places at
+// least. Every thread calls it; sh has a place per warp, sh_at two.
+template <int THREADS, int LEAST = 1, class F>
 __device__ __forceinline__ Part find_part(int64_t b, F tiles_of, int64_t* sh, int64_t* sh_at)
 {
     constexpr int W = THREADS / 32;
@@ -288,7 +288,7 @@ __device__ __forceinline__ Part find_part(int64_t b, F tiles_of, int64_t* sh, in
     int64_t s = mine;
     for (int64_t i = tid + THREADS; i < b; i += THREADS) s += tiles_of(i);
     p.line.total = block_sum64<THREADS>(s, sh);
-    p.parts = imin64(gridDim.x, p.line.total);
+    p.parts = imin64(gridDim.x, p.line.total / LEAST);
     if (blockIdx.x >= p.parts) return p;
     p.at = p.line.start(blockIdx.x, p.parts);
     p.end = p.line.start(blockIdx.x + 1, p.parts);
@@ -342,16 +342,18 @@ __device__ __forceinline__ Segment segment_at(int64_t rem, int32_t tiles, int32_
 
 // Names the join's work for a segment of g.n > 0 tiles of unit `un` (of
 // `tiles`) of sequence bi; `pos0` is the place of the unit's tile 0 in the line
-// (one thread calls it, for each segment of a part). `units`: per sequence.
+// (one thread calls it, for each segment of a part). `units`: per sequence. A
+// tile may take w places; the part with the last of them has it.
 __device__ __forceinline__ void name_cut(const CacheFwdArgs& a, const Part& p, bool first_of_part, int64_t pos0, int32_t cost,
-                                         int64_t bi, int64_t un, int64_t units, int32_t tile0, int32_t n, int32_t tiles)
+                                         int64_t bi, int64_t un, int64_t units, int32_t tile0, int32_t n, int32_t tiles,
+                                         int32_t w = 1)
 {
     if (a.cut_by_unit ? tile0 != 0 : !first_of_part || tile0 == 0) return;
     CacheFwdCut cut{-1, 0, 0, 0, 0};
-    const int64_t first = p.line.part_of(pos0, p.parts);
+    const int64_t first = p.line.part_of(pos0 + w - 1, p.parts);
     if (n != tiles)
-        cut = CacheFwdCut{bi, un, static_cast<int32_t>(first), static_cast<int32_t>(p.line.part_of(pos0 + tiles - 1, p.parts)),
-                          p.line.start(first, p.parts) >= pos0 - cost ? 0 : 1};
+        cut = CacheFwdCut{bi, un, static_cast<int32_t>(first), static_cast<int32_t>(p.line.part_of(pos0 + int64_t(tiles) * w - 1, p.parts)),
+                          p.line.start(first, p.parts) >= pos0 - cost * w ? 0 : 1};
     if (a.cut_by_unit) a.cuts[bi * units + un] = cut;
     // by part (a part's entry holds no cut at first): the one right behind the unit's first part names it
     else if (first + 1 == blockIdx.x) a.cuts[blockIdx.x] = cut;

@@ -101,12 +101,17 @@ struct Shape {
     int64_t per_head;
 };
 
-__device__ __forceinline__ Shape shape_of(const SeqView& v, int na, int nb, int32_t cost, bool pairs)
+template <int HD, bool Q4>
+struct Walk;
+
+template <int HD, bool Q4>
+__device__ __forceinline__ Shape shape_of(const SeqView& v, int na, int nb, int32_t cost)
 {
+    using W = Walk<HD, Q4>;
     Shape s;
     s.ta = v.tiles;
-    s.tb = pairs ? (v.tiles + 1) >> 1 : v.tiles;
-    s.per_head = static_cast<int64_t>(na) * (s.ta + 2 * cost) + static_cast<int64_t>(nb) * (s.tb + cost);
+    s.tb = Q4 ? v.tiles : (v.tiles + 1) >> 1;
+    s.per_head = static_cast<int64_t>(na) * ((s.ta + 2 * cost) * W::kTwo) + static_cast<int64_t>(nb) * ((s.tb + cost) * W::kOne);
     return s;
 }
 
@@ -125,21 +130,35 @@ __device__ __forceinline__ SeqView tile_view(const CacheFwdArgs& a, int64_t bi)
     else return seq_view(a, bi, kKeys, kKeys);
 }
 
-template <bool Q4>
+// A CTA's way through its part of the line.
+template <int HD, bool Q4>
 struct Walk {
+    static constexpr int kTwo = 1, kOne = 1;      // places of a step with two row tiles, with one
     int64_t at, end, bi, rem;
     int na, nb;
     SeqView sv;
     Shape sh;
     bool loaded;
 
+    __device__ __forceinline__ void begin(const CacheFwdArgs&, const Part& p, int na_, int nb_)
+    {
+        na = na_;
+        nb = nb_;
+        at = p.at;
+        end = p.end;
+        bi = p.bi;
+        rem = p.rem;
+    }
+    // Changes from segment to segment; the place of a segment's unit's tile 0.
+    __device__ __forceinline__ int64_t mark() const { return at; }
+    __device__ __forceinline__ int64_t tile0_place(const Part&, const Seg& g) const { return at + g.line_n - g.step0 - g.steps; }
     // The next segment with steps; false at the part's end.
     __device__ __forceinline__ bool next(const CacheFwdArgs& a, Seg& g)
     {
         if (at >= end) return false;
         if (!loaded) {
             sv = tile_view<Q4>(a, bi);
-            sh = shape_of(sv, na, nb, a.unit_cost, !Q4);
+            sh = shape_of<HD, Q4>(sv, na, nb, a.unit_cost);
             loaded = true;
         }
         g.bi = bi;
@@ -168,6 +187,75 @@ struct Walk {
     }
 };
 
+// Over a cache in 4 bits, d = 64: a step with one row tile takes 3/4 of the time of one
+// with two, and so of the places. It steps from unit to unit, without divisions: fewer
+// instructions in each role. 12 sequences of 16484 keys, 6 kv-heads, 296 rows 232 us, 272
+// with even places, 300 by the form above; d = 128 307 by this form, 302 by that (24 rows
+// 154 and 135), and the places as they are are even there.
+template <>
+struct Walk<64, true> {
+    static constexpr int kTwo = 4, kOne = 3;
+    int64_t left;                 // places
+    int32_t bi, gk, blk, y;       // y: the place among the unit's
+    int na, nb;
+    SeqView sv;
+    bool loaded;
+
+    static __device__ __forceinline__ int32_t places(bool two) { return two ? kTwo : kOne; }
+
+    __device__ __forceinline__ void begin(const CacheFwdArgs& a, const Part& p, int na_, int nb_)
+    {
+        na = na_;
+        nb = nb_;
+        left = p.end - p.at;
+        bi = static_cast<int32_t>(p.bi);
+        sv = tile_view<true>(a, bi);
+        loaded = true;
+        const Shape sh = shape_of<64, true>(sv, na, nb, a.unit_cost);
+        gk = static_cast<int32_t>(quotient(p.rem, sh.per_head));
+        const int64_t r = p.rem - gk * sh.per_head;
+        const int32_t each = (sh.ta + 2 * a.unit_cost) * kTwo;
+        blk = static_cast<int32_t>(imin64(na, quotient(r, each)));
+        y = static_cast<int32_t>(r - static_cast<int64_t>(blk) * each);
+    }
+    __device__ __forceinline__ int64_t mark() const { return left; }
+    __device__ __forceinline__ int64_t tile0_place(const Part& p, const Seg& g) const
+    {
+        return p.end - left - y + g.cost * places(g.two);
+    }
+    __device__ __forceinline__ bool next(const CacheFwdArgs& a, Seg& g)
+    {
+        if (left <= 0) return false;
+        if (!loaded) {
+            sv = tile_view<true>(a, bi);
+            loaded = true;
+        }
+        g.bi = bi;
+        g.gk = gk;
+        g.blk = blk;
+        g.two = blk < na;
+        g.of = sv.tiles;
+        g.cost = (g.two ? 2 : 1) * a.unit_cost;
+        const int32_t w = places(g.two);
+        g.line_n = static_cast<int32_t>(imin64((g.of + g.cost) * w - y, left));
+        g.step0 = max(0, y / w - g.cost);
+        g.steps = max(0, (y + g.line_n) / w - g.cost) - g.step0;
+        return g.steps > 0;
+    }
+    __device__ __forceinline__ void advance(const CacheFwdArgs& a, const Seg& g)
+    {
+        left -= g.line_n;
+        if (left <= 0) return;
+        y = 0;                    // (only a part's end is inside a unit)
+        if (++blk < na + nb) return;
+        blk = 0;
+        if (++gk < a.c.h_kv) return;
+        gk = 0;
+        ++bi;
+        loaded = false;
+    }
+};
+
 // Key tiles of a segment: one for each step with two row tiles, two with one
 // (the unit's last step may have only one).
 template <bool Q4>
@@ -184,6 +272,7 @@ __device__ __forceinline__ int32_t seg_tiles(const Seg& g, int32_t tiles)
 // them as they are held, two turn K's and two V's (a warp 32 keys of each tile). Q is
 // f16 as well (see cache4_fwd.cu). 12 sequences of 16484 keys, 6 kv-heads, d = 128: 24
 // rows 131 us, 128 rows 136, 256 rows 172, 296 rows 299; of 16 bits 105, 112, 138, 235.
+// d = 64: 128 rows 106, 296 rows 234.
 //
 // Below 128 rows the turning warps' chain is the bound (about 2000 cycles a tile: wait,
 // load, 200 operations, store, fence), above it that of the softmax groups beside it.
@@ -226,7 +315,7 @@ __device__ __forceinline__ bool wait_warp4(const CacheFwdArgs& a, uint32_t bar, 
 // Brings the tiles of K (is_v: V) of cached keys as they are held into a ring of raw stages, by bulk copies of as many
 // keys as a page and a tile allow, and says which keys count. It runs ahead over the ends of units.
 template <int HD, bool POS>
-__device__ __forceinline__ void tile_load4(const CacheTileArgs& ta, Walk<true> walk, uint8_t* sm, bool is_v, int lane)
+__device__ __forceinline__ void tile_load4(const CacheTileArgs& ta, Walk<HD, true> walk, uint8_t* sm, bool is_v, int lane)
 {
     const CacheFwdArgs& a = ta.f;
     using C = TileCfg<HD, true>;
@@ -320,7 +409,7 @@ __device__ __forceinline__ void tile_load4(const CacheTileArgs& ta, Walk<true> w
 // Turns 32 keys (half p) of every tile of K (is_v: V) into f16 in the 128-byte swizzle. The new tokens' tile comes from
 // their 16-bit form.
 template <int HD, bool BF16, bool POS>
-__device__ __forceinline__ void tile_convert4(const CacheTileArgs& ta, Walk<true> walk, uint8_t* sm, bool is_v, int p, int lane)
+__device__ __forceinline__ void tile_convert4(const CacheTileArgs& ta, Walk<HD, true> walk, uint8_t* sm, bool is_v, int p, int lane)
 {
     const CacheFwdArgs& a = ta.f;
     using C = TileCfg<HD, true>;
@@ -510,30 +599,27 @@ __global__ void __launch_bounds__(kTileThreads<Q4>, 1) cache_fwd_tile_kernel(con
     const int blocks = (R + 255) / 256;
     const int nb = (R - 1) % 256 < 128 ? 1 : 0;   // the last block has one row tile
     const int na = blocks - nb;
-    Walk<Q4> walk{};
-    walk.na = na;
-    walk.nb = nb;
+    using W = Walk<HD, Q4>;
     Part part{1, 0, 0, 0, 0, Line{0}};
     if (a.whole) {
         const int64_t units = a.c.h_kv * blocks;
         part.bi = blockIdx.x / units;
         const int64_t un = blockIdx.x - part.bi * units, gk = un / blocks, blk = un - gk * blocks;
-        const Shape s = shape_of(tile_view<Q4>(a, part.bi), na, nb, a.unit_cost, !Q4);
-        part.rem = gk * s.per_head + blk * (s.ta + 2 * a.unit_cost) + (blk < na ? 2 : 1) * a.unit_cost;
-        part.end = blk < na ? s.ta : s.tb;
+        const Shape s = shape_of<HD, Q4>(tile_view<Q4>(a, part.bi), na, nb, a.unit_cost);
+        const int w = blk < na ? W::kTwo : W::kOne;
+        part.rem = gk * s.per_head + blk * (s.ta + 2 * a.unit_cost) * W::kTwo + (blk < na ? 2 : 1) * a.unit_cost * w;
+        part.end = static_cast<int64_t>(blk < na ? s.ta : s.tb) * w;
     } else {
-        part = find_part<kTileThreads<Q4>>(
-            a.c.b, [&](int64_t i) { return a.c.h_kv * shape_of(tile_view<Q4>(a, i), na, nb, a.unit_cost, !Q4).per_head; }, sh_sum, sh_at);
+        part = find_part<kTileThreads<Q4>, W::kTwo>(
+            a.c.b, [&](int64_t i) { return a.c.h_kv * shape_of<HD, Q4>(tile_view<Q4>(a, i), na, nb, a.unit_cost).per_head; }, sh_sum, sh_at);
         if (tid == 0 && !a.cut_by_unit) a.cuts[blockIdx.x].bi = -1;
         if (part.end == 0) {
             grid_dep_launch();
             return;
         }
     }
-    walk.at = part.at;
-    walk.end = part.end;
-    walk.bi = part.bi;
-    walk.rem = part.rem;
+    W walk{};
+    walk.begin(a, part, na, nb);
 
     if (tid == 0) {
         misc[1] = misc[2] = 0;
@@ -865,7 +951,7 @@ __global__ void __launch_bounds__(kTileThreads<Q4>, 1) cache_fwd_tile_kernel(con
         uint8_t* bits = reinterpret_cast<uint8_t*>(misc + 16);            // and its mask's number of bits
         uint32_t it0 = 0, cnt = 0;            // ring index at the segment's start; this slot's key tiles so far
         bool ok = true;
-        const int64_t part0 = walk.at;
+        const int64_t part0 = walk.mark();
         uint32_t segs = 0;
         Seg g;
         while (walk.next(a, g)) {
@@ -878,8 +964,8 @@ __global__ void __launch_bounds__(kTileThreads<Q4>, 1) cache_fwd_tile_kernel(con
                 bits[r] = static_cast<uint8_t>(n);
             }
             if (sl == 0 && r == 0 && !a.whole)
-                name_cut(a, part, walk.at == part0, walk.at + g.line_n - g.step0 - g.steps, g.cost, g.bi,
-                         g.gk * blocks + g.blk, a.c.h_kv * blocks, g.step0, g.steps, g.of);
+                name_cut(a, part, walk.mark() == part0, walk.tile0_place(part, g), g.cost, g.bi, g.gk * blocks + g.blk,
+                         a.c.h_kv * blocks, g.step0, g.steps, g.of, g.two ? W::kTwo : W::kOne);
             // this thread's row
             const int rr = g.blk * 256 + (g.two ? sl * 128 : 0) + row;
             const int tok = rr < R ? rr / a.group : 0;
@@ -1052,7 +1138,7 @@ __global__ void __launch_bounds__(kTileThreads<Q4>, 1) cache_fwd_tile_kernel(con
             // two row tiles: each slot its rows; one: both slots the same rows,
             // each half of the features, from both slots' sums
             const bool whole = g.steps == g.of;
-            const int64_t slot = blockIdx.x * int64_t(2) + (walk.at == part0 ? 0 : 1);
+            const int64_t slot = blockIdx.x * int64_t(2) + (walk.mark() == part0 ? 0 : 1);
             const int urow = (g.two ? sl * 128 : 0) + row;         // row in the unit
             float top = m, sum = l, f0 = 1.f, f1 = 0.f;
             if (!g.two) {

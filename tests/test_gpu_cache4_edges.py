@@ -43,6 +43,12 @@ FORMS = {
     "rows_ragged_cut": ([4000, 0, 90, 2500], 4, 8, 2, 128, "f16", 64, -1, dict(q_lens=[4, 0, 1, 3], sink=True)),
     "d64_rows_window_cut": ([9000, 300], 2, 8, 2, 64, "bf16", 16, 5000, {}),
     "d64_rows_padding_cut": ([6000, 17], 4, 8, 2, 64, "f16", 48, -1, dict(tree=True, empty=0.4)),
+    "d64_rows_64": ([2300, 300], 8, 8, 1, 64, "f16", 64, -1, dict(tree=True)),
+    "d64_rows_65": ([2300, 300], 13, 5, 1, 64, "bf16", 16, 90, dict(tree=True)),
+    "d64_tiles_both": ([3900, 0, 130, 64], 37, 16, 2, 64, "bf16", 64, -1, dict(tree=True)),
+    "d64_tiles_both_f16": ([6000, 500], 33, 8, 1, 64, "f16", 16, 4000, dict(sink=True)),
+    "d64_tiles_three": ([2500, 1, 300], 60, 10, 1, 64, "bf16", 32, -1, dict(q_lens=[60, 3, 0])),
+    "d64_tiles_many": ([1500, 70, 0, 900, 2500, 64, 65], 40, 14, 2, 64, "f16", 48, -1, {}),
 }
 
 
