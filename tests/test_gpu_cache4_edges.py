@@ -49,6 +49,13 @@ FORMS = {
     "d64_tiles_both_f16": ([6000, 500], 33, 8, 1, 64, "f16", 16, 4000, dict(sink=True)),
     "d64_tiles_three": ([2500, 1, 300], 60, 10, 1, 64, "bf16", 32, -1, dict(q_lens=[60, 3, 0])),
     "d64_tiles_many": ([1500, 70, 0, 900, 2500, 64, 65], 40, 14, 2, 64, "f16", 48, -1, {}),
+    # units of one step and of many in one part; more sequences than a CTA has threads
+    "short_cut_rows": ([3, 60, 64, 65, 1, 0, 7, 130, 20, 5] * 6 + [2300], 1, 8, 2, 128, "bf16", 64, -1, {}),
+    "short_cut_blocks": ([3, 60, 64, 65, 1, 0, 7, 130, 20, 5] * 6 + [2300], 3, 8, 1, 64, "f16", 16, -1, dict(tree=True)),
+    "short_cut_tiles": ([3, 60, 1, 0, 130, 5, 64, 65] * 5 + [1300], 37, 8, 1, 64, "bf16", 16, -1, dict(tree=True)),
+    "short_cut_tiles_d128": ([3, 60, 1, 0, 130, 5, 64, 65] * 5 + [1300], 37, 8, 1, 128, "f16", 64, -1, {}),
+    "b_200_cut": ([(37 * i) % 40 for i in range(200)] + [2300], 1, 2, 1, 64, "bf16", 64, -1, {}),
+    "b_520_tiles_cut": ([(37 * i) % 40 for i in range(520)] + [1100], 9, 8, 1, 64, "bf16", 64, -1, {}),
 }
 
 
