@@ -12,7 +12,7 @@
  * Pair i is (i, i + rot / 2), or (2 i, 2 i + 1) if `interleaved`; features from rot
  * on are not rotated. pos is the token's position on axis[i] (one axis: text; time,
  * height and width: video). Angles are exact products of the int32 position and
- * the fp32 frequency, to 2^-24 of a turn, however far the position.
+ * the fp32 frequency, to 2^-24 of a turn, however far the position (|freq| up to 2^50).
  *
  * Backward, with g the gradient of y and u = R^T g:
  *     dx = r (u w' - x r^2 mean(u w' x)),  w' = w + weight_offset

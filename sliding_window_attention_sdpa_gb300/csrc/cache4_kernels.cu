@@ -54,7 +54,7 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t (&c)[8])
 }  // namespace
 
 // A warp takes 2 (d = 64: 4) adjacent slots, a lane 8 features of K and of V, head
-// after head. Bound by its operations, some 125 for 16 values, with 60 % of the issue
+// after head. Bound by its operations, some 125 for 16 values, with 73 % of the issue
 // slots busy: prompts of 16 sequences (68,000 rows of 8 kv-heads, d = 128) 84 us, of
 // 52 for their bytes. Two heads' loads are on their way, with 4 CTAs on an SM: one head
 // takes 12 us more, four with 2 CTAs 20; looking rows up for each head took 123.

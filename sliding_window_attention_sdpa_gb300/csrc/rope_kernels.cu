@@ -14,7 +14,7 @@
 //
 // Angles: a frequency is held as its 64-bit fraction of a turn a position, so that
 // the product with a 32-bit position modulo 2^64 is the angle's fraction of a turn,
-// exact to 2^-24 of one for every position: fp32 products are off by whole radians
+// exact to 2^-24 of one for every position (|freq| up to 2^50): fp32 products are off by whole radians
 // far into a text.
 #include <type_traits>
 
@@ -98,24 +98,21 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeOcc<BWD>) rope_kernel(const
     constexpr int PAIRS = HD / 64;                 // pairs of a lane when angles are computed
     __shared__ __align__(16) float2 sh_turn[kRopeWarps][HD / 2];
     __shared__ __align__(16) float sh_w[2][NORM ? HD : 1];       // weights
+    __shared__ uint64_t sh_frac[HD / 2];
     __shared__ float sh_row[MODE == kAnyHalves ? kRopeWarps : 1][MODE == kAnyHalves ? HP : 1][HD];
     __shared__ float sh_dw[BWD && NORM ? kRopeWarps : 1][2][HD];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c = lane % LK, sub = lane / LK, f0 = c * 8;
     const int half = a.rot / 2;
 
-    uint64_t turn[PAIRS];      // of the lane's pairs: a position's fraction of a turn, times 2^64
-    int axis[PAIRS];
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-        const int p = lane + 32 * i;
-        turn[i] = 0;
-        axis[i] = 0;
-        if (p < half) {
-            const double x = static_cast<double>(a.freq[p]) * 0.15915494309189533577;     // 1 / (2 pi)
-            turn[i] = __double2ull_rn((x - floor(x)) * 18446744073709551616.0);
-            if (a.axis) axis[i] = min(max(a.axis[p], 0), a.n_axes - 1);
-        }
+    // a pair's fraction of a turn a position, times 2^64 (once for the CTA: arithmetic in 64 bits is slow, and 33 k packed
+    // rows of 54 heads took 173 us, not 170, with each warp for itself)
+    if (tid < half) {
+        // f / (2 pi) as a product and what it lost (1 / (2 pi) in two doubles): one double's last place, times a position of
+        // 2^31, is 2^-24 of a turn at f = 1 and more above
+        constexpr double kInv = 0x1.45f306dc9c883p-3, kInvLow = -0x1.6b01ec5417056p-57;
+        const double f = a.freq[tid], x = f * kInv, low = fma(f, kInv, -x) + f * kInvLow;
+        sh_frac[tid] = __double2ull_rn((x - floor(x)) * 0x1p64) + static_cast<uint64_t>(__double2ll_rn((low - rint(low)) * 0x1p64));
     }
     // the lane's features of the weights' gradient, of the tensor in hand (queries first, then keys)
     uint64_t dw[4];
@@ -142,7 +139,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeOcc<BWD>) rope_kernel(const
             else v = __half2float(static_cast<const __half*>(wt)[f]);
             sh_w[i / HD][f] = v + a.weight_offset;
         }
+    int axis[PAIRS];           // of the lane's pairs
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i)
+        axis[i] = a.axis && lane + 32 * i < half ? min(max(a.axis[lane + 32 * i], 0), a.n_axes - 1) : 0;
     __syncthreads();
+    uint64_t turn[PAIRS];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) turn[i] = lane + 32 * i < half ? sh_frac[lane + 32 * i] : 0;
 
     const int64_t units_q = a.rows * a.splits[0], units = units_q + a.rows * a.splits[1];
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kRopeWarps;

@@ -189,6 +189,28 @@ def test_zero_rows_and_extremes():
         close("dw", dw, ww, tw)
 
 
+def test_fast_turns_far_away():
+    """Frequencies of many turns a position, at the last positions: against whole-number arithmetic (a 64-bit float
+    loses 2^-14 of a turn there). f16 rows (1, 0) and (0, 1) of each pair show cosine and sine."""
+    import sliding_window_attention_sdpa_gb300 as swa
+    d, half = 64, 32
+    freq = (torch.rand(half, generator=torch.Generator().manual_seed(9)) * 3000 - 1500).float()
+    freq[:3] = torch.tensor([0.0, 1.0, -1e6])
+    pos = torch.tensor([2 ** 31 - 1 - 977 * i for i in range(20)] + [-2 ** 31 + 31 * i for i in range(20)], dtype=torch.int32)
+    inv = 0x28BE60DB9391054A7F09D5F47D4D377036D8A5664F10E4107F9458EAF7AEF1586DC91B8E909374B801  # 2^328 / (2 pi), whole
+    x = torch.zeros(len(pos), 1, d, dtype=torch.float16)
+    x[..., :half] = 1
+    y, _ = swa.qk_rotate(x.cuda(), None, pos.cuda(), freq.cuda())
+    y = y.double().cpu()[:, 0]
+    for i in range(half):
+        num, den = float(freq[i]).as_integer_ratio()
+        for r in range(len(pos)):
+            part = (int(pos[r]) * num * inv // den) % (1 << 328)
+            a = 2 * math.pi * (part / (1 << 328))
+            for got, want in ((y[r, i], math.cos(a)), (y[r, half + i], math.sin(a))):
+                assert abs(float(got) - want) <= 2.0 ** -11 * abs(want) + 2.0 ** -19 + 2.0 ** -25, (i, r, float(got), want)
+
+
 def test_nan_and_infinity_stay_in_their_head():
     import sliding_window_attention_sdpa_gb300 as swa
     x = randn(3, 5, 3, 128, dtype=torch.bfloat16)
