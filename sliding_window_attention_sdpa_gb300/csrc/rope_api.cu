@@ -95,7 +95,8 @@ swa::RopeArgs args_of(const sdpa_rope_params* p, bool backward)
     a.rows = thd ? p->total : p->b * p->s;
     a.s = thd ? (p->total > 0 ? p->total : 1) : p->s;
     a.d = static_cast<int32_t>(p->d);
-    a.rot = static_cast<int32_t>(p->rot);
+    // (without rows there is nothing to turn: positions, axes and frequencies may be missing, and are not read)
+    a.rot = a.rows > 0 ? static_cast<int32_t>(p->rot) : 0;
     a.n_axes = static_cast<int32_t>(p->n_axes);
     a.heads = static_cast<int32_t>(p->h_q + p->h_kv);
     a.interleaved = p->interleaved;
