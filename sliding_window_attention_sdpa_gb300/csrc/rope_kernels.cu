@@ -112,7 +112,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeOcc<BWD>) rope_kernel(const
         // 2^31, is 2^-24 of a turn at f = 1 and more above
         constexpr double kInv = 0x1.45f306dc9c883p-3, kInvLow = -0x1.6b01ec5417056p-57;
         const double f = a.freq[tid], x = f * kInv, low = fma(f, kInv, -x) + f * kInvLow;
-        sh_frac[tid] = __double2ull_rn((x - floor(x)) * 0x1p64) + static_cast<uint64_t>(__double2ll_rn((low - rint(low)) * 0x1p64));
+        // (signed remainders of the nearest whole number: exact, where that of a small negative x from the one below, 1 - |x|, is
+        // rounded at 2^-54, 2^-23 of a turn at 2^31 positions)
+        sh_frac[tid] = static_cast<uint64_t>(__double2ll_rn((x - rint(x)) * 0x1p64)) + static_cast<uint64_t>(__double2ll_rn((low - rint(low)) * 0x1p64));
     }
     // the lane's features of the weights' gradient, of the tensor in hand (queries first, then keys)
     uint64_t dw[4];

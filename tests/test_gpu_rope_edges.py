@@ -6,6 +6,9 @@ import torch
 
 pytestmark = pytest.mark.gpu
 
+# 2^328 / (2 pi), whole
+INV = 0x28BE60DB9391054A7F09D5F47D4D377036D8A5664F10E4107F9458EAF7AEF1586DC91B8E909374B801
+
 
 @pytest.mark.parametrize("d,interleaved,axes", [(64, 0, 1), (128, 0, 3), (128, 1, 1)])
 @pytest.mark.parametrize("packed", [False, True])
@@ -31,3 +34,33 @@ def test_no_rows_and_no_arrays(packed, d, interleaved, axes):
     assert swa.sdpa_rope_fwd(p, stream) == swa.SDPA_OK, swa.last_error()
     torch.cuda.synchronize()
     assert (dw == 0).all()
+
+
+def test_turns_backwards_far_away():
+    """Negative frequencies, slow ones too, at the last positions, where the angle comes near a whole number of turns: the
+    sine there is small, and f16 shows its error. Against whole-number arithmetic."""
+    import sliding_window_attention_sdpa_gb300 as swa
+    one, near = 1 << 328, 1 << (328 - 16)
+    rows = []
+    g = torch.Generator().manual_seed(4)
+    freqs = (-(10.0 ** (torch.rand(32, generator=g, dtype=torch.float64) * 7.5 - 5))).float()       # -1e-5 to -300
+    for i, f in enumerate(freqs.tolist()):
+        num, den = f.as_integer_ratio()
+        step = (num * INV // den) % one
+        for first in (2 ** 31 - 1, -2 ** 31 + 2 ** 15):
+            for pos in range(first, first - 2 ** 15, -1):
+                part = pos * step % one
+                if part < near or one - part < near:
+                    rows.append((i, pos, (part if part < near else part - one) / one))
+                    break
+    assert len(rows) >= 16
+    x = torch.zeros(len(rows), 1, 64, dtype=torch.float16)
+    x[..., :32] = 1
+    pos = torch.tensor([r[1] for r in rows], dtype=torch.int32)
+    y, _ = swa.qk_rotate(x.cuda(), None, pos.cuda(), freqs.cuda())
+    y = y.double().cpu()
+    for r, (i, _, turn) in enumerate(rows):
+        want = math.sin(2 * math.pi * turn)
+        # 2^-24 of a turn; the sine's and the products' roundings in fp32; f16
+        tol = 2 * math.pi * 2.0 ** -24 + (2.0 ** -22 + 2.0 ** -11) * abs(want) + 2.0 ** -25
+        assert abs(float(y[r, 0, 32 + i]) - want) <= tol, (float(freqs[i]), rows[r], float(y[r, 0, 32 + i]), want)
