@@ -231,6 +231,8 @@ def _flat(name, t, shape, device, dtype):
 
 def _apart(name, t):
     """An output's rows must not share memory (an expanded dimension)."""
+    if t is None:
+        raise ValueError(f"{name}: needed where out is given")
     if any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
         raise ValueError(f"{name}: rows share memory (an expanded tensor)")
 

@@ -230,6 +230,8 @@ def qk_rotate_backward(dq, dk, q, k, positions, freq, *, q_weight=None, k_weight
     qp = kp = wqp = wkp = n = 0
     sq = sk = _NONE
     if x.norm:
+        if q is None or dk is not None and k is None:
+            raise ValueError(f"{'q' if q is None else 'k'}: needed with q_weight and k_weight")
         qp, sq = q.data_ptr(), _rows("q", q, x.qs, dev, dt)
         wq = c.empty(x.qs[-1], dtype=c.float32, device=dev)
         wqp = wq.data_ptr()
