@@ -18,6 +18,8 @@
  *     dx = r (u w' - x r^2 mean(u w' x)),  w' = w + weight_offset
  *     dw = sum over tokens and heads of u x r
  * r is computed again from x; nothing is kept from the forward call.
+ * (r^2 stays within fp32 for eps from 2^-128 on; below, for heads whose mean square is, and
+ * heads of zeros, whose dx is r u w'.)
  *
  * Conventions as in sdpa_bwd.h: the caller owns every buffer; calls enqueue on
  * `stream` and do not synchronise; arguments are checked on the host first, with a

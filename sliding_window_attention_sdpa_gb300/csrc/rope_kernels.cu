@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeOcc<BWD>) rope_kernel(const
                             y[e] = mul2(y[e], w[e]);
                             dot = fma2(y[e], x[e], dot);
                         }
-                        const float z = head_sum<LK>(lo2(dot) + hi2(dot)) * (1.f / HD) * -(r * r);
+                        // (of a head of zeros r^2 may be beyond fp32, if eps is below 2^-128)
+                        const float sum = head_sum<LK>(lo2(dot) + hi2(dot)), z = sum == 0.f ? 0.f : sum * (1.f / HD) * -(r * r);
                         const uint64_t z2 = pair2(z, z);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) y[e] = fma2(x[e], z2, y[e]);

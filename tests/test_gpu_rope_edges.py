@@ -4,6 +4,8 @@ import math
 import pytest
 import torch
 
+import rope_ref as P
+
 pytestmark = pytest.mark.gpu
 
 # 2^328 / (2 pi), whole
@@ -64,3 +66,22 @@ def test_turns_backwards_far_away():
         # 2^-24 of a turn; the sine's and the products' roundings in fp32; f16
         tol = 2 * math.pi * 2.0 ** -24 + (2.0 ** -22 + 2.0 ** -11) * abs(want) + 2.0 ** -25
         assert abs(float(y[r, 0, 32 + i]) - want) <= tol, (float(freqs[i]), rows[r], float(y[r, 0, 32 + i]), want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_heads_of_zeros_under_the_smallest_eps(d):
+    """r = eps^(-1/2) is a number whatever eps is, r^2 need not be: dx = r u w has no part of it."""
+    import sliding_window_attention_sdpa_gb300 as swa
+    eps, rows = 2.0 ** -149, 5
+    x = torch.zeros(rows, 2, d, dtype=torch.bfloat16)
+    gen = torch.Generator().manual_seed(d)
+    g = torch.randn(rows, 2, d, generator=gen).to(torch.bfloat16)
+    w = (1 + 0.2 * torch.randn(d, generator=gen)).to(torch.bfloat16)
+    pos, freq = torch.arange(rows, dtype=torch.int32), (10.0 ** (-torch.arange(d // 2) / 16)).float()
+    kw = dict(q_weight=w.cuda(), eps=eps)
+    dx, _, dw, _ = swa.qk_rotate_backward(g.cuda(), None, x.cuda(), None, pos.cuda(), freq.cuda(), **kw)
+    want, tol, _, _ = P.backward(g, x, w, pos, freq, eps=eps)
+    assert torch.isfinite(dx).all() and (dw == 0).all()
+    assert ((dx.double().cpu() - want).abs() <= tol).all()
+    y, _ = swa.qk_rotate(x.cuda(), None, pos.cuda(), freq.cuda(), **kw)
+    assert (y == 0).all()
