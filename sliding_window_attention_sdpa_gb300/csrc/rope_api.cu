@@ -98,7 +98,6 @@ swa::RopeArgs args_of(const sdpa_rope_params* p, bool backward)
     // (without rows there is nothing to turn: positions, axes and frequencies may be missing, and are not read)
     a.rot = a.rows > 0 ? static_cast<int32_t>(p->rot) : 0;
     a.n_axes = static_cast<int32_t>(p->n_axes);
-    a.heads = static_cast<int32_t>(p->h_q + p->h_kv);
     a.interleaved = p->interleaved;
     a.weight_f32 = p->weight_f32;
     a.eps = p->eps;

@@ -21,7 +21,7 @@ struct RopeTensor {
 struct RopeArgs {
     RopeTensor t[2];
     int64_t rows, s;           // all rows; rows of a sequence (THD: rows)
-    int32_t d, rot, n_axes, heads;
+    int32_t d, rot, n_axes;
     int32_t interleaved, weight_f32;
     float eps, weight_offset, rot_scale;
     const int32_t *positions, *axis, *seq_lens;
