@@ -44,7 +44,8 @@ extern "C" {
  */
 typedef struct sdpa_cache {
     int32_t dtype;              /* SDPA_BF16 | SDPA_F16 for K, V and the calls' tensors */
-    int32_t bits;               /* 0 or 16: K and V are held in dtype; 4: in 4 bits (below) */
+    int32_t bits;               /* 0 or 16: K and V are held in dtype; 4: in 4 bits (below); others are
+                                   refused (a caller clears the struct before filling it in) */
     int64_t b, h_kv, d;         /* sequences, kv-heads (up to 4096), head dimension (64 or 128) */
     int64_t n_pages, page_size; /* pages in k and v, rows of a page (any number >= 1) */
     int64_t max_pages;          /* entries of a page-table row; a sequence has room for
@@ -80,6 +81,12 @@ typedef struct sdpa_cache {
  * own; page_size is a multiple of 16, the groups of a page's head follow one
  * another, the page and head strides are non-negative multiples of 16 bytes. Pages
  * may be moved and shared as a whole.
+ * It takes 3.56 times less room than one in 16 bits; whether the forward takes less
+ * time goes by the rows of a kv-head, s_q * h_q / h_kv. 12 sequences of 16484 keys of 6
+ * kv-heads, d = 128, in 4 bits and in 16: 8 rows 46 and 109 us, 16 rows 67 and 108, 32
+ * rows 108 and 109, 64 rows 131 and 110, 256 rows 177 and 142, 296 rows 302 and 237;
+ * d = 64: 8 rows 32 and 72, 32 rows 60 and 83, 48 rows 83 and 83, 64 rows 105 and 84,
+ * 296 rows 233 and 204.
  */
 
 /* sizeof of the structs as compiled into the library, for binding checks. */
@@ -184,8 +191,9 @@ sdpa_status_t sdpa_cache_append(const sdpa_cache *cache, const sdpa_cache_append
  *    offsets[b] = total; a sequence's rows are those of its slot.
  * counts[i] rows come out (all without counts); rows behind them and behind the
  * sequence's last key are zeros. Of a cache in 4 bits the values are those that the
- * codes stand for. A start outside [0, length], a count outside the rows there are
- * and a row of no sequence are reported; rows on pages out of range are zeros.
+ * codes stand for. Of a sequence that has output rows, a start outside [0, length] and
+ * a count outside the rows there are are reported, and so is a row of no sequence; rows
+ * on pages out of range are zeros.
  */
 typedef struct sdpa_cache_read_params {
     int32_t layout;

@@ -10,9 +10,11 @@
  * angle a = pos * freq[i] and multiplies it by rot_scale:
  *     (y_lo, y_hi) = rot_scale (lo cos a - hi sin a, hi cos a + lo sin a)
  * Pair i is (i, i + rot / 2), or (2 i, 2 i + 1) if `interleaved`; features from rot
- * on are not rotated. pos is the token's position on axis[i] (one axis: text; time,
- * height and width: video). Angles are exact products of the int32 position and
- * the fp32 frequency, to 2^-24 of a turn, however far the position (|freq| up to 2^50).
+ * on are not rotated. (Halves of a rot that is no multiple of 16 take more time: 35,000
+ * rows of 54 heads, d = 128, 231 us with rot = 92, 171 with 128; backward 305 and 239.)
+ * pos is the token's position on axis[i] (one axis: text; time, height and width: video).
+ * Angles are exact products of the int32 position and the fp32 frequency, to 2^-24 of a
+ * turn, however far the position, in either direction (|freq| up to 2^50).
  *
  * Backward, with g the gradient of y and u = R^T g:
  *     dx = r (u w' - x r^2 mean(u w' x)),  w' = w + weight_offset

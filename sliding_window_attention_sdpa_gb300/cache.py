@@ -250,7 +250,10 @@ class KVCache:
     A cache in 4 bits: k, v are uint8 [n_pages, h_kv, page_size / 16, 9 d], as
     cache_append fills them (16 features of a key as whole numbers with one
     scale, in an order of the library's own), and `dtype` is that of the calls'
-    tensors. It takes cache_append, cache_read and cache_forward.
+    tensors. It takes cache_append, cache_read and cache_forward. It has 3.56 times
+    the room, and cache_forward takes less time over it than over one in 16 bits
+    with up to 16 rows of a kv-head (s_q * h_q / h_kv; d = 64: 32), about the same
+    with 32 (48), and up to 30 % more above (include/sdpa_cache.h has figures).
     """
 
     def __init__(self, k, v, lengths, *, page_table=None, next_pos=None, positions=None, weights=None, dtype=None):
@@ -328,7 +331,7 @@ class KVCache:
     def empty(cls, b: int, h_kv: int, d: int, max_len: int, *, dtype, device, page_size: int = 64,
               track: bool = False, bits: int = 16) -> "KVCache":
         """An empty cache with room for max_len keys in each of b sequences;
-        `track`: with positions and weights, as weighing and eviction need;
+        `track`: with positions and weights, as weighing and eviction need (which a cache in 4 bits does not do);
         bits: 16 (K and V in dtype) or 4 (page_size: a multiple of 16)."""
         import torch
         if bits not in (4, 16):

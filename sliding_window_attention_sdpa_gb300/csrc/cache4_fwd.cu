@@ -16,12 +16,14 @@
 // power of two that puts its largest magnitude between 2^14 and 2^15 (what then lies
 // below f16's last place is 2^-39 of that), and its scores by the inverse.
 // P is f16 for either type, with references as cache_fwd.cu has them for f16; for f16
-// output its remainder is a second product.
+// output its remainder is a second product. For bf16 output it is left out: f16's half
+// step is an eighth of O's own, and adds in squares (errors against 64 bits relative to
+// O's norm: 0.0016 to 0.0017, those of an fp32 form rounded once).
 //
 // Reading is 9/16 byte a feature, 25 us for 12 sequences of 16484 keys of 6 kv-heads, d =
 // 128 (8 rows: 47 us, 3.6 TB/s). Without the arithmetic the same kernel takes 42 us: 6 us
 // pass before the first keys are there, 6 in the join's launch and the join. With it,
-// no unit is near its rate (ALU 41 %, fp16 28 %, matrix unit 19 %, DRAM 48 % of the time), and
+// no unit is near its rate (ALU 39 %, fma 28 %, matrix unit 20 %, DRAM 47 % of the time), and
 // warps wait for operations that have just been issued. A ring for each warp instead
 // (three steps, no fifth warp: the copies' issue takes a warp some 600 cycles a step)
 // was as fast there, and took 55 us against 44 for 64 ragged sequences; twice as many

@@ -243,6 +243,11 @@ struct FwdLayout {
 // with 301, 900, 1800 keys 12.4, 14.3, 17.4 us whole and 15.4, 16.6, 17.4 cut; its
 // tile kernel (6 kv-heads of 296 rows, d = 128) 28.7, 38.6, 51.8 whole and 33.8,
 // 37.1, 37.9 cut, 12 such sequences 32.9, 43.0, 59.7 whole and 57.3, 70.3, 87.0 cut.
+// More units than the 304 (tiles: 152) places, 4 bits, d = 128, as timed on the device:
+// 512 units of 600, 1400, 1800 keys 28.7, 41.4, 49.2 whole and 32, 46.1, 52.2 cut, of 5 to
+// 1800 keys 29 and 32; with a last wave that is nearly empty, 320 units, 1000, 1400, 1800
+// keys 30.7, 36.8, 45.1 whole and 31.7, 35.1, 38.8 cut, of 5 to 1800 keys 22.6 and 25.6;
+// tiles, 512 units of 900 keys 272 whole and 313 cut, 160 units 103 and 109.
 constexpr int64_t kWholeKeys = 512, kWholeKeys4 = 2048, kWholeKeys4Tiles = 1024;
 
 FwdLayout fwd_layout(const sdpa_cache* c, const sdpa_cache_fwd_params* p, const swa::CacheFwdPlan& plan)

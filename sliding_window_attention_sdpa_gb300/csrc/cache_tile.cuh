@@ -190,8 +190,8 @@ struct Walk {
 // Over a cache in 4 bits, d = 64: a step with one row tile takes 3/4 of the time of one
 // with two, and so of the places. It steps from unit to unit, without divisions: fewer
 // instructions in each role. 12 sequences of 16484 keys, 6 kv-heads, 296 rows 232 us, 272
-// with even places, 300 by the form above; d = 128 307 by this form, 302 by that (24 rows
-// 154 and 135), and the places as they are are even there.
+// with even places, 300 by the form above; d = 128 by this form 2 % more (24 rows 14 %),
+// and the places as they are are even there.
 template <>
 struct Walk<64, true> {
     static constexpr int kTwo = 4, kOne = 3;
@@ -271,8 +271,8 @@ __device__ __forceinline__ int32_t seg_tiles(const Seg& g, int32_t tiles)
 // K and V tiles are made in shared memory, as f16, out of the codes: two warps bring
 // them as they are held, two turn K's and two V's (a warp 32 keys of each tile). Q is
 // f16 as well (see cache4_fwd.cu). 12 sequences of 16484 keys, 6 kv-heads, d = 128: 24
-// rows 131 us, 128 rows 136, 256 rows 172, 296 rows 299; of 16 bits 105, 112, 138, 235.
-// d = 64: 128 rows 106, 296 rows 234.
+// rows 131 us, 128 rows 133, 256 rows 177, 296 rows 302; of 16 bits 109, 114, 142, 237.
+// d = 64: 128 rows 105 and 84, 296 rows 233 and 204.
 //
 // Below 128 rows the turning warps' chain is the bound (about 2000 cycles a tile: wait,
 // load, 200 operations, store, fence), above it that of the softmax groups beside it.
